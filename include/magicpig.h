@@ -54,7 +54,7 @@ extern "C" {
 #define MP_API
 #endif
 
-#define MP_ABI_VERSION 6
+#define MP_ABI_VERSION 7
 #define MP_KEYS_PER_BLOCK 1024
 
 typedef enum {
@@ -324,6 +324,94 @@ MP_API mp_status mp_sampled_attention_buckets(const void* q, mp_dtype q_dtype,
                                               int d, const mp_params* prm, float* out,
                                               void* workspace, size_t ws_bytes,
                                               cudaStream_t stream);
+
+/* ---- 4-bit K/V cache ----------------------------------------------------------------------------
+ * A cache of n_capacity tokens per (sequence, KV head) in 144 bytes a token and head (bf16: 512).
+ * The pages keep K and V at the model's precision; this cache is an addition. Tensors, contiguous
+ * and 16-byte aligned, owned by the caller:
+ *   k_codes, v_codes  [B][Hkv][n_capacity][64]  uint8; byte i holds dims 2 i (low half) and 2 i + 1
+ *   params            [B][Hkv][n_capacity][8]   bf16: s, z of the key's dims 0-63, s, z of its dims
+ *                                               64-127, then the same of the value
+ * Each group of 64 dims x_e is held by its own minimum and step: z is the largest bf16 with
+ * z <= min x, s the smallest bf16 with z + 15 s >= max x, and the code is the integer nearest to
+ * (x_e - z) / s (ties to even; 0 where s = 0), so that the value held, z + s code, is within s / 2
+ * of x_e. A group with a NaN or an infinity, or whose spread passes bf16's range, is held as NaN
+ * in all its 64 dims. Keys are held minus the centre of their head (x = k - mu in float32): the
+ * offset that a head's keys share then costs no code, the softmax over one head's keys does not
+ * see it, and the cosine of the sampled decode is that of k - mu. */
+typedef struct {
+    void* k_codes;
+    void* v_codes;
+    void* params;
+    int n_capacity;
+} mp_kv4;
+#define MP_KV4_GROUP 64          /* dims that share a minimum and a step */
+#define MP_KV4_CODE_BYTES 64     /* bytes of a row of k_codes or v_codes */
+#define MP_KV4_PARAMS 8          /* bf16 of a row of params */
+
+/* Write m tokens of every head into the cache: keys and values [B][Hkv][m][d] (MP_BF16 or MP_F32)
+ * go to rows [n_begin, n_begin + m) of their head, or, with positions ([B] int32 on the device),
+ * to rows [positions[b], positions[b] + m) of sequence b (n_begin is then ignored); a row that
+ * falls outside [0, n_capacity) is not written. Other rows are left as they were. centre [B][Hkv][d]
+ * is subtracted from the keys; NULL subtracts nothing.
+ * Errors: MP_ERR_INVALID_ARG (shapes, m < 0, n_begin < 0 or n_begin + m > n_capacity without
+ * positions, null, misalignment: keys and values 16 bytes, centre 16, positions 4),
+ * MP_ERR_UNSUPPORTED (d != 128). m == 0 does nothing. */
+MP_API mp_status mp_kv4_write(const void* keys, const void* values, mp_dtype kv_dtype,
+                              const float* centre, int B, int Hkv, int m, int d, int n_begin,
+                              const int32_t* positions, const mp_kv4* cache, cudaStream_t stream);
+
+/* Read m tokens of every head back, from the rows that mp_kv4_write would write: keys and values
+ * [B][Hkv][m][d] in kv_dtype, keys with the centre added again (float32 z + s code, rounded once,
+ * plus mu, rounded, then the rounding to bf16). A row outside [0, n_capacity) reads as zero, in
+ * keys and values both. Errors as mp_kv4_write. */
+MP_API mp_status mp_kv4_read(const mp_kv4* cache, const float* centre, int B, int Hkv, int m, int d,
+                             int n_begin, const int32_t* positions, void* keys, void* values,
+                             mp_dtype kv_dtype, cudaStream_t stream);
+
+/* Workspace bytes of mp_kv4_attention for these shapes (0 if they are invalid, and a workspace is
+ * not needed where it is 0 for valid ones). The workspace needs no initial contents; two calls
+ * that may overlap, captured ones among them, need one each. */
+MP_API size_t mp_kv4_attention_workspace_bytes(int B, int Hq, int Hkv, int n, int d);
+
+/* Exact attention of one query token per sequence over the cache's first n tokens:
+ *   out[b][h] = sum_i w_i v_i / sum_i w_i,   w_i = exp(scale q.k_i),   i < length_b
+ * with the values that the cache holds; length_b = n, or lengths[b] ([B] int32 on the device,
+ * taken into [0, n]). A sequence of length 0 gets zero rows. Any Hq that Hkv divides.
+ * scale 0 means 1/sqrt(d). Scores, softmax and sums are float32: codes and the two halves of
+ * a query element or a weight (22 bits) meet in exact tensor-core products. A NaN or an infinity
+ * in a query gives NaN in its output row; one that the cache holds gives NaN to the rows that
+ * attend to it (in a value: to its 64 dims).
+ * Errors: MP_ERR_INVALID_ARG (shapes, n > n_capacity, Hq % Hkv, negative or NaN scale, null,
+ * misalignment: out 16 bytes, lengths 4, workspace 256), MP_ERR_UNSUPPORTED (d != 128),
+ * MP_ERR_WORKSPACE. */
+MP_API mp_status mp_kv4_attention(const void* q, mp_dtype q_dtype, const mp_kv4* cache, int B, int Hq,
+                                  int Hkv, int n, int d, const int32_t* lengths, float scale,
+                                  float* out, void* workspace, size_t ws_bytes,
+                                  cudaStream_t stream);
+
+/* mp_decode_attention, mp_sampled_attention and mp_sampled_attention_buckets with the keys and
+ * values of a 4-bit cache, written with the centre that these calls get: the codes are those of
+ * the keys themselves (mp_encode_keys and its variants, before the cache is written), the scores
+ * and the cosine of p_i are those of the keys that the cache holds. prm->n_capacity is the
+ * codes' capacity, cache->n_capacity the cache's own (>= n). Workspaces, the query encoding
+ * (mp_encode_query), variants and errors as for those calls. */
+MP_API mp_status mp_kv4_decode_attention(const void* q, mp_dtype q_dtype, const uint32_t* codes,
+                                         const float* centre, const void* W, mp_dtype w_dtype,
+                                         const mp_kv4* cache, int B, int Hq, int Hkv, int n, int d,
+                                         const mp_params* prm, float* out, void* workspace,
+                                         size_t ws_bytes, cudaStream_t stream);
+MP_API mp_status mp_kv4_sampled_attention(const void* q, mp_dtype q_dtype, const uint32_t* codes,
+                                          const float* centre, const mp_kv4* cache, int B, int Hq,
+                                          int Hkv, int n, int d, const mp_params* prm, float* out,
+                                          void* workspace, size_t ws_bytes, cudaStream_t stream);
+MP_API mp_status mp_kv4_sampled_attention_buckets(const void* q, mp_dtype q_dtype,
+                                                  const uint32_t* buckets, const uint32_t* codes,
+                                                  const float* centre, const mp_kv4* cache, int B,
+                                                  int Hq, int Hkv, int n, int d,
+                                                  const mp_params* prm, float* out,
+                                                  void* workspace, size_t ws_bytes,
+                                                  cudaStream_t stream);
 
 /* Workspace bytes mp_debug_select needs. */
 MP_API size_t mp_debug_workspace_bytes(int B, int Hq, int Hkv, int n, int d,

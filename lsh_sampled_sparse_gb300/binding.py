@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -34,6 +35,13 @@ class Params(ctypes.Structure):
                 ("n_local", ctypes.c_int), ("scale", ctypes.c_float), ("flags", ctypes.c_uint),
                 ("n_capacity", ctypes.c_int), ("n_indexed", ctypes.c_int),
                 ("radius", ctypes.c_void_p), ("logu_table", ctypes.c_void_p)]
+
+
+class _KV4(ctypes.Structure):
+    """mp_kv4: the tensors of a 4-bit cache and its capacity."""
+
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("params", ctypes.c_void_p), ("n_capacity", ctypes.c_int)]
 
 
 def _params(K, L, n_sink, n_local, scale=0.0, n_capacity=0, n_indexed=0, radius=None,
@@ -73,7 +81,7 @@ def library_path() -> str:
 
 
 def _declare(L):
-    P = ctypes.POINTER(Params)
+    P, Q = ctypes.POINTER(Params), ctypes.POINTER(_KV4)
     sig = {
         "mp_status_string": (ctypes.c_char_p, [_c_int]),
         "mp_abi_version": (_c_int, []),
@@ -111,6 +119,17 @@ def _declare(L):
         "mp_debug_select_buckets": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _vp, _c_int, _vp, _vp,
                                              _c_int] + [_c_int] * 5
                                     + [P, _vp, _vp, _vp, _vp, _vp, _c_size, _vp]),
+        "mp_kv4_write": (_c_int, [_vp, _vp, _c_int, _vp] + [_c_int] * 5 + [_vp, Q, _vp]),
+        "mp_kv4_read": (_c_int, [Q, _vp] + [_c_int] * 5 + [_vp, _vp, _vp, _c_int, _vp]),
+        "mp_kv4_attention_workspace_bytes": (_c_size, [_c_int] * 5),
+        "mp_kv4_attention": (_c_int, [_vp, _c_int, Q] + [_c_int] * 5
+                             + [_vp, ctypes.c_float, _vp, _vp, _c_size, _vp]),
+        "mp_kv4_decode_attention": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _c_int, Q] + [_c_int] * 5
+                                    + [P, _vp, _vp, _c_size, _vp]),
+        "mp_kv4_sampled_attention": (_c_int, [_vp, _c_int, _vp, _vp, Q] + [_c_int] * 5
+                                     + [P, _vp, _vp, _c_size, _vp]),
+        "mp_kv4_sampled_attention_buckets": (_c_int, [_vp, _c_int, _vp, _vp, _vp, Q]
+                                             + [_c_int] * 5 + [P, _vp, _vp, _c_size, _vp]),
         "mp_debug_log_inclusion": (_c_int, [_vp, _c_int, _c_int, _c_int, _vp, _vp]),
         "mp_debug_wait_expiry": (_c_int, [_c_int, _vp]),
         "mp_device_status": (_c_int, [ctypes.POINTER(_c_int)]),
@@ -450,6 +469,239 @@ def sampled_attention_buckets(q, buckets, centre, keys, values, K: int, L: int, 
         _ptr(q), _dtype(q, "q"), _ptr(buckets), _ptr(codes), _ptr(centre), _ptr(keys),
         _ptr(values), _dtype(keys, "keys"), B, Hq, Hkv, n, d, ctypes.byref(p), _ptr(out),
         _ptr(workspace), _nbytes(workspace), _stream(stream)), "mp_sampled_attention_buckets")
+    return out
+
+
+class KV4Cache(NamedTuple):
+    """A 4-bit K/V cache: k_codes and v_codes uint8 [B, Hkv, n_capacity, 64] (dim 2 i in the low
+    half of byte i), params bfloat16 [B, Hkv, n_capacity, 8] (step and minimum of the key's dims
+    0-63 and 64-127, then of the value's). Contiguous, 16-byte aligned."""
+
+    k_codes: torch.Tensor
+    v_codes: torch.Tensor
+    params: torch.Tensor
+
+
+def kv4_cache(B: int, Hkv: int, n_capacity: int, device="cuda") -> KV4Cache:
+    """A 4-bit cache of n_capacity tokens per head, contents undefined (kv4_write fills it)."""
+    return KV4Cache(torch.empty(B, Hkv, n_capacity, 64, dtype=torch.uint8, device=device),
+                    torch.empty(B, Hkv, n_capacity, 64, dtype=torch.uint8, device=device),
+                    torch.empty(B, Hkv, n_capacity, 8, dtype=torch.bfloat16, device=device))
+
+
+def _kv4(cache, B, Hkv):
+    """The cache's mp_kv4 and its device, checked against the call's B and Hkv (None: any)."""
+    k, v, p = cache
+    shape = k.shape
+    if not (k.is_cuda and v.is_cuda and p.is_cuda):
+        raise TypeError("the cache must hold CUDA tensors")
+    if k.dtype != torch.uint8 or v.dtype != torch.uint8 or p.dtype != torch.bfloat16:
+        raise TypeError("a 4-bit cache holds uint8, uint8 and bfloat16 tensors")
+    if len(shape) != 4 or shape[3] != 64 or v.shape != shape or p.shape != (*shape[:3], 8):
+        raise ValueError("k_codes and v_codes must be [B, Hkv, n_capacity, 64] and params "
+                         f"[B, Hkv, n_capacity, 8], got {tuple(shape)}, {tuple(v.shape)}, "
+                         f"{tuple(p.shape)}")
+    if B is not None and (shape[0] != B or shape[1] != Hkv):
+        raise ValueError(f"the cache holds {shape[0]} x {shape[1]} heads, the call {B} x {Hkv}")
+    if not (k.is_contiguous() and v.is_contiguous() and p.is_contiguous()):
+        raise ValueError("the cache's tensors must be contiguous")
+    _same_device(k.device, v, p)
+    return _KV4(k.data_ptr(), v.data_ptr(), p.data_ptr(), shape[2]), k.device
+
+
+def _same_device(device, *tensors):
+    """Every tensor of a 4-bit cache's call is on one device, the current one."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, not on the current device")
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device} in one call")
+
+
+def _of_batch(t, B, name, dtype, shape=None):
+    """t (or None), checked: dtype, shape [B] unless given, on the GPU, contiguous."""
+    if t is not None:
+        _cuda(t, name)
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}")
+        if tuple(t.shape) != (shape or (B,)):
+            raise ValueError(f"{name} must have shape {shape or (B,)}, got {tuple(t.shape)}")
+    return t
+
+
+def _use(stream, *tensors):
+    """Tensors allocated here stay allocated until the other stream that uses them is done."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def kv4_write(cache: KV4Cache, keys, values, n_begin: int = 0, centre=None, positions=None,
+              stream=None) -> KV4Cache:
+    """Write keys, values [B, Hkv, m, 128] (float32 or bfloat16) into rows [n_begin, n_begin + m)
+    of every head of the 4-bit cache, or with positions (int32 [B], on the GPU) into rows
+    [positions[b], positions[b] + m) of sequence b; rows outside the capacity are not written.
+    centre (key_mean's, float32 [B, Hkv, 128]) is subtracted from the keys."""
+    _cuda(keys, "keys", 4)
+    _cuda(values, "values", 4)
+    B, Hkv, m, d = keys.shape
+    if values.shape != keys.shape or values.dtype != keys.dtype:
+        raise ValueError("values must match keys in shape and dtype")
+    c, device = _kv4(cache, B, Hkv)
+    _of_batch(centre, B, "centre", torch.float32, (B, Hkv, d))
+    _of_batch(positions, B, "positions", torch.int32)
+    _same_device(device, keys, values, centre, positions)
+    _check(lib().mp_kv4_write(_ptr(keys), _ptr(values), _dtype(keys, "keys"), _ptr(centre), B, Hkv,
+                              m, d, n_begin, _ptr(positions), ctypes.byref(c), _stream(stream)),
+           "mp_kv4_write")
+    return cache
+
+
+def kv4_read(cache: KV4Cache, m: int, n_begin: int = 0, centre=None, positions=None,
+             dtype=torch.bfloat16, keys=None, values=None, stream=None):
+    """Rows [n_begin, n_begin + m) of every head (or from positions[b] on, as kv4_write) as keys,
+    values [B, Hkv, m, 128] in dtype, with centre added to the keys; rows outside the capacity
+    read as zero."""
+    c, device = _kv4(cache, None, None)
+    B, Hkv = cache.k_codes.shape[:2]
+    new = []
+    if keys is None:
+        keys = torch.empty(B, Hkv, m, 128, dtype=dtype, device=device)
+        new.append(keys)
+    if values is None:
+        values = torch.empty(B, Hkv, m, 128, dtype=keys.dtype, device=device)
+        new.append(values)
+    _cuda(keys, "keys", 4)
+    _cuda(values, "values", 4)
+    if tuple(keys.shape) != (B, Hkv, m, 128) or values.shape != keys.shape \
+            or values.dtype != keys.dtype:
+        raise ValueError(f"keys and values must be [{B}, {Hkv}, {m}, 128] of one dtype")
+    _of_batch(centre, B, "centre", torch.float32, (B, Hkv, 128))
+    _of_batch(positions, B, "positions", torch.int32)
+    _same_device(device, keys, values, centre, positions)
+    _check(lib().mp_kv4_read(ctypes.byref(c), _ptr(centre), B, Hkv, m, 128, n_begin,
+                             _ptr(positions), _ptr(keys), _ptr(values), _dtype(keys, "keys"),
+                             _stream(stream)), "mp_kv4_read")
+    _use(stream, *new)
+    return keys, values
+
+
+def kv4_attention_workspace_bytes(B: int, Hq: int, Hkv: int, n: int, d: int = 128) -> int:
+    return int(lib().mp_kv4_attention_workspace_bytes(B, Hq, Hkv, n, d))
+
+
+def _kv4_inputs(codes, centre, W, B, Hkv, cap, d, K, L, cross_polytope):
+    """The codes (laid out for the cache's capacity), centre and W of a sampled decode."""
+    _of_batch(centre, B, "centre", torch.float32, (B, Hkv, d))
+    need = (cp_codes_bytes if cross_polytope else codes_bytes)(
+        *((B, Hkv, cap, L) if cross_polytope else (B, Hkv, cap, K, L)))
+    if need and (codes is None or _nbytes(_cuda(codes, "codes")) < need):
+        raise ValueError(f"codes must hold {need} bytes, for {cap} tokens per head")
+    if W is not None and _cuda(W, "W").numel() < d * (d if cross_polytope else K) * L:
+        raise ValueError(f"W of shape {tuple(W.shape)} has too few hyperplanes")
+
+
+def _kv4_out(q, out, B, Hq, d):
+    if out is None:
+        return torch.empty(B, Hq, d, dtype=torch.float32, device=q.device), True
+    _of_batch(out, B, "out", torch.float32, (B, Hq, d))
+    return out, False
+
+
+def kv4_attention(q, cache: KV4Cache, n=None, lengths=None, scale: float = 0.0, out=None,
+                  workspace=None, stream=None):
+    """Exact attention of one query token per sequence, q [B, Hq, 128], over the first n tokens
+    (default: the capacity) of a 4-bit cache, or the first lengths[b] (int32 [B], on the GPU, at
+    most n) of sequence b; returns out [B, Hq, 128] float32, zero for a sequence of length 0."""
+    _cuda(q, "q", 3)
+    B, Hq, d = q.shape
+    Hkv = cache.k_codes.shape[1]
+    c, device = _kv4(cache, B, Hkv)
+    n, _ = _lengths(cache.k_codes.shape, n)
+    _of_batch(lengths, B, "lengths", torch.int32)
+    out, made = _kv4_out(q, out, B, Hq, d)
+    need = int(lib().mp_kv4_attention_workspace_bytes(B, Hq, Hkv, n, d))
+    ws = _workspace(workspace, need, device)
+    _same_device(device, q, lengths, out, ws)
+    _check(lib().mp_kv4_attention(_ptr(q), _dtype(q, "q"), ctypes.byref(c), B, Hq, Hkv, n, d,
+                                  _ptr(lengths), scale, _ptr(out), _ptr(ws), _nbytes(ws),
+                                  _stream(stream)), "mp_kv4_attention")
+    _use(stream, *([out] if made else []), *([ws] if workspace is None else []))
+    return out
+
+
+def kv4_decode_attention(q, codes, centre, W, cache: KV4Cache, K: int, L: int, n_sink: int,
+                         n_local: int, scale: float = 0.0, out=None, workspace=None, stream=None,
+                         n=None, radius=None, logu_table=None):
+    """decode_attention over the first n tokens of a 4-bit cache (written with this centre)."""
+    _cuda(q, "q", 3)
+    B, Hq, d = q.shape
+    Hkv = cache.k_codes.shape[1]
+    c, device = _kv4(cache, B, Hkv)
+    n, cap = _lengths(cache.k_codes.shape, n)
+    _kv4_inputs(codes, centre, _cuda(W, "W"), B, Hkv, cap, d, K, L, logu_table is not None)
+    out, made = _kv4_out(q, out, B, Hq, d)
+    p = _params(K, L, n_sink, n_local, scale, cap, radius=radius, logu_table=logu_table)
+    need = int(lib().mp_decode_workspace_bytes(B, Hq, Hkv, n, d, ctypes.byref(p)))
+    if need == 0:
+        raise MagicPIGError("mp_decode_workspace_bytes rejected the shapes/parameters")
+    ws = _workspace(workspace, need, device)
+    _same_device(device, q, codes, centre, W, out, ws, radius, logu_table)
+    _check(lib().mp_kv4_decode_attention(
+        _ptr(q), _dtype(q, "q"), _ptr(codes), _ptr(centre), _ptr(W), _dtype(W, "W"),
+        ctypes.byref(c), B, Hq, Hkv, n, d, ctypes.byref(p), _ptr(out), _ptr(ws), _nbytes(ws),
+        _stream(stream)), "mp_kv4_decode_attention")
+    _use(stream, *([out] if made else []), *([ws] if workspace is None else []))
+    return out
+
+
+def kv4_sampled_attention(q, codes, centre, cache: KV4Cache, K: int, L: int, n_sink: int,
+                          n_local: int, out, workspace, scale: float = 0.0, stream=None, n=None,
+                          radius=None, logu_table=None):
+    """Second half of kv4_decode_attention (after encode_query filled `workspace`, its keys_shape
+    [B, Hkv, n_capacity, 128])."""
+    _cuda(q, "q", 3)
+    _cuda(workspace, "workspace")
+    B, Hq, d = q.shape
+    Hkv = cache.k_codes.shape[1]
+    c, device = _kv4(cache, B, Hkv)
+    n, cap = _lengths(cache.k_codes.shape, n)
+    _kv4_inputs(codes, centre, None, B, Hkv, cap, d, K, L, logu_table is not None)
+    out, _ = _kv4_out(q, out, B, Hq, d)
+    p = _params(K, L, n_sink, n_local, scale, cap, radius=radius, logu_table=logu_table)
+    _same_device(device, q, codes, centre, out, workspace, radius, logu_table)
+    _check(lib().mp_kv4_sampled_attention(
+        _ptr(q), _dtype(q, "q"), _ptr(codes), _ptr(centre), ctypes.byref(c), B, Hq, Hkv, n, d,
+        ctypes.byref(p), _ptr(out), _ptr(workspace), _nbytes(workspace), _stream(stream)),
+        "mp_kv4_sampled_attention")
+    return out
+
+
+def kv4_sampled_attention_buckets(q, buckets, centre, cache: KV4Cache, K: int, L: int,
+                                  n_sink: int, n_local: int, out, workspace, scale: float = 0.0,
+                                  stream=None, codes=None, n=None, n_indexed=None, radius=None):
+    """sampled_attention_buckets over a 4-bit cache (written with this centre)."""
+    _cuda(q, "q", 3)
+    _cuda(workspace, "workspace")
+    _cuda(buckets, "buckets")
+    B, Hq, d = q.shape
+    Hkv = cache.k_codes.shape[1]
+    c, device = _kv4(cache, B, Hkv)
+    n, cap = _lengths(cache.k_codes.shape, n)
+    if codes is not None:
+        _kv4_inputs(codes, centre, None, B, Hkv, cap, d, K, L, False)
+    _of_batch(centre, B, "centre", torch.float32, (B, Hkv, d))
+    indexed = n if n_indexed is None else int(n_indexed)
+    if _nbytes(buckets) < buckets_bytes(B, Hkv, indexed, K, L):
+        raise ValueError(f"buckets too small for {indexed} keys per head")
+    out, _ = _kv4_out(q, out, B, Hq, d)
+    p = _params(K, L, n_sink, n_local, scale, cap, 0 if n_indexed is None else int(n_indexed),
+                radius=radius)
+    _same_device(device, q, buckets, codes, centre, out, workspace, radius)
+    _check(lib().mp_kv4_sampled_attention_buckets(
+        _ptr(q), _dtype(q, "q"), _ptr(buckets), _ptr(codes), _ptr(centre), ctypes.byref(c), B, Hq,
+        Hkv, n, d, ctypes.byref(p), _ptr(out), _ptr(workspace), _nbytes(workspace),
+        _stream(stream)), "mp_kv4_sampled_attention_buckets")
     return out
 
 

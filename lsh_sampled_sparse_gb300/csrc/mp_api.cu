@@ -42,7 +42,8 @@ bool ensure_prepared() {
         return false;
     if (prepare_misc() != cudaSuccess || prepare_decode() != cudaSuccess ||
         prepare_buckets() != cudaSuccess || prepare_append() != cudaSuccess ||
-        prepare_mips() != cudaSuccess || prepare_cross_polytope() != cudaSuccess)
+        prepare_mips() != cudaSuccess || prepare_cross_polytope() != cudaSuccess ||
+        prepare_kv4() != cudaSuccess)
         return false;
     prepare_encode_tc();   // failure only disables the tensor-core encoder
     cudaGetLastError();
@@ -179,13 +180,11 @@ cudaError_t query_encode(const void* q, bool q_bf16, const float* centre, const 
 }
 
 cudaError_t scan_and_attend(const void* q, bool q_bf16, const uint32_t* codes,
-                            const float* centre, const void* keys, const void* values,
-                            bool kv_bf16, const DecodeShape& s, float* out,
-                            const DecodeScratch& ws, cudaStream_t st, int blk0 = 0) {
-    return s.cp ? launch_collide_cp(q, q_bf16, reinterpret_cast<const uint8_t*>(codes), centre,
-                                    keys, values, kv_bf16, s, out, ws, st, blk0)
-                : launch_collide(q, q_bf16, codes, centre, keys, values, kv_bf16, s, out, ws, st,
-                                 blk0);
+                            const float* centre, const KvRef& kv, const DecodeShape& s,
+                            float* out, const DecodeScratch& ws, cudaStream_t st, int blk0 = 0) {
+    return s.cp ? launch_collide_cp(q, q_bf16, reinterpret_cast<const uint8_t*>(codes), centre, kv,
+                                    s, out, ws, st, blk0)
+                : launch_collide(q, q_bf16, codes, centre, kv, s, out, ws, st, blk0);
 }
 
 }  // namespace mp
@@ -207,7 +206,7 @@ mp_status validate_decode(const void* q, mp_dtype q_dtype, const uint32_t* codes
         (codes && !aligned(codes, 16)))
         return MP_ERR_INVALID_ARG;
     if (d != kD) return MP_ERR_UNSUPPORTED;
-    if (!decode_supported(*s, kv_dtype == MP_BF16)) return MP_ERR_UNSUPPORTED;
+    if (!decode_supported(*s, kv_dtype == MP_BF16 ? kKvBf16 : kKvF32)) return MP_ERR_UNSUPPORTED;
     return MP_OK;
 }
 }  // namespace mp
@@ -429,8 +428,8 @@ mp_status mp_decode_attention(const void* q, mp_dtype q_dtype, const uint32_t* c
     cudaError_t e = query_encode(q, q_dtype == MP_BF16, centre, W, w_dtype == MP_BF16, s, ws,
                                  stream);
     if (e != cudaSuccess) return MP_ERR_CUDA;
-    return to_status(scan_and_attend(q, q_dtype == MP_BF16, codes, centre, keys, values,
-                                     kv_dtype == MP_BF16, s, out, ws, stream));
+    return to_status(scan_and_attend(q, q_dtype == MP_BF16, codes, centre,
+                                     kv_ref(keys, values, kv_dtype), s, out, ws, stream));
 }
 
 mp_status mp_encode_query(const void* q, mp_dtype q_dtype, const float* centre, const void* W,
@@ -465,8 +464,8 @@ mp_status mp_sampled_attention(const void* q, mp_dtype q_dtype, const uint32_t* 
     if (st != MP_OK) return st;
     if (!ensure_prepared()) return MP_ERR_CUDA;
     const DecodeScratch ws = carve_decode_scratch(workspace, s, false);
-    return to_status(scan_and_attend(q, q_dtype == MP_BF16, codes, centre, keys, values,
-                                     kv_dtype == MP_BF16, s, out, ws, stream));
+    return to_status(scan_and_attend(q, q_dtype == MP_BF16, codes, centre,
+                                     kv_ref(keys, values, kv_dtype), s, out, ws, stream));
 }
 
 size_t mp_buckets_bytes(int B, int Hkv, int n, int K, int L) {
@@ -490,6 +489,154 @@ mp_status mp_build_buckets_cap(const uint32_t* codes, int B, int Hkv, int n_capa
     return to_status(launch_bucket_build(codes, B, Hkv, cblk, n, K, L, buckets, stream));
 }
 
+// The cache of a 4-bit call: its tensors and capacity.
+static bool valid_kv4(const mp_kv4* c) {
+    return c && c->k_codes && c->v_codes && c->params && c->n_capacity >= 1 &&
+           aligned(c->k_codes, 16) && aligned(c->v_codes, 16) && aligned(c->params, 16);
+}
+
+// The checks that mp_kv4_write and mp_kv4_read share; *empty: there is nothing to do.
+static mp_status check_kv4_rows(const void* keys, const void* values, mp_dtype t,
+                                const float* centre, int B, int Hkv, int m, int d, int n_begin,
+                                const int32_t* positions, const mp_kv4* cache, bool* empty) {
+    *empty = false;
+    if (B < 1 || Hkv < 1 || m < 0 || d < 1 || !valid_dtype(t)) return MP_ERR_INVALID_ARG;
+    if (d != kD) return MP_ERR_UNSUPPORTED;
+    if (!valid_kv4(cache)) return MP_ERR_INVALID_ARG;
+    if (!positions && (n_begin < 0 || n_begin > cache->n_capacity - m)) return MP_ERR_INVALID_ARG;
+    if (!aligned(keys, 16) || !aligned(values, 16) || !aligned(centre, 16) ||
+        !aligned(positions, 4))
+        return MP_ERR_INVALID_ARG;
+    *empty = m == 0;
+    if (!*empty && (!keys || !values)) return MP_ERR_INVALID_ARG;
+    // one CTA takes 16 rows or more, and a grid 2^31 - 1 CTAs
+    if (static_cast<long long>(B) * Hkv > (16ll * 0x7fffffff) / std::max(m, 1))
+        return MP_ERR_INVALID_ARG;
+    return MP_OK;
+}
+
+mp_status mp_kv4_write(const void* keys, const void* values, mp_dtype kv_dtype,
+                       const float* centre, int B, int Hkv, int m, int d, int n_begin,
+                       const int32_t* positions, const mp_kv4* cache, cudaStream_t stream) {
+    bool empty;
+    const mp_status st = check_kv4_rows(keys, values, kv_dtype, centre, B, Hkv, m, d, n_begin,
+                                        positions, cache, &empty);
+    if (st != MP_OK || empty) return st;
+    if (!ensure_prepared()) return MP_ERR_CUDA;
+    return to_status(launch_kv4_write(keys, values, kv_dtype == MP_BF16, centre, B, Hkv, m,
+                                      n_begin, positions, *cache, stream));
+}
+
+mp_status mp_kv4_read(const mp_kv4* cache, const float* centre, int B, int Hkv, int m, int d,
+                      int n_begin, const int32_t* positions, void* keys, void* values,
+                      mp_dtype kv_dtype, cudaStream_t stream) {
+    bool empty;
+    const mp_status st = check_kv4_rows(keys, values, kv_dtype, centre, B, Hkv, m, d, n_begin,
+                                        positions, cache, &empty);
+    if (st != MP_OK || empty) return st;
+    if (!ensure_prepared()) return MP_ERR_CUDA;
+    return to_status(launch_kv4_read(*cache, centre, B, Hkv, m, n_begin, positions, keys, values,
+                                     kv_dtype == MP_BF16, stream));
+}
+
+static bool valid_kv4_attention(int B, int Hq, int Hkv, int n, int d) {
+    return B >= 1 && Hq >= 1 && Hkv >= 1 && n >= 1 && d >= 1 && Hq % Hkv == 0 &&
+           static_cast<long long>(B) * Hq <= (1 << 24);
+}
+
+size_t mp_kv4_attention_workspace_bytes(int B, int Hq, int Hkv, int n, int d) {
+    if (!valid_kv4_attention(B, Hq, Hkv, n, d) || d != kD) return 0;
+    return align256(kv4_attention_scratch_bytes(B, Hq, Hkv, n));
+}
+
+mp_status mp_kv4_attention(const void* q, mp_dtype q_dtype, const mp_kv4* cache, int B, int Hq,
+                           int Hkv, int n, int d, const int32_t* lengths, float scale, float* out,
+                           void* workspace, size_t ws_bytes, cudaStream_t stream) {
+    if (!valid_kv4_attention(B, Hq, Hkv, n, d) || !valid_dtype(q_dtype)) return MP_ERR_INVALID_ARG;
+    if (d != kD) return MP_ERR_UNSUPPORTED;
+    if (!valid_kv4(cache) || n > cache->n_capacity || !(scale >= 0.0f) || isinf(scale))
+        return MP_ERR_INVALID_ARG;
+    if (!q || !out || !aligned(q, q_dtype == MP_BF16 ? 2 : 4) || !aligned(out, 16) ||
+        !aligned(lengths, 4))
+        return MP_ERR_INVALID_ARG;
+    const size_t need = mp_kv4_attention_workspace_bytes(B, Hq, Hkv, n, d);
+    if (need > 0 && (!workspace || !aligned(workspace, 256))) return MP_ERR_INVALID_ARG;
+    if (ws_bytes < need) return MP_ERR_WORKSPACE;
+    if (!ensure_prepared()) return MP_ERR_CUDA;
+    return to_status(launch_kv4_attention(
+        q, q_dtype == MP_BF16, *cache, B, Hq, Hkv, n, lengths,
+        scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(d)), out, workspace, stream));
+}
+
+// check_decode for a 4-bit cache: its codes stand in for bf16 keys and values.
+static mp_status check_kv4_decode(const void* q, mp_dtype q_dtype, const uint32_t* codes,
+                                  const float* centre, const void* W, mp_dtype w_dtype,
+                                  const mp_kv4* cache, int B, int Hq, int Hkv, int n, int d,
+                                  const mp_params* prm, float* out, void* workspace,
+                                  size_t ws_bytes, DecodeShape* s, KvRef* kv) {
+    if (!valid_kv4(cache)) return MP_ERR_INVALID_ARG;
+    const mp_status st = check_decode(q, q_dtype, codes, centre, W, w_dtype, cache->k_codes,
+                                      cache->v_codes, MP_BF16, B, Hq, Hkv, n, d, prm, out,
+                                      workspace, ws_bytes, false, s);
+    if (st != MP_OK) return st;
+    if (n > cache->n_capacity) return MP_ERR_INVALID_ARG;
+    s->ncap = cache->n_capacity;
+    *kv = KvRef{cache->k_codes, cache->v_codes, cache->params, kKv4};
+    return MP_OK;
+}
+
+mp_status mp_kv4_decode_attention(const void* q, mp_dtype q_dtype, const uint32_t* codes,
+                                  const float* centre, const void* W, mp_dtype w_dtype,
+                                  const mp_kv4* cache, int B, int Hq, int Hkv, int n, int d,
+                                  const mp_params* prm, float* out, void* workspace,
+                                  size_t ws_bytes, cudaStream_t stream) {
+    DecodeShape s;
+    KvRef kv;
+    const mp_status st = check_kv4_decode(q, q_dtype, codes, centre, W, w_dtype, cache, B, Hq, Hkv,
+                                          n, d, prm, out, workspace, ws_bytes, &s, &kv);
+    if (st != MP_OK) return st;
+    if (!ensure_prepared()) return MP_ERR_CUDA;
+    const DecodeScratch ws = carve_decode_scratch(workspace, s, false);
+    const cudaError_t e = query_encode(q, q_dtype == MP_BF16, centre, W, w_dtype == MP_BF16, s, ws,
+                                       stream);
+    if (e != cudaSuccess) return MP_ERR_CUDA;
+    return to_status(scan_and_attend(q, q_dtype == MP_BF16, codes, centre, kv, s, out, ws, stream));
+}
+
+mp_status mp_kv4_sampled_attention(const void* q, mp_dtype q_dtype, const uint32_t* codes,
+                                   const float* centre, const mp_kv4* cache, int B, int Hq,
+                                   int Hkv, int n, int d, const mp_params* prm, float* out,
+                                   void* workspace, size_t ws_bytes, cudaStream_t stream) {
+    DecodeShape s;
+    KvRef kv;
+    // W is only read by the query encoding; q stands in for it in the shared checks
+    const mp_status st = check_kv4_decode(q, q_dtype, codes, centre, q, MP_F32, cache, B, Hq, Hkv,
+                                          n, d, prm, out, workspace, ws_bytes, &s, &kv);
+    if (st != MP_OK) return st;
+    if (!ensure_prepared()) return MP_ERR_CUDA;
+    const DecodeScratch ws = carve_decode_scratch(workspace, s, false);
+    return to_status(scan_and_attend(q, q_dtype == MP_BF16, codes, centre, kv, s, out, ws, stream));
+}
+
+// The bucketed decode's second half (after its checks) on keys and values of any form.
+static mp_status buckets_attend(const void* q, mp_dtype q_dtype, const uint32_t* buckets,
+                                const uint32_t* codes, const float* centre, const KvRef& kv,
+                                const DecodeShape& s, float* out, void* workspace,
+                                cudaStream_t stream) {
+    if (s.K > kMaxBucketBits || s.cp) return MP_ERR_UNSUPPORTED;
+    // keys appended since the tables were built come from a scan of their code blocks
+    const bool tail = s.n_indexed < s.n && s.C > 0;
+    if (tail && (!codes || !aligned(codes, 16))) return MP_ERR_INVALID_ARG;
+    if (!ensure_prepared()) return MP_ERR_CUDA;
+    const DecodeScratch ws = carve_decode_scratch(workspace, s, false);
+    cudaError_t e = launch_bucket_lookup(buckets, ws.qbits, s, ws.sel_ge1, ws.selmask, stream);
+    if (e != cudaSuccess) return MP_ERR_CUDA;
+    if (tail)
+        return to_status(scan_and_attend(q, q_dtype == MP_BF16, codes, centre, kv, s, out, ws,
+                                         stream, s.n_indexed / kKeysPerBlock));
+    return to_status(launch_attend(q, q_dtype == MP_BF16, centre, kv, s, out, ws, stream));
+}
+
 mp_status mp_sampled_attention_buckets(const void* q, mp_dtype q_dtype, const uint32_t* buckets,
                                        const uint32_t* codes, const float* centre,
                                        const void* keys, const void* values, mp_dtype kv_dtype,
@@ -503,20 +650,22 @@ mp_status mp_sampled_attention_buckets(const void* q, mp_dtype q_dtype, const ui
                                       kv_dtype, B, Hq, Hkv, n, d, prm, out, workspace, ws_bytes,
                                       false, &s);
     if (st != MP_OK) return st;
-    if (s.K > kMaxBucketBits || s.cp) return MP_ERR_UNSUPPORTED;
-    // keys appended since the tables were built come from a scan of their code blocks
-    const bool tail = s.n_indexed < s.n && s.C > 0;
-    if (tail && (!codes || !aligned(codes, 16))) return MP_ERR_INVALID_ARG;
-    if (!ensure_prepared()) return MP_ERR_CUDA;
-    const DecodeScratch ws = carve_decode_scratch(workspace, s, false);
-    cudaError_t e = launch_bucket_lookup(buckets, ws.qbits, s, ws.sel_ge1, ws.selmask, stream);
-    if (e != cudaSuccess) return MP_ERR_CUDA;
-    if (tail)
-        return to_status(scan_and_attend(q, q_dtype == MP_BF16, codes, centre, keys, values,
-                                         kv_dtype == MP_BF16, s, out, ws, stream,
-                                         s.n_indexed / kKeysPerBlock));
-    return to_status(launch_attend(q, q_dtype == MP_BF16, centre, keys, values,
-                                   kv_dtype == MP_BF16, s, out, ws, stream));
+    return buckets_attend(q, q_dtype, buckets, codes, centre, kv_ref(keys, values, kv_dtype), s,
+                          out, workspace, stream);
+}
+
+mp_status mp_kv4_sampled_attention_buckets(const void* q, mp_dtype q_dtype,
+                                           const uint32_t* buckets, const uint32_t* codes,
+                                           const float* centre, const mp_kv4* cache, int B, int Hq,
+                                           int Hkv, int n, int d, const mp_params* prm, float* out,
+                                           void* workspace, size_t ws_bytes, cudaStream_t stream) {
+    if (!buckets) return MP_ERR_INVALID_ARG;
+    DecodeShape s;
+    KvRef kv;
+    const mp_status st = check_kv4_decode(q, q_dtype, buckets, centre, q, MP_F32, cache, B, Hq,
+                                          Hkv, n, d, prm, out, workspace, ws_bytes, &s, &kv);
+    if (st != MP_OK) return st;
+    return buckets_attend(q, q_dtype, buckets, codes, centre, kv, s, out, workspace, stream);
 }
 
 mp_status mp_debug_select(const void* q, mp_dtype q_dtype, const uint32_t* codes,
@@ -538,7 +687,7 @@ mp_status mp_debug_select(const void* q, mp_dtype q_dtype, const uint32_t* codes
     cudaError_t e = query_encode(q, q_dtype == MP_BF16, centre, W, w_dtype == MP_BF16, s, ws,
                                  stream);
     if (e != cudaSuccess) return MP_ERR_CUDA;
-    e = scan_and_attend(q, q_dtype == MP_BF16, codes, centre, keys, values, kv_dtype == MP_BF16, s,
+    e = scan_and_attend(q, q_dtype == MP_BF16, codes, centre, kv_ref(keys, values, kv_dtype), s,
                         out, ws, stream);
     if (e != cudaSuccess) return MP_ERR_CUDA;
     e = launch_compact_selection(ws.selmask, s.B * s.Hq, s.n, s.nblk, s.n_sink, s.n_local,
@@ -585,10 +734,10 @@ mp_status mp_debug_select_buckets(const void* q, mp_dtype q_dtype, const uint32_
     if (e != cudaSuccess) return MP_ERR_CUDA;
     // the same kernels as mp_sampled_attention_buckets
     if (tail)
-        e = scan_and_attend(q, q_dtype == MP_BF16, codes, centre, keys, values,
-                            kv_dtype == MP_BF16, s, out, ws, stream, s.n_indexed / kKeysPerBlock);
+        e = scan_and_attend(q, q_dtype == MP_BF16, codes, centre, kv_ref(keys, values, kv_dtype), s,
+                            out, ws, stream, s.n_indexed / kKeysPerBlock);
     else
-        e = launch_attend(q, q_dtype == MP_BF16, centre, keys, values, kv_dtype == MP_BF16, s,
+        e = launch_attend(q, q_dtype == MP_BF16, centre, kv_ref(keys, values, kv_dtype), s,
                           out, ws, stream);
     if (e != cudaSuccess) return MP_ERR_CUDA;
     return to_status(launch_compact_selection(ws.selmask, s.B * s.Hq, s.n, s.nblk, s.n_sink,

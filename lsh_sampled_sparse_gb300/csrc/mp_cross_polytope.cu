@@ -427,9 +427,8 @@ cudaError_t launch_qencode_cp(const void* q, bool q_bf16, const float* centre, c
 }
 
 cudaError_t launch_collide_cp(const void* q, bool q_bf16, const uint8_t* codes,
-                              const float* centre, const void* keys, const void* values,
-                              bool kv_bf16, const DecodeShape& s, float* out,
-                              const DecodeScratch& ws, cudaStream_t st, int blk0) {
+                              const float* centre, const KvRef& kv, const DecodeShape& s,
+                              float* out, const DecodeScratch& ws, cudaStream_t st, int blk0) {
     size_t smem = 0;
     CpCollideFn fn = pick_collide_cp(s.Hq / s.Hkv, &smem, s.L);
     if (!fn || smem > 48 * 1024) return cudaErrorNotSupported;
@@ -452,7 +451,7 @@ cudaError_t launch_collide_cp(const void* q, bool q_bf16, const uint8_t* codes,
                                                dim3(kCpThreads), smem, st, a);
         if (e != cudaSuccess) return e;
     }
-    return launch_attend(q, q_bf16, centre, keys, values, kv_bf16, s, out, ws, st);
+    return launch_attend(q, q_bf16, centre, kv, s, out, ws, st);
 }
 
 cudaError_t prepare_cross_polytope() {

@@ -167,10 +167,14 @@ constexpr int kRowKeys = 256;                        // selected keys listed onc
 struct AttendSmem {
     size_t work, total;
 };
-inline AttendSmem attend_smem(int nsp, size_t kv_elem) {
-    (void)nsp;
+// Bytes of a staged row: K then V, or for the 4-bit cache key codes, value codes, parameters.
+__host__ __device__ constexpr int attend_row_bytes(KvForm form) {
+    return form == kKv4 ? 2 * MP_KV4_CODE_BYTES + 2 * MP_KV4_PARAMS
+                        : 2 * kD * (form == kKvBf16 ? 2 : 4);
+}
+inline AttendSmem attend_smem(KvForm form) {
     AttendSmem m;
-    m.work = static_cast<size_t>(kAttendRows) * 2 * kD * kv_elem;
+    m.work = static_cast<size_t>(kAttendRows) * attend_row_bytes(form);
     m.total = m.work + static_cast<size_t>(kAThreads) * 4 + (kAThreads + 4) * 4 +
               static_cast<size_t>(kRowKeys) * 4 + static_cast<size_t>(kAWarps) * kCombinePitch * 4 +
               32;
@@ -345,6 +349,7 @@ struct AArgs {
     const float* centre;
     const void* keys;
     const void* values;
+    const void* params;                          // 4-bit cache: steps and minima of each row
     float* pm;
     float* pl;
     float* po;
@@ -482,8 +487,11 @@ __global__ void __launch_bounds__(kThreads, 3) collide_kernel(const CArgs a) {
     }
 }
 
-// The 8 consecutive elements [8 hl, 8 hl + 8) of a staged K or V row as floats.
-__device__ __forceinline__ void load8(const uint8_t* p, const __nv_bfloat16*, float (&f)[8]) {
+// The 8 consecutive elements [8 hl, 8 hl + 8) of a staged K (value = 0) or V (value = 1) row as
+// floats. form is a tag: std::integral_constant<KvForm, ...>.
+__device__ __forceinline__ void load8(const uint8_t* row, int value, int hl,
+                                      std::integral_constant<KvForm, kKvBf16>, float (&f)[8]) {
+    const uint8_t* p = row + (value * kD + 8 * hl) * 2;
     const uint4 v = *reinterpret_cast<const uint4*>(p);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -493,11 +501,27 @@ __device__ __forceinline__ void load8(const uint8_t* p, const __nv_bfloat16*, fl
         f[2 * i + 1] = t.y;
     }
 }
-__device__ __forceinline__ void load8(const uint8_t* p, const float*, float (&f)[8]) {
+__device__ __forceinline__ void load8(const uint8_t* row, int value, int hl,
+                                      std::integral_constant<KvForm, kKvF32>, float (&f)[8]) {
+    const uint8_t* p = row + (value * kD + 8 * hl) * 4;
     const float4 a = *reinterpret_cast<const float4*>(p);
     const float4 b = *reinterpret_cast<const float4*>(p + 16);
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+// 4-bit rows: one word holds a lane's 8 codes; their group's step s and minimum z are one word of
+// the parameters. A code becomes the float 2^23 + code, less 2^23 + 8: exact; then one fused
+// multiply-add from the group's middle z + 8 s.
+__device__ __forceinline__ void load8(const uint8_t* row, int value, int hl,
+                                      std::integral_constant<KvForm, kKv4>, float (&f)[8]) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(row + value * MP_KV4_CODE_BYTES + 4 * hl);
+    const uint32_t pr = *reinterpret_cast<const uint32_t*>(row + 2 * MP_KV4_CODE_BYTES + 8 * value +
+                                                           4 * (hl >> 3));
+    const float s = __uint_as_float(pr << 16), z = __uint_as_float(pr & 0xffff0000u);
+    const float mid = fmaf(8.0f, s, z);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        f[i] = fmaf(__uint_as_float(((w >> (4 * i)) & 15u) | 0x4b000000u) - 8388616.0f, s, mid);
 }
 
 __device__ __forceinline__ unsigned atomic_add_acq_rel_gpu(unsigned* p, unsigned v) {
@@ -517,7 +541,10 @@ __device__ __forceinline__ unsigned atomic_add_acq_rel_gpu(unsigned* p, unsigned
 // Each warp copies and folds its own rows (row e goes to half-warp e mod 8) in a pipeline of
 // groups of four rows per half-warp through two sets of row slots in shared memory: the group
 // after next is copied (cp.async) into a group's slots as soon as that group is folded.
-template <typename KV>
+// KV: the form of the rows. The 4-bit cache holds its keys minus the centre: the dot products are
+// then those of the centred keys (the softmax does not see the difference), and the cosine needs
+// neither the centre nor q.mu.
+template <KvForm KV>
 __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -527,8 +554,10 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
     const bool exact = sb == a.nsb;              // this CTA takes T
     const int nsp = a.nsb + 1;                   // partials per query row
 
-    constexpr int kRowBytes = 2 * kD * static_cast<int>(sizeof(KV));     // K then V
+    constexpr int kRowBytes = attend_row_bytes(KV);
     constexpr int kPieces = kRowBytes / 16;
+    constexpr int kHalfBytes = KV == kKv4 ? MP_KV4_CODE_BYTES : kRowBytes / 2;   // of K, and of V
+    constexpr std::integral_constant<KvForm, KV> form{};
     constexpr int kWords = kAttendBlocks * 32;                            // selection words
     static_assert(kWords == kAThreads, "one selection word per thread");
     uint8_t* stage = smem;                                    // [kAttendRows] K/V row slots
@@ -544,11 +573,11 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         q8[i] = load_elem(a.q, a.q_bf16, static_cast<size_t>(row) * kD + 8 * hl + i);
-        mu8[i] = a.centre[static_cast<size_t>(bg) * kD + 8 * hl + i];
+        mu8[i] = KV == kKv4 ? 0.0f : a.centre[static_cast<size_t>(bg) * kD + 8 * hl + i];
     }
     wait_for_predecessor();                      // selection words, query norms
     const float4 st = a.qstat[row];
-    const float qn = st.x, qmu = st.y;
+    const float qn = st.x, qmu = KV == kKv4 ? 0.0f : st.y;
     const float rad = a.radius ? a.radius[bg] : 0.0f;   // MIPS: cos = q.(k - mu) / (|q| r)
 
     // ---- the rows of this CTA: T by arithmetic, or the selected keys of its blocks, found
@@ -615,9 +644,12 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = 0.0f;
     const uint8_t* Kg = reinterpret_cast<const uint8_t*>(a.keys) +
-                        static_cast<size_t>(bg) * a.ncap * kD * sizeof(KV);
+                        static_cast<size_t>(bg) * a.ncap * kHalfBytes;
     const uint8_t* Vg = reinterpret_cast<const uint8_t*>(a.values) +
-                        static_cast<size_t>(bg) * a.ncap * kD * sizeof(KV);
+                        static_cast<size_t>(bg) * a.ncap * kHalfBytes;
+    const uint8_t* Pg = KV == kKv4 ? reinterpret_cast<const uint8_t*>(a.params) +
+                                         static_cast<size_t>(bg) * a.ncap * 2 * MP_KV4_PARAMS
+                                   : nullptr;
     const bool weighted = !exact && a.K > 0;
     const int hw = 2 * warp + half;
     constexpr int kHalves = 2 * kAWarps;
@@ -633,7 +665,7 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
         for (int j = 0; j < NB; ++j) {
             const int r = j < cnt ? ent + j * kHalves : ent;
             float kf[8];
-            load8(stage + r * kRowBytes + 8 * hl * sizeof(KV), static_cast<const KV*>(nullptr), kf);
+            load8(stage + r * kRowBytes, 0, hl, form, kf);
             float d = 0.0f, k2 = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -702,8 +734,7 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
             const float wj = __shfl_sync(hmask, wgt, src0 + LPR * j);
             if (j < cnt) {
                 float vf[8];
-                load8(stage + (ent + j * kHalves) * kRowBytes + (kD + 8 * hl) * sizeof(KV),
-                      static_cast<const KV*>(nullptr), vf);
+                load8(stage + (ent + j * kHalves) * kRowBytes, 1, hl, form, vf);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) o[i] = fmaf(wj, vf[i], o[i]);
             }
@@ -730,8 +761,10 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
                               kSiteAttendRow))
                     continue;
                 for (int pc = lane; pc < kPieces; pc += 32) {
-                    const uint8_t* src = (pc < kPieces / 2 ? Kg : Vg) + key * kD * sizeof(KV) +
-                                         16 * (pc % (kPieces / 2));
+                    constexpr int kHalfPieces = kHalfBytes / 16;
+                    const uint8_t* src = (pc < kHalfPieces ? Kg : Vg) + key * kHalfBytes +
+                                         16 * (pc % kHalfPieces);
+                    if (KV == kKv4 && pc == 2 * kHalfPieces) src = Pg + key * 2 * MP_KV4_PARAMS;
                     cp_async16(stage + r * kRowBytes + 16 * pc, src);
                 }
             }
@@ -898,8 +931,9 @@ KernelFn pick_collide(int G) {
 
 typedef void (*AttendFn)(const AArgs);
 
-AttendFn pick_attend(bool kv_bf16) {
-    return kv_bf16 ? attend_kernel<__nv_bfloat16> : attend_kernel<float>;
+AttendFn pick_attend(KvForm form) {
+    return form == kKv4 ? attend_kernel<kKv4>
+                        : (form == kKvBf16 ? attend_kernel<kKvBf16> : attend_kernel<kKvF32>);
 }
 
 size_t collide_smem_for(int G, int cpad, int K) {
@@ -912,19 +946,16 @@ size_t collide_smem_for(int G, int cpad, int K) {
     }
 }
 
-size_t attend_smem_for(int nblk, bool kv_bf16) {
-    return attend_smem(attend_partials(nblk), kv_bf16 ? 2 : 4).total;
-}
+size_t attend_smem_for(KvForm form) { return attend_smem(form).total; }
 
 constexpr size_t kMaxSmem = 232448;   // 227 KB opt-in per CTA
 
 }  // namespace
 
-bool decode_supported(const DecodeShape& s, bool kv_bf16) {
+bool decode_supported(const DecodeShape& s, KvForm form) {
     const int G = s.Hq / s.Hkv;
     if (!pick_collide(G)) return false;
-    return collide_smem_for(G, s.cpad, s.K) <= kMaxSmem &&
-           attend_smem_for(s.nblk, kv_bf16) <= kMaxSmem;
+    return collide_smem_for(G, s.cpad, s.K) <= kMaxSmem && attend_smem_for(form) <= kMaxSmem;
 }
 
 cudaError_t prepare_decode() {
@@ -935,8 +966,8 @@ cudaError_t prepare_decode() {
                                              static_cast<int>(kMaxSmem));
         if (e != cudaSuccess) return e;
     }
-    for (int bf = 0; bf < 2; ++bf) {
-        cudaError_t e = cudaFuncSetAttribute(pick_attend(bf != 0),
+    for (KvForm form : {kKvF32, kKvBf16, kKv4}) {
+        cudaError_t e = cudaFuncSetAttribute(pick_attend(form),
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(kMaxSmem));
         if (e != cudaSuccess) return e;
@@ -949,8 +980,9 @@ cudaError_t prepare_decode() {
                          reinterpret_cast<const void*>(pick_collide(2)),
                          reinterpret_cast<const void*>(pick_collide(4)),
                          reinterpret_cast<const void*>(pick_collide(8)),
-                         reinterpret_cast<const void*>(pick_attend(false)),
-                         reinterpret_cast<const void*>(pick_attend(true))};
+                         reinterpret_cast<const void*>(pick_attend(kKvF32)),
+                         reinterpret_cast<const void*>(pick_attend(kKvBf16)),
+                         reinterpret_cast<const void*>(pick_attend(kKv4))};
     for (const void* f : fns) {
         cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
                                              cudaSharedmemCarveoutMaxShared);
@@ -1024,14 +1056,13 @@ CArgs scan_args(const uint32_t* codes, const DecodeShape& s, const DecodeScratch
 }  // namespace
 
 cudaError_t launch_collide(const void* q, bool q_bf16, const uint32_t* codes,
-                           const float* centre, const void* keys, const void* values,
-                           bool kv_bf16, const DecodeShape& s, float* out,
-                           const DecodeScratch& ws, cudaStream_t st, int blk0) {
+                           const float* centre, const KvRef& kv, const DecodeShape& s,
+                           float* out, const DecodeScratch& ws, cudaStream_t st, int blk0) {
     const int G = s.Hq / s.Hkv;
     const CArgs ca = scan_args(codes, s, ws, blk0);
     KernelFn scan = pick_collide(G);
     const size_t smem_scan = collide_smem_for(G, s.cpad, s.K);
-    if (!scan || smem_scan > kMaxSmem || attend_smem_for(s.nblk, kv_bf16) > kMaxSmem)
+    if (!scan || smem_scan > kMaxSmem || attend_smem_for(kv.form) > kMaxSmem)
         return cudaErrorNotSupported;
     if (blk0 < 0 || blk0 > s.nblk) return cudaErrorInvalidValue;
     if (blk0 < s.nblk) {
@@ -1039,23 +1070,24 @@ cudaError_t launch_collide(const void* q, bool q_bf16, const uint32_t* codes,
                                                dim3(kThreads), smem_scan, st, ca);
         if (e != cudaSuccess) return e;
     }
-    return launch_attend(q, q_bf16, centre, keys, values, kv_bf16, s, out, ws, st);
+    return launch_attend(q, q_bf16, centre, kv, s, out, ws, st);
 }
 
-cudaError_t launch_attend(const void* q, bool q_bf16, const float* centre, const void* keys,
-                          const void* values, bool kv_bf16, const DecodeShape& s, float* out,
-                          const DecodeScratch& ws, cudaStream_t st) {
+cudaError_t launch_attend(const void* q, bool q_bf16, const float* centre, const KvRef& kv,
+                          const DecodeShape& s, float* out, const DecodeScratch& ws,
+                          cudaStream_t st) {
     const int G = s.Hq / s.Hkv;
-    AttendFn attend = pick_attend(kv_bf16);
-    const size_t smem_att = attend_smem_for(s.nblk, kv_bf16);
+    AttendFn attend = pick_attend(kv.form);
+    const size_t smem_att = attend_smem_for(kv.form);
     if (smem_att > kMaxSmem) return cudaErrorNotSupported;
     AArgs aa;
     aa.selmask = ws.selmask;
     aa.qstat = ws.qstat;
     aa.q = q;
     aa.centre = centre;
-    aa.keys = keys;
-    aa.values = values;
+    aa.keys = kv.keys;
+    aa.values = kv.values;
+    aa.params = kv.params;
     aa.pm = ws.pm;
     aa.pl = ws.pl;
     aa.po = ws.po;
@@ -1078,10 +1110,7 @@ cudaError_t launch_attend(const void* q, bool q_bf16, const float* centre, const
     aa.status = device_status_ptr();
     aa.radius = s.radius;
     aa.scale = s.scale;
-    {
-        const AttendSmem m = attend_smem(attend_partials(s.nblk), kv_bf16 ? 2 : 4);
-        aa.work_bytes = static_cast<int>(m.work);
-    }
+    aa.work_bytes = static_cast<int>(attend_smem(kv.form).work);
     return launch_dependent(attend, dim3(aa.nsb + 1, s.B * s.Hq), dim3(kAThreads), smem_att, st,
                             aa);
 }

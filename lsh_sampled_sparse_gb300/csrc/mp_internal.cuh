@@ -90,6 +90,19 @@ struct DecodeShape {
     const float* logu_ext;   // cross-polytope: the caller's log u table (nullptr otherwise)
 };
 
+// The keys and values a decode attends to: rows of 128 fp32 or bf16 elements, or the 4-bit cache
+// (keys, values: its codes; params: its steps and minima; the keys are held minus their centre).
+enum KvForm : int { kKvF32 = 0, kKvBf16 = 1, kKv4 = 2 };
+struct KvRef {
+    const void* keys;
+    const void* values;
+    const void* params;  // kKv4 only
+    KvForm form;
+};
+inline KvRef kv_ref(const void* keys, const void* values, mp_dtype t) {
+    return KvRef{keys, values, nullptr, t == MP_BF16 ? kKvBf16 : kKvF32};
+}
+
 size_t decode_scratch_bytes(const DecodeShape& s, bool debug);
 // Shapes, parameters, dtypes, pointers and alignment of a decode call, everything but the
 // workspace (the checks of mp_decode_attention); fills *s on success.
@@ -130,14 +143,13 @@ cudaError_t launch_qencode(const void* q, bool q_bf16, const float* centre, cons
 // blk0 == 0), then the attend kernel over every block. cudaErrorNotSupported if it cannot fit a
 // CTA
 cudaError_t launch_collide(const void* q, bool q_bf16, const uint32_t* codes,
-                           const float* centre, const void* keys, const void* values,
-                           bool kv_bf16, const DecodeShape& s, float* out,
+                           const float* centre, const KvRef& kv, const DecodeShape& s, float* out,
                            const DecodeScratch& ws, cudaStream_t st, int blk0 = 0);
-bool decode_supported(const DecodeShape& s, bool kv_bf16);
+bool decode_supported(const DecodeShape& s, KvForm form);
 // the attend kernel alone, on selection words already in ws.selmask (masked with valid & not T)
-cudaError_t launch_attend(const void* q, bool q_bf16, const float* centre, const void* keys,
-                          const void* values, bool kv_bf16, const DecodeShape& s, float* out,
-                          const DecodeScratch& ws, cudaStream_t st);
+cudaError_t launch_attend(const void* q, bool q_bf16, const float* centre, const KvRef& kv,
+                          const DecodeShape& s, float* out, const DecodeScratch& ws,
+                          cudaStream_t st);
 
 // ---- bucketed hash tables (mp_buckets.cu) ------------------------------------------------------
 size_t bucket_table_bytes(int B, int Hkv, int n, int K, int L);   // 0 if unsupported
@@ -173,6 +185,20 @@ cudaError_t prepare_misc();
 cudaError_t prepare_append();
 cudaError_t prepare_mips();
 cudaError_t prepare_cross_polytope();
+cudaError_t prepare_kv4();
+
+// ---- 4-bit K/V cache (mp_kv4.cu) ----------------------------------------------------------------
+// rows [n_begin, n_begin + m) (or from positions[b] on) of every head written / read back
+cudaError_t launch_kv4_write(const void* keys, const void* values, bool bf16, const float* centre,
+                             int B, int Hkv, int m, int n_begin, const int32_t* positions,
+                             const mp_kv4& cache, cudaStream_t st);
+cudaError_t launch_kv4_read(const mp_kv4& cache, const float* centre, int B, int Hkv, int m,
+                            int n_begin, const int32_t* positions, void* keys, void* values,
+                            bool bf16, cudaStream_t st);
+size_t kv4_attention_scratch_bytes(int B, int Hq, int Hkv, int n);
+cudaError_t launch_kv4_attention(const void* q, bool q_bf16, const mp_kv4& cache, int B, int Hq,
+                                 int Hkv, int n, const int32_t* lengths, float scale, float* out,
+                                 void* workspace, cudaStream_t st);
 
 // ---- cross-polytope variant (mp_cross_polytope.cu) ----------------------------------------------
 size_t cp_codes_bytes(int B, int Hkv, int n, int L);
@@ -188,8 +214,7 @@ cudaError_t launch_qencode_cp(const void* q, bool q_bf16, const float* centre, c
                               cudaStream_t st);
 // the byte-code scan over blocks [blk0, nblk), then the attend kernel over every block
 cudaError_t launch_collide_cp(const void* q, bool q_bf16, const uint8_t* codes,
-                              const float* centre, const void* keys, const void* values,
-                              bool kv_bf16, const DecodeShape& s, float* out,
+                              const float* centre, const KvRef& kv, const DecodeShape& s, float* out,
                               const DecodeScratch& ws, cudaStream_t st, int blk0 = 0);
 
 // ---- MIPS -> cosine variant (mp_mips.cu) -------------------------------------------------------

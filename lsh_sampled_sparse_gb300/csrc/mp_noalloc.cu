@@ -70,7 +70,7 @@ extern "C" mp_status mp_decode_attention_noalloc(
     cudaError_t e = launch_qencode(q, q_dtype == MP_BF16, centre, W, w_dtype == MP_BF16, s, ws,
                                    stream);
     if (e != cudaSuccess) return MP_ERR_CUDA;
-    e = launch_collide(q, q_dtype == MP_BF16, codes, centre, keys, values, kv_dtype == MP_BF16, s,
-                       out, ws, stream);
+    e = launch_collide(q, q_dtype == MP_BF16, codes, centre, kv_ref(keys, values, kv_dtype), s, out,
+                       ws, stream);
     return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
 }
