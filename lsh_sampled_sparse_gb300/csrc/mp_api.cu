@@ -509,9 +509,8 @@ static mp_status check_kv4_rows(const void* keys, const void* values, mp_dtype t
         return MP_ERR_INVALID_ARG;
     *empty = m == 0;
     if (!*empty && (!keys || !values)) return MP_ERR_INVALID_ARG;
-    // one CTA takes 16 rows or more, and a grid 2^31 - 1 CTAs
-    if (static_cast<long long>(B) * Hkv > (16ll * 0x7fffffff) / std::max(m, 1))
-        return MP_ERR_INVALID_ARG;
+    // rows are numbered in 32 bits (2^31 of them are a TB of bf16)
+    if (static_cast<long long>(B) * Hkv > 0x7fffffffll / std::max(m, 1)) return MP_ERR_INVALID_ARG;
     return MP_OK;
 }
 

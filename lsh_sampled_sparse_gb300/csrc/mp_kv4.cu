@@ -4,17 +4,17 @@
 //
 // A group of 64 dims x_e (two per row) is held by z, the largest bf16 <= min x, s, the smallest
 // bf16 with z + 15 s >= max x, and codes c_e = rint((x_e - z) / s), so |x_e - (z + s c_e)| <= s / 2.
-// 15 s is exact in float32 (8 + 4 bits), so s is RU_bf16(RU((max - z)) / 15): if 15 s reaches the
-// rounded-up difference it reaches the exact one, and conversely.
+// 15 s is exact in float32 (8 + 4 bits), so that it reaches max - z exactly where it reaches that
+// difference rounded up.
 #include <algorithm>
+
+#include <cuda_fp16.h>
 
 #include "mp_internal.cuh"
 
 namespace mp {
 namespace {
 
-constexpr int kGroup = MP_KV4_GROUP;
-constexpr int kGroups = kD / kGroup;
 constexpr int kCodeBytes = MP_KV4_CODE_BYTES;
 
 __device__ __forceinline__ float min_nan(float a, float b) {
@@ -29,23 +29,22 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 
 // The high half of a float is a bf16: rounding down drops the low half, one step further from
-// zero for a negative value whose low half is not 0; rounding up mirrors it.
+// zero for a negative value whose low half is not 0.
 __device__ __forceinline__ uint32_t bf16_below(float x) {
     const uint32_t u = __float_as_uint(x), t = u >> 16;
     return t + ((u >> 31) != 0u && (u & 0xffffu) != 0u ? 1u : 0u);
 }
-__device__ __forceinline__ uint32_t bf16_above_positive(float x) {
-    const uint32_t u = __float_as_uint(x);
-    return (u >> 16) + ((u & 0xffffu) != 0u ? 1u : 0u);
-}
 
 // s (low half) and z (high half) of a group from its minimum and maximum; NaN in both for a group
-// that has no finite pair (min_nan and max_nan pass a NaN on).
+// that has no finite pair (min_nan and max_nan pass a NaN on). s starts at the bf16 below a product
+// that is less than d / 15 by a millionth, so at most two steps below the smallest with 15 s >= d.
 __device__ __forceinline__ uint32_t group_params(float lo, float hi) {
     const uint32_t z = bf16_below(lo);
     const float d = __fsub_ru(hi, __uint_as_float(z << 16));
-    const uint32_t s = bf16_above_positive(__fdiv_ru(d, 15.0f));
-    const bool finite = (z & 0x7f80u) != 0x7f80u && (s & 0x7f80u) != 0x7f80u && d == d;
+    uint32_t s = __float_as_uint(d * 0.0666666f) >> 16;
+    if (15.0f * __uint_as_float(s << 16) < d) ++s;
+    if (15.0f * __uint_as_float(s << 16) < d) ++s;
+    const bool finite = (z & 0x7f80u) != 0x7f80u && (s & 0x7f80u) < 0x7f80u && d < INFINITY;
     return finite ? (s | (z << 16)) : 0x7fc07fc0u;
 }
 
@@ -53,6 +52,48 @@ __device__ __forceinline__ uint32_t group_params(float lo, float hi) {
 __device__ __noinline__ uint32_t code_exact(float x, float z, float s) {
     const double v = (static_cast<double>(x) - static_cast<double>(z)) / static_cast<double>(s);
     return static_cast<uint32_t>(static_cast<int>(rint(v)));
+}
+
+// The 16 codes of x (a quarter of a group) as two words.
+// With t = x - z and 1/s as two floats, the quotient is rounded once and then, by adding 1.5 2^23,
+// to an integer f, ties to even. t - f s is exact near s / 2 (one fused multiply-add), and tells
+// whether f is the nearest: values that are bf16 (kBf16) make t exact too, unless a border lies at
+// x = 0 and x is tiny, so that |t - f s| > s / 2 alone, or such a border, asks for 64 bits; other
+// values ask for them within 2^-18 of a border. Steps near the ends of float32's range do always.
+template <bool kBf16>
+__device__ __forceinline__ uint2 codes16(const float (&x)[16], uint32_t pr) {
+    const float s = __uint_as_float(pr << 16), z = __uint_as_float(pr & 0xffff0000u);
+    if (!(s > 0.0f)) return make_uint2(0u, 0u);                  // constant, or not a number
+    constexpr float kRound = 12582912.0f;
+    const float inv = __frcp_rn(s), low = fmaf(-s, inv, 1.0f) * inv;
+    const float half = kBf16 ? 0.5f * s : 0.5f * s * (1.0f - 3.8e-6f);
+    float worst = 0.0f;
+    uint32_t w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        w[k] = 0u;
+#pragma unroll
+        for (int i = 7; i >= 0; --i) {
+            const float t = x[8 * k + i] - z;
+            const float y = __fadd_rn(fmaf(t, inv, t * low), kRound);
+            worst = fmaxf(worst, fabsf(fmaf(-(y - kRound), s, t)));
+            // the low bits of y are its integer; what its high bits add up to is taken off below
+            w[k] = (w[k] << 4) + __float_as_uint(y);
+        }
+        w[k] -= 0x4b400000u * 0x11111111u;
+    }
+    bool ask = kBf16 ? worst > half : worst >= half;
+    ask = ask || s < 1e-30f || s > 1e30f;
+    if (kBf16) {
+        const float c = floorf(-z * inv);                        // is z + (c + 1/2) s = 0 ?
+        ask = ask || (c >= 0.0f && c < 15.0f && fmaf(c + 0.5f, s, z) == 0.0f);
+    }
+    if (ask) {
+        w[0] = w[1] = 0u;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i >> 3] |= code_exact(x[i], z, s) << (4 * (i & 7));
+    }
+    return make_uint2(w[0], w[1]);
 }
 
 struct RowArgs {
@@ -63,102 +104,178 @@ struct RowArgs {
     uint8_t* k_codes;
     uint8_t* v_codes;
     uint8_t* params;
-    long long rows;                              // B * Hkv * m
-    int Hkv, m, n_begin, ncap;
+    uint32_t rows;                               // B * Hkv * m
+    uint32_t m;
+    int Hkv, n_begin, ncap;
 };
 
-// The cache row (over all heads) of row r of the call, or -1 where it falls outside the cache.
-__device__ __forceinline__ long long cache_row(const RowArgs& a, long long r) {
-    const long long bh = r / a.m;
-    const int i = static_cast<int>(r - bh * a.m);
+// The cache row (over all heads) of token i of the call's head bh, -1 where it is outside.
+__device__ __forceinline__ long long cache_row(const RowArgs& a, uint32_t bh, uint32_t i) {
     const long long pos =
         static_cast<long long>(a.positions ? __ldg(a.positions + bh / a.Hkv) : a.n_begin) + i;
-    return pos >= 0 && pos < a.ncap ? bh * a.ncap + pos : -1;
+    return pos >= 0 && pos < a.ncap ? static_cast<long long>(bh) * a.ncap + pos : -1;
 }
 
 constexpr int kRowThreads = 256;
+constexpr int kRowLanes = 8;                     // lanes a row: 16 dims each, four a group
+constexpr int kRowsPerCta = kRowThreads / kRowLanes;
 
-// A half-warp per row, 8 dims (one word of codes) a lane; a group is 8 lanes.
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads) kv4_write_kernel(const RowArgs a) {
-    const int hl = threadIdx.x & 15;
-    const long long r = (static_cast<long long>(blockIdx.x) * kRowThreads + threadIdx.x) >> 4;
-    const bool live = r < a.rows;
-    const long long row = live ? cache_row(a, r) : -1;
-    for (int value = 0; value < 2; ++value) {
-        float x[8];
-        const T* src = static_cast<const T*>(value ? a.values : a.keys);
+__device__ __forceinline__ void load16(const float* p, float (&x)[16]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = row >= 0 ? to_float(src[r * kD + 8 * hl + i]) : 0.0f;
-        if (!value && a.centre && live) {
-            const float* mu = a.centre + (r / a.m) * kD + 8 * hl;
+    for (int i = 0; i < 4; ++i) {
+        const float4 v = __ldcs(reinterpret_cast<const float4*>(p) + i);
+        x[4 * i] = v.x;
+        x[4 * i + 1] = v.y;
+        x[4 * i + 2] = v.z;
+        x[4 * i + 3] = v.w;
+    }
+}
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&x)[16]) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __fsub_rn(x[i], mu[i]);
-        }
-        float lo = x[0], hi = x[0];
+    for (int i = 0; i < 2; ++i) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 1; i < 8; ++i) {
-            lo = min_nan(lo, x[i]);
-            hi = max_nan(hi, x[i]);
-        }
-#pragma unroll
-        for (int o = 4; o; o >>= 1) {
-            lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-            hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        }
-        const uint32_t pr = group_params(lo, hi);
-        const float s = __uint_as_float(pr << 16), z = __uint_as_float(pr & 0xffff0000u);
-        uint32_t w = 0u;
-        if (s > 0.0f) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w |= code_exact(x[i], z, s) << (4 * i);
-        }
-        if (row >= 0) {
-            uint8_t* codes = value ? a.v_codes : a.k_codes;
-            *reinterpret_cast<uint32_t*>(codes + row * kCodeBytes + 4 * hl) = w;
-            if ((hl & 7) == 0)
-                *reinterpret_cast<uint32_t*>(a.params + row * 16 + 8 * value + 4 * (hl >> 3)) = pr;
+        for (int k = 0; k < 4; ++k) {
+            x[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
+            x[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
         }
     }
 }
 
+// The parameters of a lane's group (four lanes) from its 16 values.
+__device__ __forceinline__ uint32_t lane_params(const float (&x)[16]) {
+    float lo = x[0], hi = x[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) {
+        lo = min_nan(lo, x[i]);
+        hi = max_nan(hi, x[i]);
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    return group_params(lo, hi);
+}
+
+// Eight lanes a row, four rows a warp; key and value of a row are loaded before either is coded.
 template <typename T>
-__device__ __forceinline__ T from_float(float x);
-template <>
-__device__ __forceinline__ float from_float<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) {
-    return __float2bfloat16_rn(x);
+__global__ void __launch_bounds__(kRowThreads) kv4_write_kernel(const RowArgs a) {
+    constexpr bool kBf16 = sizeof(T) == 2;
+    const int rl = threadIdx.x & (kRowLanes - 1);
+    const uint32_t r = blockIdx.x * kRowsPerCta + threadIdx.x / kRowLanes;
+    const bool live = r < a.rows;
+    const uint32_t bh = live ? r / a.m : 0u;
+    const long long row = live ? cache_row(a, bh, r - bh * a.m) : -1;
+    const size_t at = static_cast<size_t>(row >= 0 ? r : 0u) * kD + 16 * rl;   // a row that exists
+    float k[16], v[16];
+    load16(static_cast<const T*>(a.keys) + at, k);
+    load16(static_cast<const T*>(a.values) + at, v);
+    if (a.centre) {
+        const float4* mu = reinterpret_cast<const float4*>(a.centre + static_cast<size_t>(bh) * kD +
+                                                           16 * rl);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 c = __ldg(mu + i);
+            k[4 * i] = __fsub_rn(k[4 * i], c.x);
+            k[4 * i + 1] = __fsub_rn(k[4 * i + 1], c.y);
+            k[4 * i + 2] = __fsub_rn(k[4 * i + 2], c.z);
+            k[4 * i + 3] = __fsub_rn(k[4 * i + 3], c.w);
+        }
+    }
+    const uint32_t kp = lane_params(k), vp = lane_params(v);
+    const uint2 kc = codes16<false>(k, kp), vc = codes16<kBf16>(v, vp);
+    const uint32_t kp1 = __shfl_down_sync(0xffffffffu, kp, 4);
+    const uint32_t vp1 = __shfl_down_sync(0xffffffffu, vp, 4);
+    if (row < 0) return;
+    *reinterpret_cast<uint2*>(a.k_codes + row * kCodeBytes + 8 * rl) = kc;
+    *reinterpret_cast<uint2*>(a.v_codes + row * kCodeBytes + 8 * rl) = vc;
+    if (rl == 0) *reinterpret_cast<uint4*>(a.params + row * 16) = make_uint4(kp, kp1, vp, vp1);
+}
+
+__device__ __forceinline__ void store16(float* p, const float (&x)[16]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        __stcs(reinterpret_cast<float4*>(p) + i,
+               make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+}
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&x)[16]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[8 * i + 2 * k], x[8 * i + 2 * k + 1]);
+            w[k] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        __stcs(reinterpret_cast<uint4*>(p) + i, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+}
+
+// z + s c, one rounding
+__device__ __forceinline__ void values16(uint2 c, uint32_t pr, float (&x)[16]) {
+    const float s = __uint_as_float(pr << 16), z = __uint_as_float(pr & 0xffff0000u);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t n = ((i < 8 ? c.x : c.y) >> (4 * (i & 7))) & 15u;
+        x[i] = fmaf(s, __uint_as_float(n | 0x4b000000u) - 8388608.0f, z);
+    }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const RowArgs a) {
-    const int hl = threadIdx.x & 15;
-    const long long r = (static_cast<long long>(blockIdx.x) * kRowThreads + threadIdx.x) >> 4;
+    const int rl = threadIdx.x & (kRowLanes - 1);
+    const uint32_t r = blockIdx.x * kRowsPerCta + threadIdx.x / kRowLanes;
     if (r >= a.rows) return;
-    const long long row = cache_row(a, r);
-    for (int value = 0; value < 2; ++value) {
-        T* dst = static_cast<T*>(const_cast<void*>(value ? a.values : a.keys)) + r * kD + 8 * hl;
-        uint32_t w = 0u, pr = 0u;
-        if (row >= 0) {
-            w = *reinterpret_cast<const uint32_t*>((value ? a.v_codes : a.k_codes) +
-                                                   row * kCodeBytes + 4 * hl);
-            pr = *reinterpret_cast<const uint32_t*>(a.params + row * 16 + 8 * value + 4 * (hl >> 3));
-        }
-        const float s = __uint_as_float(pr << 16), z = __uint_as_float(pr & 0xffff0000u);
+    const uint32_t bh = r / a.m;
+    const long long row = cache_row(a, bh, r - bh * a.m);
+    uint2 kc = make_uint2(0u, 0u), vc = kc;
+    uint32_t kp = 0u, vp = 0u;
+    if (row >= 0) {
+        kc = *reinterpret_cast<const uint2*>(a.k_codes + row * kCodeBytes + 8 * rl);
+        vc = *reinterpret_cast<const uint2*>(a.v_codes + row * kCodeBytes + 8 * rl);
+        kp = *reinterpret_cast<const uint32_t*>(a.params + row * 16 + 4 * (rl >> 2));
+        vp = *reinterpret_cast<const uint32_t*>(a.params + row * 16 + 8 + 4 * (rl >> 2));
+    }
+    float x[16];
+    values16(kc, kp, x);
+    if (a.centre && row >= 0) {
+        const float4* mu = reinterpret_cast<const float4*>(a.centre + static_cast<size_t>(bh) * kD +
+                                                           16 * rl);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float x = fmaf(s, static_cast<float>((w >> (4 * i)) & 15u), z);
-            if (!value && a.centre && row >= 0)
-                x = __fadd_rn(x, a.centre[(r / a.m) * kD + 8 * hl + i]);
-            dst[i] = from_float<T>(x);
+        for (int i = 0; i < 4; ++i) {
+            const float4 c = __ldg(mu + i);
+            x[4 * i] = __fadd_rn(x[4 * i], c.x);
+            x[4 * i + 1] = __fadd_rn(x[4 * i + 1], c.y);
+            x[4 * i + 2] = __fadd_rn(x[4 * i + 2], c.z);
+            x[4 * i + 3] = __fadd_rn(x[4 * i + 3], c.w);
         }
     }
+    const size_t at = static_cast<size_t>(r) * kD + 16 * rl;
+    store16(static_cast<T*>(const_cast<void*>(a.keys)) + at, x);
+    values16(vc, vp, x);
+    store16(static_cast<T*>(const_cast<void*>(a.values)) + at, x);
 }
 
 // ------------------------------------------------------------------------------------------------
-// Exact attention of one query token: one CTA per (split of the tokens, query row), a warp per
-// token, four dims a lane; partial softmaxes merged by a second kernel.
+// Exact attention of one query token per sequence.
+//
+// With a key's codes c, step s and minimum z per group, q.k = sum_g s_g (sum_e q_e (c_e - 8)) +
+// (z_g + 8 s_g) sum_e q_e, and the value sum likewise: the products of codes with queries and of
+// codes with weights are matrix products of small exact integers, which the warp's tensor-core
+// instruction m16n8k16 (fp16 in, fp32 sums) takes with the 16 tokens or 16 dims as its rows and
+// four query heads as its eight columns, each head as two fp16 halves (22 bits). Steps and minima
+// join outside, in fp32. The tcgen05 instructions want 128 rows and operands unpacked into shared
+// memory, where a byte of codes would become four; here codes go from shared memory to fragments
+// in registers, an instruction of unpacking per value.
+//
+// A warp takes tiles of 64 tokens on its own, two in flight (cp.async; rows of 64 bytes whose
+// 16-byte pieces are exchanged so that ldmatrix meets no bank conflict): logits of the tile, one
+// step of the running maximum, weights, weighted codes summed from zero and added to the running
+// sums in fp32 (the tensor core's own sums round toward zero: kept short, they lose nothing that
+// matters, and the codes of odd tokens are taken minus 7, of even ones minus 8, so that the part
+// of a sum that the minima take back again stays near zero).
 // ------------------------------------------------------------------------------------------------
 struct A4Args {
     const void* q;
@@ -168,90 +285,461 @@ struct A4Args {
     const int32_t* lengths;
     float* part;                                 // [row][split][kPart]: o, m, l
     float* out;
-    int q_bf16, Hq, Hkv, n, ncap, splits, per_split;
-    float scale;
+    int q_bf16, Hq, Hkv, G, n, ncap, splits, chunks;
+    int tiles_per_split;
+    float scale;                                 // of q.k, times log2 e
 };
 constexpr int kPart = kD + 4;
 constexpr int kAttWarps = 4;
+constexpr int kAttThreads = 32 * kAttWarps;
+constexpr int kTile = 64;                        // tokens of a warp's tile
+constexpr int kSub = kTile / 16;                 // fragments of 16 tokens in it
+constexpr int kParamBytes = 2 * MP_KV4_PARAMS;
+constexpr int kStageK = 0, kStageV = kTile * kCodeBytes, kStageP = 2 * kTile * kCodeBytes;
+constexpr int kStageBytes = kStageP + kTile * kParamBytes;
+constexpr int kAttStages = 2;
+constexpr int kAttSmem = kAttWarps * kAttStages * kStageBytes;
+constexpr int kSms = 152;                        // of a GB300; a plan, and so a workspace's size,
+                                                 // is the same on the host alone
+constexpr int kMergePitch = kD + 4;              // floats a (warp, head) leaves for the CTA's merge
+static_assert(kAttThreads == kD, "the merge: a thread per dim");
+static_assert(kAttWarps * 8 * kMergePitch * 4 <= kAttSmem, "the merge reuses the stages");
 
-__device__ __forceinline__ int length_of(const A4Args& a, int b) {
-    return a.lengths ? max(0, min(a.n, __ldg(a.lengths + b))) : a.n;
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(live ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// The largest of a warp's unsigned numbers
+__device__ __forceinline__ uint32_t warp_max(uint32_t x) {
+    return __reduce_max_sync(0xffffffffu, x);
 }
 
-__global__ void __launch_bounds__(32 * kAttWarps) kv4_attention_kernel(const A4Args a) {
-    __shared__ float sm[kAttWarps][kPart];
+// Eight codes of a word as four fp16 pairs: pair i holds code i of the low half and code i of the
+// high half, less `lo` and `hi`. The nibble becomes the low bits of 1024 + c or bits 4-7 of
+// 64 + c; the constants take both away, exactly.
+template <int lo, int hi>
+__device__ __forceinline__ void unpack_pairs(uint32_t w, uint32_t (&h)[4]) {
+    constexpr uint32_t kA = (0xe400u + lo) | ((0xe400u + hi) << 16);               // -(1024 + x)
+    constexpr uint32_t kB = (0xd400u + 16 * lo) | ((0xd400u + 16 * hi) << 16);     // -(64 + x)
+    const uint32_t u = w >> 8;
+    h[0] = hadd2((w & 0x000f000fu) | 0x64006400u, kA);
+    h[1] = hadd2((w & 0x00f000f0u) | 0x54005400u, kB);
+    h[2] = hadd2((u & 0x000f000fu) | 0x64006400u, kA);
+    h[3] = hadd2((u & 0x00f000f0u) | 0x54005400u, kB);
+}
+
+// x as two fp16: its leading 11 bits in the low half, the rest of it in the high half
+__device__ __forceinline__ uint32_t split_f16(float x) {
+    const float hi = __uint_as_float(__float_as_uint(x) & 0xffffe000u);
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(x - hi), "f"(hi));
+    return r;
+}
+
+// One CTA per (head of keys and values, split of its tokens, chunk of 4 NT query heads of the
+// group). Lane (r, t) = (lane / 4, lane % 4) holds query head t (and t + 4 where NT = 2) of the
+// logits, weights and sums: tokens r and r + 8 of a fragment, dims 32 m + 4 r .. + 3.
+template <int NT>
+__global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
+    kv4_attention_kernel(const A4Args a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long row = blockIdx.x / a.splits;
-    const int split = static_cast<int>(blockIdx.x % a.splits);
-    const int b = static_cast<int>(row / a.Hq), h = static_cast<int>(row % a.Hq);
-    const long long bh = static_cast<long long>(b) * a.Hkv + h / (a.Hq / a.Hkv);
-    const int k0 = split * a.per_split, k1 = min(length_of(a, b), k0 + a.per_split);
-    float q[4], o[4] = {0.0f, 0.0f, 0.0f, 0.0f}, m = -INFINITY, l = 0.0f;
+    const int r = lane >> 2, t = lane & 3;
+    allow_dependents();
+    const unsigned ch = blockIdx.x % a.chunks, rest = blockIdx.x / a.chunks;
+    const int split = static_cast<int>(rest % a.splits);
+    const size_t bh = rest / a.splits;
+    const int b = static_cast<int>(bh / a.Hkv);
+    const int h0 = static_cast<int>(ch) * 4 * NT;                        // first head of the chunk
+    const size_t row0 = static_cast<size_t>(b) * a.Hq + (bh - static_cast<size_t>(b) * a.Hkv) * a.G +
+                        h0;
+    const int heads = min(4 * NT, a.G - h0);
+    const int len = a.lengths ? max(0, min(a.n, __ldg(a.lengths + b))) : a.n;
+    const int tile0 = split * a.tiles_per_split;
+    const int end = static_cast<int>(min(static_cast<long long>(len),    // tokens [.., end)
+                                         (tile0 + a.tiles_per_split) * static_cast<long long>(kTile)));
+    const int ntiles = (end - tile0 * kTile + kTile - 1) / kTile;        // <= 0: none
+    const int mine = ntiles > warp ? (ntiles - warp + kAttWarps - 1) / kAttWarps : 0;
+
+    const uint32_t stage0 = smem_u32(smem) + warp * kAttStages * kStageBytes;
+    const uint8_t* kg = a.k_codes + bh * a.ncap * kCodeBytes;
+    const uint8_t* vg = a.v_codes + bh * a.ncap * kCodeBytes;
+    const uint8_t* pg = a.params + bh * a.ncap * kParamBytes;
+    // a tile's copies: 16-byte piece lane % 4 of rows lane / 4 + 8 i to piece (lane % 4) ^
+    // (row / 2 % 4); rows past the end read as zero
+    const uint32_t swz = (lane >> 2) * kCodeBytes + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+    auto issue = [&](int it) {
+        if (it < mine) {
+            const int key0 = (tile0 + warp + it * kAttWarps) * kTile;
+            const uint32_t st = stage0 + (it & 1) * kStageBytes;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = load_elem(a.q, a.q_bf16, row * kD + 4 * lane + i) * a.scale;
-    for (int k = k0 + warp; k < k1; k += kAttWarps) {
-        const long long at = bh * a.ncap + k;
-        const uint32_t kw = *reinterpret_cast<const uint16_t*>(a.k_codes + at * kCodeBytes + 2 * lane);
-        const uint32_t vw = *reinterpret_cast<const uint16_t*>(a.v_codes + at * kCodeBytes + 2 * lane);
-        const uint32_t kp = *reinterpret_cast<const uint32_t*>(a.params + at * 16 + 4 * (lane >> 4));
-        const uint32_t vp = *reinterpret_cast<const uint32_t*>(a.params + at * 16 + 8 + 4 * (lane >> 4));
-        const float ks = __uint_as_float(kp << 16), kz = __uint_as_float(kp & 0xffff0000u);
-        const float vs = __uint_as_float(vp << 16), vz = __uint_as_float(vp & 0xffff0000u);
-        float d = 0.0f;
+            for (int i = 0; i < kTile / 8; ++i) {
+                const int key = key0 + 8 * i + (lane >> 2);
+                const bool live = key < end;
+                const size_t off = static_cast<size_t>(live ? key : 0) * kCodeBytes + 16 * (lane & 3);
+                copy16(st + kStageK + 8 * i * kCodeBytes + swz, kg + off, live);
+                copy16(st + kStageV + 8 * i * kCodeBytes + swz, vg + off, live);
+            }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            d = fmaf(q[i], fmaf(ks, static_cast<float>((kw >> (4 * i)) & 15u), kz), d);
+            for (int i = 0; i < kTile / 32; ++i) {
+                const int key = key0 + 32 * i + lane;
+                const bool live = key < end;
+                copy16(st + kStageP + (32 * i + lane) * kParamBytes,
+                       pg + static_cast<size_t>(live ? key : 0) * kParamBytes, live);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    issue(0);
+    issue(1);
+
+    // ---- the queries as column fragments: column 2 h is head h's leading half, 2 h + 1 the rest.
+    // A lane loads head lane / 8 of its four (dims 32 m + 8 t ..), scaled by a power of two so
+    // that the largest element lies in [1, 2); fac undoes it on the logits.
+    uint32_t qb[NT][4][4];
+    float fac[NT], qsum[NT][2];
 #pragma unroll
-        for (int s = 16; s; s >>= 1) d += __shfl_xor_sync(0xffffffffu, d, s);
-        const float mn = fmaxf(m, d);
-        const float corr = expf(m - mn), w = expf(d - mn);
-        l = fmaf(l, corr, w);
+    for (int nt = 0; nt < NT; ++nt) {
+        const int h = 4 * nt + (lane >> 3);
+        float x[4][8];
+        uint32_t big = 0u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            o[i] = fmaf(w, fmaf(vs, static_cast<float>((vw >> (4 * i)) & 15u), vz), o[i] * corr);
-        m = mn;
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[m][e] = h < heads ? load_elem(a.q, a.q_bf16, (row0 + h) * kD + 32 * m + 8 * t + e)
+                                    : 0.0f;
+                big = max(big, __float_as_uint(x[m][e]) & 0x7fffffffu);
+            }
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        const uint32_t ex = min(max(big >> 23, 1u), 253u);
+        const float down = __uint_as_float((254u - ex) << 23), up = __uint_as_float(ex << 23);
+        float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[m][e] *= down;
+                sum[m >> 1] += x[m][e];
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                // the leading half rounded to nearest, the rest; this lane's column keeps one
+                const __half2 lead = __floats2half2_rn(x[m][e], x[m][e + 4]);
+                const float2 lf = __half22float2(lead);
+                const __half2 rem = __floats2half2_rn(x[m][e] - lf.x, x[m][e + 4] - lf.y);
+                const __half2 keep = (r & 1) ? rem : lead;
+                qb[nt][m][e] = *reinterpret_cast<const uint32_t*>(&keep);
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+            sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+            qsum[nt][g] = __shfl_sync(0xffffffffu, sum[g], 8 * t);
+        }
+        fac[nt] = __shfl_sync(0xffffffffu, a.scale * up, 8 * t);
     }
+
+    float m_run[NT], l_run[NT], mid_run[NT][2], o_run[NT][4][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sm[warp][4 * lane + i] = o[i];
-    if (lane == 0) {
-        sm[warp][kD] = m;
-        sm[warp][kD + 1] = l;
+    for (int nt = 0; nt < NT; ++nt) {
+        m_run[nt] = -INFINITY;
+        l_run[nt] = mid_run[nt][0] = mid_run[nt][1] = 0.0f;
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o_run[nt][m][e] = 0.0f;
+    }
+    const float mid_steps = (r & 1) ? 7.0f : 8.0f;                       // of this lane's values
+    const uint32_t lm = (lane & 7) * kCodeBytes + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+
+    for (int it = 0; it < mine; ++it) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+        const uint32_t st = stage0 + (it & 1) * kStageBytes;
+        const uint8_t* prm = smem + (st - smem_u32(smem)) + kStageP;
+        const int key0 = (tile0 + warp + it * kAttWarps) * kTile;
+
+        // ---- logits (base 2) of tokens 16 j + r and 16 j + 8 + r
+        float lg[NT][2 * kSub];
+        uint32_t vmax[2] = {0u, 0u};
+#pragma unroll
+        for (int j = 0; j < kSub; ++j) {
+            uint32_t k0[4], k1[4];
+            ldmatrix4(k0, st + kStageK + (16 * j) * kCodeBytes + lm);
+            ldmatrix4(k1, st + kStageK + (16 * j + 8) * kCodeBytes + lm);
+            float c[NT][2][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) c[nt][g][e] = 0.0f;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                uint32_t x0[4], x1[4];
+                unpack_pairs<8, 8>(k0[m], x0);
+                unpack_pairs<8, 8>(k1[m], x1);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma16816(c[nt][m >> 1], x0[0], x1[0], x0[1], x1[1], qb[nt][m][0], qb[nt][m][1]);
+                    mma16816(c[nt][m >> 1], x0[2], x1[2], x0[3], x1[3], qb[nt][m][2], qb[nt][m][3]);
+                }
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int row = 16 * j + 8 * half + r;
+                const uint4 p = *reinterpret_cast<const uint4*>(prm + row * kParamBytes);
+                const float s0 = __uint_as_float(p.x << 16), s1 = __uint_as_float(p.y << 16);
+                const float mid0 = fmaf(8.0f, s0, __uint_as_float(p.x & 0xffff0000u));
+                const float mid1 = fmaf(8.0f, s1, __uint_as_float(p.y & 0xffff0000u));
+                // the values' largest step, of those that are numbers (a NaN step is its own row's)
+                const uint32_t v0 = p.z << 16, v1 = p.w << 16;
+                vmax[0] = max(vmax[0], v0 < 0x7f800000u ? v0 : 0u);
+                vmax[1] = max(vmax[1], v1 < 0x7f800000u ? v1 : 0u);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float u = s0 * (c[nt][0][2 * half] + c[nt][0][2 * half + 1]);
+                    u = fmaf(s1, c[nt][1][2 * half] + c[nt][1][2 * half + 1], u);
+                    u = fmaf(mid0, qsum[nt][0], u);
+                    u = fmaf(mid1, qsum[nt][1], u);
+                    lg[nt][2 * j + half] = key0 + row < end ? u * fac[nt] : -INFINITY;
+                }
+            }
+        }
+
+        // ---- one step of the running softmax; weights in place of the logits
+        float corr[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float mt = lg[nt][0];
+#pragma unroll
+            for (int i = 1; i < 2 * kSub; ++i) mt = fmaxf(mt, lg[nt][i]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+            const float mn = fmaxf(m_run[nt], mt);
+            const float base = mn == -INFINITY ? 0.0f : mn;
+            corr[nt] = exp2_fast(m_run[nt] - base);
+            m_run[nt] = mn;
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2 * kSub; ++i) {
+                lg[nt][i] = exp2_fast(lg[nt][i] - base);
+                sum += lg[nt][i];
+            }
+            l_run[nt] = fmaf(l_run[nt], corr[nt], sum);
+            mid_run[nt][0] *= corr[nt];
+            mid_run[nt][1] *= corr[nt];
+        }
+        // weights times steps become fp16 halves after a power of two per group brings the tile's
+        // largest step to [2^13, 2^14): 2^(140 - ex), taken back by 2^(ex - 140)
+        float down[2], up[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const uint32_t ex = max(warp_max(vmax[g]) >> 23, 14u);
+            down[g] = __uint_as_float((267u - ex) << 23);
+            up[g] = __uint_as_float((ex - 13u) << 23);
+        }
+
+        // ---- weighted codes of the tile
+        float acc[NT][4][2][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[nt][m][i][e] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kSub; ++j) {
+            uint32_t v0[4], v1[4], wb[NT][2][2];
+            ldmatrix4_trans(v0, st + kStageV + (16 * j) * kCodeBytes + lm);
+            ldmatrix4_trans(v1, st + kStageV + (16 * j + 8) * kCodeBytes + lm);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int row = 16 * j + 8 * half + r;
+                const uint2 p = *reinterpret_cast<const uint2*>(prm + row * kParamBytes + 8);
+                const uint32_t pw[2] = {p.x, p.y};
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const float s = __uint_as_float(pw[g] << 16);
+                    const float mid = fmaf(mid_steps, s, __uint_as_float(pw[g] & 0xffff0000u));
+                    const float sd = s * down[g];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float w = lg[nt][2 * j + half];
+                        mid_run[nt][g] = fmaf(w, mid, mid_run[nt][g]);
+                        wb[nt][g][half] = transpose8x8(split_f16(w * sd));
+                    }
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                uint32_t x0[4], x1[4];
+                unpack_pairs<8, 7>(v0[m], x0);
+                unpack_pairs<8, 7>(v1[m], x1);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint32_t b0 = wb[nt][m >> 1][0], b1 = wb[nt][m >> 1][1];
+                    mma16816(acc[nt][m][0], x0[0], x0[1], x1[0], x1[1], b0, b1);
+                    mma16816(acc[nt][m][1], x0[2], x0[3], x1[2], x1[3], b0, b1);
+                }
+            }
+        }
+        __syncwarp();
+        issue(it + 2);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        o_run[nt][m][2 * i + e] =
+                            fmaf(acc[nt][m][i][2 * e] + acc[nt][m][i][2 * e + 1], up[m >> 1],
+                                 o_run[nt][m][2 * i + e] * corr[nt]);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+
+    // ---- sums over the lanes of a head, then the CTA's four warps in order
+    __syncthreads();
+    float* join = reinterpret_cast<float*>(smem);                        // [head][warp][kMergePitch]
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            l_run[nt] += __shfl_xor_sync(0xffffffffu, l_run[nt], o);
+            mid_run[nt][0] += __shfl_xor_sync(0xffffffffu, mid_run[nt][0], o);
+            mid_run[nt][1] += __shfl_xor_sync(0xffffffffu, mid_run[nt][1], o);
+        }
+        float* dst = join + ((4 * nt + t) * kAttWarps + warp) * kMergePitch;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const float mid = mid_run[nt][m >> 1];
+            *reinterpret_cast<float4*>(dst + 32 * m + 4 * r) =
+                make_float4(o_run[nt][m][0] + mid, o_run[nt][m][1] + mid, o_run[nt][m][2] + mid,
+                            o_run[nt][m][3] + mid);
+        }
+        if (r == 0) {
+            dst[kD] = m_run[nt];
+            dst[kD + 1] = l_run[nt];
+        }
     }
     __syncthreads();
     const int e = threadIdx.x;
-    float M = -INFINITY, L = 0.0f, O = 0.0f;
-    for (int w = 0; w < kAttWarps; ++w) M = max_nan(M, sm[w][kD]);
-    for (int w = 0; w < kAttWarps; ++w) {
-        const float c = sm[w][kD] == -INFINITY ? 0.0f : expf(sm[w][kD] - M);
-        if (sm[w][kD] == -INFINITY && sm[w][kD + 1] == 0.0f) continue;
-        L = fmaf(c, sm[w][kD + 1], L);
-        O = fmaf(c, sm[w][e], O);
-    }
-    float* p = a.part + (row * a.splits + split) * kPart;
-    p[e] = O;
-    if (e == 0) {
-        p[kD] = M;
-        p[kD + 1] = L;
+    for (int h = 0; h < heads; ++h) {
+        const float* src = join + h * kAttWarps * kMergePitch;
+        float M = -INFINITY, L = 0.0f, O = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kAttWarps; ++w) M = fmaxf(M, src[w * kMergePitch + kD]);
+#pragma unroll
+        for (int w = 0; w < kAttWarps; ++w) {
+            const float mw = src[w * kMergePitch + kD];
+            const float s = mw == -INFINITY ? 0.0f : exp2_fast(mw - M);  // an empty warp holds zeros
+            L = fmaf(s, src[w * kMergePitch + kD + 1], L);
+            O = fmaf(s, src[w * kMergePitch + e], O);
+        }
+        if (a.splits == 1) {
+            a.out[(row0 + h) * kD + e] = L == 0.0f ? 0.0f : O / L;
+        } else {
+            float* p = a.part + ((row0 + h) * a.splits + split) * kPart;
+            p[e] = O;
+            if (e == 0) {
+                p[kD] = M;
+                p[kD + 1] = L;
+            }
+        }
     }
 }
 
-__global__ void __launch_bounds__(kD) kv4_merge_kernel(const float* part, int splits, float* out) {
-    const long long row = blockIdx.x;
-    const int e = threadIdx.x;
-    const float* p = part + row * splits * kPart;
+// The splits of a query row, joined in order. A split that holds nothing has m = -inf and zeros;
+// NaN passes through its zero factor.
+__global__ void __launch_bounds__(kD) kv4_merge_kernel(const A4Args a) {
+    const size_t row = blockIdx.x;
+    const int e = threadIdx.x, splits = a.splits;
+    wait_for_predecessor();
+    const float* p = a.part + row * splits * kPart;
     float M = -INFINITY, L = 0.0f, O = 0.0f;
-    for (int s = 0; s < splits; ++s) M = max_nan(M, p[s * kPart + kD]);
+    for (int s = 0; s < splits; ++s) M = fmaxf(M, __ldcg(p + s * kPart + kD));
     for (int s = 0; s < splits; ++s) {
-        const float ms = p[s * kPart + kD], ls = p[s * kPart + kD + 1];
-        if (ms == -INFINITY && ls == 0.0f) continue;
-        const float c = expf(ms - M);
-        L = fmaf(c, ls, L);
-        O = fmaf(c, p[s * kPart + e], O);
+        const float ms = __ldcg(p + s * kPart + kD);
+        const float c = ms == -INFINITY ? 0.0f : exp2_fast(ms - M);
+        L = fmaf(c, __ldcg(p + s * kPart + kD + 1), L);
+        O = fmaf(c, __ldcg(p + s * kPart + e), O);
     }
-    out[row * kD + e] = L == 0.0f ? 0.0f : O / L;
+    a.out[row * kD + e] = L == 0.0f ? 0.0f : O / L;
 }
 
-int attention_splits(int n) { return std::max(1, std::min(64, (n + 255) / 256)); }
+// How an attention call is laid over the GPU.
+struct AttPlan {
+    int nt, chunks, splits, tiles_per_split;
+};
+AttPlan attention_plan(int B, int Hq, int Hkv, int n) {
+    AttPlan p;
+    const int G = Hq / Hkv;
+    p.nt = G <= 4 ? 1 : 2;
+    p.chunks = (G + 4 * p.nt - 1) / (4 * p.nt);
+    const long long units = static_cast<long long>(B) * Hkv * p.chunks;
+    const long long slots = kSms * (p.nt == 1 ? 3 : 2);
+    const int tiles = (n + kTile - 1) / kTile;
+    // waves of CTAs times the steps (four tiles, one a warp) of a CTA, the start of a CTA and the
+    // second kernel counted in steps
+    const long long kStart = 3, kMerge = 4;
+    long long best = -1;
+    for (int s = 1; s <= 256 && s <= (tiles + kAttWarps - 1) / kAttWarps; ++s) {
+        const int per = (tiles + s - 1) / s;
+        const int per4 = (per + kAttWarps - 1) / kAttWarps * kAttWarps;
+        const int used = (tiles + per4 - 1) / per4;
+        const long long waves = (units * used + slots - 1) / slots;
+        const long long cost = waves * (per4 / kAttWarps + kStart) + (used > 1 ? kMerge : 0);
+        if (best < 0 || cost < best) {
+            best = cost;
+            p.splits = used;
+            p.tiles_per_split = per4;
+        }
+    }
+    return p;
+}
 
 RowArgs row_args(const mp_kv4& c, const float* centre, int B, int Hkv, int m, int n_begin,
                  const int32_t* positions) {
@@ -261,17 +749,14 @@ RowArgs row_args(const mp_kv4& c, const float* centre, int B, int Hkv, int m, in
     a.k_codes = static_cast<uint8_t*>(c.k_codes);
     a.v_codes = static_cast<uint8_t*>(c.v_codes);
     a.params = static_cast<uint8_t*>(c.params);
-    a.rows = static_cast<long long>(B) * Hkv * m;
+    a.rows = static_cast<uint32_t>(B) * Hkv * m;
     a.Hkv = Hkv;
     a.m = m;
     a.n_begin = n_begin;
     a.ncap = c.n_capacity;
     return a;
 }
-unsigned row_ctas(long long rows) {
-    constexpr int kPerCta = kRowThreads / 16;
-    return static_cast<unsigned>((rows + kPerCta - 1) / kPerCta);
-}
+unsigned row_ctas(uint32_t rows) { return (rows + kRowsPerCta - 1) / kRowsPerCta; }
 
 }  // namespace
 
@@ -298,13 +783,14 @@ cudaError_t launch_kv4_read(const mp_kv4& cache, const float* centre, int B, int
 }
 
 size_t kv4_attention_scratch_bytes(int B, int Hq, int Hkv, int n) {
-    (void)Hkv;
-    return static_cast<size_t>(B) * Hq * attention_splits(n) * kPart * sizeof(float);
+    const AttPlan p = attention_plan(B, Hq, Hkv, n);
+    return p.splits == 1 ? 0 : static_cast<size_t>(B) * Hq * p.splits * kPart * sizeof(float);
 }
 
 cudaError_t launch_kv4_attention(const void* q, bool q_bf16, const mp_kv4& cache, int B, int Hq,
                                  int Hkv, int n, const int32_t* lengths, float scale, float* out,
                                  void* workspace, cudaStream_t st) {
+    const AttPlan p = attention_plan(B, Hq, Hkv, n);
     A4Args a;
     a.q = q;
     a.k_codes = static_cast<const uint8_t*>(cache.k_codes);
@@ -316,17 +802,23 @@ cudaError_t launch_kv4_attention(const void* q, bool q_bf16, const mp_kv4& cache
     a.q_bf16 = q_bf16;
     a.Hq = Hq;
     a.Hkv = Hkv;
+    a.G = Hq / Hkv;
     a.n = n;
     a.ncap = cache.n_capacity;
-    a.splits = attention_splits(n);
-    a.per_split = (n + a.splits - 1) / a.splits;
-    a.scale = scale;
-    const unsigned rows = static_cast<unsigned>(B) * Hq;
-    kv4_attention_kernel<<<rows * a.splits, 32 * kAttWarps, 0, st>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    kv4_merge_kernel<<<rows, kD, 0, st>>>(a.part, a.splits, out);
-    return cudaGetLastError();
+    a.splits = p.splits;
+    a.chunks = p.chunks;
+    a.tiles_per_split = p.tiles_per_split;
+    a.scale = scale * 1.4426950408889634f;
+    const long long ctas = static_cast<long long>(B) * Hkv * p.splits * p.chunks;
+    if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
+    if (p.nt == 1)
+        kv4_attention_kernel<1><<<static_cast<unsigned>(ctas), kAttThreads, kAttSmem, st>>>(a);
+    else
+        kv4_attention_kernel<2><<<static_cast<unsigned>(ctas), kAttThreads, kAttSmem, st>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || p.splits == 1) return e;
+    return launch_dependent(kv4_merge_kernel, dim3(static_cast<unsigned>(B) * Hq), dim3(kD), 0, st,
+                            a);
 }
 
 cudaError_t prepare_kv4() {
@@ -336,7 +828,15 @@ cudaError_t prepare_kv4() {
     if ((e = cudaFuncGetAttributes(&fa, kv4_write_kernel<float>)) != cudaSuccess) return e;
     if ((e = cudaFuncGetAttributes(&fa, kv4_read_kernel<__nv_bfloat16>)) != cudaSuccess) return e;
     if ((e = cudaFuncGetAttributes(&fa, kv4_read_kernel<float>)) != cudaSuccess) return e;
-    if ((e = cudaFuncGetAttributes(&fa, kv4_attention_kernel)) != cudaSuccess) return e;
+    void (*att[2])(const A4Args) = {kv4_attention_kernel<1>, kv4_attention_kernel<2>};
+    for (auto fn : att) {
+        if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      kAttSmem)) != cudaSuccess)
+            return e;
+        if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                      cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
+            return e;
+    }
     return cudaFuncGetAttributes(&fa, kv4_merge_kernel);
 }
 
