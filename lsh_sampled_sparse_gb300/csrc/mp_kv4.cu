@@ -305,9 +305,14 @@ constexpr int kMergePitch = kD + 4;              // floats a (warp, head) leaves
 static_assert(kAttThreads == kD, "the merge: a thread per dim");
 static_assert(kAttWarps * 8 * kMergePitch * 4 <= kAttSmem, "the merge reuses the stages");
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(live ? 16 : 0)
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Zeros where the source is not live; `valid` stands in for its address then.
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, const void* valid,
+                                               bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                 "l"(live ? src : valid), "r"(live ? 16 : 0)
                  : "memory");
 }
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -350,18 +355,22 @@ __device__ __forceinline__ uint32_t warp_max(uint32_t x) {
     return __reduce_max_sync(0xffffffffu, x);
 }
 
-// Eight codes of a word as four fp16 pairs: pair i holds code i of the low half and code i of the
-// high half, less `lo` and `hi`. The nibble becomes the low bits of 1024 + c or bits 4-7 of
-// 64 + c; the constants take both away, exactly.
+// Eight codes of a word as four fp16 pairs: with c0 .. c3 the codes of its low half and c4 .. c7 of
+// its high half, `lo` to be taken off the former and `hi` off the latter, the pairs are c0 - lo and
+// c4 - hi, (c0 - lo) + 16 (c1 - lo) and so on, the same of c2, c3, c6, c7. Putting a byte under the
+// exponent of 1024 is one byte permute, and masking it one logic instruction: four on the integer
+// pipe for eight codes, which is what bounds the kernel, where a pair for every code costs five
+// (each code by mask and exponent, and a shift). The other matrix takes the sum apart again.
 template <int lo, int hi>
 __device__ __forceinline__ void unpack_pairs(uint32_t w, uint32_t (&h)[4]) {
-    constexpr uint32_t kA = (0xe400u + lo) | ((0xe400u + hi) << 16);               // -(1024 + x)
-    constexpr uint32_t kB = (0xd400u + 16 * lo) | ((0xd400u + 16 * hi) << 16);     // -(64 + x)
-    const uint32_t u = w >> 8;
-    h[0] = hadd2((w & 0x000f000fu) | 0x64006400u, kA);
-    h[1] = hadd2((w & 0x00f000f0u) | 0x54005400u, kB);
-    h[2] = hadd2((u & 0x000f000fu) | 0x64006400u, kA);
-    h[3] = hadd2((u & 0x00f000f0u) | 0x54005400u, kB);
+    constexpr uint32_t kOne = (0xe400u + lo) | ((0xe400u + hi) << 16);             // -(1024 + x)
+    constexpr uint32_t kTwo = (0xe400u + 17 * lo) | ((0xe400u + 17 * hi) << 16);   // -(1024 + 17 x)
+    const uint32_t x = __byte_perm(w, 0x64646464u, 0x4240);
+    const uint32_t y = __byte_perm(w, 0x64646464u, 0x4341);
+    h[0] = hadd2(x & 0xff0fff0fu, kOne);
+    h[1] = hadd2(x, kTwo);
+    h[2] = hadd2(y & 0xff0fff0fu, kOne);
+    h[3] = hadd2(y, kTwo);
 }
 
 // x as two fp16: its leading 11 bits in the low half, the rest of it in the high half
@@ -404,26 +413,40 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
     // a tile's copies: 16-byte piece lane % 4 of rows lane / 4 + 8 i to piece (lane % 4) ^
     // (row / 2 % 4); rows past the end read as zero
     const uint32_t swz = (lane >> 2) * kCodeBytes + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+    const size_t first = static_cast<size_t>(tile0 + warp) * kTile;
+    const uint8_t* kp = kg + (first + (lane >> 2)) * kCodeBytes + 16 * (lane & 3);
+    const uint8_t* vp = vg + (first + (lane >> 2)) * kCodeBytes + 16 * (lane & 3);
+    const uint8_t* pp = pg + (first + lane) * kParamBytes;
+    int left = end - static_cast<int>(first);    // tokens from the next tile to copy on
     auto issue = [&](int it) {
-        if (it < mine) {
-            const int key0 = (tile0 + warp + it * kAttWarps) * kTile;
-            const uint32_t st = stage0 + (it & 1) * kStageBytes;
+        const uint32_t st = stage0 + (it & 1) * kStageBytes;
+        if (left >= kTile) {
 #pragma unroll
             for (int i = 0; i < kTile / 8; ++i) {
-                const int key = key0 + 8 * i + (lane >> 2);
-                const bool live = key < end;
-                const size_t off = static_cast<size_t>(live ? key : 0) * kCodeBytes + 16 * (lane & 3);
-                copy16(st + kStageK + 8 * i * kCodeBytes + swz, kg + off, live);
-                copy16(st + kStageV + 8 * i * kCodeBytes + swz, vg + off, live);
+                copy16(st + kStageK + 8 * i * kCodeBytes + swz, kp + 8 * i * kCodeBytes);
+                copy16(st + kStageV + 8 * i * kCodeBytes + swz, vp + 8 * i * kCodeBytes);
             }
 #pragma unroll
-            for (int i = 0; i < kTile / 32; ++i) {
-                const int key = key0 + 32 * i + lane;
-                const bool live = key < end;
-                copy16(st + kStageP + (32 * i + lane) * kParamBytes,
-                       pg + static_cast<size_t>(live ? key : 0) * kParamBytes, live);
+            for (int i = 0; i < kTile / 32; ++i)
+                copy16(st + kStageP + (32 * i + lane) * kParamBytes, pp + 32 * i * kParamBytes);
+        } else if (left > 0) {
+#pragma unroll 1
+            for (int i = 0; i < kTile / 8; ++i) {
+                const bool live = 8 * i + (lane >> 2) < left;
+                copy16_or_zero(st + kStageK + 8 * i * kCodeBytes + swz, kp + 8 * i * kCodeBytes, kg,
+                               live);
+                copy16_or_zero(st + kStageV + 8 * i * kCodeBytes + swz, vp + 8 * i * kCodeBytes, vg,
+                               live);
             }
+#pragma unroll 1
+            for (int i = 0; i < kTile / 32; ++i)
+                copy16_or_zero(st + kStageP + (32 * i + lane) * kParamBytes,
+                               pp + 32 * i * kParamBytes, pg, 32 * i + lane < left);
         }
+        kp += kAttWarps * kTile * kCodeBytes;
+        vp += kAttWarps * kTile * kCodeBytes;
+        pp += kAttWarps * kTile * kParamBytes;
+        left -= kAttWarps * kTile;
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     issue(0);
@@ -431,9 +454,10 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
 
     // ---- the queries as column fragments: column 2 h is head h's leading half, 2 h + 1 the rest.
     // A lane loads head lane / 8 of its four (dims 32 m + 8 t ..), scaled by a power of two so
-    // that the largest element lies in [1, 2); fac undoes it on the logits.
+    // that the largest element lies in [2^6, 2^7); fac undoes it on the logits. Against the pairs
+    // c0 and c0 + 16 c1 of unpack_pairs stand q0 - q1 / 16 and q1 / 16.
     uint32_t qb[NT][4][4];
-    float fac[NT], qsum[NT][2];
+    float fac[NT], qsum8[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int h = 4 * nt + (lane >> 3);
@@ -449,8 +473,8 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
             }
         big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
         big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        const uint32_t ex = min(max(big >> 23, 1u), 253u);
-        const float down = __uint_as_float((254u - ex) << 23), up = __uint_as_float(ex << 23);
+        const uint32_t ex = min(max(big >> 23, 7u), 253u);
+        const float down = __uint_as_float((260u - ex) << 23), up = __uint_as_float((ex - 6u) << 23);
         float sum[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
@@ -458,6 +482,11 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
             for (int e = 0; e < 8; ++e) {
                 x[m][e] *= down;
                 sum[m >> 1] += x[m][e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                x[m][e + 1] *= 0.0625f;
+                x[m][e] -= x[m][e + 1];
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -473,15 +502,16 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
         for (int g = 0; g < 2; ++g) {
             sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
             sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
-            qsum[nt][g] = __shfl_sync(0xffffffffu, sum[g], 8 * t);
+            qsum8[nt][g] = 8.0f * __shfl_sync(0xffffffffu, sum[g], 8 * t);
         }
-        fac[nt] = __shfl_sync(0xffffffffu, a.scale * up, 8 * t);
+        fac[nt] = fmaxf(__shfl_sync(0xffffffffu, a.scale * up, 8 * t), 1.17549435e-38f);
     }
 
-    float m_run[NT], l_run[NT], mid_run[NT][2], o_run[NT][4][4];
+    // running maximum of the logits as the products leave them, the same times fac
+    float m_run[NT], base_run[NT], l_run[NT], mid_run[NT][2], o_run[NT][4][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        m_run[nt] = -INFINITY;
+        m_run[nt] = base_run[nt] = -INFINITY;
         l_run[nt] = mid_run[nt][0] = mid_run[nt][1] = 0.0f;
 #pragma unroll
         for (int m = 0; m < 4; ++m)
@@ -498,21 +528,22 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
         const uint8_t* prm = smem + (st - smem_u32(smem)) + kStageP;
         const int key0 = (tile0 + warp + it * kAttWarps) * kTile;
 
-        // ---- logits (base 2) of tokens 16 j + r and 16 j + 8 + r
+        // ---- logits (fac of them, base 2) of tokens 16 j + r and 16 j + 8 + r
         float lg[NT][2 * kSub];
-        uint32_t vmax[2] = {0u, 0u};
+        uint32_t vmax = 0u;                      // group 0 in the low half, 1 in the high half
 #pragma unroll
         for (int j = 0; j < kSub; ++j) {
             uint32_t k0[4], k1[4];
             ldmatrix4(k0, st + kStageK + (16 * j) * kCodeBytes + lm);
             ldmatrix4(k1, st + kStageK + (16 * j + 8) * kCodeBytes + lm);
-            float c[NT][2][4];
+            float c[NT][2][4];                   // from 8 sum q: codes minus 8, plus 8
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int g = 0; g < 2; ++g)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) c[nt][g][e] = 0.0f;
+                for (int g = 0; g < 2; ++g) {
+                    c[nt][g][0] = c[nt][g][2] = qsum8[nt][g];
+                    c[nt][g][1] = c[nt][g][3] = 0.0f;
+                }
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 uint32_t x0[4], x1[4];
@@ -526,24 +557,27 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
             }
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int row = 16 * j + 8 * half + r;
-                const uint4 p = *reinterpret_cast<const uint4*>(prm + row * kParamBytes);
+                const uint4 p = *reinterpret_cast<const uint4*>(
+                    prm + (16 * j + 8 * half + r) * kParamBytes);
                 const float s0 = __uint_as_float(p.x << 16), s1 = __uint_as_float(p.y << 16);
-                const float mid0 = fmaf(8.0f, s0, __uint_as_float(p.x & 0xffff0000u));
-                const float mid1 = fmaf(8.0f, s1, __uint_as_float(p.y & 0xffff0000u));
-                // the values' largest step, of those that are numbers (a NaN step is its own row's)
-                const uint32_t v0 = p.z << 16, v1 = p.w << 16;
-                vmax[0] = max(vmax[0], v0 < 0x7f800000u ? v0 : 0u);
-                vmax[1] = max(vmax[1], v1 < 0x7f800000u ? v1 : 0u);
+                const float z0 = __uint_as_float(p.x & 0xffff0000u);
+                const float z1 = __uint_as_float(p.y & 0xffff0000u);
+                vmax = __vmaxu2(vmax, __byte_perm(p.z, p.w, 0x5410));    // the values' steps
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float u = s0 * (c[nt][0][2 * half] + c[nt][0][2 * half + 1]);
                     u = fmaf(s1, c[nt][1][2 * half] + c[nt][1][2 * half + 1], u);
-                    u = fmaf(mid0, qsum[nt][0], u);
-                    u = fmaf(mid1, qsum[nt][1], u);
-                    lg[nt][2 * j + half] = key0 + row < end ? u * fac[nt] : -INFINITY;
+                    u = fmaf(z0, qsum8[nt][0] * 0.125f, u);
+                    lg[nt][2 * j + half] = fmaf(z1, qsum8[nt][1] * 0.125f, u);
                 }
             }
+        }
+        if (key0 + kTile > end) {
+#pragma unroll
+            for (int i = 0; i < 2 * kSub; ++i)
+                if (key0 + 8 * i + r >= end)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) lg[nt][i] = -INFINITY;
         }
 
         // ---- one step of the running softmax; weights in place of the logits
@@ -556,13 +590,14 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
             const float mn = fmaxf(m_run[nt], mt);
-            const float base = mn == -INFINITY ? 0.0f : mn;
-            corr[nt] = exp2_fast(m_run[nt] - base);
+            const float base = mn == -INFINITY ? 0.0f : mn * fac[nt];
+            corr[nt] = exp2_fast(base_run[nt] - base);
             m_run[nt] = mn;
+            base_run[nt] = mn == -INFINITY ? -INFINITY : base;
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < 2 * kSub; ++i) {
-                lg[nt][i] = exp2_fast(lg[nt][i] - base);
+                lg[nt][i] = exp2_fast(fmaf(lg[nt][i], fac[nt], -base));
                 sum += lg[nt][i];
             }
             l_run[nt] = fmaf(l_run[nt], corr[nt], sum);
@@ -570,11 +605,12 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
             mid_run[nt][1] *= corr[nt];
         }
         // weights times steps become fp16 halves after a power of two per group brings the tile's
-        // largest step to [2^13, 2^14): 2^(140 - ex), taken back by 2^(ex - 140)
+        // largest step to [2^13, 2^14): 2^(140 - ex), taken back by 2^(ex - 140). A step that is NaN
+        // is the largest of all; its group is NaN in every head anyhow.
         float down[2], up[2];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-            const uint32_t ex = max(warp_max(vmax[g]) >> 23, 14u);
+            const uint32_t ex = max(warp_max(g ? vmax >> 16 : vmax & 0xffffu) >> 7, 14u);
             down[g] = __uint_as_float((267u - ex) << 23);
             up[g] = __uint_as_float((ex - 13u) << 23);
         }
@@ -627,17 +663,19 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
         }
         __syncwarp();
         issue(it + 2);
+        // the second row of a pair holds its own dim's sum 16 times and the first one's once
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int m = 0; m < 4; ++m)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        o_run[nt][m][2 * i + e] =
-                            fmaf(acc[nt][m][i][2 * e] + acc[nt][m][i][2 * e + 1], up[m >> 1],
-                                 o_run[nt][m][2 * i + e] * corr[nt]);
+                for (int i = 0; i < 2; ++i) {
+                    const float one = acc[nt][m][i][0] + acc[nt][m][i][1];
+                    const float two = (acc[nt][m][i][2] + acc[nt][m][i][3]) - one;
+                    float* o = &o_run[nt][m][2 * i];
+                    o[0] = fmaf(one, up[m >> 1], o[0] * corr[nt]);
+                    o[1] = fmaf(two, up[m >> 1] * 0.0625f, o[1] * corr[nt]);
+                }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 
@@ -661,7 +699,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
                             o_run[nt][m][3] + mid);
         }
         if (r == 0) {
-            dst[kD] = m_run[nt];
+            dst[kD] = base_run[nt];
             dst[kD + 1] = l_run[nt];
         }
     }
@@ -692,22 +730,70 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
     }
 }
 
-// The splits of a query row, joined in order. A split that holds nothing has m = -inf and zeros;
-// NaN passes through its zero factor.
-__global__ void __launch_bounds__(kD) kv4_merge_kernel(const A4Args a) {
+// The splits of a query row, joined in a fixed order: warp w folds splits w, w + kMergeWarps, ...,
+// kMergeAhead of them loaded at once, four dims a lane; then the warps in order. A split that
+// holds nothing has m = -inf and zeros; NaN passes through its zero factor.
+constexpr int kMergeWarps = 8, kMergeAhead = 4;
+__global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_kernel(const A4Args a) {
+    __shared__ __align__(16) float join[kMergeWarps][kMergePitch];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, splits = a.splits;
     const size_t row = blockIdx.x;
-    const int e = threadIdx.x, splits = a.splits;
     wait_for_predecessor();
     const float* p = a.part + row * splits * kPart;
-    float M = -INFINITY, L = 0.0f, O = 0.0f;
-    for (int s = 0; s < splits; ++s) M = fmaxf(M, __ldcg(p + s * kPart + kD));
-    for (int s = 0; s < splits; ++s) {
-        const float ms = __ldcg(p + s * kPart + kD);
-        const float c = ms == -INFINITY ? 0.0f : exp2_fast(ms - M);
-        L = fmaf(c, __ldcg(p + s * kPart + kD + 1), L);
-        O = fmaf(c, __ldcg(p + s * kPart + e), O);
+    float M = -INFINITY, L = 0.0f;
+    float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s0 = warp; s0 < splits; s0 += kMergeWarps * kMergeAhead) {
+        float ms[kMergeAhead], ls[kMergeAhead];
+        float4 os[kMergeAhead];
+#pragma unroll
+        for (int i = 0; i < kMergeAhead; ++i) {
+            const int s = s0 + i * kMergeWarps;
+            ms[i] = -INFINITY;
+            ls[i] = 0.0f;
+            os[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (s < splits) {
+                const float* ps = p + static_cast<size_t>(s) * kPart;
+                ms[i] = __ldcg(ps + kD);
+                ls[i] = __ldcg(ps + kD + 1);
+                os[i] = __ldcg(reinterpret_cast<const float4*>(ps) + lane);
+            }
+        }
+        float mn = M;
+#pragma unroll
+        for (int i = 0; i < kMergeAhead; ++i) mn = fmaxf(mn, ms[i]);
+        const float base = mn == -INFINITY ? 0.0f : mn;
+        const float c = exp2_fast(M - base);
+        M = mn;
+        L *= c;
+        O = make_float4(O.x * c, O.y * c, O.z * c, O.w * c);
+#pragma unroll
+        for (int i = 0; i < kMergeAhead; ++i) {
+            const float w = exp2_fast(ms[i] - base);
+            L = fmaf(w, ls[i], L);
+            O = make_float4(fmaf(w, os[i].x, O.x), fmaf(w, os[i].y, O.y), fmaf(w, os[i].z, O.z),
+                            fmaf(w, os[i].w, O.w));
+        }
     }
-    a.out[row * kD + e] = L == 0.0f ? 0.0f : O / L;
+    *reinterpret_cast<float4*>(&join[warp][4 * lane]) = O;
+    if (lane == 0) {
+        join[warp][kD] = M;
+        join[warp][kD + 1] = L;
+    }
+    __syncthreads();
+    const int e = threadIdx.x;
+    if (e >= kD) return;
+    M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, join[w][kD]);
+    const float base = M == -INFINITY ? 0.0f : M;
+    float Ls = 0.0f, Os = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) {
+        const float c = exp2_fast(join[w][kD] - base);
+        Ls = fmaf(c, join[w][kD + 1], Ls);
+        Os = fmaf(c, join[w][e], Os);
+    }
+    a.out[row * kD + e] = Ls == 0.0f ? 0.0f : Os / Ls;
 }
 
 // How an attention call is laid over the GPU.
@@ -817,8 +903,8 @@ cudaError_t launch_kv4_attention(const void* q, bool q_bf16, const mp_kv4& cache
         kv4_attention_kernel<2><<<static_cast<unsigned>(ctas), kAttThreads, kAttSmem, st>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1) return e;
-    return launch_dependent(kv4_merge_kernel, dim3(static_cast<unsigned>(B) * Hq), dim3(kD), 0, st,
-                            a);
+    return launch_dependent(kv4_merge_kernel, dim3(static_cast<unsigned>(B) * Hq),
+                            dim3(32 * kMergeWarps), 0, st, a);
 }
 
 cudaError_t prepare_kv4() {
