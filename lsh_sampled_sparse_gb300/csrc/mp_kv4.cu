@@ -16,6 +16,8 @@ namespace mp {
 namespace {
 
 constexpr int kCodeBytes = MP_KV4_CODE_BYTES;
+constexpr int kSms = 152;                        // of a GB300; a plan, and so a workspace's size,
+                                                 // is the same on the host alone
 
 __device__ __forceinline__ float min_nan(float a, float b) {
     float r;
@@ -25,6 +27,47 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Two floats in one 64-bit register: the packed instructions halve the issue slots that the codes
+// of a row take, which is what bounds their writing.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 pack2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
     return r;
 }
 
@@ -48,50 +91,78 @@ __device__ __forceinline__ uint32_t group_params(float lo, float hi) {
     return finite ? (s | (z << 16)) : 0x7fc07fc0u;
 }
 
-// rint((x - z) / s) from the definition in 64 bits: what decides next to a border.
+// rint((x - z) / s), ties to even, decided in 64 bits where x lies next to a border. f is off by one
+// at most; d = (x - z) - f s is exact around s / 2 (x - z rounded to 53 bits, as the definition has
+// it), so the comparison decides as the rounded quotient would.
 __device__ __noinline__ uint32_t code_exact(float x, float z, float s) {
-    const double v = (static_cast<double>(x) - static_cast<double>(z)) / static_cast<double>(s);
-    return static_cast<uint32_t>(static_cast<int>(rint(v)));
+    const float t = x - z;
+    float f = rintf(__fdiv_rn(t, s));
+    const float h = 0.5f * s;
+    if (!(fabsf(fmaf(-f, s, t)) < h * (1.0f - 3.8e-6f)) || s < 1e-30f) {
+        const double d = fma(-static_cast<double>(f), static_cast<double>(s),
+                             static_cast<double>(x) - static_cast<double>(z));
+        const double hd = 0.5 * static_cast<double>(s);
+        const bool odd = static_cast<int>(f) & 1;
+        if (d > hd || (d == hd && odd)) f += 1.0f;
+        else if (d < -hd || (d == -hd && odd)) f -= 1.0f;
+    }
+    return static_cast<uint32_t>(static_cast<int>(f));
 }
 
-// The 16 codes of x (a quarter of a group) as two words.
-// With t = x - z and 1/s as two floats, the quotient is rounded once and then, by adding 1.5 2^23,
-// to an integer f, ties to even. t - f s is exact near s / 2 (one fused multiply-add), and tells
-// whether f is the nearest: values that are bf16 (kBf16) make t exact too, unless a border lies at
-// x = 0 and x is tiny, so that |t - f s| > s / 2 alone, or such a border, asks for 64 bits; other
-// values ask for them within 2^-18 of a border. Steps near the ends of float32's range do always.
+// The 16 codes of x (a quarter of a group, pairs in order) as two words.
+// With t = x - z, the quotient t / s is rounded to an integer f by adding 1.5 2^23, and t - f s,
+// which one fused multiply-add gives exactly near s / 2, tells whether f is the nearest integer.
+// Values that are bf16 (kBf16) often lie half-way: 1 / s as two floats rounds their quotient
+// properly first, so that the addition sends a tie to the even integer, and |t - f s| > s / 2 alone
+// asks for 64 bits; t is exact then too, unless x is tiny and a border lies at x = 0. Other values
+// ask for 64 bits within 2^-18 of a border; steps near the ends of float32's range do always.
 template <bool kBf16>
-__device__ __forceinline__ uint2 codes16(const float (&x)[16], uint32_t pr) {
+__device__ __forceinline__ uint2 codes16(const F2 (&x)[8], uint32_t pr) {
     const float s = __uint_as_float(pr << 16), z = __uint_as_float(pr & 0xffff0000u);
     if (!(s > 0.0f)) return make_uint2(0u, 0u);                  // constant, or not a number
-    constexpr float kRound = 12582912.0f;
-    const float inv = __frcp_rn(s), low = fmaf(-s, inv, 1.0f) * inv;
-    const float half = kBf16 ? 0.5f * s : 0.5f * s * (1.0f - 3.8e-6f);
+    const F2 round = pack2(12582912.0f, 12582912.0f), back = pack2(-12582912.0f, -12582912.0f);
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    const float low = fmaf(-s, inv, 1.0f) * inv;
+    const F2 inv2 = pack2(inv, inv), low2 = pack2(low, low), minus_z = pack2(-z, -z),
+             minus_s = pack2(-s, -s);
     float worst = 0.0f;
     uint32_t w[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         w[k] = 0u;
 #pragma unroll
-        for (int i = 7; i >= 0; --i) {
-            const float t = x[8 * k + i] - z;
-            const float y = __fadd_rn(fmaf(t, inv, t * low), kRound);
-            worst = fmaxf(worst, fabsf(fmaf(-(y - kRound), s, t)));
+        for (int i = 3; i >= 0; --i) {
+            const F2 t = add2(x[4 * k + i], minus_z);
+            const F2 y = kBf16 ? add2(fma2(t, inv2, mul2(t, low2)), round) : fma2(t, inv2, round);
+            const float2 off = unpack2(fma2(add2(y, back), minus_s, t));
+            worst = fmaxf(fmaxf(worst, fabsf(off.x)), fabsf(off.y));
             // the low bits of y are its integer; what its high bits add up to is taken off below
-            w[k] = (w[k] << 4) + __float_as_uint(y);
+            const float2 yf = unpack2(y);
+            w[k] = (w[k] << 4) + __float_as_uint(yf.y);
+            w[k] = (w[k] << 4) + __float_as_uint(yf.x);
         }
         w[k] -= 0x4b400000u * 0x11111111u;
     }
-    bool ask = kBf16 ? worst > half : worst >= half;
+    bool ask = kBf16 ? worst > 0.5f * s : worst >= 0.5f * s * (1.0f - 3.8e-6f);
     ask = ask || s < 1e-30f || s > 1e30f;
     if (kBf16) {
         const float c = floorf(-z * inv);                        // is z + (c + 1/2) s = 0 ?
-        ask = ask || (c >= 0.0f && c < 15.0f && fmaf(c + 0.5f, s, z) == 0.0f);
+        if (c >= 0.0f && c < 15.0f && fmaf(c + 0.5f, s, z) == 0.0f) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 v = unpack2(x[i]);
+                ask = ask || fabsf(v.x) < 1e-4f * s || fabsf(v.y) < 1e-4f * s;
+            }
+        }
     }
     if (ask) {
         w[0] = w[1] = 0u;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i >> 3] |= code_exact(x[i], z, s) << (4 * (i & 7));
+        for (int i = 0; i < 8; ++i) {
+            const float2 v = unpack2(x[i]);
+            w[i >> 2] |= (code_exact(v.x, z, s) | (code_exact(v.y, z, s) << 4)) << (8 * (i & 3));
+        }
     }
     return make_uint2(w[0], w[1]);
 }
@@ -105,112 +176,201 @@ struct RowArgs {
     uint8_t* v_codes;
     uint8_t* params;
     uint32_t rows;                               // B * Hkv * m
+    uint32_t blocks;                             // of kRowsPerCta rows
     uint32_t m;
     int Hkv, n_begin, ncap;
 };
-
-// The cache row (over all heads) of token i of the call's head bh, -1 where it is outside.
-__device__ __forceinline__ long long cache_row(const RowArgs& a, uint32_t bh, uint32_t i) {
-    const long long pos =
-        static_cast<long long>(a.positions ? __ldg(a.positions + bh / a.Hkv) : a.n_begin) + i;
-    return pos >= 0 && pos < a.ncap ? static_cast<long long>(bh) * a.ncap + pos : -1;
-}
 
 constexpr int kRowThreads = 256;
 constexpr int kRowLanes = 8;                     // lanes a row: 16 dims each, four a group
 constexpr int kRowsPerCta = kRowThreads / kRowLanes;
 
-__device__ __forceinline__ void load16(const float* p, float (&x)[16]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 v = __ldcs(reinterpret_cast<const float4*>(p) + i);
-        x[4 * i] = v.x;
-        x[4 * i + 1] = v.y;
-        x[4 * i + 2] = v.z;
-        x[4 * i + 3] = v.w;
+// Where a lane's row of block `blk` (kRowsPerCta rows) is: head and token in the call, row of the
+// cache over all heads (-1: outside the cache, or past the call's rows). A block spans two heads at
+// most where a head has more rows than a block: one division, of uniform numbers, does then.
+struct RowAt {
+    uint32_t r, bh;
+    long long row;
+};
+__device__ __forceinline__ RowAt row_at(const RowArgs& a, uint32_t blk) {
+    const uint32_t r0 = blk * kRowsPerCta, r = r0 + threadIdx.x / kRowLanes;
+    RowAt w;
+    w.r = min(r, a.rows - 1u);
+    uint32_t i;
+    if (a.m >= kRowsPerCta) {
+        w.bh = r0 / a.m;
+        i = w.r - w.bh * a.m;
+        if (i >= a.m) {
+            ++w.bh;
+            i -= a.m;
+        }
+    } else {
+        w.bh = w.r / a.m;
+        i = w.r - w.bh * a.m;
     }
+    const long long pos =
+        static_cast<long long>(a.positions ? __ldg(a.positions + w.bh / a.Hkv) : a.n_begin) + i;
+    w.row = r < a.rows && pos >= 0 && pos < a.ncap
+                ? static_cast<long long>(w.bh) * a.ncap + pos : -1;
+    return w;
 }
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&x)[16]) {
+
+// 32 bytes of a row: one access where they are aligned (kWide: a whole sector a lane; two accesses
+// of 16 bytes touch every sector twice), else two.
+template <bool kWide>
+__device__ __forceinline__ void load32(const void* p, uint32_t* w) {
+    if constexpr (kWide) {
+        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                       "=r"(w[6]), "=r"(w[7])
+                     : "l"(p));
+    } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            x[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
-            x[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        for (int i = 0; i < 2; ++i) {
+            const uint4 v = __ldg(static_cast<const uint4*>(p) + i);
+            w[4 * i] = v.x;
+            w[4 * i + 1] = v.y;
+            w[4 * i + 2] = v.z;
+            w[4 * i + 3] = v.w;
         }
     }
 }
-
-// The parameters of a lane's group (four lanes) from its 16 values.
-__device__ __forceinline__ uint32_t lane_params(const float (&x)[16]) {
-    float lo = x[0], hi = x[0];
+template <bool kWide>
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+    if constexpr (kWide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                     "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
 #pragma unroll
-    for (int i = 1; i < 16; ++i) {
-        lo = min_nan(lo, x[i]);
-        hi = max_nan(hi, x[i]);
+        for (int i = 0; i < 2; ++i)
+            static_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2],
+                                                   w[4 * i + 3]);
     }
+}
+
+__device__ __forceinline__ F2 of_bf16x2(uint32_t w) {
+    return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+// The least and the largest of 16 dims (NaN if one is)
+__device__ __forceinline__ float2 bounds16(const F2 (&x)[8]) {
+    const float2 v = unpack2(x[0]);
+    float lo = min_nan(v.x, v.y), hi = max_nan(v.x, v.y);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        const float2 u = unpack2(x[i]);
+        lo = min_nan(lo, u.x, u.y);
+        hi = max_nan(hi, u.x, u.y);
+    }
+    return make_float2(lo, hi);
+}
+// The same of 16 bf16 as they are in memory
+__device__ __forceinline__ float2 bounds16(const uint32_t (&w)[8]) {
+    uint32_t lo = w[0], hi = w[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(lo) : "r"(w[i]));
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(hi) : "r"(w[i]));
+    }
+    return make_float2(min_nan(__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u)),
+                       max_nan(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)));
+}
+
+// The parameters of a group from the bounds of its four lanes.
+__device__ __forceinline__ uint32_t lanes_params(float2 v) {
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
-        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        v.x = min_nan(v.x, __shfl_xor_sync(0xffffffffu, v.x, o));
+        v.y = max_nan(v.y, __shfl_xor_sync(0xffffffffu, v.y, o));
     }
-    return group_params(lo, hi);
+    return group_params(v.x, v.y);
 }
 
-// Eight lanes a row, four rows a warp; key and value of a row are loaded before either is coded.
-template <typename T>
+// Eight lanes a row, four rows a warp. A CTA takes every gridDim.x-th block of 32 rows and loads the
+// next block's keys and values before it codes the ones it has: with a block a CTA and no loop, a
+// third of the time went by between a warp's loads and its stores.
+template <typename T, bool kWide>
 __global__ void __launch_bounds__(kRowThreads) kv4_write_kernel(const RowArgs a) {
     constexpr bool kBf16 = sizeof(T) == 2;
+    constexpr int kWords = 16 * sizeof(T) / 4;   // of 16 dims
     const int rl = threadIdx.x & (kRowLanes - 1);
-    const uint32_t r = blockIdx.x * kRowsPerCta + threadIdx.x / kRowLanes;
-    const bool live = r < a.rows;
-    const uint32_t bh = live ? r / a.m : 0u;
-    const long long row = live ? cache_row(a, bh, r - bh * a.m) : -1;
-    const size_t at = static_cast<size_t>(row >= 0 ? r : 0u) * kD + 16 * rl;   // a row that exists
-    float k[16], v[16];
-    load16(static_cast<const T*>(a.keys) + at, k);
-    load16(static_cast<const T*>(a.values) + at, v);
-    if (a.centre) {
-        const float4* mu = reinterpret_cast<const float4*>(a.centre + static_cast<size_t>(bh) * kD +
-                                                           16 * rl);
+    const F2 minus = pack2(-1.0f, -1.0f);
+    uint32_t kw[kWords], vw[kWords];
+    auto load = [&](uint32_t r) {
+        const size_t at = static_cast<size_t>(r) * kD + 16 * rl;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 c = __ldg(mu + i);
-            k[4 * i] = __fsub_rn(k[4 * i], c.x);
-            k[4 * i + 1] = __fsub_rn(k[4 * i + 1], c.y);
-            k[4 * i + 2] = __fsub_rn(k[4 * i + 2], c.z);
-            k[4 * i + 3] = __fsub_rn(k[4 * i + 3], c.w);
+        for (int j = 0; j < kWords / 8; ++j) {
+            load32<kWide>(static_cast<const T*>(a.keys) + at + 8 * j, kw + 8 * j);
+            load32<kWide>(static_cast<const T*>(a.values) + at + 8 * j, vw + 8 * j);
+        }
+    };
+    RowAt w = row_at(a, blockIdx.x);
+    load(w.r);
+    for (uint32_t blk = blockIdx.x; blk < a.blocks; blk += gridDim.x) {
+        F2 k[8], v[8];
+        float2 vb;
+        if constexpr (kBf16) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                k[j] = of_bf16x2(kw[j]);
+                v[j] = of_bf16x2(vw[j]);
+            }
+            vb = bounds16(vw);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                k[j] = pack2(__uint_as_float(kw[2 * j]), __uint_as_float(kw[2 * j + 1]));
+                v[j] = pack2(__uint_as_float(vw[2 * j]), __uint_as_float(vw[2 * j + 1]));
+            }
+            vb = bounds16(v);
+        }
+        const RowAt now = w;
+        if (blk + gridDim.x < a.blocks) {
+            w = row_at(a, blk + gridDim.x);
+            load(w.r);
+        }
+        if (a.centre) {
+            const float4* mu = reinterpret_cast<const float4*>(
+                a.centre + static_cast<size_t>(now.bh) * kD + 16 * rl);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 c = __ldg(mu + j);
+                k[2 * j] = fma2(pack2(c.x, c.y), minus, k[2 * j]);       // k - c, one rounding
+                k[2 * j + 1] = fma2(pack2(c.z, c.w), minus, k[2 * j + 1]);
+            }
+        }
+        const uint32_t kp = lanes_params(bounds16(k)), vp = lanes_params(vb);
+        const uint2 kc = codes16<false>(k, kp), vc = codes16<kBf16>(v, vp);
+        const uint32_t kp1 = __shfl_down_sync(0xffffffffu, kp, 4);
+        const uint32_t vp1 = __shfl_down_sync(0xffffffffu, vp, 4);
+        if (now.row >= 0) {
+            *reinterpret_cast<uint2*>(a.k_codes + now.row * kCodeBytes + 8 * rl) = kc;
+            *reinterpret_cast<uint2*>(a.v_codes + now.row * kCodeBytes + 8 * rl) = vc;
+            if (rl == 0)
+                *reinterpret_cast<uint4*>(a.params + now.row * 16) = make_uint4(kp, kp1, vp, vp1);
         }
     }
-    const uint32_t kp = lane_params(k), vp = lane_params(v);
-    const uint2 kc = codes16<false>(k, kp), vc = codes16<kBf16>(v, vp);
-    const uint32_t kp1 = __shfl_down_sync(0xffffffffu, kp, 4);
-    const uint32_t vp1 = __shfl_down_sync(0xffffffffu, vp, 4);
-    if (row < 0) return;
-    *reinterpret_cast<uint2*>(a.k_codes + row * kCodeBytes + 8 * rl) = kc;
-    *reinterpret_cast<uint2*>(a.v_codes + row * kCodeBytes + 8 * rl) = vc;
-    if (rl == 0) *reinterpret_cast<uint4*>(a.params + row * 16) = make_uint4(kp, kp1, vp, vp1);
 }
 
+template <bool kWide>
 __device__ __forceinline__ void store16(float* p, const float (&x)[16]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        __stcs(reinterpret_cast<float4*>(p) + i,
-               make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
-}
-__device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&x)[16]) {
-#pragma unroll
     for (int i = 0; i < 2; ++i) {
-        uint32_t w[4];
+        uint32_t w[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x[8 * i + 2 * k], x[8 * i + 2 * k + 1]);
-            w[k] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        __stcs(reinterpret_cast<uint4*>(p) + i, make_uint4(w[0], w[1], w[2], w[3]));
+        for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(x[8 * i + k]);
+        store32<kWide>(p + 8 * i, w);
     }
+}
+template <bool kWide>
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&x)[16]) {
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    store32<kWide>(p, w);
 }
 
 // z + s c, one rounding
@@ -223,39 +383,51 @@ __device__ __forceinline__ void values16(uint2 c, uint32_t pr, float (&x)[16]) {
     }
 }
 
-template <typename T>
+template <typename T, bool kWide>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const RowArgs a) {
     const int rl = threadIdx.x & (kRowLanes - 1);
-    const uint32_t r = blockIdx.x * kRowsPerCta + threadIdx.x / kRowLanes;
-    if (r >= a.rows) return;
-    const uint32_t bh = r / a.m;
-    const long long row = cache_row(a, bh, r - bh * a.m);
-    uint2 kc = make_uint2(0u, 0u), vc = kc;
-    uint32_t kp = 0u, vp = 0u;
-    if (row >= 0) {
-        kc = *reinterpret_cast<const uint2*>(a.k_codes + row * kCodeBytes + 8 * rl);
-        vc = *reinterpret_cast<const uint2*>(a.v_codes + row * kCodeBytes + 8 * rl);
-        kp = *reinterpret_cast<const uint32_t*>(a.params + row * 16 + 4 * (rl >> 2));
-        vp = *reinterpret_cast<const uint32_t*>(a.params + row * 16 + 8 + 4 * (rl >> 2));
-    }
-    float x[16];
-    values16(kc, kp, x);
-    if (a.centre && row >= 0) {
-        const float4* mu = reinterpret_cast<const float4*>(a.centre + static_cast<size_t>(bh) * kD +
-                                                           16 * rl);
+    uint2 kc, vc;
+    uint32_t kp, vp;
+    auto load = [&](long long row) {
+        kc = vc = make_uint2(0u, 0u);
+        kp = vp = 0u;
+        if (row >= 0) {
+            kc = __ldg(reinterpret_cast<const uint2*>(a.k_codes + row * kCodeBytes + 8 * rl));
+            vc = __ldg(reinterpret_cast<const uint2*>(a.v_codes + row * kCodeBytes + 8 * rl));
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(a.params + row * 16) + (rl >> 2);
+            kp = __ldg(p);
+            vp = __ldg(p + 2);
+        }
+    };
+    RowAt w = row_at(a, blockIdx.x);
+    load(w.row);
+    for (uint32_t blk = blockIdx.x; blk < a.blocks; blk += gridDim.x) {
+        const RowAt now = w;
+        float k[16], v[16];
+        values16(kc, kp, k);
+        values16(vc, vp, v);
+        if (blk + gridDim.x < a.blocks) {
+            w = row_at(a, blk + gridDim.x);
+            load(w.row);
+        }
+        if (a.centre && now.row >= 0) {
+            const float4* mu = reinterpret_cast<const float4*>(
+                a.centre + static_cast<size_t>(now.bh) * kD + 16 * rl);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 c = __ldg(mu + i);
-            x[4 * i] = __fadd_rn(x[4 * i], c.x);
-            x[4 * i + 1] = __fadd_rn(x[4 * i + 1], c.y);
-            x[4 * i + 2] = __fadd_rn(x[4 * i + 2], c.z);
-            x[4 * i + 3] = __fadd_rn(x[4 * i + 3], c.w);
+            for (int i = 0; i < 4; ++i) {
+                const float4 c = __ldg(mu + i);
+                k[4 * i] = __fadd_rn(k[4 * i], c.x);
+                k[4 * i + 1] = __fadd_rn(k[4 * i + 1], c.y);
+                k[4 * i + 2] = __fadd_rn(k[4 * i + 2], c.z);
+                k[4 * i + 3] = __fadd_rn(k[4 * i + 3], c.w);
+            }
+        }
+        if (blk * kRowsPerCta + threadIdx.x / kRowLanes < a.rows) {
+            const size_t at = static_cast<size_t>(now.r) * kD + 16 * rl;
+            store16<kWide>(static_cast<T*>(const_cast<void*>(a.keys)) + at, k);
+            store16<kWide>(static_cast<T*>(const_cast<void*>(a.values)) + at, v);
         }
     }
-    const size_t at = static_cast<size_t>(r) * kD + 16 * rl;
-    store16(static_cast<T*>(const_cast<void*>(a.keys)) + at, x);
-    values16(vc, vp, x);
-    store16(static_cast<T*>(const_cast<void*>(a.values)) + at, x);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -299,8 +471,6 @@ constexpr int kStageK = 0, kStageV = kTile * kCodeBytes, kStageP = 2 * kTile * k
 constexpr int kStageBytes = kStageP + kTile * kParamBytes;
 constexpr int kAttStages = 2;
 constexpr int kAttSmem = kAttWarps * kAttStages * kStageBytes;
-constexpr int kSms = 152;                        // of a GB300; a plan, and so a workspace's size,
-                                                 // is the same on the host alone
 constexpr int kMergePitch = kD + 4;              // floats a (warp, head) leaves for the CTA's merge
 static_assert(kAttThreads == kD, "the merge: a thread per dim");
 static_assert(kAttWarps * 8 * kMergePitch * 4 <= kAttSmem, "the merge reuses the stages");
@@ -836,13 +1006,29 @@ RowArgs row_args(const mp_kv4& c, const float* centre, int B, int Hkv, int m, in
     a.v_codes = static_cast<uint8_t*>(c.v_codes);
     a.params = static_cast<uint8_t*>(c.params);
     a.rows = static_cast<uint32_t>(B) * Hkv * m;
+    a.blocks = (a.rows + kRowsPerCta - 1) / kRowsPerCta;
     a.Hkv = Hkv;
     a.m = m;
     a.n_begin = n_begin;
     a.ncap = c.n_capacity;
     return a;
 }
-unsigned row_ctas(uint32_t rows) { return (rows + kRowsPerCta - 1) / kRowsPerCta; }
+typedef void (*RowFn)(const RowArgs);
+RowFn pick_write(bool bf16, bool wide) {
+    if (bf16) return wide ? kv4_write_kernel<__nv_bfloat16, true> : kv4_write_kernel<__nv_bfloat16, false>;
+    return wide ? kv4_write_kernel<float, true> : kv4_write_kernel<float, false>;
+}
+RowFn pick_read(bool bf16, bool wide) {
+    if (bf16) return wide ? kv4_read_kernel<__nv_bfloat16, true> : kv4_read_kernel<__nv_bfloat16, false>;
+    return wide ? kv4_read_kernel<float, true> : kv4_read_kernel<float, false>;
+}
+bool wide_rows(const void* keys, const void* values) {
+    return ((reinterpret_cast<uintptr_t>(keys) | reinterpret_cast<uintptr_t>(values)) & 31u) == 0u;
+}
+// As many CTAs as the GPU holds at once, or as there are blocks
+unsigned row_ctas(const RowArgs& a, int per_sm) {
+    return std::min<unsigned>(a.blocks, kSms * per_sm);
+}
 
 }  // namespace
 
@@ -852,8 +1038,7 @@ cudaError_t launch_kv4_write(const void* keys, const void* values, bool bf16, co
     RowArgs a = row_args(cache, centre, B, Hkv, m, n_begin, positions);
     a.keys = keys;
     a.values = values;
-    if (bf16) kv4_write_kernel<__nv_bfloat16><<<row_ctas(a.rows), kRowThreads, 0, st>>>(a);
-    else kv4_write_kernel<float><<<row_ctas(a.rows), kRowThreads, 0, st>>>(a);
+    pick_write(bf16, wide_rows(keys, values))<<<row_ctas(a, bf16 ? 3 : 2), kRowThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -863,8 +1048,7 @@ cudaError_t launch_kv4_read(const mp_kv4& cache, const float* centre, int B, int
     RowArgs a = row_args(cache, centre, B, Hkv, m, n_begin, positions);
     a.keys = keys;
     a.values = values;
-    if (bf16) kv4_read_kernel<__nv_bfloat16><<<row_ctas(a.rows), kRowThreads, 0, st>>>(a);
-    else kv4_read_kernel<float><<<row_ctas(a.rows), kRowThreads, 0, st>>>(a);
+    pick_read(bf16, wide_rows(keys, values))<<<row_ctas(a, 4), kRowThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -910,10 +1094,10 @@ cudaError_t launch_kv4_attention(const void* q, bool q_bf16, const mp_kv4& cache
 cudaError_t prepare_kv4() {
     cudaFuncAttributes fa;
     cudaError_t e;
-    if ((e = cudaFuncGetAttributes(&fa, kv4_write_kernel<__nv_bfloat16>)) != cudaSuccess) return e;
-    if ((e = cudaFuncGetAttributes(&fa, kv4_write_kernel<float>)) != cudaSuccess) return e;
-    if ((e = cudaFuncGetAttributes(&fa, kv4_read_kernel<__nv_bfloat16>)) != cudaSuccess) return e;
-    if ((e = cudaFuncGetAttributes(&fa, kv4_read_kernel<float>)) != cudaSuccess) return e;
+    for (int i = 0; i < 4; ++i) {
+        if ((e = cudaFuncGetAttributes(&fa, pick_write(i & 1, i & 2))) != cudaSuccess) return e;
+        if ((e = cudaFuncGetAttributes(&fa, pick_read(i & 1, i & 2))) != cudaSuccess) return e;
+    }
     void (*att[2])(const A4Args) = {kv4_attention_kernel<1>, kv4_attention_kernel<2>};
     for (auto fn : att) {
         if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
