@@ -489,44 +489,64 @@ def kv4_cache(B: int, Hkv: int, n_capacity: int, device="cuda") -> KV4Cache:
                     torch.empty(B, Hkv, n_capacity, 8, dtype=torch.bfloat16, device=device))
 
 
-def _kv4(cache, B, Hkv):
-    """The cache's mp_kv4 and its device, checked against the call's B and Hkv (None: any)."""
+# The calls over a 4-bit cache take microseconds on the GPU, so what stands before their launch is
+# kept short: tensors are checked by a few attribute reads each, addresses go to ctypes as plain
+# integers, and the current stream's handle is read without a Stream object.
+
+def _arg(t, device: int, name: str, dtype, shape):
+    """The address of t (None: no tensor), checked: on this device, dtype, shape, contiguous."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        _not_there(t, device, name)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, is {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _not_there(t, device, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    raise ValueError(f"{name} is on {t.device}, the cache on cuda:{device}")
+
+
+def _kv4(cache):
+    """(mp_kv4, device, B, Hkv, n_capacity) of a cache, its tensors checked; the device must be
+    the current one."""
     k, v, p = cache
-    shape = k.shape
-    if not (k.is_cuda and v.is_cuda and p.is_cuda):
+    device = k.get_device()
+    if device < 0:
         raise TypeError("the cache must hold CUDA tensors")
-    if k.dtype != torch.uint8 or v.dtype != torch.uint8 or p.dtype != torch.bfloat16:
-        raise TypeError("a 4-bit cache holds uint8, uint8 and bfloat16 tensors")
-    if len(shape) != 4 or shape[3] != 64 or v.shape != shape or p.shape != (*shape[:3], 8):
-        raise ValueError("k_codes and v_codes must be [B, Hkv, n_capacity, 64] and params "
-                         f"[B, Hkv, n_capacity, 8], got {tuple(shape)}, {tuple(v.shape)}, "
-                         f"{tuple(p.shape)}")
-    if B is not None and (shape[0] != B or shape[1] != Hkv):
-        raise ValueError(f"the cache holds {shape[0]} x {shape[1]} heads, the call {B} x {Hkv}")
-    if not (k.is_contiguous() and v.is_contiguous() and p.is_contiguous()):
-        raise ValueError("the cache's tensors must be contiguous")
-    _same_device(k.device, v, p)
-    return _KV4(k.data_ptr(), v.data_ptr(), p.data_ptr(), shape[2]), k.device
+    if device != torch._C._cuda_getDevice():
+        raise ValueError(f"the cache is on cuda:{device}, which is not the current device")
+    shape = k.shape
+    if len(shape) != 4 or shape[3] != 64:
+        raise ValueError(f"k_codes must be [B, Hkv, n_capacity, 64], got {tuple(shape)}")
+    B, Hkv, cap, _ = shape
+    return _KV4(_arg(k, device, "k_codes", torch.uint8, shape),
+                _arg(v, device, "v_codes", torch.uint8, shape),
+                _arg(p, device, "params", torch.bfloat16, (B, Hkv, cap, 8)),
+                cap), device, B, Hkv, cap
 
 
-def _same_device(device, *tensors):
-    """Every tensor of a 4-bit cache's call is on one device, the current one."""
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {device}, not on the current device")
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device} in one call")
+def _kv4_stream(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
-def _of_batch(t, B, name, dtype, shape=None):
-    """t (or None), checked: dtype, shape [B] unless given, on the GPU, contiguous."""
-    if t is not None:
-        _cuda(t, name)
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}")
-        if tuple(t.shape) != (shape or (B,)):
-            raise ValueError(f"{name} must have shape {shape or (B,)}, got {tuple(t.shape)}")
-    return t
+def _rows_arg(t, device, name, B, Hkv):
+    """(address, dtype code, m) of keys or values [B, Hkv, m, 128]."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        _not_there(t, device, name)
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != B or shape[1] != Hkv:
+        raise ValueError(f"{name} must be [{B}, {Hkv}, m, 128], got {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr(), _dtype(t, name), shape[2]
 
 
 def _use(stream, *tensors):
@@ -542,18 +562,15 @@ def kv4_write(cache: KV4Cache, keys, values, n_begin: int = 0, centre=None, posi
     of every head of the 4-bit cache, or with positions (int32 [B], on the GPU) into rows
     [positions[b], positions[b] + m) of sequence b; rows outside the capacity are not written.
     centre (key_mean's, float32 [B, Hkv, 128]) is subtracted from the keys."""
-    _cuda(keys, "keys", 4)
-    _cuda(values, "values", 4)
-    B, Hkv, m, d = keys.shape
-    if values.shape != keys.shape or values.dtype != keys.dtype:
-        raise ValueError("values must match keys in shape and dtype")
-    c, device = _kv4(cache, B, Hkv)
-    _of_batch(centre, B, "centre", torch.float32, (B, Hkv, d))
-    _of_batch(positions, B, "positions", torch.int32)
-    _same_device(device, keys, values, centre, positions)
-    _check(lib().mp_kv4_write(_ptr(keys), _ptr(values), _dtype(keys, "keys"), _ptr(centre), B, Hkv,
-                              m, d, n_begin, _ptr(positions), ctypes.byref(c), _stream(stream)),
-           "mp_kv4_write")
+    c, device, B, Hkv, _ = _kv4(cache)
+    kp, dt, m = _rows_arg(keys, device, "keys", B, Hkv)
+    d = keys.shape[3]
+    status = lib().mp_kv4_write(
+        kp, _arg(values, device, "values", keys.dtype, keys.shape), dt,
+        _arg(centre, device, "centre", torch.float32, (B, Hkv, d)), B, Hkv, m, d, n_begin,
+        _arg(positions, device, "positions", torch.int32, (B,)), ctypes.byref(c),
+        _kv4_stream(stream, device))
+    _check(status, "mp_kv4_write")
     return cache
 
 
@@ -562,26 +579,25 @@ def kv4_read(cache: KV4Cache, m: int, n_begin: int = 0, centre=None, positions=N
     """Rows [n_begin, n_begin + m) of every head (or from positions[b] on, as kv4_write) as keys,
     values [B, Hkv, m, 128] in dtype, with centre added to the keys; rows outside the capacity
     read as zero."""
-    c, device = _kv4(cache, None, None)
-    B, Hkv = cache.k_codes.shape[:2]
+    c, device, B, Hkv, _ = _kv4(cache)
+    if m < 0:
+        raise ValueError(f"m = {m} tokens")
+    shape = (B, Hkv, m, 128)
     new = []
     if keys is None:
-        keys = torch.empty(B, Hkv, m, 128, dtype=dtype, device=device)
+        keys = torch.empty(shape, dtype=dtype if values is None else values.dtype,
+                           device=cache.k_codes.device)
         new.append(keys)
     if values is None:
-        values = torch.empty(B, Hkv, m, 128, dtype=keys.dtype, device=device)
+        values = torch.empty_like(keys)
         new.append(values)
-    _cuda(keys, "keys", 4)
-    _cuda(values, "values", 4)
-    if tuple(keys.shape) != (B, Hkv, m, 128) or values.shape != keys.shape \
-            or values.dtype != keys.dtype:
-        raise ValueError(f"keys and values must be [{B}, {Hkv}, {m}, 128] of one dtype")
-    _of_batch(centre, B, "centre", torch.float32, (B, Hkv, 128))
-    _of_batch(positions, B, "positions", torch.int32)
-    _same_device(device, keys, values, centre, positions)
-    _check(lib().mp_kv4_read(ctypes.byref(c), _ptr(centre), B, Hkv, m, 128, n_begin,
-                             _ptr(positions), _ptr(keys), _ptr(values), _dtype(keys, "keys"),
-                             _stream(stream)), "mp_kv4_read")
+    kp, dt, _ = _rows_arg(keys, device, "keys", B, Hkv)
+    status = lib().mp_kv4_read(
+        ctypes.byref(c), _arg(centre, device, "centre", torch.float32, (B, Hkv, 128)), B, Hkv, m,
+        128, n_begin, _arg(positions, device, "positions", torch.int32, (B,)),
+        _arg(keys, device, "keys", keys.dtype, shape),
+        _arg(values, device, "values", keys.dtype, shape), dt, _kv4_stream(stream, device))
+    _check(status, "mp_kv4_read")
     _use(stream, *new)
     return keys, values
 
@@ -590,22 +606,34 @@ def kv4_attention_workspace_bytes(B: int, Hq: int, Hkv: int, n: int, d: int = 12
     return int(lib().mp_kv4_attention_workspace_bytes(B, Hq, Hkv, n, d))
 
 
-def _kv4_inputs(codes, centre, W, B, Hkv, cap, d, K, L, cross_polytope):
-    """The codes (laid out for the cache's capacity), centre and W of a sampled decode."""
-    _of_batch(centre, B, "centre", torch.float32, (B, Hkv, d))
-    need = (cp_codes_bytes if cross_polytope else codes_bytes)(
-        *((B, Hkv, cap, L) if cross_polytope else (B, Hkv, cap, K, L)))
-    if need and (codes is None or _nbytes(_cuda(codes, "codes")) < need):
-        raise ValueError(f"codes must hold {need} bytes, for {cap} tokens per head")
-    if W is not None and _cuda(W, "W").numel() < d * (d if cross_polytope else K) * L:
-        raise ValueError(f"W of shape {tuple(W.shape)} has too few hyperplanes")
-
-
-def _kv4_out(q, out, B, Hq, d):
+def _kv4_call(q, cache, n, out, workspace, need):
+    """What the calls on queries share: checks of q, out and the workspace, which are allocated
+    where they are None (need: its size from B, Hq, Hkv, n, d, n_capacity)."""
+    c, device, B, Hkv, cap = _kv4(cache)
+    if not isinstance(q, torch.Tensor) or q.get_device() != device:
+        _not_there(q, device, "q")
+    shape = q.shape
+    if len(shape) != 3 or shape[0] != B:
+        raise ValueError(f"q must be [{B}, Hq, 128], got {tuple(shape)}")
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    n = cap if n is None else int(n)
+    if not 1 <= n <= cap:
+        raise ValueError(f"n = {n} outside [1, {cap}] (the cache's capacity)")
+    qt = _dtype(q, "q")
+    new = []
     if out is None:
-        return torch.empty(B, Hq, d, dtype=torch.float32, device=q.device), True
-    _of_batch(out, B, "out", torch.float32, (B, Hq, d))
-    return out, False
+        out = torch.empty(shape, dtype=torch.float32, device=q.device)
+        new.append(out)
+    op = _arg(out, device, "out", torch.float32, shape)
+    if workspace is None:
+        workspace = torch.empty(max(need(B, shape[1], Hkv, n, shape[2], cap), 256),
+                                dtype=torch.uint8, device=q.device)
+        new.append(workspace)
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous and on the cache's device")
+    return (c, device, (B, shape[1], Hkv, n, shape[2]), cap, q.data_ptr(), qt, out, op,
+            workspace.data_ptr(), _nbytes(workspace), new)
 
 
 def kv4_attention(q, cache: KV4Cache, n=None, lengths=None, scale: float = 0.0, out=None,
@@ -613,45 +641,62 @@ def kv4_attention(q, cache: KV4Cache, n=None, lengths=None, scale: float = 0.0, 
     """Exact attention of one query token per sequence, q [B, Hq, 128], over the first n tokens
     (default: the capacity) of a 4-bit cache, or the first lengths[b] (int32 [B], on the GPU, at
     most n) of sequence b; returns out [B, Hq, 128] float32, zero for a sequence of length 0."""
-    _cuda(q, "q", 3)
-    B, Hq, d = q.shape
-    Hkv = cache.k_codes.shape[1]
-    c, device = _kv4(cache, B, Hkv)
-    n, _ = _lengths(cache.k_codes.shape, n)
-    _of_batch(lengths, B, "lengths", torch.int32)
-    out, made = _kv4_out(q, out, B, Hq, d)
-    need = int(lib().mp_kv4_attention_workspace_bytes(B, Hq, Hkv, n, d))
-    ws = _workspace(workspace, need, device)
-    _same_device(device, q, lengths, out, ws)
-    _check(lib().mp_kv4_attention(_ptr(q), _dtype(q, "q"), ctypes.byref(c), B, Hq, Hkv, n, d,
-                                  _ptr(lengths), scale, _ptr(out), _ptr(ws), _nbytes(ws),
-                                  _stream(stream)), "mp_kv4_attention")
-    _use(stream, *([out] if made else []), *([ws] if workspace is None else []))
+    c, device, dims, _, qp, qt, out, op, wp, size, new = _kv4_call(
+        q, cache, n, out, workspace,
+        lambda B, Hq, Hkv, n, d, cap: kv4_attention_workspace_bytes(B, Hq, Hkv, n, d))
+    status = lib().mp_kv4_attention(
+        qp, qt, ctypes.byref(c), *dims, _arg(lengths, device, "lengths", torch.int32, dims[:1]),
+        scale, op, wp, size, _kv4_stream(stream, device))
+    _check(status, "mp_kv4_attention")
+    _use(stream, *new)
     return out
+
+
+def _kv4_sampled(q, codes, centre, cache, K, L, n_sink, n_local, scale, out, workspace, n, radius,
+                 logu_table, n_indexed=0, scanned=True):
+    """_kv4_call for a sampled decode, with its parameters, and its codes (laid out for the
+    cache's capacity; not needed where nothing is scanned) and centre checked."""
+    cap = cache.k_codes.shape[2]
+    p = _params(K, L, n_sink, n_local, scale, cap, n_indexed, radius=radius, logu_table=logu_table)
+
+    def need(B, Hq, Hkv, n, d, cap):
+        size = int(lib().mp_decode_workspace_bytes(B, Hq, Hkv, n, d, ctypes.byref(p)))
+        if size == 0:
+            raise MagicPIGError("mp_decode_workspace_bytes rejected the shapes/parameters")
+        return size
+
+    call = _kv4_call(q, cache, n, out, workspace, need)
+    device, (B, _, Hkv, _, d) = call[1], call[2]
+    size = cp_codes_bytes(B, Hkv, cap, L) if logu_table is not None \
+        else codes_bytes(B, Hkv, cap, K, L)
+    if codes is not None:
+        _cuda(codes, "codes")
+    if size and scanned and (codes is None or _nbytes(codes) < size):
+        raise ValueError(f"codes must hold {size} bytes, for {cap} tokens per head")
+    for t in (codes, radius, logu_table):
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"a tensor is on {t.device}, the cache on cuda:{device}")
+    cp = _arg(centre, device, "centre", torch.float32, (B, Hkv, d))
+    return call, p, None if codes is None else codes.data_ptr(), cp
 
 
 def kv4_decode_attention(q, codes, centre, W, cache: KV4Cache, K: int, L: int, n_sink: int,
                          n_local: int, scale: float = 0.0, out=None, workspace=None, stream=None,
                          n=None, radius=None, logu_table=None):
     """decode_attention over the first n tokens of a 4-bit cache (written with this centre)."""
-    _cuda(q, "q", 3)
-    B, Hq, d = q.shape
-    Hkv = cache.k_codes.shape[1]
-    c, device = _kv4(cache, B, Hkv)
-    n, cap = _lengths(cache.k_codes.shape, n)
-    _kv4_inputs(codes, centre, _cuda(W, "W"), B, Hkv, cap, d, K, L, logu_table is not None)
-    out, made = _kv4_out(q, out, B, Hq, d)
-    p = _params(K, L, n_sink, n_local, scale, cap, radius=radius, logu_table=logu_table)
-    need = int(lib().mp_decode_workspace_bytes(B, Hq, Hkv, n, d, ctypes.byref(p)))
-    if need == 0:
-        raise MagicPIGError("mp_decode_workspace_bytes rejected the shapes/parameters")
-    ws = _workspace(workspace, need, device)
-    _same_device(device, q, codes, centre, W, out, ws, radius, logu_table)
-    _check(lib().mp_kv4_decode_attention(
-        _ptr(q), _dtype(q, "q"), _ptr(codes), _ptr(centre), _ptr(W), _dtype(W, "W"),
-        ctypes.byref(c), B, Hq, Hkv, n, d, ctypes.byref(p), _ptr(out), _ptr(ws), _nbytes(ws),
-        _stream(stream)), "mp_kv4_decode_attention")
-    _use(stream, *([out] if made else []), *([ws] if workspace is None else []))
+    call, p, codes_p, centre_p = _kv4_sampled(q, codes, centre, cache, K, L, n_sink, n_local,
+                                              scale, out, workspace, n, radius, logu_table)
+    c, device, dims, _, qp, qt, out, op, wp, size, new = call
+    _cuda(W, "W")
+    if W.get_device() != device:
+        _not_there(W, device, "W")
+    if W.numel() < dims[4] * (dims[4] if logu_table is not None else K) * L:
+        raise ValueError(f"W of shape {tuple(W.shape)} has too few hyperplanes")
+    status = lib().mp_kv4_decode_attention(
+        qp, qt, codes_p, centre_p, W.data_ptr(), _dtype(W, "W"), ctypes.byref(c), *dims,
+        ctypes.byref(p), op, wp, size, _kv4_stream(stream, device))
+    _check(status, "mp_kv4_decode_attention")
+    _use(stream, *new)
     return out
 
 
@@ -660,20 +705,15 @@ def kv4_sampled_attention(q, codes, centre, cache: KV4Cache, K: int, L: int, n_s
                           radius=None, logu_table=None):
     """Second half of kv4_decode_attention (after encode_query filled `workspace`, its keys_shape
     [B, Hkv, n_capacity, 128])."""
-    _cuda(q, "q", 3)
-    _cuda(workspace, "workspace")
-    B, Hq, d = q.shape
-    Hkv = cache.k_codes.shape[1]
-    c, device = _kv4(cache, B, Hkv)
-    n, cap = _lengths(cache.k_codes.shape, n)
-    _kv4_inputs(codes, centre, None, B, Hkv, cap, d, K, L, logu_table is not None)
-    out, _ = _kv4_out(q, out, B, Hq, d)
-    p = _params(K, L, n_sink, n_local, scale, cap, radius=radius, logu_table=logu_table)
-    _same_device(device, q, codes, centre, out, workspace, radius, logu_table)
-    _check(lib().mp_kv4_sampled_attention(
-        _ptr(q), _dtype(q, "q"), _ptr(codes), _ptr(centre), ctypes.byref(c), B, Hq, Hkv, n, d,
-        ctypes.byref(p), _ptr(out), _ptr(workspace), _nbytes(workspace), _stream(stream)),
-        "mp_kv4_sampled_attention")
+    call, p, codes_p, centre_p = _kv4_sampled(q, codes, centre, cache, K, L, n_sink, n_local,
+                                              scale, out, _cuda(workspace, "workspace"), n, radius,
+                                              logu_table)
+    c, device, dims, _, qp, qt, out, op, wp, size, new = call
+    status = lib().mp_kv4_sampled_attention(
+        qp, qt, codes_p, centre_p, ctypes.byref(c), *dims, ctypes.byref(p), op, wp, size,
+        _kv4_stream(stream, device))
+    _check(status, "mp_kv4_sampled_attention")
+    _use(stream, *new)
     return out
 
 
@@ -681,27 +721,20 @@ def kv4_sampled_attention_buckets(q, buckets, centre, cache: KV4Cache, K: int, L
                                   n_sink: int, n_local: int, out, workspace, scale: float = 0.0,
                                   stream=None, codes=None, n=None, n_indexed=None, radius=None):
     """sampled_attention_buckets over a 4-bit cache (written with this centre)."""
-    _cuda(q, "q", 3)
-    _cuda(workspace, "workspace")
+    call, p, codes_p, centre_p = _kv4_sampled(
+        q, codes, centre, cache, K, L, n_sink, n_local, scale, out, _cuda(workspace, "workspace"),
+        n, radius, None, 0 if n_indexed is None else int(n_indexed), codes is not None)
+    c, device, dims, _, qp, qt, out, op, wp, size, new = call
     _cuda(buckets, "buckets")
-    B, Hq, d = q.shape
-    Hkv = cache.k_codes.shape[1]
-    c, device = _kv4(cache, B, Hkv)
-    n, cap = _lengths(cache.k_codes.shape, n)
-    if codes is not None:
-        _kv4_inputs(codes, centre, None, B, Hkv, cap, d, K, L, False)
-    _of_batch(centre, B, "centre", torch.float32, (B, Hkv, d))
-    indexed = n if n_indexed is None else int(n_indexed)
-    if _nbytes(buckets) < buckets_bytes(B, Hkv, indexed, K, L):
-        raise ValueError(f"buckets too small for {indexed} keys per head")
-    out, _ = _kv4_out(q, out, B, Hq, d)
-    p = _params(K, L, n_sink, n_local, scale, cap, 0 if n_indexed is None else int(n_indexed),
-                radius=radius)
-    _same_device(device, q, buckets, codes, centre, out, workspace, radius)
-    _check(lib().mp_kv4_sampled_attention_buckets(
-        _ptr(q), _dtype(q, "q"), _ptr(buckets), _ptr(codes), _ptr(centre), ctypes.byref(c), B, Hq,
-        Hkv, n, d, ctypes.byref(p), _ptr(out), _ptr(workspace), _nbytes(workspace),
-        _stream(stream)), "mp_kv4_sampled_attention_buckets")
+    indexed = dims[3] if not n_indexed else int(n_indexed)
+    if buckets.get_device() != device \
+            or _nbytes(buckets) < buckets_bytes(dims[0], dims[2], indexed, K, L):
+        raise ValueError(f"buckets too small for {indexed} keys per head, or elsewhere")
+    status = lib().mp_kv4_sampled_attention_buckets(
+        qp, qt, buckets.data_ptr(), codes_p, centre_p, ctypes.byref(c), *dims, ctypes.byref(p), op,
+        wp, size, _kv4_stream(stream, device))
+    _check(status, "mp_kv4_sampled_attention_buckets")
+    _use(stream, *new)
     return out
 
 

@@ -976,24 +976,28 @@ AttPlan attention_plan(int B, int Hq, int Hkv, int n) {
     p.nt = G <= 4 ? 1 : 2;
     p.chunks = (G + 4 * p.nt - 1) / (4 * p.nt);
     const long long units = static_cast<long long>(B) * Hkv * p.chunks;
-    const long long slots = kSms * (p.nt == 1 ? 3 : 2);
-    const int tiles = (n + kTile - 1) / kTile;
-    // waves of CTAs times the steps (four tiles, one a warp) of a CTA, the start of a CTA and the
-    // second kernel counted in steps
+    const int slots = kSms * (p.nt == 1 ? 3 : 2);
+    // steps (four tiles, one a warp) of a unit; a split takes `per` of them
+    const int steps = (n - 1) / (kTile * kAttWarps) + 1;
+    // waves of CTAs times the steps of a CTA, the start of a CTA and the second kernel counted in
+    // steps. One split, else about as many as fill one, two or three waves: what lies between
+    // leaves a wave part empty, what lies beyond pays more starts.
     const long long kStart = 3, kMerge = 4;
-    long long best = -1;
-    for (int s = 1; s <= 256 && s <= (tiles + kAttWarps - 1) / kAttWarps; ++s) {
-        const int per = (tiles + s - 1) / s;
-        const int per4 = (per + kAttWarps - 1) / kAttWarps * kAttWarps;
-        const int used = (tiles + per4 - 1) / per4;
-        const long long waves = (units * used + slots - 1) / slots;
-        const long long cost = waves * (per4 / kAttWarps + kStart) + (used > 1 ? kMerge : 0);
-        if (best < 0 || cost < best) {
+    int per = steps;
+    long long best = ((units + slots - 1) / slots) * (steps + kStart);
+    for (int waves = 1; waves <= 3; ++waves) {
+        const long long most = std::min<long long>(256, slots * waves / units);
+        if (most < 2) continue;
+        const int each = static_cast<int>((steps + most - 1) / most);
+        const int used = (steps + each - 1) / each;
+        const long long cost = ((units * used + slots - 1) / slots) * (each + kStart) + kMerge;
+        if (used > 1 && cost < best) {
             best = cost;
-            p.splits = used;
-            p.tiles_per_split = per4;
+            per = each;
         }
     }
+    p.splits = (steps + per - 1) / per;
+    p.tiles_per_split = per * kAttWarps;
     return p;
 }
 
