@@ -433,21 +433,23 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const RowArgs a) 
 // ------------------------------------------------------------------------------------------------
 // Exact attention of one query token per sequence.
 //
-// With a key's codes c, step s and minimum z per group, q.k = sum_g s_g (sum_e q_e (c_e - 8)) +
-// (z_g + 8 s_g) sum_e q_e, and the value sum likewise: the products of codes with queries and of
-// codes with weights are matrix products of small exact integers, which the warp's tensor-core
-// instruction m16n8k16 (fp16 in, fp32 sums) takes with the 16 tokens or 16 dims as its rows and
-// four query heads as its eight columns, each head as two fp16 halves (22 bits). Steps and minima
-// join outside, in fp32. The tcgen05 instructions want 128 rows and operands unpacked into shared
-// memory, where a byte of codes would become four; here codes go from shared memory to fragments
-// in registers, an instruction of unpacking per value.
+// With a key's codes c, step s and minimum z per group, q.k = sum_g s_g (sum_e q_e c_e) + z_g sum_e
+// q_e, and the value sum likewise: the products of codes with queries and of codes with weights
+// are matrix products of small exact integers, which the warp's tensor-core instruction m16n8k16
+// (fp16 in, fp32 sums) takes with the 16 tokens or 16 dims as its rows and four query heads as its
+// eight columns, each head as two fp16 halves (22 bits). Steps and minima join outside, in fp32.
+// The tcgen05 instructions want 128 rows and operands unpacked into shared memory, where a byte of
+// codes would become four; here codes go from shared memory to fragments in registers, half an
+// instruction of unpacking a value.
 //
 // A warp takes tiles of 64 tokens on its own, two in flight (cp.async; rows of 64 bytes whose
 // 16-byte pieces are exchanged so that ldmatrix meets no bank conflict): logits of the tile, one
 // step of the running maximum, weights, weighted codes summed from zero and added to the running
-// sums in fp32 (the tensor core's own sums round toward zero: kept short, they lose nothing that
-// matters, and the codes of odd tokens are taken minus 7, of even ones minus 8, so that the part
-// of a sum that the minima take back again stays near zero).
+// sums in fp32. The tensor core's own sums round toward zero. They are kept short, and near zero:
+// the codes of tokens 8-15 of a fragment enter as 15 - c under negative weights, and what that and
+// the minima make up, sum w z over tokens 0-7 and sum w (z + 15 s) over tokens 8-15, is summed in
+// fp32 token by token, where the two cancel as well. Without it the mean code of 7.5 times the
+// weights would stand against a sum that is 100 times smaller, and its rounding with it.
 // ------------------------------------------------------------------------------------------------
 struct A4Args {
     const void* q;
@@ -499,21 +501,16 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
 }
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
@@ -526,21 +523,15 @@ __device__ __forceinline__ uint32_t warp_max(uint32_t x) {
 }
 
 // Eight codes of a word as four fp16 pairs: with c0 .. c3 the codes of its low half and c4 .. c7 of
-// its high half, `lo` to be taken off the former and `hi` off the latter, the pairs are c0 - lo and
-// c4 - hi, (c0 - lo) + 16 (c1 - lo) and so on, the same of c2, c3, c6, c7. Putting a byte under the
-// exponent of 1024 is one byte permute, and masking it one logic instruction: four on the integer
-// pipe for eight codes, which is what bounds the kernel, where a pair for every code costs five
-// (each code by mask and exponent, and a shift). The other matrix takes the sum apart again.
-template <int lo, int hi>
+// its high half, the pairs are (c0, c4), (c0 + 16 c1, c4 + 16 c5) and the same of c2, c3, c6, c7, all
+// times 2^-24: a byte is a subnormal fp16 as it stands, and the tensor core takes those exactly.
+// Two byte permutes and two masks for eight codes; the other matrix takes the sums of two codes
+// apart again. (Codes under the exponent of 1024, with 1024 + 8 taken off, cost twice that.)
 __device__ __forceinline__ void unpack_pairs(uint32_t w, uint32_t (&h)[4]) {
-    constexpr uint32_t kOne = (0xe400u + lo) | ((0xe400u + hi) << 16);             // -(1024 + x)
-    constexpr uint32_t kTwo = (0xe400u + 17 * lo) | ((0xe400u + 17 * hi) << 16);   // -(1024 + 17 x)
-    const uint32_t x = __byte_perm(w, 0x64646464u, 0x4240);
-    const uint32_t y = __byte_perm(w, 0x64646464u, 0x4341);
-    h[0] = hadd2(x & 0xff0fff0fu, kOne);
-    h[1] = hadd2(x, kTwo);
-    h[2] = hadd2(y & 0xff0fff0fu, kOne);
-    h[3] = hadd2(y, kTwo);
+    h[1] = __byte_perm(w, 0u, 0x4240);
+    h[3] = __byte_perm(w, 0u, 0x4341);
+    h[0] = h[1] & 0x000f000fu;
+    h[2] = h[3] & 0x000f000fu;
 }
 
 // x as two fp16: its leading 11 bits in the low half, the rest of it in the high half
@@ -624,10 +615,10 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
 
     // ---- the queries as column fragments: column 2 h is head h's leading half, 2 h + 1 the rest.
     // A lane loads head lane / 8 of its four (dims 32 m + 8 t ..), scaled by a power of two so
-    // that the largest element lies in [2^6, 2^7); fac undoes it on the logits. Against the pairs
-    // c0 and c0 + 16 c1 of unpack_pairs stand q0 - q1 / 16 and q1 / 16.
+    // that the largest element lies in [2^14, 2^15); fac undoes it on the logits, and the 2^-24 of
+    // the codes. Against the pairs c0 and c0 + 16 c1 of unpack_pairs stand q0 - q1 / 16 and q1 / 16.
     uint32_t qb[NT][4][4];
-    float fac[NT], qsum8[NT][2];
+    float fac[NT], qsum[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int h = 4 * nt + (lane >> 3);
@@ -643,8 +634,8 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
             }
         big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
         big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        const uint32_t ex = min(max(big >> 23, 7u), 253u);
-        const float down = __uint_as_float((260u - ex) << 23), up = __uint_as_float((ex - 6u) << 23);
+        const uint32_t ex = min(max(big >> 23, 15u), 243u);
+        const float down = __uint_as_float((268u - ex) << 23), up = __uint_as_float((ex + 10u) << 23);
         float sum[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
@@ -672,7 +663,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
         for (int g = 0; g < 2; ++g) {
             sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
             sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
-            qsum8[nt][g] = 8.0f * __shfl_sync(0xffffffffu, sum[g], 8 * t);
+            qsum[nt][g] = 0x1p-24f * __shfl_sync(0xffffffffu, sum[g], 8 * t);
         }
         fac[nt] = fmaxf(__shfl_sync(0xffffffffu, a.scale * up, 8 * t), 1.17549435e-38f);
     }
@@ -688,57 +679,59 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o_run[nt][m][e] = 0.0f;
     }
-    const float mid_steps = (r & 1) ? 7.0f : 8.0f;                       // of this lane's values
-    const uint32_t lm = (lane & 7) * kCodeBytes + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+    // ldmatrix: matrices 0, 1 are the two pieces of a group of dims of tokens 0-7 of a fragment,
+    // 2, 3 those of tokens 8-15; the other group's pieces differ in bit 5 of the address
+    const uint32_t lm = (8 * (lane >> 4) + (lane & 7)) * kCodeBytes +
+                        ((((lane >> 3) & 1) ^ ((lane >> 1) & 3)) << 4);
 
     for (int it = 0; it < mine; ++it) {
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();
         const uint32_t st = stage0 + (it & 1) * kStageBytes;
-        const uint8_t* prm = smem + (st - smem_u32(smem)) + kStageP;
+        const uint8_t* prm = smem + (st - smem_u32(smem)) + kStageP + r * kParamBytes;
         const int key0 = (tile0 + warp + it * kAttWarps) * kTile;
 
-        // ---- logits (fac of them, base 2) of tokens 16 j + r and 16 j + 8 + r
+        // ---- logits (fac of them, base 2) of tokens 16 j + r and 16 j + 8 + r, a group at a time
         float lg[NT][2 * kSub];
-        uint32_t vmax = 0u;                      // group 0 in the low half, 1 in the high half
 #pragma unroll
-        for (int j = 0; j < kSub; ++j) {
-            uint32_t k0[4], k1[4];
-            ldmatrix4(k0, st + kStageK + (16 * j) * kCodeBytes + lm);
-            ldmatrix4(k1, st + kStageK + (16 * j + 8) * kCodeBytes + lm);
-            float c[NT][2][4];                   // from 8 sum q: codes minus 8, plus 8
+        for (int g = 0; g < 2; ++g) {
+            float c[NT][kSub][4];
+            uint32_t kw[kSub][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int j = 0; j < kSub; ++j) {
+                ldmatrix4(kw[j], st + kStageK + 16 * j * kCodeBytes + (lm ^ (g << 5)));
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    c[nt][g][0] = c[nt][g][2] = qsum8[nt][g];
-                    c[nt][g][1] = c[nt][g][3] = 0.0f;
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) c[nt][j][e] = 0.0f;
+            }
+            // the fragments' products side by side: those of one fragment wait for each other
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                uint32_t x0[kSub][4], x1[kSub][4];
+#pragma unroll
+                for (int j = 0; j < kSub; ++j) {
+                    unpack_pairs(kw[j][m], x0[j]);
+                    unpack_pairs(kw[j][m + 2], x1[j]);
                 }
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                uint32_t x0[4], x1[4];
-                unpack_pairs<8, 8>(k0[m], x0);
-                unpack_pairs<8, 8>(k1[m], x1);
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma16816(c[nt][m >> 1], x0[0], x1[0], x0[1], x1[1], qb[nt][m][0], qb[nt][m][1]);
-                    mma16816(c[nt][m >> 1], x0[2], x1[2], x0[3], x1[3], qb[nt][m][2], qb[nt][m][3]);
-                }
+                    for (int i = 0; i < 4; i += 2)
+#pragma unroll
+                        for (int j = 0; j < kSub; ++j)
+                            mma16816(c[nt][j], x0[j][i], x1[j][i], x0[j][i + 1], x1[j][i + 1],
+                                     qb[nt][2 * g + m][i], qb[nt][2 * g + m][i + 1]);
             }
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const uint4 p = *reinterpret_cast<const uint4*>(
-                    prm + (16 * j + 8 * half + r) * kParamBytes);
-                const float s0 = __uint_as_float(p.x << 16), s1 = __uint_as_float(p.y << 16);
-                const float z0 = __uint_as_float(p.x & 0xffff0000u);
-                const float z1 = __uint_as_float(p.y & 0xffff0000u);
-                vmax = __vmaxu2(vmax, __byte_perm(p.z, p.w, 0x5410));    // the values' steps
+            for (int i = 0; i < 2 * kSub; ++i) {
+                const uint32_t p = *reinterpret_cast<const uint32_t*>(prm + 8 * i * kParamBytes + 4 * g);
+                const float s = __uint_as_float(p << 16), z = __uint_as_float(p & 0xffff0000u);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float u = s0 * (c[nt][0][2 * half] + c[nt][0][2 * half + 1]);
-                    u = fmaf(s1, c[nt][1][2 * half] + c[nt][1][2 * half + 1], u);
-                    u = fmaf(z0, qsum8[nt][0] * 0.125f, u);
-                    lg[nt][2 * j + half] = fmaf(z1, qsum8[nt][1] * 0.125f, u);
+                    const float (&d)[4] = c[nt][i >> 1];
+                    const float u = g == 0 ? z * qsum[nt][g] : fmaf(z, qsum[nt][g], lg[nt][i]);
+                    lg[nt][i] = fmaf(s, d[2 * (i & 1)] + d[2 * (i & 1) + 1], u);
                 }
             }
         }
@@ -771,81 +764,81 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
                 sum += lg[nt][i];
             }
             l_run[nt] = fmaf(l_run[nt], corr[nt], sum);
-            mid_run[nt][0] *= corr[nt];
-            mid_run[nt][1] *= corr[nt];
-        }
-        // weights times steps become fp16 halves after a power of two per group brings the tile's
-        // largest step to [2^13, 2^14): 2^(140 - ex), taken back by 2^(ex - 140). A step that is NaN
-        // is the largest of all; its group is NaN in every head anyhow.
-        float down[2], up[2];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            const uint32_t ex = max(warp_max(g ? vmax >> 16 : vmax & 0xffffu) >> 7, 14u);
-            down[g] = __uint_as_float((267u - ex) << 23);
-            up[g] = __uint_as_float((ex - 13u) << 23);
         }
 
-        // ---- weighted codes of the tile
-        float acc[NT][4][2][4];
+        // ---- weighted codes of the tile, a group at a time. Weights times steps become fp16 halves
+        // after a power of two brings the tile's largest step to [2^13, 2^14): 2^(140 - ex), taken
+        // back by 2^(ex - 140). A step that is NaN is the largest of all; its group is NaN in every
+        // head anyhow.
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int g = 0; g < 2; ++g) {
+            uint32_t pw[2 * kSub], vmax = 0u;
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
+            for (int i = 0; i < 2 * kSub; ++i) {
+                pw[i] = *reinterpret_cast<const uint32_t*>(prm + 8 * i * kParamBytes + 8 + 4 * g);
+                vmax = __vmaxu2(vmax, pw[i]);
+            }
+            const uint32_t ex = max(warp_max(vmax & 0xffffu) >> 7, 14u);
+            const float down = __uint_as_float((267u - ex) << 23);
+            const float up = __uint_as_float((ex - 13u) << 23);
+            float acc[NT][2][2][4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+            for (int nt = 0; nt < NT; ++nt) {
+                mid_run[nt][g] *= corr[nt];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[nt][m][i][e] = 0.0f;
+                for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int j = 0; j < kSub; ++j) {
-            uint32_t v0[4], v1[4], wb[NT][2][2];
-            ldmatrix4_trans(v0, st + kStageV + (16 * j) * kCodeBytes + lm);
-            ldmatrix4_trans(v1, st + kStageV + (16 * j + 8) * kCodeBytes + lm);
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int row = 16 * j + 8 * half + r;
-                const uint2 p = *reinterpret_cast<const uint2*>(prm + row * kParamBytes + 8);
-                const uint32_t pw[2] = {p.x, p.y};
+                        for (int e = 0; e < 4; ++e) acc[nt][m][i][e] = 0.0f;
+            }
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const float s = __uint_as_float(pw[g] << 16);
-                    const float mid = fmaf(mid_steps, s, __uint_as_float(pw[g] & 0xffff0000u));
-                    const float sd = s * down[g];
+            for (int j = 0; j < kSub; ++j) {
+                uint32_t vw[4], x[4][4], wb[NT][2];
+                ldmatrix4_trans(vw, st + kStageV + 16 * j * kCodeBytes + (lm ^ (g << 5)));
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t p = pw[2 * j + half];
+                    const float s = __uint_as_float(p << 16);
+                    float mid = __uint_as_float(p & 0xffff0000u);
+                    if (half) mid = fmaf(15.0f, s, mid);
+                    const float sd = half ? s * -down : s * down;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const float w = lg[nt][2 * j + half];
                         mid_run[nt][g] = fmaf(w, mid, mid_run[nt][g]);
-                        wb[nt][g][half] = transpose8x8(split_f16(w * sd));
+                        wb[nt][half] = transpose8x8(split_f16(w * sd));
                     }
                 }
-            }
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                uint32_t x0[4], x1[4];
-                unpack_pairs<8, 7>(v0[m], x0);
-                unpack_pairs<8, 7>(v1[m], x1);
+                for (int i = 0; i < 4; ++i) unpack_pairs(i < 2 ? vw[i] : ~vw[i], x[i]);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const uint32_t b0 = wb[nt][m >> 1][0], b1 = wb[nt][m >> 1][1];
-                    mma16816(acc[nt][m][0], x0[0], x0[1], x1[0], x1[1], b0, b1);
-                    mma16816(acc[nt][m][1], x0[2], x0[3], x1[2], x1[3], b0, b1);
-                }
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            mma16816(acc[nt][m][i], x[m][2 * i], x[m][2 * i + 1], x[m + 2][2 * i],
+                                     x[m + 2][2 * i + 1], wb[nt][0], wb[nt][1]);
             }
+            if (g == 1) {
+                __syncwarp();
+                issue(it + 2);
+            }
+            // the second row of a pair holds its own dim's sum 16 times and the first one's once
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float one = acc[nt][m][i][0] + acc[nt][m][i][1];
+                        const float two = (acc[nt][m][i][2] + acc[nt][m][i][3]) - one;
+                        float* o = &o_run[nt][2 * g + m][2 * i];
+                        o[0] = fmaf(one, up, o[0] * corr[nt]);
+                        o[1] = fmaf(two, up * 0.0625f, o[1] * corr[nt]);
+                    }
         }
-        __syncwarp();
-        issue(it + 2);
-        // the second row of a pair holds its own dim's sum 16 times and the first one's once
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float one = acc[nt][m][i][0] + acc[nt][m][i][1];
-                    const float two = (acc[nt][m][i][2] + acc[nt][m][i][3]) - one;
-                    float* o = &o_run[nt][m][2 * i];
-                    o[0] = fmaf(one, up[m >> 1], o[0] * corr[nt]);
-                    o[1] = fmaf(two, up[m >> 1] * 0.0625f, o[1] * corr[nt]);
-                }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 
@@ -864,9 +857,10 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const float mid = mid_run[nt][m >> 1];
+            const float (&o)[4] = o_run[nt][m];  // sums of codes, times 2^-24
             *reinterpret_cast<float4*>(dst + 32 * m + 4 * r) =
-                make_float4(o_run[nt][m][0] + mid, o_run[nt][m][1] + mid, o_run[nt][m][2] + mid,
-                            o_run[nt][m][3] + mid);
+                make_float4(fmaf(o[0], 0x1p24f, mid), fmaf(o[1], 0x1p24f, mid),
+                            fmaf(o[2], 0x1p24f, mid), fmaf(o[3], 0x1p24f, mid));
         }
         if (r == 0) {
             dst[kD] = base_run[nt];
@@ -903,7 +897,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
 // The splits of a query row, joined in a fixed order: warp w folds splits w, w + kMergeWarps, ...,
 // kMergeAhead of them loaded at once, four dims a lane; then the warps in order. A split that
 // holds nothing has m = -inf and zeros; NaN passes through its zero factor.
-constexpr int kMergeWarps = 8, kMergeAhead = 4;
+constexpr int kMergeWarps = 16, kMergeAhead = 4;
 __global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_kernel(const A4Args a) {
     __shared__ __align__(16) float join[kMergeWarps][kMergePitch];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, splits = a.splits;
