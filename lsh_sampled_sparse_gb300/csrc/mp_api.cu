@@ -539,8 +539,9 @@ mp_status mp_kv4_read(const mp_kv4* cache, const float* centre, int B, int Hkv, 
 }
 
 static bool valid_kv4_attention(int B, int Hq, int Hkv, int n, int d) {
-    return B >= 1 && Hq >= 1 && Hkv >= 1 && n >= 1 && d >= 1 && Hq % Hkv == 0 &&
-           static_cast<long long>(B) * Hq <= (1 << 24);
+    // tokens, a CTA's share past them included, and query rows are numbered in 32 bits
+    return B >= 1 && Hq >= 1 && Hkv >= 1 && n >= 1 && n <= (1 << 30) && d >= 1 && Hq % Hkv == 0 &&
+           static_cast<long long>(B) * Hq <= (1 << 22);
 }
 
 size_t mp_kv4_attention_workspace_bytes(int B, int Hq, int Hkv, int n, int d) {

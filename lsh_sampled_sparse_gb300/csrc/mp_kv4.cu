@@ -439,8 +439,8 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const RowArgs a) 
 // (fp16 in, fp32 sums) takes with the 16 tokens or 16 dims as its rows and four query heads as its
 // eight columns, each head as two fp16 halves (22 bits). Steps and minima join outside, in fp32.
 // The tcgen05 instructions want 128 rows and operands unpacked into shared memory, where a byte of
-// codes would become four; here codes go from shared memory to fragments in registers, half an
-// instruction of unpacking a value.
+// codes would become four; here codes go from shared memory to fragments in registers, three
+// quarters of an instruction of unpacking a value.
 //
 // A warp takes tiles of 64 tokens on its own, two in flight (cp.async; rows of 64 bytes whose
 // 16-byte pieces are exchanged so that ldmatrix meets no bank conflict): logits of the tile, one
@@ -459,7 +459,7 @@ struct A4Args {
     const int32_t* lengths;
     float* part;                                 // [row][split][kPart]: o, m, l
     float* out;
-    int q_bf16, Hq, Hkv, G, n, ncap, splits, chunks;
+    int q_bf16, q_wide, Hq, Hkv, G, n, ncap, splits, chunks;
     int tiles_per_split;
     float scale;                                 // of q.k, times log2 e
 };
@@ -512,6 +512,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -523,15 +528,17 @@ __device__ __forceinline__ uint32_t warp_max(uint32_t x) {
 }
 
 // Eight codes of a word as four fp16 pairs: with c0 .. c3 the codes of its low half and c4 .. c7 of
-// its high half, the pairs are (c0, c4), (c0 + 16 c1, c4 + 16 c5) and the same of c2, c3, c6, c7, all
-// times 2^-24: a byte is a subnormal fp16 as it stands, and the tensor core takes those exactly.
-// Two byte permutes and two masks for eight codes; the other matrix takes the sums of two codes
-// apart again. (Codes under the exponent of 1024, with 1024 + 8 taken off, cost twice that.)
+// its high half, the pairs are (c0, c4) 2^-10, (c0 + 16 c1, c4 + 16 c5) 2^-24 and the same of c2, c3,
+// c6, c7; the other matrix takes the sums of two codes apart again. A byte is a subnormal fp16 as
+// it stands, which the tensor core takes but adds as if it were 2^-14 large: of a sum of two codes
+// that costs c1 nothing (16 times smaller), but c0 by itself would keep 17 bits only (outputs off by
+// 6e-6 instead of 6e-7), and is multiplied up to a normal number. Six instructions for eight codes,
+// four of them on the integer pipe.
 __device__ __forceinline__ void unpack_pairs(uint32_t w, uint32_t (&h)[4]) {
     h[1] = __byte_perm(w, 0u, 0x4240);
     h[3] = __byte_perm(w, 0u, 0x4341);
-    h[0] = h[1] & 0x000f000fu;
-    h[2] = h[3] & 0x000f000fu;
+    h[0] = mul_f16x2(h[1] & 0x000f000fu, 0x74007400u);           // 2^14
+    h[2] = mul_f16x2(h[3] & 0x000f000fu, 0x74007400u);
 }
 
 // x as two fp16: its leading 11 bits in the low half, the rest of it in the high half
@@ -540,6 +547,39 @@ __device__ __forceinline__ uint32_t split_f16(float x) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(x - hi), "f"(hi));
     return r;
+}
+
+// Eight elements of a query from element i on: the loads, where the queries are aligned for loads
+// of 16 bytes, and later the values (zeros where there is no query).
+struct Query8 {
+    uint4 a, b;
+};
+__device__ __forceinline__ Query8 load_query8(const A4Args& a, size_t i, bool live) {
+    Query8 v;
+    v.a = v.b = make_uint4(0u, 0u, 0u, 0u);
+    if (live && a.q_wide) {
+        if (a.q_bf16) {
+            v.a = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + i));
+        } else {
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + i);
+            v.a = __ldg(p);
+            v.b = __ldg(p + 1);
+        }
+    }
+    return v;
+}
+__device__ __forceinline__ void values_of(const Query8& v, const A4Args& a, size_t i, bool live,
+                                          float (&x)[8]) {
+    const uint32_t w[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
+    if (!a.q_wide) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = live ? load_elem(a.q, a.q_bf16, i + e) : 0.0f;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] = __uint_as_float(!a.q_bf16 ? w[e]
+                                             : (e & 1) ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+    }
 }
 
 // One CTA per (head of keys and values, split of its tokens, chunk of 4 NT query heads of the
@@ -610,13 +650,22 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
         left -= kAttWarps * kTile;
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    // the queries' loads first: behind the tiles of the whole GPU they would hold up the first step
+    Query8 raw[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int h = 4 * nt + (lane >> 3);
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            raw[nt][m] = load_query8(a, (row0 + h) * kD + 32 * m + 8 * t, h < heads);
+    }
     issue(0);
     issue(1);
 
     // ---- the queries as column fragments: column 2 h is head h's leading half, 2 h + 1 the rest.
     // A lane loads head lane / 8 of its four (dims 32 m + 8 t ..), scaled by a power of two so
-    // that the largest element lies in [2^14, 2^15); fac undoes it on the logits, and the 2^-24 of
-    // the codes. Against the pairs c0 and c0 + 16 c1 of unpack_pairs stand q0 - q1 / 16 and q1 / 16.
+    // that the largest element lies in [2^4, 2^5); fac undoes it on the logits, and the 2^-10 of
+    // the codes. Against the pairs of unpack_pairs stand q0 - q1 / 16 and 2^14 q1 / 16.
     uint32_t qb[NT][4][4];
     float fac[NT], qsum[NT][2];
 #pragma unroll
@@ -625,17 +674,15 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
         float x[4][8];
         uint32_t big = 0u;
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+        for (int m = 0; m < 4; ++m) {
+            values_of(raw[nt][m], a, (row0 + h) * kD + 32 * m + 8 * t, h < heads, x[m]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[m][e] = h < heads ? load_elem(a.q, a.q_bf16, (row0 + h) * kD + 32 * m + 8 * t + e)
-                                    : 0.0f;
-                big = max(big, __float_as_uint(x[m][e]) & 0x7fffffffu);
-            }
+            for (int e = 0; e < 8; ++e) big = max(big, __float_as_uint(x[m][e]) & 0x7fffffffu);
+        }
         big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
         big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        const uint32_t ex = min(max(big >> 23, 15u), 243u);
-        const float down = __uint_as_float((268u - ex) << 23), up = __uint_as_float((ex + 10u) << 23);
+        const uint32_t ex = min(max(big >> 23, 5u), 247u);
+        const float down = __uint_as_float((258u - ex) << 23), up = __uint_as_float((ex + 6u) << 23);
         float sum[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
@@ -646,8 +693,8 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
             }
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
-                x[m][e + 1] *= 0.0625f;
-                x[m][e] -= x[m][e + 1];
+                x[m][e] = fmaf(x[m][e + 1], -0.0625f, x[m][e]);
+                x[m][e + 1] *= 1024.0f;
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -663,7 +710,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
         for (int g = 0; g < 2; ++g) {
             sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
             sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
-            qsum[nt][g] = 0x1p-24f * __shfl_sync(0xffffffffu, sum[g], 8 * t);
+            qsum[nt][g] = 0x1p-10f * __shfl_sync(0xffffffffu, sum[g], 8 * t);
         }
         fac[nt] = fmaxf(__shfl_sync(0xffffffffu, a.scale * up, 8 * t), 1.17549435e-38f);
     }
@@ -768,7 +815,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
 
         // ---- weighted codes of the tile, a group at a time. Weights times steps become fp16 halves
         // after a power of two brings the tile's largest step to [2^13, 2^14): 2^(140 - ex), taken
-        // back by 2^(ex - 140). A step that is NaN is the largest of all; its group is NaN in every
+        // back by 2^(ex - 140), with the 2^-10 of the codes. A step that is NaN is the largest of all; its group is NaN in every
         // head anyhow.
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
@@ -780,7 +827,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
             }
             const uint32_t ex = max(warp_max(vmax & 0xffffu) >> 7, 14u);
             const float down = __uint_as_float((267u - ex) << 23);
-            const float up = __uint_as_float((ex - 13u) << 23);
+            const float up = __uint_as_float((ex - 3u) << 23);
             float acc[NT][2][2][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -825,7 +872,8 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
                 __syncwarp();
                 issue(it + 2);
             }
-            // the second row of a pair holds its own dim's sum 16 times and the first one's once
+            // the second row of a pair holds its own dim's sum 16 times and the first one's once, in
+            // units 2^14 smaller
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -833,7 +881,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const float one = acc[nt][m][i][0] + acc[nt][m][i][1];
-                        const float two = (acc[nt][m][i][2] + acc[nt][m][i][3]) - one;
+                        const float two = fmaf(acc[nt][m][i][2] + acc[nt][m][i][3], 16384.0f, -one);
                         float* o = &o_run[nt][2 * g + m][2 * i];
                         o[0] = fmaf(one, up, o[0] * corr[nt]);
                         o[1] = fmaf(two, up * 0.0625f, o[1] * corr[nt]);
@@ -857,10 +905,9 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const float mid = mid_run[nt][m >> 1];
-            const float (&o)[4] = o_run[nt][m];  // sums of codes, times 2^-24
+            const float (&o)[4] = o_run[nt][m];
             *reinterpret_cast<float4*>(dst + 32 * m + 4 * r) =
-                make_float4(fmaf(o[0], 0x1p24f, mid), fmaf(o[1], 0x1p24f, mid),
-                            fmaf(o[2], 0x1p24f, mid), fmaf(o[3], 0x1p24f, mid));
+                make_float4(o[0] + mid, o[1] + mid, o[2] + mid, o[3] + mid);
         }
         if (r == 0) {
             dst[kD] = base_run[nt];
@@ -964,34 +1011,43 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_kernel(const A4Arg
 struct AttPlan {
     int nt, chunks, splits, tiles_per_split;
 };
-AttPlan attention_plan(int B, int Hq, int Hkv, int n) {
+// How many splits: the least of a model of a call's time, in units of 10 ns, over the counts that
+// fill one, two or three CTAs an SM, and three in two or three waves. Measured with NT = 1 (one to
+// three CTAs an SM, 2 to 12 steps each, a step being a tile a warp): what a step takes on an SM
+// with k CTAs when memory does not hold it up is 0.86, 0.66 and 0.72 us over k; memory gives 6.67
+// TB/s whatever the layout; and 5.3, 6.2 and 8.7 us come on top, 4.0 where nothing is split. More
+// CTAs than the call needs lose: 8 heads of 96K tokens take 25.0 us in 152 CTAs, 23.3 in 280 and
+// 26.0 in 440. Sequences shorter than n (`ragged`) leave memory less to do, and a CTA of a later
+// wave goes where a short one has ended, but the CTAs of one wave wait for the longest.
+AttPlan attention_plan(int B, int Hq, int Hkv, int n, bool ragged) {
     AttPlan p;
     const int G = Hq / Hkv;
     p.nt = G <= 4 ? 1 : 2;
     p.chunks = (G + 4 * p.nt - 1) / (4 * p.nt);
     const long long units = static_cast<long long>(B) * Hkv * p.chunks;
-    const int slots = kSms * (p.nt == 1 ? 3 : 2);
-    // steps (four tiles, one a warp) of a unit; a split takes `per` of them
-    const int steps = (n - 1) / (kTile * kAttWarps) + 1;
-    // waves of CTAs times the steps of a CTA, the start of a CTA and the second kernel counted in
-    // steps. One split, else about as many as fill one, two or three waves: what lies between
-    // leaves a wave part empty, what lies beyond pays more starts.
-    const long long kStart = 3, kMerge = 4;
-    int per = steps;
-    long long best = ((units + slots - 1) / slots) * (steps + kStart);
-    for (int waves = 1; waves <= 3; ++waves) {
-        const long long most = std::min<long long>(256, slots * waves / units);
-        if (most < 2) continue;
+    const int steps = (n - 1) / (kTile * kAttWarps) + 1, resident = p.nt == 1 ? 3 : 2;
+    const int step_cost[2][3] = {{86, 66, 72}, {120, 107, 107}};
+    const double memory = static_cast<double>(B) * Hkv * n * (2 * kCodeBytes + kParamBytes) / 66700.0 *
+                          (ragged ? 0.75 : 1.0);
+    double best = -1.0;
+    for (int k = 0; k <= 5; ++k) {               // no split; k CTAs an SM; waves of `resident`
+        const int per_sm = k <= resident ? k : (k - resident + 1) * resident;
+        const long long most = k == 0 ? 1 : std::min<long long>(256, kSms * per_sm / units);
+        if (most < 1 || (k > 0 && most < 2)) continue;
         const int each = static_cast<int>((steps + most - 1) / most);
         const int used = (steps + each - 1) / each;
-        const long long cost = ((units * used + slots - 1) / slots) * (each + kStart) + kMerge;
-        if (used > 1 && cost < best) {
+        const long long busy = (units * used + kSms - 1) / kSms;         // CTAs of the fullest SM
+        const int at_once = static_cast<int>(std::min<long long>(busy, resident));
+        double steps_there = static_cast<double>((busy + at_once - 1) / at_once * at_once) * each;
+        if (ragged && busy > resident) steps_there = 0.75 * steps_there + 0.25 * resident * each;
+        const double fixed = used == 1 ? 400.0 : at_once == 1 ? 530.0 : at_once == 2 ? 620.0 : 870.0;
+        const double cost = fixed + std::max(memory, steps_there * step_cost[p.nt - 1][at_once - 1]);
+        if (best < 0.0 || cost < best) {
             best = cost;
-            per = each;
+            p.splits = used;
+            p.tiles_per_split = each * kAttWarps;
         }
     }
-    p.splits = (steps + per - 1) / per;
-    p.tiles_per_split = per * kAttWarps;
     return p;
 }
 
@@ -1051,14 +1107,16 @@ cudaError_t launch_kv4_read(const mp_kv4& cache, const float* centre, int B, int
 }
 
 size_t kv4_attention_scratch_bytes(int B, int Hq, int Hkv, int n) {
-    const AttPlan p = attention_plan(B, Hq, Hkv, n);
-    return p.splits == 1 ? 0 : static_cast<size_t>(B) * Hq * p.splits * kPart * sizeof(float);
+    // enough for either layout: the caller of a size does not say whether lengths will differ
+    const int splits = std::max(attention_plan(B, Hq, Hkv, n, false).splits,
+                                attention_plan(B, Hq, Hkv, n, true).splits);
+    return splits == 1 ? 0 : static_cast<size_t>(B) * Hq * splits * kPart * sizeof(float);
 }
 
 cudaError_t launch_kv4_attention(const void* q, bool q_bf16, const mp_kv4& cache, int B, int Hq,
                                  int Hkv, int n, const int32_t* lengths, float scale, float* out,
                                  void* workspace, cudaStream_t st) {
-    const AttPlan p = attention_plan(B, Hq, Hkv, n);
+    const AttPlan p = attention_plan(B, Hq, Hkv, n, lengths != nullptr);
     A4Args a;
     a.q = q;
     a.k_codes = static_cast<const uint8_t*>(cache.k_codes);
@@ -1068,6 +1126,7 @@ cudaError_t launch_kv4_attention(const void* q, bool q_bf16, const mp_kv4& cache
     a.part = static_cast<float*>(workspace);
     a.out = out;
     a.q_bf16 = q_bf16;
+    a.q_wide = (reinterpret_cast<uintptr_t>(q) & 15u) == 0u;
     a.Hq = Hq;
     a.Hkv = Hkv;
     a.G = Hq / Hkv;
