@@ -509,19 +509,52 @@ __device__ __forceinline__ void load8(const uint8_t* row, int value, int hl,
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
-// 4-bit rows: one word holds a lane's 8 codes; their group's step s and minimum z are one word of
-// the parameters. A code becomes the float 2^23 + code, less 2^23 + 8: exact; then one fused
-// multiply-add from the group's middle z + 8 s.
-__device__ __forceinline__ void load8(const uint8_t* row, int value, int hl,
-                                      std::integral_constant<KvForm, kKv4>, float (&f)[8]) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(row + value * MP_KV4_CODE_BYTES + 4 * hl);
-    const uint32_t pr = *reinterpret_cast<const uint32_t*>(row + 2 * MP_KV4_CODE_BYTES + 8 * value +
-                                                           4 * (hl >> 3));
-    const float s = __uint_as_float(pr << 16), z = __uint_as_float(pr & 0xffff0000u);
-    const float mid = fmaf(8.0f, s, z);
+// 4-bit rows: a word holds a lane's 8 codes. Code i stands 4 k_i bits up in the word or, from
+// code 5 on, in the word less its low 20 bits (k = 0 .. 4, 0, 1, 2), so under the exponent of 2^23
+// it is the float 2^23 + 16^k c, and one subtraction leaves 16^k (c - 8), exactly: a mask and half
+// a packed addition a code. The powers of 16 go into the other factor, or out of the sums at the
+// end. Pairs as the packed instructions take them.
+__device__ __forceinline__ float code_unit(int i) {
+    const int k = i < 5 ? i : i - 5;
+    return static_cast<float>(1 << (4 * k));
+}
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 of_pair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// 16^k (c - 8) of the codes of w, in pairs
+__device__ __forceinline__ void code_pairs(uint32_t w, uint64_t (&p)[4]) {
+    const uint32_t u = w >> 20;
+    float f[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        f[i] = fmaf(__uint_as_float(((w >> (4 * i)) & 15u) | 0x4b000000u) - 8388616.0f, s, mid);
+    for (int i = 0; i < 8; ++i) {
+        const int k = i < 5 ? i : i - 5;
+        f[i] = __uint_as_float(((i < 5 ? w : u) & (15u << (4 * k))) | 0x4b000000u);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t off = pair_of(-8388608.0f - 8.0f * code_unit(2 * i),
+                                     -8388608.0f - 8.0f * code_unit(2 * i + 1));
+        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p[i]) : "l"(pair_of(f[2 * i], f[2 * i + 1])), "l"(off));
+    }
+}
+// Step s and middle z + 8 s of a staged row's group, of its key (value = 0) or its value (1)
+__device__ __forceinline__ float2 step_and_middle(const uint8_t* row, int value, int hl) {
+    const uint32_t p = *reinterpret_cast<const uint32_t*>(row + 2 * MP_KV4_CODE_BYTES + 8 * value +
+                                                          4 * (hl >> 3));
+    const float s = __uint_as_float(p << 16);
+    return make_float2(s, fmaf(8.0f, s, __uint_as_float(p & 0xffff0000u)));
 }
 
 __device__ __forceinline__ unsigned atomic_add_acq_rel_gpu(unsigned* p, unsigned v) {
@@ -650,6 +683,19 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
     const uint8_t* Pg = KV == kKv4 ? reinterpret_cast<const uint8_t*>(a.params) +
                                          static_cast<size_t>(bg) * a.ncap * 2 * MP_KV4_PARAMS
                                    : nullptr;
+    // 4-bit rows: q over its codes' units, the lane's sum of q, value sums in units of 16^k, and the
+    // sum of weighted middles (all dims of a lane lie in one group)
+    uint64_t q2[4], o2[4];
+    float qsum = 0.0f, mid = 0.0f;
+    if constexpr (KV == kKv4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            q2[i] = pair_of(q8[2 * i] / code_unit(2 * i), q8[2 * i + 1] / code_unit(2 * i + 1));
+            o2[i] = 0ull;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) qsum += q8[i];
+    }
     const bool weighted = !exact && a.K > 0;
     const int hw = 2 * warp + half;
     constexpr int kHalves = 2 * kAWarps;
@@ -664,14 +710,33 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             const int r = j < cnt ? ent + j * kHalves : ent;
-            float kf[8];
-            load8(stage + r * kRowBytes, 0, hl, form, kf);
+            const uint8_t* slot = stage + r * kRowBytes;
             float d = 0.0f, k2 = 0.0f;
+            if constexpr (KV == kKv4) {
+                // sums of q (c - 8) in float, of c - 8 and its square in integers
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(slot + 4 * hl);
+                const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
+                const int sum = __dp4a(even, 0x01010101u, __dp4a(odd, 0x01010101u, 0u));
+                const int square = __dp4a(even, even, __dp4a(odd, odd, 0u));
+                const float c1 = static_cast<float>(sum - 64);
+                const float c2 = static_cast<float>(square - 16 * sum + 512);
+                const float2 sm = step_and_middle(slot, 0, hl);
+                uint64_t c[4], acc = 0ull;
+                code_pairs(w, c);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float x = kf[i] - mu8[i];
-                k2 = fmaf(x, x, k2);
-                d = fmaf(q8[i], kf[i], d);
+                for (int i = 0; i < 4; ++i) acc = fma_pair(c[i], q2[i], acc);
+                const float2 dd = of_pair(acc);
+                d = fmaf(sm.x, dd.x + dd.y, sm.y * qsum);
+                k2 = fmaf(sm.x * sm.x, c2, sm.y * fmaf(2.0f * sm.x, c1, 8.0f * sm.y));
+            } else {
+                float kf[8];
+                load8(slot, 0, hl, form, kf);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float x = kf[i] - mu8[i];
+                    k2 = fmaf(x, x, k2);
+                    d = fmaf(q8[i], kf[i], d);
+                }
             }
             pd[j] = d;
             pk[j] = k2;
@@ -726,17 +791,36 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
 #pragma unroll
         for (int sh = 8; sh; sh >>= 1) ws += __shfl_xor_sync(hmask, ws, sh);
         l = fmaf(l, corr, ws);
+        if constexpr (KV == kKv4) {
+            mid *= corr;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] *= corr;
+            for (int i = 0; i < 4; ++i) o2[i] = fma_pair(o2[i], pair_of(corr, corr), 0ull);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] *= corr;
+        }
         const int src0 = lane & 16;
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             const float wj = __shfl_sync(hmask, wgt, src0 + LPR * j);
             if (j < cnt) {
-                float vf[8];
-                load8(stage + (ent + j * kHalves) * kRowBytes, 1, hl, form, vf);
+                const uint8_t* slot = stage + (ent + j * kHalves) * kRowBytes;
+                if constexpr (KV == kKv4) {
+                    const uint32_t w =
+                        *reinterpret_cast<const uint32_t*>(slot + MP_KV4_CODE_BYTES + 4 * hl);
+                    const float2 sm = step_and_middle(slot, 1, hl);
+                    const uint64_t ws2 = pair_of(wj * sm.x, wj * sm.x);
+                    uint64_t c[4];
+                    code_pairs(w, c);
+                    mid = fmaf(wj, sm.y, mid);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = fmaf(wj, vf[i], o[i]);
+                    for (int i = 0; i < 4; ++i) o2[i] = fma_pair(c[i], ws2, o2[i]);
+                } else {
+                    float vf[8];
+                    load8(slot, 1, hl, form, vf);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i] = fmaf(wj, vf[i], o[i]);
+                }
             }
         }
         m = mn;
@@ -750,9 +834,14 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
     const int lo_hw = 2 * warp;                  // the warp's first half-warp has its most rows
     const int ngroups = nsel > lo_hw ? ((nsel - lo_hw + kHalves - 1) / kHalves + 3) / 4 : 0;
     const int my_rows = nsel > hw ? (nsel - hw + kHalves - 1) / kHalves : 0;
-    auto issue = [&](int k) {                    // one row (K then V) per instruction
+    auto issue = [&](int k) {                    // one row (K then V) per instruction, 4-bit: three
         if (k < ngroups) {
-            for (int jj = 0; jj < 8; ++jj) {
+            constexpr int kAtOnce = KV == kKv4 ? 3 : 1;
+            constexpr int kHalfPieces = kHalfBytes / 16;
+            for (int j0 = 0; j0 < 8; j0 += kAtOnce) {
+                const int jj = kAtOnce > 1 ? j0 + lane / kPieces : j0;
+                const int pc0 = kAtOnce > 1 ? lane % kPieces : lane;
+                if (kAtOnce > 1 && (jj >= min(8, j0 + kAtOnce))) continue;
                 const int e = lo_hw + (jj & 1) + kHalves * (4 * k + (jj >> 1));
                 if (e >= nsel) continue;
                 const int r = lo_hw + (jj & 1) + kHalves * (4 * (k & 1) + (jj >> 1));
@@ -760,8 +849,7 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
                 if (!mp_check(a.status, static_cast<long long>(key), min(a.n, a.ncap),
                               kSiteAttendRow))
                     continue;
-                for (int pc = lane; pc < kPieces; pc += 32) {
-                    constexpr int kHalfPieces = kHalfBytes / 16;
+                for (int pc = pc0; pc < kPieces; pc += 32) {
                     const uint8_t* src = (pc < kHalfPieces ? Kg : Vg) + key * kHalfBytes +
                                          16 * (pc % kHalfPieces);
                     if (KV == kKv4 && pc == 2 * kHalfPieces) src = Pg + key * 2 * MP_KV4_PARAMS;
@@ -782,6 +870,14 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
         issue(k + 2);
     }
     cp_async_wait_pending<0>();
+    if constexpr (KV == kKv4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = of_pair(o2[i]);
+            o[2 * i] = fmaf(v.x, 1.0f / code_unit(2 * i), mid);
+            o[2 * i + 1] = fmaf(v.y, 1.0f / code_unit(2 * i + 1), mid);
+        }
+    }
 
     // ---- merge the two half-warps, then the warps (fixed order)
     {
