@@ -586,17 +586,22 @@ def kv4_read(cache: KV4Cache, m: int, n_begin: int = 0, centre=None, positions=N
     new = []
     if keys is None:
         keys = torch.empty(shape, dtype=dtype if values is None else values.dtype,
-                           device=cache.k_codes.device)
+                           device=cache[0].device)
         new.append(keys)
+        kp, dt = keys.data_ptr(), _dtype(keys, "keys")
+    else:
+        kp, dt, _ = _rows_arg(keys, device, "keys", B, Hkv)
+        _arg(keys, device, "keys", keys.dtype, shape)
     if values is None:
-        values = torch.empty_like(keys)
+        values = torch.empty(shape, dtype=keys.dtype, device=cache[0].device)
         new.append(values)
-    kp, dt, _ = _rows_arg(keys, device, "keys", B, Hkv)
+        vp = values.data_ptr()
+    else:
+        vp = _arg(values, device, "values", keys.dtype, shape)
     status = lib().mp_kv4_read(
         ctypes.byref(c), _arg(centre, device, "centre", torch.float32, (B, Hkv, 128)), B, Hkv, m,
-        128, n_begin, _arg(positions, device, "positions", torch.int32, (B,)),
-        _arg(keys, device, "keys", keys.dtype, shape),
-        _arg(values, device, "values", keys.dtype, shape), dt, _kv4_stream(stream, device))
+        128, n_begin, _arg(positions, device, "positions", torch.int32, (B,)), kp, vp, dt,
+        _kv4_stream(stream, device))
     _check(status, "mp_kv4_read")
     _use(stream, *new)
     return keys, values

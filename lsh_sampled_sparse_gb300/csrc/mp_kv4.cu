@@ -109,17 +109,22 @@ __device__ __noinline__ uint32_t code_exact(float x, float z, float s) {
     return static_cast<uint32_t>(static_cast<int>(f));
 }
 
-// The 16 codes of x (a quarter of a group, pairs in order) as two words.
+// The codes of a lane's kPairs pairs x of a group, in order, as words of eight.
 // With t = x - z, the quotient t / s is rounded to an integer f by adding 1.5 2^23, and t - f s,
 // which one fused multiply-add gives exactly near s / 2, tells whether f is the nearest integer.
 // Values that are bf16 (kBf16) often lie half-way: 1 / s as two floats rounds their quotient
 // properly first, so that the addition sends a tie to the even integer, and |t - f s| > s / 2 alone
 // asks for 64 bits; t is exact then too, unless x is tiny and a border lies at x = 0. Other values
 // ask for 64 bits within 2^-18 of a border; steps near the ends of float32's range do always.
-template <bool kBf16>
-__device__ __forceinline__ uint2 codes16(const F2 (&x)[8], uint32_t pr) {
+template <bool kBf16, int kPairs>
+__device__ __forceinline__ void codes_of(const F2 (&x)[kPairs], uint32_t pr,
+                                         uint32_t (&w)[kPairs / 4]) {
     const float s = __uint_as_float(pr << 16), z = __uint_as_float(pr & 0xffff0000u);
-    if (!(s > 0.0f)) return make_uint2(0u, 0u);                  // constant, or not a number
+    if (!(s > 0.0f)) {                           // constant, or not a number
+#pragma unroll
+        for (int k = 0; k < kPairs / 4; ++k) w[k] = 0u;
+        return;
+    }
     const F2 round = pack2(12582912.0f, 12582912.0f), back = pack2(-12582912.0f, -12582912.0f);
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
@@ -127,9 +132,8 @@ __device__ __forceinline__ uint2 codes16(const F2 (&x)[8], uint32_t pr) {
     const F2 inv2 = pack2(inv, inv), low2 = pack2(low, low), minus_z = pack2(-z, -z),
              minus_s = pack2(-s, -s);
     float worst = 0.0f;
-    uint32_t w[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < kPairs / 4; ++k) {
         w[k] = 0u;
 #pragma unroll
         for (int i = 3; i >= 0; --i) {
@@ -150,21 +154,27 @@ __device__ __forceinline__ uint2 codes16(const F2 (&x)[8], uint32_t pr) {
         const float c = floorf(-z * inv);                        // is z + (c + 1/2) s = 0 ?
         if (c >= 0.0f && c < 15.0f && fmaf(c + 0.5f, s, z) == 0.0f) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < kPairs; ++i) {
                 const float2 v = unpack2(x[i]);
                 ask = ask || fabsf(v.x) < 1e-4f * s || fabsf(v.y) < 1e-4f * s;
             }
         }
     }
     if (ask) {
-        w[0] = w[1] = 0u;
+        const float near = 0.5f * s * (1.0f - 3.8e-6f);
+        const bool all = s < 1e-30f || s > 1e30f;
+        auto code = [&](float v) -> uint32_t {
+            const float y = __fadd_rn(__fmul_rn(v - z, inv), 12582912.0f);
+            if (all || !(fabsf(fmaf(12582912.0f - y, s, v - z)) < near)) return code_exact(v, z, s);
+            return __float_as_uint(y) & 15u;
+        };
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kPairs; ++i) {
             const float2 v = unpack2(x[i]);
-            w[i >> 2] |= (code_exact(v.x, z, s) | (code_exact(v.y, z, s) << 4)) << (8 * (i & 3));
+            const uint32_t pair = code(v.x) | (code(v.y) << 4);
+            w[i >> 2] = (i & 3) == 0 ? pair : w[i >> 2] | (pair << (8 * (i & 3)));
         }
     }
-    return make_uint2(w[0], w[1]);
 }
 
 struct RowArgs {
@@ -176,24 +186,31 @@ struct RowArgs {
     uint8_t* v_codes;
     uint8_t* params;
     uint32_t rows;                               // B * Hkv * m
-    uint32_t blocks;                             // of kRowsPerCta rows
+    uint32_t blocks;                             // of kRowThreads / (lanes a row) rows
     uint32_t m;
     int Hkv, n_begin, ncap;
 };
 
 constexpr int kRowThreads = 256;
-constexpr int kRowLanes = 8;                     // lanes a row: 16 dims each, four a group
-constexpr int kRowsPerCta = kRowThreads / kRowLanes;
+// Lanes a row of 128 dims: 8 with 16 dims each, or, to write many bf16 rows, 4 with 32 dims each:
+// what a lane does once for its dims (bounds, parameters, addresses) took more issue slots than
+// their codes (786432 rows: 111 us with 8 lanes, 96 us with 4). The longer code starts later: 256
+// rows take 2.9 us with 8 lanes, 4.1 us with 4.
+constexpr int kReadLanes = 8;
+constexpr uint32_t kManyRows = 2 * kSms * (kRowThreads / 4);     // two CTAs an SM of 4-lane rows
+int write_lanes(bool bf16, uint32_t rows) { return bf16 && rows >= kManyRows ? 4 : 8; }
 
-// Where a lane's row of block `blk` (kRowsPerCta rows) is: head and token in the call, row of the
+// Where a lane's row of block `blk` (kRowThreads / kLanes rows) is: head and token in the call, row of the
 // cache over all heads (-1: outside the cache, or past the call's rows). A block spans two heads at
 // most where a head has more rows than a block: one division, of uniform numbers, does then.
 struct RowAt {
     uint32_t r, bh;
     long long row;
 };
+template <int kLanes>
 __device__ __forceinline__ RowAt row_at(const RowArgs& a, uint32_t blk) {
-    const uint32_t r0 = blk * kRowsPerCta, r = r0 + threadIdx.x / kRowLanes;
+    constexpr uint32_t kRowsPerCta = kRowThreads / kLanes;
+    const uint32_t r0 = blk * kRowsPerCta, r = r0 + threadIdx.x / kLanes;
     RowAt w;
     w.r = min(r, a.rows - 1u);
     uint32_t i;
@@ -252,23 +269,25 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
 __device__ __forceinline__ F2 of_bf16x2(uint32_t w) {
     return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
-// The least and the largest of 16 dims (NaN if one is)
-__device__ __forceinline__ float2 bounds16(const F2 (&x)[8]) {
+// The least and the largest of a lane's dims (NaN if one is)
+template <int kPairs>
+__device__ __forceinline__ float2 bounds_of(const F2 (&x)[kPairs]) {
     const float2 v = unpack2(x[0]);
     float lo = min_nan(v.x, v.y), hi = max_nan(v.x, v.y);
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
+    for (int i = 1; i < kPairs; ++i) {
         const float2 u = unpack2(x[i]);
         lo = min_nan(lo, u.x, u.y);
         hi = max_nan(hi, u.x, u.y);
     }
     return make_float2(lo, hi);
 }
-// The same of 16 bf16 as they are in memory
-__device__ __forceinline__ float2 bounds16(const uint32_t (&w)[8]) {
+// The same of bf16 pairs as they are in memory
+template <int kPairs>
+__device__ __forceinline__ float2 bounds_of(const uint32_t (&w)[kPairs]) {
     uint32_t lo = w[0], hi = w[0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
+    for (int i = 1; i < kPairs; ++i) {
         asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(lo) : "r"(w[i]));
         asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(hi) : "r"(w[i]));
     }
@@ -276,76 +295,85 @@ __device__ __forceinline__ float2 bounds16(const uint32_t (&w)[8]) {
                        max_nan(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)));
 }
 
-// The parameters of a group from the bounds of its four lanes.
+// The parameters of a group from the bounds of its kLanes lanes.
+template <int kLanes>
 __device__ __forceinline__ uint32_t lanes_params(float2 v) {
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
+    for (int o = 1; o < kLanes; o <<= 1) {
         v.x = min_nan(v.x, __shfl_xor_sync(0xffffffffu, v.x, o));
         v.y = max_nan(v.y, __shfl_xor_sync(0xffffffffu, v.y, o));
     }
     return group_params(v.x, v.y);
 }
+template <int kWords>
+__device__ __forceinline__ void store_codes(uint8_t* p, const uint32_t (&w)[kWords]) {
+    if constexpr (kWords == 4)
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
 
-// Eight lanes a row, four rows a warp. A CTA takes every gridDim.x-th block of 32 rows and loads the
-// next block's keys and values before it codes the ones it has: with a block a CTA and no loop, a
-// third of the time went by between a warp's loads and its stores.
-template <typename T, bool kWide>
-__global__ void __launch_bounds__(kRowThreads) kv4_write_kernel(const RowArgs a) {
+// A CTA takes every gridDim.x-th block of rows and loads the next block's keys and values before it
+// codes the ones it has: with a block a CTA and no loop, a third of the time went by between a
+// warp's loads and its stores.
+template <typename T, bool kWide, int kLanes>
+__global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 && kLanes == 8 ? 3 : 2)
+    kv4_write_kernel(const RowArgs a) {
     constexpr bool kBf16 = sizeof(T) == 2;
-    constexpr int kWords = 16 * sizeof(T) / 4;   // of 16 dims
-    const int rl = threadIdx.x & (kRowLanes - 1);
+    constexpr int kDims = kD / kLanes, kPairs = kDims / 2;
+    constexpr int kWords = kDims * sizeof(T) / 4;
+    const int rl = threadIdx.x & (kLanes - 1);
     const F2 minus = pack2(-1.0f, -1.0f);
     uint32_t kw[kWords], vw[kWords];
     auto load = [&](uint32_t r) {
-        const size_t at = static_cast<size_t>(r) * kD + 16 * rl;
+        const size_t at = static_cast<size_t>(r) * kD + kDims * rl;
 #pragma unroll
         for (int j = 0; j < kWords / 8; ++j) {
-            load32<kWide>(static_cast<const T*>(a.keys) + at + 8 * j, kw + 8 * j);
-            load32<kWide>(static_cast<const T*>(a.values) + at + 8 * j, vw + 8 * j);
+            load32<kWide>(static_cast<const T*>(a.keys) + at + j * (32 / sizeof(T)), kw + 8 * j);
+            load32<kWide>(static_cast<const T*>(a.values) + at + j * (32 / sizeof(T)), vw + 8 * j);
         }
     };
-    RowAt w = row_at(a, blockIdx.x);
+    auto pairs_of = [](const uint32_t (&w)[kWords], F2 (&x)[kPairs]) {
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+            if constexpr (kBf16) x[j] = of_bf16x2(w[j]);
+            else x[j] = pack2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+        }
+    };
+    RowAt w = row_at<kLanes>(a, blockIdx.x);
     load(w.r);
     for (uint32_t blk = blockIdx.x; blk < a.blocks; blk += gridDim.x) {
-        F2 k[8], v[8];
+        F2 x[kPairs], v[kPairs];
+        pairs_of(kw, x);
+        pairs_of(vw, v);
         float2 vb;
-        if constexpr (kBf16) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                k[j] = of_bf16x2(kw[j]);
-                v[j] = of_bf16x2(vw[j]);
-            }
-            vb = bounds16(vw);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                k[j] = pack2(__uint_as_float(kw[2 * j]), __uint_as_float(kw[2 * j + 1]));
-                v[j] = pack2(__uint_as_float(vw[2 * j]), __uint_as_float(vw[2 * j + 1]));
-            }
-            vb = bounds16(v);
-        }
+        if constexpr (kBf16) vb = bounds_of(vw);
+        else vb = bounds_of(v);
         const RowAt now = w;
         if (blk + gridDim.x < a.blocks) {
-            w = row_at(a, blk + gridDim.x);
+            w = row_at<kLanes>(a, blk + gridDim.x);
             load(w.r);
         }
         if (a.centre) {
             const float4* mu = reinterpret_cast<const float4*>(
-                a.centre + static_cast<size_t>(now.bh) * kD + 16 * rl);
+                a.centre + static_cast<size_t>(now.bh) * kD + kDims * rl);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kPairs / 2; ++j) {
                 const float4 c = __ldg(mu + j);
-                k[2 * j] = fma2(pack2(c.x, c.y), minus, k[2 * j]);       // k - c, one rounding
-                k[2 * j + 1] = fma2(pack2(c.z, c.w), minus, k[2 * j + 1]);
+                x[2 * j] = fma2(pack2(c.x, c.y), minus, x[2 * j]);       // k - c, one rounding
+                x[2 * j + 1] = fma2(pack2(c.z, c.w), minus, x[2 * j + 1]);
             }
         }
-        const uint32_t kp = lanes_params(bounds16(k)), vp = lanes_params(vb);
-        const uint2 kc = codes16<false>(k, kp), vc = codes16<kBf16>(v, vp);
-        const uint32_t kp1 = __shfl_down_sync(0xffffffffu, kp, 4);
-        const uint32_t vp1 = __shfl_down_sync(0xffffffffu, vp, 4);
+        const uint32_t kp = lanes_params<kLanes / 2>(bounds_of(x));
+        const uint32_t vp = lanes_params<kLanes / 2>(vb);
+        uint32_t kc[kPairs / 4], vc[kPairs / 4];
+        codes_of<false>(x, kp, kc);
+        codes_of<kBf16>(v, vp, vc);
+        const uint32_t kp1 = __shfl_down_sync(0xffffffffu, kp, kLanes / 2);
+        const uint32_t vp1 = __shfl_down_sync(0xffffffffu, vp, kLanes / 2);
         if (now.row >= 0) {
-            *reinterpret_cast<uint2*>(a.k_codes + now.row * kCodeBytes + 8 * rl) = kc;
-            *reinterpret_cast<uint2*>(a.v_codes + now.row * kCodeBytes + 8 * rl) = vc;
+            store_codes(a.k_codes + now.row * kCodeBytes + kDims / 2 * rl, kc);
+            store_codes(a.v_codes + now.row * kCodeBytes + kDims / 2 * rl, vc);
             if (rl == 0)
                 *reinterpret_cast<uint4*>(a.params + now.row * 16) = make_uint4(kp, kp1, vp, vp1);
         }
@@ -385,7 +413,7 @@ __device__ __forceinline__ void values16(uint2 c, uint32_t pr, float (&x)[16]) {
 
 template <typename T, bool kWide>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const RowArgs a) {
-    const int rl = threadIdx.x & (kRowLanes - 1);
+    const int rl = threadIdx.x & (kReadLanes - 1);
     uint2 kc, vc;
     uint32_t kp, vp;
     auto load = [&](long long row) {
@@ -399,7 +427,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const RowArgs a) 
             vp = __ldg(p + 2);
         }
     };
-    RowAt w = row_at(a, blockIdx.x);
+    RowAt w = row_at<kReadLanes>(a, blockIdx.x);
     load(w.row);
     for (uint32_t blk = blockIdx.x; blk < a.blocks; blk += gridDim.x) {
         const RowAt now = w;
@@ -407,7 +435,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const RowArgs a) 
         values16(kc, kp, k);
         values16(vc, vp, v);
         if (blk + gridDim.x < a.blocks) {
-            w = row_at(a, blk + gridDim.x);
+            w = row_at<kReadLanes>(a, blk + gridDim.x);
             load(w.row);
         }
         if (a.centre && now.row >= 0) {
@@ -422,7 +450,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const RowArgs a) 
                 k[4 * i + 3] = __fadd_rn(k[4 * i + 3], c.w);
             }
         }
-        if (blk * kRowsPerCta + threadIdx.x / kRowLanes < a.rows) {
+        if (blk * (kRowThreads / kReadLanes) + threadIdx.x / kReadLanes < a.rows) {
             const size_t at = static_cast<size_t>(now.r) * kD + 16 * rl;
             store16<kWide>(static_cast<T*>(const_cast<void*>(a.keys)) + at, k);
             store16<kWide>(static_cast<T*>(const_cast<void*>(a.values)) + at, v);
@@ -1060,7 +1088,6 @@ RowArgs row_args(const mp_kv4& c, const float* centre, int B, int Hkv, int m, in
     a.v_codes = static_cast<uint8_t*>(c.v_codes);
     a.params = static_cast<uint8_t*>(c.params);
     a.rows = static_cast<uint32_t>(B) * Hkv * m;
-    a.blocks = (a.rows + kRowsPerCta - 1) / kRowsPerCta;
     a.Hkv = Hkv;
     a.m = m;
     a.n_begin = n_begin;
@@ -1068,19 +1095,24 @@ RowArgs row_args(const mp_kv4& c, const float* centre, int B, int Hkv, int m, in
     return a;
 }
 typedef void (*RowFn)(const RowArgs);
-RowFn pick_write(bool bf16, bool wide) {
-    if (bf16) return wide ? kv4_write_kernel<__nv_bfloat16, true> : kv4_write_kernel<__nv_bfloat16, false>;
-    return wide ? kv4_write_kernel<float, true> : kv4_write_kernel<float, false>;
+RowFn pick_write(bool bf16, bool wide, int lanes) {
+    using Bf16 = __nv_bfloat16;
+    if (!bf16) return wide ? kv4_write_kernel<float, true, 8> : kv4_write_kernel<float, false, 8>;
+    if (lanes == 8) return wide ? kv4_write_kernel<Bf16, true, 8> : kv4_write_kernel<Bf16, false, 8>;
+    return wide ? kv4_write_kernel<Bf16, true, 4> : kv4_write_kernel<Bf16, false, 4>;
 }
 RowFn pick_read(bool bf16, bool wide) {
-    if (bf16) return wide ? kv4_read_kernel<__nv_bfloat16, true> : kv4_read_kernel<__nv_bfloat16, false>;
+    using Bf16 = __nv_bfloat16;
+    if (bf16) return wide ? kv4_read_kernel<Bf16, true> : kv4_read_kernel<Bf16, false>;
     return wide ? kv4_read_kernel<float, true> : kv4_read_kernel<float, false>;
 }
 bool wide_rows(const void* keys, const void* values) {
     return ((reinterpret_cast<uintptr_t>(keys) | reinterpret_cast<uintptr_t>(values)) & 31u) == 0u;
 }
 // As many CTAs as the GPU holds at once, or as there are blocks
-unsigned row_ctas(const RowArgs& a, int per_sm) {
+unsigned row_ctas(RowArgs& a, int lanes, int per_sm) {
+    const uint32_t per_cta = kRowThreads / lanes;
+    a.blocks = (a.rows + per_cta - 1) / per_cta;
     return std::min<unsigned>(a.blocks, kSms * per_sm);
 }
 
@@ -1092,7 +1124,9 @@ cudaError_t launch_kv4_write(const void* keys, const void* values, bool bf16, co
     RowArgs a = row_args(cache, centre, B, Hkv, m, n_begin, positions);
     a.keys = keys;
     a.values = values;
-    pick_write(bf16, wide_rows(keys, values))<<<row_ctas(a, bf16 ? 3 : 2), kRowThreads, 0, st>>>(a);
+    const int lanes = write_lanes(bf16, a.rows);
+    const unsigned ctas = row_ctas(a, lanes, bf16 && lanes == 8 ? 3 : 2);
+    pick_write(bf16, wide_rows(keys, values), lanes)<<<ctas, kRowThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -1102,7 +1136,8 @@ cudaError_t launch_kv4_read(const mp_kv4& cache, const float* centre, int B, int
     RowArgs a = row_args(cache, centre, B, Hkv, m, n_begin, positions);
     a.keys = keys;
     a.values = values;
-    pick_read(bf16, wide_rows(keys, values))<<<row_ctas(a, 4), kRowThreads, 0, st>>>(a);
+    const unsigned ctas = row_ctas(a, kReadLanes, 4);
+    pick_read(bf16, wide_rows(keys, values))<<<ctas, kRowThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -1152,7 +1187,9 @@ cudaError_t prepare_kv4() {
     cudaFuncAttributes fa;
     cudaError_t e;
     for (int i = 0; i < 4; ++i) {
-        if ((e = cudaFuncGetAttributes(&fa, pick_write(i & 1, i & 2))) != cudaSuccess) return e;
+        for (int lanes : {4, 8})
+            if ((e = cudaFuncGetAttributes(&fa, pick_write(i & 1, i & 2, lanes))) != cudaSuccess)
+                return e;
         if ((e = cudaFuncGetAttributes(&fa, pick_read(i & 1, i & 2))) != cudaSuccess) return e;
     }
     void (*att[2])(const A4Args) = {kv4_attention_kernel<1>, kv4_attention_kernel<2>};

@@ -85,6 +85,42 @@ def test_write_is_the_definition_bit_for_bit(mp, dt, B, Hkv, m, cap, n0, centred
     _check_rows(cache, before, keys, values, centre, [n0] * B)
 
 
+def _at_16_bytes(t):
+    """The same tensor 16 bytes past a 32-byte boundary."""
+    n = 16 // t.element_size()
+    room = torch.empty(t.numel() + 2 * n, dtype=t.dtype, device=t.device)
+    assert room.data_ptr() % 32 == 0
+    u = room[n:n + t.numel()].view(t.shape)
+    u.copy_(t)
+    return u
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("m,shifted", [(31, True), (2003, False), (2003, True)])
+def test_many_rows_and_rows_aligned_to_16_bytes_only(mp, dt, m, shifted):
+    """20030 bf16 rows go through the kernel of four lanes a row; hard rows among them."""
+    B, Hkv, cap = 2, 5, m + 3
+    g = _gen(m)
+    keys = torch.randn(B, Hkv, m, 128, generator=g, device="cuda") * 2
+    values = torch.randn(B, Hkv, m, 128, generator=g, device="cuda")
+    hard = torch.from_numpy(_hard_rows()).cuda()[:m]
+    keys[1, 2, -hard.shape[0]:] = hard
+    values[1, 3, :hard.shape[0]] = hard
+    keys, values = keys.to(dt), values.to(dt)
+    centre = torch.randn(B, Hkv, 128, generator=g, device="cuda")
+    if shifted:
+        keys, values = _at_16_bytes(keys), _at_16_bytes(values)
+    cache = _filled(mp, B, Hkv, cap)
+    before = _clone(cache)
+    mp.kv4_write(cache, keys, values, n_begin=2, centre=centre)
+    _check_rows(cache, before, keys, values, centre, [2] * B)
+    k, v = mp.kv4_read(cache, m, n_begin=2, centre=centre, dtype=dt)
+    if shifted:
+        out = _at_16_bytes(torch.zeros_like(k)), _at_16_bytes(torch.zeros_like(v))
+        mp.kv4_read(cache, m, n_begin=2, centre=centre, keys=out[0], values=out[1])
+        assert _same(out[0], k) and _same(out[1], v)
+
+
 def _hard_rows():
     """Rows whose groups sit where the format can go wrong."""
     rng = np.random.default_rng(11)
@@ -235,6 +271,29 @@ def test_attention_with_sharp_scores_and_a_scale_of_its_own(mp, qt):
     for f in (2.0 ** 60, 2.0 ** -60):
         _attend_and_check(mp, (q.float() * f).to(qt), cache, 1500, scale=0.1 / f)
     _attend_and_check(mp, torch.zeros_like(q), cache, 1500)
+
+
+@pytest.mark.parametrize("qt", [BF, F32])
+def test_attention_of_queries_aligned_to_their_element_only(mp, qt):
+    cache = _random_cache(mp, 2, 3, 700, 700, seed=77)
+    for G in (2, 7):
+        q = torch.randn(2, 3 * G, 128, generator=_gen(G), device="cuda").to(qt)
+        room = torch.empty(q.numel() + 1, dtype=qt, device="cuda")
+        shifted = room[1:].view(q.shape)
+        shifted.copy_(q)
+        assert torch.equal(mp.kv4_attention(shifted, cache), _attend_and_check(mp, q, cache, 700))
+
+
+def test_attention_layouts_of_one_two_and_three_ctas_an_sm(mp):
+    """Shapes that the plan lays out with one split, as many as fill one or two CTAs an SM, and in
+    several waves, long sequences among them."""
+    for B, Hkv, G, n in ((1, 8, 4, 16384), (2, 8, 4, 30000), (40, 8, 1, 1100), (9, 8, 8, 2500),
+                         (1, 1, 2, 70001), (150, 4, 3, 300), (1, 2, 24, 5000)):
+        cache = _random_cache(mp, B, Hkv, n, n, seed=n)
+        q = torch.randn(B, Hkv * G, 128, generator=_gen(n), device="cuda")
+        _attend_and_check(mp, q, cache, n)
+        lengths = torch.randint(0, n + 1, (B,), generator=_gen(B), device="cuda").int()
+        _attend_and_check(mp, q, cache, n, lengths)
 
 
 def test_attention_over_values_of_very_different_sizes(mp):
