@@ -487,7 +487,7 @@ struct A4Args {
     const int32_t* lengths;
     float* part;                                 // [row][split][kPart]: o, m, l
     float* out;
-    int q_bf16, q_wide, Hq, Hkv, G, n, ncap, splits, chunks;
+    int q_bf16, q_wide, Hq, Hkv, G, n, ncap, splits, chunks, cluster;
     int tiles_per_split;
     float scale;                                 // of q.k, times log2 e
 };
@@ -501,9 +501,10 @@ constexpr int kStageK = 0, kStageV = kTile * kCodeBytes, kStageP = 2 * kTile * k
 constexpr int kStageBytes = kStageP + kTile * kParamBytes;
 constexpr int kAttStages = 2;
 constexpr int kAttSmem = kAttWarps * kAttStages * kStageBytes;
+constexpr int kClusterSplits = 8;                // up to so many splits are joined within a cluster
 constexpr int kMergePitch = kD + 4;              // floats a (warp, head) leaves for the CTA's merge
 static_assert(kAttThreads == kD, "the merge: a thread per dim");
-static_assert(kAttWarps * 8 * kMergePitch * 4 <= kAttSmem, "the merge reuses the stages");
+static_assert((kAttWarps + 1) * 8 * kMergePitch * 4 <= kAttSmem, "the merge reuses the stages");
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -553,6 +554,22 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // The largest of a warp's unsigned numbers
 __device__ __forceinline__ uint32_t warp_max(uint32_t x) {
     return __reduce_max_sync(0xffffffffu, x);
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+                 ::: "memory");
+}
+// The address of this CTA's shared memory in CTA `rank` of the cluster, and a float from there
+__device__ __forceinline__ uint32_t peer_address(uint32_t addr, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float load_peer(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 // Eight codes of a word as four fp16 pairs: with c0 .. c3 the codes of its low half and c4 .. c7 of
@@ -620,9 +637,9 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane >> 2, t = lane & 3;
     allow_dependents();
-    const unsigned ch = blockIdx.x % a.chunks, rest = blockIdx.x / a.chunks;
-    const int split = static_cast<int>(rest % a.splits);
-    const size_t bh = rest / a.splits;
+    const int split = static_cast<int>(blockIdx.x % a.splits);
+    const unsigned ch = blockIdx.x / a.splits % a.chunks;
+    const size_t bh = blockIdx.x / a.splits / a.chunks;
     const int b = static_cast<int>(bh / a.Hkv);
     const int h0 = static_cast<int>(ch) * 4 * NT;                        // first head of the chunk
     const size_t row0 = static_cast<size_t>(b) * a.Hq + (bh - static_cast<size_t>(b) * a.Hkv) * a.G +
@@ -944,6 +961,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
     }
     __syncthreads();
     const int e = threadIdx.x;
+    float* share = join + 4 * NT * kAttWarps * kMergePitch;              // [head][kMergePitch]
     for (int h = 0; h < heads; ++h) {
         const float* src = join + h * kAttWarps * kMergePitch;
         float M = -INFINITY, L = 0.0f, O = 0.0f;
@@ -958,6 +976,13 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
         }
         if (a.splits == 1) {
             a.out[(row0 + h) * kD + e] = L == 0.0f ? 0.0f : O / L;
+        } else if (a.cluster) {
+            float* p = share + h * kMergePitch;
+            p[e] = O;
+            if (e == 0) {
+                p[kD] = M;
+                p[kD + 1] = L;
+            }
         } else {
             float* p = a.part + ((row0 + h) * a.splits + split) * kPart;
             p[e] = O;
@@ -966,6 +991,40 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
                 p[kD + 1] = L;
             }
         }
+    }
+    // few splits are one cluster: each CTA joins some of the heads from the CTAs' shared memory
+    // (against the second kernel: 4 x 8 heads of 16K tokens 18.8 -> 18.4 us, 16 sequences of up to
+    // 5000 22.5 -> 21.0 us, and a launch less; not over several waves, where the CTAs of a cluster
+    // would hold their places until the longest is done: 155 us against 176 us for 32 sequences of
+    // 16K to 32K tokens)
+    if (a.cluster) {
+        cluster_barrier();
+        for (int h = split; h < heads; h += a.splits) {
+            const uint32_t at = smem_u32(share + h * kMergePitch);
+            float ms[kClusterSplits], ls[kClusterSplits], os[kClusterSplits], M = -INFINITY;
+#pragma unroll
+            for (int s = 0; s < kClusterSplits; ++s) {
+                ms[s] = -INFINITY;
+                ls[s] = os[s] = 0.0f;
+                if (s < a.splits) {
+                    const uint32_t there = peer_address(at, s);
+                    ms[s] = load_peer(there + 4 * kD);
+                    ls[s] = load_peer(there + 4 * (kD + 1));
+                    os[s] = load_peer(there + 4 * e);
+                }
+                M = fmaxf(M, ms[s]);
+            }
+            const float base = M == -INFINITY ? 0.0f : M;
+            float L = 0.0f, O = 0.0f;
+#pragma unroll
+            for (int s = 0; s < kClusterSplits; ++s) {
+                const float c = exp2_fast(ms[s] - base);
+                L = fmaf(c, ls[s], L);
+                O = fmaf(c, os[s], O);
+            }
+            a.out[(row0 + h) * kD + e] = L == 0.0f ? 0.0f : O / L;
+        }
+        cluster_barrier();                       // no CTA leaves while another reads from it
     }
 }
 
@@ -1038,6 +1097,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_kernel(const A4Arg
 // How an attention call is laid over the GPU.
 struct AttPlan {
     int nt, chunks, splits, tiles_per_split;
+    bool cluster;                                // the splits of a unit are one cluster
 };
 // How many splits: the least of a model of a call's time, in units of 10 ns, over the counts that
 // fill one, two or three CTAs an SM, and three in two or three waves. Measured with NT = 1 (one to
@@ -1068,12 +1128,15 @@ AttPlan attention_plan(int B, int Hq, int Hkv, int n, bool ragged) {
         const int at_once = static_cast<int>(std::min<long long>(busy, resident));
         double steps_there = static_cast<double>((busy + at_once - 1) / at_once * at_once) * each;
         if (ragged && busy > resident) steps_there = 0.75 * steps_there + 0.25 * resident * each;
-        const double fixed = used == 1 ? 400.0 : at_once == 1 ? 530.0 : at_once == 2 ? 620.0 : 870.0;
+        const bool clustered = used > 1 && used <= kClusterSplits && busy <= resident;
+        const double fixed = (used == 1 ? 400.0 : at_once == 1 ? 530.0 : at_once == 2 ? 620.0 : 870.0) -
+                             (clustered ? 40.0 : 0.0);
         const double cost = fixed + std::max(memory, steps_there * step_cost[p.nt - 1][at_once - 1]);
         if (best < 0.0 || cost < best) {
             best = cost;
             p.splits = used;
             p.tiles_per_split = each * kAttWarps;
+            p.cluster = clustered;
         }
     }
     return p;
@@ -1143,9 +1206,12 @@ cudaError_t launch_kv4_read(const mp_kv4& cache, const float* centre, int B, int
 
 size_t kv4_attention_scratch_bytes(int B, int Hq, int Hkv, int n) {
     // enough for either layout: the caller of a size does not say whether lengths will differ
-    const int splits = std::max(attention_plan(B, Hq, Hkv, n, false).splits,
-                                attention_plan(B, Hq, Hkv, n, true).splits);
-    return splits == 1 ? 0 : static_cast<size_t>(B) * Hq * splits * kPart * sizeof(float);
+    int splits = 0;
+    for (bool ragged : {false, true}) {
+        const AttPlan p = attention_plan(B, Hq, Hkv, n, ragged);
+        if (p.splits > 1 && !p.cluster) splits = std::max(splits, p.splits);
+    }
+    return static_cast<size_t>(B) * Hq * splits * kPart * sizeof(float);
 }
 
 cudaError_t launch_kv4_attention(const void* q, bool q_bf16, const mp_kv4& cache, int B, int Hq,
@@ -1168,17 +1234,26 @@ cudaError_t launch_kv4_attention(const void* q, bool q_bf16, const mp_kv4& cache
     a.n = n;
     a.ncap = cache.n_capacity;
     a.splits = p.splits;
+    a.cluster = p.cluster;
     a.chunks = p.chunks;
     a.tiles_per_split = p.tiles_per_split;
     a.scale = scale * 1.4426950408889634f;
     const long long ctas = static_cast<long long>(B) * Hkv * p.splits * p.chunks;
     if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
-    if (p.nt == 1)
-        kv4_attention_kernel<1><<<static_cast<unsigned>(ctas), kAttThreads, kAttSmem, st>>>(a);
-    else
-        kv4_attention_kernel<2><<<static_cast<unsigned>(ctas), kAttThreads, kAttSmem, st>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.splits == 1) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kAttThreads);
+    cfg.dynamicSmemBytes = kAttSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(
+        &cfg, p.nt == 1 ? kv4_attention_kernel<1> : kv4_attention_kernel<2>, a);
+    if (e != cudaSuccess || p.splits == 1 || p.cluster) return e;
     return launch_dependent(kv4_merge_kernel, dim3(static_cast<unsigned>(B) * Hq),
                             dim3(32 * kMergeWarps), 0, st, a);
 }
