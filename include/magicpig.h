@@ -499,8 +499,8 @@ MP_API mp_status mp_decode_attention_noalloc(const void* q, mp_dtype q_dtype,
 MP_API mp_status mp_device_status(int* status);
 
 /* The MP_CHECKS build (the library compiled with -DMP_CHECKS=1, libmagicpig_checks.so): every
- * kernel of the decode path, the bucketed lookup and the tensor-core encoder check the indices of
- * their global accesses (code blocks, selection words, K/V rows, partial states, bucket ranges
+ * kernel of the decode path, the bucketed lookup, the tensor-core encoder and the 4-bit cache check
+ * the indices of their global accesses (code blocks, selection words, K/V rows, partial states, bucket ranges
  * and members, code words written) and skip an access that is out of range instead of making
  * it, raising MP_ERR_BOUNDS in the status word. A stand-in for a memory checker: the paper has
  * no counterpart. Synchronises the device and returns through *enabled 1 in that build, 0 in the
@@ -508,7 +508,8 @@ MP_API mp_status mp_device_status(int* status);
  * last reset (0 if none): 1 query encoding stores, 2 scanned code block, 3 selection words
  * written, 4 K/V row copied, 5 partial state or output written, 6 selection words read,
  * 7 bucket range beyond the table's keys, 8 bucket member beyond n_indexed, 9 code words written
- * by the encoder. Neither word is reset. Errors: MP_ERR_INVALID_ARG (null), MP_ERR_CUDA. */
+ * by the encoder, 10 a row of the 4-bit cache, 11 rows read back from it, partial states and output
+ * rows of its attention. Neither word is reset. Errors: MP_ERR_INVALID_ARG (null), MP_ERR_CUDA. */
 MP_API mp_status mp_debug_check_report(int* enabled, int* site);
 
 #ifdef __cplusplus

@@ -497,21 +497,30 @@ def _arg(t, device: int, name: str, dtype, shape):
     """The address of t (None: no tensor), checked: on this device, dtype, shape, contiguous."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.get_device() != device:
-        _not_there(t, device, name)
+    try:
+        if t.get_device() == device and t.dtype is dtype and t.shape == shape \
+                and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, device, name, dtype, shape)
+
+
+def _refuse(t, device, name, dtype, shape):
+    """Raise what _arg found."""
+    _on_device(t, device, name)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, is {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _not_there(t, device, name):
+def _on_device(t, device, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    raise ValueError(f"{name} is on {t.device}, the cache on cuda:{device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{device}")
 
 
 def _kv4(cache):
@@ -539,8 +548,7 @@ def _kv4_stream(stream, device):
 
 def _rows_arg(t, device, name, B, Hkv):
     """(address, dtype code, m) of keys or values [B, Hkv, m, 128]."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != device:
-        _not_there(t, device, name)
+    _on_device(t, device, name)
     shape = t.shape
     if len(shape) != 4 or shape[0] != B or shape[1] != Hkv:
         raise ValueError(f"{name} must be [{B}, {Hkv}, m, 128], got {tuple(shape)}")
@@ -549,11 +557,13 @@ def _rows_arg(t, device, name, B, Hkv):
     return t.data_ptr(), _dtype(t, name), shape[2]
 
 
-def _use(stream, *tensors):
-    """Tensors allocated here stay allocated until the other stream that uses them is done."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
+def _empty(shape, dtype, device, stream):
+    """A new tensor in the memory of the stream that the call runs on: what that memory held before
+    is ordered with the call, and so is what it will hold once the tensor is gone."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def kv4_write(cache: KV4Cache, keys, values, n_begin: int = 0, centre=None, positions=None,
@@ -565,12 +575,15 @@ def kv4_write(cache: KV4Cache, keys, values, n_begin: int = 0, centre=None, posi
     c, device, B, Hkv, _ = _kv4(cache)
     kp, dt, m = _rows_arg(keys, device, "keys", B, Hkv)
     d = keys.shape[3]
+    if n_begin >> 31 not in (0, -1):             # what a C int would cut off
+        raise ValueError(f"n_begin = {n_begin}")
     status = lib().mp_kv4_write(
         kp, _arg(values, device, "values", keys.dtype, keys.shape), dt,
         _arg(centre, device, "centre", torch.float32, (B, Hkv, d)), B, Hkv, m, d, n_begin,
         _arg(positions, device, "positions", torch.int32, (B,)), ctypes.byref(c),
         _kv4_stream(stream, device))
-    _check(status, "mp_kv4_write")
+    if status:
+        _check(status, "mp_kv4_write")
     return cache
 
 
@@ -580,21 +593,17 @@ def kv4_read(cache: KV4Cache, m: int, n_begin: int = 0, centre=None, positions=N
     values [B, Hkv, m, 128] in dtype, with centre added to the keys; rows outside the capacity
     read as zero."""
     c, device, B, Hkv, _ = _kv4(cache)
-    if m < 0:
-        raise ValueError(f"m = {m} tokens")
+    if m < 0 or m >> 31 or n_begin >> 31 not in (0, -1):
+        raise ValueError(f"m = {m} tokens from n_begin = {n_begin}")
     shape = (B, Hkv, m, 128)
-    new = []
     if keys is None:
-        keys = torch.empty(shape, dtype=dtype if values is None else values.dtype,
-                           device=cache[0].device)
-        new.append(keys)
+        keys = _empty(shape, dtype if values is None else values.dtype, cache[0].device, stream)
         kp, dt = keys.data_ptr(), _dtype(keys, "keys")
     else:
         kp, dt, _ = _rows_arg(keys, device, "keys", B, Hkv)
         _arg(keys, device, "keys", keys.dtype, shape)
     if values is None:
-        values = torch.empty(shape, dtype=keys.dtype, device=cache[0].device)
-        new.append(values)
+        values = _empty(shape, keys.dtype, cache[0].device, stream)
         vp = values.data_ptr()
     else:
         vp = _arg(values, device, "values", keys.dtype, shape)
@@ -602,8 +611,8 @@ def kv4_read(cache: KV4Cache, m: int, n_begin: int = 0, centre=None, positions=N
         ctypes.byref(c), _arg(centre, device, "centre", torch.float32, (B, Hkv, 128)), B, Hkv, m,
         128, n_begin, _arg(positions, device, "positions", torch.int32, (B,)), kp, vp, dt,
         _kv4_stream(stream, device))
-    _check(status, "mp_kv4_read")
-    _use(stream, *new)
+    if status:
+        _check(status, "mp_kv4_read")
     return keys, values
 
 
@@ -611,12 +620,11 @@ def kv4_attention_workspace_bytes(B: int, Hq: int, Hkv: int, n: int, d: int = 12
     return int(lib().mp_kv4_attention_workspace_bytes(B, Hq, Hkv, n, d))
 
 
-def _kv4_call(q, cache, n, out, workspace, need):
+def _kv4_call(q, cache, n, out, workspace, need, stream):
     """What the calls on queries share: checks of q, out and the workspace, which are allocated
-    where they are None (need: its size from B, Hq, Hkv, n, d, n_capacity)."""
+    where they are None (need: its size from B, Hq, Hkv, n, d)."""
     c, device, B, Hkv, cap = _kv4(cache)
-    if not isinstance(q, torch.Tensor) or q.get_device() != device:
-        _not_there(q, device, "q")
+    _on_device(q, device, "q")
     shape = q.shape
     if len(shape) != 3 or shape[0] != B:
         raise ValueError(f"q must be [{B}, Hq, 128], got {tuple(shape)}")
@@ -626,19 +634,16 @@ def _kv4_call(q, cache, n, out, workspace, need):
     if not 1 <= n <= cap:
         raise ValueError(f"n = {n} outside [1, {cap}] (the cache's capacity)")
     qt = _dtype(q, "q")
-    new = []
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=q.device)
-        new.append(out)
+        out = _empty(shape, torch.float32, q.device, stream)
     op = _arg(out, device, "out", torch.float32, shape)
     if workspace is None:
-        workspace = torch.empty(max(need(B, shape[1], Hkv, n, shape[2], cap), 256),
-                                dtype=torch.uint8, device=q.device)
-        new.append(workspace)
+        workspace = _empty((max(need(B, shape[1], Hkv, n, shape[2]), 256),), torch.uint8, q.device,
+                           stream)
     elif workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous and on the cache's device")
-    return (c, device, (B, shape[1], Hkv, n, shape[2]), cap, q.data_ptr(), qt, out, op,
-            workspace.data_ptr(), _nbytes(workspace), new)
+    return (c, device, (B, shape[1], Hkv, n, shape[2]), q.data_ptr(), qt, out, op,
+            workspace, workspace.data_ptr(), _nbytes(workspace))
 
 
 def kv4_attention(q, cache: KV4Cache, n=None, lengths=None, scale: float = 0.0, out=None,
@@ -646,31 +651,30 @@ def kv4_attention(q, cache: KV4Cache, n=None, lengths=None, scale: float = 0.0, 
     """Exact attention of one query token per sequence, q [B, Hq, 128], over the first n tokens
     (default: the capacity) of a 4-bit cache, or the first lengths[b] (int32 [B], on the GPU, at
     most n) of sequence b; returns out [B, Hq, 128] float32, zero for a sequence of length 0."""
-    c, device, dims, _, qp, qt, out, op, wp, size, new = _kv4_call(
-        q, cache, n, out, workspace,
-        lambda B, Hq, Hkv, n, d, cap: kv4_attention_workspace_bytes(B, Hq, Hkv, n, d))
+    c, device, dims, qp, qt, out, op, workspace, wp, size = _kv4_call(
+        q, cache, n, out, workspace, kv4_attention_workspace_bytes, stream)
     status = lib().mp_kv4_attention(
         qp, qt, ctypes.byref(c), *dims, _arg(lengths, device, "lengths", torch.int32, dims[:1]),
         scale, op, wp, size, _kv4_stream(stream, device))
-    _check(status, "mp_kv4_attention")
-    _use(stream, *new)
+    if status:
+        _check(status, "mp_kv4_attention")
     return out
 
 
 def _kv4_sampled(q, codes, centre, cache, K, L, n_sink, n_local, scale, out, workspace, n, radius,
-                 logu_table, n_indexed=0, scanned=True):
+                 logu_table, stream, n_indexed=0, scanned=True):
     """_kv4_call for a sampled decode, with its parameters, and its codes (laid out for the
     cache's capacity; not needed where nothing is scanned) and centre checked."""
     cap = cache.k_codes.shape[2]
     p = _params(K, L, n_sink, n_local, scale, cap, n_indexed, radius=radius, logu_table=logu_table)
 
-    def need(B, Hq, Hkv, n, d, cap):
+    def need(B, Hq, Hkv, n, d):
         size = int(lib().mp_decode_workspace_bytes(B, Hq, Hkv, n, d, ctypes.byref(p)))
         if size == 0:
             raise MagicPIGError("mp_decode_workspace_bytes rejected the shapes/parameters")
         return size
 
-    call = _kv4_call(q, cache, n, out, workspace, need)
+    call = _kv4_call(q, cache, n, out, workspace, need, stream)
     device, (B, _, Hkv, _, d) = call[1], call[2]
     size = cp_codes_bytes(B, Hkv, cap, L) if logu_table is not None \
         else codes_bytes(B, Hkv, cap, K, L)
@@ -678,9 +682,12 @@ def _kv4_sampled(q, codes, centre, cache, K, L, n_sink, n_local, scale, out, wor
         _cuda(codes, "codes")
     if size and scanned and (codes is None or _nbytes(codes) < size):
         raise ValueError(f"codes must hold {size} bytes, for {cap} tokens per head")
-    for t in (codes, radius, logu_table):
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"a tensor is on {t.device}, the cache on cuda:{device}")
+    for t, name, most in ((codes, "codes", 0), (radius, "radius", B * Hkv),
+                          (logu_table, "logu_table", MP_LOGU_TABLE_ENTRIES)):
+        if t is not None:
+            _on_device(t, device, name)
+            if t.numel() < most:
+                raise ValueError(f"{name} has {t.numel()} elements, needs {most}")
     cp = _arg(centre, device, "centre", torch.float32, (B, Hkv, d))
     return call, p, None if codes is None else codes.data_ptr(), cp
 
@@ -690,18 +697,18 @@ def kv4_decode_attention(q, codes, centre, W, cache: KV4Cache, K: int, L: int, n
                          n=None, radius=None, logu_table=None):
     """decode_attention over the first n tokens of a 4-bit cache (written with this centre)."""
     call, p, codes_p, centre_p = _kv4_sampled(q, codes, centre, cache, K, L, n_sink, n_local,
-                                              scale, out, workspace, n, radius, logu_table)
-    c, device, dims, _, qp, qt, out, op, wp, size, new = call
+                                              scale, out, workspace, n, radius, logu_table,
+                                              stream)
+    c, device, dims, qp, qt, out, op, workspace, wp, size = call
     _cuda(W, "W")
-    if W.get_device() != device:
-        _not_there(W, device, "W")
+    _on_device(W, device, "W")
     if W.numel() < dims[4] * (dims[4] if logu_table is not None else K) * L:
         raise ValueError(f"W of shape {tuple(W.shape)} has too few hyperplanes")
     status = lib().mp_kv4_decode_attention(
         qp, qt, codes_p, centre_p, W.data_ptr(), _dtype(W, "W"), ctypes.byref(c), *dims,
         ctypes.byref(p), op, wp, size, _kv4_stream(stream, device))
-    _check(status, "mp_kv4_decode_attention")
-    _use(stream, *new)
+    if status:
+        _check(status, "mp_kv4_decode_attention")
     return out
 
 
@@ -712,13 +719,13 @@ def kv4_sampled_attention(q, codes, centre, cache: KV4Cache, K: int, L: int, n_s
     [B, Hkv, n_capacity, 128])."""
     call, p, codes_p, centre_p = _kv4_sampled(q, codes, centre, cache, K, L, n_sink, n_local,
                                               scale, out, _cuda(workspace, "workspace"), n, radius,
-                                              logu_table)
-    c, device, dims, _, qp, qt, out, op, wp, size, new = call
+                                              logu_table, stream)
+    c, device, dims, qp, qt, out, op, workspace, wp, size = call
     status = lib().mp_kv4_sampled_attention(
         qp, qt, codes_p, centre_p, ctypes.byref(c), *dims, ctypes.byref(p), op, wp, size,
         _kv4_stream(stream, device))
-    _check(status, "mp_kv4_sampled_attention")
-    _use(stream, *new)
+    if status:
+        _check(status, "mp_kv4_sampled_attention")
     return out
 
 
@@ -728,8 +735,8 @@ def kv4_sampled_attention_buckets(q, buckets, centre, cache: KV4Cache, K: int, L
     """sampled_attention_buckets over a 4-bit cache (written with this centre)."""
     call, p, codes_p, centre_p = _kv4_sampled(
         q, codes, centre, cache, K, L, n_sink, n_local, scale, out, _cuda(workspace, "workspace"),
-        n, radius, None, 0 if n_indexed is None else int(n_indexed), codes is not None)
-    c, device, dims, _, qp, qt, out, op, wp, size, new = call
+        n, radius, None, stream, 0 if n_indexed is None else int(n_indexed), codes is not None)
+    c, device, dims, qp, qt, out, op, workspace, wp, size = call
     _cuda(buckets, "buckets")
     indexed = dims[3] if not n_indexed else int(n_indexed)
     if buckets.get_device() != device \
@@ -738,8 +745,8 @@ def kv4_sampled_attention_buckets(q, buckets, centre, cache: KV4Cache, K: int, L
     status = lib().mp_kv4_sampled_attention_buckets(
         qp, qt, buckets.data_ptr(), codes_p, centre_p, ctypes.byref(c), *dims, ctypes.byref(p), op,
         wp, size, _kv4_stream(stream, device))
-    _check(status, "mp_kv4_sampled_attention_buckets")
-    _use(stream, *new)
+    if status:
+        _check(status, "mp_kv4_sampled_attention_buckets")
     return out
 
 

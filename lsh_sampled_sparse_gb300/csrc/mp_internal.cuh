@@ -41,6 +41,8 @@ enum CheckSite : int {
     kSiteBucketRange = 7,        // a bucket's [offset, next offset) outside the table's n keys
     kSiteBucketKey = 8,          // a bucket member outside [0, n)
     kSiteEncodeCodes = 9,        // the code words an encoder CTA writes
+    kSiteKv4Row = 10,            // a row of the 4-bit cache written, read or copied
+    kSiteKv4Out = 11,            // rows read back, partial states or output rows of its attention
 };
 
 // Index check of the MP_CHECKS build (the memory checker's stand-in): there an index outside

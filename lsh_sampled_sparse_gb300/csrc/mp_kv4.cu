@@ -189,6 +189,7 @@ struct RowArgs {
     uint32_t blocks;                             // of kRowThreads / (lanes a row) rows
     uint32_t m;
     int Hkv, n_begin, ncap;
+    int* status;                                 // index checks of the MP_CHECKS build
 };
 
 constexpr int kRowThreads = 256;
@@ -371,7 +372,8 @@ __global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 && kLanes == 8 ? 3
         codes_of<kBf16>(v, vp, vc);
         const uint32_t kp1 = __shfl_down_sync(0xffffffffu, kp, kLanes / 2);
         const uint32_t vp1 = __shfl_down_sync(0xffffffffu, vp, kLanes / 2);
-        if (now.row >= 0) {
+        if (now.row >= 0 &&
+            mp_check(a.status, now.row, static_cast<long long>(a.rows / a.m) * a.ncap, kSiteKv4Row)) {
             store_codes(a.k_codes + now.row * kCodeBytes + kDims / 2 * rl, kc);
             store_codes(a.v_codes + now.row * kCodeBytes + kDims / 2 * rl, vc);
             if (rl == 0)
@@ -419,7 +421,8 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const RowArgs a) 
     auto load = [&](long long row) {
         kc = vc = make_uint2(0u, 0u);
         kp = vp = 0u;
-        if (row >= 0) {
+        if (row >= 0 &&
+            mp_check(a.status, row, static_cast<long long>(a.rows / a.m) * a.ncap, kSiteKv4Row)) {
             kc = __ldg(reinterpret_cast<const uint2*>(a.k_codes + row * kCodeBytes + 8 * rl));
             vc = __ldg(reinterpret_cast<const uint2*>(a.v_codes + row * kCodeBytes + 8 * rl));
             const uint32_t* p = reinterpret_cast<const uint32_t*>(a.params + row * 16) + (rl >> 2);
@@ -450,7 +453,8 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const RowArgs a) 
                 k[4 * i + 3] = __fadd_rn(k[4 * i + 3], c.w);
             }
         }
-        if (blk * (kRowThreads / kReadLanes) + threadIdx.x / kReadLanes < a.rows) {
+        if (blk * (kRowThreads / kReadLanes) + threadIdx.x / kReadLanes < a.rows &&
+            mp_check(a.status, now.r, a.rows, kSiteKv4Out)) {
             const size_t at = static_cast<size_t>(now.r) * kD + 16 * rl;
             store16<kWide>(static_cast<T*>(const_cast<void*>(a.keys)) + at, k);
             store16<kWide>(static_cast<T*>(const_cast<void*>(a.values)) + at, v);
@@ -490,6 +494,8 @@ struct A4Args {
     int q_bf16, q_wide, Hq, Hkv, G, n, ncap, splits, chunks, cluster;
     int tiles_per_split;
     float scale;                                 // of q.k, times log2 e
+    long long rows;                              // B * Hq
+    int* status;                                 // index checks of the MP_CHECKS build
 };
 constexpr int kPart = kD + 4;
 constexpr int kAttWarps = 4;
@@ -647,8 +653,9 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
     const int heads = min(4 * NT, a.G - h0);
     const int len = a.lengths ? max(0, min(a.n, __ldg(a.lengths + b))) : a.n;
     const int tile0 = split * a.tiles_per_split;
-    const int end = static_cast<int>(min(static_cast<long long>(len),    // tokens [.., end)
-                                         (tile0 + a.tiles_per_split) * static_cast<long long>(kTile)));
+    const long long split_end = static_cast<long long>(tile0 + a.tiles_per_split) * kTile;
+    int end = static_cast<int>(min(static_cast<long long>(len), split_end));     // tokens [.., end)
+    if (!mp_check(a.status, end, static_cast<long long>(a.ncap) + 1, kSiteKv4Row)) end = 0;
     const int ntiles = (end - tile0 * kTile + kTile - 1) / kTile;        // <= 0: none
     const int mine = ntiles > warp ? (ntiles - warp + kAttWarps - 1) / kAttWarps : 0;
 
@@ -974,6 +981,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
             L = fmaf(s, src[w * kMergePitch + kD + 1], L);
             O = fmaf(s, src[w * kMergePitch + e], O);
         }
+        if (!mp_check(a.status, static_cast<long long>(row0 + h), a.rows, kSiteKv4Out)) continue;
         if (a.splits == 1) {
             a.out[(row0 + h) * kD + e] = L == 0.0f ? 0.0f : O / L;
         } else if (a.cluster) {
@@ -1155,6 +1163,7 @@ RowArgs row_args(const mp_kv4& c, const float* centre, int B, int Hkv, int m, in
     a.m = m;
     a.n_begin = n_begin;
     a.ncap = c.n_capacity;
+    a.status = device_status_ptr();
     return a;
 }
 typedef void (*RowFn)(const RowArgs);
@@ -1237,6 +1246,8 @@ cudaError_t launch_kv4_attention(const void* q, bool q_bf16, const mp_kv4& cache
     a.cluster = p.cluster;
     a.chunks = p.chunks;
     a.tiles_per_split = p.tiles_per_split;
+    a.rows = static_cast<long long>(B) * Hq;
+    a.status = device_status_ptr();
     a.scale = scale * 1.4426950408889634f;
     const long long ctas = static_cast<long long>(B) * Hkv * p.splits * p.chunks;
     if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;

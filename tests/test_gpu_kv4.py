@@ -600,6 +600,11 @@ def test_refusals_of_the_binding(mp):
         mp.kv4_write(cache._replace(params=cache.params.float()), x, x)
     with pytest.raises(ValueError):
         mp.kv4_write(cache._replace(v_codes=cache.v_codes[:, :, :60]), x, x)
+    for big in (2 ** 31, -2 ** 31 - 1, 2 ** 32):
+        with pytest.raises(ValueError):
+            mp.kv4_write(cache, x, x, n_begin=big)
+        with pytest.raises(ValueError):
+            mp.kv4_read(cache, 4, n_begin=big)
     with pytest.raises(mp.MagicPIGError):
         mp.kv4_read(cache, 65)
     with pytest.raises(TypeError):
@@ -631,4 +636,18 @@ def test_refusals_of_the_binding(mp):
         mp.kv4_decode_attention(q, codes, centre, W[:, :70].contiguous(), cache, 8, 10, 4, 8)
     with pytest.raises(ValueError):
         mp.kv4_decode_attention(q, codes, centre[:1], W, cache, 8, 10, 4, 8)
+    with pytest.raises(ValueError):
+        mp.kv4_decode_attention(q, codes, centre, W, cache, 8, 10, 4, 8,
+                                radius=torch.zeros(3, device="cuda"))
+    with pytest.raises(ValueError):
+        mp.kv4_attention(q, cache, workspace=torch.zeros(2, 512, device="cuda")[:, ::2])
+    # a workspace too small for what the call needs, here or in the sampled decode
+    long = mp.kv4_cache(1, 8, 98304)
+    assert mp.kv4_attention_workspace_bytes(1, 32, 8, 98304) > 256
+    with pytest.raises(mp.MagicPIGError):
+        mp.kv4_attention(torch.zeros(1, 32, 128, device="cuda"), long,
+                         workspace=torch.zeros(64, device="cuda"))
+    with pytest.raises(mp.MagicPIGError):
+        mp.kv4_decode_attention(q, codes, centre, W, cache, 8, 10, 4, 8,
+                                workspace=torch.zeros(64, device="cuda"))
     assert mp.device_status() == 0
