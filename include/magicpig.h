@@ -393,7 +393,8 @@ MP_API mp_status mp_kv4_attention(const void* q, mp_dtype q_dtype, const mp_kv4*
 /* mp_decode_attention, mp_sampled_attention and mp_sampled_attention_buckets with the keys and
  * values of a 4-bit cache, written with the centre that these calls get: the codes are those of
  * the keys themselves (mp_encode_keys and its variants, before the cache is written), the scores
- * and the cosine of p_i are those of the keys that the cache holds. prm->n_capacity is the
+ * and the cosine of p_i are those of the keys that the cache holds, and log u of the SimHash codes
+ * is evaluated for each sampled key, to about 2e-7. prm->n_capacity is the
  * codes' capacity, cache->n_capacity the cache's own (>= n). Workspaces, the query encoding
  * (mp_encode_query), variants and errors as for those calls. */
 MP_API mp_status mp_kv4_decode_attention(const void* q, mp_dtype q_dtype, const uint32_t* codes,

@@ -357,6 +357,7 @@ struct AArgs {
     float* out;
     const float* logu_tab;                       // log u over the cosine (SimHash: per call)
     int table_only;                              // cross-polytope: the table at every cosine
+    FineLogU fine;                               // 4-bit cache: log u of a key, SimHash codes
     int q_bf16, n, nblk, nsb, Hq, Hkv, G, K, L, n_sink, n_local;
     int ncap;                                    // K/V rows per head in memory
     int* status;                                 // index checks of the MP_CHECKS build
@@ -775,6 +776,8 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
                     const int ti = min(static_cast<int>(tt), kLuIntervals - 1);
                     const float g0 = __ldg(a.logu_tab + ti), g1 = __ldg(a.logu_tab + ti + 1);
                     lw = fmaf(tt - static_cast<float>(ti), g1 - g0, g0);
+                } else if constexpr (KV == kKv4) {
+                    lw = log_inclusion_fine(cs, a.fine);
                 } else {
                     lw = log_inclusion_at(cs, a.logu_tab, a.K, a.L);
                 }
@@ -1191,6 +1194,7 @@ cudaError_t launch_attend(const void* q, bool q_bf16, const float* centre, const
     aa.out = out;
     aa.logu_tab = s.logu_ext ? s.logu_ext : ws.logu_tab;
     aa.table_only = s.logu_ext != nullptr;     // cross-polytope: p has no closed form
+    aa.fine = fine_log_u(s.K, s.L);
     aa.q_bf16 = q_bf16;
     aa.n = s.n;
     aa.nblk = s.nblk;

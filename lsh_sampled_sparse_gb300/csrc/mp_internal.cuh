@@ -3,6 +3,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "magicpig.h"
@@ -335,6 +336,64 @@ __device__ inline float log_inclusion_p(float p, int K, int L) {
 // without the cancellation of 1 - (1 - small) as c approaches -1.
 __device__ inline float log_inclusion_cos(float c, int K, int L) {
     return log_inclusion_p(acosf(-c) * 0.318309886183790672f, K, L);
+}
+
+// log u of the same cosine to about 2e-7 (the closed form above: 1e-6, most of it the rounding of
+// K log p, 2 K log p being near -14), for the 4-bit cache's decode. With g(c) = log(1 + 2 asin(c) /
+// pi), K log p = K g - K log 2, x = p^K = e^{K g} 2^-K, and below lambda = L x = 3/2
+//   log u = c0 + 2 K g + (L - 2) log1p(-x) + log(1 + sum_{j>=3} t_j / t_2),
+//   c0 = log(L (L - 1) / 2) - 2 K log 2, rounded once,
+// with ten terms of the sum (the rest is under 3e-8) from ratio[i] = (L - j) / (j + 1), j = 2 + i;
+// above it u is 0.44 or more and needs no care. For |c| <= 1/2, g(c) / c is the interpolant of
+// degree 11 at the Chebyshev nodes of that interval (off by 2e-8 relative). A cosine below -1/2,
+// where 1 + 2 asin(c) / pi loses bits, takes the form above: no key is likely to be sampled there.
+struct FineLogU {
+    float c0, unit;                              // unit: 2^-K
+    float ratio[10];
+    int K, L;
+};
+inline FineLogU fine_log_u(int K, int L) {
+    FineLogU f = {};
+    f.K = K;
+    f.L = L;
+    f.c0 = L >= 2 ? static_cast<float>(log(0.5 * L * (L - 1.0)) - 2.0 * K * 0.69314718055994530942)
+                  : 0.0f;
+    f.unit = ldexpf(1.0f, -K);
+    for (int i = 0; i < 10; ++i)
+        f.ratio[i] = L > 2 + i ? static_cast<float>((L - 2.0 - i) / (3.0 + i)) : 0.0f;
+    return f;
+}
+__device__ __forceinline__ float log_inclusion_fine(float c, const FineLogU& f) {
+    if (c < -0.5f || f.L < 2 || f.K == 0) return log_inclusion_cos(c, f.K, f.L);
+    float g;
+    if (c <= 0.5f) {
+        constexpr float kG[12] = {0.636619747f,  -0.202642366f,  0.19211027f,  -0.108613737f,
+                                  0.111530021f,  -0.0743881315f, 0.0806043595f, -0.0585757904f,
+                                  0.0445040204f, -0.0329948924f, 0.0982281566f, -0.0787201822f};
+        g = kG[11];
+#pragma unroll
+        for (int i = 10; i >= 0; --i) g = fmaf(g, c, kG[i]);
+        g *= c;
+    } else {
+        g = log1pf(0.63661977236758134f * asinf(c));
+    }
+    const float kg = static_cast<float>(f.K) * g, Lf = static_cast<float>(f.L);
+    const float x = __expf(kg) * f.unit, lam = Lf * x;
+    if (x >= 1.0f) return 0.0f;
+    float l1;                                    // log1p(-x); x < 0.03 where L >= 50 and it counts
+    if (f.L >= 50 && lam < 1.5f)
+        l1 = -x * fmaf(x, fmaf(x, fmaf(x, fmaf(x, 0.2f, 0.25f), 0.333333333f), 0.5f), 1.0f);
+    else
+        l1 = log1pf(-x);
+    if (lam >= 1.5f) return logf(-expm1f(Lf * l1) - lam * expf((Lf - 1.0f) * l1));
+    const float r = __fdividef(x, 1.0f - x);
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 9; i >= 0; --i) {
+        const float t = f.ratio[i] * r;
+        sum = fmaf(sum, t, t);
+    }
+    return f.c0 + (2.0f * kg + ((Lf - 2.0f) * l1 + logf(1.0f + sum)));
 }
 
 // The attend kernel's log u for SimHash keys: linear interpolation in a per-call table of the

@@ -510,6 +510,25 @@ def test_sampled_decode_against_the_oracle_on_the_stored_cache(mp, dt, B, Hq, Hk
         assert torch.equal(bucketed, out)
 
 
+@pytest.mark.parametrize("K,L", [(1, 2), (2, 3), (3, 49), (4, 200), (7, 50), (12, 300), (20, 1000)])
+def test_sampled_decode_weighs_keys_to_a_few_millionths(mp, K, L):
+    """Over few and many tables, where the weights' log u takes each of its forms. The tolerance is
+    attention64's, and 2 x 3e-6 of the largest value for log u off by 3e-6 at most (twelve fp32
+    roundings of numbers up to 2 K log 2 = 28, the largest of the pairs)."""
+    wl = small_workload(name="kv4u", index=763, B=1, Hq=4, Hkv=2, n=4000, K=K, L=L, kv_dtype=F32,
+                        q_dtype=F32, w_dtype=F32, key_spread=4.0)
+    x, W, kc, centre, cache, codes, _ = _sampled_case(mp, wl, wl.n)
+    args = (wl.K, wl.L, wl.n_sink, wl.n_local)
+    out = mp.kv4_decode_attention(x["q"], codes, centre, W, cache, *args)
+    counts = mp.debug_select(x["q"], codes, centre, W, kc, torch.zeros_like(kc),
+                             *args)["cnt"].cpu().numpy()
+    want = _oracle_out(wl, x, W, centre, cache, codes, mp, x["q"], wl.n, counts)
+    _, tol = R.attention64(x["q"], cache, [wl.n], 128 ** -0.5)
+    vmax = R.values64(cache.v_codes, cache.params, 1).abs().max()
+    off = (out.double().cpu() - torch.from_numpy(want)).abs()
+    assert (off <= (tol + 6e-6 * vmax).cpu()).all(), float(off.max())
+
+
 @pytest.mark.parametrize("variant,K,L", [("mips", 9, 100), ("cp", 1, 16)])
 def test_variants_run_over_the_stored_cache(mp, variant, K, L):
     """Against the same variant's decode over the rows read back: the same values, at most
