@@ -354,8 +354,8 @@ typedef struct {
  * to rows [positions[b], positions[b] + m) of sequence b (n_begin is then ignored); a row that
  * falls outside [0, n_capacity) is not written. Other rows are left as they were. centre [B][Hkv][d]
  * is subtracted from the keys; NULL subtracts nothing.
- * Errors: MP_ERR_INVALID_ARG (shapes, m < 0, n_begin < 0 or n_begin + m > n_capacity without
- * positions, null, misalignment: keys and values 16 bytes, centre 16, positions 4),
+ * Errors: MP_ERR_INVALID_ARG (shapes, m < 0, B Hkv m > 2^31 - 1, n_begin < 0 or n_begin + m >
+ * n_capacity without positions, null, misalignment: keys and values 16 bytes, centre 16, positions 4),
  * MP_ERR_UNSUPPORTED (d != 128). m == 0 does nothing. */
 MP_API mp_status mp_kv4_write(const void* keys, const void* values, mp_dtype kv_dtype,
                               const float* centre, int B, int Hkv, int m, int d, int n_begin,
@@ -378,12 +378,12 @@ MP_API size_t mp_kv4_attention_workspace_bytes(int B, int Hq, int Hkv, int n, in
  *   out[b][h] = sum_i w_i v_i / sum_i w_i,   w_i = exp(scale q.k_i),   i < length_b
  * with the values that the cache holds; length_b = n, or lengths[b] ([B] int32 on the device,
  * taken into [0, n]). A sequence of length 0 gets zero rows. Any Hq that Hkv divides.
- * scale 0 means 1/sqrt(d). Scores, softmax and sums are float32: codes and the two halves of
+ * scale 0 means 1/sqrt(d). Scores, softmax and sums are float32: codes and the two fp16 halves of
  * a query element or a weight (22 bits) meet in exact tensor-core products. A NaN or an infinity
- * in a query gives NaN in its output row; one that the cache holds gives NaN to the rows that
- * attend to it (in a value: to its 64 dims).
- * Errors: MP_ERR_INVALID_ARG (shapes, n > n_capacity, Hq % Hkv, negative or NaN scale, null,
- * misalignment: out 16 bytes, lengths 4, workspace 256), MP_ERR_UNSUPPORTED (d != 128),
+ * in a query gives NaN in its output row (so may an element of 2^121 or more); one that the cache
+ * holds gives NaN to the rows that attend to it (in a value: to its 64 dims).
+ * Errors: MP_ERR_INVALID_ARG (shapes, n > n_capacity or 2^30, B Hq > 2^22, Hq % Hkv, a scale that is
+ * negative, infinite or NaN, null, misalignment: out 16 bytes, lengths 4, workspace 256), MP_ERR_UNSUPPORTED (d != 128),
  * MP_ERR_WORKSPACE. */
 MP_API mp_status mp_kv4_attention(const void* q, mp_dtype q_dtype, const mp_kv4* cache, int B, int Hq,
                                   int Hkv, int n, int d, const int32_t* lengths, float scale,
@@ -501,9 +501,9 @@ MP_API mp_status mp_device_status(int* status);
 
 /* The MP_CHECKS build (the library compiled with -DMP_CHECKS=1, libmagicpig_checks.so): every
  * kernel of the decode path, the bucketed lookup, the tensor-core encoder and the 4-bit cache check
- * the indices of their global accesses (code blocks, selection words, K/V rows, partial states, bucket ranges
- * and members, code words written) and skip an access that is out of range instead of making
- * it, raising MP_ERR_BOUNDS in the status word. A stand-in for a memory checker: the paper has
+ * the indices of their global accesses (code blocks, selection words, K/V rows, partial states,
+ * bucket ranges and members, code words written) and skip an access that is out of range instead of
+ * making it, raising MP_ERR_BOUNDS in the status word. A stand-in for a memory checker: the paper has
  * no counterpart. Synchronises the device and returns through *enabled 1 in that build, 0 in the
  * product build, and through *site the site of the first failed check since the status word was
  * last reset (0 if none): 1 query encoding stores, 2 scanned code block, 3 selection words

@@ -201,8 +201,8 @@ constexpr int kReadLanes = 8;
 constexpr uint32_t kManyRows = 2 * kSms * (kRowThreads / 4);     // two CTAs an SM of 4-lane rows
 int write_lanes(bool bf16, uint32_t rows) { return bf16 && rows >= kManyRows ? 4 : 8; }
 
-// Where a lane's row of block `blk` (kRowThreads / kLanes rows) is: head and token in the call, row of the
-// cache over all heads (-1: outside the cache, or past the call's rows). A block spans two heads at
+// Where a lane's row of block `blk` (kRowThreads / kLanes rows) is: head and token in the call, row
+// of the cache over all heads (-1: outside the cache, or past the call's rows). A block spans two heads at
 // most where a head has more rows than a block: one division, of uniform numbers, does then.
 struct RowAt {
     uint32_t r, bh;
@@ -231,6 +231,10 @@ __device__ __forceinline__ RowAt row_at(const RowArgs& a, uint32_t blk) {
     w.row = r < a.rows && pos >= 0 && pos < a.ncap
                 ? static_cast<long long>(w.bh) * a.ncap + pos : -1;
     return w;
+}
+
+__device__ __forceinline__ long long cache_rows(const RowArgs& a) {
+    return static_cast<long long>(a.rows / a.m) * a.ncap;
 }
 
 // 32 bytes of a row: one access where they are aligned (kWide: a whole sector a lane; two accesses
@@ -372,8 +376,7 @@ __global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 && kLanes == 8 ? 3
         codes_of<kBf16>(v, vp, vc);
         const uint32_t kp1 = __shfl_down_sync(0xffffffffu, kp, kLanes / 2);
         const uint32_t vp1 = __shfl_down_sync(0xffffffffu, vp, kLanes / 2);
-        if (now.row >= 0 &&
-            mp_check(a.status, now.row, static_cast<long long>(a.rows / a.m) * a.ncap, kSiteKv4Row)) {
+        if (now.row >= 0 && mp_check(a.status, now.row, cache_rows(a), kSiteKv4Row)) {
             store_codes(a.k_codes + now.row * kCodeBytes + kDims / 2 * rl, kc);
             store_codes(a.v_codes + now.row * kCodeBytes + kDims / 2 * rl, vc);
             if (rl == 0)
@@ -421,8 +424,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const RowArgs a) 
     auto load = [&](long long row) {
         kc = vc = make_uint2(0u, 0u);
         kp = vp = 0u;
-        if (row >= 0 &&
-            mp_check(a.status, row, static_cast<long long>(a.rows / a.m) * a.ncap, kSiteKv4Row)) {
+        if (row >= 0 && mp_check(a.status, row, cache_rows(a), kSiteKv4Row)) {
             kc = __ldg(reinterpret_cast<const uint2*>(a.k_codes + row * kCodeBytes + 8 * rl));
             vc = __ldg(reinterpret_cast<const uint2*>(a.v_codes + row * kCodeBytes + 8 * rl));
             const uint32_t* p = reinterpret_cast<const uint32_t*>(a.params + row * 16) + (rl >> 2);
@@ -648,8 +650,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
     const size_t bh = blockIdx.x / a.splits / a.chunks;
     const int b = static_cast<int>(bh / a.Hkv);
     const int h0 = static_cast<int>(ch) * 4 * NT;                        // first head of the chunk
-    const size_t row0 = static_cast<size_t>(b) * a.Hq + (bh - static_cast<size_t>(b) * a.Hkv) * a.G +
-                        h0;
+    const size_t row0 = static_cast<size_t>(b) * a.Hq + bh % a.Hkv * a.G + h0;
     const int heads = min(4 * NT, a.G - h0);
     const int len = a.lengths ? max(0, min(a.n, __ldg(a.lengths + b))) : a.n;
     const int tile0 = split * a.tiles_per_split;
@@ -734,7 +735,8 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
         big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
         big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
         const uint32_t ex = min(max(big >> 23, 5u), 247u);
-        const float down = __uint_as_float((258u - ex) << 23), up = __uint_as_float((ex + 6u) << 23);
+        const float down = __uint_as_float((258u - ex) << 23);
+        const float up = __uint_as_float((ex + 6u) << 23);
         float sum[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
@@ -824,7 +826,8 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
             }
 #pragma unroll
             for (int i = 0; i < 2 * kSub; ++i) {
-                const uint32_t p = *reinterpret_cast<const uint32_t*>(prm + 8 * i * kParamBytes + 4 * g);
+                const uint32_t p =
+                    *reinterpret_cast<const uint32_t*>(prm + 8 * i * kParamBytes + 4 * g);
                 const float s = __uint_as_float(p << 16), z = __uint_as_float(p & 0xffff0000u);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -865,10 +868,10 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
             l_run[nt] = fmaf(l_run[nt], corr[nt], sum);
         }
 
-        // ---- weighted codes of the tile, a group at a time. Weights times steps become fp16 halves
-        // after a power of two brings the tile's largest step to [2^13, 2^14): 2^(140 - ex), taken
-        // back by 2^(ex - 140), with the 2^-10 of the codes. A step that is NaN is the largest of all; its group is NaN in every
-        // head anyhow.
+        // ---- weighted codes of the tile, a group at a time. Weights times steps become fp16
+        // halves after a power of two brings the tile's largest step to [2^13, 2^14): 2^(140 - ex),
+        // taken back by 2^(ex - 140), with the 2^-10 of the codes. A step that is NaN is the
+        // largest of all; its group is NaN in every head anyhow.
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
             uint32_t pw[2 * kSub], vmax = 0u;
@@ -924,8 +927,8 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
                 __syncwarp();
                 issue(it + 2);
             }
-            // the second row of a pair holds its own dim's sum 16 times and the first one's once, in
-            // units 2^14 smaller
+            // the second row of a pair holds its own dim's sum 16 times and the first one's once,
+            // in units 2^14 smaller
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -944,7 +947,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
 
     // ---- sums over the lanes of a head, then the CTA's four warps in order
     __syncthreads();
-    float* join = reinterpret_cast<float*>(smem);                        // [head][warp][kMergePitch]
+    float* join = reinterpret_cast<float*>(smem);        // [head][warp][kMergePitch]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -977,7 +980,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
 #pragma unroll
         for (int w = 0; w < kAttWarps; ++w) {
             const float mw = src[w * kMergePitch + kD];
-            const float s = mw == -INFINITY ? 0.0f : exp2_fast(mw - M);  // an empty warp holds zeros
+            const float s = mw == -INFINITY ? 0.0f : exp2_fast(mw - M);  // empty: zeros
             L = fmaf(s, src[w * kMergePitch + kD + 1], L);
             O = fmaf(s, src[w * kMergePitch + e], O);
         }
@@ -1123,8 +1126,8 @@ AttPlan attention_plan(int B, int Hq, int Hkv, int n, bool ragged) {
     const long long units = static_cast<long long>(B) * Hkv * p.chunks;
     const int steps = (n - 1) / (kTile * kAttWarps) + 1, resident = p.nt == 1 ? 3 : 2;
     const int step_cost[2][3] = {{86, 66, 72}, {120, 107, 107}};
-    const double memory = static_cast<double>(B) * Hkv * n * (2 * kCodeBytes + kParamBytes) / 66700.0 *
-                          (ragged ? 0.75 : 1.0);
+    const double memory = static_cast<double>(B) * Hkv * n * (2 * kCodeBytes + kParamBytes) /
+                          66700.0 * (ragged ? 0.75 : 1.0);
     double best = -1.0;
     for (int k = 0; k <= 5; ++k) {               // no split; k CTAs an SM; waves of `resident`
         const int per_sm = k <= resident ? k : (k - resident + 1) * resident;
@@ -1137,9 +1140,10 @@ AttPlan attention_plan(int B, int Hq, int Hkv, int n, bool ragged) {
         double steps_there = static_cast<double>((busy + at_once - 1) / at_once * at_once) * each;
         if (ragged && busy > resident) steps_there = 0.75 * steps_there + 0.25 * resident * each;
         const bool clustered = used > 1 && used <= kClusterSplits && busy <= resident;
-        const double fixed = (used == 1 ? 400.0 : at_once == 1 ? 530.0 : at_once == 2 ? 620.0 : 870.0) -
-                             (clustered ? 40.0 : 0.0);
-        const double cost = fixed + std::max(memory, steps_there * step_cost[p.nt - 1][at_once - 1]);
+        const double split_fixed[3] = {530.0, 620.0, 870.0};
+        const double fixed = used == 1 ? 400.0 : split_fixed[at_once - 1] - (clustered ? 40.0 : 0.0);
+        const double compute = steps_there * step_cost[p.nt - 1][at_once - 1];
+        const double cost = fixed + std::max(memory, compute);
         if (best < 0.0 || cost < best) {
             best = cost;
             p.splits = used;
@@ -1170,7 +1174,8 @@ typedef void (*RowFn)(const RowArgs);
 RowFn pick_write(bool bf16, bool wide, int lanes) {
     using Bf16 = __nv_bfloat16;
     if (!bf16) return wide ? kv4_write_kernel<float, true, 8> : kv4_write_kernel<float, false, 8>;
-    if (lanes == 8) return wide ? kv4_write_kernel<Bf16, true, 8> : kv4_write_kernel<Bf16, false, 8>;
+    if (lanes == 8)
+        return wide ? kv4_write_kernel<Bf16, true, 8> : kv4_write_kernel<Bf16, false, 8>;
     return wide ? kv4_write_kernel<Bf16, true, 4> : kv4_write_kernel<Bf16, false, 4>;
 }
 RowFn pick_read(bool bf16, bool wide) {

@@ -441,7 +441,8 @@ def _sampled_case(mp, wl, cap, variant="simhash"):
     if variant == "mips":
         W = torch.cat([W, torch.randn(1, W.shape[1], generator=_gen(9), device="cuda").to(W.dtype)])
         extra["radius"] = mp.key_radius(kc, centre, n=wl.n)
-        codes = mp.encode_keys_mips(kc, centre, W.contiguous(), extra["radius"], wl.K, wl.L, 0, wl.n)
+        codes = mp.encode_keys_mips(kc, centre, W.contiguous(), extra["radius"], wl.K, wl.L, 0,
+                                    wl.n)
     elif variant == "cp":
         W = torch.randn(wl.L, 128, 128, generator=_gen(9), device="cuda").to(wl.w_dtype)
         extra["logu_table"] = mp.cp_logu_table(1, wl.L)
@@ -477,7 +478,8 @@ def _oracle_out(wl, x, W, centre, cache, codes, mp, q, n, counts):
 
 @pytest.mark.parametrize("dt,B,Hq,Hkv,n,cap,K,L", [
     (BF, 2, 8, 2, 5000, 5000, 10, 150), (F32, 1, 2, 2, 1500, 2100, 6, 40),
-    (BF, 1, 8, 1, 4097, 9000, 9, 120), (BF, 3, 4, 4, 70, 100, 8, 75), (F32, 1, 2, 1, 900, 900, 0, 2)])
+    (BF, 1, 8, 1, 4097, 9000, 9, 120), (BF, 3, 4, 4, 70, 100, 8, 75),
+    (F32, 1, 2, 1, 900, 900, 0, 2)])
 def test_sampled_decode_against_the_oracle_on_the_stored_cache(mp, dt, B, Hq, Hkv, n, cap, K, L):
     wl = small_workload(name="kv4", index=760, B=B, Hq=Hq, Hkv=Hkv, n=n, K=K, L=L, kv_dtype=dt,
                         q_dtype=dt, w_dtype=dt)
