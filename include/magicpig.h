@@ -383,8 +383,8 @@ MP_API size_t mp_kv4_attention_workspace_bytes(int B, int Hq, int Hkv, int n, in
  * in a query gives NaN in its output row (so may an element of 2^121 or more); one that the cache
  * holds gives NaN to the rows that attend to it (in a value: to its 64 dims).
  * Errors: MP_ERR_INVALID_ARG (shapes, n > n_capacity or 2^30, B Hq > 2^22, Hq % Hkv, a scale that is
- * negative, infinite or NaN, null, misalignment: out 16 bytes, lengths 4, workspace 256), MP_ERR_UNSUPPORTED (d != 128),
- * MP_ERR_WORKSPACE. */
+ * negative, infinite or NaN, null, misalignment: out 16 bytes, lengths 4, workspace 256),
+ * MP_ERR_UNSUPPORTED (d != 128), MP_ERR_WORKSPACE. */
 MP_API mp_status mp_kv4_attention(const void* q, mp_dtype q_dtype, const mp_kv4* cache, int B, int Hq,
                                   int Hkv, int n, int d, const int32_t* lengths, float scale,
                                   float* out, void* workspace, size_t ws_bytes,
@@ -394,9 +394,10 @@ MP_API mp_status mp_kv4_attention(const void* q, mp_dtype q_dtype, const mp_kv4*
  * values of a 4-bit cache, written with the centre that these calls get: the codes are those of
  * the keys themselves (mp_encode_keys and its variants, before the cache is written), the scores
  * and the cosine of p_i are those of the keys that the cache holds, and log u of the SimHash codes
- * is evaluated for each sampled key, to about 2e-7. prm->n_capacity is the
- * codes' capacity, cache->n_capacity the cache's own (>= n). Workspaces, the query encoding
- * (mp_encode_query), variants and errors as for those calls. */
+ * is evaluated for each sampled key, to about 2e-7. Values whose groups span more than 2^110 may
+ * overflow on the way. prm->n_capacity is the codes' capacity, cache->n_capacity the cache's own
+ * (>= n). Workspaces, the query encoding (mp_encode_query), variants and errors as for those
+ * calls. */
 MP_API mp_status mp_kv4_decode_attention(const void* q, mp_dtype q_dtype, const uint32_t* codes,
                                          const float* centre, const void* W, mp_dtype w_dtype,
                                          const mp_kv4* cache, int B, int Hq, int Hkv, int n, int d,

@@ -637,13 +637,16 @@ def _kv4_call(q, cache, n, out, workspace, need, stream):
     if out is None:
         out = _empty(shape, torch.float32, q.device, stream)
     op = _arg(out, device, "out", torch.float32, shape)
+    dims = (B, shape[1], Hkv, n, shape[2])
     if workspace is None:
-        workspace = _empty((max(need(B, shape[1], Hkv, n, shape[2]), 256),), torch.uint8, q.device,
-                           stream)
+        size = need(*dims)
+        if size == 0:                            # not every attention needs one
+            return c, device, dims, q.data_ptr(), qt, out, op, None, None, 0
+        workspace = _empty((size,), torch.uint8, q.device, stream)
     elif workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous and on the cache's device")
-    return (c, device, (B, shape[1], Hkv, n, shape[2]), q.data_ptr(), qt, out, op,
-            workspace, workspace.data_ptr(), _nbytes(workspace))
+    return (c, device, dims, q.data_ptr(), qt, out, op, workspace, workspace.data_ptr(),
+            _nbytes(workspace))
 
 
 def kv4_attention(q, cache: KV4Cache, n=None, lengths=None, scale: float = 0.0, out=None,
