@@ -183,6 +183,17 @@ MP_API mp_status mp_encode_keys(const void* keys, mp_dtype key_dtype, const floa
                                 int n_begin, int n_end, int d, int K, int L, uint32_t* codes,
                                 cudaStream_t stream);
 
+/* mp_encode_keys for keys that no cache of full precision holds (a 4-bit cache, mp_kv4 below):
+ * keys [B][Hkv][m][d] are the rows that join the context at [n_begin, n_begin + m) of every head.
+ * Bits of all other keys are kept; codes as for mp_encode_keys. Up to three launches: the part of a
+ * 1024-key block that the range begins in, whole blocks, the part that it ends in.
+ * Errors: MP_ERR_INVALID_ARG (shapes, m < 0, n_begin < 0 or n_begin + m > n_capacity, null,
+ * misalignment), MP_ERR_UNSUPPORTED (d != 128). m == 0 does nothing. */
+MP_API mp_status mp_encode_rows(const void* keys, mp_dtype key_dtype, const float* centre,
+                                const void* W, mp_dtype w_dtype, int B, int Hkv, int m,
+                                int n_capacity, int n_begin, int d, int K, int L, uint32_t* codes,
+                                cudaStream_t stream);
+
 /* Workspace bytes mp_decode_attention (and its two halves below) need for these shapes;
  * 0 if the shapes or parameters are invalid. */
 MP_API size_t mp_decode_workspace_bytes(int B, int Hq, int Hkv, int n, int d,

@@ -91,6 +91,7 @@ def _declare(L):
                                  _vp]),
         "mp_key_mean_cap": (_c_int, [_vp, _c_int] + [_c_int] * 5 + [_vp, _vp, _c_size, _vp]),
         "mp_encode_keys": (_c_int, [_vp, _c_int, _vp, _vp, _c_int] + [_c_int] * 8 + [_vp, _vp]),
+        "mp_encode_rows": (_c_int, [_vp, _c_int, _vp, _vp, _c_int] + [_c_int] * 8 + [_vp, _vp]),
         "mp_key_radius": (_c_int, [_vp, _c_int, _vp] + [_c_int] * 5 + [_vp, _vp]),
         "mp_cp_codes_bytes": (_c_size, [_c_int] * 4),
         "mp_cp_logu_table": (_c_int, [_c_int] * 3 + [_vp, _vp]),
@@ -275,6 +276,31 @@ def encode_keys(keys, centre, W, K: int, L: int, n_begin: int, n_end: int, codes
     _check(lib().mp_encode_keys(_ptr(keys), _dtype(keys, "keys"), _ptr(centre), _ptr(W),
                                 _dtype(W, "W"), B, Hkv, cap, n_begin, n_end, d, K, L,
                                 _ptr(codes), _stream(stream)), "mp_encode_keys")
+    return codes
+
+
+def encode_rows(keys, centre, W, K: int, L: int, n_begin: int, n_capacity: int, codes=None,
+                stream=None):
+    """encode_keys for keys that no full-precision cache holds (a 4-bit cache): the rows
+    [B, Hkv, m, d] that join every head's context at n_begin, into codes laid out for n_capacity
+    (allocated, all zero, where they are None). The bits of other keys are kept."""
+    _cuda(keys, "keys", 4)
+    B, Hkv, m, d = keys.shape
+    if not 0 <= n_begin <= n_capacity - m or n_capacity >> 31:
+        raise ValueError(f"{m} keys from {n_begin} on do not fit {n_capacity}")
+    nbytes = codes_bytes(B, Hkv, n_capacity, K, L)
+    if codes is None:
+        codes = torch.zeros(max(nbytes // 4, 4), dtype=torch.int32, device=keys.device)
+    _cuda(codes, "codes")
+    if _nbytes(codes) < nbytes:
+        raise ValueError("codes buffer too small for the capacity")
+    _cuda(centre, "centre", 3)
+    _cuda(W, "W", 2)
+    if tuple(centre.shape) != (B, Hkv, d) or tuple(W.shape) != (d, K * L):
+        raise ValueError(f"centre {tuple(centre.shape)} or W {tuple(W.shape)} does not fit the keys")
+    _check(lib().mp_encode_rows(_ptr(keys), _dtype(keys, "keys"), _ptr(centre), _ptr(W),
+                                _dtype(W, "W"), B, Hkv, m, n_capacity, n_begin, d, K, L,
+                                _ptr(codes), _stream(stream)), "mp_encode_rows")
     return codes
 
 

@@ -301,7 +301,8 @@ mp_status mp_encode_keys(const void* keys, mp_dtype key_dtype, const float* cent
     const bool kbf = key_dtype == MP_BF16, wbf = w_dtype == MP_BF16;
     if (n_end - n_begin <= kAppendMaxKeys)
         return to_status(launch_encode_append(keys, kbf, centre, W, wbf, B, Hkv, n_capacity,
-                                              n_begin, n_end, K, L, codes, stream));
+                                              n_begin, n_capacity, n_begin, n_end, K, L, codes,
+                                              stream));
     const int blk0 = n_begin / kKeysPerBlock;
     const int blk1 = (n_end + kKeysPerBlock - 1) / kKeysPerBlock;
     if (kbf && wbf) {
@@ -312,6 +313,52 @@ mp_status mp_encode_keys(const void* keys, mp_dtype key_dtype, const float* cent
     }
     return to_status(launch_encode_simt(keys, kbf, centre, W, wbf, B, Hkv, n_capacity, blk0,
                                         blk1, K, L, codes, stream));
+}
+
+mp_status mp_encode_rows(const void* keys, mp_dtype key_dtype, const float* centre, const void* W,
+                         mp_dtype w_dtype, int B, int Hkv, int m, int n_capacity, int n_begin,
+                         int d, int K, int L, uint32_t* codes, cudaStream_t stream) {
+    if (B < 1 || Hkv < 1 || m < 0 || n_capacity < 1 || d < 1 || K < 0 || K > 32 || L < 1)
+        return MP_ERR_INVALID_ARG;
+    if (n_begin < 0 || n_begin > n_capacity - m) return MP_ERR_INVALID_ARG;
+    if (!valid_dtype(key_dtype) || !valid_dtype(w_dtype)) return MP_ERR_INVALID_ARG;
+    if (d != kD) return MP_ERR_UNSUPPORTED;
+    if (static_cast<long long>(K) * L > (1 << 20)) return MP_ERR_INVALID_ARG;
+    if (K == 0 || m == 0) return MP_OK;   // nothing to encode
+    if (!keys || !centre || !W || !codes) return MP_ERR_INVALID_ARG;
+    if (!aligned(keys, 16) || !aligned(codes, 16) || !aligned(centre, 4) ||
+        !aligned(W, w_dtype == MP_BF16 ? 2 : 4))
+        return MP_ERR_INVALID_ARG;
+    if (!ensure_prepared()) return MP_ERR_CUDA;
+    const bool kbf = key_dtype == MP_BF16, wbf = w_dtype == MP_BF16;
+    const int cblk = (n_capacity + kKeysPerBlock - 1) / kKeysPerBlock;
+    for (int row = 0; row < m;) {
+        const int pos = n_begin + row, at = pos % kKeysPerBlock;
+        // whole blocks, or part of one, whose other keys' bits are kept
+        const bool whole = at == 0 && m - row >= kKeysPerBlock;
+        const int n = whole ? (m - row) / kKeysPerBlock * kKeysPerBlock
+                            : std::min(m - row, kKeysPerBlock - at);
+        const void* k = static_cast<const char*>(keys) +
+                        static_cast<size_t>(row) * kD * (kbf ? 2 : 4);
+        uint32_t* to = codes + static_cast<size_t>(pos / kKeysPerBlock) * K * L * kWordsPerBlock;
+        const bool few = n <= kAppendMaxKeys;
+        cudaError_t e = cudaErrorNotSupported;
+        if (kbf && wbf && !few)
+            e = launch_encode_tc(k, centre, W, B, Hkv, whole ? n : at + n, 0,
+                                 whole ? n / kKeysPerBlock : 1, K, L, to, device_status_ptr(),
+                                 stream, nullptr, nullptr, false, m, cblk, whole ? -1 : at);
+        if (e == cudaErrorNotSupported) {
+            cudaGetLastError();
+            e = whole ? launch_encode_simt(k, kbf, centre, W, wbf, B, Hkv, n, 0,
+                                           n / kKeysPerBlock, K, L, to, stream, m, cblk)
+                      : (few ? launch_encode_append : launch_encode_part)(
+                            keys, kbf, centre, W, wbf, B, Hkv, m, row, n_capacity, pos, pos + n, K,
+                            L, codes, stream);
+        }
+        if (e != cudaSuccess) return MP_ERR_CUDA;
+        row += n;
+    }
+    return MP_OK;
 }
 
 mp_status mp_key_radius(const void* keys, mp_dtype key_dtype, const float* centre, int B,

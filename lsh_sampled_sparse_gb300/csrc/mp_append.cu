@@ -24,7 +24,8 @@ constexpr int kAppendKeysAtOnce = 4;                           // independent su
 // fmaf(W[e][j], k[e] - mu[e], acc): the arithmetic of the CUDA-core block encoder.
 __global__ void __launch_bounds__(kAppendThreads)
     encode_append_kernel(const void* keys, int keys_bf16, const float* centre, const void* W,
-                         int w_bf16, int ncap, int n0, int n1, int C, int cblk, uint32_t* codes) {
+                         int w_bf16, int head_rows, int row0, int n0, int n1, int C, int cblk,
+                         uint32_t* codes) {
     extern __shared__ __align__(16) float sm[];
     float* Ws = sm;                                   // [kD][kAppendPlanes]
     float* kbar = sm + kD * kAppendPlanes;            // [n1 - n0][kD]
@@ -53,7 +54,8 @@ __global__ void __launch_bounds__(kAppendThreads)
             const int idx = base + u * kAppendThreads + tid;
             v[u] = idx < m * kD
                        ? load_elem(keys, keys_bf16,
-                                   (static_cast<size_t>(bh) * ncap + n0 + idx / kD) * kD + idx % kD) -
+                                   (static_cast<size_t>(bh) * head_rows + row0 + idx / kD) * kD +
+                                       idx % kD) -
                              centre[static_cast<size_t>(bh) * kD + idx % kD]
                        : 0.0f;
         }
@@ -96,8 +98,9 @@ __global__ void __launch_bounds__(kAppendThreads)
 }  // namespace
 
 cudaError_t launch_encode_append(const void* keys, bool keys_bf16, const float* centre,
-                                 const void* W, bool w_bf16, int B, int Hkv, int ncap, int n0,
-                                 int n1, int K, int L, uint32_t* codes, cudaStream_t st) {
+                                 const void* W, bool w_bf16, int B, int Hkv, int head_rows, int row0,
+                                 int ncap, int n0, int n1, int K, int L, uint32_t* codes,
+                                 cudaStream_t st) {
     const int C = K * L;
     if (C == 0 || n1 <= n0) return cudaSuccess;
     if (n1 - n0 > kAppendMaxKeys) return cudaErrorInvalidValue;
@@ -105,8 +108,8 @@ cudaError_t launch_encode_append(const void* keys, bool keys_bf16, const float* 
     const size_t smem = (static_cast<size_t>(kD) * kAppendPlanes +
                          static_cast<size_t>(n1 - n0) * kD) * sizeof(float);
     const dim3 grid((C + kAppendPlanes - 1) / kAppendPlanes, B * Hkv);
-    encode_append_kernel<<<grid, kAppendThreads, smem, st>>>(keys, keys_bf16, centre, W, w_bf16,
-                                                            ncap, n0, n1, C, cblk, codes);
+    encode_append_kernel<<<grid, kAppendThreads, smem, st>>>(
+        keys, keys_bf16, centre, W, w_bf16, head_rows, row0, n0, n1, C, cblk, codes);
     return cudaGetLastError();
 }
 

@@ -55,7 +55,8 @@ constexpr int kCSlots = 3;
 constexpr int kOnesSlice = 3;
 static_assert(kStgPitch == 257, "staging pitch");
 
-constexpr int kSign = 0, kMips = 1, kArgmax = 2;         // epilogue modes of the encoder
+// modes of the encoder; kPart: kSign for some keys of one block, whose other keys' bits are kept
+constexpr int kSign = 0, kMips = 1, kArgmax = 2, kPart = 3;
 
 // Shared memory of an encoder CTA: the A-tile ring, the -W chunk (B), the centre region, for
 // the MIPS variant its key slices, the word staging, barriers and the MIPS row of W. The MIPS
@@ -92,10 +93,18 @@ struct EncodeArgs {
     int C, nchunk, nblk, n, units, parts;
     int blk0;                       // first block encoded; a unit's block is blk0 + u % nblk
     int cblk;                       // code blocks per head in memory (the codes' head stride)
+    int lo;                         // kPart: keys [lo, n) of the block, the map's first row is lo
     // MIPS variant only: |k_i - mu| per key [BH][n] and r per head [BH]
     const float* norms;
     const float* radius;
 };
+
+// Word w of a block: the new bits of keys [lo, n), the old ones of the others.
+__device__ __forceinline__ uint32_t part_of(uint32_t was, uint32_t now, int w,
+                                            const EncodeArgs& a) {
+    const uint32_t range = bits_below(a.n - 32 * w) & ~bits_below(a.lo - 32 * w);
+    return (was & ~range) | (now & range);
+}
 
 // ---- PTX wrappers -----------------------------------------------------------------------------
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
@@ -357,7 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) {
                         mbar_arrive_expect_tx(bar_full + 8 * s, kStageBytes);
                         const uint32_t dst = smem_u32(sA + s * kStageBytes);
-                        const int row0 = (a.blk0 + blk) * kKeysPerBlock + t * kTileM;
+                        const int row0 = (a.blk0 + blk) * kKeysPerBlock + t * kTileM -
+                                         (kMode == kPart ? a.lo : 0);     // < 0 reads as zero
                         tma_load_3d(dst, &kmap, bar_full + 8 * s, 0, row0, bg);
                         tma_load_3d(dst + kHalfBytes, &kmap, bar_full + 8 * s, 64, row0, bg);
                     }
@@ -558,7 +568,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                             v.y = stg[(c4 + 1) * kStgPitch + r];
                             v.z = stg[(c4 + 2) * kStgPitch + r];
                             v.w = stg[(c4 + 3) * kStgPitch + r];
-                            *reinterpret_cast<uint4*>(dst + r * kWordsPerBlock + c4) = v;
+                            uint4* at = reinterpret_cast<uint4*>(dst + r * kWordsPerBlock + c4);
+                            if constexpr (kMode == kPart) {
+                                const uint4 old = *at;
+                                v.x = part_of(old.x, v.x, c4, a);
+                                v.y = part_of(old.y, v.y, c4 + 1, a);
+                                v.z = part_of(old.z, v.z, c4 + 2, a);
+                                v.w = part_of(old.w, v.w, c4 + 3, a);
+                            }
+                            *at = v;
                         }
                     }
                 }
@@ -723,7 +741,8 @@ cudaError_t prepare_encode_tc() {
         uint32_t smem;
     } kernels[] = {{encode_tc_kernel<kSign>, EncLayout<kSign>::kSmemBytes},
                    {encode_tc_kernel<kMips>, EncLayout<kMips>::kSmemBytes},
-                   {encode_tc_kernel<kArgmax>, EncLayout<kArgmax>::kSmemBytes}};
+                   {encode_tc_kernel<kArgmax>, EncLayout<kArgmax>::kSmemBytes},
+                   {encode_tc_kernel<kPart>, EncLayout<kPart>::kSmemBytes}};
     for (const auto& k : kernels) {
         const cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(k.smem));
@@ -735,16 +754,19 @@ cudaError_t prepare_encode_tc() {
 cudaError_t launch_encode_tc(const void* keys, const float* centre, const void* W, int B,
                              int Hkv, int ncap, int blk0, int blk1, int K, int L,
                              uint32_t* codes, int* status, cudaStream_t st, const float* norms,
-                             const float* radius, bool argmax) {
+                             const float* radius, bool argmax, int head_rows, int cblk, int lo) {
     const int C = K * L;
     if (C == 0 || blk1 <= blk0) return cudaSuccess;
+    if (lo >= 0 && (blk0 != 0 || blk1 != 1 || ncap > kKeysPerBlock || lo >= ncap))
+        return cudaErrorInvalidValue;
     EncodeTiledFn enc = encode_tiled_fn();
     if (!enc) return cudaErrorNotSupported;
     CUtensorMap map;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(ncap),
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD),
+                                static_cast<cuuint64_t>(lo > 0 ? ncap - lo : ncap),
                                 static_cast<cuuint64_t>(B) * Hkv};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kD) * 2,
-                                   static_cast<cuuint64_t>(ncap) * kD * 2};
+                                   static_cast<cuuint64_t>(head_rows ? head_rows : ncap) * kD * 2};
     const cuuint32_t box[3] = {64, kTileM, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = enc(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(keys), dims,
@@ -760,8 +782,9 @@ cudaError_t launch_encode_tc(const void* keys, const float* centre, const void* 
     a.nchunk = (C + kChunkN - 1) / kChunkN;
     a.nblk = blk1 - blk0;
     a.n = ncap;
+    a.lo = lo;
     a.blk0 = blk0;
-    a.cblk = (ncap + kKeysPerBlock - 1) / kKeysPerBlock;
+    a.cblk = cblk ? cblk : (ncap + kKeysPerBlock - 1) / kKeysPerBlock;
     a.norms = norms;
     a.radius = radius;
     a.units = B * Hkv * a.nblk;
@@ -774,6 +797,9 @@ cudaError_t launch_encode_tc(const void* keys, const float* centre, const void* 
                                     st>>>(map, a);
     else if (norms)
         encode_tc_kernel<kMips><<<a.nchunk * parts, kThreads, EncLayout<kMips>::kSmemBytes,
+                                  st>>>(map, a);
+    else if (lo >= 0)
+        encode_tc_kernel<kPart><<<a.nchunk * parts, kThreads, EncLayout<kPart>::kSmemBytes,
                                   st>>>(map, a);
     else
         encode_tc_kernel<kSign><<<a.nchunk * parts, kThreads, EncLayout<kSign>::kSmemBytes,

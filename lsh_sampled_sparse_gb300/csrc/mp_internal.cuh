@@ -124,19 +124,30 @@ int key_mean_splits(int BH, int n);
 // per head (keys >= ncap read as zero).
 // With norms (|k_i - mu| per key, [B*Hkv][ncap]) and radius ([B*Hkv]): the MIPS variant, W with
 // d + 1 rows. With argmax: the cross-polytope codes (bytes), W = G [L][d][d], K = d (a table is
-// d hyperplanes).
+// d hyperplanes). head_rows: rows from one head's keys to the next one's in memory (0: ncap); cblk:
+// blocks per head of the codes (0: as many as ncap keys have). lo >= 0: keys [lo, ncap) of one block
+// (blk0 = 0, blk1 = 1, ncap <= 1024; keys points at the first of them), the other keys' bits kept.
 cudaError_t launch_encode_tc(const void* keys, const float* centre, const void* W, int B,
                              int Hkv, int ncap, int blk0, int blk1, int K, int L,
                              uint32_t* codes, int* status, cudaStream_t st,
                              const float* norms = nullptr, const float* radius = nullptr,
-                             bool argmax = false);
+                             bool argmax = false, int head_rows = 0, int cblk = 0, int lo = -1);
 cudaError_t launch_encode_simt(const void* keys, bool keys_bf16, const float* centre,
                                const void* W, bool w_bf16, int B, int Hkv, int ncap, int blk0,
-                               int blk1, int K, int L, uint32_t* codes, cudaStream_t st);
-// Encode keys [n0, n1) (a short range) into their words, keeping the other keys' bits.
+                               int blk1, int K, int L, uint32_t* codes, cudaStream_t st,
+                               int head_rows = 0, int cblk = 0);
+// Encode keys [n0, n1) of one block of codes laid out for ncap on CUDA cores, keeping the other
+// keys' bits; key n0 of a head is row row0 of its head_rows.
+cudaError_t launch_encode_part(const void* keys, bool keys_bf16, const float* centre,
+                               const void* W, bool w_bf16, int B, int Hkv, int head_rows, int row0,
+                               int ncap, int n0, int n1, int K, int L, uint32_t* codes,
+                               cudaStream_t st);
+// Encode keys [n0, n1) (a short range) into their words of codes laid out for ncap, keeping the
+// other keys' bits; key n0 of a head is row row0 of its head_rows.
 cudaError_t launch_encode_append(const void* keys, bool keys_bf16, const float* centre,
-                                 const void* W, bool w_bf16, int B, int Hkv, int ncap, int n0,
-                                 int n1, int K, int L, uint32_t* codes, cudaStream_t st);
+                                 const void* W, bool w_bf16, int B, int Hkv, int head_rows, int row0,
+                                 int ncap, int n0, int n1, int K, int L, uint32_t* codes,
+                                 cudaStream_t st);
 
 // query sign bits, |q| and q.mu into the scratch; also resets the merge counters
 cudaError_t launch_qencode(const void* q, bool q_bf16, const float* centre, const void* W,

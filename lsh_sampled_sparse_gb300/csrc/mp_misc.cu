@@ -103,7 +103,8 @@ __global__ void __launch_bounds__(kMeanThreads)
 // fp32 CUDA-core encoder for dtype pairs the tensor-core path does not take (fp32 keys or W):
 // bit_{i,j} = [sum_e W[e][j] (k_i[e] - mu[e]) > 0] in fp32, one key per thread, a warp's 32 keys
 // form one word per hyperplane through a ballot. Whole 1024-key blocks from blk0 on (keys at or
-// past ncap read as zero). Grid z splits the hyperplanes when there are few keys, so that short
+// past ncap read as zero), or the keys [lo, hi) of one block, whose other keys' bits are kept: head
+// bh's rows in memory are head_rows from one head to the next, key `first` its first one. Grid z splits the hyperplanes when there are few keys, so that short
 // contexts still fill the GPU; every sum is the same sequence of fmaf over e either way.
 // ------------------------------------------------------------------------------------------------
 constexpr int kSimtKeys = 64;      // keys per CTA (2 words)
@@ -111,17 +112,20 @@ constexpr int kSimtPlanes = 16;    // hyperplanes per pass
 
 __global__ void __launch_bounds__(kSimtKeys)
     encode_simt_kernel(const void* keys, int keys_bf16, const float* centre, const void* W,
-                       int w_bf16, int ncap, int C, int cblk, int blk0, uint32_t* codes) {
+                       int w_bf16, int lo, int hi, int head_rows, int first, bool keep, int C,
+                       int cblk, int blk0, uint32_t* codes) {
     __shared__ float kbar[kSimtKeys][kD + 1];
     __shared__ float Wsm[kD][kSimtPlanes];
     const int bh = blockIdx.y, tile = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
     const int warp = tid >> 5;
     const int i0 = blk0 * kKeysPerBlock + tile * kSimtKeys;
+    if (keep && (i0 >= hi || i0 + kSimtKeys <= lo)) return;
     for (int idx = tid; idx < kSimtKeys * kD; idx += kSimtKeys) {
         const int r = idx / kD, e = idx % kD, i = i0 + r;
         float v = 0.0f;
-        if (i < ncap)
-            v = load_elem(keys, keys_bf16, (static_cast<size_t>(bh) * ncap + i) * kD + e) -
+        if (i >= lo && i < hi)
+            v = load_elem(keys, keys_bf16,
+                          (static_cast<size_t>(bh) * head_rows + i - first) * kD + e) -
                 centre[static_cast<size_t>(bh) * kD + e];
         kbar[r][e] = v;
     }
@@ -129,6 +133,8 @@ __global__ void __launch_bounds__(kSimtKeys)
     const int word = (i0 % kKeysPerBlock) / 32 + warp;
     uint32_t* dst = codes + (static_cast<size_t>(bh) * cblk + blk) * static_cast<size_t>(C) *
                                 kWordsPerBlock + word;
+    const int k0 = i0 + 32 * warp;                                 // of this warp's word
+    const uint32_t range = keep ? bits_below(hi - k0) & ~bits_below(lo - k0) : 0xffffffffu;
     const int passes = (C + kSimtPlanes - 1) / kSimtPlanes;
     const int per = (passes + gridDim.z - 1) / gridDim.z;          // passes of this CTA
     const int j_lo = blockIdx.z * per * kSimtPlanes;
@@ -154,8 +160,10 @@ __global__ void __launch_bounds__(kSimtKeys)
             const uint32_t bal = __ballot_sync(0xffffffffu, P[c] > 0.0f);
             if (lane == c) mine = bal;
         }
-        if (lane < kSimtPlanes && j0 + lane < C)
-            dst[static_cast<size_t>(j0 + lane) * kWordsPerBlock] = mine;
+        if (lane < kSimtPlanes && j0 + lane < C && range != 0u) {
+            uint32_t* word_at = dst + static_cast<size_t>(j0 + lane) * kWordsPerBlock;
+            *word_at = range == 0xffffffffu ? mine : (*word_at & ~range) | (mine & range);
+        }
     }
 }
 
@@ -277,20 +285,38 @@ cudaError_t launch_key_mean(const void* keys, bool bf16, int BH, int ncap, int n
     return cudaGetLastError();
 }
 
-cudaError_t launch_encode_simt(const void* keys, bool keys_bf16, const float* centre,
-                               const void* W, bool w_bf16, int B, int Hkv, int ncap, int blk0,
-                               int blk1, int K, int L, uint32_t* codes, cudaStream_t st) {
-    const int C = K * L;
-    if (C == 0 || blk1 <= blk0) return cudaSuccess;
-    const int cblk = (ncap + kKeysPerBlock - 1) / kKeysPerBlock;
-    const int tiles = (blk1 - blk0) * (kKeysPerBlock / kSimtKeys) * B * Hkv;
-    // hyperplane parts: enough CTAs for about four per SM, at most one part per pass
+// hyperplane parts: enough CTAs for about four per SM, at most one part per pass
+static dim3 simt_grid(int blocks, int heads, int C) {
+    const int tiles = blocks * (kKeysPerBlock / kSimtKeys) * heads;
     const int passes = (C + kSimtPlanes - 1) / kSimtPlanes;
     const int want = (4 * device_sm_count() + tiles - 1) / tiles;
-    const int parts = std::max(1, std::min(passes, want));
-    const dim3 grid((blk1 - blk0) * (kKeysPerBlock / kSimtKeys), B * Hkv, parts);
-    encode_simt_kernel<<<grid, kSimtKeys, 0, st>>>(keys, keys_bf16, centre, W, w_bf16, ncap, C,
-                                                    cblk, blk0, codes);
+    return dim3(blocks * (kKeysPerBlock / kSimtKeys), heads, std::max(1, std::min(passes, want)));
+}
+
+cudaError_t launch_encode_simt(const void* keys, bool keys_bf16, const float* centre,
+                               const void* W, bool w_bf16, int B, int Hkv, int ncap, int blk0,
+                               int blk1, int K, int L, uint32_t* codes, cudaStream_t st,
+                               int head_rows, int cblk) {
+    const int C = K * L;
+    if (C == 0 || blk1 <= blk0) return cudaSuccess;
+    if (head_rows == 0) head_rows = ncap;
+    if (cblk == 0) cblk = (ncap + kKeysPerBlock - 1) / kKeysPerBlock;
+    encode_simt_kernel<<<simt_grid(blk1 - blk0, B * Hkv, C), kSimtKeys, 0, st>>>(
+        keys, keys_bf16, centre, W, w_bf16, 0, ncap, head_rows, 0, false, C, cblk, blk0, codes);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_encode_part(const void* keys, bool keys_bf16, const float* centre,
+                               const void* W, bool w_bf16, int B, int Hkv, int head_rows, int row0,
+                               int ncap, int n0, int n1, int K, int L, uint32_t* codes,
+                               cudaStream_t st) {
+    const int C = K * L, blk0 = n0 / kKeysPerBlock;
+    if (C == 0 || n1 <= n0) return cudaSuccess;
+    if ((n1 - 1) / kKeysPerBlock != blk0) return cudaErrorInvalidValue;
+    const int cblk = (ncap + kKeysPerBlock - 1) / kKeysPerBlock;
+    encode_simt_kernel<<<simt_grid(1, B * Hkv, C), kSimtKeys, 0, st>>>(
+        keys, keys_bf16, centre, W, w_bf16, n0, n1, head_rows, n0 - row0, true, C, cblk, blk0,
+        codes);
     return cudaGetLastError();
 }
 

@@ -672,3 +672,79 @@ def test_refusals_of_the_binding(mp):
         mp.kv4_decode_attention(q, codes, centre, W, cache, 8, 10, 4, 8,
                                 workspace=torch.zeros(64, device="cuda"))
     assert mp.device_status() == 0
+
+
+def _code_bits(mp, codes, B, Hkv, cap, C):
+    """The sign bits [B, Hkv, blocks * 1024, C] of bit-sliced codes."""
+    w = codes.view(B, Hkv, -(-cap // 1024), C, 32, 1)
+    bits = (w >> torch.arange(32, dtype=torch.int32, device="cuda")) & 1
+    return bits.flatten(4).transpose(3, 4).flatten(2, 3)
+
+
+# whole blocks, parts of blocks (short and long; begun or ended by the range, or both), fp32
+@pytest.mark.parametrize("kd, wd, B, Hkv, m, cap, n0, K, L", [
+    (BF, BF, 2, 2, 1, 1500, 0, 10, 150), (BF, BF, 1, 3, 64, 2048, 1000, 10, 13),
+    (BF, BF, 2, 2, 65, 5000, 1023, 9, 20), (BF, BF, 1, 2, 2500, 5000, 0, 10, 150),
+    (BF, BF, 2, 1, 3100, 4200, 1024, 5, 7), (BF, BF, 1, 1, 1024, 1024, 0, 10, 30),
+    (BF, BF, 2, 3, 500, 1700, 300, 10, 150), (BF, BF, 1, 2, 900, 1000, 100, 10, 33),
+    (BF, BF, 2, 2, 66, 2000, 958, 10, 20), (BF, BF, 1, 2, 1300, 2600, 1100, 8, 25),
+    (F32, F32, 1, 2, 2300, 4000, 700, 10, 30), (F32, BF, 1, 2, 1, 1024, 1023, 10, 30),
+    (BF, F32, 3, 1, 130, 300, 170, 1, 5)])
+def test_codes_of_rows_that_no_cache_holds(mp, kd, wd, B, Hkv, m, cap, n0, K, L):
+    """Signs of w . (k - mu) in 64 bits wherever float32 can tell (128 products and sums: an error
+    below 2^-16 of the sum of the magnitudes); every other key's bits stay."""
+    g = _gen(900 + m)
+    C = K * L
+    keys = (torch.randn(B, Hkv, m, 128, generator=g, device="cuda") + 0.5).to(kd)
+    W = torch.randn(128, C, generator=g, device="cuda").to(wd)
+    centre = 0.5 + 0.1 * torch.randn(B, Hkv, 128, generator=g, device="cuda")
+    before = torch.randint(-2 ** 31, 2 ** 31, (mp.codes_bytes(B, Hkv, cap, K, L) // 4,),
+                           generator=g, device="cuda", dtype=torch.int32)
+    codes = mp.encode_rows(keys, centre, W, K, L, n0, cap, codes=before.clone())
+    was = _code_bits(mp, before, B, Hkv, cap, C)
+    got = _code_bits(mp, codes, B, Hkv, cap, C)
+    kd64, mu, Wd = keys.double(), centre.double().unsqueeze(2), W.double()
+    P = (kd64 - mu) @ Wd
+    sure = P.abs() > 2.0 ** -16 * (kd64.abs() + mu.abs()) @ Wd.abs()
+    assert sure.double().mean() > 0.99
+    new = got[:, :, n0:n0 + m]
+    assert torch.equal(new[sure], (P > 0).int()[sure])
+    assert torch.equal(got[:, :, :n0], was[:, :, :n0])
+    assert torch.equal(got[:, :, n0 + m:], was[:, :, n0 + m:])
+
+
+def test_a_run_without_a_full_precision_cache(mp):
+    """Prompt and appended tokens encoded and stored from their own rows alone, in pieces that
+    begin and end inside blocks: the codes and the sampled decode are those of a bf16 cache."""
+    B, Hq, Hkv, n0, steps, cap = 2, 8, 2, 3200, 3, 3300
+    wl = small_workload(name="kv4rows", index=763, B=B, Hq=Hq, Hkv=Hkv, n=n0 + steps, K=10, L=150)
+    x = {k: v.cuda() for k, v in make_layer(wl).items()}
+    W = make_hyperplanes(wl).cuda()
+    n = n0 + steps
+    prompt = x["keys"][:, :, :n0].contiguous()
+    centre = mp.key_mean(prompt)
+    cache = _filled(mp, B, Hkv, cap)
+    codes = None
+    for a, b in [(0, 700), (700, 2900), (2900, n0)] + [(i, i + 1) for i in range(n0, n)]:
+        k, v = (x[t][:, :, a:b].contiguous() for t in ("keys", "values"))
+        codes = mp.encode_rows(k, centre, W, wl.K, wl.L, a, cap, codes=codes)
+        mp.kv4_write(cache, k, v, n_begin=a, centre=centre)
+    kc = torch.zeros(B, Hkv, cap, 128, dtype=BF, device="cuda")
+    kc[:, :, :n] = x["keys"][:, :, :n]
+    dbg = mp.debug_select(x["q"], codes, centre, W, kc, torch.zeros_like(kc), wl.K, wl.L,
+                          wl.n_sink, wl.n_local, n=n)
+    sampled = mp.kv4_decode_attention(x["q"], codes, centre, W, cache, wl.K, wl.L, wl.n_sink,
+                                      wl.n_local, n=n)
+    want = _oracle_out(wl, x, W, centre, cache, codes, mp, x["q"], n, dbg["cnt"].cpu().numpy())
+    assert row_rel_err(sampled.cpu().numpy(), want) <= OUT_REL_TOL
+    one = mp.build_tables(x["keys"][:, :, :n].contiguous(), centre, W, wl.K, wl.L)
+    C, blocks = wl.K * wl.L, -(-n // 1024)
+    differ = _code_bits(mp, codes, B, Hkv, cap, C)[:, :, :n] \
+        != _code_bits(mp, one, B, Hkv, blocks * 1024, C)[:, :, :n]
+    assert differ.double().mean() < 1e-5                     # signs that float32 cannot tell
+    with pytest.raises(ValueError):
+        mp.encode_rows(prompt, centre, W, wl.K, wl.L, cap - n0 + 1, cap)
+    with pytest.raises(ValueError):
+        mp.encode_rows(prompt, centre, W, wl.K, wl.L, 0, cap, codes=codes[:-1].contiguous())
+    with pytest.raises(ValueError):
+        mp.encode_rows(prompt, centre[:, :1].contiguous(), W, wl.K, wl.L, 0, cap)

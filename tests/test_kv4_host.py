@@ -149,3 +149,25 @@ def test_binding_refuses_cpu_tensors(L):
         mp.kv4_read(cache, 4)
     with pytest.raises(TypeError):
         mp.kv4_attention(torch.zeros(1, 1, 128), cache)
+
+
+def test_encode_rows_rejects_bad_arguments_before_launch(L):
+    P = ctypes.c_void_p
+    ok = P(0x10000)
+
+    def enc(keys=ok, kd=1, centre=ok, W=ok, wd=1, B=1, Hkv=1, m=10, cap=100, n0=0, d=128, K=10,
+            tables=5, codes=ok):
+        return L.mp_encode_rows(keys, kd, centre, W, wd, B, Hkv, m, cap, n0, d, K, tables, codes,
+                                None)
+
+    assert enc(keys=None) == INVALID and enc(centre=None) == INVALID
+    assert enc(W=None) == INVALID and enc(codes=None) == INVALID
+    assert enc(kd=2) == INVALID and enc(wd=-1) == INVALID
+    assert enc(B=0) == INVALID and enc(Hkv=0) == INVALID and enc(m=-1) == INVALID
+    assert enc(cap=0) == INVALID and enc(n0=-1) == INVALID and enc(n0=91) == INVALID
+    assert enc(m=101) == INVALID and enc(n0=2 ** 31 - 5) == INVALID
+    assert enc(K=33) == INVALID and enc(tables=0) == INVALID
+    assert enc(keys=P(0x10008)) == INVALID and enc(codes=P(0x10004)) == INVALID
+    assert enc(centre=P(0x10002)) == INVALID and enc(W=P(0x10001)) == INVALID
+    assert enc(d=64) == UNSUPPORTED
+    assert enc(m=0, keys=None) == 0 and enc(K=0, codes=None) == 0      # nothing to do
