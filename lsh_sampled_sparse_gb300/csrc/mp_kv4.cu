@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 && kLanes == 8 ? 3
             else x[j] = pack2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
         }
     };
+    wait_for_predecessor();
     RowAt w = row_at<kLanes>(a, blockIdx.x);
     load(w.r);
     for (uint32_t blk = blockIdx.x; blk < a.blocks; blk += gridDim.x) {
@@ -436,6 +437,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const RowArgs a) 
             vp = __ldg(p + 2);
         }
     };
+    wait_for_predecessor();
     RowAt w = row_at<kReadLanes>(a, blockIdx.x);
     load(w.row);
     for (uint32_t blk = blockIdx.x; blk < a.blocks; blk += gridDim.x) {
@@ -646,14 +648,15 @@ __device__ __forceinline__ void values_of(const Query8& v, const A4Args& a, size
 // Four query heads a KV head: 32 sequences x 8 heads x 32K tokens take 195 us (6.2 TB/s, bound by
 // memory), 1 x 8 x 96K 24.1 us, of which about 6 are the launch, the queries and the join. Eight:
 // 2 x 8 x 128K take 66.6 us (4.5 TB/s); there a tile's arithmetic (1600 instructions a warp) takes
-// longer than its bytes, at two CTAs an SM, for which the registers do.
+// longer than its bytes, at two CTAs an SM, for which the registers do. Like the other kernels here
+// it is launched as a dependent of what precedes it in the stream and waits for that before its
+// first access: queued calls follow each other 2 to 3 us sooner (1 x 8 x 96K 26.7 -> 23.7 us).
 template <int NT>
 __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
     kv4_attention_kernel(const A4Args a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane >> 2, t = lane & 3;
-    allow_dependents();
     const int split = static_cast<int>(blockIdx.x % a.splits);
     const unsigned ch = blockIdx.x / a.splits % a.chunks;
     const size_t bh = blockIdx.x / a.splits / a.chunks;
@@ -661,6 +664,10 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
     const int h0 = static_cast<int>(ch) * 4 * NT;                        // first head of the chunk
     const size_t row0 = static_cast<size_t>(b) * a.Hq + bh % a.Hkv * a.G + h0;
     const int heads = min(4 * NT, a.G - h0);
+    wait_for_predecessor();
+    // the merge may start. Without one the dependent is another call, whose CTAs would take the
+    // places of this one's that end first (4 x 8 heads of 16K tokens 18.5 -> 22.2 us)
+    if (a.splits > 1 && !a.cluster) allow_dependents();
     const int len = a.lengths ? max(0, min(a.n, __ldg(a.lengths + b))) : a.n;
     const int tile0 = split * a.tiles_per_split;
     const long long split_end = static_cast<long long>(tile0 + a.tiles_per_split) * kTile;
@@ -1212,8 +1219,8 @@ cudaError_t launch_kv4_write(const void* keys, const void* values, bool bf16, co
     a.values = values;
     const int lanes = write_lanes(bf16, a.rows);
     const unsigned ctas = row_ctas(a, lanes, bf16 && lanes == 8 ? 3 : 2);
-    pick_write(bf16, wide_rows(keys, values), lanes)<<<ctas, kRowThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(pick_write(bf16, wide_rows(keys, values), lanes), dim3(ctas),
+                            dim3(kRowThreads), 0, st, a);
 }
 
 cudaError_t launch_kv4_read(const mp_kv4& cache, const float* centre, int B, int Hkv, int m,
@@ -1223,8 +1230,8 @@ cudaError_t launch_kv4_read(const mp_kv4& cache, const float* centre, int B, int
     a.keys = keys;
     a.values = values;
     const unsigned ctas = row_ctas(a, kReadLanes, 4);
-    pick_read(bf16, wide_rows(keys, values))<<<ctas, kRowThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(pick_read(bf16, wide_rows(keys, values)), dim3(ctas),
+                            dim3(kRowThreads), 0, st, a);
 }
 
 size_t kv4_attention_scratch_bytes(int B, int Hq, int Hkv, int n) {
@@ -1270,12 +1277,14 @@ cudaError_t launch_kv4_attention(const void* q, bool q_bf16, const mp_kv4& cache
     cfg.blockDim = dim3(kAttThreads);
     cfg.dynamicSmemBytes = kAttSmem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = p.splits;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.splits;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = p.cluster ? 1 : 0;
+    cfg.numAttrs = p.cluster ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(
         &cfg, p.nt == 1 ? kv4_attention_kernel<1> : kv4_attention_kernel<2>, a);
     if (e != cudaSuccess || p.splits == 1 || p.cluster) return e;

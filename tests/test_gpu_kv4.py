@@ -748,3 +748,105 @@ def test_a_run_without_a_full_precision_cache(mp):
         mp.encode_rows(prompt, centre, W, wl.K, wl.L, 0, cap, codes=codes[:-1].contiguous())
     with pytest.raises(ValueError):
         mp.encode_rows(prompt, centre[:, :1].contiguous(), W, wl.K, wl.L, 0, cap)
+
+
+def _chain(mp, x, n0, steps, sync):
+    """Tokens appended and attended to, the calls back to back or each waited for."""
+    B, Hkv = x["keys"].shape[:2]
+    cap = n0 + steps
+    cache = _filled(mp, B, Hkv, cap)
+    pos = torch.full((B,), n0, dtype=torch.int32, device="cuda")
+    mp.kv4_write(cache, x["keys"][:, :, :n0].contiguous(), x["values"][:, :, :n0].contiguous(),
+                 centre=x["centre"])
+    q = x["q"].clone()
+    codes = mp.encode_rows(x["keys"][:, :, :n0].contiguous(), x["centre"], x["W"], 4, 20, 0, cap)
+    rows = [[x[t][:, :, n0 + i:n0 + i + 1].contiguous() for t in ("keys", "values")]
+            for i in range(steps)]
+    outs = []
+    wait = torch.cuda.synchronize if sync else (lambda: None)
+    wait()
+    for i, (k, v) in enumerate(rows):
+        mp.kv4_write(cache, k, v, centre=x["centre"], positions=pos)
+        wait()
+        mp.encode_rows(k, x["centre"], x["W"], 4, 20, n0 + i, cap, codes=codes)
+        wait()
+        pos += 1
+        outs.append(mp.kv4_attention(q, cache, n=cap, lengths=pos))
+        wait()
+        outs.append(mp.kv4_decode_attention(q, codes, x["centre"], x["W"], cache, 4, 20, 4, 64,
+                                            n=n0 + i + 1))
+        wait()
+        q.mul_(0.5).add_(outs[-2].to(q.dtype))               # what the next step attends with
+        outs.extend(mp.kv4_read(cache, 5, n_begin=n0 + i - 4, dtype=F32))
+        wait()
+    return outs + list(cache)
+
+
+@pytest.mark.parametrize("B, Hq, Hkv, n0", [(1, 8, 2, 600), (2, 16, 4, 9000), (24, 32, 8, 700)])
+def test_calls_back_to_back_equal_calls_waited_for(mp, B, Hq, Hkv, n0):
+    """The kernels may start before their predecessors end: a step's output feeds the next one's
+    queries, rows and codes, over layouts with one split, a cluster and a merge."""
+    g = _gen(77)
+    steps = 6
+    x = {t: torch.randn(B, Hkv, n0 + steps, 128, generator=g, device="cuda").to(BF)
+         for t in ("keys", "values")}
+    x["q"] = torch.randn(B, Hq, 128, generator=g, device="cuda")
+    x["W"] = torch.randn(128, 80, generator=g, device="cuda").to(BF)
+    x["centre"] = mp.key_mean(x["keys"])
+    want = _chain(mp, x, n0, steps, True)
+    for _ in range(3):
+        got = _chain(mp, x, n0, steps, False)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert _same(a, b)
+
+
+def test_captured_behind_copies_and_other_streams(mp):
+    """In a graph the calls follow a copy from the host, a fill, a join of two streams, or
+    nothing."""
+    B, Hq, Hkv, cap = 2, 8, 2, 5000
+    g = _gen(78)
+    kv = [torch.randn(B, Hkv, 3, 128, generator=g, device="cuda").to(BF) for _ in range(2)]
+    cache = _random_cache(mp, B, Hkv, cap, cap, seed=79)
+    before = _clone(cache)
+    host = torch.randn(B, Hq, 128).pin_memory()
+    q, q2 = torch.zeros(B, Hq, 128, device="cuda"), torch.zeros(B, Hq, 128, device="cuda")
+    out = [torch.zeros(B, Hq, 128, device="cuda") for _ in range(3)]
+    ws = torch.empty(mp.kv4_attention_workspace_bytes(B, Hq, Hkv, cap) + 256, dtype=torch.uint8,
+                     device="cuda")
+    kr = [torch.zeros_like(kv[0]) for _ in range(2)]
+    side = torch.cuda.Stream()
+
+    def work():
+        mp.kv4_attention(q2, cache, out=out[0], workspace=ws)            # first in the graph
+        q.copy_(host, non_blocking=True)
+        mp.kv4_attention(q, cache, out=out[1], workspace=ws)             # behind a copy
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            q2.copy_(q).mul_(2.0)
+        mp.kv4_write(cache, *kv, n_begin=7)
+        torch.cuda.current_stream().wait_stream(side)
+        mp.kv4_attention(q2, cache, out=out[2], workspace=ws)            # behind two streams
+        kr[0].zero_()
+        mp.kv4_read(cache, 3, n_begin=7, keys=kr[0], values=kr[1])       # behind a fill
+
+    work()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in out[1:] + kr]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work()
+    for t, was in zip(cache, before):
+        t.copy_(was)
+    for t in out + kr:
+        t.zero_()
+    q2.copy_(host.cuda())
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    # the second replay's first two calls meet the rows that the first one wrote
+    first = mp.kv4_attention(2.0 * host.cuda(), cache)
+    assert _same(out[0], first)
+    assert _same(out[1], mp.kv4_attention(host.cuda(), cache))
+    for a, b in zip(out[2:] + kr, want[1:]):
+        assert _same(a, b)
