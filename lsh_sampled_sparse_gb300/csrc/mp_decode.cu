@@ -165,6 +165,10 @@ struct CArgs {
 // work region holds kAttendRows row slots of staged K/V rows; cbuf joins the warps' partials.
 constexpr int kAttendRows = 64;                      // row slots in an attend CTA's stage
 constexpr int kRowKeys = 256;                        // selected keys listed once per attend CTA
+// The rows of a 4-bit cache leave room for a list of all keys of a CTA, 16 bits each
+__host__ __device__ constexpr int attend_list_bytes(KvForm form) {
+    return form == kKv4 ? kAttendBlocks * kKeysPerBlock * 2 : kRowKeys * 4;
+}
 struct AttendSmem {
     size_t work, total;
 };
@@ -177,7 +181,7 @@ inline AttendSmem attend_smem(KvForm form) {
     AttendSmem m;
     m.work = static_cast<size_t>(kAttendRows) * attend_row_bytes(form);
     m.total = m.work + static_cast<size_t>(kAThreads) * 4 + (kAThreads + 4) * 4 +
-              static_cast<size_t>(kRowKeys) * 4 + static_cast<size_t>(kAWarps) * kCombinePitch * 4 +
+              attend_list_bytes(form) + static_cast<size_t>(kAWarps) * kCombinePitch * 4 +
               32;
     return m;
 }
@@ -361,6 +365,7 @@ struct AArgs {
     FineLogU fine;                               // 4-bit cache: log u of a key, SimHash codes
     int q_bf16, n, nblk, nsb, Hq, Hkv, G, K, L, n_sink, n_local;
     int ncap;                                    // K/V rows per head in memory
+    int share;                                   // 4-bit cache: 2^share CTAs, a cluster, per partial
     int* status;                                 // index checks of the MP_CHECKS build
     const float* radius;                         // MIPS variant: longest centred key per head
     float scale;
@@ -579,11 +584,13 @@ __device__ __forceinline__ unsigned atomic_add_acq_rel_gpu(unsigned* p, unsigned
 // KV: the form of the rows. The 4-bit cache holds its keys minus the centre: the dot products are
 // then those of the centred keys (the softmax does not see the difference), and the cosine needs
 // neither the centre nor q.mu.
-template <KvForm KV>
+// kShared: the rows of a partial are shared by a cluster of 2^share CTAs.
+template <KvForm KV, bool kShared>
 __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int sb = blockIdx.x, row = blockIdx.y;
+    const int share = kShared ? a.share : 0;
+    const int sb = blockIdx.x >> share, rank = blockIdx.x & ((1 << share) - 1), row = blockIdx.y;
     const int b = row / a.Hq, h = row % a.Hq;
     const int bg = b * a.Hkv + h / a.G;
     const bool exact = sb == a.nsb;              // this CTA takes T
@@ -599,7 +606,9 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
     uint32_t* wsel = reinterpret_cast<uint32_t*>(smem + a.work_bytes);      // [kWords]
     int* wpre = reinterpret_cast<int*>(wsel + kWords);                      // [kWords + 4]
     int* rowkey = wpre + kWords + 4;                                        // [kRowKeys]
-    float* cbuf = reinterpret_cast<float*>(rowkey + kRowKeys);              // [4][kCombinePitch]
+    uint16_t* rowlist = reinterpret_cast<uint16_t*>(rowkey);                // 4-bit: [kWords * 32]
+    float* cbuf = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(rowkey) +
+                                           attend_list_bytes(KV));          // [4][kCombinePitch]
     int* misc = reinterpret_cast<int*>(cbuf + kAWarps * kCombinePitch);     // [8]
 
     const int half = lane >> 4, hl = lane & 15;
@@ -638,7 +647,7 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
                          kSiteAttendSelect))
                 U = a.selmask[wi] & valid & ~tmask;
         }
-        wsel[tid] = U;
+        if constexpr (KV != kKv4) wsel[tid] = U;
         const int c = __popc(U);
         int incl = c;
 #pragma unroll
@@ -650,15 +659,24 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
         __syncthreads();
         int before = 0;
         for (int w = 0; w < warp; ++w) before += misc[w];
-        wpre[tid] = before + incl - c;
+        if constexpr (KV == kKv4) {
+            for (int i = before + incl - c; U; U &= U - 1u, ++i)
+                if ((i & ((1 << share) - 1)) == rank)
+                    rowlist[i >> share] = static_cast<uint16_t>(tid * 32 + __ffs(U) - 1);
+        } else {
+            wpre[tid] = before + incl - c;
+        }
         if (tid == kAThreads - 1) wpre[kWords] = before + incl;
         __syncthreads();
         nsel = wpre[kWords];
     }
+    // of a cluster's rows every 2^share-th is this CTA's
+    nsel = (nsel - rank + (1 << share) - 1) >> share;
     // key of entry i: T by arithmetic; else the word holding it (the last with wpre <= i) and its
     // (i - wpre)-th set bit
     auto key_of = [&](int i) -> int {
-        if (exact) return i < t_a ? i : t_b + (i - t_a);
+        i = (i << share) + rank;
+        if (exact || KV == kKv4) return i < t_a ? i : t_b + (i - t_a);
         int lo = 0, hi = kWords - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -830,9 +848,11 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
         m = mn;
     };
     static_assert(kAttendRows == 8 * kHalves, "the stage gives each half-warp 8 row slots");
-    // the keys of the first kRowKeys entries, listed once (later ones are found on demand)
-    for (int i = tid; i < min(nsel, kRowKeys); i += kAThreads) rowkey[i] = key_of(i);
-    __syncthreads();
+    // the keys of the first kRowKeys entries, listed once (4-bit: all are) (later ones are found on demand)
+    if constexpr (KV != kKv4) {
+        for (int i = tid; i < min(nsel, kRowKeys); i += kAThreads) rowkey[i] = key_of(i);
+        __syncthreads();
+    }
     // Group k of a warp: entries hw + 8 (4 k + j), j < 4, of its two half-warps, in the slots
     // hw + 8 (4 (k & 1) + j); group k + 2 reuses group k's slots once group k is folded.
     const int lo_hw = 2 * warp;                  // the warp's first half-warp has its most rows
@@ -849,7 +869,11 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
                 const int e = lo_hw + (jj & 1) + kHalves * (4 * k + (jj >> 1));
                 if (e >= nsel) continue;
                 const int r = lo_hw + (jj & 1) + kHalves * (4 * (k & 1) + (jj >> 1));
-                const size_t key = static_cast<size_t>(e < kRowKeys ? rowkey[e] : key_of(e));
+                size_t key;
+                if constexpr (KV == kKv4)
+                    key = exact ? key_of(e) : blk0 * kKeysPerBlock + rowlist[e];
+                else
+                    key = static_cast<size_t>(e < kRowKeys ? rowkey[e] : key_of(e));
                 if (!mp_check(a.status, static_cast<long long>(key), min(a.n, a.ncap),
                               kSiteAttendRow))
                     continue;
@@ -909,8 +933,7 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
     }
     __syncthreads();
     const size_t prow = static_cast<size_t>(row) * nsp + sb;
-    if (tid < kD && mp_check(a.status, static_cast<long long>(prow),
-                             static_cast<long long>(gridDim.y) * nsp, kSiteAttendPartial)) {
+    {
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kAWarps; ++w) M = fmaxf(M, cbuf[w * kCombinePitch + 128]);
@@ -924,10 +947,38 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
                 Os += s * rr[tid];
             }
         }
-        a.po[prow * kD + tid] = Os;
-        if (tid == 0) {
-            a.pm[prow] = M;
-            a.pl[prow] = Ls;
+        if constexpr (kShared) {                 // the CTAs of a cluster, in order, by the first
+            __syncthreads();
+            cbuf[tid] = Os;
+            if (tid == 0) {
+                cbuf[128] = M;
+                cbuf[129] = Ls;
+            }
+            cluster_barrier();
+            if (rank == 0) {
+                const uint32_t at = smem_u32(cbuf);
+                for (int r = 1; r < (1 << share); ++r) {
+                    const uint32_t there = peer_address(at, r);
+                    const float mr = load_peer(there + 4 * 128), mn = fmaxf(M, mr);
+                    const float lr = load_peer(there + 4 * 129);
+                    const float orr = load_peer(there + 4 * tid);
+                    const float s0 = mn == -INFINITY ? 0.0f : __expf(M - mn);
+                    const float s1 = mn == -INFINITY ? 0.0f : __expf(mr - mn);
+                    Ls = Ls * s0 + lr * s1;
+                    Os = Os * s0 + orr * s1;
+                    M = mn;
+                }
+            }
+            cluster_barrier();                   // no CTA leaves while the first reads from it
+            if (rank != 0) return;
+        }
+        if (mp_check(a.status, static_cast<long long>(prow),
+                     static_cast<long long>(gridDim.y) * nsp, kSiteAttendPartial)) {
+            a.po[prow * kD + tid] = Os;
+            if (tid == 0) {
+                a.pm[prow] = M;
+                a.pl[prow] = Ls;
+            }
         }
     }
 
@@ -1031,9 +1082,10 @@ KernelFn pick_collide(int G) {
 
 typedef void (*AttendFn)(const AArgs);
 
-AttendFn pick_attend(KvForm form) {
-    return form == kKv4 ? attend_kernel<kKv4>
-                        : (form == kKvBf16 ? attend_kernel<kKvBf16> : attend_kernel<kKvF32>);
+AttendFn pick_attend(KvForm form, bool shared = false) {
+    return form == kKv4 ? (shared ? attend_kernel<kKv4, true> : attend_kernel<kKv4, false>)
+                        : (form == kKvBf16 ? attend_kernel<kKvBf16, false>
+                                           : attend_kernel<kKvF32, false>);
 }
 
 size_t collide_smem_for(int G, int cpad, int K) {
@@ -1072,6 +1124,10 @@ cudaError_t prepare_decode() {
                                              static_cast<int>(kMaxSmem));
         if (e != cudaSuccess) return e;
     }
+    const cudaError_t es = cudaFuncSetAttribute(pick_attend(kKv4, true),
+                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                static_cast<int>(kMaxSmem));
+    if (es != cudaSuccess) return es;
     // one shared-memory carve-out (the largest) for every kernel of a decode step: an SM still
     // running CTAs of one kernel can then take CTAs of the next without first draining to
     // reconfigure its L1 / shared-memory split
@@ -1082,7 +1138,8 @@ cudaError_t prepare_decode() {
                          reinterpret_cast<const void*>(pick_collide(8)),
                          reinterpret_cast<const void*>(pick_attend(kKvF32)),
                          reinterpret_cast<const void*>(pick_attend(kKvBf16)),
-                         reinterpret_cast<const void*>(pick_attend(kKv4))};
+                         reinterpret_cast<const void*>(pick_attend(kKv4)),
+                         reinterpret_cast<const void*>(pick_attend(kKv4, true))};
     for (const void* f : fns) {
         cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
                                              cudaSharedmemCarveoutMaxShared);
@@ -1185,7 +1242,6 @@ cudaError_t launch_attend(const void* q, bool q_bf16, const float* centre, const
                           const DecodeShape& s, float* out, const DecodeScratch& ws,
                           cudaStream_t st) {
     const int G = s.Hq / s.Hkv;
-    AttendFn attend = pick_attend(kv.form);
     const size_t smem_att = attend_smem_for(kv.form);
     if (smem_att > kMaxSmem) return cudaErrorNotSupported;
     AArgs aa;
@@ -1220,8 +1276,23 @@ cudaError_t launch_attend(const void* q, bool q_bf16, const float* centre, const
     aa.radius = s.radius;
     aa.scale = s.scale;
     aa.work_bytes = static_cast<int>(attend_smem(kv.form).work);
-    return launch_dependent(attend, dim3(aa.nsb + 1, s.B * s.Hq), dim3(kAThreads), smem_att, st,
-                            aa);
+    // While the GPU holds more CTAs than there are (six an SM), a CTA with more rows than twice
+    // its slots shares them with up to seven others: of keys without a bias toward the query a share of
+    // 1 - (1 + x) e^-x collides twice, x = L times the chance in one table. 16 query heads, 3200 keys,
+    // (7, 195): 144 -> 35 us; with few rows a cluster's start and join cost 1 us more than they save.
+    // Only over the 4-bit cache: the other forms' sums keep their order.
+    const long long ctas = static_cast<long long>(s.B) * s.Hq * (aa.nsb + 1);
+    const double x = s.L * (s.cp ? 0.5 / kD : ldexp(1.0, -s.K));
+    const int keys = std::min(s.n, kAttendBlocks * kKeysPerBlock);
+    const long long rows = std::max(static_cast<long long>(keys * (1.0 - (1.0 + x) * exp(-x))),
+                                    std::min<long long>(s.n, 0ll + s.n_sink + s.n_local));
+    aa.share = 0;
+    while (kv.form == kKv4 && rows > 2 * kAttendRows && aa.share < 3 &&
+           ctas << (aa.share + 1) <= 6 * device_sm_count())
+        ++aa.share;
+    const AttendFn attend = pick_attend(kv.form, aa.share > 0);
+    return launch_dependent(attend, dim3((aa.nsb + 1) << aa.share, s.B * s.Hq), dim3(kAThreads),
+                            smem_att, st, aa, 1 << aa.share);
 }
 
 }  // namespace mp

@@ -243,20 +243,24 @@ cudaError_t launch_encode_mips(const void* keys, bool keys_bf16, const float* ce
                                int ncap, int n0, int n1, int K, int L, uint32_t* codes,
                                cudaStream_t st);
 
-// Launch `kern` as a programmatic dependent of the previous kernel in the stream.
+// Launch `kern` as a programmatic dependent of the previous kernel in the stream, `cluster` CTAs of
+// its grid's x a cluster.
 template <typename Arg>
 cudaError_t launch_dependent(void (*kern)(Arg), dim3 grid, dim3 block, size_t smem,
-                             cudaStream_t st, const Arg& arg) {
+                             cudaStream_t st, const Arg& arg, int cluster = 1) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, arg);
 }
 
@@ -301,6 +305,23 @@ __device__ __forceinline__ uint32_t warp_transpose32(uint32_t x, int lane) {
 // Programmatic dependent launch: the next kernel in the stream may be scheduled once every CTA
 // of this one has started; a kernel launched that way waits for its predecessor's completion
 // (and memory) before it touches anything the predecessor writes.
+// Thread-block clusters: a barrier of all their threads, the address of this CTA's shared memory in
+// CTA `rank` of the cluster, and a float from there
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+                 ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_address(uint32_t addr, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float load_peer(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ void allow_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

@@ -570,22 +570,6 @@ __device__ __forceinline__ uint32_t warp_max(uint32_t x) {
     return __reduce_max_sync(0xffffffffu, x);
 }
 
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
-                 ::: "memory");
-}
-// The address of this CTA's shared memory in CTA `rank` of the cluster, and a float from there
-__device__ __forceinline__ uint32_t peer_address(uint32_t addr, int rank) {
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ float load_peer(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-
 // Eight codes of a word as four fp16 pairs: with c0 .. c3 the codes of its low half and c4 .. c7 of
 // its high half, the pairs are (c0, c4) 2^-10, (c0 + 16 c1, c4 + 16 c5) 2^-24 and the same of c2, c3,
 // c6, c7; the other matrix takes the sums of two codes apart again. A byte is a subnormal fp16 as
@@ -1272,21 +1256,10 @@ cudaError_t launch_kv4_attention(const void* q, bool q_bf16, const mp_kv4& cache
     a.scale = scale * 1.4426950408889634f;
     const long long ctas = static_cast<long long>(B) * Hkv * p.splits * p.chunks;
     if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(kAttThreads);
-    cfg.dynamicSmemBytes = kAttSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = p.splits;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.cluster ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(
-        &cfg, p.nt == 1 ? kv4_attention_kernel<1> : kv4_attention_kernel<2>, a);
+    const cudaError_t e = launch_dependent(
+        p.nt == 1 ? kv4_attention_kernel<1> : kv4_attention_kernel<2>,
+        dim3(static_cast<unsigned>(ctas)), dim3(kAttThreads), kAttSmem, st, a,
+        p.cluster ? p.splits : 1);
     if (e != cudaSuccess || p.splits == 1 || p.cluster) return e;
     return launch_dependent(kv4_merge_kernel, dim3(static_cast<unsigned>(B) * Hq),
                             dim3(32 * kMergeWarps), 0, st, a);

@@ -531,6 +531,29 @@ def test_sampled_decode_weighs_keys_to_a_few_millionths(mp, K, L):
     assert (off <= (tol + 6e-6 * vmax).cpu()).all(), float(off.max())
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,n,K,L,n_sink,n_local", [
+    (1, 16, 8, 3194, 7, 195, 4, 64), (4, 16, 8, 700, 6, 180, 4, 64), (4, 32, 8, 901, 6, 99, 0, 64),
+    (8, 64, 8, 1500, 5, 100, 4, 64), (1, 2, 1, 2000, 10, 150, 300, 1200),
+    (1, 1, 1, 200, 10, 150, 150, 150), (1, 2, 2, 8200, 4, 90, 1, 1)])
+def test_sampled_decode_where_much_is_sampled(mp, B, Hq, Hkv, n, K, L, n_sink, n_local):
+    """A CTA's many rows, alone or shared with one, three or seven others; a long exact set. The
+    tolerance is that of the test above."""
+    wl = small_workload(name="kv4d", index=764, B=B, Hq=Hq, Hkv=Hkv, n=n, K=K, L=L, kv_dtype=BF,
+                        q_dtype=F32, w_dtype=BF, n_sink=n_sink, n_local=n_local)
+    x, W, kc, centre, cache, codes, _ = _sampled_case(mp, wl, n + 3)
+    args = (wl.K, wl.L, wl.n_sink, wl.n_local)
+    out = mp.kv4_decode_attention(x["q"], codes, centre, W, cache, *args, n=n)
+    counts = mp.debug_select(x["q"], codes, centre, W, kc, torch.zeros_like(kc), *args,
+                             n=n)["cnt"].cpu().numpy()
+    want = _oracle_out(wl, x, W, centre, cache, codes, mp, x["q"], n, counts)
+    _, tol = R.attention64(x["q"], cache, [n] * B, 128 ** -0.5)
+    vmax = R.values64(cache.v_codes, cache.params, 1)[:, :, :n].abs().max()
+    off = (out.double().cpu() - torch.from_numpy(want)).abs()
+    assert (off <= (tol + 6e-6 * vmax).cpu()).all(), float(off.max())
+    again = mp.kv4_decode_attention(x["q"], codes, centre, W, cache, *args, n=n)
+    assert torch.equal(out, again)
+
+
 @pytest.mark.parametrize("variant,K,L", [("mips", 9, 100), ("cp", 1, 16)])
 def test_variants_run_over_the_stored_cache(mp, variant, K, L):
     """Against the same variant's decode over the rows read back: the same values, at most
