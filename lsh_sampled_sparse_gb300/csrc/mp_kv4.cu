@@ -584,12 +584,21 @@ __device__ __forceinline__ void unpack_pairs(uint32_t w, uint32_t (&h)[4]) {
     h[2] = mul_f16x2(h[3] & 0x000f000fu, 0x74007400u);
 }
 
-// x as two fp16: its leading 11 bits in the low half, the rest of it in the high half
-__device__ __forceinline__ uint32_t split_f16(float x) {
-    const float hi = __uint_as_float(__float_as_uint(x) & 0xffffe000u);
+// The leading 11 bits of x; two floats as fp16
+__device__ __forceinline__ float leading_bits(float x) {
+    return __uint_as_float(__float_as_uint(x) & 0xffffe000u);
+}
+__device__ __forceinline__ uint32_t pack_f16(float low, float high) {
     uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(x - hi), "f"(hi));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(high), "f"(low));
     return r;
+}
+
+// What row r + 8 half of a lane's products holds for its head nt: the sum of two columns, or (NT = 2)
+// one that has both halves' products
+template <int NT>
+__device__ __forceinline__ float head_of(const float (&c)[4], int half, int nt) {
+    return NT == 1 ? c[2 * half] + c[2 * half + 1] : c[2 * half + nt];
 }
 
 // Eight elements of a query from element i on: the loads, where the queries are aligned for loads
@@ -626,7 +635,7 @@ __device__ __forceinline__ void values_of(const Query8& v, const A4Args& a, size
 }
 
 // One CTA per (head of keys and values, split of its tokens, chunk of 4 NT query heads of the
-// group). Lane (r, t) = (lane / 4, lane % 4) holds query head t (and t + 4 where NT = 2) of the
+// group). Lane (r, t) = (lane / 4, lane % 4) holds query head t (2 t and 2 t + 1 where NT = 2) of the
 // logits, weights and sums: tokens r and r + 8 of a fragment, dims 32 m + 4 r .. + 3.
 //
 // Four query heads a KV head: 32 sequences x 8 heads x 32K tokens take 195 us (6.2 TB/s, bound by
@@ -704,31 +713,27 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     // the queries' loads first: behind the tiles of the whole GPU they would hold up the first step
-    Query8 raw[NT][4];
+    Query8 raw[4];
+    const int qh = NT == 1 ? r >> 1 : r;                                 // this lane's column's head
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int h = 4 * nt + (lane >> 3);
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-            raw[nt][m] = load_query8(a, (row0 + h) * kD + 32 * m + 8 * t, h < heads);
-    }
+    for (int m = 0; m < 4; ++m)
+        raw[m] = load_query8(a, (row0 + qh) * kD + 32 * m + 8 * t, qh < heads);
     issue(0);
     issue(1);
 
-    // ---- the queries as column fragments: column 2 h is head h's leading half, 2 h + 1 the rest.
-    // A lane loads head lane / 8 of its four (dims 32 m + 8 t ..), scaled by a power of two so
-    // that the largest element lies in [2^4, 2^5); fac undoes it on the logits, and the 2^-10 of
-    // the codes. Against the pairs of unpack_pairs stand q0 - q1 / 16 and 2^14 q1 / 16.
+    // ---- the queries as column fragments, qb[0] of the leading halves and qb[1] of the rest, a
+    // column a head, or for NT = 1 qb[0] alone: column 2 h is head h's leading half, 2 h + 1 the rest.
+    // A lane loads its column's head (dims 32 m + 8 t ..), scaled by a power of two so that the
+    // largest element lies in [2^4, 2^5); fac undoes it on the logits, and the 2^-10 of the codes.
+    // Against the pairs of unpack_pairs stand q0 - q1 / 16 and 2^14 q1 / 16.
     uint32_t qb[NT][4][4];
     float fac[NT], qsum[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int h = 4 * nt + (lane >> 3);
+    {
         float x[4][8];
         uint32_t big = 0u;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            values_of(raw[nt][m], a, (row0 + h) * kD + 32 * m + 8 * t, h < heads, x[m]);
+            values_of(raw[m], a, (row0 + qh) * kD + 32 * m + 8 * t, qh < heads, x[m]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) big = max(big, __float_as_uint(x[m][e]) & 0x7fffffffu);
         }
@@ -752,21 +757,28 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                // the leading half rounded to nearest, the rest; this lane's column keeps one
+                // the leading half rounded to nearest, the rest
                 const __half2 lead = __floats2half2_rn(x[m][e], x[m][e + 4]);
                 const float2 lf = __half22float2(lead);
                 const __half2 rem = __floats2half2_rn(x[m][e] - lf.x, x[m][e + 4] - lf.y);
-                const __half2 keep = (r & 1) ? rem : lead;
-                qb[nt][m][e] = *reinterpret_cast<const uint32_t*>(&keep);
+                const __half2 first = NT == 1 && (r & 1) ? rem : lead;
+                qb[0][m][e] = *reinterpret_cast<const uint32_t*>(&first);
+                if constexpr (NT == 2) qb[1][m][e] = *reinterpret_cast<const uint32_t*>(&rem);
             }
         }
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
             sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
             sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
-            qsum[nt][g] = 0x1p-10f * __shfl_sync(0xffffffffu, sum[g], 8 * t);
         }
-        fac[nt] = fmaxf(__shfl_sync(0xffffffffu, a.scale * up, 8 * t), 1.17549435e-38f);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int from = 8 * t + 4 * nt;                             // a lane of the head's column
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+                qsum[nt][g] = 0x1p-10f * __shfl_sync(0xffffffffu, sum[g], from);
+            fac[nt] = fmaxf(__shfl_sync(0xffffffffu, a.scale * up, from), 1.17549435e-38f);
+        }
     }
 
     // running maximum of the logits as the products leave them, the same times fac
@@ -796,15 +808,13 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
         float lg[NT][2 * kSub];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-            float c[NT][kSub][4];
+            float c[kSub][4];
             uint32_t kw[kSub][4];
 #pragma unroll
             for (int j = 0; j < kSub; ++j) {
                 ldmatrix4(kw[j], st + kStageK + 16 * j * kCodeBytes + (lm ^ (g << 5)));
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) c[nt][j][e] = 0.0f;
+                for (int e = 0; e < 4; ++e) c[j][e] = 0.0f;
             }
             // the fragments' products side by side: those of one fragment wait for each other
 #pragma unroll
@@ -821,7 +831,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
                     for (int i = 0; i < 4; i += 2)
 #pragma unroll
                         for (int j = 0; j < kSub; ++j)
-                            mma16816(c[nt][j], x0[j][i], x1[j][i], x0[j][i + 1], x1[j][i + 1],
+                            mma16816(c[j], x0[j][i], x1[j][i], x0[j][i + 1], x1[j][i + 1],
                                      qb[nt][2 * g + m][i], qb[nt][2 * g + m][i + 1]);
             }
 #pragma unroll
@@ -831,9 +841,8 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
                 const float s = __uint_as_float(p << 16), z = __uint_as_float(p & 0xffff0000u);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float (&d)[4] = c[nt][i >> 1];
                     const float u = g == 0 ? z * qsum[nt][g] : fmaf(z, qsum[nt][g], lg[nt][i]);
-                    lg[nt][i] = fmaf(s, d[2 * (i & 1)] + d[2 * (i & 1) + 1], u);
+                    lg[nt][i] = fmaf(s, head_of<NT>(c[i >> 1], i & 1, nt), u);
                 }
             }
         }
@@ -883,17 +892,15 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
             const uint32_t ex = max(warp_max(vmax & 0xffffu) >> 7, 14u);
             const float down = __uint_as_float((267u - ex) << 23);
             const float up = __uint_as_float((ex - 3u) << 23);
-            float acc[NT][2][2][4];
+            float acc[2][2][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                mid_run[nt][g] *= corr[nt];
+            for (int nt = 0; nt < NT; ++nt) mid_run[nt][g] *= corr[nt];
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[nt][m][i][e] = 0.0f;
-            }
+                    for (int e = 0; e < 4; ++e) acc[m][i][e] = 0.0f;
 #pragma unroll
             for (int j = 0; j < kSub; ++j) {
                 uint32_t vw[4], x[4][4], wb[NT][2];
@@ -905,11 +912,19 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
                     float mid = __uint_as_float(p & 0xffff0000u);
                     if (half) mid = fmaf(15.0f, s, mid);
                     const float sd = half ? s * -down : s * down;
+                    float w[NT], lead[NT];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const float w = lg[nt][2 * j + half];
-                        mid_run[nt][g] = fmaf(w, mid, mid_run[nt][g]);
-                        wb[nt][half] = transpose8x8(split_f16(w * sd));
+                        const float u = lg[nt][2 * j + half];
+                        mid_run[nt][g] = fmaf(u, mid, mid_run[nt][g]);
+                        w[nt] = u * sd;
+                        lead[nt] = leading_bits(w[nt]);
+                    }
+                    if constexpr (NT == 1) {
+                        wb[0][half] = transpose8x8(pack_f16(lead[0], w[0] - lead[0]));
+                    } else {
+                        wb[0][half] = transpose8x8(pack_f16(lead[0], lead[1]));
+                        wb[1][half] = transpose8x8(pack_f16(w[0] - lead[0], w[1] - lead[1]));
                     }
                 }
 #pragma unroll
@@ -920,7 +935,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
-                            mma16816(acc[nt][m][i], x[m][2 * i], x[m][2 * i + 1], x[m + 2][2 * i],
+                            mma16816(acc[m][i], x[m][2 * i], x[m][2 * i + 1], x[m + 2][2 * i],
                                      x[m + 2][2 * i + 1], wb[nt][0], wb[nt][1]);
             }
             if (g == 1) {
@@ -935,8 +950,8 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float one = acc[nt][m][i][0] + acc[nt][m][i][1];
-                        const float two = fmaf(acc[nt][m][i][2] + acc[nt][m][i][3], 16384.0f, -one);
+                        const float one = head_of<NT>(acc[m][i], 0, nt);
+                        const float two = fmaf(head_of<NT>(acc[m][i], 1, nt), 16384.0f, -one);
                         float* o = &o_run[nt][2 * g + m][2 * i];
                         o[0] = fmaf(one, up, o[0] * corr[nt]);
                         o[1] = fmaf(two, up * 0.0625f, o[1] * corr[nt]);
@@ -956,7 +971,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
             mid_run[nt][0] += __shfl_xor_sync(0xffffffffu, mid_run[nt][0], o);
             mid_run[nt][1] += __shfl_xor_sync(0xffffffffu, mid_run[nt][1], o);
         }
-        float* dst = join + ((4 * nt + t) * kAttWarps + warp) * kMergePitch;
+        float* dst = join + ((NT * t + nt) * kAttWarps + warp) * kMergePitch;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const float mid = mid_run[nt][m >> 1];
