@@ -1132,7 +1132,9 @@ struct AttPlan {
 // TB/s whatever the layout; and 5.3, 6.2 and 8.7 us come on top, 4.0 where nothing is split. More
 // CTAs than the call needs lose: 8 heads of 96K tokens take 25.0 us in 152 CTAs, 23.3 in 280 and
 // 26.0 in 440. Sequences shorter than n (`ragged`) leave memory less to do, and a CTA of a later
-// wave goes where a short one has ended, but the CTAs of one wave wait for the longest.
+// wave goes where a short one has ended, but the CTAs of one wave wait for the longest. With NT = 2
+// (1.20 and 1.07 us) each wave more costs 2.5 us (20 sequences of up to 9000 tokens, 16 heads over 2:
+// 21.7 us in 720 CTAs, 19.5 in 240).
 AttPlan attention_plan(int B, int Hq, int Hkv, int n, bool ragged) {
     AttPlan p;
     const int G = Hq / Hkv;
@@ -1156,7 +1158,8 @@ AttPlan attention_plan(int B, int Hq, int Hkv, int n, bool ragged) {
         if (ragged && busy > resident) steps_there = 0.75 * steps_there + 0.25 * resident * each;
         const bool clustered = used > 1 && used <= kClusterSplits && busy <= resident;
         const double split_fixed[3] = {530.0, 620.0, 870.0};
-        const double fixed = used == 1 ? 400.0 : split_fixed[at_once - 1] - (clustered ? 40.0 : 0.0);
+        double fixed = used == 1 ? 400.0 : split_fixed[at_once - 1] - (clustered ? 40.0 : 0.0);
+        if (p.nt == 2) fixed += 250.0 * static_cast<double>((busy - 1) / at_once);
         const double compute = steps_there * step_cost[p.nt - 1][at_once - 1];
         const double cost = fixed + std::max(memory, compute);
         if (best < 0.0 || cost < best) {
