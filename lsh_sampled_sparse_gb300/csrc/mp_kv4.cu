@@ -476,8 +476,10 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const RowArgs a) 
 // With a key's codes c, step s and minimum z per group, q.k = sum_g s_g (sum_e q_e c_e) + z_g sum_e
 // q_e, and the value sum likewise: the products of codes with queries and of codes with weights
 // are matrix products of small exact integers, which the warp's tensor-core instruction m16n8k16
-// (fp16 in, fp32 sums) takes with the 16 tokens or 16 dims as its rows and four query heads as its
-// eight columns, each head as two fp16 halves (22 bits). Steps and minima join outside, in fp32.
+// (fp16 in, fp32 sums) takes with the 16 tokens or 16 dims as its rows and the query heads as its
+// eight columns, each number of theirs as two fp16 halves (22 bits): two columns a head (up to four
+// heads, NT = 1), or a column a head and two products (up to eight, NT = 2, over the same unpacked
+// codes). Steps and minima join outside, in fp32.
 // The tcgen05 instructions want 128 rows and operands unpacked into shared memory, where a byte of
 // codes would become four; here codes go from shared memory to fragments in registers, three
 // quarters of an instruction of unpacking a value.
@@ -640,7 +642,7 @@ __device__ __forceinline__ void values_of(const Query8& v, const A4Args& a, size
 //
 // Four query heads a KV head: 32 sequences x 8 heads x 32K tokens take 195 us (6.2 TB/s, bound by
 // memory), 1 x 8 x 96K 24.1 us, of which about 6 are the launch, the queries and the join. Eight:
-// 2 x 8 x 128K take 66.6 us (4.5 TB/s); there a tile's arithmetic (1600 instructions a warp) takes
+// 2 x 8 x 128K take 65.7 us (4.6 TB/s); there a tile's arithmetic (1400 instructions a warp) takes
 // longer than its bytes, at two CTAs an SM, for which the registers do. Like the other kernels here
 // it is launched as a dependent of what precedes it in the stream and waits for that before its
 // first access: queued calls follow each other 2 to 3 us sooner (1 x 8 x 96K 26.7 -> 23.7 us).
