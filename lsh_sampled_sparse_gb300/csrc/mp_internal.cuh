@@ -376,7 +376,8 @@ __device__ inline float log_inclusion_cos(float c, int K, int L) {
 //   log u = c0 + 2 K g + (L - 2) log1p(-x) + log(1 + sum_{j>=3} t_j / t_2),
 //   c0 = log(L (L - 1) / 2) - 2 K log 2, rounded once,
 // with ten terms of the sum (the rest is under 3e-8) from ratio[i] = (L - j) / (j + 1), j = 2 + i;
-// above it u is 0.44 or more and needs no care. For |c| <= 1/2, g(c) / c is the interpolant of
+// above it log(1 - e^{L log1p(-x)} (1 + L x / (1 - x))), u being 0.44 or more. The two share their
+// logarithm: a warp's keys lie on both sides. For |c| <= 1/2, g(c) / c is the interpolant of
 // degree 11 at the Chebyshev nodes of that interval (off by 2e-8 relative). A cosine below -1/2,
 // where 1 + 2 asin(c) / pi loses bits, takes the form above: no key is likely to be sampled there.
 struct FineLogU {
@@ -410,14 +411,11 @@ __device__ __forceinline__ float log_inclusion_fine(float c, const FineLogU& f) 
         g = log1pf(0.63661977236758134f * asinf(c));
     }
     const float kg = static_cast<float>(f.K) * g, Lf = static_cast<float>(f.L);
-    const float x = __expf(kg) * f.unit, lam = Lf * x;
+    const float x = __expf(kg) * f.unit;
     if (x >= 1.0f) return 0.0f;
-    float l1;                                    // log1p(-x); x < 0.03 where L >= 50 and it counts
-    if (f.L >= 50 && lam < 1.5f)
-        l1 = -x * fmaf(x, fmaf(x, fmaf(x, fmaf(x, 0.2f, 0.25f), 0.333333333f), 0.5f), 1.0f);
-    else
-        l1 = log1pf(-x);
-    if (lam >= 1.5f) return logf(-expm1f(Lf * l1) - lam * expf((Lf - 1.0f) * l1));
+    const float l1 = x < 0.03f
+        ? -x * fmaf(x, fmaf(x, fmaf(x, fmaf(x, 0.2f, 0.25f), 0.333333333f), 0.5f), 1.0f)
+        : log1pf(-x);
     const float r = __fdividef(x, 1.0f - x);
     float sum = 0.0f;
 #pragma unroll
@@ -425,7 +423,10 @@ __device__ __forceinline__ float log_inclusion_fine(float c, const FineLogU& f) 
         const float t = f.ratio[i] * r;
         sum = fmaf(sum, t, t);
     }
-    return f.c0 + (2.0f * kg + ((Lf - 2.0f) * l1 + logf(1.0f + sum)));
+    const float none_or_one = __expf(Lf * l1) * fmaf(Lf, r, 1.0f);
+    const bool few = Lf * x < 1.5f;
+    const float log_rest = logf(few ? 1.0f + sum : 1.0f - none_or_one);
+    return few ? f.c0 + (2.0f * kg + ((Lf - 2.0f) * l1 + log_rest)) : log_rest;
 }
 
 // The attend kernel's log u for SimHash keys: linear interpolation in a per-call table of the
