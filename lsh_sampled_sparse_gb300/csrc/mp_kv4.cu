@@ -828,7 +828,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
                     unpack_pairs(kw[j][m + 2], x1[j]);
                 }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = NT - 1; nt >= 0; --nt)
 #pragma unroll
                     for (int i = 0; i < 4; i += 2)
 #pragma unroll
@@ -932,7 +932,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) unpack_pairs(i < 2 ? vw[i] : ~vw[i], x[i]);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = NT - 1; nt >= 0; --nt)             // the rests first: they round less
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
