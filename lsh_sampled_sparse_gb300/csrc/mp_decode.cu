@@ -1276,11 +1276,12 @@ cudaError_t launch_attend(const void* q, bool q_bf16, const float* centre, const
     aa.radius = s.radius;
     aa.scale = s.scale;
     aa.work_bytes = static_cast<int>(attend_smem(kv.form).work);
-    // While the GPU holds more CTAs than there are (six an SM), a CTA with more rows than twice
-    // its slots shares them with up to seven others: of keys without a bias toward the query a share of
-    // 1 - (1 + x) e^-x collides twice, x = L times the chance in one table. 16 query heads, 3200 keys,
-    // (7, 195): 144 -> 35 us; with few rows a cluster's start and join cost 1 us more than they save.
-    // Only over the 4-bit cache: the other forms' sums keep their order.
+    // While the GPU holds more CTAs than there are (six an SM), a CTA with more rows than twice its
+    // slots shares them with up to seven others: of keys without a bias toward the query a share of
+    // 1 - (1 + x) e^-x collides twice, x = L times the chance in one table. 16 query heads, 3194
+    // keys, (7, 195): 144 us with neither this nor the whole list, 35 us with both; with few rows a
+    // cluster's start and join cost 1 us more than they save. Only over the 4-bit cache: the other
+    // forms' sums keep their order.
     const long long ctas = static_cast<long long>(s.B) * s.Hq * (aa.nsb + 1);
     const double x = s.L * (s.cp ? 0.5 / kD : ldexp(1.0, -s.K));
     const int keys = std::min(s.n, kAttendBlocks * kKeysPerBlock);

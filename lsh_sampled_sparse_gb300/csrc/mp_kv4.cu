@@ -642,7 +642,7 @@ __device__ __forceinline__ void values_of(const Query8& v, const A4Args& a, size
 //
 // Four query heads a KV head: 32 sequences x 8 heads x 32K tokens take 195 us (6.2 TB/s, bound by
 // memory), 1 x 8 x 96K 24.1 us, of which about 6 are the launch, the queries and the join. Eight:
-// 2 x 8 x 128K take 65.7 us (4.6 TB/s); there a tile's arithmetic (1400 instructions a warp) takes
+// 2 x 8 x 128K take 66 us (4.6 TB/s); there a tile's arithmetic (1400 instructions a warp) takes
 // longer than its bytes, at two CTAs an SM, for which the registers do. Like the other kernels here
 // it is launched as a dependent of what precedes it in the stream and waits for that before its
 // first access: queued calls follow each other 2 to 3 us sooner (1 x 8 x 96K 26.7 -> 23.7 us).
