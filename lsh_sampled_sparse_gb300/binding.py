@@ -286,18 +286,26 @@ def encode_rows(keys, centre, W, K: int, L: int, n_begin: int, n_capacity: int, 
     (allocated, all zero, where they are None). The bits of other keys are kept."""
     _cuda(keys, "keys", 4)
     B, Hkv, m, d = keys.shape
+    device = keys.get_device()
+    if device != torch._C._cuda_getDevice():
+        raise ValueError(f"keys are on cuda:{device}, which is not the current device")
     if not 0 <= n_begin <= n_capacity - m or n_capacity >> 31:
         raise ValueError(f"{m} keys from {n_begin} on do not fit {n_capacity}")
     nbytes = codes_bytes(B, Hkv, n_capacity, K, L)
     if codes is None:
-        codes = torch.zeros(max(nbytes // 4, 4), dtype=torch.int32, device=keys.device)
-    _cuda(codes, "codes")
+        codes = _empty((max(nbytes // 4, 4),), torch.int32, keys.device, stream)
+        with torch.cuda.stream(stream):          # None: the current one
+            codes.zero_()
+    for t, name in ((codes, "codes"), (centre, "centre"), (W, "W")):
+        _cuda(t, name)
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}, the keys on cuda:{device}")
     if _nbytes(codes) < nbytes:
         raise ValueError("codes buffer too small for the capacity")
-    _cuda(centre, "centre", 3)
-    _cuda(W, "W", 2)
     if tuple(centre.shape) != (B, Hkv, d) or tuple(W.shape) != (d, K * L):
         raise ValueError(f"centre {tuple(centre.shape)} or W {tuple(W.shape)} does not fit the keys")
+    if centre.dtype is not torch.float32:
+        raise TypeError(f"centre must be float32, is {centre.dtype}")
     _check(lib().mp_encode_rows(_ptr(keys), _dtype(keys, "keys"), _ptr(centre), _ptr(W),
                                 _dtype(W, "W"), B, Hkv, m, n_capacity, n_begin, d, K, L,
                                 _ptr(codes), _stream(stream)), "mp_encode_rows")

@@ -765,6 +765,15 @@ def test_a_run_without_a_full_precision_cache(mp):
     differ = _code_bits(mp, codes, B, Hkv, cap, C)[:, :, :n] \
         != _code_bits(mp, one, B, Hkv, blocks * 1024, C)[:, :, :n]
     assert differ.double().mean() < 1e-5                     # signs that float32 cannot tell
+    side = torch.cuda.Stream()                               # codes made and written there
+    side.wait_stream(torch.cuda.current_stream())
+    there = mp.encode_rows(prompt, centre, W, wl.K, wl.L, 0, cap, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(there, mp.encode_rows(prompt, centre, W, wl.K, wl.L, 0, cap))
+    with pytest.raises(TypeError):
+        mp.encode_rows(prompt, centre.to(BF), W, wl.K, wl.L, 0, cap)
+    with pytest.raises(TypeError):
+        mp.encode_rows(prompt, centre, W.cpu(), wl.K, wl.L, 0, cap)
     with pytest.raises(ValueError):
         mp.encode_rows(prompt, centre, W, wl.K, wl.L, cap - n0 + 1, cap)
     with pytest.raises(ValueError):
