@@ -567,10 +567,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// The largest of a warp's unsigned numbers
-__device__ __forceinline__ uint32_t warp_max(uint32_t x) {
-    return __reduce_max_sync(0xffffffffu, x);
-}
 
 // Eight codes of a word as four fp16 pairs: with c0 .. c3 the codes of its low half and c4 .. c7 of
 // its high half, the pairs are (c0, c4) 2^-10, (c0 + 16 c1, c4 + 16 c5) 2^-24 and the same of c2, c3,
@@ -784,11 +780,11 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
     }
 
     // running maximum of the logits as the products leave them, the same times fac
-    float m_run[NT], base_run[NT], l_run[NT], mid_run[NT][2], o_run[NT][4][4];
+    float m_run[NT], base_run[NT], l_run[NT], mid_run[NT][2], o_run[NT][4][4], top[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         m_run[nt] = base_run[nt] = -INFINITY;
-        l_run[nt] = mid_run[nt][0] = mid_run[nt][1] = 0.0f;
+        l_run[nt] = mid_run[nt][0] = mid_run[nt][1] = top[nt][0] = top[nt][1] = 0.0f;
 #pragma unroll
         for (int m = 0; m < 4; ++m)
 #pragma unroll
@@ -880,20 +876,60 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
         }
 
         // ---- weighted codes of the tile, a group at a time. Weights times steps become fp16
-        // halves after a power of two brings the tile's largest step to [2^13, 2^14): 2^(140 - ex),
-        // taken back by 2^(ex - 140), with the 2^-10 of the codes. A step that is NaN is the
-        // largest of all; its group is NaN in every head anyhow.
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            uint32_t pw[2 * kSub], vmax = 0u;
+        // halves, scaled by a power of two, 2^(138 - ex), which brings the head's largest product so
+        // far (`top`, in units of the present base) to [2^11, 2^12); 2^(ex - 138) takes it back,
+        // with the 2^-10 of the codes. Where a step exceeds 8 top, which its weight may undo, the
+        // tile's own products are looked at: a head's tokens are held to 2^-36 of a product that
+        // its sum contains, whatever the steps of tokens without weight and other heads' weights.
+        // (By the tile's largest step alone a token of no weight, 2^34 times larger than the rest,
+        // moved outputs by 3%.) NaN is not the largest of anything and goes through.
+        {
+            uint32_t vmax[2] = {0u, 0u};
 #pragma unroll
             for (int i = 0; i < 2 * kSub; ++i) {
-                pw[i] = *reinterpret_cast<const uint32_t*>(prm + 8 * i * kParamBytes + 8 + 4 * g);
-                vmax = __vmaxu2(vmax, pw[i]);
+                const uint2 p = *reinterpret_cast<const uint2*>(prm + 8 * i * kParamBytes + 8);
+                vmax[0] = __vmaxu2(vmax[0], p.x);
+                vmax[1] = __vmaxu2(vmax[1], p.y);
             }
-            const uint32_t ex = max(warp_max(vmax & 0xffffu) >> 7, 14u);
-            const float down = __uint_as_float((267u - ex) << 23);
-            const float up = __uint_as_float((ex - 3u) << 23);
+            bool above = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    top[nt][g] *= corr[nt];
+                    above = above || !(__uint_as_float(vmax[g] << 16) <= 8.0f * top[nt][g]);
+                }
+            if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int i = 0; i < 2 * kSub; ++i) {
+                        const uint2 p =
+                            *reinterpret_cast<const uint2*>(prm + 8 * i * kParamBytes + 8);
+                        top[nt][0] = fmaxf(top[nt][0], lg[nt][i] * __uint_as_float(p.x << 16));
+                        top[nt][1] = fmaxf(top[nt][1], lg[nt][i] * __uint_as_float(p.y << 16));
+                    }
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) {
+                        top[nt][0] = fmaxf(top[nt][0], __shfl_xor_sync(0xffffffffu, top[nt][0], o));
+                        top[nt][1] = fmaxf(top[nt][1], __shfl_xor_sync(0xffffffffu, top[nt][1], o));
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            uint32_t pw[2 * kSub];
+#pragma unroll
+            for (int i = 0; i < 2 * kSub; ++i)
+                pw[i] = *reinterpret_cast<const uint32_t*>(prm + 8 * i * kParamBytes + 8 + 4 * g);
+            float down[NT], up[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint32_t ex = max(__float_as_uint(top[nt][g]) >> 23, 14u);
+                down[nt] = __uint_as_float((265u - ex) << 23);
+                up[nt] = __uint_as_float((ex - 1u) << 23);
+            }
             float acc[2][2][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mid_run[nt][g] *= corr[nt];
@@ -913,13 +949,12 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
                     const float s = __uint_as_float(p << 16);
                     float mid = __uint_as_float(p & 0xffff0000u);
                     if (half) mid = fmaf(15.0f, s, mid);
-                    const float sd = half ? s * -down : s * down;
                     float w[NT], lead[NT];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const float u = lg[nt][2 * j + half];
                         mid_run[nt][g] = fmaf(u, mid, mid_run[nt][g]);
-                        w[nt] = u * sd;
+                        w[nt] = u * s * (half ? -down[nt] : down[nt]);
                         lead[nt] = leading_bits(w[nt]);
                     }
                     if constexpr (NT == 1) {
@@ -955,8 +990,8 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
                         const float one = head_of<NT>(acc[m][i], 0, nt);
                         const float two = fmaf(head_of<NT>(acc[m][i], 1, nt), 16384.0f, -one);
                         float* o = &o_run[nt][2 * g + m][2 * i];
-                        o[0] = fmaf(one, up, o[0] * corr[nt]);
-                        o[1] = fmaf(two, up * 0.0625f, o[1] * corr[nt]);
+                        o[0] = fmaf(one, up[nt], o[0] * corr[nt]);
+                        o[1] = fmaf(two, up[nt] * 0.0625f, o[1] * corr[nt]);
                     }
         }
     }
