@@ -389,10 +389,13 @@ MP_API size_t mp_kv4_attention_workspace_bytes(int B, int Hq, int Hkv, int n, in
  *   out[b][h] = sum_i w_i v_i / sum_i w_i,   w_i = exp(scale q.k_i),   i < length_b
  * with the values that the cache holds; length_b = n, or lengths[b] ([B] int32 on the device,
  * taken into [0, n]). A sequence of length 0 gets zero rows. Any Hq that Hkv divides.
- * scale 0 means 1/sqrt(d). Scores, softmax and sums are float32: codes and the two fp16 halves of
- * a query element or a weight (22 bits) meet in exact tensor-core products. A NaN or an infinity
- * in a query gives NaN in its output row (so may an element of 2^121 or more); one that the cache
- * holds gives NaN to the rows that attend to it (in a value: to its 64 dims).
+ * scale 0 means 1/sqrt(d). Scores, softmax and sums are float32: codes and the two fp16 halves of a
+ * query element or a weight (22 bits) meet in exact tensor-core products. An element of a query
+ * enters within 2^-22 of itself and 2^-25 of the largest of its row. Sums over tokens take weights
+ * of up to 1 each, before the division: they may overflow where the largest value attended to,
+ * whatever its weight, times the tokens passes 2^126; so may scores where a key passes 2^124. A NaN
+ * or an infinity in a query gives NaN in its output row (so may an element of 2^121 or more); one
+ * that the cache holds gives NaN to the rows that attend to it (in a value: to its 64 dims).
  * Errors: MP_ERR_INVALID_ARG (shapes, n > n_capacity or 2^30, B Hq > 2^22, Hq % Hkv, a scale that is
  * negative, infinite or NaN, null, misalignment: out 16 bytes, lengths 4, workspace 256),
  * MP_ERR_UNSUPPORTED (d != 128), MP_ERR_WORKSPACE. */

@@ -18,7 +18,7 @@ def mp():
     return mp
 
 
-def _weighted64(q, cache, scale):
+def _weighted64(q, cache, scale, held=0.0):
     """softmax(scale q.k) . v in 64 bits and the error [B, Hq, 128] that a float32 evaluation may
     have of it, by the weights w_i: with V_i the largest value of token i in a dim's group and V the
     mean of V_i under the weights,
@@ -29,7 +29,8 @@ def _weighted64(q, cache, scale):
     about sqrt(128) = 11.3 roundings of up to 2 2^-24 A_i (32 leaves a factor of 1.4), and by the
     rounding of its distance D_i from the largest logit; the exponential adds 4. A weight that is
     off by e_i moves the output by w_i e_i (v_i - out). The sums over n tokens add a random walk of
-    sqrt(n) roundings of 2 2^-24, in numerator and denominator."""
+    sqrt(n) roundings of 2 2^-24, in numerator and denominator. `held`: what a query's elements may be
+    off by, as a share of the row's largest, besides 2^-22 of themselves (counted if it is not 0)."""
     k, v = R.values64(cache[0], cache[2], 0), R.values64(cache[1], cache[2], 1)
     B, Hq, _ = q.shape
     G = Hq // k.shape[1]
@@ -42,6 +43,9 @@ def _weighted64(q, cache, scale):
     D = s.amax(-1, keepdim=True) - s
     big = v.abs().unflatten(-1, (2, 64)).amax(-1)                        # [B, Hq, n, 2]
     mean = (w.unsqueeze(-1) * big).sum(2, keepdim=True)
+    if held:
+        A = A + scale / (32 * e) * (k.abs() @ (2.0 ** -22 * qd.abs()
+                                               + held * qd.abs().amax(-2, keepdim=True))).squeeze(-1)
     tol = (w.unsqueeze(-1) * e * (32 * A + 2 * D + 4).unsqueeze(-1) * (big + mean)).sum(2) \
         + e * (4 * n ** 0.5 + 16) * mean.squeeze(2)
     return (w.unsqueeze(2) @ v).squeeze(2), tol.repeat_interleave(64, -1)
@@ -92,3 +96,50 @@ def test_heads_of_one_tile_do_not_share_a_scale(mp, G):
     for out in (mp.kv4_attention(q, cache), mp.kv4_attention(q, cache, lengths=lengths)):
         off = (out.double() - want).abs()
         assert (off <= tol).all(), float((off / tol).max())
+
+
+@pytest.mark.parametrize("G", [1, 4, 8])
+@pytest.mark.parametrize("at", [3, 12])
+@pytest.mark.parametrize("ends", [(0.0, 2.0 ** 126), (-2.0 ** 126, 2.0 ** 126), (-2.0 ** 126, 0.0)])
+def test_values_of_the_documented_size(mp, G, at, ends):
+    """Values up to 2^126 in size, whose codes the sums take in 15 steps at once: without weight they
+    cost the others nothing; with all the weight (the last head) they come out."""
+    n = 40
+    q, keys, values, _ = _opposed(mp, 1, 2, G, n, at, 20.0, seed=60 + G)
+    values[:, :, at, :64] = torch.linspace(*ends, 64, device="cuda")
+    cache = mp.kv4_write(mp.kv4_cache(1, 2, n), keys, values)
+    assert torch.isfinite(cache.params.float()).all()
+    out = mp.kv4_attention(q, cache)
+    want, tol = _weighted64(q, cache, 128 ** -0.5)
+    assert ((out.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("ratio", [2.0 ** 6, 2.0 ** 12, 2.0 ** 18])
+@pytest.mark.parametrize("G", [1, 4, 8])
+def test_queries_and_keys_of_opposite_sizes(mp, G, ratio):
+    """The small elements of a query meet the large ones of the keys and the other way round: an
+    element is held to 2^-25 of its row's largest, as the header says."""
+    n = 300
+    g = torch.Generator(device="cuda")
+    g.manual_seed(80 + G)
+    q = torch.randn(1, 2 * G, 128, generator=g, device="cuda")
+    keys = torch.randn(1, 2, n, 128, generator=g, device="cuda")
+    values = torch.randn(1, 2, n, 128, generator=g, device="cuda")
+    q[..., 64:] /= ratio
+    keys[..., 64:] *= ratio
+    cache = mp.kv4_write(mp.kv4_cache(1, 2, n), keys, values)
+    want, tol = _weighted64(q, cache, 128 ** -0.5, held=2.0 ** -25)
+    assert ((mp.kv4_attention(q, cache).double() - want).abs() <= tol).all()
+
+
+def test_keys_up_to_the_documented_size(mp):
+    n = 70
+    g = torch.Generator(device="cuda")
+    g.manual_seed(90)
+    keys = torch.randn(1, 2, n, 128, generator=g, device="cuda")
+    keys = keys / keys.abs().max() * 2.0 ** 124
+    values = torch.randn(1, 2, n, 128, generator=g, device="cuda")
+    q = torch.randn(1, 8, 128, generator=g, device="cuda") * 2.0 ** -121
+    cache = mp.kv4_write(mp.kv4_cache(1, 2, n), keys, values)
+    want, tol = _weighted64(q, cache, 128 ** -0.5)
+    assert ((mp.kv4_attention(q, cache).double() - want).abs() <= tol).all()
