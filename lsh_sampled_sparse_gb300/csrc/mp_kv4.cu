@@ -6,6 +6,10 @@
 // bf16 with z + 15 s >= max x, and codes c_e = rint((x_e - z) / s), so |x_e - (z + s c_e)| <= s / 2.
 // 15 s is exact in float32 (8 + 4 bits), so that it reaches max - z exactly where it reaches that
 // difference rounded up.
+//
+// The kernels are launched as dependents of what precedes them in the stream: their lives begin
+// before it has written what they read. So no load here is a non-coherent one, which would promise
+// that nobody writes its memory meanwhile; ordinary loads stay behind the wait.
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -227,7 +231,7 @@ __device__ __forceinline__ RowAt row_at(const RowArgs& a, uint32_t blk) {
         i = w.r - w.bh * a.m;
     }
     const long long pos =
-        static_cast<long long>(a.positions ? __ldg(a.positions + w.bh / a.Hkv) : a.n_begin) + i;
+        static_cast<long long>(a.positions ? a.positions[w.bh / a.Hkv] : a.n_begin) + i;
     w.row = r < a.rows && pos >= 0 && pos < a.ncap
                 ? static_cast<long long>(w.bh) * a.ncap + pos : -1;
     return w;
@@ -242,14 +246,14 @@ __device__ __forceinline__ long long cache_rows(const RowArgs& a) {
 template <bool kWide>
 __device__ __forceinline__ void load32(const void* p, uint32_t* w) {
     if constexpr (kWide) {
-        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
                        "=r"(w[6]), "=r"(w[7])
                      : "l"(p));
     } else {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const uint4 v = __ldg(static_cast<const uint4*>(p) + i);
+            const uint4 v = static_cast<const uint4*>(p)[i];
             w[4 * i] = v.x;
             w[4 * i + 1] = v.y;
             w[4 * i + 2] = v.z;
@@ -367,7 +371,7 @@ __global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 && kLanes == 8 ? 3
                 a.centre + static_cast<size_t>(now.bh) * kD + kDims * rl);
 #pragma unroll
             for (int j = 0; j < kPairs / 2; ++j) {
-                const float4 c = __ldg(mu + j);
+                const float4 c = mu[j];
                 x[2 * j] = fma2(pack2(c.x, c.y), minus, x[2 * j]);       // k - c, one rounding
                 x[2 * j + 1] = fma2(pack2(c.z, c.w), minus, x[2 * j + 1]);
             }
@@ -430,11 +434,11 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const RowArgs a) 
         kc = vc = make_uint2(0u, 0u);
         kp = vp = 0u;
         if (row >= 0 && mp_check(a.status, row, cache_rows(a), kSiteKv4Row)) {
-            kc = __ldg(reinterpret_cast<const uint2*>(a.k_codes + row * kCodeBytes + 8 * rl));
-            vc = __ldg(reinterpret_cast<const uint2*>(a.v_codes + row * kCodeBytes + 8 * rl));
+            kc = *reinterpret_cast<const uint2*>(a.k_codes + row * kCodeBytes + 8 * rl);
+            vc = *reinterpret_cast<const uint2*>(a.v_codes + row * kCodeBytes + 8 * rl);
             const uint32_t* p = reinterpret_cast<const uint32_t*>(a.params + row * 16) + (rl >> 2);
-            kp = __ldg(p);
-            vp = __ldg(p + 2);
+            kp = p[0];
+            vp = p[2];
         }
     };
     wait_for_predecessor();
@@ -454,7 +458,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const RowArgs a) 
                 a.centre + static_cast<size_t>(now.bh) * kD + 16 * rl);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float4 c = __ldg(mu + i);
+                const float4 c = mu[i];
                 k[4 * i] = __fadd_rn(k[4 * i], c.x);
                 k[4 * i + 1] = __fadd_rn(k[4 * i + 1], c.y);
                 k[4 * i + 2] = __fadd_rn(k[4 * i + 2], c.z);
@@ -611,11 +615,11 @@ __device__ __forceinline__ Query8 load_query8(const A4Args& a, size_t i, bool li
     v.a = v.b = make_uint4(0u, 0u, 0u, 0u);
     if (live && a.q_wide) {
         if (a.q_bf16) {
-            v.a = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + i));
+            v.a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + i);
         } else {
             const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + i);
-            v.a = __ldg(p);
-            v.b = __ldg(p + 1);
+            v.a = p[0];
+            v.b = p[1];
         }
     }
     return v;
@@ -661,7 +665,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
     // the merge may start. Without one the dependent is another call, whose CTAs would take the
     // places of this one's that end first (4 x 8 heads of 16K tokens 18.5 -> 22.2 us)
     if (a.splits > 1 && !a.cluster) allow_dependents();
-    const int len = a.lengths ? max(0, min(a.n, __ldg(a.lengths + b))) : a.n;
+    const int len = a.lengths ? max(0, min(a.n, a.lengths[b])) : a.n;
     const int tile0 = split * a.tiles_per_split;
     const long long split_end = static_cast<long long>(tile0 + a.tiles_per_split) * kTile;
     int end = static_cast<int>(min(static_cast<long long>(len), split_end));     // tokens [.., end)
