@@ -515,17 +515,19 @@ MP_API mp_status mp_decode_attention_noalloc(const void* q, mp_dtype q_dtype,
 MP_API mp_status mp_device_status(int* status);
 
 /* The MP_CHECKS build (the library compiled with -DMP_CHECKS=1, libmagicpig_checks.so): every
- * kernel of the decode path, the bucketed lookup, the tensor-core encoder and the 4-bit cache check
- * the indices of their global accesses (code blocks, selection words, K/V rows, partial states,
- * bucket ranges and members, code words written) and skip an access that is out of range instead of
- * making it, raising MP_ERR_BOUNDS in the status word. A stand-in for a memory checker: the paper has
- * no counterpart. Synchronises the device and returns through *enabled 1 in that build, 0 in the
- * product build, and through *site the site of the first failed check since the status word was
- * last reset (0 if none): 1 query encoding stores, 2 scanned code block, 3 selection words
- * written, 4 K/V row copied, 5 partial state or output written, 6 selection words read,
- * 7 bucket range beyond the table's keys, 8 bucket member beyond n_indexed, 9 code words written
- * by the encoder, 10 a row of the 4-bit cache, 11 rows read back from it, partial states and output
- * rows of its attention. Neither word is reset. Errors: MP_ERR_INVALID_ARG (null), MP_ERR_CUDA. */
+ * kernel of the decode path, the bucketed lookup, the tensor-core encoder, the CUDA-core encoders
+ * of mp_encode_keys and mp_encode_rows and the 4-bit cache check the indices of their global
+ * accesses (code blocks, selection words, K/V rows, partial states, bucket ranges and members, code
+ * words written) and skip an access that is out of range instead of making it, raising
+ * MP_ERR_BOUNDS in the status word. A stand-in for a memory checker: the paper has no counterpart.
+ * Synchronises the device and returns through *enabled 1 in that build, 0 in the product build, and
+ * through *site the site of the first failed check since the status word was last reset (0 if
+ * none): 1 query encoding stores, 2 scanned code block, 3 selection words written, 4 K/V row
+ * copied, 5 partial state or output written, 6 selection words read, 7 bucket range beyond the
+ * table's keys, 8 bucket member beyond n_indexed, 9 code words written by the encoders, 10 a row of
+ * the 4-bit cache, 11 rows read back from it, partial states and output rows of its attention, 12 a
+ * key row that a CUDA-core encoder reads, 13 the list of an attend CTA's selected keys. Neither
+ * word is reset. Errors: MP_ERR_INVALID_ARG (null), MP_ERR_CUDA. */
 MP_API mp_status mp_debug_check_report(int* enabled, int* site);
 
 #ifdef __cplusplus

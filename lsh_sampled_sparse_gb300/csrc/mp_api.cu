@@ -340,17 +340,18 @@ mp_status mp_encode_rows(const void* keys, mp_dtype key_dtype, const float* cent
                             : std::min(m - row, kKeysPerBlock - at);
         const void* k = static_cast<const char*>(keys) +
                         static_cast<size_t>(row) * kD * (kbf ? 2 : 4);
-        uint32_t* to = codes + static_cast<size_t>(pos / kKeysPerBlock) * K * L * kWordsPerBlock;
+        const int to_blk = pos / kKeysPerBlock;
         const bool few = n <= kAppendMaxKeys;
         cudaError_t e = cudaErrorNotSupported;
         if (kbf && wbf && !few)
             e = launch_encode_tc(k, centre, W, B, Hkv, whole ? n : at + n, 0,
-                                 whole ? n / kKeysPerBlock : 1, K, L, to, device_status_ptr(),
-                                 stream, nullptr, nullptr, false, m, cblk, whole ? -1 : at);
+                                 whole ? n / kKeysPerBlock : 1, K, L, codes, device_status_ptr(),
+                                 stream, nullptr, nullptr, false, m, cblk, to_blk,
+                                 whole ? -1 : at);
         if (e == cudaErrorNotSupported) {
             cudaGetLastError();
             e = whole ? launch_encode_simt(k, kbf, centre, W, wbf, B, Hkv, n, 0,
-                                           n / kKeysPerBlock, K, L, to, stream, m, cblk)
+                                           n / kKeysPerBlock, K, L, codes, stream, m, cblk, to_blk)
                       : (few ? launch_encode_append : launch_encode_part)(
                             keys, kbf, centre, W, wbf, B, Hkv, m, row, n_capacity, pos, pos + n, K,
                             L, codes, stream);

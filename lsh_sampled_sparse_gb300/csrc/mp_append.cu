@@ -25,7 +25,7 @@ constexpr int kAppendKeysAtOnce = 4;                           // independent su
 __global__ void __launch_bounds__(kAppendThreads)
     encode_append_kernel(const void* keys, int keys_bf16, const float* centre, const void* W,
                          int w_bf16, int head_rows, int row0, int n0, int n1, int C, int cblk,
-                         uint32_t* codes) {
+                         uint32_t* codes, int* status) {
     extern __shared__ __align__(16) float sm[];
     float* Ws = sm;                                   // [kD][kAppendPlanes]
     float* kbar = sm + kD * kAppendPlanes;            // [n1 - n0][kD]
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kAppendThreads)
 #pragma unroll
         for (int u = 0; u < kStageBatch; ++u) {
             const int idx = base + u * kAppendThreads + tid;
-            v[u] = idx < m * kD
+            v[u] = idx < m * kD && mp_check(status, row0 + idx / kD, head_rows, kSiteEncodeRow)
                        ? load_elem(keys, keys_bf16,
                                    (static_cast<size_t>(bh) * head_rows + row0 + idx / kD) * kD +
                                        idx % kD) -
@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(kAppendThreads)
     const uint32_t range = bits_below(k1 - w * 32) & ~bits_below(k0 - w * 32);
     uint32_t* dst = codes + ((static_cast<size_t>(bh) * cblk + w / kWordsPerBlock) * C + j) *
                                 kWordsPerBlock + w % kWordsPerBlock;
-    *dst = (*dst & ~range) | bits;
+    if (mp_check(status, w / kWordsPerBlock, cblk, kSiteEncodeCodes))
+        *dst = (*dst & ~range) | bits;
 }
 
 }  // namespace
@@ -109,7 +110,8 @@ cudaError_t launch_encode_append(const void* keys, bool keys_bf16, const float* 
                          static_cast<size_t>(n1 - n0) * kD) * sizeof(float);
     const dim3 grid((C + kAppendPlanes - 1) / kAppendPlanes, B * Hkv);
     encode_append_kernel<<<grid, kAppendThreads, smem, st>>>(
-        keys, keys_bf16, centre, W, w_bf16, head_rows, row0, n0, n1, C, cblk, codes);
+        keys, keys_bf16, centre, W, w_bf16, head_rows, row0, n0, n1, C, cblk, codes,
+        device_status_ptr());
     return cudaGetLastError();
 }
 

@@ -661,7 +661,8 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
         for (int w = 0; w < warp; ++w) before += misc[w];
         if constexpr (KV == kKv4) {
             for (int i = before + incl - c; U; U &= U - 1u, ++i)
-                if ((i & ((1 << share) - 1)) == rank)
+                if ((i & ((1 << share) - 1)) == rank &&
+                    mp_check(a.status, i >> share, kWords * 32, kSiteAttendList))
                     rowlist[i >> share] = static_cast<uint16_t>(tid * 32 + __ffs(U) - 1);
         } else {
             wpre[tid] = before + incl - c;

@@ -93,6 +93,7 @@ struct EncodeArgs {
     int C, nchunk, nblk, n, units, parts;
     int blk0;                       // first block encoded; a unit's block is blk0 + u % nblk
     int cblk;                       // code blocks per head in memory (the codes' head stride)
+    int code_blk;                   // the block of codes that block 0 of the keys goes to
     int lo;                         // kPart: keys [lo, n) of the block, the map's first row is lo
     // MIPS variant only: |k_i - mu| per key [BH][n] and r per head [BH]
     const float* norms;
@@ -533,15 +534,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the argmax codes, its Nc / d table rows of 1024 code bytes
         uint8_t* stg_bytes = reinterpret_cast<uint8_t*>(stg);
         auto store_unit = [&](int bg, int blk) {
-            const bool in_range =
-                mp_check(a.status, static_cast<long long>(bg) * a.cblk + a.blk0 + blk,
-                         static_cast<long long>(a.units / a.nblk) * a.cblk, kSiteEncodeCodes);
+            const int to_blk = a.code_blk + a.blk0 + blk;
+            const bool in_range = mp_check(a.status, to_blk, a.cblk, kSiteEncodeCodes) &&
+                                  mp_check(a.status, bg, a.units / a.nblk, kSiteEncodeCodes);
             if constexpr (kMode == kArgmax) {
                 epi_sync();
                 if (!aborted && in_range) {
                     const int ntab = Nc / kD, L = a.C / kD;
                     uint8_t* dst = reinterpret_cast<uint8_t*>(a.codes) +
-                                   ((static_cast<size_t>(bg) * a.cblk + a.blk0 + blk) * L + j0 / kD) *
+                                   ((static_cast<size_t>(bg) * a.cblk + to_blk) * L + j0 / kD) *
                                        kKeysPerBlock;
                     if (et < ntab * (kKeysPerBlock / 4))
                         reinterpret_cast<uint32_t*>(dst)[et] =
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // column group alone, so those four store them, between barriers of their own
                 group_sync(ew >> 2);
                 if (!aborted && in_range) {
-                    uint32_t* dst = a.codes + (static_cast<size_t>(bg) * a.cblk + a.blk0 + blk) *
+                    uint32_t* dst = a.codes + (static_cast<size_t>(bg) * a.cblk + to_blk) *
                                                   static_cast<size_t>(a.C) * kWordsPerBlock +
                                     static_cast<size_t>(j0) * kWordsPerBlock;
                     // four rows per warp instruction: lane l takes words 4 (l % 8) .. + 3 of
@@ -754,7 +755,8 @@ cudaError_t prepare_encode_tc() {
 cudaError_t launch_encode_tc(const void* keys, const float* centre, const void* W, int B,
                              int Hkv, int ncap, int blk0, int blk1, int K, int L,
                              uint32_t* codes, int* status, cudaStream_t st, const float* norms,
-                             const float* radius, bool argmax, int head_rows, int cblk, int lo) {
+                             const float* radius, bool argmax, int head_rows, int cblk,
+                             int code_blk, int lo) {
     const int C = K * L;
     if (C == 0 || blk1 <= blk0) return cudaSuccess;
     if (lo >= 0 && (blk0 != 0 || blk1 != 1 || ncap > kKeysPerBlock || lo >= ncap))
@@ -785,6 +787,7 @@ cudaError_t launch_encode_tc(const void* keys, const float* centre, const void* 
     a.lo = lo;
     a.blk0 = blk0;
     a.cblk = cblk ? cblk : (ncap + kKeysPerBlock - 1) / kKeysPerBlock;
+    a.code_blk = code_blk;
     a.norms = norms;
     a.radius = radius;
     a.units = B * Hkv * a.nblk;

@@ -44,6 +44,8 @@ enum CheckSite : int {
     kSiteEncodeCodes = 9,        // the code words an encoder CTA writes
     kSiteKv4Row = 10,            // a row of the 4-bit cache written, read or copied
     kSiteKv4Out = 11,            // rows read back, partial states or output rows of its attention
+    kSiteEncodeRow = 12,         // a key row that a CUDA-core encoder reads
+    kSiteAttendList = 13,        // the list of selected keys of an attend CTA (shared memory)
 };
 
 // Index check of the MP_CHECKS build (the memory checker's stand-in): there an index outside
@@ -125,17 +127,19 @@ int key_mean_splits(int BH, int n);
 // With norms (|k_i - mu| per key, [B*Hkv][ncap]) and radius ([B*Hkv]): the MIPS variant, W with
 // d + 1 rows. With argmax: the cross-polytope codes (bytes), W = G [L][d][d], K = d (a table is
 // d hyperplanes). head_rows: rows from one head's keys to the next one's in memory (0: ncap); cblk:
-// blocks per head of the codes (0: as many as ncap keys have). lo >= 0: keys [lo, ncap) of one block
+// blocks per head of the codes (0: as many as ncap keys have), block 0 of the keys going to their
+// block code_blk. lo >= 0: keys [lo, ncap) of one block
 // (blk0 = 0, blk1 = 1, ncap <= 1024; keys points at the first of them), the other keys' bits kept.
 cudaError_t launch_encode_tc(const void* keys, const float* centre, const void* W, int B,
                              int Hkv, int ncap, int blk0, int blk1, int K, int L,
                              uint32_t* codes, int* status, cudaStream_t st,
                              const float* norms = nullptr, const float* radius = nullptr,
-                             bool argmax = false, int head_rows = 0, int cblk = 0, int lo = -1);
+                             bool argmax = false, int head_rows = 0, int cblk = 0,
+                             int code_blk = 0, int lo = -1);
 cudaError_t launch_encode_simt(const void* keys, bool keys_bf16, const float* centre,
                                const void* W, bool w_bf16, int B, int Hkv, int ncap, int blk0,
                                int blk1, int K, int L, uint32_t* codes, cudaStream_t st,
-                               int head_rows = 0, int cblk = 0);
+                               int head_rows = 0, int cblk = 0, int code_blk = 0);
 // Encode keys [n0, n1) of one block of codes laid out for ncap on CUDA cores, keeping the other
 // keys' bits; key n0 of a head is row row0 of its head_rows.
 cudaError_t launch_encode_part(const void* keys, bool keys_bf16, const float* centre,

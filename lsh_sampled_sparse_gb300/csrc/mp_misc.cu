@@ -113,7 +113,7 @@ constexpr int kSimtPlanes = 16;    // hyperplanes per pass
 __global__ void __launch_bounds__(kSimtKeys)
     encode_simt_kernel(const void* keys, int keys_bf16, const float* centre, const void* W,
                        int w_bf16, int lo, int hi, int head_rows, int first, bool keep, int C,
-                       int cblk, int blk0, uint32_t* codes) {
+                       int cblk, int blk0, int code_blk, uint32_t* codes, int* status) {
     __shared__ float kbar[kSimtKeys][kD + 1];
     __shared__ float Wsm[kD][kSimtPlanes];
     const int bh = blockIdx.y, tile = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kSimtKeys)
     for (int idx = tid; idx < kSimtKeys * kD; idx += kSimtKeys) {
         const int r = idx / kD, e = idx % kD, i = i0 + r;
         float v = 0.0f;
-        if (i >= lo && i < hi)
+        if (i >= lo && i < hi && mp_check(status, i - first, head_rows, kSiteEncodeRow))
             v = load_elem(keys, keys_bf16,
                           (static_cast<size_t>(bh) * head_rows + i - first) * kD + e) -
                 centre[static_cast<size_t>(bh) * kD + e];
@@ -131,8 +131,9 @@ __global__ void __launch_bounds__(kSimtKeys)
     }
     const int blk = i0 / kKeysPerBlock;
     const int word = (i0 % kKeysPerBlock) / 32 + warp;
-    uint32_t* dst = codes + (static_cast<size_t>(bh) * cblk + blk) * static_cast<size_t>(C) *
-                                kWordsPerBlock + word;
+    if (!mp_check(status, code_blk + blk, cblk, kSiteEncodeCodes)) return;       // the whole CTA
+    uint32_t* dst = codes + (static_cast<size_t>(bh) * cblk + code_blk + blk) *
+                                static_cast<size_t>(C) * kWordsPerBlock + word;
     const int k0 = i0 + 32 * warp;                                 // of this warp's word
     const uint32_t range = keep ? bits_below(hi - k0) & ~bits_below(lo - k0) : 0xffffffffu;
     const int passes = (C + kSimtPlanes - 1) / kSimtPlanes;
@@ -296,13 +297,14 @@ static dim3 simt_grid(int blocks, int heads, int C) {
 cudaError_t launch_encode_simt(const void* keys, bool keys_bf16, const float* centre,
                                const void* W, bool w_bf16, int B, int Hkv, int ncap, int blk0,
                                int blk1, int K, int L, uint32_t* codes, cudaStream_t st,
-                               int head_rows, int cblk) {
+                               int head_rows, int cblk, int code_blk) {
     const int C = K * L;
     if (C == 0 || blk1 <= blk0) return cudaSuccess;
     if (head_rows == 0) head_rows = ncap;
     if (cblk == 0) cblk = (ncap + kKeysPerBlock - 1) / kKeysPerBlock;
     encode_simt_kernel<<<simt_grid(blk1 - blk0, B * Hkv, C), kSimtKeys, 0, st>>>(
-        keys, keys_bf16, centre, W, w_bf16, 0, ncap, head_rows, 0, false, C, cblk, blk0, codes);
+        keys, keys_bf16, centre, W, w_bf16, 0, ncap, head_rows, 0, false, C, cblk, blk0, code_blk,
+        codes, device_status_ptr());
     return cudaGetLastError();
 }
 
@@ -315,8 +317,8 @@ cudaError_t launch_encode_part(const void* keys, bool keys_bf16, const float* ce
     if ((n1 - 1) / kKeysPerBlock != blk0) return cudaErrorInvalidValue;
     const int cblk = (ncap + kKeysPerBlock - 1) / kKeysPerBlock;
     encode_simt_kernel<<<simt_grid(1, B * Hkv, C), kSimtKeys, 0, st>>>(
-        keys, keys_bf16, centre, W, w_bf16, n0, n1, head_rows, n0 - row0, true, C, cblk, blk0,
-        codes);
+        keys, keys_bf16, centre, W, w_bf16, n0, n1, head_rows, n0 - row0, true, C, cblk, blk0, 0,
+        codes, device_status_ptr());
     return cudaGetLastError();
 }
 
