@@ -405,13 +405,13 @@ MP_API mp_status mp_kv4_attention(const void* q, mp_dtype q_dtype, const mp_kv4*
                                   cudaStream_t stream);
 
 /* mp_decode_attention, mp_sampled_attention and mp_sampled_attention_buckets with the keys and
- * values of a 4-bit cache, written with the centre that these calls get: the codes are those of
- * the keys themselves (mp_encode_keys and its variants, before the cache is written), the scores
- * and the cosine of p_i are those of the keys that the cache holds, and log u of the SimHash codes
- * is evaluated for each sampled key, to about 2e-7. Values whose groups span more than 2^110 may
- * overflow on the way. prm->n_capacity is the codes' capacity, cache->n_capacity the cache's own
- * (>= n). Workspaces, the query encoding (mp_encode_query), variants and errors as for those
- * calls. */
+ * values of a 4-bit cache, written with the centre that these calls get: the codes are those of the
+ * keys themselves (mp_encode_keys and its variants, before the cache is written), the scores and
+ * the cosine of p_i are those of the keys that the cache holds, and log u of the SimHash codes is
+ * evaluated for each sampled key (off by about 2^-22 (K + 1) at most). Keys beyond 2^60 and values
+ * whose groups span more than 2^110 may overflow on the way. prm->n_capacity is the codes'
+ * capacity, cache->n_capacity the cache's own (>= n). Workspaces, the query encoding
+ * (mp_encode_query), variants and errors as for those calls. */
 MP_API mp_status mp_kv4_decode_attention(const void* q, mp_dtype q_dtype, const uint32_t* codes,
                                          const float* centre, const void* W, mp_dtype w_dtype,
                                          const mp_kv4* cache, int B, int Hq, int Hkv, int n, int d,

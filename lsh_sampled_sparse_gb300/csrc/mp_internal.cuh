@@ -306,9 +306,6 @@ __device__ __forceinline__ uint32_t warp_transpose32(uint32_t x, int lane) {
     return x;
 }
 
-// Programmatic dependent launch: the next kernel in the stream may be scheduled once every CTA
-// of this one has started; a kernel launched that way waits for its predecessor's completion
-// (and memory) before it touches anything the predecessor writes.
 // Thread-block clusters: a barrier of all their threads, the address of this CTA's shared memory in
 // CTA `rank` of the cluster, and a float from there
 __device__ __forceinline__ void cluster_barrier() {
@@ -326,6 +323,9 @@ __device__ __forceinline__ float load_peer(uint32_t addr) {
     return v;
 }
 
+// Programmatic dependent launch: the next kernel in the stream may be scheduled once every CTA
+// of this one has started; a kernel launched that way waits for its predecessor's completion
+// (and memory) before it touches anything the predecessor writes.
 __device__ __forceinline__ void allow_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -374,16 +374,20 @@ __device__ inline float log_inclusion_cos(float c, int K, int L) {
     return log_inclusion_p(acosf(-c) * 0.318309886183790672f, K, L);
 }
 
-// log u of the same cosine to about 2e-7 (the closed form above: 1e-6, most of it the rounding of
-// K log p, 2 K log p being near -14), for the 4-bit cache's decode. With g(c) = log(1 + 2 asin(c) /
+// log u of the same cosine, for the 4-bit cache's decode, from K log p less its largest part, which
+// is a constant (the closed form above rounds K log p itself). Off by about 2^-22 (K + 1) at most for
+// cosines from -1/2 on: numbers of up to 2 K log 2 are added in float32, and g's own rounding counts
+// 2 K times. In an emulation at (10, 150) that is 2.0e-6 at cosine -1/2, 6.8e-7 from -0.1 on and 1.5e-7
+// on average; 4.5e-6 at (32, 1000). With g(c) = log(1 + 2 asin(c) /
 // pi), K log p = K g - K log 2, x = p^K = e^{K g} 2^-K, and below lambda = L x = 3/2
 //   log u = c0 + 2 K g + (L - 2) log1p(-x) + log(1 + sum_{j>=3} t_j / t_2),
 //   c0 = log(L (L - 1) / 2) - 2 K log 2, rounded once,
 // with ten terms of the sum (the rest is under 3e-8) from ratio[i] = (L - j) / (j + 1), j = 2 + i;
 // above it log(1 - e^{L log1p(-x)} (1 + L x / (1 - x))), u being 0.44 or more. The two share their
 // logarithm: a warp's keys lie on both sides. For |c| <= 1/2, g(c) / c is the interpolant of
-// degree 11 at the Chebyshev nodes of that interval (off by 2e-8 relative). A cosine below -1/2,
-// where 1 + 2 asin(c) / pi loses bits, takes the form above: no key is likely to be sampled there.
+// degree 11 at the Chebyshev nodes of that interval (off by 4.4e-8 relative, 1.5e-8 absolute). A
+// cosine below -1/2, where 1 + 2 asin(c) / pi loses bits, takes the form above, with its error: few
+// keys, unless K is small.
 struct FineLogU {
     float c0, unit;                              // unit: 2^-K
     float ratio[10];
