@@ -235,7 +235,9 @@ MP_API mp_status mp_decode_attention(const void* q, mp_dtype q_dtype, const uint
  *
  * mp_encode_query: q_code = Encode(q, W), plus |q| and q.mu (Algorithm 1's first step).
  * mp_sampled_attention: collision counts, S, gather of K_S and V_S, importance weights, and the
- * merged softmax with the exact set T (Algorithm 1's remaining steps).
+ * merged softmax with the exact set T (Algorithm 1's remaining steps). It may load codes, q and
+ * centre before the work queued ahead of it has ended: they are to be written before
+ * mp_encode_query is called, not between the two (keys and values may be).
  * Errors as mp_decode_attention. */
 MP_API mp_status mp_encode_query(const void* q, mp_dtype q_dtype, const float* centre,
                                  const void* W, mp_dtype w_dtype, int B, int Hq, int Hkv, int n,
