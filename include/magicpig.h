@@ -382,10 +382,15 @@ MP_API mp_status mp_kv4_read(const mp_kv4* cache, const float* centre, int B, in
                              int n_begin, const int32_t* positions, void* keys, void* values,
                              mp_dtype kv_dtype, cudaStream_t stream);
 
-/* Workspace bytes of mp_kv4_attention for these shapes (0 if they are invalid, and a workspace is
- * not needed where it is 0 for valid ones). The workspace needs no initial contents; two calls
- * that may overlap, captured ones among them, need one each. */
+/* Workspace bytes of mp_kv4_attention for these shapes and for any smaller n (0 if they are invalid,
+ * and where no such call needs one): a decode that grows keeps the workspace of its capacity. The
+ * workspace needs no initial contents; two calls that may overlap, captured ones among them, need
+ * one each. */
 MP_API size_t mp_kv4_attention_workspace_bytes(int B, int Hq, int Hkv, int n, int d);
+
+/* 1 if mp_kv4_attention of exactly these shapes uses its workspace, 0 if NULL does (and for shapes
+ * that are invalid). */
+MP_API int mp_kv4_attention_uses_workspace(int B, int Hq, int Hkv, int n, int d);
 
 /* Exact attention of one query token per sequence over the cache's first n tokens:
  *   out[b][h] = sum_i w_i v_i / sum_i w_i,   w_i = exp(scale q.k_i),   i < length_b

@@ -123,6 +123,7 @@ def _declare(L):
         "mp_kv4_write": (_c_int, [_vp, _vp, _c_int, _vp] + [_c_int] * 5 + [_vp, Q, _vp]),
         "mp_kv4_read": (_c_int, [Q, _vp] + [_c_int] * 5 + [_vp, _vp, _vp, _c_int, _vp]),
         "mp_kv4_attention_workspace_bytes": (_c_size, [_c_int] * 5),
+        "mp_kv4_attention_uses_workspace": (_c_int, [_c_int] * 5),
         "mp_kv4_attention": (_c_int, [_vp, _c_int, Q] + [_c_int] * 5
                              + [_vp, ctypes.c_float, _vp, _vp, _c_size, _vp]),
         "mp_kv4_decode_attention": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _c_int, Q] + [_c_int] * 5
@@ -651,7 +652,14 @@ def kv4_read(cache: KV4Cache, m: int, n_begin: int = 0, centre=None, positions=N
 
 
 def kv4_attention_workspace_bytes(B: int, Hq: int, Hkv: int, n: int, d: int = 128) -> int:
+    """Workspace bytes of kv4_attention over up to n tokens (0 where no such call needs one)."""
     return int(lib().mp_kv4_attention_workspace_bytes(B, Hq, Hkv, n, d))
+
+
+def _kv4_attention_need(*dims):
+    """The same for a call over exactly n tokens: not every one uses a workspace."""
+    L = lib()
+    return L.mp_kv4_attention_uses_workspace(*dims) and L.mp_kv4_attention_workspace_bytes(*dims)
 
 
 def _kv4_call(q, cache, n, out, workspace, need, stream):
@@ -689,7 +697,7 @@ def kv4_attention(q, cache: KV4Cache, n=None, lengths=None, scale: float = 0.0, 
     (default: the capacity) of a 4-bit cache, or the first lengths[b] (int32 [B], on the GPU, at
     most n) of sequence b; returns out [B, Hq, 128] float32, zero for a sequence of length 0."""
     c, device, dims, qp, qt, out, op, workspace, wp, size = _kv4_call(
-        q, cache, n, out, workspace, kv4_attention_workspace_bytes, stream)
+        q, cache, n, out, workspace, _kv4_attention_need, stream)
     status = lib().mp_kv4_attention(
         qp, qt, ctypes.byref(c), *dims, _arg(lengths, device, "lengths", torch.int32, dims[:1]),
         scale, op, wp, size, _kv4_stream(stream, device))

@@ -597,6 +597,11 @@ size_t mp_kv4_attention_workspace_bytes(int B, int Hq, int Hkv, int n, int d) {
     return align256(kv4_attention_scratch_bytes(B, Hq, Hkv, n));
 }
 
+int mp_kv4_attention_uses_workspace(int B, int Hq, int Hkv, int n, int d) {
+    return valid_kv4_attention(B, Hq, Hkv, n, d) && d == kD &&
+           kv4_attention_uses_scratch(B, Hq, Hkv, n);
+}
+
 mp_status mp_kv4_attention(const void* q, mp_dtype q_dtype, const mp_kv4* cache, int B, int Hq,
                            int Hkv, int n, int d, const int32_t* lengths, float scale, float* out,
                            void* workspace, size_t ws_bytes, cudaStream_t stream) {
@@ -607,7 +612,8 @@ mp_status mp_kv4_attention(const void* q, mp_dtype q_dtype, const mp_kv4* cache,
     if (!q || !out || !aligned(q, q_dtype == MP_BF16 ? 2 : 4) || !aligned(out, 16) ||
         !aligned(lengths, 4))
         return MP_ERR_INVALID_ARG;
-    const size_t need = mp_kv4_attention_workspace_bytes(B, Hq, Hkv, n, d);
+    const size_t need = kv4_attention_uses_scratch(B, Hq, Hkv, n)
+                            ? mp_kv4_attention_workspace_bytes(B, Hq, Hkv, n, d) : 0;
     if (need > 0 && (!workspace || !aligned(workspace, 256))) return MP_ERR_INVALID_ARG;
     if (ws_bytes < need) return MP_ERR_WORKSPACE;
     if (!ensure_prepared()) return MP_ERR_CUDA;

@@ -213,7 +213,8 @@ cudaError_t launch_kv4_write(const void* keys, const void* values, bool bf16, co
 cudaError_t launch_kv4_read(const mp_kv4& cache, const float* centre, int B, int Hkv, int m,
                             int n_begin, const int32_t* positions, void* keys, void* values,
                             bool bf16, cudaStream_t st);
-size_t kv4_attention_scratch_bytes(int B, int Hq, int Hkv, int n);
+size_t kv4_attention_scratch_bytes(int B, int Hq, int Hkv, int n);   // of up to n tokens
+bool kv4_attention_uses_scratch(int B, int Hq, int Hkv, int n);      // of n tokens
 cudaError_t launch_kv4_attention(const void* q, bool q_bf16, const mp_kv4& cache, int B, int Hq,
                                  int Hkv, int n, const int32_t* lengths, float scale, float* out,
                                  void* workspace, cudaStream_t st);

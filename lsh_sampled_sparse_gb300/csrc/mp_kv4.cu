@@ -1168,6 +1168,21 @@ struct AttPlan {
     int nt, chunks, splits, tiles_per_split;
     bool cluster;                                // the splits of a unit are one cluster
 };
+constexpr int kPlans = 6;                        // no split; k CTAs an SM; waves of `resident`
+int plan_ctas(int k, int resident) { return k <= resident ? k : (k - resident + 1) * resident; }
+int resident_ctas(int nt) { return nt == 1 ? 3 : 2; }
+int steps_of(int n) { return (n - 1) / (kTile * kAttWarps) + 1; }
+int heads_plan(int G, int* nt) {                 // chunks of query heads, of 4 nt each
+    *nt = G <= 4 ? 1 : 2;
+    return (G + 4 * *nt - 1) / (4 * *nt);
+}
+// The most splits that attention_plan takes for n tokens or fewer
+long long most_splits(int B, int Hq, int Hkv, int n) {
+    int nt;
+    const long long units = static_cast<long long>(B) * Hkv * heads_plan(Hq / Hkv, &nt);
+    return std::min<long long>({256, kSms * plan_ctas(kPlans - 1, resident_ctas(nt)) / units,
+                                steps_of(n)});
+}
 // How many splits: the least of a model of a call's time, in units of 10 ns, over the counts that
 // fill one, two or three CTAs an SM, and three in two or three waves. Measured with NT = 1 (one to
 // three CTAs an SM, 2 to 12 steps each, a step being a tile a warp): what a step takes on an SM
@@ -1180,18 +1195,16 @@ struct AttPlan {
 // 21.7 us in 720 CTAs, 19.5 in 240).
 AttPlan attention_plan(int B, int Hq, int Hkv, int n, bool ragged) {
     AttPlan p;
-    const int G = Hq / Hkv;
-    p.nt = G <= 4 ? 1 : 2;
-    p.chunks = (G + 4 * p.nt - 1) / (4 * p.nt);
+    p.chunks = heads_plan(Hq / Hkv, &p.nt);
     const long long units = static_cast<long long>(B) * Hkv * p.chunks;
-    const int steps = (n - 1) / (kTile * kAttWarps) + 1, resident = p.nt == 1 ? 3 : 2;
+    const int steps = steps_of(n), resident = resident_ctas(p.nt);
     const int step_cost[2][3] = {{86, 66, 72}, {120, 107, 107}};
     const double memory = static_cast<double>(B) * Hkv * n * (2 * kCodeBytes + kParamBytes) /
                           66700.0 * (ragged ? 0.75 : 1.0);
     double best = -1.0;
-    for (int k = 0; k <= 5; ++k) {               // no split; k CTAs an SM; waves of `resident`
-        const int per_sm = k <= resident ? k : (k - resident + 1) * resident;
-        const long long most = k == 0 ? 1 : std::min<long long>(256, kSms * per_sm / units);
+    for (int k = 0; k < kPlans; ++k) {
+        const long long most =
+            k == 0 ? 1 : std::min<long long>(256, kSms * plan_ctas(k, resident) / units);
         if (most < 1 || (k > 0 && most < 2)) continue;
         const int each = static_cast<int>((steps + most - 1) / most);
         const int used = (steps + each - 1) / each;
@@ -1280,13 +1293,19 @@ cudaError_t launch_kv4_read(const mp_kv4& cache, const float* centre, int B, int
 }
 
 size_t kv4_attention_scratch_bytes(int B, int Hq, int Hkv, int n) {
-    // enough for either layout: the caller of a size does not say whether lengths will differ
-    int splits = 0;
+    // the most splits that a plan of up to n tokens can have: the plans themselves have more for some
+    // n than for larger ones (4 x 8 heads: a cluster at 16384 tokens, 9 splits in memory at 16128)
+    const long long splits = most_splits(B, Hq, Hkv, n);
+    return splits < 2 ? 0 : static_cast<size_t>(B) * Hq * splits * kPart * sizeof(float);
+}
+
+bool kv4_attention_uses_scratch(int B, int Hq, int Hkv, int n) {
+    // in either layout: who asks does not say whether lengths will differ
     for (bool ragged : {false, true}) {
         const AttPlan p = attention_plan(B, Hq, Hkv, n, ragged);
-        if (p.splits > 1 && !p.cluster) splits = std::max(splits, p.splits);
+        if (p.splits > 1 && !p.cluster) return true;
     }
-    return static_cast<size_t>(B) * Hq * splits * kPart * sizeof(float);
+    return false;
 }
 
 cudaError_t launch_kv4_attention(const void* q, bool q_bf16, const mp_kv4& cache, int B, int Hq,

@@ -143,3 +143,18 @@ def test_keys_up_to_the_documented_size(mp):
     cache = mp.kv4_write(mp.kv4_cache(1, 2, n), keys, values)
     want, tol = _weighted64(q, cache, 128 ** -0.5)
     assert ((mp.kv4_attention(q, cache).double() - want).abs() <= tol).all()
+
+
+def test_one_workspace_serves_a_growing_decode(mp):
+    B, Hq, Hkv, cap = 4, 32, 8, 16384              # a cluster at the capacity, a merge below it
+    g = torch.Generator(device="cuda")
+    g.manual_seed(7)
+    cache = mp.kv4_write(mp.kv4_cache(B, Hkv, cap),
+                         *(torch.randn(B, Hkv, cap, 128, generator=g, device="cuda")
+                           for _ in range(2)))
+    q = torch.randn(B, Hq, 128, generator=g, device="cuda")
+    ws = torch.empty(mp.kv4_attention_workspace_bytes(B, Hq, Hkv, cap), dtype=torch.uint8,
+                     device="cuda")
+    for n in (1, 300, 5000, 10001, 16128, cap):
+        assert torch.equal(mp.kv4_attention(q, cache, n=n, workspace=ws),
+                           mp.kv4_attention(q, cache, n=n))
