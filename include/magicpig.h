@@ -395,7 +395,8 @@ MP_API int mp_kv4_attention_uses_workspace(int B, int Hq, int Hkv, int n, int d)
 /* Exact attention of one query token per sequence over the cache's first n tokens:
  *   out[b][h] = sum_i w_i v_i / sum_i w_i,   w_i = exp(scale q.k_i),   i < length_b
  * with the values that the cache holds; length_b = n, or lengths[b] ([B] int32 on the device,
- * taken into [0, n]). A sequence of length 0 gets zero rows. Any Hq that Hkv divides.
+ * taken into [0, n]). A sequence of length 0 gets zero rows. The work is laid out for n: where every
+ * length is far below it, a smaller n is faster. Any Hq that Hkv divides.
  * scale 0 means 1/sqrt(d). Scores, softmax and sums are float32: codes and the two fp16 halves of a
  * query element or a weight (22 bits) meet in exact tensor-core products. An element of a query
  * enters within 2^-22 of itself and 2^-25 of the largest of its row. Sums over tokens take weights

@@ -849,7 +849,8 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
         m = mn;
     };
     static_assert(kAttendRows == 8 * kHalves, "the stage gives each half-warp 8 row slots");
-    // the keys of the first kRowKeys entries, listed once (4-bit: all are) (later ones are found on demand)
+    // the keys of the first kRowKeys entries, listed once; later ones are found on demand (a 4-bit
+    // cache's are all listed by now)
     if constexpr (KV != kKv4) {
         for (int i = tid; i < min(nsel, kRowKeys); i += kAThreads) rowkey[i] = key_of(i);
         __syncthreads();

@@ -642,10 +642,12 @@ __device__ __forceinline__ void values_of(const Query8& v, const A4Args& a, size
 // group). Lane (r, t) = (lane / 4, lane % 4) holds query head t (2 t and 2 t + 1 where NT = 2) of the
 // logits, weights and sums: tokens r and r + 8 of a fragment, dims 32 m + 4 r .. + 3.
 //
-// Four query heads a KV head: 32 sequences x 8 heads x 32K tokens take 195 us (6.2 TB/s, bound by
+// Four query heads a KV head: 32 sequences x 8 heads x 32K tokens take 199 us (6.1 TB/s, bound by
 // memory), 1 x 8 x 96K 24.1 us, of which about 6 are the launch, the queries and the join. Eight:
-// 2 x 8 x 128K take 66 us (4.6 TB/s); there a tile's arithmetic (1400 instructions a warp) takes
-// longer than its bytes, at two CTAs an SM, for which the registers do. Like the other kernels here
+// 2 x 8 x 128K take 66.7 us (4.5 TB/s); there a tile's arithmetic (1320 instructions a warp) takes
+// longer than its bytes, at two CTAs an SM, for which the registers do. More than eight: every chunk
+// of eight copies and unpacks the codes for itself (4 sequences x 128K tokens of one KV head with 8,
+// 16 and 32 query heads: 25, 38 and 64 us). Like the other kernels here
 // it is launched as a dependent of what precedes it in the stream and waits for that before its
 // first access: queued calls follow each other 2 to 3 us sooner (1 x 8 x 96K 26.7 -> 23.7 us).
 template <int NT>
@@ -888,7 +890,9 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
         // tile's own products are looked at: a head's tokens are held to 2^-36 of a product that
         // its sum contains, whatever the steps of tokens without weight and other heads' weights.
         // (By the tile's largest step alone a token of no weight, 2^34 times larger than the rest,
-        // moved outputs by 3%.) NaN is not the largest of anything and goes through.
+        // moved outputs by 3%.) Looking at every tile's products costs 3% (8 x 96K tokens 24.6
+        // against 24.2 us, 32 x 8 x 32K 206 against 199). NaN is not the largest of anything and
+        // goes through.
         {
             uint32_t vmax[2] = {0u, 0u};
 #pragma unroll
@@ -1189,8 +1193,12 @@ long long most_splits(int B, int Hq, int Hkv, int n) {
 // with k CTAs when memory does not hold it up is 0.86, 0.66 and 0.72 us over k; memory gives 6.67
 // TB/s whatever the layout; and 5.3, 6.2 and 8.7 us come on top, 4.0 where nothing is split. More
 // CTAs than the call needs lose: 8 heads of 96K tokens take 25.0 us in 152 CTAs, 23.3 in 280 and
-// 26.0 in 440. Sequences shorter than n (`ragged`) leave memory less to do, and a CTA of a later
-// wave goes where a short one has ended, but the CTAs of one wave wait for the longest. With NT = 2
+// 26.0 in 440. Sequences shorter than n (`ragged`; the lengths are on the device, and are taken to
+// average 3/4 n, as if spread evenly between n / 2 and n) leave memory less to do, and a CTA of a
+// later wave goes where a short one has ended, but the CTAs of one wave wait for the longest.
+// Planned as if all were n, 32 x 8 heads of 16K to 32K tokens take 195 us against 163, of 0 to 32K
+// 186 against 128, 5 x 12 heads of 36K to 72K 131 against 84. Lengths that are all far below n still
+// go by the splits of n: 20000 tokens of n = 98304 take 21.9 us, and 9.6 where n is 20000. With NT = 2
 // (1.20 and 1.07 us) each wave more costs 2.5 us (20 sequences of up to 9000 tokens, 16 heads over 2:
 // 21.7 us in 720 CTAs, 19.5 in 240).
 AttPlan attention_plan(int B, int Hq, int Hkv, int n, bool ragged) {
