@@ -54,7 +54,7 @@ extern "C" {
 #define MP_API
 #endif
 
-#define MP_ABI_VERSION 7
+#define MP_ABI_VERSION 8
 #define MP_KEYS_PER_BLOCK 1024
 
 typedef enum {
