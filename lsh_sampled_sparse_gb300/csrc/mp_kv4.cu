@@ -783,7 +783,9 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 3 : 2)
 #pragma unroll
             for (int g = 0; g < 2; ++g)
                 qsum[nt][g] = 0x1p-10f * __shfl_sync(0xffffffffu, sum[g], from);
-            fac[nt] = fmaxf(__shfl_sync(0xffffffffu, a.scale * up, from), 1.17549435e-38f);
+            // not 0, which an infinite logit would turn into NaN; as a subnormal number it is off by
+            // 2^-150, times logits of up to 2^126 within their own rounding
+            fac[nt] = fmaxf(__shfl_sync(0xffffffffu, a.scale * up, from), 0x1p-149f);
         }
     }
 

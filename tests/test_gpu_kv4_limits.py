@@ -158,3 +158,17 @@ def test_one_workspace_serves_a_growing_decode(mp):
     for n in (1, 300, 5000, 10001, 16128, cap):
         assert torch.equal(mp.kv4_attention(q, cache, n=n, workspace=ws),
                            mp.kv4_attention(q, cache, n=n))
+
+
+def test_a_small_scale_of_small_queries_over_large_keys(mp):
+    """scale times a query below 2^-126: a product that float32 holds only as a subnormal number."""
+    n = 200
+    g = torch.Generator(device="cuda")
+    g.manual_seed(91)
+    keys = torch.randn(1, 2, n, 128, generator=g, device="cuda")
+    keys = keys / keys.abs().max() * 2.0 ** 124
+    values = torch.randn(1, 2, n, 128, generator=g, device="cuda")
+    q = torch.randn(1, 8, 128, generator=g, device="cuda") * 2.0 ** -121
+    cache = mp.kv4_write(mp.kv4_cache(1, 2, n), keys, values)
+    want, tol = _weighted64(q, cache, 2.0 ** -20)
+    assert ((mp.kv4_attention(q, cache, scale=2.0 ** -20).double() - want).abs() <= tol).all()
