@@ -54,7 +54,7 @@ extern "C" {
 #define MP_API
 #endif
 
-#define MP_ABI_VERSION 8
+#define MP_ABI_VERSION 9
 #define MP_KEYS_PER_BLOCK 1024
 
 typedef enum {
@@ -193,6 +193,17 @@ MP_API mp_status mp_encode_rows(const void* keys, mp_dtype key_dtype, const floa
                                 const void* W, mp_dtype w_dtype, int B, int Hkv, int m,
                                 int n_capacity, int n_begin, int d, int K, int L, uint32_t* codes,
                                 cudaStream_t stream);
+
+/* mp_encode_rows for sequences of different lengths: keys [B][Hkv][m][d] join the context of sequence
+ * b at [positions[b], positions[b] + m) ([B] int32 on the device). A key that falls outside
+ * [0, n_capacity) is left out; bits of all other keys are kept. For the few tokens of a decode step:
+ * one launch on CUDA cores, with the sums of mp_encode_keys's short ranges (bit for bit).
+ * Errors: MP_ERR_INVALID_ARG (shapes, m < 0, null, misalignment: positions 4 bytes),
+ * MP_ERR_UNSUPPORTED (d != 128, m > 64: longer ranges are mp_encode_rows's). m == 0 does nothing. */
+MP_API mp_status mp_encode_rows_at(const void* keys, mp_dtype key_dtype, const float* centre,
+                                   const void* W, mp_dtype w_dtype, int B, int Hkv, int m,
+                                   int n_capacity, const int32_t* positions, int d, int K, int L,
+                                   uint32_t* codes, cudaStream_t stream);
 
 /* Workspace bytes mp_decode_attention (and its two halves below) need for these shapes;
  * 0 if the shapes or parameters are invalid. */
@@ -436,6 +447,102 @@ MP_API mp_status mp_kv4_sampled_attention_buckets(const void* q, mp_dtype q_dtyp
                                                   const mp_params* prm, float* out,
                                                   void* workspace, size_t ws_bytes,
                                                   cudaStream_t stream);
+
+/* ---- Paged K/V cache ----------------------------------------------------------------------------
+ * A pool of pages of page_size tokens of every KV head, keys and values at full precision, and a
+ * table that says which pages a sequence's tokens lie in: sequences of any lengths share one pool,
+ * grow by a page at a time and may share pages that hold the same tokens. Tensors, owned by the
+ * caller:
+ *   keys, values  [n_pages][Hkv][page_size][d]   MP_BF16 or MP_F32, contiguous, 16-byte aligned
+ *   page_table    [B] rows of n_slots int32, table_stride apart; slot j of row b is the page of
+ *                 tokens [j page_size, (j + 1) page_size) of sequence b
+ * A slot that holds a number outside [0, n_pages) has no page: its tokens are not written, and
+ * attention goes on as if they were not there. Slots behind a call's last token are not looked at.
+ * page_size is a multiple of 8. A call may write a token's row once: two sequences that share a page
+ * may read it in one call, not write the same rows of it. */
+typedef struct {
+    void* keys;
+    void* values;
+    const int32_t* page_table;
+    mp_dtype dtype;
+    int n_pages;
+    int page_size;
+    int n_slots;
+    int table_stride;
+} mp_paged;
+
+/* Rows [B][H][m][d] of a tensor whose first three dims have strides of their own (in elements; a
+ * row's d elements follow each other): the queries, keys or values of one fused projection are such
+ * rows. data and the strides of dims longer than one are multiples of 16 bytes. */
+typedef struct {
+    const void* data;
+    long long stride_b;
+    long long stride_h;
+    long long stride_m;
+} mp_rows;
+
+/* Append m tokens of every sequence to the cache, with their rotary positions applied on the way.
+ * Token i of sequence b stands at p = n_begin + i, or, with positions ([B] int32 on the device), at
+ * p = positions[b] + i (n_begin is then ignored). With counts ([B] int32 on the device) only the
+ * first counts[b] tokens of a sequence are there (taken into [0, m]); nothing is written for others.
+ *   keys, values  [B][Hkv][m][d] of rows_dtype: go to row p of the pages of their sequence, in the
+ *                 cache's type; a token whose p has no page is not written
+ *   q             [B][Hq][m][d] of rows_dtype: the rotated queries go to q_out, [B][Hq][m][d] of the
+ *                 same type, contiguous. NULL where there are none. q_out may be q's own memory.
+ *   keys_out      [B][Hkv][m][d] of the cache's type, contiguous, or NULL: the keys as the cache holds
+ *                 them, for the calls that encode them (of tokens without a page too)
+ * Rotation: the first rotary_dims dims of a row are pairs; pair j = (x, y) becomes
+ * (x cos a - y sin a, y cos a + x sin a), a = p inv_freq[j] (float32 on the device, rotary_dims / 2
+ * of them), in float32, rounded once to the type it is stored in. Pairs are dims (j, j + rotary_dims /
+ * 2), or with interleaved != 0 dims (2 j, 2 j + 1). The angle is reduced in 64-bit fixed point: it is
+ * off by less than 2^-51 |p| max(|inv_freq[j]|, 2^-10) + 2^-22 radians at any position. inv_freq NULL
+ * (rotary_dims then ignored) turns nothing. An inv_freq that is infinite or NaN has unspecified
+ * results.
+ * Errors: MP_ERR_INVALID_ARG (shapes, m < 0, B m (Hq + 2 Hkv) > 2^31 - 1, n_begin < 0 or n_begin + m >
+ * n_slots page_size without positions, null, misalignment: rows, outputs 16 bytes, others 4),
+ * MP_ERR_UNSUPPORTED (d != 128, page_size not a multiple of 8, rotary_dims not a multiple of 16 in
+ * [16, 128]). m == 0 does nothing. */
+MP_API mp_status mp_paged_append(const mp_rows* keys, const mp_rows* values, const mp_rows* q,
+                                 mp_dtype rows_dtype, const float* inv_freq, int rotary_dims,
+                                 int interleaved, int B, int Hq, int Hkv, int m, int d, int n_begin,
+                                 const int32_t* positions, const int32_t* counts,
+                                 const mp_paged* cache, void* q_out, void* keys_out,
+                                 cudaStream_t stream);
+
+/* Workspace bytes of mp_paged_attention for these shapes, whatever n is (0 if they are invalid). It
+ * needs no initial contents; two calls that may overlap, captured ones among them, need one each. */
+MP_API size_t mp_paged_attention_workspace_bytes(int B, int Hq, int Hkv, int n, int d);
+
+/* Exact attention of one query token per sequence over the first n tokens of its pages:
+ *   out[b][h] = sum_i w_i v_i / sum_i w_i,   w_i = exp(scale q.k_i),   i < length_b
+ * length_b = n, or lengths[b] ([B] int32 on the device, taken into [0, n]). The work is shared out by
+ * the lengths themselves, on the device: n may be the table's whole capacity. A sequence of length
+ * 0, or whose tokens have no page, gets zero rows. Any Hq that Hkv divides. scale 0 means 1/sqrt(d).
+ * Scores, softmax and sums are float32: over a bf16 cache the products are tensor-core products of
+ * bf16, a float32 query element or a weight being three bf16 terms (24 bits). What the pages hold
+ * beyond a sequence's length is not looked at, NaN included. A NaN or an infinity in a query (float32
+ * queries over a bf16 cache: an element past the largest bf16, too), or in a key or value attended
+ * to, may give NaN in the rows that it meets.
+ * Errors: MP_ERR_INVALID_ARG (shapes, n > n_slots page_size or 2^30, B Hq > 2^22, Hq % Hkv, a scale
+ * that is negative, infinite or NaN, null, misalignment: out 16 bytes, lengths 4, workspace 256),
+ * MP_ERR_UNSUPPORTED (d != 128, page_size not a multiple of 8), MP_ERR_WORKSPACE. */
+MP_API mp_status mp_paged_attention(const void* q, mp_dtype q_dtype, const mp_paged* cache, int B,
+                                    int Hq, int Hkv, int n, int d, const int32_t* lengths,
+                                    float scale, float* out, void* workspace, size_t ws_bytes,
+                                    cudaStream_t stream);
+
+/* mp_decode_attention over a paged cache, for sequences of different lengths: keys i < length_b
+ * (mp_paged_attention's) of sequence b, T = {0 .. n_sink-1} u {length_b-n_local .. length_b-1}. The
+ * codes are contiguous per sequence, as for the other calls, laid out for prm->n_capacity tokens (0
+ * means n), and hold the keys' own tokens at their positions (mp_encode_rows, mp_encode_rows_at of
+ * the keys that mp_paged_append returns). A token without a page is left out, of T too. log u of the
+ * SimHash codes is evaluated for each sampled key. Workspace: mp_decode_workspace_bytes.
+ * Errors as mp_decode_attention and mp_paged_attention. */
+MP_API mp_status mp_paged_decode_attention(const void* q, mp_dtype q_dtype, const uint32_t* codes,
+                                           const float* centre, const void* W, mp_dtype w_dtype,
+                                           const mp_paged* cache, int B, int Hq, int Hkv, int n, int d,
+                                           const int32_t* lengths, const mp_params* prm, float* out,
+                                           void* workspace, size_t ws_bytes, cudaStream_t stream);
 
 /* Workspace bytes mp_debug_select needs. */
 MP_API size_t mp_debug_workspace_bytes(int B, int Hq, int Hkv, int n, int d,

@@ -44,6 +44,22 @@ class _KV4(ctypes.Structure):
                 ("params", ctypes.c_void_p), ("n_capacity", ctypes.c_int)]
 
 
+class _Paged(ctypes.Structure):
+    """mp_paged: the pool of a paged cache, a batch's page table, and their sizes."""
+
+    _fields_ = [("keys", ctypes.c_void_p), ("values", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("n_slots", ctypes.c_int),
+                ("table_stride", ctypes.c_int)]
+
+
+class _Rows(ctypes.Structure):
+    """mp_rows: rows [B][H][m][d] with strides of their own, in elements."""
+
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_longlong),
+                ("stride_h", ctypes.c_longlong), ("stride_m", ctypes.c_longlong)]
+
+
 def _params(K, L, n_sink, n_local, scale=0.0, n_capacity=0, n_indexed=0, radius=None,
             logu_table=None) -> Params:
     flags = 0
@@ -82,6 +98,7 @@ def library_path() -> str:
 
 def _declare(L):
     P, Q = ctypes.POINTER(Params), ctypes.POINTER(_KV4)
+    G, R = ctypes.POINTER(_Paged), ctypes.POINTER(_Rows)
     sig = {
         "mp_status_string": (ctypes.c_char_p, [_c_int]),
         "mp_abi_version": (_c_int, []),
@@ -92,6 +109,15 @@ def _declare(L):
         "mp_key_mean_cap": (_c_int, [_vp, _c_int] + [_c_int] * 5 + [_vp, _vp, _c_size, _vp]),
         "mp_encode_keys": (_c_int, [_vp, _c_int, _vp, _vp, _c_int] + [_c_int] * 8 + [_vp, _vp]),
         "mp_encode_rows": (_c_int, [_vp, _c_int, _vp, _vp, _c_int] + [_c_int] * 8 + [_vp, _vp]),
+        "mp_encode_rows_at": (_c_int, [_vp, _c_int, _vp, _vp, _c_int] + [_c_int] * 4 + [_vp]
+                              + [_c_int] * 3 + [_vp, _vp]),
+        "mp_paged_append": (_c_int, [R, R, R, _c_int, _vp] + [_c_int] * 8 + [_vp, _vp, G, _vp, _vp,
+                                                                            _vp]),
+        "mp_paged_attention_workspace_bytes": (_c_size, [_c_int] * 5),
+        "mp_paged_attention": (_c_int, [_vp, _c_int, G] + [_c_int] * 5
+                               + [_vp, ctypes.c_float, _vp, _vp, _c_size, _vp]),
+        "mp_paged_decode_attention": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _c_int, G]
+                                      + [_c_int] * 5 + [_vp, P, _vp, _vp, _c_size, _vp]),
         "mp_key_radius": (_c_int, [_vp, _c_int, _vp] + [_c_int] * 5 + [_vp, _vp]),
         "mp_cp_codes_bytes": (_c_size, [_c_int] * 4),
         "mp_cp_logu_table": (_c_int, [_c_int] * 3 + [_vp, _vp]),
@@ -310,6 +336,36 @@ def encode_rows(keys, centre, W, K: int, L: int, n_begin: int, n_capacity: int, 
     _check(lib().mp_encode_rows(_ptr(keys), _dtype(keys, "keys"), _ptr(centre), _ptr(W),
                                 _dtype(W, "W"), B, Hkv, m, n_capacity, n_begin, d, K, L,
                                 _ptr(codes), _stream(stream)), "mp_encode_rows")
+    return codes
+
+
+def encode_rows_at(keys, centre, W, K: int, L: int, positions, n_capacity: int, codes,
+                   stream=None):
+    """encode_rows for sequences of different lengths: the rows [B, Hkv, m, d] (m at most 64) that join
+    the context of sequence b at positions[b] (int32 [B], on the GPU), into codes laid out for
+    n_capacity. Keys outside the capacity are left out; the bits of other keys are kept."""
+    _cuda(keys, "keys", 4)
+    B, Hkv, m, d = keys.shape
+    device = keys.get_device()
+    if device != torch._C._cuda_getDevice():
+        raise ValueError(f"keys are on cuda:{device}, which is not the current device")
+    if n_capacity < 1 or n_capacity >> 31:
+        raise ValueError(f"n_capacity = {n_capacity}")
+    for t, name in ((codes, "codes"), (centre, "centre"), (W, "W")):
+        _cuda(t, name)
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}, the keys on cuda:{device}")
+    if _nbytes(codes) < codes_bytes(B, Hkv, n_capacity, K, L):
+        raise ValueError("codes buffer too small for the capacity")
+    if tuple(W.shape) != (d, K * L):
+        raise ValueError(f"W {tuple(W.shape)} does not fit the keys")
+    status = lib().mp_encode_rows_at(
+        keys.data_ptr(), _dtype(keys, "keys"),
+        _arg(centre, device, "centre", torch.float32, (B, Hkv, d)), W.data_ptr(), _dtype(W, "W"), B,
+        Hkv, m, n_capacity, _needed(positions, device, "positions", torch.int32, (B,)), d, K, L,
+        codes.data_ptr(), _raw_stream(stream, device))
+    if status:
+        _check(status, "mp_encode_rows_at")
     return codes
 
 
@@ -541,6 +597,13 @@ def _arg(t, device: int, name: str, dtype, shape):
     _refuse(t, device, name, dtype, shape)
 
 
+def _needed(t, device, name, dtype, shape):
+    """_arg of a tensor that there has to be."""
+    if t is None:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return _arg(t, device, name, dtype, shape)
+
+
 def _refuse(t, device, name, dtype, shape):
     """Raise what _arg found."""
     _on_device(t, device, name)
@@ -577,7 +640,7 @@ def _kv4(cache):
                 cap), device, B, Hkv, cap
 
 
-def _kv4_stream(stream, device):
+def _raw_stream(stream, device):
     return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
@@ -616,7 +679,7 @@ def kv4_write(cache: KV4Cache, keys, values, n_begin: int = 0, centre=None, posi
         kp, _arg(values, device, "values", keys.dtype, keys.shape), dt,
         _arg(centre, device, "centre", torch.float32, (B, Hkv, d)), B, Hkv, m, d, n_begin,
         _arg(positions, device, "positions", torch.int32, (B,)), ctypes.byref(c),
-        _kv4_stream(stream, device))
+        _raw_stream(stream, device))
     if status:
         _check(status, "mp_kv4_write")
     return cache
@@ -645,7 +708,7 @@ def kv4_read(cache: KV4Cache, m: int, n_begin: int = 0, centre=None, positions=N
     status = lib().mp_kv4_read(
         ctypes.byref(c), _arg(centre, device, "centre", torch.float32, (B, Hkv, 128)), B, Hkv, m,
         128, n_begin, _arg(positions, device, "positions", torch.int32, (B,)), kp, vp, dt,
-        _kv4_stream(stream, device))
+        _raw_stream(stream, device))
     if status:
         _check(status, "mp_kv4_read")
     return keys, values
@@ -700,7 +763,7 @@ def kv4_attention(q, cache: KV4Cache, n=None, lengths=None, scale: float = 0.0, 
         q, cache, n, out, workspace, _kv4_attention_need, stream)
     status = lib().mp_kv4_attention(
         qp, qt, ctypes.byref(c), *dims, _arg(lengths, device, "lengths", torch.int32, dims[:1]),
-        scale, op, wp, size, _kv4_stream(stream, device))
+        scale, op, wp, size, _raw_stream(stream, device))
     if status:
         _check(status, "mp_kv4_attention")
     return out
@@ -751,7 +814,7 @@ def kv4_decode_attention(q, codes, centre, W, cache: KV4Cache, K: int, L: int, n
         raise ValueError(f"W of shape {tuple(W.shape)} has too few hyperplanes")
     status = lib().mp_kv4_decode_attention(
         qp, qt, codes_p, centre_p, W.data_ptr(), _dtype(W, "W"), ctypes.byref(c), *dims,
-        ctypes.byref(p), op, wp, size, _kv4_stream(stream, device))
+        ctypes.byref(p), op, wp, size, _raw_stream(stream, device))
     if status:
         _check(status, "mp_kv4_decode_attention")
     return out
@@ -768,7 +831,7 @@ def kv4_sampled_attention(q, codes, centre, cache: KV4Cache, K: int, L: int, n_s
     c, device, dims, qp, qt, out, op, workspace, wp, size = call
     status = lib().mp_kv4_sampled_attention(
         qp, qt, codes_p, centre_p, ctypes.byref(c), *dims, ctypes.byref(p), op, wp, size,
-        _kv4_stream(stream, device))
+        _raw_stream(stream, device))
     if status:
         _check(status, "mp_kv4_sampled_attention")
     return out
@@ -789,9 +852,210 @@ def kv4_sampled_attention_buckets(q, buckets, centre, cache: KV4Cache, K: int, L
         raise ValueError(f"buckets too small for {indexed} keys per head, or elsewhere")
     status = lib().mp_kv4_sampled_attention_buckets(
         qp, qt, buckets.data_ptr(), codes_p, centre_p, ctypes.byref(c), *dims, ctypes.byref(p), op,
-        wp, size, _kv4_stream(stream, device))
+        wp, size, _raw_stream(stream, device))
     if status:
         _check(status, "mp_kv4_sampled_attention_buckets")
+    return out
+
+
+class PagedCache(NamedTuple):
+    """The pool of a paged K/V cache: keys and values [n_pages, Hkv, page_size, 128], both bfloat16
+    or both float32, contiguous. Which pages a batch's sequences have is said by a page table, an
+    int32 tensor [B, slots] on the GPU (a view of a wider one may be given): the tokens [j page_size,
+    (j + 1) page_size) of sequence b lie in page page_table[b, j]; a number outside the pool, such as
+    -1, is no page."""
+
+    keys: torch.Tensor
+    values: torch.Tensor
+
+
+def paged_cache(n_pages: int, Hkv: int, page_size: int, dtype=torch.bfloat16,
+                device="cuda") -> PagedCache:
+    """A pool of n_pages pages of page_size tokens (a multiple of 8), contents undefined."""
+    shape = (n_pages, Hkv, page_size, 128)
+    return PagedCache(torch.empty(shape, dtype=dtype, device=device),
+                      torch.empty(shape, dtype=dtype, device=device))
+
+
+def _paged(cache, page_table):
+    """(mp_paged, device, B, Hkv, tokens of the table) of a pool and a batch's page table, their
+    tensors checked; the device must be the current one."""
+    k, v = cache
+    if not isinstance(k, torch.Tensor) or not k.is_cuda:
+        raise TypeError("the cache must hold CUDA tensors")
+    device = k.get_device()
+    if device != torch._C._cuda_getDevice():
+        raise ValueError(f"the cache is on cuda:{device}, which is not the current device")
+    shape = k.shape
+    if len(shape) != 4:
+        raise ValueError(f"keys must be [n_pages, Hkv, page_size, 128], got {tuple(shape)}")
+    dt = _dtype(k, "keys")
+    _on_device(page_table, device, "page_table")
+    if page_table.dtype is not torch.int32:
+        raise TypeError(f"page_table must be int32, is {page_table.dtype}")
+    if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be [B, slots], its rows contiguous")
+    B, slots = page_table.shape
+    stride = page_table.stride(0) if B > 1 else slots
+    if stride < slots or stride >> 31:
+        raise ValueError(f"page_table's rows overlap or are too far apart (stride {stride})")
+    if shape[3] != 128:
+        raise ValueError(f"rows must have 128 elements, got {shape[3]}")
+    return _Paged(_arg(k, device, "keys", k.dtype, shape), _arg(v, device, "values", k.dtype, shape),
+                  page_table.data_ptr(), dt, shape[0], shape[2], slots, stride), device, B, \
+        shape[1], slots * shape[2]
+
+
+def _strided_rows(t, device, name, dtype, shape):
+    """mp_rows of a tensor whose rows are contiguous; other strides are its own."""
+    _on_device(t, device, name)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, is {t.dtype}")
+    if t.dim() != 4 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must have shape {shape or '[B, H, m, 128]'}, got {tuple(t.shape)}")
+    if t.stride(3) != 1 and t.shape[3] != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return _Rows(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+
+
+def paged_append(cache: PagedCache, page_table, keys, values, n_begin: int = 0, positions=None,
+                 counts=None, inv_freq=None, interleaved: bool = False, q=None, q_out=None,
+                 keys_out=None, stream=None):
+    """Append m tokens of every sequence, keys and values [B, Hkv, m, 128] (float32 or bfloat16; any
+    strides of the first three dims), to the pages of their sequences, from n_begin on or, with
+    positions (int32 [B], on the GPU), from positions[b] on. With counts (int32 [B]) only the first
+    counts[b] tokens of sequence b are there. inv_freq (float32 [rotary_dims / 2], on the GPU) turns
+    the keys, and q [B, Hq, m, 128] if it is given, by their positions: pairs of dims (j, j +
+    rotary_dims / 2), or (2 j, 2 j + 1) if interleaved. Returns q_out, the turned queries [B, Hq, m,
+    128] (allocated where it is None; None without q); rows of tokens that are not there are left as
+    they were. keys_out [B, Hkv, m, 128] in the cache's type takes the keys as the cache holds
+    them."""
+    c, device, B, Hkv, _ = _paged(cache, page_table)
+    _on_device(keys, device, "keys")
+    dt = _dtype(keys, "keys")
+    if keys.dim() != 4 or keys.shape[0] != B or keys.shape[1] != Hkv:
+        raise ValueError(f"keys must be [{B}, {Hkv}, m, 128], got {tuple(keys.shape)}")
+    m, d = keys.shape[2:]
+    kr = _strided_rows(keys, device, "keys", keys.dtype, keys.shape)
+    vr = _strided_rows(values, device, "values", keys.dtype, keys.shape)
+    if n_begin >> 31 not in (0, -1):             # what a C int would cut off
+        raise ValueError(f"n_begin = {n_begin}")
+    rotary = 0
+    if inv_freq is not None:
+        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+            raise TypeError("inv_freq must be a CUDA tensor [rotary_dims / 2]")
+        rotary = 2 * inv_freq.shape[0]
+    Hq, qr = 0, None
+    if q is not None:
+        _on_device(q, device, "q")
+        if q.dim() != 4 or q.shape[0] != B or tuple(q.shape[2:]) != (m, d):
+            raise ValueError(f"q must be [{B}, Hq, {m}, {d}], got {tuple(q.shape)}")
+        qr, Hq = ctypes.byref(_strided_rows(q, device, "q", keys.dtype, q.shape)), q.shape[1]
+        if q_out is None:
+            q_out = _empty(tuple(q.shape), q.dtype, q.device, stream)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    status = lib().mp_paged_append(
+        ctypes.byref(kr), ctypes.byref(vr), qr, dt,
+        _arg(inv_freq, device, "inv_freq", torch.float32, (rotary // 2,)), rotary,
+        bool(interleaved), B, Hq, Hkv, m, d, n_begin,
+        _arg(positions, device, "positions", torch.int32, (B,)),
+        _arg(counts, device, "counts", torch.int32, (B,)), ctypes.byref(c),
+        _arg(q_out, device, "q_out", keys.dtype, (B, Hq, m, d)),
+        _arg(keys_out, device, "keys_out", cache[0].dtype, (B, Hkv, m, d)),
+        _raw_stream(stream, device))
+    if status:
+        _check(status, "mp_paged_append")
+    return q_out
+
+
+def paged_attention_workspace_bytes(B: int, Hq: int, Hkv: int, n: int, d: int = 128) -> int:
+    """Workspace bytes of paged_attention (the same for every n)."""
+    return int(lib().mp_paged_attention_workspace_bytes(B, Hq, Hkv, n, d))
+
+
+def _paged_call(q, cache, page_table, n, lengths, out, workspace, need, stream):
+    """What the calls on queries share: checks of q, lengths, out and the workspace, the last two
+    allocated where they are None (need: the workspace's size from B, Hq, Hkv, n, d)."""
+    c, device, B, Hkv, cap = _paged(cache, page_table)
+    _on_device(q, device, "q")
+    shape = q.shape
+    if len(shape) != 3 or shape[0] != B:
+        raise ValueError(f"q must be [{B}, Hq, 128], got {tuple(shape)}")
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    n = cap if n is None else int(n)
+    if not 1 <= n <= cap:
+        raise ValueError(f"n = {n} outside [1, {cap}] (the page table's tokens)")
+    qt = _dtype(q, "q")
+    if out is None:
+        out = _empty(shape, torch.float32, q.device, stream)
+    op = _arg(out, device, "out", torch.float32, shape)
+    dims = (B, shape[1], Hkv, n, shape[2])
+    if workspace is None:
+        workspace = _empty((max(need(*dims), 256),), torch.uint8, q.device, stream)
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous and on the cache's device")
+    return (c, device, dims, q.data_ptr(), qt,
+            _arg(lengths, device, "lengths", torch.int32, (B,)), out, op, workspace)
+
+
+def paged_attention(q, cache: PagedCache, page_table, n=None, lengths=None, scale: float = 0.0,
+                    out=None, workspace=None, stream=None):
+    """Exact attention of one query token per sequence, q [B, Hq, 128], over the first n tokens
+    (default: the page table's) of a paged cache, or the first lengths[b] (int32 [B], on the GPU, at
+    most n) of sequence b; returns out [B, Hq, 128] float32, zero for a sequence of length 0."""
+    c, device, dims, qp, qt, lp, out, op, ws = _paged_call(
+        q, cache, page_table, n, lengths, out, workspace,
+        lib().mp_paged_attention_workspace_bytes, stream)
+    status = lib().mp_paged_attention(qp, qt, ctypes.byref(c), *dims, lp, scale, op, ws.data_ptr(),
+                                      _nbytes(ws), _raw_stream(stream, device))
+    if status:
+        _check(status, "mp_paged_attention")
+    return out
+
+
+def paged_decode_attention(q, codes, centre, W, cache: PagedCache, page_table, K: int, L: int,
+                           n_sink: int, n_local: int, scale: float = 0.0, out=None, workspace=None,
+                           stream=None, n=None, lengths=None, n_capacity=None, radius=None,
+                           logu_table=None):
+    """decode_attention over a paged cache, the first n tokens (default: the page table's) or the
+    first lengths[b] (int32 [B], on the GPU) of each sequence; the codes are laid out for n_capacity
+    tokens per sequence (default: the page table's)."""
+    cap = page_table.shape[1] * cache[0].shape[2] if n_capacity is None else int(n_capacity)
+    if cap >> 31:
+        raise ValueError(f"n_capacity = {cap}")
+    p = _params(K, L, n_sink, n_local, scale, cap, radius=radius, logu_table=logu_table)
+
+    def need(B, Hq, Hkv, n, d):
+        size = int(lib().mp_decode_workspace_bytes(B, Hq, Hkv, n, d, ctypes.byref(p)))
+        if size == 0:
+            raise MagicPIGError("mp_decode_workspace_bytes rejected the shapes/parameters")
+        return size
+
+    c, device, dims, qp, qt, lp, out, op, ws = _paged_call(q, cache, page_table, n, lengths, out,
+                                                           workspace, need, stream)
+    B, _, Hkv, _, d = dims
+    size = cp_codes_bytes(B, Hkv, cap, L) if logu_table is not None \
+        else codes_bytes(B, Hkv, cap, K, L)
+    if codes is not None:
+        _cuda(codes, "codes")
+    if size and (codes is None or _nbytes(codes) < size):
+        raise ValueError(f"codes must hold {size} bytes, for {cap} tokens per head")
+    for t, name, most in ((codes, "codes", 0), (radius, "radius", B * Hkv),
+                          (logu_table, "logu_table", MP_LOGU_TABLE_ENTRIES),
+                          (W, "W", d * (d if logu_table is not None else K) * L)):
+        if t is not None:
+            _on_device(_cuda(t, name), device, name)
+            if t.numel() < most:
+                raise ValueError(f"{name} has {t.numel()} elements, needs {most}")
+    status = lib().mp_paged_decode_attention(
+        qp, qt, None if codes is None else codes.data_ptr(),
+        _needed(centre, device, "centre", torch.float32, (B, Hkv, d)), W.data_ptr(), _dtype(W, "W"),
+        ctypes.byref(c), *dims, lp, ctypes.byref(p), op, ws.data_ptr(), _nbytes(ws),
+        _raw_stream(stream, device))
+    if status:
+        _check(status, "mp_paged_decode_attention")
     return out
 
 

@@ -43,7 +43,7 @@ bool ensure_prepared() {
     if (prepare_misc() != cudaSuccess || prepare_decode() != cudaSuccess ||
         prepare_buckets() != cudaSuccess || prepare_append() != cudaSuccess ||
         prepare_mips() != cudaSuccess || prepare_cross_polytope() != cudaSuccess ||
-        prepare_kv4() != cudaSuccess)
+        prepare_kv4() != cudaSuccess || prepare_paged() != cudaSuccess)
         return false;
     prepare_encode_tc();   // failure only disables the tensor-core encoder
     cudaGetLastError();
@@ -360,6 +360,27 @@ mp_status mp_encode_rows(const void* keys, mp_dtype key_dtype, const float* cent
         row += n;
     }
     return MP_OK;
+}
+
+mp_status mp_encode_rows_at(const void* keys, mp_dtype key_dtype, const float* centre, const void* W,
+                            mp_dtype w_dtype, int B, int Hkv, int m, int n_capacity,
+                            const int32_t* positions, int d, int K, int L, uint32_t* codes,
+                            cudaStream_t stream) {
+    if (B < 1 || Hkv < 1 || m < 0 || n_capacity < 1 || d < 1 || K < 0 || K > 32 || L < 1)
+        return MP_ERR_INVALID_ARG;
+    if (!valid_dtype(key_dtype) || !valid_dtype(w_dtype)) return MP_ERR_INVALID_ARG;
+    if (d != kD || m > kAppendMaxKeys) return MP_ERR_UNSUPPORTED;
+    if (static_cast<long long>(K) * L > (1 << 20)) return MP_ERR_INVALID_ARG;
+    if (static_cast<long long>(B) * Hkv > (1 << 18)) return MP_ERR_INVALID_ARG;   // heads of a grid
+    if (K == 0 || m == 0) return MP_OK;   // nothing to encode
+    if (!keys || !centre || !W || !codes || !positions) return MP_ERR_INVALID_ARG;
+    if (!aligned(keys, 16) || !aligned(codes, 16) || !aligned(centre, 4) || !aligned(positions, 4) ||
+        !aligned(W, w_dtype == MP_BF16 ? 2 : 4))
+        return MP_ERR_INVALID_ARG;
+    if (!ensure_prepared()) return MP_ERR_CUDA;
+    return to_status(launch_encode_rows_at(keys, key_dtype == MP_BF16, centre, W,
+                                           w_dtype == MP_BF16, B, Hkv, m, n_capacity, positions,
+                                           K * L, codes, stream));
 }
 
 mp_status mp_key_radius(const void* keys, mp_dtype key_dtype, const float* centre, int B,
@@ -720,6 +741,109 @@ mp_status mp_kv4_sampled_attention_buckets(const void* q, mp_dtype q_dtype,
                                           Hkv, n, d, prm, out, workspace, ws_bytes, &s, &kv);
     if (st != MP_OK) return st;
     return buckets_attend(q, q_dtype, buckets, codes, centre, kv, s, out, workspace, stream);
+}
+
+// The cache of a paged call: pool, table and sizes. Tokens are numbered in 32 bits, a pool's rows too
+// (2^31 of them are a TB of bf16).
+static mp_status check_paged(const mp_paged* c, int Hkv) {
+    if (!c || !c->keys || !c->values || !c->page_table || !valid_dtype(c->dtype) || c->n_pages < 1 ||
+        c->page_size < 1 || c->n_slots < 1 || c->table_stride < c->n_slots)
+        return MP_ERR_INVALID_ARG;
+    if (!aligned(c->keys, 16) || !aligned(c->values, 16) || !aligned(c->page_table, 4))
+        return MP_ERR_INVALID_ARG;
+    if (c->page_size % 8) return MP_ERR_UNSUPPORTED;
+    if (static_cast<long long>(c->n_slots) * c->page_size > 0x7fffffffll ||
+        static_cast<long long>(c->n_pages) * Hkv > 0x7fffffffll / c->page_size)
+        return MP_ERR_INVALID_ARG;
+    return MP_OK;
+}
+
+// Rows of a strided tensor: 16-byte loads of each
+static bool valid_rows(const mp_rows* r, mp_dtype t, int B, int H, int m) {
+    const long long unit = t == MP_BF16 ? 8 : 4;
+    return r && r->data && aligned(r->data, 16) && (B == 1 || r->stride_b % unit == 0) &&
+           (H == 1 || r->stride_h % unit == 0) && (m == 1 || r->stride_m % unit == 0);
+}
+
+mp_status mp_paged_append(const mp_rows* keys, const mp_rows* values, const mp_rows* q,
+                          mp_dtype rows_dtype, const float* inv_freq, int rotary_dims,
+                          int interleaved, int B, int Hq, int Hkv, int m, int d, int n_begin,
+                          const int32_t* positions, const int32_t* counts, const mp_paged* cache,
+                          void* q_out, void* keys_out, cudaStream_t stream) {
+    if (B < 1 || Hkv < 1 || m < 0 || d < 1 || !valid_dtype(rows_dtype) || (q && Hq < 1))
+        return MP_ERR_INVALID_ARG;
+    if (d != kD) return MP_ERR_UNSUPPORTED;
+    const mp_status st = check_paged(cache, Hkv);
+    if (st != MP_OK) return st;
+    if (inv_freq && (rotary_dims < 16 || rotary_dims > d || rotary_dims % 16))
+        return MP_ERR_UNSUPPORTED;
+    const long long capacity = static_cast<long long>(cache->n_slots) * cache->page_size;
+    if (!positions && (n_begin < 0 || n_begin > capacity - m)) return MP_ERR_INVALID_ARG;
+    if (!aligned(inv_freq, 4) || !aligned(positions, 4) || !aligned(counts, 4) ||
+        !aligned(q_out, 16) || !aligned(keys_out, 16))
+        return MP_ERR_INVALID_ARG;
+    if (m == 0) return MP_OK;
+    if (!valid_rows(keys, rows_dtype, B, Hkv, m) || !valid_rows(values, rows_dtype, B, Hkv, m))
+        return MP_ERR_INVALID_ARG;
+    if (q && (!valid_rows(q, rows_dtype, B, Hq, m) || !q_out)) return MP_ERR_INVALID_ARG;
+    const long long heads = (q ? Hq : 0) + 2ll * Hkv;
+    if (heads > 0x7fffffffll / 4 || static_cast<long long>(B) * m > 0x7fffffffll / heads)
+        return MP_ERR_INVALID_ARG;
+    if (!ensure_prepared()) return MP_ERR_CUDA;
+    return to_status(launch_paged_append(*keys, *values, q, rows_dtype == MP_BF16, inv_freq,
+                                         rotary_dims, interleaved != 0, B, Hq, Hkv, m, n_begin,
+                                         positions, counts, *cache, q_out, keys_out, stream));
+}
+
+size_t mp_paged_attention_workspace_bytes(int B, int Hq, int Hkv, int n, int d) {
+    if (!valid_kv4_attention(B, Hq, Hkv, n, d) || d != kD) return 0;
+    return align256(paged_attention_scratch_bytes(B, Hq, Hkv));
+}
+
+mp_status mp_paged_attention(const void* q, mp_dtype q_dtype, const mp_paged* cache, int B, int Hq,
+                             int Hkv, int n, int d, const int32_t* lengths, float scale, float* out,
+                             void* workspace, size_t ws_bytes, cudaStream_t stream) {
+    if (!valid_kv4_attention(B, Hq, Hkv, n, d) || !valid_dtype(q_dtype)) return MP_ERR_INVALID_ARG;
+    if (d != kD) return MP_ERR_UNSUPPORTED;
+    const mp_status st = check_paged(cache, Hkv);
+    if (st != MP_OK) return st;
+    if (n > static_cast<long long>(cache->n_slots) * cache->page_size || !(scale >= 0.0f) ||
+        isinf(scale))
+        return MP_ERR_INVALID_ARG;
+    if (!q || !out || !aligned(q, q_dtype == MP_BF16 ? 2 : 4) || !aligned(out, 16) ||
+        !aligned(lengths, 4) || !workspace || !aligned(workspace, 256))
+        return MP_ERR_INVALID_ARG;
+    if (ws_bytes < mp_paged_attention_workspace_bytes(B, Hq, Hkv, n, d)) return MP_ERR_WORKSPACE;
+    if (!ensure_prepared()) return MP_ERR_CUDA;
+    return to_status(launch_paged_attention(
+        q, q_dtype == MP_BF16, *cache, B, Hq, Hkv, n, lengths,
+        scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(d)), out, workspace, stream));
+}
+
+mp_status mp_paged_decode_attention(const void* q, mp_dtype q_dtype, const uint32_t* codes,
+                                    const float* centre, const void* W, mp_dtype w_dtype,
+                                    const mp_paged* cache, int B, int Hq, int Hkv, int n, int d,
+                                    const int32_t* lengths, const mp_params* prm, float* out,
+                                    void* workspace, size_t ws_bytes, cudaStream_t stream) {
+    if (B < 1 || Hkv < 1 || !aligned(lengths, 4)) return MP_ERR_INVALID_ARG;
+    const mp_status sp = check_paged(cache, Hkv);
+    if (sp != MP_OK) return sp;
+    DecodeShape s;
+    const mp_status st = check_decode(q, q_dtype, codes, centre, W, w_dtype, cache->keys,
+                                      cache->values, cache->dtype, B, Hq, Hkv, n, d, prm, out,
+                                      workspace, ws_bytes, false, &s);
+    if (st != MP_OK) return st;
+    if (n > static_cast<long long>(cache->n_slots) * cache->page_size) return MP_ERR_INVALID_ARG;
+    if (!ensure_prepared()) return MP_ERR_CUDA;
+    const PageRef pages{cache->page_table, lengths, cache->n_pages, cache->page_size, cache->n_slots,
+                        cache->table_stride};
+    KvRef kv = kv_ref(cache->keys, cache->values, cache->dtype);
+    kv.pages = &pages;
+    const DecodeScratch ws = carve_decode_scratch(workspace, s, false);
+    const cudaError_t e = query_encode(q, q_dtype == MP_BF16, centre, W, w_dtype == MP_BF16, s, ws,
+                                       stream);
+    if (e != cudaSuccess) return MP_ERR_CUDA;
+    return to_status(scan_and_attend(q, q_dtype == MP_BF16, codes, centre, kv, s, out, ws, stream));
 }
 
 mp_status mp_debug_select(const void* q, mp_dtype q_dtype, const uint32_t* codes,

@@ -96,6 +96,73 @@ __global__ void __launch_bounds__(kAppendThreads)
         *dst = (*dst & ~range) | bits;
 }
 
+// The codes of a few tokens of every sequence at places of its own: the definition and the sums of
+// the kernel above (each over e in order), laid out for many heads with a key or a few each. A lane
+// holds one hyperplane's 128 elements in registers, for all the heads its warp takes; keys come from
+// shared memory, centred. Each (plane, word) of a head belongs to one lane, so that a word's bits are
+// replaced by a plain read and write.
+struct AtArgs {
+    const void* keys;
+    const void* W;
+    const float* centre;
+    const int32_t* positions;
+    uint32_t* codes;
+    int* status;
+    int keys_bf16, w_bf16, BH, Hkv, m, ncap, C, cblk;
+};
+constexpr int kAtWarps = 4;                                    // 32 hyperplanes each
+constexpr int kAtHeads = 8;                                    // heads a CTA takes one after another
+
+__global__ void __launch_bounds__(32 * kAtWarps) encode_rows_at_kernel(const AtArgs a) {
+    __shared__ __align__(16) float kbar[kAppendMaxKeys * kD];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int j = (blockIdx.x * kAtWarps + (tid >> 5)) * 32 + lane;
+    float w[kD];
+#pragma unroll
+    for (int e = 0; e < kD; ++e)
+        w[e] = j < a.C ? load_elem(a.W, a.w_bf16, static_cast<size_t>(e) * a.C + j) : 0.0f;
+    const int bh1 = min(a.BH, static_cast<int>(blockIdx.y + 1) * kAtHeads);
+    for (int bh = blockIdx.y * kAtHeads; bh < bh1; ++bh) {
+        const int at = a.positions[bh / a.Hkv];
+        const float mu = a.centre[static_cast<size_t>(bh) * kD + (tid & (kD - 1))];
+        __syncthreads();                                       // the last head's keys are read
+        for (int idx = tid; idx < a.m * kD; idx += 32 * kAtWarps)
+            kbar[idx] = load_elem(a.keys, a.keys_bf16, static_cast<size_t>(bh) * a.m * kD + idx) - mu;
+        __syncthreads();
+        // keys [i0, i1) of the m lie inside the capacity
+        const int i0 = at < 0 ? static_cast<int>(min(static_cast<long long>(a.m),
+                                                     -static_cast<long long>(at))) : 0;
+        const int i1 = static_cast<int>(min(static_cast<long long>(a.m),
+                                            static_cast<long long>(a.ncap) - at));
+        uint32_t range = 0u, bits = 0u;
+        for (int i = i0; i < i1; ++i) {
+            float sum = 0.0f;
+            const float4* k4 = reinterpret_cast<const float4*>(kbar + i * kD);
+#pragma unroll
+            for (int e = 0; e < kD / 4; ++e) {
+                const float4 k = k4[e];
+                sum = fmaf(w[4 * e], k.x, sum);
+                sum = fmaf(w[4 * e + 1], k.y, sum);
+                sum = fmaf(w[4 * e + 2], k.z, sum);
+                sum = fmaf(w[4 * e + 3], k.w, sum);
+            }
+            const int pos = at + i;
+            range |= 1u << (pos & 31);
+            if (sum > 0.0f) bits |= 1u << (pos & 31);
+            if ((pos & 31) == 31 || i + 1 == i1) {             // the word's last key of the range
+                const int blk = pos / kKeysPerBlock;
+                if (j < a.C && mp_check(a.status, blk, a.cblk, kSiteEncodeCodes)) {
+                    uint32_t* dst = a.codes +
+                                    ((static_cast<size_t>(bh) * a.cblk + blk) * a.C + j) *
+                                        kWordsPerBlock + pos % kKeysPerBlock / 32;
+                    *dst = (*dst & ~range) | bits;
+                }
+                range = bits = 0u;
+            }
+        }
+    }
+}
+
 }  // namespace
 
 cudaError_t launch_encode_append(const void* keys, bool keys_bf16, const float* centre,
@@ -115,8 +182,36 @@ cudaError_t launch_encode_append(const void* keys, bool keys_bf16, const float* 
     return cudaGetLastError();
 }
 
+cudaError_t launch_encode_rows_at(const void* keys, bool keys_bf16, const float* centre,
+                                  const void* W, bool w_bf16, int B, int Hkv, int m, int ncap,
+                                  const int32_t* positions, int C, uint32_t* codes,
+                                  cudaStream_t st) {
+    AtArgs a;
+    a.keys = keys;
+    a.W = W;
+    a.centre = centre;
+    a.positions = positions;
+    a.codes = codes;
+    a.status = device_status_ptr();
+    a.keys_bf16 = keys_bf16;
+    a.w_bf16 = w_bf16;
+    a.BH = B * Hkv;
+    a.Hkv = Hkv;
+    a.m = m;
+    a.ncap = ncap;
+    a.C = C;
+    a.cblk = (ncap + kKeysPerBlock - 1) / kKeysPerBlock;
+    const unsigned groups = (a.BH + kAtHeads - 1) / kAtHeads;
+    if (groups > 65535u) return cudaErrorInvalidValue;
+    encode_rows_at_kernel<<<dim3((C + 32 * kAtWarps - 1) / (32 * kAtWarps), groups), 32 * kAtWarps,
+                            0, st>>>(a);
+    return cudaGetLastError();
+}
+
 cudaError_t prepare_append() {
     cudaFuncAttributes fa;
+    const cudaError_t e = cudaFuncGetAttributes(&fa, encode_rows_at_kernel);
+    if (e != cudaSuccess) return e;
     return cudaFuncGetAttributes(&fa, encode_append_kernel);
 }
 

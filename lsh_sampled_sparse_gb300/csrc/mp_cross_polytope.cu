@@ -444,8 +444,9 @@ cudaError_t launch_collide_cp(const void* q, bool q_bf16, const uint8_t* codes,
     a.Hkv = s.Hkv;
     a.L = s.L;
     a.qbytes = s.qwords * 4;
-    a.n_sink = s.n_sink;
-    a.n_local = s.n_local;
+    // over a paged cache T goes by each sequence's own length: the attend kernel's mask
+    a.n_sink = kv.pages ? 0 : s.n_sink;
+    a.n_local = kv.pages ? 0 : s.n_local;
     if (blk0 < s.nblk) {
         const cudaError_t e = launch_dependent(fn, dim3(s.nblk - blk0, s.B * s.Hkv),
                                                dim3(kCpThreads), smem, st, a);

@@ -158,6 +158,7 @@ struct CArgs {
     int n, nblk, Hq, Hkv, K, L, C, cpad, n_sink, n_local;
     int cblk;                                    // code blocks per head in memory
     int blk0;                                    // first block scanned (grid x + blk0)
+    const int32_t* lengths;                      // paged cache: of each sequence, or NULL
     int* status;                                 // index checks of the MP_CHECKS build
 };
 
@@ -370,6 +371,7 @@ struct AArgs {
     const float* radius;                         // MIPS variant: longest centred key per head
     float scale;
     int work_bytes;                              // bytes of the row stage region
+    PageRef pages;                               // paged cache only
 };
 
 // The scan of one (1024-key block, sequence x KV head) for its GQA group of G query heads,
@@ -477,6 +479,11 @@ __global__ void __launch_bounds__(kThreads, 3) collide_kernel(const CArgs a) {
         !mp_check(a.status, blk, a.nblk, kSiteScanCodes))
         return;                                  // the whole CTA: the condition is uniform
     const int b = bg / a.Hkv, g = bg % a.Hkv;
+    if (a.lengths && a.lengths[b] <= blk * kKeysPerBlock) {      // behind the sequence's last key
+        allow_dependents();
+        wait_for_predecessor();
+        return;                                  // its selection words are masked when they are read
+    }
     const int row0 = b * a.Hq + g * G;          // first query row of this KV head's group
     uint32_t* qneg = reinterpret_cast<uint32_t*>(smem);                    // [cpad][G]
     uint32_t* area = qneg + static_cast<size_t>(a.cpad) * G;
@@ -585,7 +592,9 @@ __device__ __forceinline__ unsigned atomic_add_acq_rel_gpu(unsigned* p, unsigned
 // then those of the centred keys (the softmax does not see the difference), and the cosine needs
 // neither the centre nor q.mu.
 // kShared: the rows of a partial are shared by a cluster of 2^share CTAs.
-template <KvForm KV, bool kShared>
+// kPaged: rows lie in pages, each sequence has a length of its own (the scan then leaves valid and T to
+// this kernel's mask), and log u is evaluated for each key, as for the 4-bit cache.
+template <KvForm KV, bool kShared, bool kPaged>
 __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -595,6 +604,9 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
     const int bg = b * a.Hkv + h / a.G;
     const bool exact = sb == a.nsb;              // this CTA takes T
     const int nsp = a.nsb + 1;                   // partials per query row
+    // inputs of the call, like q and the centre
+    const int n = kPaged && a.pages.lengths ? max(0, min(a.n, a.pages.lengths[b])) : a.n;
+    const int32_t* slots = kPaged ? a.pages.table + static_cast<long long>(b) * a.pages.stride : nullptr;
 
     constexpr int kRowBytes = attend_row_bytes(KV);
     constexpr int kPieces = kRowBytes / 16;
@@ -626,11 +638,11 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
 
     // ---- the rows of this CTA: T by arithmetic, or the selected keys of its blocks, found
     //      through the selection words and their prefix counts (no list is materialised)
-    const int t_a = min(a.n_sink, a.n), t_b = max(a.n - a.n_local, t_a);
+    const int t_a = min(a.n_sink, n), t_b = max(n - a.n_local, t_a);
     const int blk0 = sb * kAttendBlocks;
     int nsel;
     if (exact) {
-        nsel = t_a + (a.n - t_b);
+        nsel = t_a + (n - t_b);
     } else {
         const int nb = min(kAttendBlocks, a.nblk - blk0);
         uint32_t U = 0u;
@@ -639,9 +651,9 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
             // lookup's >= 2 bitmap) need valid & not T here
             const int blk = blk0 + warp;
             const int key0 = blk * kKeysPerBlock + lane * 32;
-            const uint32_t valid = bits_below(a.n - key0);
+            const uint32_t valid = bits_below(n - key0);
             const uint32_t tmask =
-                (bits_below(a.n_sink - key0) | ~bits_below(a.n - a.n_local - key0)) & valid;
+                (bits_below(a.n_sink - key0) | ~bits_below(n - a.n_local - key0)) & valid;
             const long long wi = (static_cast<long long>(row) * a.nblk + blk) * 32 + lane;
             if (mp_check(a.status, wi, static_cast<long long>(gridDim.y) * a.nblk * 32,
                          kSiteAttendSelect))
@@ -697,10 +709,9 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
     float m = -INFINITY, l = 0.0f, o[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = 0.0f;
-    const uint8_t* Kg = reinterpret_cast<const uint8_t*>(a.keys) +
-                        static_cast<size_t>(bg) * a.ncap * kHalfBytes;
-    const uint8_t* Vg = reinterpret_cast<const uint8_t*>(a.values) +
-                        static_cast<size_t>(bg) * a.ncap * kHalfBytes;
+    const size_t head0 = kPaged ? 0 : static_cast<size_t>(bg) * a.ncap;
+    const uint8_t* Kg = reinterpret_cast<const uint8_t*>(a.keys) + head0 * kHalfBytes;
+    const uint8_t* Vg = reinterpret_cast<const uint8_t*>(a.values) + head0 * kHalfBytes;
     const uint8_t* Pg = KV == kKv4 ? reinterpret_cast<const uint8_t*>(a.params) +
                                          static_cast<size_t>(bg) * a.ncap * 2 * MP_KV4_PARAMS
                                    : nullptr;
@@ -723,7 +734,8 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
     // One online-softmax step of this half-warp over its rows ent + kHalves j, j < cnt <= NB: the
     // partial sums of NB rows are reduce-scattered so that lanes j LPR .. j LPR + LPR - 1 hold row
     // j's (LPR = 16 / NB), the log-weight is computed lane-parallel, V is folded in.
-    auto fold = [&](int ent, int cnt, auto nb_tag) {
+    // paged: bit j of `there` says whether the j-th of those rows has a page
+    auto fold = [&](int ent, int cnt, auto nb_tag, unsigned there) {
         constexpr int NB = decltype(nb_tag)::value;
         constexpr int LPR = 16 / NB;
         if (cnt <= 0) return;
@@ -796,18 +808,20 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
                     const int ti = min(static_cast<int>(tt), kLuIntervals - 1);
                     const float g0 = __ldg(a.logu_tab + ti), g1 = __ldg(a.logu_tab + ti + 1);
                     lw = fmaf(tt - static_cast<float>(ti), g1 - g0, g0);
-                } else if constexpr (KV == kKv4) {
+                } else if constexpr (KV == kKv4 || kPaged) {
                     lw = log_inclusion_fine(cs, a.fine);
                 } else {
                     lw = log_inclusion_at(cs, a.logu_tab, a.K, a.L);
                 }
             }
             logit = dot * a.scale - lw;
+            if (kPaged && !((there >> jl) & 1u)) logit = -INFINITY;
         }
         float bm = logit;
 #pragma unroll
         for (int sh = 8; sh; sh >>= 1) bm = fmaxf(bm, __shfl_xor_sync(hmask, bm, sh));
-        const float mn = fmaxf(m, bm);
+        float mn = fmaxf(m, bm);
+        if (kPaged && mn == -INFINITY) mn = -3.0e38f;          // none of the rows has a page yet
         const float corr = __expf(m - mn);
         const float wgt = jl < cnt ? __expf(logit - mn) : 0.0f;
         float ws = (hl % LPR) ? 0.0f : wgt;                    // each row counted once
@@ -852,7 +866,10 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
     // the keys of the first kRowKeys entries, listed once; later ones are found on demand (a 4-bit
     // cache's are all listed by now)
     if constexpr (KV != kKv4) {
-        for (int i = tid; i < min(nsel, kRowKeys); i += kAThreads) rowkey[i] = key_of(i);
+        // (paged: their rows of the pool, -1 where a slot holds no page)
+        for (int i = tid; i < min(nsel, kRowKeys); i += kAThreads)
+            rowkey[i] = kPaged ? static_cast<int>(paged_row(a.pages, slots, key_of(i), a.Hkv, h / a.G))
+                               : key_of(i);
         __syncthreads();
     }
     // Group k of a warp: entries hw + 8 (4 k + j), j < 4, of its two half-warps, in the slots
@@ -860,7 +877,10 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
     const int lo_hw = 2 * warp;                  // the warp's first half-warp has its most rows
     const int ngroups = nsel > lo_hw ? ((nsel - lo_hw + kHalves - 1) / kHalves + 3) / 4 : 0;
     const int my_rows = nsel > hw ? (nsel - hw + kHalves - 1) / kHalves : 0;
+    // paged: which rows of groups k and k + 1 have pages, bit 8 (k & 1) + 2 j + half
+    unsigned there = 0u;
     auto issue = [&](int k) {                    // one row (K then V) per instruction, 4-bit: three
+        if (kPaged) there &= ~(0xffu << (8 * (k & 1)));
         if (k < ngroups) {
             constexpr int kAtOnce = KV == kKv4 ? 3 : 1;
             constexpr int kHalfPieces = kHalfBytes / 16;
@@ -874,9 +894,24 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
                 size_t key;
                 if constexpr (KV == kKv4)
                     key = exact ? key_of(e) : blk0 * kKeysPerBlock + rowlist[e];
-                else
+                else if constexpr (kPaged) {
+                    const int at = e < kRowKeys
+                        ? rowkey[e]
+                        : static_cast<int>(paged_row(a.pages, slots, key_of(e), a.Hkv, h / a.G));
+                    if (at < 0) {                // no page: zeros, which its weight of 0 keeps
+                        for (int pc = pc0; pc < kPieces; pc += 32)
+                            *reinterpret_cast<uint4*>(stage + r * kRowBytes + 16 * pc) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                        continue;
+                    }
+                    there |= 1u << (8 * (k & 1) + jj);
+                    key = static_cast<size_t>(at);
+                } else
                     key = static_cast<size_t>(e < kRowKeys ? rowkey[e] : key_of(e));
-                if (!mp_check(a.status, static_cast<long long>(key), min(a.n, a.ncap),
+                if (!mp_check(a.status, static_cast<long long>(key),
+                              kPaged ? static_cast<long long>(a.pages.n_pages) * a.Hkv *
+                                           a.pages.page_size
+                                     : min(a.n, a.ncap),
                               kSiteAttendRow))
                     continue;
                 for (int pc = pc0; pc < kPieces; pc += 32) {
@@ -889,13 +924,19 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
         }
         cp_async_commit();                       // one group per call, empty or not
     };
+    // bit j: whether this half-warp's j-th row of group k has a page
+    auto rows_there = [&](int k) -> unsigned {
+        if (!kPaged) return ~0u;
+        const unsigned t = there >> (8 * (k & 1) + half);
+        return (t & 1u) | (t >> 1 & 2u) | (t >> 2 & 4u) | (t >> 3 & 8u);
+    };
     issue(0);
     issue(1);
     for (int k = 0; k < ngroups; ++k) {
         cp_async_wait_pending<1>();              // group k has landed (group k + 1 may not have)
         __syncwarp();
         fold(hw + kHalves * 4 * (k & 1), min(4, max(0, my_rows - 4 * k)),
-             std::integral_constant<int, 4>());
+             std::integral_constant<int, 4>(), rows_there(k));
         __syncwarp();                            // every lane is done with group k's slots
         issue(k + 2);
     }
@@ -1084,10 +1125,14 @@ KernelFn pick_collide(int G) {
 
 typedef void (*AttendFn)(const AArgs);
 
-AttendFn pick_attend(KvForm form, bool shared = false) {
-    return form == kKv4 ? (shared ? attend_kernel<kKv4, true> : attend_kernel<kKv4, false>)
-                        : (form == kKvBf16 ? attend_kernel<kKvBf16, false>
-                                           : attend_kernel<kKvF32, false>);
+AttendFn pick_attend(KvForm form, bool shared = false, bool paged = false) {
+    if (paged)
+        return form == kKvBf16 ? attend_kernel<kKvBf16, false, true>
+                               : attend_kernel<kKvF32, false, true>;
+    return form == kKv4 ? (shared ? attend_kernel<kKv4, true, false>
+                                  : attend_kernel<kKv4, false, false>)
+                        : (form == kKvBf16 ? attend_kernel<kKvBf16, false, false>
+                                           : attend_kernel<kKvF32, false, false>);
 }
 
 size_t collide_smem_for(int G, int cpad, int K) {
@@ -1120,9 +1165,9 @@ cudaError_t prepare_decode() {
                                              static_cast<int>(kMaxSmem));
         if (e != cudaSuccess) return e;
     }
-    for (KvForm form : {kKvF32, kKvBf16, kKv4}) {
-        cudaError_t e = cudaFuncSetAttribute(pick_attend(form),
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+    for (const AttendFn fn : {pick_attend(kKvF32), pick_attend(kKvBf16), pick_attend(kKv4),
+                              pick_attend(kKvF32, false, true), pick_attend(kKvBf16, false, true)}) {
+        cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(kMaxSmem));
         if (e != cudaSuccess) return e;
     }
@@ -1141,7 +1186,9 @@ cudaError_t prepare_decode() {
                          reinterpret_cast<const void*>(pick_attend(kKvF32)),
                          reinterpret_cast<const void*>(pick_attend(kKvBf16)),
                          reinterpret_cast<const void*>(pick_attend(kKv4)),
-                         reinterpret_cast<const void*>(pick_attend(kKv4, true))};
+                         reinterpret_cast<const void*>(pick_attend(kKv4, true)),
+                         reinterpret_cast<const void*>(pick_attend(kKvF32, false, true)),
+                         reinterpret_cast<const void*>(pick_attend(kKvBf16, false, true))};
     for (const void* f : fns) {
         cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
                                              cudaSharedmemCarveoutMaxShared);
@@ -1216,6 +1263,7 @@ CArgs scan_args(const uint32_t* codes, const DecodeShape& s, const DecodeScratch
     ca.n_local = s.n_local;
     ca.cblk = s.cblk;
     ca.blk0 = blk0;
+    ca.lengths = nullptr;
     ca.status = device_status_ptr();
     return ca;
 }
@@ -1226,7 +1274,12 @@ cudaError_t launch_collide(const void* q, bool q_bf16, const uint32_t* codes,
                            const float* centre, const KvRef& kv, const DecodeShape& s,
                            float* out, const DecodeScratch& ws, cudaStream_t st, int blk0) {
     const int G = s.Hq / s.Hkv;
-    const CArgs ca = scan_args(codes, s, ws, blk0);
+    CArgs ca = scan_args(codes, s, ws, blk0);
+    if (kv.pages) {
+        // T and the valid keys go by each sequence's own length: the attend kernel's mask
+        ca.lengths = kv.pages->lengths;
+        ca.n_sink = ca.n_local = 0;
+    }
     KernelFn scan = pick_collide(G);
     const size_t smem_scan = collide_smem_for(G, s.cpad, s.K);
     if (!scan || smem_scan > kMaxSmem || attend_smem_for(kv.form) > kMaxSmem)
@@ -1278,6 +1331,7 @@ cudaError_t launch_attend(const void* q, bool q_bf16, const float* centre, const
     aa.radius = s.radius;
     aa.scale = s.scale;
     aa.work_bytes = static_cast<int>(attend_smem(kv.form).work);
+    aa.pages = kv.pages ? *kv.pages : PageRef{};
     // While the GPU holds more CTAs than there are (six an SM), a CTA with more rows than twice its
     // slots shares them with up to seven others: of keys without a bias toward the query a share of
     // 1 - (1 + x) e^-x collides twice, x = L times the chance in one table. 16 query heads, 3194
@@ -1293,7 +1347,7 @@ cudaError_t launch_attend(const void* q, bool q_bf16, const float* centre, const
     while (kv.form == kKv4 && rows > 2 * kAttendRows && aa.share < 3 &&
            ctas << (aa.share + 1) <= 6 * device_sm_count())
         ++aa.share;
-    const AttendFn attend = pick_attend(kv.form, aa.share > 0);
+    const AttendFn attend = pick_attend(kv.form, aa.share > 0, kv.pages != nullptr);
     return launch_dependent(attend, dim3((aa.nsb + 1) << aa.share, s.B * s.Hq), dim3(kAThreads),
                             smem_att, st, aa, 1 << aa.share);
 }

@@ -46,6 +46,8 @@ enum CheckSite : int {
     kSiteKv4Out = 11,            // rows read back, partial states or output rows of its attention
     kSiteEncodeRow = 12,         // a key row that a CUDA-core encoder reads
     kSiteAttendList = 13,        // the list of selected keys of an attend CTA (shared memory)
+    kSitePagedRow = 14,          // a row of the paged cache written, read or copied
+    kSitePagedOut = 15,          // rows returned by an append, partial states, output rows
 };
 
 // Index check of the MP_CHECKS build (the memory checker's stand-in): there an index outside
@@ -98,11 +100,19 @@ struct DecodeShape {
 // The keys and values a decode attends to: rows of 128 fp32 or bf16 elements, or the 4-bit cache
 // (keys, values: its codes; params: its steps and minima; the keys are held minus their centre).
 enum KvForm : int { kKvF32 = 0, kKvBf16 = 1, kKv4 = 2 };
+// With a page table the rows lie in pages of a pool, [page][Hkv][page_size], and each sequence has a
+// length of its own.
+struct PageRef {
+    const int32_t* table;
+    const int32_t* lengths;                      // NULL: n
+    int n_pages, page_size, n_slots, stride;
+};
 struct KvRef {
     const void* keys;
     const void* values;
     const void* params;  // kKv4 only
     KvForm form;
+    const PageRef* pages = nullptr;              // kKvF32 and kKvBf16 only
 };
 inline KvRef kv_ref(const void* keys, const void* values, mp_dtype t) {
     return KvRef{keys, values, nullptr, t == MP_BF16 ? kKvBf16 : kKvF32};
@@ -152,6 +162,13 @@ cudaError_t launch_encode_append(const void* keys, bool keys_bf16, const float* 
                                  const void* W, bool w_bf16, int B, int Hkv, int head_rows, int row0,
                                  int ncap, int n0, int n1, int K, int L, uint32_t* codes,
                                  cudaStream_t st);
+
+// Encode keys [B*Hkv][m][d] (m <= kAppendMaxKeys) at positions[b] .. of each sequence, into codes laid
+// out for ncap, keeping the other keys' bits
+cudaError_t launch_encode_rows_at(const void* keys, bool keys_bf16, const float* centre,
+                                  const void* W, bool w_bf16, int B, int Hkv, int m, int ncap,
+                                  const int32_t* positions, int C, uint32_t* codes,
+                                  cudaStream_t st);
 
 // query sign bits, |q| and q.mu into the scratch; also resets the merge counters
 cudaError_t launch_qencode(const void* q, bool q_bf16, const float* centre, const void* W,
@@ -204,6 +221,7 @@ cudaError_t prepare_append();
 cudaError_t prepare_mips();
 cudaError_t prepare_cross_polytope();
 cudaError_t prepare_kv4();
+cudaError_t prepare_paged();
 
 // ---- 4-bit K/V cache (mp_kv4.cu) ----------------------------------------------------------------
 // rows [n_begin, n_begin + m) (or from positions[b] on) of every head written / read back
@@ -218,6 +236,18 @@ bool kv4_attention_uses_scratch(int B, int Hq, int Hkv, int n);      // of n tok
 cudaError_t launch_kv4_attention(const void* q, bool q_bf16, const mp_kv4& cache, int B, int Hq,
                                  int Hkv, int n, const int32_t* lengths, float scale, float* out,
                                  void* workspace, cudaStream_t st);
+
+// ---- paged K/V cache (mp_paged.cu) ---------------------------------------------------------------
+// m tokens of every sequence into its pages, q and keys turned by their positions on the way
+cudaError_t launch_paged_append(const mp_rows& keys, const mp_rows& values, const mp_rows* q,
+                                bool rows_bf16, const float* inv_freq, int rotary_dims,
+                                bool interleaved, int B, int Hq, int Hkv, int m, int n_begin,
+                                const int32_t* positions, const int32_t* counts,
+                                const mp_paged& cache, void* q_out, void* keys_out, cudaStream_t st);
+size_t paged_attention_scratch_bytes(int B, int Hq, int Hkv);
+cudaError_t launch_paged_attention(const void* q, bool q_bf16, const mp_paged& cache, int B, int Hq,
+                                   int Hkv, int n, const int32_t* lengths, float scale, float* out,
+                                   void* workspace, cudaStream_t st);
 
 // ---- cross-polytope variant (mp_cross_polytope.cu) ----------------------------------------------
 size_t cp_codes_bytes(int B, int Hkv, int n, int L);
@@ -267,6 +297,16 @@ cudaError_t launch_dependent(void (*kern)(Arg), dim3 grid, dim3 block, size_t sm
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, arg);
+}
+
+// The pool row of token `key` of a sequence with this row of a page table and KV head g; -1 where its
+// slot holds no page. key lies in [0, n_slots page_size).
+__device__ __forceinline__ long long paged_row(const PageRef& p, const int32_t* slots, int key,
+                                               int Hkv, int g) {
+    const int slot = key / p.page_size, pg = slots[slot];
+    return pg >= 0 && pg < p.n_pages
+               ? (static_cast<long long>(pg) * Hkv + g) * p.page_size + (key - slot * p.page_size)
+               : -1;
 }
 
 // ---- small device helpers ---------------------------------------------------------------------
