@@ -8,7 +8,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "mp_internal.cuh"
+#include "mp_paged.cuh"
 
 namespace mp {
 namespace {
@@ -16,12 +16,6 @@ namespace {
 constexpr int kSms = 152;                        // of a GB300; a workspace's size is the same on the
                                                  // host alone
 using Bf16 = __nv_bfloat16;
-
-__device__ __forceinline__ float exp2_fast(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 
 // ------------------------------------------------------------------------------------------------
 // Append. Pair j of a row at position p turns by a = p inv_freq[j]; in half turns a / pi = 2 frac(p t)
@@ -174,163 +168,14 @@ __global__ void __launch_bounds__(kAppThreads) paged_append_kernel(const AppendA
     }
 }
 
-// ------------------------------------------------------------------------------------------------
-// Attention of one query token per sequence.
-//
-// A unit is (sequence, KV head, chunk of up to NH query heads of its group); its keys come in tiles.
-// The tiles of all units, laid end to end, are shared out evenly over as many CTAs as the GPU holds at
-// once, by the lengths themselves: each CTA takes a run of tiles, whatever units they belong to. A
-// unit that one CTA has to itself is written out by that CTA; the others' partial softmax states (at
-// most two a CTA: the rest of a unit that began before, the beginning of one that ends after) go to
-// the workspace and are joined by a second kernel in a fixed order.
-// ------------------------------------------------------------------------------------------------
-struct PArgs {
-    const void* q;
-    const void* keys;
-    const void* values;
-    PageRef pages;
-    float* part;                                 // [CTA][2][NH][kPart]: o, m, l
-    long long* before;                           // [B + 1] tiles of the sequences before (lengths only)
-    float* out;
-    int q_bf16, B, Hq, Hkv, G, chunks, nh, n, ctas, tile;
-    float scale;                                 // of q.k, times log2 e
-    int* status;                                 // index checks of the MP_CHECKS build
-};
-constexpr int kPart = kD + 4;
-
-__device__ __forceinline__ int length_of(const PArgs& a, int b) {
-    return a.pages.lengths ? max(0, min(a.n, a.pages.lengths[b])) : a.n;
-}
-__device__ __forceinline__ int tiles_of(const PArgs& a, int len) { return (len + a.tile - 1) / a.tile; }
-// How many CTAs share `total` tiles, the first tile of CTA c, the CTA that has tile t
-__device__ __forceinline__ int shares_of(const PArgs& a, long long total) {
-    return static_cast<int>(min(static_cast<long long>(a.ctas), total));
-}
-__device__ __forceinline__ long long first_tile(long long total, int shares, int c) {
-    return total * c / shares;
-}
-__device__ __forceinline__ int share_with(long long total, int shares, long long t) {
-    return static_cast<int>(((t + 1) * shares - 1) / total);
-}
-
-// Where a CTA's run of tiles begins, and how many there are; walked through by next().
-struct Walk {
-    long long left;                              // tiles of the run from here on
-    int b, unit, t, tiles, len;                  // unit of the sequence, its next tile, all its tiles
-    __device__ __forceinline__ int here() const {
-        return static_cast<int>(min(left, static_cast<long long>(tiles - t)));
-    }
-    // past `here` tiles: the next unit, if the run goes on
-    __device__ __forceinline__ void next(const PArgs& a, int here) {
-        left -= here;
-        t = 0;
-        if (left <= 0 || ++unit < a.Hkv * a.chunks) return;
-        unit = 0;
-        do {
-            len = length_of(a, ++b);
-            tiles = tiles_of(a, len);
-        } while (tiles == 0);
-    }
-};
-
-struct PlanSmem {
-    long long warp_sum[32];
-    Walk walk;
-};
-// The run of this CTA; every thread of the CTA calls it. CTA 0 leaves the sums for the join.
-__device__ inline Walk plan_run(const PArgs& a, PlanSmem& s) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
-    const int per_tile = a.Hkv * a.chunks;       // tiles of a sequence for each tile of its length
-    if (!a.pages.lengths) {
-        Walk w;
-        w.len = a.n;
-        w.tiles = tiles_of(a, a.n);
-        const long long each = static_cast<long long>(per_tile) * w.tiles, total = each * a.B;
-        const int shares = shares_of(a, total);
-        const long long lo = first_tile(total, shares, c);
-        w.left = c < shares ? first_tile(total, shares, c + 1) - lo : 0;
-        w.b = static_cast<int>(lo / each);
-        const long long in_b = lo - w.b * each;
-        w.unit = static_cast<int>(in_b / w.tiles);
-        w.t = static_cast<int>(in_b - static_cast<long long>(w.unit) * w.tiles);
-        return w;
-    }
-    // a stretch of sequences a thread, their sums added up over the CTA
-    const int each = (a.B + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
-    const int b0 = min(a.B, tid * each), b1 = min(a.B, b0 + each);
-    long long sum = 0;
-    for (int b = b0; b < b1; ++b) sum += static_cast<long long>(per_tile) * tiles_of(a, length_of(a, b));
-    long long incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) s.warp_sum[warp] = incl;
-    if (tid == 0) s.walk.left = 0;
-    __syncthreads();
-    long long before = incl - sum, total = 0;
-    for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) {
-        if (w < warp) before += s.warp_sum[w];
-        total += s.warp_sum[w];
-    }
-    const int shares = shares_of(a, total);
-    const long long lo = shares > 0 ? first_tile(total, shares, c) : 0;
-    const bool mine = c < shares && lo >= before && lo < before + sum;
-    if (c == 0 || mine) {
-        for (int b = b0; b < b1; ++b) {
-            if (c == 0) a.before[b] = before;
-            const int len = length_of(a, b), tiles = tiles_of(a, len);
-            const long long here = static_cast<long long>(per_tile) * tiles;
-            if (mine && lo >= before && lo < before + here) {
-                Walk w;
-                w.left = first_tile(total, shares, c + 1) - lo;
-                w.b = b;
-                w.unit = static_cast<int>((lo - before) / tiles);
-                w.t = static_cast<int>(lo - before - static_cast<long long>(w.unit) * tiles);
-                w.tiles = tiles;
-                w.len = len;
-                s.walk = w;
-            }
-            before += here;
-        }
-        if (c == 0 && tid == static_cast<int>(blockDim.x) - 1) a.before[a.B] = total;
-    }
-    __syncthreads();
-    return s.walk;
-}
-
-// Where a unit's state goes: out, where the CTA has all its tiles, else one of its two places
-__device__ __forceinline__ float* part_of(const PArgs& a, bool from_start, int h) {
-    return a.part + ((static_cast<size_t>(blockIdx.x) * 2 + (from_start ? 1 : 0)) * a.nh + h) * kPart;
-}
-
-// CUDA cores: a warp takes groups of four tokens, a lane four dims of each. The NH scores of four
+// A float32 cache, on CUDA cores: a warp takes groups of four tokens, a lane four dims of each. The NH scores of four
 // tokens are summed over the lanes by a reduce-scatter, which leaves a score a lane (two lanes where
 // NH = 4), the softmax steps are lane-parallel, weights come back through shared memory.
 constexpr int kSimtWarps = 8;
 constexpr int kSimtThreads = 32 * kSimtWarps;
 constexpr int kSimtTile = 4 * kSimtWarps;        // tokens
 
-template <typename T>
-struct Four;                                     // four elements as they are in memory
-template <>
-struct Four<float> {
-    float4 v;
-    __device__ __forceinline__ void get(float (&x)[4]) const { x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w; }
-};
-template <>
-struct Four<Bf16> {
-    uint2 v;
-    __device__ __forceinline__ void get(float (&x)[4]) const {
-        x[0] = __uint_as_float(v.x << 16);
-        x[1] = __uint_as_float(v.x & 0xffff0000u);
-        x[2] = __uint_as_float(v.y << 16);
-        x[3] = __uint_as_float(v.y & 0xffff0000u);
-    }
-};
-
-template <typename T, int NH>
+template <int NH>
 __global__ void __launch_bounds__(kSimtThreads, 2) paged_attention_simt_kernel(const PArgs a) {
     __shared__ PlanSmem plan;
     __shared__ __align__(16) float weights[kSimtWarps][4 * NH + NH];
@@ -351,7 +196,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attention_simt_kernel(c
             for (int e = 0; e < 4; ++e)
                 q[h][e] = h < heads ? load_elem(a.q, a.q_bf16, (row0 + h) * kD + 4 * lane + e) : 0.0f;
         // a group of tokens: four of one page (pages hold multiples of eight)
-        Four<T> kn[4], vn[4];
+        float4 kn[4], vn[4];
         int live = 0;
         auto load = [&](int k) {
             const int tok = (w.t + k) * kSimtTile + 4 * warp;
@@ -362,16 +207,15 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attention_simt_kernel(c
                                                                 a.Hkv * a.pages.page_size,
                                          kSitePagedRow))
                     live = min(4, w.len - tok);
-                const T* kp = static_cast<const T*>(a.keys) + row * kD + 4 * lane;
-                const T* vp = static_cast<const T*>(a.values) + row * kD + 4 * lane;
+                const float* kp = static_cast<const float*>(a.keys) + row * kD + 4 * lane;
+                const float* vp = static_cast<const float*>(a.values) + row * kD + 4 * lane;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if (i < live) {
-                        kn[i].v = *reinterpret_cast<const decltype(kn[i].v)*>(kp + i * kD);
-                        vn[i].v = *reinterpret_cast<const decltype(vn[i].v)*>(vp + i * kD);
+                        kn[i] = *reinterpret_cast<const float4*>(kp + i * kD);
+                        vn[i] = *reinterpret_cast<const float4*>(vp + i * kD);
                     } else {
-                        kn[i].v = {};
-                        vn[i].v = {};
+                        kn[i] = vn[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     }
                 }
             }
@@ -387,13 +231,15 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attention_simt_kernel(c
             float v[4][4], s[4 * NH];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float x[4];
-                kn[i].get(x);
-                vn[i].get(v[i]);
+                const float4 x = kn[i];
+                v[i][0] = vn[i].x;
+                v[i][1] = vn[i].y;
+                v[i][2] = vn[i].z;
+                v[i][3] = vn[i].w;
 #pragma unroll
                 for (int h = 0; h < NH; ++h)
-                    s[i * NH + h] = fmaf(x[3], q[h][3], fmaf(x[2], q[h][2],
-                                                             fmaf(x[1], q[h][1], x[0] * q[h][0])));
+                    s[i * NH + h] = fmaf(x.w, q[h][3], fmaf(x.z, q[h][2],
+                                                            fmaf(x.y, q[h][1], x.x * q[h][0])));
             }
             load(k + 1);
             if (now == 0) continue;
@@ -570,9 +416,8 @@ constexpr int kSimtCtas = 2 * kSms;
 int simt_heads(int G) { return G <= 4 ? 4 : 8; }
 
 typedef void (*PFn)(const PArgs);
-PFn pick_simt(bool bf16, int nh) {
-    if (bf16) return nh == 4 ? paged_attention_simt_kernel<Bf16, 4> : paged_attention_simt_kernel<Bf16, 8>;
-    return nh == 4 ? paged_attention_simt_kernel<float, 4> : paged_attention_simt_kernel<float, 8>;
+PFn pick_simt(int nh) {
+    return nh == 4 ? paged_attention_simt_kernel<4> : paged_attention_simt_kernel<8>;
 }
 
 typedef void (*AppendFn)(const AppendArgs);
@@ -627,9 +472,10 @@ cudaError_t launch_paged_append(const mp_rows& keys, const mp_rows& values, cons
 }
 
 size_t paged_attention_scratch_bytes(int B, int Hq, int Hkv) {
-    const int nh = simt_heads(Hq / Hkv);
-    return static_cast<size_t>(kSimtCtas) * 2 * nh * kPart * sizeof(float) +
-           (static_cast<size_t>(B) + 1) * sizeof(long long);
+    // of either kind of cache: who asks does not say which
+    const size_t parts = std::max(kSimtCtas * simt_heads(Hq / Hkv),
+                                  kPagedTcCtas * paged_tc_heads(Hq / Hkv));
+    return parts * 2 * kPart * sizeof(float) + (static_cast<size_t>(B) + 1) * sizeof(long long);
 }
 
 cudaError_t launch_paged_attention(const void* q, bool q_bf16, const mp_paged& cache, int B, int Hq,
@@ -646,17 +492,19 @@ cudaError_t launch_paged_attention(const void* q, bool q_bf16, const mp_paged& c
     a.Hq = Hq;
     a.Hkv = Hkv;
     a.G = Hq / Hkv;
-    a.nh = simt_heads(a.G);
+    const bool tc = cache.dtype == MP_BF16;
+    a.nh = tc ? paged_tc_heads(a.G) : simt_heads(a.G);
     a.chunks = (a.G + a.nh - 1) / a.nh;
     a.n = n;
-    a.ctas = kSimtCtas;
-    a.tile = kSimtTile;
+    a.ctas = tc ? kPagedTcCtas : kSimtCtas;
+    a.tile = tc ? kPagedTcTile : kSimtTile;
     a.scale = scale * 1.4426950408889634f;
     a.status = device_status_ptr();
     a.part = static_cast<float*>(workspace);
     a.before = reinterpret_cast<long long*>(a.part + static_cast<size_t>(a.ctas) * 2 * a.nh * kPart);
-    const cudaError_t e = launch_dependent(pick_simt(cache.dtype == MP_BF16, a.nh), dim3(a.ctas),
-                                           dim3(kSimtThreads), 0, st, a);
+    const cudaError_t e = tc ? launch_paged_attention_tc(a, cache, st)
+                             : launch_dependent(pick_simt(a.nh), dim3(a.ctas), dim3(kSimtThreads), 0,
+                                                st, a);
     if (e != cudaSuccess) return e;
     return launch_dependent(paged_join_kernel, dim3(static_cast<unsigned>(B) * Hq),
                             dim3(32 * kJoinWarps), 0, st, a);
@@ -667,8 +515,10 @@ cudaError_t prepare_paged() {
     cudaError_t e;
     for (int i = 0; i < 4; ++i) {
         if ((e = cudaFuncGetAttributes(&fa, pick_append(i & 1, i & 2))) != cudaSuccess) return e;
-        if ((e = cudaFuncGetAttributes(&fa, pick_simt(i & 1, i & 2 ? 4 : 8))) != cudaSuccess) return e;
     }
+    for (int nh : {4, 8})
+        if ((e = cudaFuncGetAttributes(&fa, pick_simt(nh))) != cudaSuccess) return e;
+    if ((e = prepare_paged_tc()) != cudaSuccess) return e;
     return cudaFuncGetAttributes(&fa, paged_join_kernel);
 }
 

@@ -1,0 +1,517 @@
+// Exact attention of single query tokens over a bf16 paged cache, on the tcgen05 tensor cores.
+//
+// A tile is 128 tokens. Scores: S = K Q^T with the tile's keys as the 128 rows of the MMA and the
+// query heads as its columns, sums in tensor memory, a token a lane. Values: O = V^T P with the 128
+// dims as rows (the same layout of V in shared memory read with its dims along M) and the heads'
+// weights as columns. Keys and values so go from memory to the tensor cores by TMA alone: no register
+// and no instruction of theirs, whatever the heads that share them. A float32 number (a query element
+// of a float32 query, a weight) meets the bf16 ones as three bf16 terms, 24 bits, a column each; a bf16
+// query is one term. Products are exact, sums float32.
+//
+// TMA: keys and values are tensors [page x head][8-token groups][2 halves][8 tokens][64 dims], boxes one
+// page's part of a tile. In shared memory a group of 8 tokens by 64 dims is one 128-byte-swizzled
+// kilobyte, which K reads as 8 rows along M and V as 8 steps along K. A box whose slot holds no page,
+// or that begins behind the sequence's end, is taken from outside the tensor: it reads as zeros, and
+// no memory is touched.
+//
+// Structure, one CTA an SM, on a run of tiles of its own (mp_paged.cuh):
+//   warps 0-3  softmax: S from tensor memory, masks, running maximum (over a warp by redux, over the
+//              four through shared memory), weights in three terms to shared memory; the last tile's O
+//              from tensor memory into float32 registers, a dim a thread
+//   warp 4     TMA producer: rings of K and V tiles of 32 KB, a box a lane
+//   warp 5     allocates tensor memory, issues the MMAs: S of the next tile before O of this one
+//   warp 6     queries of the next unit into shared memory
+// The sums of a tile start from zero and are added up in registers: the tensor core's own sums round
+// toward zero, which stays small over 128 tokens.
+//
+// Every wait is bounded; on expiry the CTA records MP_ERR_TIMEOUT in the device status word, stops
+// issuing work and still frees its tensor memory.
+#include <algorithm>
+
+#include "mp_paged.cuh"
+#include "mp_tcgen05.cuh"
+
+namespace mp {
+namespace {
+
+constexpr int kTile = kPagedTcTile;              // tokens
+constexpr int kSoftWarps = 4, kSoftThreads = 32 * kSoftWarps;
+constexpr int kWarps = 7, kThreads = 32 * kWarps;
+constexpr uint32_t kStage = kTile * kD * 2;      // 32 KB: a tile of K or of V
+constexpr uint32_t kGroup = 2048;                // 8 tokens: two swizzled kilobytes
+constexpr int kTerms = 3;
+
+template <int NH>
+struct Lay {
+    static constexpr int kN = (kTerms * NH + 15) / 16 * 16;              // columns of an MMA
+    static constexpr int kColumns = kN <= 16 ? 16 : (kN <= 32 ? 32 : 64);    // apart in tensor memory
+    static constexpr int kTmem = kColumns == 16 ? 64 : 4 * kColumns;     // S, S, O
+    static constexpr int kKStages = 3, kVStages = NH <= 8 ? 3 : 2;
+    static constexpr uint32_t kOperand = kN * kD * 2;                    // Q, or P: N rows of 256 bytes
+    static constexpr uint32_t kOffV = kKStages * kStage;
+    static constexpr uint32_t kOffP = kOffV + kVStages * kStage;
+    static constexpr uint32_t kOffQ = kOffP + kOperand;
+    static constexpr uint32_t kOffBars = kOffQ + 2 * kOperand;
+    static constexpr uint32_t kOffMax = kOffBars + 256;                  // [2][warps][NH]
+    static constexpr uint32_t kOffPlan = kOffMax + 2 * kSoftWarps * NH * 4;
+    static constexpr uint32_t kBytes = kOffPlan + sizeof(PlanSmem) + 1024;   // + alignment slack
+    static_assert(kBytes <= 232448, "shared memory budget");
+    static_assert(kOperand % 1024 == 0, "swizzled operands start on 1024-byte boundaries");
+};
+
+// Three bf16 terms of two floats, packed (low: the first)
+__device__ __forceinline__ uint32_t pack_bf16(float low, float high) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(high), "f"(low));
+    return r;
+}
+__device__ __forceinline__ void three_terms(float a, float b, uint32_t (&t)[kTerms]) {
+#pragma unroll
+    for (int i = 0; i < kTerms; ++i) {
+        t[i] = pack_bf16(a, b);
+        a -= __uint_as_float(t[i] << 16);
+        b -= __uint_as_float(t[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ float warp_max(float x) {                     // of what is not NaN
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ void softmax_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory");
+}
+
+template <int NH>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attention_tc_kernel(const __grid_constant__ CUtensorMap kmap,
+                              const __grid_constant__ CUtensorMap vmap, const PArgs a) {
+    using L = Lay<NH>;
+    constexpr int N = L::kN;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_word;
+    volatile int* abort_flag = &abort_word;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = smem_u32(smem);
+    const uint32_t k_full = base + L::kOffBars, k_empty = k_full + 8 * L::kKStages;
+    const uint32_t v_full = k_empty + 8 * L::kKStages, v_empty = v_full + 8 * L::kVStages;
+    const uint32_t s_full = v_empty + 8 * L::kVStages, s_empty = s_full + 16;
+    const uint32_t q_full = s_empty + 16, q_empty = q_full + 16;
+    const uint32_t p_full = q_empty + 16, o_full = p_full + 8;
+    if (tid == 0) {
+        for (int i = 0; i < 2 * (L::kKStages + L::kVStages); ++i) mbar_init(k_full + 8 * i, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(s_empty + 8 * i, kSoftWarps);
+            mbar_init(q_full + 8 * i, 1);
+            mbar_init(q_empty + 8 * i, 1);
+        }
+        mbar_init(p_full, kSoftWarps);
+        mbar_init(o_full, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 5) tmem_alloc(smem_u32(&tmem_slot), L::kTmem);
+    tc_fence_before();
+    wait_for_predecessor();
+    allow_dependents();
+    const Walk run = plan_run(a, *reinterpret_cast<PlanSmem*>(smem + L::kOffPlan));
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem_o = tmem + 2 * L::kColumns;
+    Walk w = run;
+
+    if (warp < kSoftWarps) {
+        // ---------------- softmax ----------------
+        const uint32_t quad = static_cast<uint32_t>(warp * 32) << 16;    // this warp's TMEM lanes
+        const uint32_t chunk = (tid & 63) >> 3;
+        const uint32_t p_at = base + L::kOffP + (tid >> 6) * (N * 128) + (chunk << 4) + (tid & 7) * 2;
+        bool aborted = false;
+        auto wait = [&](uint32_t bar, int phase) {
+            if (!aborted)
+                aborted = !__all_sync(0xffffffffu, mbar_wait(bar, phase & 1, abort_flag, a.status));
+        };
+        int it = 0;
+        while (w.left > 0) {
+            const int here = w.here(), g = w.unit / a.chunks, h0 = (w.unit - g * a.chunks) * NH;
+            const int32_t* slots = a.pages.table + static_cast<long long>(w.b) * a.pages.stride;
+            float m[NH], l[NH], o[NH];
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+                m[h] = -INFINITY;
+                l[h] = o[h] = 0.0f;
+            }
+            auto add_o = [&](int at) {           // the sums of tile `at`, added to the running ones
+                wait(o_full, at);
+                if (aborted) return;
+                tc_fence_after();
+                uint32_t t0[NH], t1[NH], t2[NH];
+                tmem_ld(tmem_o + quad, t0);
+                tmem_ld(tmem_o + quad + NH, t1);
+                tmem_ld(tmem_o + quad + 2 * NH, t2);
+                tmem_ld_wait();
+#pragma unroll
+                for (int h = 0; h < NH; ++h)
+                    o[h] += __uint_as_float(t0[h]) +
+                            (__uint_as_float(t1[h]) + __uint_as_float(t2[h]));
+            };
+            auto page_at = [&](int k) {          // the slot of this thread's token of tile k
+                const int tok = (w.t + k) * kTile + tid;
+                return k < here && tok < w.len ? slots[tok / a.pages.page_size] : -1;
+            };
+            int page = page_at(0);
+            for (int k = 0; k < here; ++k, ++it) {
+                const int tok0 = (w.t + k) * kTile;
+                const bool live = page >= 0 && page < a.pages.n_pages;   // and before the end
+                page = page_at(k + 1);
+                float s[NH];
+                wait(s_full + 8 * (it & 1), it >> 1);
+                if (!aborted) {
+                    tc_fence_after();
+                    const uint32_t from = tmem + quad + (it & 1) * L::kColumns;
+                    uint32_t t0[NH];
+                    tmem_ld(from, t0);
+                    if (!a.q_bf16) {
+                        uint32_t t1[NH], t2[NH];
+                        tmem_ld(from + NH, t1);
+                        tmem_ld(from + 2 * NH, t2);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int h = 0; h < NH; ++h)
+                            s[h] = __uint_as_float(t0[h]) +
+                                   (__uint_as_float(t1[h]) + __uint_as_float(t2[h]));
+                    } else {
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int h = 0; h < NH; ++h) s[h] = __uint_as_float(t0[h]);
+                    }
+                } else {
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) s[h] = 0.0f;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_empty + 8 * (it & 1));
+                // ---- the tile's maxima, over the warp and over the four
+                float* most = reinterpret_cast<float*>(smem + L::kOffMax) + (it & 1) * kSoftWarps * NH;
+                float mine[NH];
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    s[h] = live ? s[h] * a.scale : -INFINITY;
+                    mine[h] = warp_max(s[h]);
+                }
+                if (lane == 0) {
+#pragma unroll
+                    for (int h = 0; h < NH; h += 4)
+                        *reinterpret_cast<float4*>(most + warp * NH + h) =
+                            make_float4(mine[h], mine[h + 1], mine[h + 2], mine[h + 3]);
+                }
+                softmax_sync();
+                float corr[NH];
+#pragma unroll
+                for (int h = 0; h < NH; h += 4) {
+                    float4 x = *reinterpret_cast<const float4*>(most + h);
+#pragma unroll
+                    for (int i = 1; i < kSoftWarps; ++i) {
+                        const float4 y = *reinterpret_cast<const float4*>(most + i * NH + h);
+                        x = make_float4(fmaxf(x.x, y.x), fmaxf(x.y, y.y), fmaxf(x.z, y.z),
+                                        fmaxf(x.w, y.w));
+                    }
+                    const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float mn = fmaxf(m[h + j], xs[j]);
+                        const float from = mn == -INFINITY ? 0.0f : mn;
+                        corr[h + j] = exp2_fast(m[h + j] - from);
+                        s[h + j] = exp2_fast(s[h + j] - from);           // the weight
+                        l[h + j] = fmaf(l[h + j], corr[h + j], s[h + j]);
+                        m[h + j] = mn;
+                    }
+                }
+                // ---- the last tile's values; the weights take the place of the last ones then
+                if (k > 0) {
+                    add_o(it - 1);
+                    tc_fence_before();
+                }
+#pragma unroll
+                for (int h = 0; h < NH; ++h) o[h] *= corr[h];
+#pragma unroll
+                for (int h = 0; h < NH; h += 2) {
+                    uint32_t t[kTerms];
+                    three_terms(s[h], s[h + 1], t);
+#pragma unroll
+                    for (int i = 0; i < kTerms; ++i) {
+                        const int n0 = i * NH + h;
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"((p_at ^ ((n0 & 7) << 4)) + n0 * 128),
+                                     "h"(static_cast<uint16_t>(t[i])) : "memory");
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(
+                                         (p_at ^ (((n0 + 1) & 7) << 4)) + (n0 + 1) * 128),
+                                     "h"(static_cast<uint16_t>(t[i] >> 16)) : "memory");
+                    }
+                }
+                // ---- rows of V behind the sequence's end: a weight of 0 does not undo a NaN there
+                if (tok0 + kTile > w.len) {
+                    const int stage = it % L::kVStages;
+                    wait(v_full + 8 * stage, it / L::kVStages);
+                    if (!aborted && tok0 + tid >= w.len) {
+                        uint8_t* row = smem + L::kOffV + stage * kStage + (tid >> 3) * kGroup +
+                                       (tid & 7) * 128;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            *reinterpret_cast<uint4*>(row + (i >> 3) * 1024 + (i & 7) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full);
+            }
+            add_o(it - 1);
+            tc_fence_before();
+            // ---- the unit's state: sums of weights over the threads, then a dim a thread
+            float* sums = reinterpret_cast<float*>(smem + L::kOffMax) + (it & 1) * kSoftWarps * NH;
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+#pragma unroll
+                for (int x = 16; x; x >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
+            if (lane == 0) {
+#pragma unroll
+                for (int h = 0; h < NH; ++h) sums[warp * NH + h] = l[h];
+            }
+            softmax_sync();
+            const int heads = min(NH, a.G - h0);
+            const size_t row0 = static_cast<size_t>(w.b) * a.Hq + g * a.G + h0;
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+                if (h >= heads || aborted) continue;
+                const float sum = (sums[h] + sums[NH + h]) + (sums[2 * NH + h] + sums[3 * NH + h]);
+                if (here == w.tiles) {
+                    if (mp_check(a.status, static_cast<long long>(row0 + h),
+                                 static_cast<long long>(a.B) * a.Hq, kSitePagedOut))
+                        a.out[(row0 + h) * kD + tid] = sum == 0.0f ? 0.0f : o[h] / sum;
+                } else {
+                    float* p = part_of(a, w.t == 0, h);
+                    p[tid] = o[h];
+                    if (tid == 0) {
+                        p[kD] = m[h];
+                        p[kD + 1] = sum;
+                    }
+                }
+            }
+            softmax_sync();                      // the sums' place is the next unit's maxima's
+            w.next(a, here);
+        }
+    } else if (warp == 4) {
+        // ---------------- TMA producer ----------------
+        const int rows = min(kTile, a.pages.page_size & -a.pages.page_size);     // of a box
+        const int boxes = kTile / rows;
+        int it = 0;
+        bool ok = true;
+        while (w.left > 0 && ok) {
+            const int here = w.here(), g = w.unit / a.chunks;
+            const int32_t* slots = a.pages.table + static_cast<long long>(w.b) * a.pages.stride;
+            auto page_at = [&](int k) {
+                const int tok = (w.t + k) * kTile + lane * rows;
+                return k < here && lane < boxes && tok < w.len ? slots[tok / a.pages.page_size] : -1;
+            };
+            int page = page_at(0);
+            for (int k = 0; k < here; ++k, ++it) {
+                const int tok = (w.t + k) * kTile + lane * rows;
+                const bool there = page >= 0 && page < a.pages.n_pages;
+                // outside the tensor where there is no page
+                const int c4 = there ? page * a.Hkv + g : a.pages.n_pages * a.Hkv;
+                const int c3 = tok % a.pages.page_size / 8;
+                page = page_at(k + 1);
+                const int ks = it % L::kKStages, vs = it % L::kVStages;
+                if (!__all_sync(0xffffffffu, mbar_wait(k_empty + 8 * ks, (it / L::kKStages & 1) ^ 1,
+                                                       abort_flag, a.status))) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(k_full + 8 * ks, kStage);
+                __syncwarp();
+                if (lane < boxes)
+                    tma_load_5d(base + ks * kStage + lane * (rows / 8) * kGroup, &kmap,
+                                k_full + 8 * ks, 0, 0, 0, c3, c4);
+                if (!__all_sync(0xffffffffu, mbar_wait(v_empty + 8 * vs, (it / L::kVStages & 1) ^ 1,
+                                                       abort_flag, a.status))) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(v_full + 8 * vs, kStage);
+                __syncwarp();
+                if (lane < boxes)
+                    tma_load_5d(base + L::kOffV + vs * kStage + lane * (rows / 8) * kGroup, &vmap,
+                                v_full + 8 * vs, 0, 0, 0, c3, c4);
+            }
+            if (ok) w.next(a, here);
+        }
+        if (!ok && lane == 0) {
+            // let the loads already issued land before the CTA can exit (bounded): those of tile `it`
+            // may have stopped after K
+            volatile int never = 0;
+            for (int i = max(0, it - L::kKStages + 1); i <= it; ++i)
+                mbar_wait(k_full + 8 * (i % L::kKStages), i / L::kKStages & 1, &never, a.status,
+                          kWaitLimitNs / 8);
+            for (int i = max(0, it - L::kVStages); i < it; ++i)
+                mbar_wait(v_full + 8 * (i % L::kVStages), i / L::kVStages & 1, &never, a.status,
+                          kWaitLimitNs / 8);
+        }
+    } else if (warp == 5) {
+        // ---------------- MMA issuer ----------------
+        if (lane == 0 && w.left > 0) {
+            const uint32_t s_desc = make_idesc(kTile, N), o_desc = make_idesc(kD, N, true);
+            const long long total = w.left;
+            int seg = 0, in_seg = w.here();      // tiles of the unit not scored yet
+            auto wait = [&](uint32_t bar, int phase) {
+                return mbar_wait(bar, phase & 1, abort_flag, a.status);
+            };
+            bool fresh = true;                   // the next tile is its unit's first here
+            auto score = [&](int it) {           // S of tile it
+                const int ks = it % L::kKStages, slot = seg & 1;
+                if (fresh && !wait(q_full + 8 * slot, seg >> 1)) return false;
+                fresh = false;
+                if (!wait(k_full + 8 * ks, it / L::kKStages) ||
+                    !wait(s_empty + 8 * (it & 1), (it >> 1) ^ 1))
+                    return false;
+                tc_fence_after();
+                const uint32_t k_at = base + ks * kStage, q_at = base + L::kOffQ + slot * L::kOperand;
+#pragma unroll
+                for (int x = 0; x < kD / 16; ++x)
+                    tc_mma(tmem + (it & 1) * L::kColumns,
+                           sw128_desc(k_at + (x >> 2) * 1024 + (x & 3) * 32, kGroup),
+                           sw128_desc(q_at + (x >> 2) * (N * 128) + (x & 3) * 32), s_desc, x > 0);
+                tc_commit(k_empty + 8 * ks);
+                tc_commit(s_full + 8 * (it & 1));
+                if (--in_seg == 0) {
+                    tc_commit(q_empty + 8 * slot);
+                    ++seg;
+                    fresh = true;
+                    w.next(a, w.here());
+                    if (w.left > 0) in_seg = w.here();
+                }
+                return true;
+            };
+            bool ok = score(0);
+            for (int it = 0; it < total && ok; ++it) {
+                if (it + 1 < total && !(ok = score(it + 1))) break;
+                const int vs = it % L::kVStages;
+                if (!(ok = wait(p_full, it) && wait(v_full + 8 * vs, it / L::kVStages))) break;
+                tc_fence_after();
+                const uint32_t v_at = base + L::kOffV + vs * kStage, p_at = base + L::kOffP;
+#pragma unroll
+                for (int x = 0; x < kTile / 16; ++x)
+                    tc_mma(tmem_o, sw128_desc(v_at + x * 2 * kGroup, kGroup, 1024),
+                           sw128_desc(p_at + (x >> 2) * (N * 128) + (x & 3) * 32), o_desc, x > 0);
+                tc_commit(v_empty + 8 * vs);
+                tc_commit(o_full);
+            }
+        }
+    } else {
+        // ---------------- queries ----------------
+        int seg = 0;
+        while (w.left > 0) {
+            const int here = w.here(), g = w.unit / a.chunks, h0 = (w.unit - g * a.chunks) * NH;
+            const int heads = min(NH, a.G - h0);
+            const size_t row0 = static_cast<size_t>(w.b) * a.Hq + g * a.G + h0;
+            if (!__all_sync(0xffffffffu, mbar_wait(q_empty + 8 * (seg & 1), (seg >> 1 & 1) ^ 1,
+                                                   abort_flag, a.status)))
+                break;
+            uint8_t* dst = smem + L::kOffQ + (seg & 1) * L::kOperand + (lane >> 4) * (N * 128);
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[e] = h < heads ? load_elem(a.q, a.q_bf16, (row0 + h) * kD + 4 * lane + e) : 0.0f;
+                uint32_t t0[kTerms], t1[kTerms];
+                three_terms(x[0], x[1], t0);
+                three_terms(x[2], x[3], t1);
+#pragma unroll
+                for (int i = 0; i < kTerms; ++i) {
+                    const int n = i * NH + h;
+                    *reinterpret_cast<uint2*>(dst + n * 128 + ((((lane & 15) >> 1) ^ (n & 7)) << 4) +
+                                              (lane & 1) * 8) = make_uint2(t0[i], t1[i]);
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full + 8 * (seg & 1));
+            ++seg;
+            w.next(a, here);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 5) {
+        __syncwarp();
+        tmem_dealloc(tmem, L::kTmem);
+    }
+}
+
+typedef void (*TcFn)(const CUtensorMap, const CUtensorMap, const PArgs);
+TcFn pick_tc(int nh, uint32_t* smem) {
+    switch (nh) {
+        case 4: *smem = Lay<4>::kBytes; return paged_attention_tc_kernel<4>;
+        case 8: *smem = Lay<8>::kBytes; return paged_attention_tc_kernel<8>;
+        default: *smem = Lay<16>::kBytes; return paged_attention_tc_kernel<16>;
+    }
+}
+
+bool page_map(CUtensorMap* map, const void* pool, const mp_paged& c, int Hkv) {
+    const cuuint64_t page_bytes = static_cast<cuuint64_t>(c.page_size) * kD * 2;
+    const cuuint64_t dims[5] = {64, 8, 2, static_cast<cuuint64_t>(c.page_size / 8),
+                                static_cast<cuuint64_t>(c.n_pages) * Hkv};
+    const cuuint64_t strides[4] = {kD * 2, 128, kGroup, page_bytes};
+    const cuuint32_t rows = std::min(kTile, c.page_size & -c.page_size);
+    const cuuint32_t box[5] = {64, 8, 2, rows / 8, 1}, step[5] = {1, 1, 1, 1, 1};
+    return encode_tiled_fn()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(pool), dims,
+                             strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+int paged_tc_heads(int G) { return G <= 4 ? 4 : (G <= 8 ? 8 : 16); }
+
+cudaError_t launch_paged_attention_tc(PArgs a, const mp_paged& cache, cudaStream_t st) {
+    if (!encode_tiled_fn()) return cudaErrorNotSupported;
+    CUtensorMap kmap, vmap;
+    if (!page_map(&kmap, cache.keys, cache, a.Hkv) || !page_map(&vmap, cache.values, cache, a.Hkv))
+        return cudaErrorInvalidValue;
+    uint32_t smem;
+    const TcFn fn = pick_tc(a.nh, &smem);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, kmap, vmap, a);
+}
+
+cudaError_t prepare_paged_tc() {
+    for (int nh : {4, 8, 16}) {
+        uint32_t smem;
+        const TcFn fn = pick_tc(nh, &smem);
+        cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     cudaSharedmemCarveoutMaxShared);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace mp
