@@ -198,7 +198,7 @@ MP_API mp_status mp_encode_rows(const void* keys, mp_dtype key_dtype, const floa
  * b at [positions[b], positions[b] + m) ([B] int32 on the device). A key that falls outside
  * [0, n_capacity) is left out; bits of all other keys are kept. For the few tokens of a decode step:
  * one launch on CUDA cores, with the sums of mp_encode_keys's short ranges (bit for bit).
- * Errors: MP_ERR_INVALID_ARG (shapes, m < 0, null, misalignment: positions 4 bytes),
+ * Errors: MP_ERR_INVALID_ARG (shapes, m < 0, B Hkv > 65535, null, misalignment: positions 4 bytes),
  * MP_ERR_UNSUPPORTED (d != 128, m > 64: longer ranges are mp_encode_rows's). m == 0 does nothing. */
 MP_API mp_status mp_encode_rows_at(const void* keys, mp_dtype key_dtype, const float* centre,
                                    const void* W, mp_dtype w_dtype, int B, int Hkv, int m,
@@ -488,17 +488,17 @@ typedef struct {
  *   keys, values  [B][Hkv][m][d] of rows_dtype: go to row p of the pages of their sequence, in the
  *                 cache's type; a token whose p has no page is not written
  *   q             [B][Hq][m][d] of rows_dtype: the rotated queries go to q_out, [B][Hq][m][d] of the
- *                 same type, contiguous. NULL where there are none. q_out may be q's own memory.
+ *                 same type, contiguous. NULL where there are none. q_out may be q where q is contiguous.
  *   keys_out      [B][Hkv][m][d] of the cache's type, contiguous, or NULL: the keys as the cache holds
  *                 them, for the calls that encode them (of tokens without a page too)
  * Rotation: the first rotary_dims dims of a row are pairs; pair j = (x, y) becomes
  * (x cos a - y sin a, y cos a + x sin a), a = p inv_freq[j] (float32 on the device, rotary_dims / 2
  * of them), in float32, rounded once to the type it is stored in. Pairs are dims (j, j + rotary_dims /
  * 2), or with interleaved != 0 dims (2 j, 2 j + 1). The angle is reduced in 64-bit fixed point: it is
- * off by less than 2^-51 |p| max(|inv_freq[j]|, 2^-10) + 2^-22 radians at any position. inv_freq NULL
+ * off by less than 2^-61 |p| (1 + |inv_freq[j]|) + 2^-22 radians at any position. inv_freq NULL
  * (rotary_dims then ignored) turns nothing. An inv_freq that is infinite or NaN has unspecified
  * results.
- * Errors: MP_ERR_INVALID_ARG (shapes, m < 0, B m (Hq + 2 Hkv) > 2^31 - 1, n_begin < 0 or n_begin + m >
+ * Errors: MP_ERR_INVALID_ARG (shapes, m < 0, Hq + 2 Hkv > 2^19, B m (Hq + 2 Hkv) > 2^31 - 1, n_begin < 0 or n_begin + m >
  * n_slots page_size without positions, null, misalignment: rows, outputs 16 bytes, others 4),
  * MP_ERR_UNSUPPORTED (d != 128, page_size not a multiple of 8, rotary_dims not a multiple of 16 in
  * [16, 128]). m == 0 does nothing. */

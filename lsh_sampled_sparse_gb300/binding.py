@@ -881,41 +881,58 @@ def _paged(cache, page_table):
     """(mp_paged, device, B, Hkv, tokens of the table) of a pool and a batch's page table, their
     tensors checked; the device must be the current one."""
     k, v = cache
-    if not isinstance(k, torch.Tensor) or not k.is_cuda:
+    try:
+        device, shape, kt = k.get_device(), k.shape, k.dtype
+    except AttributeError:
+        raise TypeError("the cache must hold CUDA tensors") from None
+    if device < 0:
         raise TypeError("the cache must hold CUDA tensors")
-    device = k.get_device()
     if device != torch._C._cuda_getDevice():
         raise ValueError(f"the cache is on cuda:{device}, which is not the current device")
-    shape = k.shape
-    if len(shape) != 4:
+    if len(shape) != 4 or shape[3] != 128:
         raise ValueError(f"keys must be [n_pages, Hkv, page_size, 128], got {tuple(shape)}")
-    dt = _dtype(k, "keys")
-    _on_device(page_table, device, "page_table")
-    if page_table.dtype is not torch.int32:
-        raise TypeError(f"page_table must be int32, is {page_table.dtype}")
-    if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError("page_table must be [B, slots], its rows contiguous")
-    B, slots = page_table.shape
-    stride = page_table.stride(0) if B > 1 else slots
+    n_pages, Hkv, page_size, _ = shape
+    try:
+        if page_table.get_device() != device or page_table.dtype is not torch.int32:
+            raise AttributeError
+        B, slots = page_table.shape
+        stride, unit = page_table.stride()
+    except (AttributeError, ValueError):
+        _refuse_table(page_table, device)
+    if unit != 1 and slots > 1:
+        raise ValueError("the rows of page_table must be contiguous")
+    if B <= 1:
+        stride = slots
     if stride < slots or stride >> 31:
         raise ValueError(f"page_table's rows overlap or are too far apart (stride {stride})")
-    if shape[3] != 128:
-        raise ValueError(f"rows must have 128 elements, got {shape[3]}")
-    return _Paged(_arg(k, device, "keys", k.dtype, shape), _arg(v, device, "values", k.dtype, shape),
-                  page_table.data_ptr(), dt, shape[0], shape[2], slots, stride), device, B, \
-        shape[1], slots * shape[2]
+    return _Paged(_arg(k, device, "keys", kt, shape), _arg(v, device, "values", kt, shape),
+                  page_table.data_ptr(), _dtype(k, "keys"), n_pages, page_size, slots,
+                  stride), device, B, Hkv, slots * page_size
+
+
+def _refuse_table(t, device):
+    """Raise what _paged found in a page table."""
+    _on_device(t, device, "page_table")
+    if t.dtype is not torch.int32:
+        raise TypeError(f"page_table must be int32, is {t.dtype}")
+    raise ValueError(f"page_table must be [B, slots], got {tuple(t.shape)}")
 
 
 def _strided_rows(t, device, name, dtype, shape):
-    """mp_rows of a tensor whose rows are contiguous; other strides are its own."""
+    """A reference to the mp_rows of a tensor whose rows are contiguous; other strides are its own."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device:
+            sb, sh, sm, unit = t.stride()
+            if unit == 1:
+                return ctypes.byref(_Rows(t.data_ptr(), sb, sh, sm))
+    except AttributeError:
+        pass
     _on_device(t, device, name)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, is {t.dtype}")
-    if t.dim() != 4 or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} must have shape {shape or '[B, H, m, 128]'}, got {tuple(t.shape)}")
-    if t.stride(3) != 1 and t.shape[3] != 1:
-        raise ValueError(f"the rows of {name} must be contiguous")
-    return _Rows(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"the rows of {name} must be contiguous")
 
 
 def paged_append(cache: PagedCache, page_table, keys, values, n_begin: int = 0, positions=None,
@@ -932,38 +949,38 @@ def paged_append(cache: PagedCache, page_table, keys, values, n_begin: int = 0, 
     them."""
     c, device, B, Hkv, _ = _paged(cache, page_table)
     _on_device(keys, device, "keys")
+    dtype, shape = keys.dtype, keys.shape
     dt = _dtype(keys, "keys")
-    if keys.dim() != 4 or keys.shape[0] != B or keys.shape[1] != Hkv:
-        raise ValueError(f"keys must be [{B}, {Hkv}, m, 128], got {tuple(keys.shape)}")
-    m, d = keys.shape[2:]
-    kr = _strided_rows(keys, device, "keys", keys.dtype, keys.shape)
-    vr = _strided_rows(values, device, "values", keys.dtype, keys.shape)
+    if len(shape) != 4 or shape[0] != B or shape[1] != Hkv:
+        raise ValueError(f"keys must be [{B}, {Hkv}, m, 128], got {tuple(shape)}")
+    m, d = shape[2], shape[3]
     if n_begin >> 31 not in (0, -1):             # what a C int would cut off
         raise ValueError(f"n_begin = {n_begin}")
-    rotary = 0
+    rotary, freq = 0, None
     if inv_freq is not None:
         if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
             raise TypeError("inv_freq must be a CUDA tensor [rotary_dims / 2]")
-        rotary = 2 * inv_freq.shape[0]
-    Hq, qr = 0, None
+        rotary = 2 * inv_freq.numel()
+        freq = _arg(inv_freq, device, "inv_freq", torch.float32, (rotary >> 1,))
+    Hq, qr, qp = 0, None, None
     if q is not None:
         _on_device(q, device, "q")
-        if q.dim() != 4 or q.shape[0] != B or tuple(q.shape[2:]) != (m, d):
-            raise ValueError(f"q must be [{B}, Hq, {m}, {d}], got {tuple(q.shape)}")
-        qr, Hq = ctypes.byref(_strided_rows(q, device, "q", keys.dtype, q.shape)), q.shape[1]
+        qs = q.shape
+        if len(qs) != 4 or qs[0] != B or qs[2] != m or qs[3] != d:
+            raise ValueError(f"q must be [{B}, Hq, {m}, {d}], got {tuple(qs)}")
+        Hq, qr = qs[1], _strided_rows(q, device, "q", dtype, qs)
         if q_out is None:
-            q_out = _empty(tuple(q.shape), q.dtype, q.device, stream)
+            q_out = _empty(tuple(qs), dtype, q.device, stream)
+        qp = _arg(q_out, device, "q_out", dtype, qs)
     elif q_out is not None:
         raise ValueError("q_out without q")
     status = lib().mp_paged_append(
-        ctypes.byref(kr), ctypes.byref(vr), qr, dt,
-        _arg(inv_freq, device, "inv_freq", torch.float32, (rotary // 2,)), rotary,
-        bool(interleaved), B, Hq, Hkv, m, d, n_begin,
+        _strided_rows(keys, device, "keys", dtype, shape),
+        _strided_rows(values, device, "values", dtype, shape), qr, dt, freq, rotary,
+        1 if interleaved else 0, B, Hq, Hkv, m, d, n_begin,
         _arg(positions, device, "positions", torch.int32, (B,)),
-        _arg(counts, device, "counts", torch.int32, (B,)), ctypes.byref(c),
-        _arg(q_out, device, "q_out", keys.dtype, (B, Hq, m, d)),
-        _arg(keys_out, device, "keys_out", cache[0].dtype, (B, Hkv, m, d)),
-        _raw_stream(stream, device))
+        _arg(counts, device, "counts", torch.int32, (B,)), ctypes.byref(c), qp,
+        _arg(keys_out, device, "keys_out", cache[0].dtype, shape), _raw_stream(stream, device))
     if status:
         _check(status, "mp_paged_append")
     return q_out

@@ -371,7 +371,7 @@ mp_status mp_encode_rows_at(const void* keys, mp_dtype key_dtype, const float* c
     if (!valid_dtype(key_dtype) || !valid_dtype(w_dtype)) return MP_ERR_INVALID_ARG;
     if (d != kD || m > kAppendMaxKeys) return MP_ERR_UNSUPPORTED;
     if (static_cast<long long>(K) * L > (1 << 20)) return MP_ERR_INVALID_ARG;
-    if (static_cast<long long>(B) * Hkv > (1 << 18)) return MP_ERR_INVALID_ARG;   // heads of a grid
+    if (static_cast<long long>(B) * Hkv > 65535) return MP_ERR_INVALID_ARG;   // heads of a grid
     if (K == 0 || m == 0) return MP_OK;   // nothing to encode
     if (!keys || !centre || !W || !codes || !positions) return MP_ERR_INVALID_ARG;
     if (!aligned(keys, 16) || !aligned(codes, 16) || !aligned(centre, 4) || !aligned(positions, 4) ||
@@ -787,7 +787,7 @@ mp_status mp_paged_append(const mp_rows* keys, const mp_rows* values, const mp_r
         return MP_ERR_INVALID_ARG;
     if (q && (!valid_rows(q, rows_dtype, B, Hq, m) || !q_out)) return MP_ERR_INVALID_ARG;
     const long long heads = (q ? Hq : 0) + 2ll * Hkv;
-    if (heads > 0x7fffffffll / 4 || static_cast<long long>(B) * m > 0x7fffffffll / heads)
+    if (heads > 1 << 19 || static_cast<long long>(B) * m > 0x7fffffffll / heads)   // a grid's rows
         return MP_ERR_INVALID_ARG;
     if (!ensure_prepared()) return MP_ERR_CUDA;
     return to_status(launch_paged_append(*keys, *values, q, rows_dtype == MP_BF16, inv_freq,

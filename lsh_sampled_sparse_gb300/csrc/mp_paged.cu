@@ -19,10 +19,9 @@ using Bf16 = __nv_bfloat16;
 
 // ------------------------------------------------------------------------------------------------
 // Append. Pair j of a row at position p turns by a = p inv_freq[j]; in half turns a / pi = 2 frac(p t)
-// with t = inv_freq[j] / (2 pi). t mod 1 is taken to 64 fractional bits once a thread (in float64),
-// p t mod 1 is then one wrapping 64-bit product, exact, and cos and sin are those of a number in
-// [-1, 1] half turns: no loss at far positions, where p inv_freq in float32 is off by whole fractions
-// of a turn.
+// with t = inv_freq[j] / (2 pi). t mod 1 is taken to 64 fractional bits, p t mod 1 is then one
+// wrapping 64-bit product, exact, and cos and sin are those of a number in [-1, 1] half turns: no loss
+// at far positions, where p inv_freq in float32 is off by whole fractions of a turn.
 // ------------------------------------------------------------------------------------------------
 struct AppendArgs {
     mp_rows k, v, q;                             // strides in elements
@@ -34,289 +33,388 @@ struct AppendArgs {
     const int32_t* counts;
     const float* inv_freq;
     PageRef pages;
-    int pairs, interleaved, B, Hq, Hkv, m, n_begin, toks, tok_blocks, rows;
+    int pairs, interleaved, B, Hq, Hkv, m, n_begin, tok_shift, tok_blocks;
     int* status;                                 // index checks of the MP_CHECKS build
 };
 
 constexpr int kAppThreads = 256;
 constexpr int kRowLanes = 8;                     // lanes a row, 2 x 8 dims each
 constexpr int kAppRows = kAppThreads / kRowLanes;
-constexpr int kMaxToks = 4;                      // tokens a CTA turns
+constexpr int kAppCtas = 6;                      // an SM
+constexpr int kMaxToks = 4;                      // tokens a block has
+static_assert(kMaxToks * (kD / 2) == kAppThreads, "a thread an angle");
 
-// 8 elements as floats, and back
-__device__ __forceinline__ void load_row8(const float* p, float (&x)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void load_row8(const Bf16* p, float (&x)[8]) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// 8 elements as they are in memory, two of them as floats
+template <typename T>
+struct Eight {
+    uint4 v[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
+    __device__ __forceinline__ float2 two(int e) const {                 // elements 2 e, 2 e + 1
+        const uint4& q = v[sizeof(T) == 2 ? 0 : e >> 1];
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t w = e == 0 ? q.x : (e == 1 ? q.y : (e == 2 ? q.z : q.w));
+            return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+        } else {
+            return e & 1 ? make_float2(__uint_as_float(q.z), __uint_as_float(q.w))
+                         : make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+        }
+    }
+};
+__device__ __forceinline__ uint32_t two_bf16(float2 x) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// x cos - y sin, y cos + x sin
+__device__ __forceinline__ void turn_pair(float& x, float& y, float2 t) {
+    const float x0 = x;
+    x = fmaf(x0, t.x, -(y * t.y));
+    y = fmaf(y, t.x, x0 * t.y);
+}
+// A lane's two pieces of a row, turned (cs: cos and sin of its eight pairs, NULL: as they are) and
+// rounded to D, to dst and, unless it is NULL, to dst2 too.
+template <typename T, typename D>
+__device__ __forceinline__ void turn_and_store(const Eight<T>& a, const Eight<T>& b, const float2* cs,
+                                               bool interleaved, D* dst, D* dst2, int da, int db) {
+    auto turned = [&](int e, float2& x, float2& y) {
+        x = a.two(e);
+        y = b.two(e);
+        if (!cs) return;
+        if (interleaved) {
+            turn_pair(x.x, x.y, cs[e]);
+            turn_pair(y.x, y.y, cs[e + 4]);
+        } else {
+            const float4 t = reinterpret_cast<const float4*>(cs)[e];
+            turn_pair(x.x, y.x, make_float2(t.x, t.y));
+            turn_pair(x.y, y.y, make_float2(t.z, t.w));
+        }
+    };
+    if constexpr (sizeof(D) == 2) {
+        uint32_t wa[4], wb[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float2 x, y;
+            turned(e, x, y);
+            wa[e] = two_bf16(x);
+            wb[e] = two_bf16(y);
+        }
+        const uint4 va = make_uint4(wa[0], wa[1], wa[2], wa[3]), vb = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+        if (dst) {
+            *reinterpret_cast<uint4*>(dst + da) = va;
+            *reinterpret_cast<uint4*>(dst + db) = vb;
+        }
+        if (dst2) {
+            *reinterpret_cast<uint4*>(dst2 + da) = va;
+            *reinterpret_cast<uint4*>(dst2 + db) = vb;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+            float2 x0, y0, x1, y1;
+            turned(e, x0, y0);
+            turned(e + 1, x1, y1);
+            const float4 va = make_float4(x0.x, x0.y, x1.x, x1.y), vb = make_float4(y0.x, y0.y, y1.x, y1.y);
+            if (dst) {
+                *reinterpret_cast<float4*>(dst + da + 2 * e) = va;
+                *reinterpret_cast<float4*>(dst + db + 2 * e) = vb;
+            }
+            if (dst2) {
+                *reinterpret_cast<float4*>(dst2 + da + 2 * e) = va;
+                *reinterpret_cast<float4*>(dst2 + db + 2 * e) = vb;
+            }
+        }
     }
 }
-__device__ __forceinline__ void store_row8(float* p, const float (&x)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ void store_row8(Bf16* p, const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+
+// 2^64 (f / (2 pi) mod 1), toward zero, of a float f: its 24 bits times 2^64 / (2 pi), shifted by its
+// exponent. Off by less than 1 + |f| (in units of 2^-64).
+__device__ __forceinline__ uint64_t turn_of(float f) {
+    constexpr uint64_t kPerTurn = 0x28be60db9391054aull;                 // 2^64 / (2 pi)
+    const uint32_t bits = __float_as_uint(f), ex = (bits >> 23) & 255u;
+    const uint64_t mant = (bits & 0x7fffffu) | (ex ? 0x800000u : 0u);
+    const int down = 150 - static_cast<int>(ex ? ex : 1u);               // f = mant 2^-down
+    const uint64_t lo = mant * kPerTurn, hi = __umul64hi(mant, kPerTurn);
+    uint64_t t;
+    if (down >= 64) t = down < 128 ? hi >> (down - 64) : 0ull;
+    else if (down > 0) t = (lo >> down) | (hi << (64 - down));
+    else t = down > -64 ? lo << -down : 0ull;
+    return bits >> 31 ? 0ull - t : t;
 }
 
-// A CTA takes `toks` tokens of one sequence and a share of their rows (of the query heads, then the
-// key heads, then the value heads): the angles of a token are made once for all its heads.
+// A CTA takes 32 rows of up to 2^tok_shift tokens of one sequence (blockIdx.y: of which heads; the query
+// heads come first, then the key heads, then the value heads), a row to eight lanes, all on their way
+// before anything is known of the tokens. No CTA takes more than that: of what a loop over rows had in
+// flight ahead, less than the rows of the CTAs that fit an SM (8192 tokens of 32 + 8 + 8 heads: 45 us).
 template <typename T, typename C>
-__global__ void __launch_bounds__(kAppThreads) paged_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kAppThreads, kAppCtas) paged_append_kernel(const AppendArgs a) {
     __shared__ __align__(16) float2 turn[kMaxToks][kD / 2];
-    const int tid = threadIdx.x;
-    const int b = blockIdx.x / a.tok_blocks, i0 = static_cast<int>(blockIdx.x % a.tok_blocks) * a.toks;
-    wait_for_predecessor();
-    const int live = a.counts ? min(a.m, a.counts[b]) : a.m;
-    const int toks = min(a.toks, live - i0);
-    if (toks <= 0) return;
-    const long long p0 = (a.positions ? static_cast<long long>(a.positions[b]) : a.n_begin) + i0;
-    for (int x = tid; x < toks * a.pairs; x += kAppThreads) {
-        const int i = x / a.pairs, j = x - i * a.pairs;
-        double t = static_cast<double>(a.inv_freq[j]) * 0.15915494309189533577;   // 1 / (2 pi)
-        t -= floor(t);
-        const unsigned long long step = __double2ull_rz(t * 18446744073709551616.0);     // 2^64
-        const long long frac = static_cast<long long>(step * static_cast<unsigned long long>(p0 + i));
-        float s, c;
-        sincospif(static_cast<float>(frac) * 0x1p-63f, &s, &c);
-        turn[i][j] = make_float2(c, s);
-    }
-    __syncthreads();
-    const int lane = tid & (kRowLanes - 1);
+    __shared__ long long place[kMaxToks];        // a token's row of the pool for KV head 0, or -1
+    const int tid = threadIdx.x, lane = tid & (kRowLanes - 1), row = tid / kRowLanes;
+    const int b = blockIdx.x / a.tok_blocks;
+    const int i0 = static_cast<int>(blockIdx.x - static_cast<unsigned>(b) * a.tok_blocks) << a.tok_shift;
+    const int i = row & ((1 << a.tok_shift) - 1), tok = i0 + i;
+    const int h = (row >> a.tok_shift) + blockIdx.y * (kAppRows >> a.tok_shift);
+    const int hk = h - a.Hq, hv = hk - a.Hkv;    // < 0: a query's row, a key's
     // this lane's two pieces of 8 dims: a pair's two halves, or whole pairs, or dims that stay
     const int turned = a.pairs / 8;              // lanes whose pieces turn
-    int da = 16 * lane, db = 16 * lane + 8;
-    if (!a.interleaved && lane < turned) {
-        da = 8 * lane;
-        db = a.pairs + 8 * lane;
+    const bool halves = !a.interleaved && lane < turned;
+    const int da = halves ? 8 * lane : 16 * lane, db = halves ? a.pairs + 8 * lane : 16 * lane + 8;
+    wait_for_predecessor();
+    allow_dependents();
+    Eight<T> xa, xb;
+    const bool mine = tok < a.m && hv < a.Hkv;
+    if (mine) {
+        const mp_rows& from = hk < 0 ? a.q : (hv < 0 ? a.k : a.v);
+        const T* src = static_cast<const T*>(from.data) + b * from.stride_b + tok * from.stride_m +
+                       (hk < 0 ? h : (hv < 0 ? hk : hv)) * from.stride_h;
+        xa.load(src + da);
+        xb.load(src + db);
     }
-    const long long cap = static_cast<long long>(a.pages.n_slots) * a.pages.page_size;
-    const int heads = a.Hq + 2 * a.Hkv;
-    for (int r = blockIdx.y * kAppRows + tid / kRowLanes; r < heads * toks; r += gridDim.y * kAppRows) {
-        const int h = r / toks, i = r - h * toks;
-        const int kind = h < a.Hq ? 0 : (h < a.Hq + a.Hkv ? 1 : 2);
-        const mp_rows& from = kind == 0 ? a.q : (kind == 1 ? a.k : a.v);
-        const int g = kind == 0 ? h : (kind == 1 ? h - a.Hq : h - a.Hq - a.Hkv);
-        const T* src = static_cast<const T*>(from.data) + b * from.stride_b + g * from.stride_h +
-                       (i0 + i) * from.stride_m;
-        float x[8], y[8];
-        load_row8(src + da, x);
-        load_row8(src + db, y);
-        if (kind < 2 && lane < turned) {
-            const float2* cs = &turn[i][8 * lane];
-            if (a.interleaved) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 u = cs[e], w = cs[e + 4];
-                    const float x0 = x[2 * e], y0 = y[2 * e];
-                    x[2 * e] = fmaf(x0, u.x, -(x[2 * e + 1] * u.y));
-                    x[2 * e + 1] = fmaf(x[2 * e + 1], u.x, x0 * u.y);
-                    y[2 * e] = fmaf(y0, w.x, -(y[2 * e + 1] * w.y));
-                    y[2 * e + 1] = fmaf(y[2 * e + 1], w.x, y0 * w.y);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float2 u = cs[e];
-                    const float x0 = x[e];
-                    x[e] = fmaf(x0, u.x, -(y[e] * u.y));
-                    y[e] = fmaf(y[e], u.x, x0 * u.y);
-                }
-            }
-        }
-        if (kind == 0) {
-            const long long row = (static_cast<long long>(b) * a.Hq + g) * a.m + i0 + i;
-            if (mp_check(a.status, row, static_cast<long long>(a.B) * a.Hq * a.m, kSitePagedOut)) {
-                T* dst = static_cast<T*>(a.q_out) + row * kD;
-                store_row8(dst + da, x);
-                store_row8(dst + db, y);
-            }
-            continue;
-        }
-        if (kind == 1 && a.k_out) {
-            const long long row = (static_cast<long long>(b) * a.Hkv + g) * a.m + i0 + i;
-            if (mp_check(a.status, row, static_cast<long long>(a.B) * a.Hkv * a.m, kSitePagedOut)) {
-                C* dst = static_cast<C*>(a.k_out) + row * kD;
-                store_row8(dst + da, x);
-                store_row8(dst + db, y);
-            }
-        }
-        const long long p = p0 + i;
-        if (p < 0 || p >= cap) continue;
-        const long long row = paged_row(a.pages, a.pages.table + static_cast<long long>(b) *
-                                                                     a.pages.stride,
-                                        static_cast<int>(p), a.Hkv, g);
-        if (row >= 0 && mp_check(a.status, row, static_cast<long long>(a.pages.n_pages) * a.Hkv *
-                                                    a.pages.page_size, kSitePagedRow)) {
-            C* dst = static_cast<C*>(kind == 1 ? a.keys : a.values) + row * kD;
-            store_row8(dst + da, x);
-            store_row8(dst + db, y);
-        }
+    const int live = a.counts ? min(a.m, a.counts[b]) : a.m;
+    const long long p0 = (a.positions ? static_cast<long long>(a.positions[b]) : a.n_begin) + i0;
+    if (tid < 1 << a.tok_shift) {
+        const long long p = p0 + tid;
+        place[tid] = p >= 0 && p < static_cast<long long>(a.pages.n_slots) * a.pages.page_size
+                         ? paged_row(a.pages, a.pages.table + static_cast<long long>(b) * a.pages.stride,
+                                     static_cast<int>(p), a.Hkv, 0)
+                         : -1;
     }
+    if ((tid & 63) < a.pairs && tid >> 6 < 1 << a.tok_shift) {
+        const long long part = static_cast<long long>(turn_of(a.inv_freq[tid & 63]) *
+                                                      static_cast<uint64_t>(p0 + (tid >> 6)));
+        float s, c;
+        sincospif(static_cast<float>(part) * 0x1p-63f, &s, &c);
+        turn[tid >> 6][tid & 63] = make_float2(c, s);
+    }
+    __syncthreads();
+    if (!mine || tok >= live) return;
+    const float2* cs = hv < 0 && lane < turned ? &turn[i][8 * lane] : nullptr;
+    if (hk < 0) {
+        const long long r = (static_cast<long long>(b) * a.Hq + h) * a.m + tok;
+        if (mp_check(a.status, r, static_cast<long long>(a.B) * a.Hq * a.m, kSitePagedOut))
+            turn_and_store<T, T>(xa, xb, cs, a.interleaved, static_cast<T*>(a.q_out) + r * kD, nullptr, da,
+                                 db);
+        return;
+    }
+    const long long in_pool = place[i] + static_cast<long long>(hv < 0 ? hk : hv) * a.pages.page_size;
+    const long long in_rows = (static_cast<long long>(b) * a.Hkv + hk) * a.m + tok;
+    C* dst = place[i] >= 0 && mp_check(a.status, in_pool, static_cast<long long>(a.pages.n_pages) * a.Hkv *
+                                                              a.pages.page_size, kSitePagedRow)
+                 ? static_cast<C*>(hv < 0 ? a.keys : a.values) + in_pool * kD : nullptr;
+    C* dst2 = hv < 0 && a.k_out && mp_check(a.status, in_rows, static_cast<long long>(a.B) * a.Hkv * a.m,
+                                            kSitePagedOut)
+                  ? static_cast<C*>(a.k_out) + in_rows * kD : nullptr;
+    turn_and_store<T, C>(xa, xb, cs, a.interleaved, dst, dst2, da, db);
 }
 
-// A float32 cache, on CUDA cores: a warp takes groups of four tokens, a lane four dims of each. The NH scores of four
-// tokens are summed over the lanes by a reduce-scatter, which leaves a score a lane (two lanes where
-// NH = 4), the softmax steps are lane-parallel, weights come back through shared memory.
+// A float32 cache, on CUDA cores: a warp takes groups of four tokens of one page (pages hold multiples
+// of eight), a lane four dims of each. Groups come through a ring of three in the warp's own piece of
+// shared memory (cp.async: 12 KB in flight a warp), across the units of the run; a lane copies what it
+// reads itself. The NH scores of four tokens are summed over the lanes by a reduce-scatter, which leaves a
+// score to 8 / NH lanes, the softmax steps are lane-parallel, weights come back through
+// shared memory.
 constexpr int kSimtWarps = 8;
 constexpr int kSimtThreads = 32 * kSimtWarps;
 constexpr int kSimtTile = 4 * kSimtWarps;        // tokens
+constexpr int kRing = 3;
+constexpr int kGroupBytes = 2 * 4 * kD * 4;      // four rows of K, four of V
+
+template <int NH>
+struct SimtSmem {
+    // [warp][kRing] groups (a warp's state in the place of a group it is done with), weights and
+    // factors of a group, m and l of the warps, a cluster's states, the plan
+    static constexpr int kOffWeights = kSimtWarps * kRing * kGroupBytes;
+    static constexpr int kOffMl = kOffWeights + kSimtWarps * 5 * NH * 4;
+    static constexpr int kOffShare = kOffMl + kSimtWarps * NH * 8;
+    static constexpr int kOffPlan = (kOffShare + NH * kPart * 4 + 15) / 16 * 16;
+    static constexpr int kBytes = kOffPlan + static_cast<int>(sizeof(PlanSmem));
+    static_assert(NH * kD * 4 <= kGroupBytes, "a warp's state takes the place of a group");
+    static_assert(2 * (kBytes + 1024) <= 233472, "two CTAs an SM");
+};
+
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(live ? 16 : 0)
+                 : "memory");
+}
 
 template <int NH>
 __global__ void __launch_bounds__(kSimtThreads, 2) paged_attention_simt_kernel(const PArgs a) {
-    __shared__ PlanSmem plan;
-    __shared__ __align__(16) float weights[kSimtWarps][4 * NH + NH];
-    __shared__ __align__(16) float join[kSimtWarps][NH][kPart];
+    using S = SimtSmem<NH>;
+    extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float* weights = reinterpret_cast<float*>(smem + S::kOffWeights) + warp * 5 * NH;
+    float2* ml = reinterpret_cast<float2*>(smem + S::kOffMl);            // [warp][NH]
+    float* share = reinterpret_cast<float*>(smem + S::kOffShare);
+    const uint8_t* ring = smem + warp * kRing * kGroupBytes + 16 * lane;
     wait_for_predecessor();
     allow_dependents();
-    Walk w = plan_run(a, plan);
+    Walk w = plan_run(a, *reinterpret_cast<PlanSmem*>(smem + S::kOffPlan));
+    const int unit_b = w.b, unit = w.unit;       // of a cluster: its only ones
+    if (a.cluster && w.left == 0) {              // fewer tiles than CTAs
+        for (int i = tid; i < NH * kPart; i += kSimtThreads)
+            share[i] = i % kPart == kD ? -INFINITY : 0.0f;
+    }
+    // ---- the group to copy next: its unit, its tile there, its slot's entry of the table, looked up
+    // one group ahead; bits 4 i .. of `live`: how many tokens the group in place i of the ring holds
+    Walk ahead = w;
+    int ahead_here = w.left > 0 ? w.here() : 0, ahead_k = 0;
+    uint32_t live = 0u;
+    auto entry = [&]() {
+        const int tok = (ahead.t + ahead_k) * kSimtTile + 4 * warp;
+        return ahead.left > 0 && tok < ahead.len
+                   ? a.pages.table[static_cast<long long>(ahead.b) * a.pages.stride + slot_of(a, tok)]
+                   : -1;
+    };
+    int page = entry();
+    auto issue = [&](int place) {
+        if (ahead.left > 0) {
+            const int tok = (ahead.t + ahead_k) * kSimtTile + 4 * warp;
+            const bool there = page >= 0 && page < a.pages.n_pages;
+            const long long row = there ? (static_cast<long long>(page) * a.Hkv +
+                                           kv_head(a, ahead.unit)) * a.pages.page_size +
+                                              (tok - slot_of(a, tok) * a.pages.page_size)
+                                        : 0;
+            const int now = there && mp_check(a.status, row + 3,
+                                              static_cast<long long>(a.pages.n_pages) * a.Hkv *
+                                                  a.pages.page_size, kSitePagedRow)
+                                ? min(4, ahead.len - tok) : 0;
+            live = (live & ~(15u << (4 * place))) | (static_cast<uint32_t>(now) << (4 * place));
+            const float* kp = static_cast<const float*>(a.keys) + row * kD + 4 * lane;
+            const float* vp = static_cast<const float*>(a.values) + row * kD + 4 * lane;
+            const uint32_t dst = smem_u32(ring) + place * kGroupBytes;
+            if (now > 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    copy16_or_zero(dst + i * kD * 4, kp + (i < now ? i * kD : 0), i < now);
+                    copy16_or_zero(dst + (4 + i) * kD * 4, vp + (i < now ? i * kD : 0), i < now);
+                }
+            }
+            if (++ahead_k == ahead_here) {
+                ahead.next(a, ahead_here);
+                ahead_k = 0;
+                if (ahead.left > 0) ahead_here = ahead.here();
+            }
+            page = entry();
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kRing; ++i) issue(i);
+    int place = 0;
     while (w.left > 0) {
-        const int here = w.here(), g = w.unit / a.chunks, h0 = (w.unit - g * a.chunks) * NH;
+        const int here = w.here(), g = kv_head(a, w.unit), h0 = (w.unit - g * a.chunks) * NH;
         const int heads = min(NH, a.G - h0);
         const size_t row0 = static_cast<size_t>(w.b) * a.Hq + g * a.G + h0;
-        const int32_t* slots = a.pages.table + static_cast<long long>(w.b) * a.pages.stride;
         float q[NH][4];
 #pragma unroll
         for (int h = 0; h < NH; ++h)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 q[h][e] = h < heads ? load_elem(a.q, a.q_bf16, (row0 + h) * kD + 4 * lane + e) : 0.0f;
-        // a group of tokens: four of one page (pages hold multiples of eight)
-        float4 kn[4], vn[4];
-        int live = 0;
-        auto load = [&](int k) {
-            const int tok = (w.t + k) * kSimtTile + 4 * warp;
-            live = 0;
-            if (k < here && tok < w.len) {
-                const long long row = paged_row(a.pages, slots, tok, a.Hkv, g);
-                if (row >= 0 && mp_check(a.status, row + 3, static_cast<long long>(a.pages.n_pages) *
-                                                                a.Hkv * a.pages.page_size,
-                                         kSitePagedRow))
-                    live = min(4, w.len - tok);
-                const float* kp = static_cast<const float*>(a.keys) + row * kD + 4 * lane;
-                const float* vp = static_cast<const float*>(a.values) + row * kD + 4 * lane;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (i < live) {
-                        kn[i] = *reinterpret_cast<const float4*>(kp + i * kD);
-                        vn[i] = *reinterpret_cast<const float4*>(vp + i * kD);
-                    } else {
-                        kn[i] = vn[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    }
-                }
-            }
-        };
         float m = -INFINITY, l = 0.0f, o[NH][4];
 #pragma unroll
         for (int h = 0; h < NH; ++h)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[h][e] = 0.0f;
-        load(0);
         for (int k = 0; k < here; ++k) {
-            const int now = live;
-            float v[4][4], s[4 * NH];
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+            const float4* group = reinterpret_cast<const float4*>(ring + place * kGroupBytes);
+            const int now = (live >> (4 * place)) & 15u;
+            if (now > 0) {
+                float s[4 * NH];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float4 x = kn[i];
-                v[i][0] = vn[i].x;
-                v[i][1] = vn[i].y;
-                v[i][2] = vn[i].z;
-                v[i][3] = vn[i].w;
+                for (int i = 0; i < 4; ++i) {
+                    const float4 x = group[i * (kD / 4)];
 #pragma unroll
-                for (int h = 0; h < NH; ++h)
-                    s[i * NH + h] = fmaf(x.w, q[h][3], fmaf(x.z, q[h][2],
-                                                            fmaf(x.y, q[h][1], x.x * q[h][0])));
-            }
-            load(k + 1);
-            if (now == 0) continue;
-#pragma unroll
-            for (int lv = 0; (16 >> lv) >= (NH == 8 ? 1 : 2); ++lv) {
-                const int off = 16 >> lv, keep = (2 * NH) >> lv;
-                const bool up = (lane & off) != 0;
-#pragma unroll
-                for (int i = 0; i < keep; ++i) {
-                    const float send = up ? s[i] : s[i + keep];
-                    s[i] = (up ? s[i + keep] : s[i]) + __shfl_xor_sync(0xffffffffu, send, off);
+                    for (int h = 0; h < NH; ++h)
+                        s[i * NH + h] = fmaf(x.w, q[h][3], fmaf(x.z, q[h][2],
+                                                                fmaf(x.y, q[h][1], x.x * q[h][0])));
                 }
-            }
-            float logit = s[0];
-            if (NH == 4) logit += __shfl_xor_sync(0xffffffffu, logit, 1);
-            logit = (lane >> 3) < now ? logit * a.scale : -INFINITY;
-            float mt = fmaxf(logit, __shfl_xor_sync(0xffffffffu, logit, 8));
-            mt = fmaxf(m, fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16)));
-            const float base = mt == -INFINITY ? 0.0f : mt;
-            const float corr = exp2_fast(m - base), p = exp2_fast(logit - base);
-            m = mt;
-            l = fmaf(l, corr, p);
-            const int at = NH == 8 ? lane : lane >> 1;                   // token NH + head
-            weights[warp][at] = p;
-            if (lane < 8) weights[warp][4 * NH + at] = corr;
-            __syncwarp();
 #pragma unroll
-            for (int h = 0; h < NH; h += 4) {
-                const float4 c = *reinterpret_cast<const float4*>(&weights[warp][4 * NH + h]);
-                const float cc[4] = {c.x, c.y, c.z, c.w};
+                for (int lv = 0; ((2 * NH) >> lv) >= 1; ++lv) {
+                    const int off = 16 >> lv, keep = (2 * NH) >> lv;
+                    const bool up = (lane & off) != 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[h + j][e] *= cc[j];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int h = 0; h < NH; h += 4) {
-                    const float4 c = *reinterpret_cast<const float4*>(&weights[warp][i * NH + h]);
-                    const float pp[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[h + j][e] = fmaf(pp[j], v[i][e], o[h + j][e]);
+                    for (int i = 0; i < keep; ++i) {
+                        const float send = up ? s[i] : s[i + keep];
+                        s[i] = (up ? s[i + keep] : s[i]) + __shfl_xor_sync(0xffffffffu, send, off);
+                    }
                 }
-            __syncwarp();
+                float logit = s[0];
+#pragma unroll
+                for (int off = 4 / NH; off >= 1; off >>= 1)
+                    logit += __shfl_xor_sync(0xffffffffu, logit, off);
+                logit = (lane >> 3) < now ? logit * a.scale : -INFINITY;
+                float mt = fmaxf(logit, __shfl_xor_sync(0xffffffffu, logit, 8));
+                mt = fmaxf(m, fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16)));
+                const float from = mt == -INFINITY ? 0.0f : mt;
+                const float corr = exp2_fast(m - from), p = exp2_fast(logit - from);
+                m = mt;
+                l = fmaf(l, corr, p);
+                const int at = lane * NH / 8;                            // token NH + head
+                weights[at] = p;
+                if (lane < 8) weights[4 * NH + at] = corr;
+                __syncwarp();
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    const float c = weights[4 * NH + h];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[h][e] *= c;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 x = group[(4 + i) * (kD / 4)];
+                    const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) {
+                        const float c = weights[i * NH + h];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[h][e] = fmaf(c, v[e], o[h][e]);
+                    }
+                }
+                __syncwarp();
+            }
+            if (k + 1 < here) {
+                issue(place);
+                place = place == kRing - 1 ? 0 : place + 1;
+            }
         }
+        // ---- the warps' states, each in the place of the group it took last, joined in order
         l += __shfl_xor_sync(0xffffffffu, l, 8);
         l += __shfl_xor_sync(0xffffffffu, l, 16);
-        // ---- the warps' states, joined in order
-        __syncthreads();                                                 // the last unit's are read
+        float4* state = reinterpret_cast<float4*>(smem + (warp * kRing + place) * kGroupBytes);
 #pragma unroll
         for (int h = 0; h < NH; ++h)
-            *reinterpret_cast<float4*>(&join[warp][h][4 * lane]) =
-                make_float4(o[h][0], o[h][1], o[h][2], o[h][3]);
-        if (lane < 8 && (NH == 8 || (lane & 1) == 0)) {
-            join[warp][NH == 8 ? lane : lane >> 1][kD] = m;
-            join[warp][NH == 8 ? lane : lane >> 1][kD + 1] = l;
-        }
+            state[h * (kD / 4) + lane] = make_float4(o[h][0], o[h][1], o[h][2], o[h][3]);
+        if (lane < 8) ml[warp * NH + lane * NH / 8] = make_float2(m, l);
         __syncthreads();
         const int e = tid & (kD - 1);
         for (int h = tid / kD; h < heads; h += kSimtThreads / kD) {
             float M = -INFINITY, L = 0.0f, O = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kSimtWarps; ++i) M = fmaxf(M, join[i][h][kD]);
-            const float base = M == -INFINITY ? 0.0f : M;
+            for (int i = 0; i < kSimtWarps; ++i) M = fmaxf(M, ml[i * NH + h].x);
+            const float from = M == -INFINITY ? 0.0f : M;
 #pragma unroll
             for (int i = 0; i < kSimtWarps; ++i) {
-                const float c = exp2_fast(join[i][h][kD] - base);
-                L = fmaf(c, join[i][h][kD + 1], L);
-                O = fmaf(c, join[i][h][e], O);
+                const float2 x = ml[i * NH + h];
+                const float c = exp2_fast(x.x - from);
+                L = fmaf(c, x.y, L);
+                O = fmaf(c, reinterpret_cast<const float*>(smem + (i * kRing + place) *
+                                                                      kGroupBytes)[h * kD + e], O);
             }
-            if (here == w.tiles) {
+            if (a.cluster) {
+                share[h * kPart + e] = O;
+                if (e == 0) {
+                    share[h * kPart + kD] = M;
+                    share[h * kPart + kD + 1] = L;
+                }
+            } else if (here == w.tiles) {
                 if (mp_check(a.status, static_cast<long long>(row0 + h),
                              static_cast<long long>(a.B) * a.Hq, kSitePagedOut))
-                    a.out[(row0 + h) * kD + e] = L == 0.0f ? 0.0f : O / L;
+                    a.out[(row0 + h) * kD + e] = L == 0.0f ? 0.0f : O * __frcp_rn(L);
             } else {
                 float* p = part_of(a, w.t == 0, h);
                 p[e] = O;
@@ -326,7 +424,15 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attention_simt_kernel(c
                 }
             }
         }
+        __syncthreads();                         // the states are read: their places may be filled
+        issue(place);
+        place = place == kRing - 1 ? 0 : place + 1;
         w.next(a, here);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (a.cluster) {
+        __syncthreads();
+        join_cluster(a, share, unit_b, unit);
     }
 }
 
@@ -350,8 +456,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const PArgs
     const long long total = a.pages.lengths ? __ldcg(a.before + a.B) : each * a.B;
     const long long t0 = (a.pages.lengths ? __ldcg(a.before + b) : each * b) +
                          static_cast<long long>(unit) * tiles;
-    const int shares = shares_of(a, total);
-    const int c0 = share_with(total, shares, t0), c1 = share_with(total, shares, t0 + tiles - 1);
+    const Shares share(a, total);
+    const int c0 = share.of(t0), c1 = share.of(t0 + tiles - 1);
     if (c0 == c1) return;
     float M = -INFINITY, L = 0.0f;
     float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -409,15 +515,30 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const PArgs
         Os = fmaf(c, join[i][e], Os);
     }
     if (mp_check(a.status, row, static_cast<long long>(a.B) * a.Hq, kSitePagedOut))
-        a.out[static_cast<size_t>(row) * kD + e] = Ls == 0.0f ? 0.0f : Os / Ls;
+        a.out[static_cast<size_t>(row) * kD + e] = Ls == 0.0f ? 0.0f : Os * __frcp_rn(Ls);
 }
 
 constexpr int kSimtCtas = 2 * kSms;
-int simt_heads(int G) { return G <= 4 ? 4 : 8; }
+constexpr int kJoinTiles = 2;
+int simt_heads(int G) { return G <= 2 ? G : (G <= 4 ? 4 : 8); }
 
 typedef void (*PFn)(const PArgs);
-PFn pick_simt(int nh) {
-    return nh == 4 ? paged_attention_simt_kernel<4> : paged_attention_simt_kernel<8>;
+template <int NH>
+PFn simt(int* smem) {
+    *smem = SimtSmem<NH>::kBytes;
+    return paged_attention_simt_kernel<NH>;
+}
+PFn pick_simt(int nh, int* smem) {
+    return nh == 1 ? simt<1>(smem) : (nh == 2 ? simt<2>(smem) : (nh == 4 ? simt<4>(smem) : simt<8>(smem)));
+}
+
+// The CTAs of the cluster that shares a unit of `tiles` tiles, 0 where all CTAs share all tiles.
+int cluster_size(long long units, int tiles, int ctas) {
+    if (units > ctas) return 0;
+    const int most = std::min({kPagedMaxCluster, tiles, static_cast<int>(ctas / units)});
+    const int each = (tiles + most - 1) / most;
+    const long long even = (units * tiles + ctas - 1) / ctas;
+    return each - even <= kJoinTiles ? (tiles + each - 1) / each : 0;
 }
 
 typedef void (*AppendFn)(const AppendArgs);
@@ -457,18 +578,14 @@ cudaError_t launch_paged_append(const mp_rows& keys, const mp_rows& values, cons
     a.m = m;
     a.n_begin = n_begin;
     a.status = device_status_ptr();
-    // tokens a CTA: as many as leave two CTAs an SM; rows split over CTAs where there are fewer
     const int heads = a.Hq + 2 * Hkv;
-    a.toks = 1;
-    while (a.toks < kMaxToks && static_cast<long long>(B) * m >= 4ll * kSms * a.toks) a.toks *= 2;
-    a.tok_blocks = (m + a.toks - 1) / a.toks;
-    const long long blocks = static_cast<long long>(B) * a.tok_blocks;
-    if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-    const long long passes = (static_cast<long long>(heads) * a.toks + kAppRows - 1) / kAppRows;
-    const unsigned split = static_cast<unsigned>(
-        std::max<long long>(1, std::min<long long>(passes, 4 * kSms / std::max<long long>(blocks, 1))));
-    return launch_dependent(pick_append(rows_bf16, cache.dtype == MP_BF16),
-                            dim3(static_cast<unsigned>(blocks), split), dim3(kAppThreads), 0, st, a);
+    a.tok_shift = m >= 3 ? 2 : m - 1;            // up to kMaxToks tokens
+    a.tok_blocks = (m + (1 << a.tok_shift) - 1) >> a.tok_shift;
+    const int heads_a_cta = kAppRows >> a.tok_shift;
+    const dim3 grid(static_cast<unsigned>(B) * a.tok_blocks, (heads + heads_a_cta - 1) / heads_a_cta);
+    if (grid.y > 65535u) return cudaErrorInvalidValue;
+    return launch_dependent(pick_append(rows_bf16, cache.dtype == MP_BF16), grid, dim3(kAppThreads), 0, st,
+                            a);
 }
 
 size_t paged_attention_scratch_bytes(int B, int Hq, int Hkv) {
@@ -498,14 +615,26 @@ cudaError_t launch_paged_attention(const void* q, bool q_bf16, const mp_paged& c
     a.n = n;
     a.ctas = tc ? kPagedTcCtas : kSimtCtas;
     a.tile = tc ? kPagedTcTile : kSimtTile;
+    a.q_wide = (reinterpret_cast<uintptr_t>(q) & 15u) == 0u;
+    a.page_shift = -1;
+    for (int i = 3; i < 31; ++i)
+        if (cache.page_size == 1 << i) a.page_shift = i;
+    const int tiles = (n - 1) / a.tile + 1;
+    const long long units = static_cast<long long>(B) * Hkv * a.chunks;
+    a.cluster = cluster_size(units, tiles, a.ctas);
     a.scale = scale * 1.4426950408889634f;
     a.status = device_status_ptr();
     a.part = static_cast<float*>(workspace);
     a.before = reinterpret_cast<long long*>(a.part + static_cast<size_t>(a.ctas) * 2 * a.nh * kPart);
-    const cudaError_t e = tc ? launch_paged_attention_tc(a, cache, st)
-                             : launch_dependent(pick_simt(a.nh), dim3(a.ctas), dim3(kSimtThreads), 0,
-                                                st, a);
-    if (e != cudaSuccess) return e;
+    const unsigned grid = a.cluster ? static_cast<unsigned>(units) * a.cluster : a.ctas;
+    int smem;
+    const cudaError_t e = tc ? launch_paged_attention_tc(a, cache, grid, st)
+                             : launch_dependent(pick_simt(a.nh, &smem), dim3(grid), dim3(kSimtThreads),
+                                                smem, st, a, std::max(1, a.cluster));
+    if (e != cudaSuccess || a.cluster) return e;
+    // where every sequence has the same tiles, the shares may fall on whole units
+    const long long total = units * tiles, shares = std::min<long long>(a.ctas, total);
+    if (!lengths && total % shares == 0 && total / shares % tiles == 0) return e;
     return launch_dependent(paged_join_kernel, dim3(static_cast<unsigned>(B) * Hq),
                             dim3(32 * kJoinWarps), 0, st, a);
 }
@@ -516,8 +645,15 @@ cudaError_t prepare_paged() {
     for (int i = 0; i < 4; ++i) {
         if ((e = cudaFuncGetAttributes(&fa, pick_append(i & 1, i & 2))) != cudaSuccess) return e;
     }
-    for (int nh : {4, 8})
-        if ((e = cudaFuncGetAttributes(&fa, pick_simt(nh))) != cudaSuccess) return e;
+    for (int nh : {1, 2, 4, 8}) {
+        int smem;
+        const PFn fn = pick_simt(nh, &smem);
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     cudaSharedmemCarveoutMaxShared);
+        if (e != cudaSuccess) return e;
+    }
     if ((e = prepare_paged_tc()) != cudaSuccess) return e;
     return cudaFuncGetAttributes(&fa, paged_join_kernel);
 }

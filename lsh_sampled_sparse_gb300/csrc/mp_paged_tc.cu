@@ -114,19 +114,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (warp == 4 && lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
+    }
     if (warp == 5) tmem_alloc(smem_u32(&tmem_slot), L::kTmem);
     tc_fence_before();
-    wait_for_predecessor();
-    allow_dependents();
-    const Walk run = plan_run(a, *reinterpret_cast<PlanSmem*>(smem + L::kOffPlan));
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     const uint32_t tmem_o = tmem + 2 * L::kColumns;
-    Walk w = run;
+    wait_for_predecessor();
+    allow_dependents();
+    Walk w = plan_run(a, *reinterpret_cast<PlanSmem*>(smem + L::kOffPlan));
+    // a cluster's states: in the place of the first tile of K, once it is scored
+    float* share = reinterpret_cast<float*>(smem);
+    const int unit_b = w.b, unit = w.unit;       // of a cluster: its only ones
 
     if (warp < kSoftWarps) {
         // ---------------- softmax ----------------
+        if (a.cluster && w.left == 0) {          // fewer tiles than CTAs
+            for (int h = 0; h < NH; ++h) share[h * kPart + tid] = 0.0f;
+            if (tid < NH) {
+                share[tid * kPart + kD] = -INFINITY;
+                share[tid * kPart + kD + 1] = 0.0f;
+            }
+        }
         const uint32_t quad = static_cast<uint32_t>(warp * 32) << 16;    // this warp's TMEM lanes
         const uint32_t chunk = (tid & 63) >> 3;
         const uint32_t p_at = base + L::kOffP + (tid >> 6) * (N * 128) + (chunk << 4) + (tid & 7) * 2;
@@ -137,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         int it = 0;
         while (w.left > 0) {
-            const int here = w.here(), g = w.unit / a.chunks, h0 = (w.unit - g * a.chunks) * NH;
+            const int here = w.here(), g = kv_head(a, w.unit), h0 = (w.unit - g * a.chunks) * NH;
             const int32_t* slots = a.pages.table + static_cast<long long>(w.b) * a.pages.stride;
             float m[NH], l[NH], o[NH];
 #pragma unroll
@@ -161,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto page_at = [&](int k) {          // the slot of this thread's token of tile k
                 const int tok = (w.t + k) * kTile + tid;
-                return k < here && tok < w.len ? slots[tok / a.pages.page_size] : -1;
+                return k < here && tok < w.len ? slots[slot_of(a, tok)] : -1;
             };
             int page = page_at(0);
             for (int k = 0; k < here; ++k, ++it) {
@@ -283,16 +296,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int h = 0; h < NH; ++h) sums[warp * NH + h] = l[h];
             }
             softmax_sync();
-            const int heads = min(NH, a.G - h0);
+            const int heads = aborted ? 0 : min(NH, a.G - h0);
             const size_t row0 = static_cast<size_t>(w.b) * a.Hq + g * a.G + h0;
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
-                if (h >= heads || aborted) continue;
                 const float sum = (sums[h] + sums[NH + h]) + (sums[2 * NH + h] + sums[3 * NH + h]);
-                if (here == w.tiles) {
+                if (h >= heads) continue;
+                if (a.cluster) {
+                    share[h * kPart + tid] = o[h];
+                    if (tid == 0) {
+                        share[h * kPart + kD] = m[h];
+                        share[h * kPart + kD + 1] = sum;
+                    }
+                } else if (here == w.tiles) {
                     if (mp_check(a.status, static_cast<long long>(row0 + h),
                                  static_cast<long long>(a.B) * a.Hq, kSitePagedOut))
-                        a.out[(row0 + h) * kD + tid] = sum == 0.0f ? 0.0f : o[h] / sum;
+                        a.out[(row0 + h) * kD + tid] = sum == 0.0f ? 0.0f : o[h] * __frcp_rn(sum);
                 } else {
                     float* p = part_of(a, w.t == 0, h);
                     p[tid] = o[h];
@@ -312,11 +331,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         int it = 0;
         bool ok = true;
         while (w.left > 0 && ok) {
-            const int here = w.here(), g = w.unit / a.chunks;
+            const int here = w.here(), g = kv_head(a, w.unit);
             const int32_t* slots = a.pages.table + static_cast<long long>(w.b) * a.pages.stride;
             auto page_at = [&](int k) {
                 const int tok = (w.t + k) * kTile + lane * rows;
-                return k < here && lane < boxes && tok < w.len ? slots[tok / a.pages.page_size] : -1;
+                return k < here && lane < boxes && tok < w.len ? slots[slot_of(a, tok)] : -1;
             };
             int page = page_at(0);
             for (int k = 0; k < here; ++k, ++it) {
@@ -324,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool there = page >= 0 && page < a.pages.n_pages;
                 // outside the tensor where there is no page
                 const int c4 = there ? page * a.Hkv + g : a.pages.n_pages * a.Hkv;
-                const int c3 = tok % a.pages.page_size / 8;
+                const int c3 = (tok - slot_of(a, tok) * a.pages.page_size) >> 3;
                 page = page_at(k + 1);
                 const int ks = it % L::kKStages, vs = it % L::kVStages;
                 if (!__all_sync(0xffffffffu, mbar_wait(k_empty + 8 * ks, (it / L::kKStages & 1) ^ 1,
@@ -415,27 +434,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- queries ----------------
         int seg = 0;
         while (w.left > 0) {
-            const int here = w.here(), g = w.unit / a.chunks, h0 = (w.unit - g * a.chunks) * NH;
+            const int here = w.here(), g = kv_head(a, w.unit), h0 = (w.unit - g * a.chunks) * NH;
             const int heads = min(NH, a.G - h0);
             const size_t row0 = static_cast<size_t>(w.b) * a.Hq + g * a.G + h0;
             if (!__all_sync(0xffffffffu, mbar_wait(q_empty + 8 * (seg & 1), (seg >> 1 & 1) ^ 1,
                                                    abort_flag, a.status)))
                 break;
             uint8_t* dst = smem + L::kOffQ + (seg & 1) * L::kOperand + (lane >> 4) * (N * 128);
+            float x[NH][4];
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
-                float x[4];
+                const size_t from = (row0 + min(h, heads - 1)) * kD + 4 * lane;
+                if (!a.q_wide) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    x[e] = h < heads ? load_elem(a.q, a.q_bf16, (row0 + h) * kD + 4 * lane + e) : 0.0f;
+                    for (int e = 0; e < 4; ++e) x[h][e] = load_elem(a.q, a.q_bf16, from + e);
+                } else if (a.q_bf16) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(
+                        static_cast<const __nv_bfloat16*>(a.q) + from);
+                    x[h][0] = __uint_as_float(v.x << 16);
+                    x[h][1] = __uint_as_float(v.x & 0xffff0000u);
+                    x[h][2] = __uint_as_float(v.y << 16);
+                    x[h][3] = __uint_as_float(v.y & 0xffff0000u);
+                } else {
+                    const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) +
+                                                                      from);
+                    x[h][0] = v.x;
+                    x[h][1] = v.y;
+                    x[h][2] = v.z;
+                    x[h][3] = v.w;
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
                 uint32_t t0[kTerms], t1[kTerms];
-                three_terms(x[0], x[1], t0);
-                three_terms(x[2], x[3], t1);
+                three_terms(x[h][0], x[h][1], t0);
+                three_terms(x[h][2], x[h][3], t1);
 #pragma unroll
                 for (int i = 0; i < kTerms; ++i) {
                     const int n = i * NH + h;
-                    *reinterpret_cast<uint2*>(dst + n * 128 + ((((lane & 15) >> 1) ^ (n & 7)) << 4) +
-                                              (lane & 1) * 8) = make_uint2(t0[i], t1[i]);
+                    if (i == 0 || !a.q_bf16)
+                        *reinterpret_cast<uint2*>(dst + n * 128 +
+                                                  ((((lane & 15) >> 1) ^ (n & 7)) << 4) +
+                                                  (lane & 1) * 8) = make_uint2(t0[i], t1[i]);
                 }
             }
             fence_async_smem();
@@ -452,6 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         tmem_dealloc(tmem, L::kTmem);
     }
+    if (a.cluster) join_cluster(a, share, unit_b, unit);
 }
 
 typedef void (*TcFn)(const CUtensorMap, const CUtensorMap, const PArgs);
@@ -480,7 +521,8 @@ bool page_map(CUtensorMap* map, const void* pool, const mp_paged& c, int Hkv) {
 
 int paged_tc_heads(int G) { return G <= 4 ? 4 : (G <= 8 ? 8 : 16); }
 
-cudaError_t launch_paged_attention_tc(PArgs a, const mp_paged& cache, cudaStream_t st) {
+cudaError_t launch_paged_attention_tc(const PArgs& a, const mp_paged& cache, unsigned grid,
+                                      cudaStream_t st) {
     if (!encode_tiled_fn()) return cudaErrorNotSupported;
     CUtensorMap kmap, vmap;
     if (!page_map(&kmap, cache.keys, cache, a.Hkv) || !page_map(&vmap, cache.values, cache, a.Hkv))
@@ -488,15 +530,18 @@ cudaError_t launch_paged_attention_tc(PArgs a, const mp_paged& cache, cudaStream
     uint32_t smem;
     const TcFn fn = pick_tc(a.nh, &smem);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.ctas);
+    cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, fn, kmap, vmap, a);
 }
 

@@ -139,10 +139,14 @@ def test_dependent_kernels_of_the_paged_cache_make_no_non_coherent_load():
 @pytest.mark.parametrize("ctas", [1, 152, 304])
 def test_the_shares_of_a_call_cover_its_tiles_once(total, ctas):
     """The arithmetic that shares tiles out to CTAs and finds a tile's CTA again."""
-    shares = min(ctas, total)
-    first = [total * c // shares for c in range(shares + 1)]
+    n = min(ctas, total)
+    each, more = total // n, total % n
+    first = [each * c + min(c, more) for c in range(n + 1)]
     assert first[0] == 0 and first[-1] == total and all(a < b for a, b in zip(first, first[1:]))
-    for c in range(shares):
+    for c in range(n):
         for t in {first[c], (first[c] + first[c + 1] - 1) // 2, first[c + 1] - 1}:
-            assert ((t + 1) * shares - 1) // total == c
-    assert (total + 1) * shares < 2 ** 63
+            of = t // (each + 1) if t < more * (each + 1) else more + (t - more * (each + 1)) // each
+            assert of == c
+    for size in range(1, 9):                     # a cluster's ranks
+        part = [r * total // size for r in range(size + 1)]
+        assert part[0] == 0 and part[-1] == total and all(a <= b for a, b in zip(part, part[1:]))
