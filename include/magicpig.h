@@ -523,8 +523,8 @@ MP_API size_t mp_paged_attention_workspace_bytes(int B, int Hq, int Hkv, int n, 
  * beyond a sequence's length is not looked at, NaN included. A NaN or an infinity in a query (float32
  * queries over a bf16 cache: an element past the largest bf16, too), or in a key or value attended
  * to, may give NaN in the rows that it meets.
- * Errors: MP_ERR_INVALID_ARG (shapes, n > n_slots page_size or 2^30, B Hq > 2^22, Hq % Hkv, a scale
- * that is negative, infinite or NaN, null, misalignment: out 16 bytes, lengths 4, workspace 256),
+ * Errors: MP_ERR_INVALID_ARG (shapes, n > n_slots page_size or 2^30, B Hq > 2^22, B Hq n > 2^35, Hq %
+ * Hkv, a scale that is negative, infinite or NaN, null, misalignment: out 16 bytes, lengths 4, workspace 256),
  * MP_ERR_UNSUPPORTED (d != 128, page_size not a multiple of 8), MP_ERR_WORKSPACE. */
 MP_API mp_status mp_paged_attention(const void* q, mp_dtype q_dtype, const mp_paged* cache, int B,
                                     int Hq, int Hkv, int n, int d, const int32_t* lengths,

@@ -810,6 +810,8 @@ mp_status mp_paged_attention(const void* q, mp_dtype q_dtype, const mp_paged* ca
     if (n > static_cast<long long>(cache->n_slots) * cache->page_size || !(scale >= 0.0f) ||
         isinf(scale))
         return MP_ERR_INVALID_ARG;
+    // the tiles of all units are numbered in 32 bits
+    if (static_cast<long long>(B) * Hq * n > 1ll << 35) return MP_ERR_INVALID_ARG;
     if (!q || !out || !aligned(q, q_dtype == MP_BF16 ? 2 : 4) || !aligned(out, 16) ||
         !aligned(lengths, 4) || !workspace || !aligned(workspace, 256))
         return MP_ERR_INVALID_ARG;

@@ -217,7 +217,9 @@ __global__ void __launch_bounds__(kAppThreads, kAppCtas) paged_append_kernel(con
 // shared memory.
 constexpr int kSimtWarps = 8;
 constexpr int kSimtThreads = 32 * kSimtWarps;
-constexpr int kSimtTile = 4 * kSimtWarps;        // tokens
+constexpr int kSimtShift = 5;                    // log2 of a tile's tokens: four a warp
+constexpr int kSimtTile = 1 << kSimtShift;
+static_assert(kSimtTile == 4 * kSimtWarps, "a group a warp");
 constexpr int kRing = 3;
 constexpr int kGroupBytes = 2 * 4 * kD * 4;      // four rows of K, four of V
 
@@ -414,7 +416,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attention_simt_kernel(c
             } else if (here == w.tiles) {
                 if (mp_check(a.status, static_cast<long long>(row0 + h),
                              static_cast<long long>(a.B) * a.Hq, kSitePagedOut))
-                    a.out[(row0 + h) * kD + e] = L == 0.0f ? 0.0f : O * __frcp_rn(L);
+                    a.out[(row0 + h) * kD + e] = over_sum(O, L);
             } else {
                 float* p = part_of(a, w.t == 0, h);
                 p[e] = O;
@@ -452,10 +454,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const PArgs
         if (threadIdx.x < kD) a.out[static_cast<size_t>(row) * kD + threadIdx.x] = 0.0f;
         return;
     }
-    const long long each = static_cast<long long>(per_tile) * tiles;
-    const long long total = a.pages.lengths ? __ldcg(a.before + a.B) : each * a.B;
-    const long long t0 = (a.pages.lengths ? __ldcg(a.before + b) : each * b) +
-                         static_cast<long long>(unit) * tiles;
+    const int each = per_tile * tiles;
+    const int total = a.pages.lengths ? __ldcg(a.before + a.B) : each * a.B;
+    const int t0 = (a.pages.lengths ? __ldcg(a.before + b) : each * b) + unit * tiles;
     const Shares share(a, total);
     const int c0 = share.of(t0), c1 = share.of(t0 + tiles - 1);
     if (c0 == c1) return;
@@ -515,7 +516,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const PArgs
         Os = fmaf(c, join[i][e], Os);
     }
     if (mp_check(a.status, row, static_cast<long long>(a.B) * a.Hq, kSitePagedOut))
-        a.out[static_cast<size_t>(row) * kD + e] = Ls == 0.0f ? 0.0f : Os * __frcp_rn(Ls);
+        a.out[static_cast<size_t>(row) * kD + e] = over_sum(Os, Ls);
 }
 
 constexpr int kSimtCtas = 2 * kSms;
@@ -592,7 +593,7 @@ size_t paged_attention_scratch_bytes(int B, int Hq, int Hkv) {
     // of either kind of cache: who asks does not say which
     const size_t parts = std::max(kSimtCtas * simt_heads(Hq / Hkv),
                                   kPagedTcCtas * paged_tc_heads(Hq / Hkv));
-    return parts * 2 * kPart * sizeof(float) + (static_cast<size_t>(B) + 1) * sizeof(long long);
+    return parts * 2 * kPart * sizeof(float) + (static_cast<size_t>(B) + 1) * sizeof(int);
 }
 
 cudaError_t launch_paged_attention(const void* q, bool q_bf16, const mp_paged& cache, int B, int Hq,
@@ -614,18 +615,18 @@ cudaError_t launch_paged_attention(const void* q, bool q_bf16, const mp_paged& c
     a.chunks = (a.G + a.nh - 1) / a.nh;
     a.n = n;
     a.ctas = tc ? kPagedTcCtas : kSimtCtas;
-    a.tile = tc ? kPagedTcTile : kSimtTile;
+    a.tile_shift = tc ? kPagedTcShift : kSimtShift;
     a.q_wide = (reinterpret_cast<uintptr_t>(q) & 15u) == 0u;
     a.page_shift = -1;
     for (int i = 3; i < 31; ++i)
         if (cache.page_size == 1 << i) a.page_shift = i;
-    const int tiles = (n - 1) / a.tile + 1;
+    const int tiles = ((n - 1) >> a.tile_shift) + 1;
     const long long units = static_cast<long long>(B) * Hkv * a.chunks;
     a.cluster = cluster_size(units, tiles, a.ctas);
     a.scale = scale * 1.4426950408889634f;
     a.status = device_status_ptr();
     a.part = static_cast<float*>(workspace);
-    a.before = reinterpret_cast<long long*>(a.part + static_cast<size_t>(a.ctas) * 2 * a.nh * kPart);
+    a.before = reinterpret_cast<int*>(a.part + static_cast<size_t>(a.ctas) * 2 * a.nh * kPart);
     const unsigned grid = a.cluster ? static_cast<unsigned>(units) * a.cluster : a.ctas;
     int smem;
     const cudaError_t e = tc ? launch_paged_attention_tc(a, cache, grid, st)

@@ -11,6 +11,13 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return r;
 }
 
+// A sum of values over the sum of their weights, which is 1 at least, or 0 where there are none (or NaN)
+__device__ __forceinline__ float over_sum(float o, float sum) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sum));
+    return sum == 0.0f ? 0.0f : o * r;
+}
+
 // ------------------------------------------------------------------------------------------------
 // Attention of one query token per sequence.
 //
@@ -27,10 +34,11 @@ struct PArgs {
     const void* keys;
     const void* values;
     PageRef pages;
-    float* part;                                 // [CTA][2][NH][kPart]: o, m, l
-    long long* before;                           // [B + 1] tiles of the sequences before (lengths only)
+    float* part;                                 // [CTA][2][nh][kPart]: o, m, l
+    int* before;                                 // [B + 1] tiles of the sequences before (lengths only)
     float* out;
-    int q_bf16, q_wide, B, Hq, Hkv, G, chunks, nh, n, ctas, tile;
+    int q_bf16, q_wide, B, Hq, Hkv, G, chunks, nh, n, ctas;
+    int tile_shift;                              // log2 of a tile's tokens
     int cluster;                                 // CTAs a unit is shared out to, a cluster; 0: all
     int page_shift;                              // log2 of page_size, -1: no power of two
     float scale;                                 // of q.k, times log2 e
@@ -41,47 +49,37 @@ constexpr int kPart = kD + 4;
 __device__ __forceinline__ int length_of(const PArgs& a, int b) {
     return a.pages.lengths ? max(0, min(a.n, a.pages.lengths[b])) : a.n;
 }
-__device__ __forceinline__ int tiles_of(const PArgs& a, int len) { return (len + a.tile - 1) / a.tile; }
-// a / b of numbers that mostly fit 32 bits, where a division takes a fifth of the time
-__device__ __forceinline__ long long quotient(long long a, int b) {
-    if ((a >> 32) == 0) return static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
-    return a / b;
+__device__ __forceinline__ int tiles_of(const PArgs& a, int len) {
+    return (len + (1 << a.tile_shift) - 1) >> a.tile_shift;
 }
-// `total` tiles shared out to CTAs: the first `more` of them take each + 1, the others `each`
+// `total` tiles (less than 2^31: a call's sizes see to that) shared out to CTAs: the first `more` of
+// them take each + 1, the others `each`
 struct Shares {
-    long long each, more;
-    int n;                                       // CTAs that have any
-    __device__ __forceinline__ Shares(const PArgs& a, long long total) {
-        n = static_cast<int>(min(static_cast<long long>(a.ctas), total));
-        each = n > 0 ? quotient(total, n) : 0;
+    int each, more, n;                           // n: CTAs that have any
+    __device__ __forceinline__ Shares(const PArgs& a, int total) {
+        n = min(a.ctas, total);
+        each = n > 0 ? total / n : 0;
         more = total - each * n;
     }
-    __device__ __forceinline__ long long first(int c) const {            // tile of CTA c
-        return each * c + min(static_cast<long long>(c), more);
-    }
-    __device__ __forceinline__ int of(long long t) const {               // the CTA that has tile t
-        const long long in_more = more * (each + 1);
-        if (each >= 0x7fffffffll) return static_cast<int>(t < in_more ? t / (each + 1)
-                                                                      : more + (t - in_more) / each);
-        return static_cast<int>(t < in_more ? quotient(t, static_cast<int>(each) + 1)
-                                            : more + quotient(t - in_more, static_cast<int>(each)));
+    __device__ __forceinline__ int first(int c) const { return each * c + min(c, more); }  // tile of CTA c
+    __device__ __forceinline__ int of(int t) const {                     // the CTA that has tile t
+        const int in_more = more * (each + 1);
+        return t < in_more ? t / (each + 1) : more + (t - in_more) / each;
     }
 };
 __device__ __forceinline__ int slot_of(const PArgs& a, int token) {
     return a.page_shift >= 0 ? token >> a.page_shift : token / a.pages.page_size;
 }
-// KV head of a unit of a sequence, and the first query head of its group that it takes
+// KV head of a unit of a sequence
 __device__ __forceinline__ int kv_head(const PArgs& a, int unit) {
     return a.chunks == 1 ? unit : unit / a.chunks;
 }
 
 // Where a CTA's run of tiles begins, and how many there are; walked through by next().
 struct Walk {
-    long long left;                              // tiles of the run from here on
+    int left;                                    // tiles of the run from here on
     int b, unit, t, tiles, len;                  // unit of the sequence, its next tile, all its tiles
-    __device__ __forceinline__ int here() const {
-        return static_cast<int>(min(left, static_cast<long long>(tiles - t)));
-    }
+    __device__ __forceinline__ int here() const { return min(left, tiles - t); }
     // past `here` tiles: the next unit, if the run goes on
     __device__ __forceinline__ void next(const PArgs& a, int here) {
         left -= here;
@@ -96,7 +94,7 @@ struct Walk {
 };
 
 struct PlanSmem {
-    long long warp_sum[32];
+    int warp_sum[32];
     Walk walk;
 };
 // The run of this CTA; every thread of the CTA calls it. CTA 0 leaves the sums for the join.
@@ -110,62 +108,62 @@ __device__ inline Walk plan_run(const PArgs& a, PlanSmem& s) {
         w.unit = id - w.b * per_tile;
         w.len = length_of(a, w.b);
         w.tiles = tiles_of(a, w.len);
-        w.t = static_cast<int>(static_cast<uint32_t>(rank * w.tiles) / a.cluster);
-        w.left = static_cast<int>(static_cast<uint32_t>((rank + 1) * w.tiles) / a.cluster) - w.t;
+        w.t = rank * w.tiles / a.cluster;
+        w.left = (rank + 1) * w.tiles / a.cluster - w.t;
         return w;
     }
     const int c = blockIdx.x;
     if (!a.pages.lengths) {
         w.len = a.n;
         w.tiles = tiles_of(a, a.n);
-        const long long unit_tiles = static_cast<long long>(per_tile) * a.B;
-        const Shares share(a, unit_tiles * w.tiles);
-        const long long lo = share.first(c), unit = quotient(lo, w.tiles);
+        const Shares share(a, per_tile * a.B * w.tiles);
+        const int lo = share.first(c), unit = lo / w.tiles;
         w.left = c < share.n ? share.first(c + 1) - lo : 0;
-        w.t = static_cast<int>(lo - unit * w.tiles);
-        w.b = static_cast<int>(quotient(unit, per_tile));
-        w.unit = static_cast<int>(unit - static_cast<long long>(w.b) * per_tile);
+        w.t = lo - unit * w.tiles;
+        w.b = unit / per_tile;
+        w.unit = unit - w.b * per_tile;
         return w;
     }
     // a stretch of sequences a thread, their sums added up over the CTA
-    const int each = (a.B + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
+    const int threads = static_cast<int>(blockDim.x);
+    const int each = a.B <= threads ? 1 : (a.B + threads - 1) / threads;
     const int b0 = min(a.B, tid * each), b1 = min(a.B, b0 + each);
-    long long sum = 0;
-    for (int b = b0; b < b1; ++b) sum += static_cast<long long>(per_tile) * tiles_of(a, length_of(a, b));
-    long long incl = sum;
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) sum += per_tile * tiles_of(a, length_of(a, b));
+    int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
     }
     if (lane == 31) s.warp_sum[warp] = incl;
     if (tid == 0) s.walk.left = 0;
     __syncthreads();
-    long long before = incl - sum, total = 0;
-    for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) {
-        if (i < warp) before += s.warp_sum[i];
-        total += s.warp_sum[i];
+    int before = incl - sum, total = 0;
+    for (int i = 0; i < threads / 32; ++i) {
+        const int x = s.warp_sum[i];
+        if (i < warp) before += x;
+        total += x;
     }
     const Shares share(a, total);
-    const long long lo = share.first(c);
+    const int lo = share.first(c);
     const bool mine = c < share.n && lo >= before && lo < before + sum;
     if (c == 0 || mine) {
         for (int b = b0; b < b1; ++b) {
             if (c == 0) a.before[b] = before;
-            const int len = length_of(a, b), tiles = tiles_of(a, len);
-            const long long here = static_cast<long long>(per_tile) * tiles;
+            const int len = length_of(a, b), tiles = tiles_of(a, len), here = per_tile * tiles;
             if (mine && lo >= before && lo < before + here) {
                 w.left = share.first(c + 1) - lo;
                 w.b = b;
-                w.unit = static_cast<int>(quotient(lo - before, tiles));
-                w.t = static_cast<int>(lo - before - static_cast<long long>(w.unit) * tiles);
+                w.unit = (lo - before) / tiles;
+                w.t = lo - before - w.unit * tiles;
                 w.tiles = tiles;
                 w.len = len;
                 s.walk = w;
             }
             before += here;
         }
-        if (c == 0 && tid == static_cast<int>(blockDim.x) - 1) a.before[a.B] = total;
+        if (c == 0 && tid == threads - 1) a.before[a.B] = total;
     }
     __syncthreads();
     return s.walk;
@@ -211,7 +209,7 @@ __device__ inline void join_cluster(const PArgs& a, const float* share, int b, i
             const size_t row = static_cast<size_t>(b) * a.Hq + g * a.G + h0 + h;
             if (mp_check(a.status, static_cast<long long>(row), static_cast<long long>(a.B) * a.Hq,
                          kSitePagedOut))
-                a.out[row * kD + tid] = sum == 0.0f ? 0.0f : out * __frcp_rn(sum);
+                a.out[row * kD + tid] = over_sum(out, sum);
         }
     }
     if (a.cluster > 1) cluster_barrier();        // no CTA leaves while another reads from it
@@ -220,7 +218,7 @@ __device__ inline void join_cluster(const PArgs& a, const float* share, int b, i
 // Over a bf16 cache, on the tensor cores (mp_paged_tc.cu): query heads a unit takes for a group of G,
 // its CTAs, the tokens of its tiles, and the launch.
 int paged_tc_heads(int G);
-constexpr int kPagedTcCtas = 152, kPagedTcTile = 128;
+constexpr int kPagedTcCtas = 152, kPagedTcShift = 7;
 cudaError_t launch_paged_attention_tc(const PArgs& a, const mp_paged& cache, unsigned grid,
                                       cudaStream_t st);
 cudaError_t prepare_paged_tc();

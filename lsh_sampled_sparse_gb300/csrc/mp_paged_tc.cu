@@ -34,29 +34,32 @@
 namespace mp {
 namespace {
 
-constexpr int kTile = kPagedTcTile;              // tokens
+constexpr int kTile = 1 << kPagedTcShift;        // tokens
+static_assert(kTile == kD, "the MMA's 128 rows are a tile's tokens, or the dims");
 constexpr int kSoftWarps = 4, kSoftThreads = 32 * kSoftWarps;
 constexpr int kWarps = 7, kThreads = 32 * kWarps;
 constexpr uint32_t kStage = kTile * kD * 2;      // 32 KB: a tile of K or of V
 constexpr uint32_t kGroup = 2048;                // 8 tokens: two swizzled kilobytes
 constexpr int kTerms = 3;
 
-template <int NH>
+// NH query heads a unit, QT terms a query element
+template <int NH, int QT>
 struct Lay {
-    static constexpr int kN = (kTerms * NH + 15) / 16 * 16;              // columns of an MMA
-    static constexpr int kColumns = kN <= 16 ? 16 : (kN <= 32 ? 32 : 64);    // apart in tensor memory
-    static constexpr int kTmem = kColumns == 16 ? 64 : 4 * kColumns;     // S, S, O
-    static constexpr int kKStages = 3, kVStages = NH <= 8 ? 3 : 2;
-    static constexpr uint32_t kOperand = kN * kD * 2;                    // Q, or P: N rows of 256 bytes
+    static constexpr int kN = (kTerms * NH + 15) / 16 * 16;              // columns of O: of the weights
+    static constexpr int kNq = (QT * NH + 15) / 16 * 16;                 // columns of S: of the queries
+    static constexpr uint32_t kTmemS = 64, kTmemO = 128, kTmem = 256;    // S, S, O: columns apart
+    static constexpr int kKStages = 3, kVStages = NH == 16 && QT == 3 ? 2 : 3;
+    static constexpr uint32_t kP = kN * kD * 2, kQ = kNq * kD * 2;       // rows of 256 bytes
     static constexpr uint32_t kOffV = kKStages * kStage;
     static constexpr uint32_t kOffP = kOffV + kVStages * kStage;
-    static constexpr uint32_t kOffQ = kOffP + kOperand;
-    static constexpr uint32_t kOffBars = kOffQ + 2 * kOperand;
+    static constexpr uint32_t kOffQ = kOffP + kP;
+    static constexpr uint32_t kOffBars = kOffQ + 2 * kQ;
     static constexpr uint32_t kOffMax = kOffBars + 256;                  // [2][warps][NH]
-    static constexpr uint32_t kOffPlan = kOffMax + 2 * kSoftWarps * NH * 4;
+    static constexpr uint32_t kOffSum = kOffMax + 2 * kSoftWarps * NH * 4;   // [warps][NH]
+    static constexpr uint32_t kOffPlan = kOffSum + kSoftWarps * NH * 4;
     static constexpr uint32_t kBytes = kOffPlan + sizeof(PlanSmem) + 1024;   // + alignment slack
-    static_assert(kBytes <= 232448, "shared memory budget");
-    static_assert(kOperand % 1024 == 0, "swizzled operands start on 1024-byte boundaries");
+    static_assert(kN <= kTmemS && kBytes <= 232448 - 64, "tensor memory, shared memory");
+    static_assert(kP % 1024 == 0 && kQ % 1024 == 0, "swizzled operands start on 1024-byte boundaries");
 };
 
 // Three bf16 terms of two floats, packed (low: the first)
@@ -82,11 +85,11 @@ __device__ __forceinline__ void softmax_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory");
 }
 
-template <int NH>
+template <int NH, int QT>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attention_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                               const __grid_constant__ CUtensorMap vmap, const PArgs a) {
-    using L = Lay<NH>;
+    using L = Lay<NH, QT>;
     constexpr int N = L::kN;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -123,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    const uint32_t tmem_o = tmem + 2 * L::kColumns;
+    const uint32_t tmem_o = tmem + L::kTmemO;
     wait_for_predecessor();
     allow_dependents();
     Walk w = plan_run(a, *reinterpret_cast<PlanSmem*>(smem + L::kOffPlan));
@@ -131,6 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* share = reinterpret_cast<float*>(smem);
     const int unit_b = w.b, unit = w.unit;       // of a cluster: its only ones
 
+    const int box_rows = min(kTile, a.pages.page_size & -a.pages.page_size);
     if (warp < kSoftWarps) {
         // ---------------- softmax ----------------
         if (a.cluster && w.left == 0) {          // fewer tiles than CTAs
@@ -143,52 +147,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t quad = static_cast<uint32_t>(warp * 32) << 16;    // this warp's TMEM lanes
         const uint32_t chunk = (tid & 63) >> 3;
         const uint32_t p_at = base + L::kOffP + (tid >> 6) * (N * 128) + (chunk << 4) + (tid & 7) * 2;
+        float* sums = reinterpret_cast<float*>(smem + L::kOffSum);
         bool aborted = false;
         auto wait = [&](uint32_t bar, int phase) {
             if (!aborted)
                 aborted = !__all_sync(0xffffffffu, mbar_wait(bar, phase & 1, abort_flag, a.status));
         };
-        int it = 0;
-        while (w.left > 0) {
-            const int here = w.here(), g = kv_head(a, w.unit), h0 = (w.unit - g * a.chunks) * NH;
-            const int32_t* slots = a.pages.table + static_cast<long long>(w.b) * a.pages.stride;
-            float m[NH], l[NH], o[NH];
+        // the unit at hand, and the one before, whose last tile's values are still to come while this
+        // one's first scores are worked on
+        struct Unit {
+            int b, g, h0, t, len;
+            bool whole;
+        };
+        Unit now{0, 0, 0, 0, 0, false}, last = now;
+        const int32_t* slots = nullptr;
+        const int total = w.left;
+        int here = 0, k = 0, page = -1;
+        float m[NH], l[NH], o[NH];
 #pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                m[h] = -INFINITY;
-                l[h] = o[h] = 0.0f;
+        for (int h = 0; h < NH; ++h) {
+            m[h] = -INFINITY;
+            l[h] = o[h] = 0.0f;
+        }
+        for (int it = 0; total > 0; ++it) {
+            const bool more = it < total, fresh = k == here;             // fresh: a unit's first, or the end
+            float m_last[NH], l_last[NH], s[NH], corr[NH];
+            if (fresh) {
+                last = now;
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    m_last[h] = m[h];
+                    l_last[h] = l[h];
+                    m[h] = -INFINITY;
+                    l[h] = 0.0f;
+                }
+                if (more) {
+                    here = w.here();
+                    k = 0;
+                    const int g = kv_head(a, w.unit);
+                    now = Unit{w.b, g, (w.unit - g * a.chunks) * NH, w.t, w.len, here == w.tiles};
+                    slots = a.pages.table + static_cast<long long>(w.b) * a.pages.stride;
+                    const int tok = now.t * kTile + tid;
+                    page = tok < now.len ? slots[slot_of(a, tok)] : -1;
+                    w.next(a, here);
+                }
             }
-            auto add_o = [&](int at) {           // the sums of tile `at`, added to the running ones
-                wait(o_full, at);
-                if (aborted) return;
-                tc_fence_after();
-                uint32_t t0[NH], t1[NH], t2[NH];
-                tmem_ld(tmem_o + quad, t0);
-                tmem_ld(tmem_o + quad + NH, t1);
-                tmem_ld(tmem_o + quad + 2 * NH, t2);
-                tmem_ld_wait();
-#pragma unroll
-                for (int h = 0; h < NH; ++h)
-                    o[h] += __uint_as_float(t0[h]) +
-                            (__uint_as_float(t1[h]) + __uint_as_float(t2[h]));
-            };
-            auto page_at = [&](int k) {          // the slot of this thread's token of tile k
-                const int tok = (w.t + k) * kTile + tid;
-                return k < here && tok < w.len ? slots[slot_of(a, tok)] : -1;
-            };
-            int page = page_at(0);
-            for (int k = 0; k < here; ++k, ++it) {
-                const int tok0 = (w.t + k) * kTile;
-                const bool live = page >= 0 && page < a.pages.n_pages;   // and before the end
-                page = page_at(k + 1);
-                float s[NH];
+            const int tok0 = (now.t + k) * kTile;
+            if (more) {
                 wait(s_full + 8 * (it & 1), it >> 1);
                 if (!aborted) {
                     tc_fence_after();
-                    const uint32_t from = tmem + quad + (it & 1) * L::kColumns;
+                    const uint32_t from = tmem + quad + (it & 1) * L::kTmemS;
                     uint32_t t0[NH];
                     tmem_ld(from, t0);
-                    if (!a.q_bf16) {
+                    if constexpr (QT == 3) {
                         uint32_t t1[NH], t2[NH];
                         tmem_ld(from + NH, t1);
                         tmem_ld(from + 2 * NH, t2);
@@ -209,6 +221,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_empty + 8 * (it & 1));
+                const bool live = page >= 0 && page < a.pages.n_pages;   // and before the end
+                const int tok = tok0 + kTile + tid;
+                page = k + 1 < here && tok < now.len ? slots[slot_of(a, tok)] : -1;
                 // ---- the tile's maxima, over the warp and over the four
                 float* most = reinterpret_cast<float*>(smem + L::kOffMax) + (it & 1) * kSoftWarps * NH;
                 float mine[NH];
@@ -224,7 +239,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                             make_float4(mine[h], mine[h + 1], mine[h + 2], mine[h + 3]);
                 }
                 softmax_sync();
-                float corr[NH];
 #pragma unroll
                 for (int h = 0; h < NH; h += 4) {
                     float4 x = *reinterpret_cast<const float4*>(most + h);
@@ -245,13 +259,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                         m[h + j] = mn;
                     }
                 }
-                // ---- the last tile's values; the weights take the place of the last ones then
-                if (k > 0) {
-                    add_o(it - 1);
-                    tc_fence_before();
-                }
+            }
+            // ---- the last tile's values; the weights take the place of the last ones then
+            if (it > 0) {
+                wait(o_full, it - 1);
+                if (!aborted) {
+                    tc_fence_after();
+                    uint32_t t0[NH], t1[NH], t2[NH];
+                    tmem_ld(tmem_o + quad, t0);
+                    tmem_ld(tmem_o + quad + NH, t1);
+                    tmem_ld(tmem_o + quad + 2 * NH, t2);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int h = 0; h < NH; ++h) o[h] *= corr[h];
+                    for (int h = 0; h < NH; ++h)
+                        o[h] += __uint_as_float(t0[h]) +
+                                (__uint_as_float(t1[h]) + __uint_as_float(t2[h]));
+                }
+                tc_fence_before();
+            }
+            if (more) {
 #pragma unroll
                 for (int h = 0; h < NH; h += 2) {
                     uint32_t t[kTerms];
@@ -266,86 +292,118 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      "h"(static_cast<uint16_t>(t[i] >> 16)) : "memory");
                     }
                 }
-                // ---- rows of V behind the sequence's end: a weight of 0 does not undo a NaN there
-                if (tok0 + kTile > w.len) {
-                    const int stage = it % L::kVStages;
+                // ---- rows of V from the sequence's end to the end of their box: a weight of 0 does not
+                // undo a NaN there (boxes behind it read as zeros)
+                if (tok0 + kTile > now.len) {
+                    const int stage = it % L::kVStages, row0 = now.len - tok0;
+                    const int lines = ((row0 + box_rows - 1) / box_rows * box_rows - row0) * 16;
                     wait(v_full + 8 * stage, it / L::kVStages);
-                    if (!aborted && tok0 + tid >= w.len) {
-                        uint8_t* row = smem + L::kOffV + stage * kStage + (tid >> 3) * kGroup +
-                                       (tid & 7) * 128;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            *reinterpret_cast<uint4*>(row + (i >> 3) * 1024 + (i & 7) * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
+                    for (int x = tid; !aborted && x < lines; x += kSoftThreads) {
+                        const int row = row0 + (x >> 4);                 // 16 pieces of 16 bytes a row
+                        *reinterpret_cast<uint4*>(smem + L::kOffV + stage * kStage +
+                                                  (row >> 3) * kGroup + (x >> 3 & 1) * 1024 +
+                                                  (row & 7) * 128 + (x & 7) * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
                     }
                 }
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full);
             }
-            add_o(it - 1);
-            tc_fence_before();
-            // ---- the unit's state: sums of weights over the threads, then a dim a thread
-            float* sums = reinterpret_cast<float*>(smem + L::kOffMax) + (it & 1) * kSoftWarps * NH;
+            if (!fresh) {
 #pragma unroll
-            for (int h = 0; h < NH; ++h)
+                for (int h = 0; h < NH; ++h) o[h] *= corr[h];
+            } else {
+                if (it > 0) {
+                    // ---- the last unit's state: its weights' sums by a reduce-scatter over the lanes (to
+                    // 32 / NH of them), then over the warps; a dim a thread
+                    float* r = l_last;
 #pragma unroll
-                for (int x = 16; x; x >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
-            if (lane == 0) {
+                    for (int lv = 0; (NH / 2 >> lv) >= 1; ++lv) {
+                        const int off = 16 >> lv, keep = NH / 2 >> lv;
+                        const bool up = (lane & off) != 0;
 #pragma unroll
-                for (int h = 0; h < NH; ++h) sums[warp * NH + h] = l[h];
-            }
-            softmax_sync();
-            const int heads = aborted ? 0 : min(NH, a.G - h0);
-            const size_t row0 = static_cast<size_t>(w.b) * a.Hq + g * a.G + h0;
-#pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                const float sum = (sums[h] + sums[NH + h]) + (sums[2 * NH + h] + sums[3 * NH + h]);
-                if (h >= heads) continue;
-                if (a.cluster) {
-                    share[h * kPart + tid] = o[h];
-                    if (tid == 0) {
-                        share[h * kPart + kD] = m[h];
-                        share[h * kPart + kD + 1] = sum;
+                        for (int i = 0; i < keep; ++i) {
+                            const float send = up ? r[i] : r[i + keep];
+                            r[i] = (up ? r[i + keep] : r[i]) + __shfl_xor_sync(0xffffffffu, send, off);
+                        }
                     }
-                } else if (here == w.tiles) {
-                    if (mp_check(a.status, static_cast<long long>(row0 + h),
-                                 static_cast<long long>(a.B) * a.Hq, kSitePagedOut))
-                        a.out[(row0 + h) * kD + tid] = sum == 0.0f ? 0.0f : o[h] * __frcp_rn(sum);
-                } else {
-                    float* p = part_of(a, w.t == 0, h);
-                    p[tid] = o[h];
-                    if (tid == 0) {
-                        p[kD] = m[h];
-                        p[kD + 1] = sum;
+#pragma unroll
+                    for (int off = 16 / NH; off >= 1; off >>= 1)
+                        r[0] += __shfl_xor_sync(0xffffffffu, r[0], off);
+                    if ((lane & (32 / NH - 1)) == 0) sums[warp * NH + lane * NH / 32] = r[0];
+                    softmax_sync();
+                    const int heads = aborted ? 0 : min(NH, a.G - last.h0);
+                    const size_t row0 = static_cast<size_t>(last.b) * a.Hq + last.g * a.G + last.h0;
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) {
+                        if (h >= heads) break;
+                        const float sum = (sums[h] + sums[NH + h]) + (sums[2 * NH + h] + sums[3 * NH + h]);
+                        if (a.cluster) {
+                            share[h * kPart + tid] = o[h];
+                            if (tid == 0) {
+                                share[h * kPart + kD] = m_last[h];
+                                share[h * kPart + kD + 1] = sum;
+                            }
+                        } else if (last.whole) {
+                            if (mp_check(a.status, static_cast<long long>(row0 + h),
+                                         static_cast<long long>(a.B) * a.Hq, kSitePagedOut))
+                                a.out[(row0 + h) * kD + tid] = over_sum(o[h], sum);
+                        } else {
+                            float* p = part_of(a, last.t == 0, h);
+                            p[tid] = o[h];
+                            if (tid == 0) {
+                                p[kD] = m_last[h];
+                                p[kD + 1] = sum;
+                            }
+                        }
                     }
                 }
+#pragma unroll
+                for (int h = 0; h < NH; ++h) o[h] = 0.0f;
+                if (!more) break;
             }
-            softmax_sync();                      // the sums' place is the next unit's maxima's
-            w.next(a, here);
+            ++k;
         }
     } else if (warp == 4) {
         // ---------------- TMA producer ----------------
-        const int rows = min(kTile, a.pages.page_size & -a.pages.page_size);     // of a box
-        const int boxes = kTile / rows;
+        // a batch: the table's entries of the next 32 boxes of a unit, an entry a lane, looked up while
+        // the last batch's tiles are copied
+        const int boxes = kTile / box_rows;      // of a tile
+        const int box_shift = __ffs(boxes) - 1, batch = 32 >> box_shift;
+        struct Batch {
+            int tiles, page, head, group;        // tiles in it; the entry, the KV head, the group of a page
+        };
+        int k = 0;
+        auto look_up = [&]() {
+            Batch x{0, -1, 0, 0};
+            if (w.left <= 0) return x;
+            const int here = w.here(), tok = (w.t + k) * kTile + lane * box_rows;
+            x.tiles = min(batch, here - k);
+            x.head = kv_head(a, w.unit);
+            if (tok < w.len && lane < x.tiles << box_shift) {
+                const int slot = slot_of(a, tok);
+                x.page = a.pages.table[static_cast<long long>(w.b) * a.pages.stride + slot];
+                x.group = (tok - slot * a.pages.page_size) >> 3;
+            }
+            k += x.tiles;
+            if (k == here) {
+                w.next(a, here);
+                k = 0;
+            }
+            return x;
+        };
         int it = 0;
         bool ok = true;
-        while (w.left > 0 && ok) {
-            const int here = w.here(), g = kv_head(a, w.unit);
-            const int32_t* slots = a.pages.table + static_cast<long long>(w.b) * a.pages.stride;
-            auto page_at = [&](int k) {
-                const int tok = (w.t + k) * kTile + lane * rows;
-                return k < here && lane < boxes && tok < w.len ? slots[slot_of(a, tok)] : -1;
-            };
-            int page = page_at(0);
-            for (int k = 0; k < here; ++k, ++it) {
-                const int tok = (w.t + k) * kTile + lane * rows;
-                const bool there = page >= 0 && page < a.pages.n_pages;
-                // outside the tensor where there is no page
-                const int c4 = there ? page * a.Hkv + g : a.pages.n_pages * a.Hkv;
-                const int c3 = (tok - slot_of(a, tok) * a.pages.page_size) >> 3;
-                page = page_at(k + 1);
+        for (Batch x = look_up(); x.tiles > 0 && ok;) {
+            const Batch ahead = look_up();
+            // outside the tensor where there is no page
+            const bool there = x.page >= 0 && x.page < a.pages.n_pages;
+            const int at = there ? x.page * a.Hkv + x.head : a.pages.n_pages * a.Hkv;
+            const uint32_t dst = base + (lane & (boxes - 1)) * (box_rows / 8) * kGroup;
+            for (int i = 0; i < x.tiles; ++i, ++it) {
                 const int ks = it % L::kKStages, vs = it % L::kVStages;
+                const bool mine = lane >> box_shift == i;
                 if (!__all_sync(0xffffffffu, mbar_wait(k_empty + 8 * ks, (it / L::kKStages & 1) ^ 1,
                                                        abort_flag, a.status))) {
                     ok = false;
@@ -353,9 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (lane == 0) mbar_arrive_expect_tx(k_full + 8 * ks, kStage);
                 __syncwarp();
-                if (lane < boxes)
-                    tma_load_5d(base + ks * kStage + lane * (rows / 8) * kGroup, &kmap,
-                                k_full + 8 * ks, 0, 0, 0, c3, c4);
+                if (mine) tma_load_5d(dst + ks * kStage, &kmap, k_full + 8 * ks, 0, 0, 0, x.group, at);
                 if (!__all_sync(0xffffffffu, mbar_wait(v_empty + 8 * vs, (it / L::kVStages & 1) ^ 1,
                                                        abort_flag, a.status))) {
                     ok = false;
@@ -363,11 +419,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (lane == 0) mbar_arrive_expect_tx(v_full + 8 * vs, kStage);
                 __syncwarp();
-                if (lane < boxes)
-                    tma_load_5d(base + L::kOffV + vs * kStage + lane * (rows / 8) * kGroup, &vmap,
-                                v_full + 8 * vs, 0, 0, 0, c3, c4);
+                if (mine)
+                    tma_load_5d(dst + L::kOffV + vs * kStage, &vmap, v_full + 8 * vs, 0, 0, 0, x.group, at);
             }
-            if (ok) w.next(a, here);
+            x = ahead;
         }
         if (!ok && lane == 0) {
             // let the loads already issued land before the CTA can exit (bounded): those of tile `it`
@@ -383,8 +438,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 5) {
         // ---------------- MMA issuer ----------------
         if (lane == 0 && w.left > 0) {
-            const uint32_t s_desc = make_idesc(kTile, N), o_desc = make_idesc(kD, N, true);
-            const long long total = w.left;
+            const uint32_t s_desc = make_idesc(kTile, L::kNq), o_desc = make_idesc(kD, N, true);
+            const int total = w.left;
             int seg = 0, in_seg = w.here();      // tiles of the unit not scored yet
             auto wait = [&](uint32_t bar, int phase) {
                 return mbar_wait(bar, phase & 1, abort_flag, a.status);
@@ -398,12 +453,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     !wait(s_empty + 8 * (it & 1), (it >> 1) ^ 1))
                     return false;
                 tc_fence_after();
-                const uint32_t k_at = base + ks * kStage, q_at = base + L::kOffQ + slot * L::kOperand;
+                const uint32_t k_at = base + ks * kStage, q_at = base + L::kOffQ + slot * L::kQ;
 #pragma unroll
                 for (int x = 0; x < kD / 16; ++x)
-                    tc_mma(tmem + (it & 1) * L::kColumns,
+                    tc_mma(tmem + (it & 1) * L::kTmemS,
                            sw128_desc(k_at + (x >> 2) * 1024 + (x & 3) * 32, kGroup),
-                           sw128_desc(q_at + (x >> 2) * (N * 128) + (x & 3) * 32), s_desc, x > 0);
+                           sw128_desc(q_at + (x >> 2) * (L::kNq * 128) + (x & 3) * 32), s_desc, x > 0);
                 tc_commit(k_empty + 8 * ks);
                 tc_commit(s_full + 8 * (it & 1));
                 if (--in_seg == 0) {
@@ -440,15 +495,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!__all_sync(0xffffffffu, mbar_wait(q_empty + 8 * (seg & 1), (seg >> 1 & 1) ^ 1,
                                                    abort_flag, a.status)))
                 break;
-            uint8_t* dst = smem + L::kOffQ + (seg & 1) * L::kOperand + (lane >> 4) * (N * 128);
+            uint8_t* dst = smem + L::kOffQ + (seg & 1) * L::kQ + (lane >> 4) * (L::kNq * 128);
             float x[NH][4];
 #pragma unroll
-            for (int h = 0; h < NH; ++h) {
+            for (int h = 0; h < NH; ++h) {       // q is bf16 where QT is 1
                 const size_t from = (row0 + min(h, heads - 1)) * kD + 4 * lane;
                 if (!a.q_wide) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[h][e] = load_elem(a.q, a.q_bf16, from + e);
-                } else if (a.q_bf16) {
+                } else if constexpr (QT == 1) {
                     const uint2 v = *reinterpret_cast<const uint2*>(
                         static_cast<const __nv_bfloat16*>(a.q) + from);
                     x[h][0] = __uint_as_float(v.x << 16);
@@ -470,9 +525,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 three_terms(x[h][0], x[h][1], t0);
                 three_terms(x[h][2], x[h][3], t1);
 #pragma unroll
-                for (int i = 0; i < kTerms; ++i) {
+                for (int i = 0; i < QT; ++i) {
                     const int n = i * NH + h;
-                    if (i == 0 || !a.q_bf16)
                         *reinterpret_cast<uint2*>(dst + n * 128 +
                                                   ((((lane & 15) >> 1) ^ (n & 7)) << 4) +
                                                   (lane & 1) * 8) = make_uint2(t0[i], t1[i]);
@@ -496,11 +550,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 typedef void (*TcFn)(const CUtensorMap, const CUtensorMap, const PArgs);
-TcFn pick_tc(int nh, uint32_t* smem) {
+template <int NH, int QT>
+TcFn tc(uint32_t* smem) {
+    *smem = Lay<NH, QT>::kBytes;
+    return paged_attention_tc_kernel<NH, QT>;
+}
+TcFn pick_tc(int nh, bool q_bf16, uint32_t* smem) {
     switch (nh) {
-        case 4: *smem = Lay<4>::kBytes; return paged_attention_tc_kernel<4>;
-        case 8: *smem = Lay<8>::kBytes; return paged_attention_tc_kernel<8>;
-        default: *smem = Lay<16>::kBytes; return paged_attention_tc_kernel<16>;
+        case 4: return q_bf16 ? tc<4, 1>(smem) : tc<4, 3>(smem);
+        case 8: return q_bf16 ? tc<8, 1>(smem) : tc<8, 3>(smem);
+        default: return q_bf16 ? tc<16, 1>(smem) : tc<16, 3>(smem);
     }
 }
 
@@ -528,7 +587,7 @@ cudaError_t launch_paged_attention_tc(const PArgs& a, const mp_paged& cache, uns
     if (!page_map(&kmap, cache.keys, cache, a.Hkv) || !page_map(&vmap, cache.values, cache, a.Hkv))
         return cudaErrorInvalidValue;
     uint32_t smem;
-    const TcFn fn = pick_tc(a.nh, &smem);
+    const TcFn fn = pick_tc(a.nh, a.q_bf16, &smem);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
@@ -546,9 +605,9 @@ cudaError_t launch_paged_attention_tc(const PArgs& a, const mp_paged& cache, uns
 }
 
 cudaError_t prepare_paged_tc() {
-    for (int nh : {4, 8, 16}) {
+    for (int i = 0; i < 6; ++i) {
         uint32_t smem;
-        const TcFn fn = pick_tc(nh, &smem);
+        const TcFn fn = pick_tc(4 << i / 2, i & 1, &smem);
         cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
         if (e == cudaSuccess)
