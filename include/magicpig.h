@@ -631,7 +631,7 @@ MP_API mp_status mp_device_status(int* status);
 
 /* The MP_CHECKS build (the library compiled with -DMP_CHECKS=1, libmagicpig_checks.so): every
  * kernel of the decode path, the bucketed lookup, the tensor-core encoder, the CUDA-core encoders
- * of mp_encode_keys and mp_encode_rows and the 4-bit cache check the indices of their global
+ * of mp_encode_keys and mp_encode_rows, the 4-bit cache and the paged cache check the indices of their global
  * accesses (code blocks, selection words, K/V rows, partial states, bucket ranges and members, code
  * words written) and skip an access that is out of range instead of making it, raising
  * MP_ERR_BOUNDS in the status word. A stand-in for a memory checker: the paper has no counterpart.
@@ -641,8 +641,9 @@ MP_API mp_status mp_device_status(int* status);
  * copied, 5 partial state or output written, 6 selection words read, 7 bucket range beyond the
  * table's keys, 8 bucket member beyond n_indexed, 9 code words written by the encoders, 10 a row of
  * the 4-bit cache, 11 rows read back from it, partial states and output rows of its attention, 12 a
- * key row that a CUDA-core encoder reads, 13 the list of an attend CTA's selected keys. Neither
- * word is reset. Errors: MP_ERR_INVALID_ARG (null), MP_ERR_CUDA. */
+ * key row that a CUDA-core encoder reads, 13 the list of an attend CTA's selected keys, 14 a row of the
+ * paged cache, 15 rows returned by an append to it and output rows of its attention. Neither word is
+ * reset. Errors: MP_ERR_INVALID_ARG (null), MP_ERR_CUDA. */
 MP_API mp_status mp_debug_check_report(int* enabled, int* site);
 
 #ifdef __cplusplus

@@ -797,7 +797,7 @@ mp_status mp_paged_append(const mp_rows* keys, const mp_rows* values, const mp_r
 
 size_t mp_paged_attention_workspace_bytes(int B, int Hq, int Hkv, int n, int d) {
     if (!valid_kv4_attention(B, Hq, Hkv, n, d) || d != kD) return 0;
-    return align256(paged_attention_scratch_bytes(B, Hq, Hkv));
+    return align256(paged_attention_scratch_bytes(Hq, Hkv));
 }
 
 mp_status mp_paged_attention(const void* q, mp_dtype q_dtype, const mp_paged* cache, int B, int Hq,

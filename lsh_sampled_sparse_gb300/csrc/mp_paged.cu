@@ -432,34 +432,30 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attention_simt_kernel(c
         w.next(a, here);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+    zero_empty(a, tid, kSimtThreads);
     if (a.cluster) {
         __syncthreads();
         join_cluster(a, share, unit_b, unit);
     }
 }
 
-// The parts of a query row, joined in a fixed order: warp w folds parts w, w + kJoinWarps, ...,
-// kJoinAhead of them loaded at once, four dims a lane; then the warps in order. A part that holds
-// nothing has m = -inf and zeros; NaN passes through its zero factor. A row that one CTA had to itself is
-// left as that CTA wrote it; rows of a sequence of length 0 are zero.
+// The parts of the units that several CTAs have, joined in a fixed order, a query row a CTA: blockIdx.x + 1
+// is the first of the CTAs whose run begins within the unit. Warp w folds parts w, w + kJoinWarps, ...,
+// kJoinAhead of them loaded at once, four dims a lane; then the warps in order. A part that holds nothing
+// has m = -inf and zeros; NaN passes through its zero factor.
 constexpr int kJoinWarps = 8, kJoinAhead = 4;
 __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const PArgs a) {
     __shared__ __align__(16) float join[kJoinWarps][kPart];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.x;
-    const int b = row / a.Hq, h = row - b * a.Hq, g = h / a.G, ch = (h - g * a.G) / a.nh;
-    const int hc = h - g * a.G - ch * a.nh, unit = g * a.chunks + ch, per_tile = a.Hkv * a.chunks;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x + 1;
     wait_for_predecessor();
-    const int tiles = tiles_of(a, length_of(a, b));
-    if (tiles == 0) {
-        if (threadIdx.x < kD) a.out[static_cast<size_t>(row) * kD + threadIdx.x] = 0.0f;
-        return;
-    }
-    const int each = per_tile * tiles;
-    const int total = a.pages.lengths ? __ldcg(a.before + a.B) : each * a.B;
-    const int t0 = (a.pages.lengths ? __ldcg(a.before + b) : each * b) + unit * tiles;
+    const int total = __ldcg(&a.begin[a.ctas].x);
+    const int4 at = __ldcg(a.begin + c);         // b, unit, t, tiles
     const Shares share(a, total);
-    const int c0 = share.of(t0), c1 = share.of(t0 + tiles - 1);
-    if (c0 == c1) return;
+    if (c >= share.n || at.z == 0) return;
+    const int t0 = share.first(c) - at.z, c0 = share.of(t0), c1 = share.of(t0 + at.w - 1);
+    const int g = kv_head(a, at.y), hc = blockIdx.y, h = (at.y - g * a.chunks) * a.nh + hc;
+    if (c0 != c - 1 || h >= a.G) return;
+    const size_t row = static_cast<size_t>(at.x) * a.Hq + g * a.G + h;
     float M = -INFINITY, L = 0.0f;
     float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int s0 = c0 + warp; s0 <= c1; s0 += kJoinWarps * kJoinAhead) {
@@ -515,12 +511,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const PArgs
         Ls = fmaf(c, join[i][kD + 1], Ls);
         Os = fmaf(c, join[i][e], Os);
     }
-    if (mp_check(a.status, row, static_cast<long long>(a.B) * a.Hq, kSitePagedOut))
-        a.out[static_cast<size_t>(row) * kD + e] = over_sum(Os, Ls);
+    if (mp_check(a.status, static_cast<long long>(row), static_cast<long long>(a.B) * a.Hq, kSitePagedOut))
+        a.out[row * kD + e] = over_sum(Os, Ls);
 }
 
 constexpr int kSimtCtas = 2 * kSms;
-constexpr int kJoinTiles = 2;
+constexpr int kJoinTokens = 512;
 int simt_heads(int G) { return G <= 2 ? G : (G <= 4 ? 4 : 8); }
 
 typedef void (*PFn)(const PArgs);
@@ -534,12 +530,12 @@ PFn pick_simt(int nh, int* smem) {
 }
 
 // The CTAs of the cluster that shares a unit of `tiles` tiles, 0 where all CTAs share all tiles.
-int cluster_size(long long units, int tiles, int ctas) {
+int cluster_size(long long units, int tiles, int ctas, int tile_shift) {
     if (units > ctas) return 0;
     const int most = std::min({kPagedMaxCluster, tiles, static_cast<int>(ctas / units)});
     const int each = (tiles + most - 1) / most;
     const long long even = (units * tiles + ctas - 1) / ctas;
-    return each - even <= kJoinTiles ? (tiles + each - 1) / each : 0;
+    return each - even <= kJoinTokens >> tile_shift ? (tiles + each - 1) / each : 0;
 }
 
 typedef void (*AppendFn)(const AppendArgs);
@@ -589,11 +585,11 @@ cudaError_t launch_paged_append(const mp_rows& keys, const mp_rows& values, cons
                             a);
 }
 
-size_t paged_attention_scratch_bytes(int B, int Hq, int Hkv) {
+size_t paged_attention_scratch_bytes(int Hq, int Hkv) {
     // of either kind of cache: who asks does not say which
     const size_t parts = std::max(kSimtCtas * simt_heads(Hq / Hkv),
                                   kPagedTcCtas * paged_tc_heads(Hq / Hkv));
-    return parts * 2 * kPart * sizeof(float) + (static_cast<size_t>(B) + 1) * sizeof(int);
+    return parts * 2 * kPart * sizeof(float) + (std::max(kSimtCtas, kPagedTcCtas) + 1) * sizeof(int4);
 }
 
 cudaError_t launch_paged_attention(const void* q, bool q_bf16, const mp_paged& cache, int B, int Hq,
@@ -622,11 +618,11 @@ cudaError_t launch_paged_attention(const void* q, bool q_bf16, const mp_paged& c
         if (cache.page_size == 1 << i) a.page_shift = i;
     const int tiles = ((n - 1) >> a.tile_shift) + 1;
     const long long units = static_cast<long long>(B) * Hkv * a.chunks;
-    a.cluster = cluster_size(units, tiles, a.ctas);
+    a.cluster = cluster_size(units, tiles, a.ctas, a.tile_shift);
     a.scale = scale * 1.4426950408889634f;
     a.status = device_status_ptr();
     a.part = static_cast<float*>(workspace);
-    a.before = reinterpret_cast<int*>(a.part + static_cast<size_t>(a.ctas) * 2 * a.nh * kPart);
+    a.begin = reinterpret_cast<int4*>(a.part + static_cast<size_t>(a.ctas) * 2 * a.nh * kPart);
     const unsigned grid = a.cluster ? static_cast<unsigned>(units) * a.cluster : a.ctas;
     int smem;
     const cudaError_t e = tc ? launch_paged_attention_tc(a, cache, grid, st)
@@ -636,7 +632,8 @@ cudaError_t launch_paged_attention(const void* q, bool q_bf16, const mp_paged& c
     // where every sequence has the same tiles, the shares may fall on whole units
     const long long total = units * tiles, shares = std::min<long long>(a.ctas, total);
     if (!lengths && total % shares == 0 && total / shares % tiles == 0) return e;
-    return launch_dependent(paged_join_kernel, dim3(static_cast<unsigned>(B) * Hq),
+    if (shares < 2) return e;
+    return launch_dependent(paged_join_kernel, dim3(static_cast<unsigned>(shares) - 1, std::min(a.nh, a.G)),
                             dim3(32 * kJoinWarps), 0, st, a);
 }
 

@@ -35,7 +35,8 @@ struct PArgs {
     const void* values;
     PageRef pages;
     float* part;                                 // [CTA][2][nh][kPart]: o, m, l
-    int* before;                                 // [B + 1] tiles of the sequences before (lengths only)
+    int4* begin;                                 // [CTA] where its run begins: b, unit, t, tiles; then the
+                                                 // number of all tiles
     float* out;
     int q_bf16, q_wide, B, Hq, Hkv, G, chunks, nh, n, ctas;
     int tile_shift;                              // log2 of a tile's tokens
@@ -97,7 +98,7 @@ struct PlanSmem {
     int warp_sum[32];
     Walk walk;
 };
-// The run of this CTA; every thread of the CTA calls it. CTA 0 leaves the sums for the join.
+// The run of this CTA; every thread of the CTA calls it. Where it begins is left for the join.
 __device__ inline Walk plan_run(const PArgs& a, PlanSmem& s) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per_tile = a.Hkv * a.chunks;       // tiles of a sequence for each tile of its length
@@ -122,14 +123,19 @@ __device__ inline Walk plan_run(const PArgs& a, PlanSmem& s) {
         w.t = lo - unit * w.tiles;
         w.b = unit / per_tile;
         w.unit = unit - w.b * per_tile;
+        if (tid == 0) {
+            a.begin[c] = make_int4(w.b, w.unit, w.t, w.tiles);
+            if (c == 0) a.begin[a.ctas].x = per_tile * a.B * w.tiles;
+        }
         return w;
     }
     // a stretch of sequences a thread, their sums added up over the CTA
     const int threads = static_cast<int>(blockDim.x);
     const int each = a.B <= threads ? 1 : (a.B + threads - 1) / threads;
     const int b0 = min(a.B, tid * each), b1 = min(a.B, b0 + each);
-    int sum = 0;
-    for (int b = b0; b < b1; ++b) sum += per_tile * tiles_of(a, length_of(a, b));
+    const int len0 = b0 < b1 ? length_of(a, b0) : 0;             // mostly the only one
+    int sum = per_tile * tiles_of(a, len0);
+    for (int b = b0 + 1; b < b1; ++b) sum += per_tile * tiles_of(a, length_of(a, b));
     int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -148,25 +154,34 @@ __device__ inline Walk plan_run(const PArgs& a, PlanSmem& s) {
     const Shares share(a, total);
     const int lo = share.first(c);
     const bool mine = c < share.n && lo >= before && lo < before + sum;
-    if (c == 0 || mine) {
-        for (int b = b0; b < b1; ++b) {
-            if (c == 0) a.before[b] = before;
-            const int len = length_of(a, b), tiles = tiles_of(a, len), here = per_tile * tiles;
-            if (mine && lo >= before && lo < before + here) {
-                w.left = share.first(c + 1) - lo;
-                w.b = b;
-                w.unit = (lo - before) / tiles;
-                w.t = lo - before - w.unit * tiles;
-                w.tiles = tiles;
-                w.len = len;
-                s.walk = w;
-            }
-            before += here;
+    if (mine) {
+        int b = b0, len = len0, tiles = tiles_of(a, len0);
+        for (; lo >= before + per_tile * tiles; tiles = tiles_of(a, len)) {
+            before += per_tile * tiles;
+            len = length_of(a, ++b);
         }
-        if (c == 0 && tid == threads - 1) a.before[a.B] = total;
+        w.left = share.first(c + 1) - lo;
+        w.b = b;
+        w.unit = (lo - before) / tiles;
+        w.t = lo - before - w.unit * tiles;
+        w.tiles = tiles;
+        w.len = len;
+        s.walk = w;
+        a.begin[c] = make_int4(w.b, w.unit, w.t, w.tiles);
     }
+    if (c == 0 && tid == 0) a.begin[a.ctas].x = total;
     __syncthreads();
     return s.walk;
+}
+
+// Sequences of length 0 have no tiles: their rows, shared out to the CTAs, are zeroed by `threads` threads
+__device__ inline void zero_empty(const PArgs& a, int thread, int threads) {
+    if (a.cluster || !a.pages.lengths) return;
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+        if (length_of(a, b) == 0)
+            for (int i = thread; i < a.Hq * kD / 4; i += threads)
+                reinterpret_cast<float4*>(a.out + static_cast<size_t>(b) * a.Hq * kD)[i] =
+                    make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 }
 
 // Where a unit's state goes: out, where the CTA has all its tiles, else one of its two places

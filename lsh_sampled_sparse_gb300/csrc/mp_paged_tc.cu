@@ -538,6 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++seg;
             w.next(a, here);
         }
+        zero_empty(a, lane, 32);
     }
     tc_fence_before();
     __syncthreads();
