@@ -631,15 +631,28 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
         q8[i] = load_elem(a.q, a.q_bf16, static_cast<size_t>(row) * kD + 8 * hl + i);
         mu8[i] = KV == kKv4 ? 0.0f : a.centre[static_cast<size_t>(bg) * kD + 8 * hl + i];
     }
-    wait_for_predecessor();                      // selection words, query norms
-    const float4 st = a.qstat[row];
-    const float qn = st.x, qmu = KV == kKv4 ? 0.0f : st.y;
+    const int blk0 = sb * kAttendBlocks;
+    int* pslot = reinterpret_cast<int*>(cbuf);   // paged: the table's entries of this CTA's blocks
+    static_assert(kAWarps * kCombinePitch >= kAttendBlocks * kKeysPerBlock / 8, "pages of 8 tokens or more");
+    const int slot0 = kPaged ? blk0 * kKeysPerBlock / a.pages.page_size : 0;
+    if (kPaged && !exact) {
+        const int last = min(n, (blk0 + kAttendBlocks) * kKeysPerBlock) - 1;
+        for (int i = tid; slot0 + i <= last / a.pages.page_size; i += kAThreads) pslot[i] = slots[slot0 + i];
+    }
+    // (paged: T's rows are inputs of the call, too, and folded before the wait)
+    const bool early = kPaged && exact;
+    float4 st = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (!early) {
+        wait_for_predecessor();                  // selection words, query norms
+        st = a.qstat[row];
+    }
+    const float qmu = KV == kKv4 ? 0.0f : st.y;
+    float qn = st.x;
     const float rad = a.radius ? a.radius[bg] : 0.0f;   // MIPS: cos = q.(k - mu) / (|q| r)
 
     // ---- the rows of this CTA: T by arithmetic, or the selected keys of its blocks, found
     //      through the selection words and their prefix counts (no list is materialised)
     const int t_a = min(a.n_sink, n), t_b = max(n - a.n_local, t_a);
-    const int blk0 = sb * kAttendBlocks;
     int nsel;
     if (exact) {
         nsel = t_a + (n - t_b);
@@ -679,6 +692,17 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
         } else {
             wpre[tid] = before + incl - c;
         }
+        if constexpr (kPaged) {
+            // the first kRowKeys keys' rows of the pool, -1 where a slot holds no page
+            const int key0 = blk0 * kKeysPerBlock + tid * 32;
+            for (int i = before + incl - c; U && i < kRowKeys; U &= U - 1u, ++i) {
+                const int key = key0 + __ffs(U) - 1, slot = key / a.pages.page_size;
+                const int pg = pslot[slot - slot0];
+                rowkey[i] = pg >= 0 && pg < a.pages.n_pages
+                                ? (pg * a.Hkv + h / a.G) * a.pages.page_size + key - slot * a.pages.page_size
+                                : -1;
+            }
+        }
         if (tid == kAThreads - 1) wpre[kWords] = before + incl;
         __syncthreads();
         nsel = wpre[kWords];
@@ -717,8 +741,16 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
                                    : nullptr;
     // 4-bit rows: q over its codes' units, the lane's sum of q, value sums in units of 16^k, and the
     // sum of weighted middles (all dims of a lane lie in one group)
-    uint64_t q2[4], o2[4];
+    uint64_t q2[4], o2[4], mu2[4];
     float qsum = 0.0f, mid = 0.0f;
+    if constexpr (kPaged) {                      // packed arithmetic, on plain values
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            q2[i] = pair_of(q8[2 * i], q8[2 * i + 1]);
+            mu2[i] = pair_of(-mu8[2 * i], -mu8[2 * i + 1]);
+            o2[i] = 0ull;
+        }
+    }
     if constexpr (KV == kKv4) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -761,6 +793,21 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
                 const float2 dd = of_pair(acc);
                 d = fmaf(sm.x, dd.x + dd.y, sm.y * qsum);
                 k2 = fmaf(sm.x * sm.x, c2, sm.y * fmaf(2.0f * sm.x, c1, 8.0f * sm.y));
+            } else if constexpr (kPaged) {
+                float kf[8];
+                load8(slot, 0, hl, form, kf);
+                uint64_t dots = 0ull, squares = 0ull;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint64_t kp = pair_of(kf[2 * i], kf[2 * i + 1]);
+                    uint64_t x;
+                    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(kp), "l"(mu2[i]));
+                    squares = fma_pair(x, x, squares);
+                    dots = fma_pair(q2[i], kp, dots);
+                }
+                const float2 dd = of_pair(dots), kk = of_pair(squares);
+                d = dd.x + dd.y;
+                k2 = kk.x + kk.y;
             } else {
                 float kf[8];
                 load8(slot, 0, hl, form, kf);
@@ -832,6 +879,9 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
             mid *= corr;
 #pragma unroll
             for (int i = 0; i < 4; ++i) o2[i] = fma_pair(o2[i], pair_of(corr, corr), 0ull);
+        } else if constexpr (kPaged) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o2[i] = fma_pair(o2[i], pair_of(corr, corr), 0ull);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] *= corr;
@@ -852,6 +902,13 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
                     mid = fmaf(wj, sm.y, mid);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o2[i] = fma_pair(c[i], ws2, o2[i]);
+                } else if constexpr (kPaged) {
+                    float vf[8];
+                    load8(slot, 1, hl, form, vf);
+                    const uint64_t w2 = pair_of(wj, wj);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        o2[i] = fma_pair(w2, pair_of(vf[2 * i], vf[2 * i + 1]), o2[i]);
                 } else {
                     float vf[8];
                     load8(slot, 1, hl, form, vf);
@@ -864,13 +921,14 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
     };
     static_assert(kAttendRows == 8 * kHalves, "the stage gives each half-warp 8 row slots");
     // the keys of the first kRowKeys entries, listed once; later ones are found on demand (a 4-bit
-    // cache's are all listed by now)
+    // cache's are all listed by now, a paged one's as rows of the pool, but for T's)
     if constexpr (KV != kKv4) {
-        // (paged: their rows of the pool, -1 where a slot holds no page)
-        for (int i = tid; i < min(nsel, kRowKeys); i += kAThreads)
-            rowkey[i] = kPaged ? static_cast<int>(paged_row(a.pages, slots, key_of(i), a.Hkv, h / a.G))
-                               : key_of(i);
-        __syncthreads();
+        if (!kPaged || exact) {
+            for (int i = tid; i < min(nsel, kRowKeys); i += kAThreads)
+                rowkey[i] = kPaged ? static_cast<int>(paged_row(a.pages, slots, key_of(i), a.Hkv, h / a.G))
+                                   : key_of(i);
+            __syncthreads();
+        }
     }
     // Group k of a warp: entries hw + 8 (4 k + j), j < 4, of its two half-warps, in the slots
     // hw + 8 (4 (k & 1) + j); group k + 2 reuses group k's slots once group k is folded.
@@ -941,6 +999,18 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
         issue(k + 2);
     }
     cp_async_wait_pending<0>();
+    if (early) {
+        wait_for_predecessor();                  // the query's norm, what the last call left in its place
+        qn = a.qstat[row].x;
+    }
+    if constexpr (kPaged) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = of_pair(o2[i]);
+            o[2 * i] = v.x;
+            o[2 * i + 1] = v.y;
+        }
+    }
     if constexpr (KV == kKv4) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
