@@ -212,8 +212,8 @@ __global__ void __launch_bounds__(kAppThreads, kAppCtas) paged_append_kernel(con
 // A float32 cache, on CUDA cores: a warp takes groups of four tokens of one page (pages hold multiples
 // of eight), a lane four dims of each. Groups come through a ring of three in the warp's own piece of
 // shared memory (cp.async: 12 KB in flight a warp), across the units of the run; a lane copies what it
-// reads itself. The NH scores of four tokens are summed over the lanes by a reduce-scatter, which leaves a
-// score to 8 / NH lanes, the softmax steps are lane-parallel, weights come back through
+// reads itself. The NH scores of four tokens are summed over the lanes by a reduce-scatter, which leaves
+// a score to 8 / NH lanes, the softmax steps are lane-parallel, weights come back through
 // shared memory.
 constexpr int kSimtWarps = 8;
 constexpr int kSimtThreads = 32 * kSimtWarps;
@@ -242,9 +242,50 @@ __device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bo
                  : "memory");
 }
 
+// A lane's four dims of a row or of a head's sums, in pairs, whose packed instructions halve the issue
+// slots of the sums (8 sequences x 8 heads x 8K tokens, four query heads each: 92 -> 88 us).
+struct Four {
+    unsigned long long v[2];
+    __device__ __forceinline__ void set(float4 x) {
+        asm("mov.b64 %0, {%1, %2};" : "=l"(v[0]) : "f"(x.x), "f"(x.y));
+        asm("mov.b64 %0, {%1, %2};" : "=l"(v[1]) : "f"(x.z), "f"(x.w));
+    }
+    __device__ __forceinline__ float4 get() const {
+        float4 x;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(x.x), "=f"(x.y) : "l"(v[0]));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(x.z), "=f"(x.w) : "l"(v[1]));
+        return x;
+    }
+    static __device__ __forceinline__ unsigned long long twice(float f) {
+        unsigned long long r;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(f));
+        return r;
+    }
+    __device__ __forceinline__ float dot(const Four& q) const {
+        unsigned long long r;
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(v[0]), "l"(q.v[0]));
+        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(r) : "l"(v[1]), "l"(q.v[1]));
+        float lo, hi;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(r));
+        return lo + hi;
+    }
+    __device__ __forceinline__ void scale(float f) {
+        const unsigned long long t = twice(f);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v[i]) : "l"(t));
+    }
+    __device__ __forceinline__ void add(float f, const Four& x) {
+        const unsigned long long t = twice(f);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(v[i]) : "l"(t), "l"(x.v[i]));
+    }
+};
+
 template <int NH>
 __global__ void __launch_bounds__(kSimtThreads, 2) paged_attention_simt_kernel(const PArgs a) {
     using S = SimtSmem<NH>;
+    constexpr int kLanes = 8 / NH;               // lanes that hold a score
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float* weights = reinterpret_cast<float*>(smem + S::kOffWeights) + warp * 5 * NH;
@@ -310,17 +351,15 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attention_simt_kernel(c
         const int here = w.here(), g = kv_head(a, w.unit), h0 = (w.unit - g * a.chunks) * NH;
         const int heads = min(NH, a.G - h0);
         const size_t row0 = static_cast<size_t>(w.b) * a.Hq + g * a.G + h0;
-        float q[NH][4];
+        Four q[NH], o[NH];
 #pragma unroll
-        for (int h = 0; h < NH; ++h)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                q[h][e] = h < heads ? load_elem(a.q, a.q_bf16, (row0 + h) * kD + 4 * lane + e) : 0.0f;
-        float m = -INFINITY, l = 0.0f, o[NH][4];
-#pragma unroll
-        for (int h = 0; h < NH; ++h)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[h][e] = 0.0f;
+        for (int h = 0; h < NH; ++h) {
+            float x[4];
+            load_query4(a, (row0 + min(h, heads - 1)) * kD + 4 * lane, x);
+            q[h].set(make_float4(x[0], x[1], x[2], x[3]));
+            o[h].set(make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+        }
+        float m = -INFINITY, l = 0.0f;
         for (int k = 0; k < here; ++k) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
             const float4* group = reinterpret_cast<const float4*>(ring + place * kGroupBytes);
@@ -329,11 +368,10 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attention_simt_kernel(c
                 float s[4 * NH];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float4 x = group[i * (kD / 4)];
+                    Four x;
+                    x.set(group[i * (kD / 4)]);
 #pragma unroll
-                    for (int h = 0; h < NH; ++h)
-                        s[i * NH + h] = fmaf(x.w, q[h][3], fmaf(x.z, q[h][2],
-                                                                fmaf(x.y, q[h][1], x.x * q[h][0])));
+                    for (int h = 0; h < NH; ++h) s[i * NH + h] = x.dot(q[h]);
                 }
 #pragma unroll
                 for (int lv = 0; ((2 * NH) >> lv) >= 1; ++lv) {
@@ -347,35 +385,51 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attention_simt_kernel(c
                 }
                 float logit = s[0];
 #pragma unroll
-                for (int off = 4 / NH; off >= 1; off >>= 1)
+                for (int off = kLanes / 2; off >= 1; off >>= 1)
                     logit += __shfl_xor_sync(0xffffffffu, logit, off);
-                logit = (lane >> 3) < now ? logit * a.scale : -INFINITY;
-                float mt = fmaxf(logit, __shfl_xor_sync(0xffffffffu, logit, 8));
-                mt = fmaxf(m, fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16)));
+                logit = lane / (kLanes * NH) < now ? logit * a.scale : -INFINITY;
+                float mt = logit;
+#pragma unroll
+                for (int off = 16; off >= kLanes * NH; off >>= 1)
+                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
+                mt = fmaxf(m, mt);
                 const float from = mt == -INFINITY ? 0.0f : mt;
                 const float corr = exp2_fast(m - from), p = exp2_fast(logit - from);
+                const bool moved = __any_sync(0xffffffffu, corr != 1.0f);
                 m = mt;
                 l = fmaf(l, corr, p);
-                const int at = lane * NH / 8;                            // token NH + head
-                weights[at] = p;
-                if (lane < 8) weights[4 * NH + at] = corr;
+                weights[lane / kLanes] = p;                              // token NH + head
+                if (lane < kLanes * NH) weights[4 * NH + lane / kLanes] = corr;
                 __syncwarp();
+                // NH numbers, four a load where there are (a load costs what it returns to the lanes)
+                auto factors = [&](const float* from, float (&f)[NH]) {
+                    if constexpr (NH >= 4) {
 #pragma unroll
-                for (int h = 0; h < NH; ++h) {
-                    const float c = weights[4 * NH + h];
+                        for (int h = 0; h < NH; h += 4) {
+                            const float4 x = *reinterpret_cast<const float4*>(from + h);
+                            f[h] = x.x;
+                            f[h + 1] = x.y;
+                            f[h + 2] = x.z;
+                            f[h + 3] = x.w;
+                        }
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[h][e] *= c;
+                        for (int h = 0; h < NH; ++h) f[h] = from[h];
+                    }
+                };
+                float f[NH];
+                if (moved) {
+                    factors(weights + 4 * NH, f);
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) o[h].scale(f[h]);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float4 x = group[(4 + i) * (kD / 4)];
-                    const float v[4] = {x.x, x.y, x.z, x.w};
+                    Four x;
+                    x.set(group[(4 + i) * (kD / 4)]);
+                    factors(weights + i * NH, f);
 #pragma unroll
-                    for (int h = 0; h < NH; ++h) {
-                        const float c = weights[i * NH + h];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[h][e] = fmaf(c, v[e], o[h][e]);
-                    }
+                    for (int h = 0; h < NH; ++h) o[h].add(f[h], x);
                 }
                 __syncwarp();
             }
@@ -385,13 +439,13 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attention_simt_kernel(c
             }
         }
         // ---- the warps' states, each in the place of the group it took last, joined in order
-        l += __shfl_xor_sync(0xffffffffu, l, 8);
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
+#pragma unroll
+        for (int off = 16; off >= kLanes * NH; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
         float4* state = reinterpret_cast<float4*>(smem + (warp * kRing + place) * kGroupBytes);
 #pragma unroll
         for (int h = 0; h < NH; ++h)
-            state[h * (kD / 4) + lane] = make_float4(o[h][0], o[h][1], o[h][2], o[h][3]);
-        if (lane < 8) ml[warp * NH + lane * NH / 8] = make_float2(m, l);
+            state[h * (kD / 4) + lane] = o[h].get();
+        if (lane < kLanes * NH) ml[warp * NH + lane / kLanes] = make_float2(m, l);
         __syncthreads();
         const int e = tid & (kD - 1);
         for (int h = tid / kD; h < heads; h += kSimtThreads / kD) {

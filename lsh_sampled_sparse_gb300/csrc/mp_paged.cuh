@@ -174,6 +174,26 @@ __device__ inline Walk plan_run(const PArgs& a, PlanSmem& s) {
     return s.walk;
 }
 
+// Four query elements from element i on (a multiple of four), as floats
+__device__ __forceinline__ void load_query4(const PArgs& a, size_t i, float (&x)[4]) {
+    if (!a.q_wide) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = load_elem(a.q, a.q_bf16, i + e);
+    } else if (a.q_bf16) {
+        const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + i);
+        x[0] = __uint_as_float(v.x << 16);
+        x[1] = __uint_as_float(v.x & 0xffff0000u);
+        x[2] = __uint_as_float(v.y << 16);
+        x[3] = __uint_as_float(v.y & 0xffff0000u);
+    } else {
+        const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + i);
+        x[0] = v.x;
+        x[1] = v.y;
+        x[2] = v.z;
+        x[3] = v.w;
+    }
+}
+
 // Sequences of length 0 have no tiles: their rows, shared out to the CTAs, are zeroed by `threads` threads
 __device__ inline void zero_empty(const PArgs& a, int thread, int threads) {
     if (a.cluster || !a.pages.lengths) return;

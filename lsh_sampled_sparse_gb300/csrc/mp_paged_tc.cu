@@ -498,27 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* dst = smem + L::kOffQ + (seg & 1) * L::kQ + (lane >> 4) * (L::kNq * 128);
             float x[NH][4];
 #pragma unroll
-            for (int h = 0; h < NH; ++h) {       // q is bf16 where QT is 1
-                const size_t from = (row0 + min(h, heads - 1)) * kD + 4 * lane;
-                if (!a.q_wide) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[h][e] = load_elem(a.q, a.q_bf16, from + e);
-                } else if constexpr (QT == 1) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(
-                        static_cast<const __nv_bfloat16*>(a.q) + from);
-                    x[h][0] = __uint_as_float(v.x << 16);
-                    x[h][1] = __uint_as_float(v.x & 0xffff0000u);
-                    x[h][2] = __uint_as_float(v.y << 16);
-                    x[h][3] = __uint_as_float(v.y & 0xffff0000u);
-                } else {
-                    const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) +
-                                                                      from);
-                    x[h][0] = v.x;
-                    x[h][1] = v.y;
-                    x[h][2] = v.z;
-                    x[h][3] = v.w;
-                }
-            }
+            for (int h = 0; h < NH; ++h)
+                load_query4(a, (row0 + min(h, heads - 1)) * kD + 4 * lane, x[h]);
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
                 uint32_t t0[kTerms], t1[kTerms];
