@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import NamedTuple
 
 import torch
@@ -44,20 +45,9 @@ class _KV4(ctypes.Structure):
                 ("params", ctypes.c_void_p), ("n_capacity", ctypes.c_int)]
 
 
-class _Paged(ctypes.Structure):
-    """mp_paged: the pool of a paged cache, a batch's page table, and their sizes."""
-
-    _fields_ = [("keys", ctypes.c_void_p), ("values", ctypes.c_void_p),
-                ("page_table", ctypes.c_void_p), ("dtype", ctypes.c_int),
-                ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("n_slots", ctypes.c_int),
-                ("table_stride", ctypes.c_int)]
-
-
-class _Rows(ctypes.Structure):
-    """mp_rows: rows [B][H][m][d] with strides of their own, in elements."""
-
-    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_longlong),
-                ("stride_h", ctypes.c_longlong), ("stride_m", ctypes.c_longlong)]
+# mp_paged (keys, values, page_table, dtype, n_pages, page_size, n_slots, table_stride) and mp_rows (data
+# and the strides of B, H, m) as bytes: half the time of a ctypes.Structure
+_PAGED, _ROWS = struct.Struct("PPPiiiii4x").pack, struct.Struct("Pqqq").pack
 
 
 def _params(K, L, n_sink, n_local, scale=0.0, n_capacity=0, n_indexed=0, radius=None,
@@ -98,7 +88,6 @@ def library_path() -> str:
 
 def _declare(L):
     P, Q = ctypes.POINTER(Params), ctypes.POINTER(_KV4)
-    G, R = ctypes.POINTER(_Paged), ctypes.POINTER(_Rows)
     sig = {
         "mp_status_string": (ctypes.c_char_p, [_c_int]),
         "mp_abi_version": (_c_int, []),
@@ -111,12 +100,11 @@ def _declare(L):
         "mp_encode_rows": (_c_int, [_vp, _c_int, _vp, _vp, _c_int] + [_c_int] * 8 + [_vp, _vp]),
         "mp_encode_rows_at": (_c_int, [_vp, _c_int, _vp, _vp, _c_int] + [_c_int] * 4 + [_vp]
                               + [_c_int] * 3 + [_vp, _vp]),
-        "mp_paged_append": (_c_int, [R, R, R, _c_int, _vp] + [_c_int] * 8 + [_vp, _vp, G, _vp, _vp,
-                                                                            _vp]),
+        "mp_paged_append": (_c_int, [_vp, _vp, _vp, _c_int, _vp] + [_c_int] * 8 + [_vp] * 6),
         "mp_paged_attention_workspace_bytes": (_c_size, [_c_int] * 5),
-        "mp_paged_attention": (_c_int, [_vp, _c_int, G] + [_c_int] * 5
+        "mp_paged_attention": (_c_int, [_vp, _c_int, _vp] + [_c_int] * 5
                                + [_vp, ctypes.c_float, _vp, _vp, _c_size, _vp]),
-        "mp_paged_decode_attention": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _c_int, G]
+        "mp_paged_decode_attention": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _c_int, _vp]
                                       + [_c_int] * 5 + [_vp, P, _vp, _vp, _c_size, _vp]),
         "mp_key_radius": (_c_int, [_vp, _c_int, _vp] + [_c_int] * 5 + [_vp, _vp]),
         "mp_cp_codes_bytes": (_c_size, [_c_int] * 4),
@@ -201,6 +189,9 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return _vp(stream.cuda_stream)
+
+
+_DTYPES = {torch.float32: MP_F32, torch.bfloat16: MP_BF16}
 
 
 def _dtype(t: torch.Tensor, name: str) -> int:
@@ -349,19 +340,18 @@ def encode_rows_at(keys, centre, W, K: int, L: int, positions, n_capacity: int, 
     device = keys.get_device()
     if device != torch._C._cuda_getDevice():
         raise ValueError(f"keys are on cuda:{device}, which is not the current device")
-    if n_capacity < 1 or n_capacity >> 31:
+    if not 1 <= n_capacity < 2 ** 31:
         raise ValueError(f"n_capacity = {n_capacity}")
-    for t, name in ((codes, "codes"), (centre, "centre"), (W, "W")):
-        _cuda(t, name)
-        if t.get_device() != device:
-            raise ValueError(f"{name} is on {t.device}, the keys on cuda:{device}")
-    if _nbytes(codes) < codes_bytes(B, Hkv, n_capacity, K, L):
+    for t, name in ((codes, "codes"), (W, "W")):
+        if t.get_device() != device or not t.is_contiguous():
+            _on_device(_cuda(t, name), device, name)
+    if _nbytes(codes) < B * Hkv * ((n_capacity + 1023) // 1024) * K * L * 128:   # mp_codes_bytes
         raise ValueError("codes buffer too small for the capacity")
-    if tuple(W.shape) != (d, K * L):
+    if W.shape != (d, K * L):
         raise ValueError(f"W {tuple(W.shape)} does not fit the keys")
     status = lib().mp_encode_rows_at(
         keys.data_ptr(), _dtype(keys, "keys"),
-        _arg(centre, device, "centre", torch.float32, (B, Hkv, d)), W.data_ptr(), _dtype(W, "W"), B,
+        _needed(centre, device, "centre", torch.float32, (B, Hkv, d)), W.data_ptr(), _dtype(W, "W"), B,
         Hkv, m, n_capacity, _needed(positions, device, "positions", torch.int32, (B,)), d, K, L,
         codes.data_ptr(), _raw_stream(stream, device))
     if status:
@@ -883,48 +873,51 @@ def _paged(cache, page_table):
     k, v = cache
     try:
         device, shape, kt = k.get_device(), k.shape, k.dtype
-    except AttributeError:
-        raise TypeError("the cache must hold CUDA tensors") from None
-    if device < 0:
-        raise TypeError("the cache must hold CUDA tensors")
-    if device != torch._C._cuda_getDevice():
-        raise ValueError(f"the cache is on cuda:{device}, which is not the current device")
-    if len(shape) != 4 or shape[3] != 128:
-        raise ValueError(f"keys must be [n_pages, Hkv, page_size, 128], got {tuple(shape)}")
-    n_pages, Hkv, page_size, _ = shape
-    try:
-        if page_table.get_device() != device or page_table.dtype is not torch.int32:
-            raise AttributeError
+        n_pages, Hkv, page_size, d = shape
         B, slots = page_table.shape
         stride, unit = page_table.stride()
-    except (AttributeError, ValueError):
-        _refuse_table(page_table, device)
-    if unit != 1 and slots > 1:
-        raise ValueError("the rows of page_table must be contiguous")
-    if B <= 1:
-        stride = slots
-    if stride < slots or stride >> 31:
-        raise ValueError(f"page_table's rows overlap or are too far apart (stride {stride})")
-    return _Paged(_arg(k, device, "keys", kt, shape), _arg(v, device, "values", kt, shape),
-                  page_table.data_ptr(), _dtype(k, "keys"), n_pages, page_size, slots,
-                  stride), device, B, Hkv, slots * page_size
+        if B <= 1:
+            stride = slots
+        if device == torch._C._cuda_getDevice() and kt in _DTYPES and d == 128 \
+                and v.shape == shape and v.dtype is kt and v.get_device() == device \
+                and k.is_contiguous() and v.is_contiguous() \
+                and page_table.dtype is torch.int32 and page_table.get_device() == device \
+                and (unit == 1 or slots <= 1) and slots <= stride < 2 ** 31:
+            return _PAGED(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), _DTYPES[kt], n_pages,
+                          page_size, slots, stride), device, B, Hkv, slots * page_size
+    except (AttributeError, TypeError, ValueError):
+        pass
+    _refuse_paged(k, v, page_table)
 
 
-def _refuse_table(t, device):
-    """Raise what _paged found in a page table."""
-    _on_device(t, device, "page_table")
-    if t.dtype is not torch.int32:
-        raise TypeError(f"page_table must be int32, is {t.dtype}")
-    raise ValueError(f"page_table must be [B, slots], got {tuple(t.shape)}")
+def _refuse_paged(k, v, table):
+    """Raise what _paged found."""
+    if not isinstance(k, torch.Tensor) or not k.is_cuda:
+        raise TypeError("the cache must hold CUDA tensors")
+    device, shape = k.get_device(), k.shape
+    if device != torch._C._cuda_getDevice():
+        raise ValueError(f"the cache is on cuda:{device}, which is not the current device")
+    _dtype(k, "keys")
+    if len(shape) != 4 or shape[3] != 128:
+        raise ValueError(f"keys must be [n_pages, Hkv, page_size, 128], got {tuple(shape)}")
+    _arg(k, device, "keys", k.dtype, shape)
+    _arg(v, device, "values", k.dtype, shape)
+    _on_device(table, device, "page_table")
+    if table.dtype is not torch.int32:
+        raise TypeError(f"page_table must be int32, is {table.dtype}")
+    if table.dim() != 2:
+        raise ValueError(f"page_table must be [B, slots], got {tuple(table.shape)}")
+    raise ValueError("the rows of page_table must be contiguous, apart and less than 2^31 elements "
+                     f"from each other: strides {table.stride()}")
 
 
 def _strided_rows(t, device, name, dtype, shape):
-    """A reference to the mp_rows of a tensor whose rows are contiguous; other strides are its own."""
+    """mp_rows of a tensor whose rows are contiguous; other strides are its own."""
     try:
         if t.dtype is dtype and t.shape == shape and t.get_device() == device:
             sb, sh, sm, unit = t.stride()
             if unit == 1:
-                return ctypes.byref(_Rows(t.data_ptr(), sb, sh, sm))
+                return _ROWS(t.data_ptr(), sb, sh, sm)
     except AttributeError:
         pass
     _on_device(t, device, name)
@@ -948,39 +941,44 @@ def paged_append(cache: PagedCache, page_table, keys, values, n_begin: int = 0, 
     they were. keys_out [B, Hkv, m, 128] in the cache's type takes the keys as the cache holds
     them."""
     c, device, B, Hkv, _ = _paged(cache, page_table)
-    _on_device(keys, device, "keys")
-    dtype, shape = keys.dtype, keys.shape
-    dt = _dtype(keys, "keys")
-    if len(shape) != 4 or shape[0] != B or shape[1] != Hkv:
-        raise ValueError(f"keys must be [{B}, {Hkv}, m, 128], got {tuple(shape)}")
-    m, d = shape[2], shape[3]
-    if n_begin >> 31 not in (0, -1):             # what a C int would cut off
+    try:
+        dtype, shape = keys.dtype, keys.shape
+        b, h, m, d = shape
+        if b != B or h != Hkv or dtype not in _DTYPES:
+            raise ValueError
+    except (AttributeError, ValueError):
+        _rows_arg(keys, device, "keys", B, Hkv)
+        raise ValueError(f"keys must be [{B}, {Hkv}, m, 128], got {tuple(keys.shape)}") from None
+    if not -2 ** 31 <= n_begin < 2 ** 31:        # what a C int would cut off
         raise ValueError(f"n_begin = {n_begin}")
     rotary, freq = 0, None
     if inv_freq is not None:
-        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+        if not isinstance(inv_freq, torch.Tensor):
             raise TypeError("inv_freq must be a CUDA tensor [rotary_dims / 2]")
         rotary = 2 * inv_freq.numel()
-        freq = _arg(inv_freq, device, "inv_freq", torch.float32, (rotary >> 1,))
+        freq = _arg(inv_freq, device, "inv_freq", torch.float32, (rotary // 2,))
     Hq, qr, qp = 0, None, None
     if q is not None:
         _on_device(q, device, "q")
         qs = q.shape
-        if len(qs) != 4 or qs[0] != B or qs[2] != m or qs[3] != d:
+        if len(qs) != 4:
             raise ValueError(f"q must be [{B}, Hq, {m}, {d}], got {tuple(qs)}")
-        Hq, qr = qs[1], _strided_rows(q, device, "q", dtype, qs)
+        Hq = qs[1]
+        qr = _strided_rows(q, device, "q", dtype, (B, Hq, m, d))
         if q_out is None:
             q_out = _empty(tuple(qs), dtype, q.device, stream)
         qp = _arg(q_out, device, "q_out", dtype, qs)
     elif q_out is not None:
         raise ValueError("q_out without q")
+    one = (B,)
     status = lib().mp_paged_append(
         _strided_rows(keys, device, "keys", dtype, shape),
-        _strided_rows(values, device, "values", dtype, shape), qr, dt, freq, rotary,
+        _strided_rows(values, device, "values", dtype, shape), qr, _DTYPES[dtype], freq, rotary,
         1 if interleaved else 0, B, Hq, Hkv, m, d, n_begin,
-        _arg(positions, device, "positions", torch.int32, (B,)),
-        _arg(counts, device, "counts", torch.int32, (B,)), ctypes.byref(c), qp,
-        _arg(keys_out, device, "keys_out", cache[0].dtype, shape), _raw_stream(stream, device))
+        None if positions is None else _arg(positions, device, "positions", torch.int32, one),
+        None if counts is None else _arg(counts, device, "counts", torch.int32, one), c, qp,
+        None if keys_out is None else _arg(keys_out, device, "keys_out", cache[0].dtype, shape),
+        torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream)
     if status:
         _check(status, "mp_paged_append")
     return q_out
@@ -995,16 +993,20 @@ def _paged_call(q, cache, page_table, n, lengths, out, workspace, need, stream):
     """What the calls on queries share: checks of q, lengths, out and the workspace, the last two
     allocated where they are None (need: the workspace's size from B, Hq, Hkv, n, d)."""
     c, device, B, Hkv, cap = _paged(cache, page_table)
-    _on_device(q, device, "q")
-    shape = q.shape
-    if len(shape) != 3 or shape[0] != B:
-        raise ValueError(f"q must be [{B}, Hq, 128], got {tuple(shape)}")
-    if not q.is_contiguous():
-        raise ValueError("q must be contiguous")
+    try:
+        shape, qt = q.shape, _DTYPES.get(q.dtype)
+        if q.get_device() != device or len(shape) != 3 or shape[0] != B or qt is None \
+                or not q.is_contiguous():
+            raise ValueError
+    except (AttributeError, TypeError, ValueError):
+        _on_device(q, device, "q")
+        _dtype(q, "q")
+        if len(shape) != 3 or shape[0] != B:
+            raise ValueError(f"q must be [{B}, Hq, 128], got {tuple(shape)}") from None
+        raise ValueError("q must be contiguous") from None
     n = cap if n is None else int(n)
     if not 1 <= n <= cap:
         raise ValueError(f"n = {n} outside [1, {cap}] (the page table's tokens)")
-    qt = _dtype(q, "q")
     if out is None:
         out = _empty(shape, torch.float32, q.device, stream)
     op = _arg(out, device, "out", torch.float32, shape)
@@ -1014,7 +1016,8 @@ def _paged_call(q, cache, page_table, n, lengths, out, workspace, need, stream):
     elif workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous and on the cache's device")
     return (c, device, dims, q.data_ptr(), qt,
-            _arg(lengths, device, "lengths", torch.int32, (B,)), out, op, workspace)
+            None if lengths is None else _arg(lengths, device, "lengths", torch.int32, (B,)), out, op,
+            workspace)
 
 
 def paged_attention(q, cache: PagedCache, page_table, n=None, lengths=None, scale: float = 0.0,
@@ -1025,7 +1028,7 @@ def paged_attention(q, cache: PagedCache, page_table, n=None, lengths=None, scal
     c, device, dims, qp, qt, lp, out, op, ws = _paged_call(
         q, cache, page_table, n, lengths, out, workspace,
         lib().mp_paged_attention_workspace_bytes, stream)
-    status = lib().mp_paged_attention(qp, qt, ctypes.byref(c), *dims, lp, scale, op, ws.data_ptr(),
+    status = lib().mp_paged_attention(qp, qt, c, *dims, lp, scale, op, ws.data_ptr(),
                                       _nbytes(ws), _raw_stream(stream, device))
     if status:
         _check(status, "mp_paged_attention")
@@ -1040,8 +1043,8 @@ def paged_decode_attention(q, codes, centre, W, cache: PagedCache, page_table, K
     first lengths[b] (int32 [B], on the GPU) of each sequence; the codes are laid out for n_capacity
     tokens per sequence (default: the page table's)."""
     cap = page_table.shape[1] * cache[0].shape[2] if n_capacity is None else int(n_capacity)
-    if cap >> 31:
-        raise ValueError(f"n_capacity = {cap}")
+    if not 0 <= cap < 2 ** 31:
+        raise ValueError(f"n_capacity = {n_capacity}")
     p = _params(K, L, n_sink, n_local, scale, cap, radius=radius, logu_table=logu_table)
 
     def need(B, Hq, Hkv, n, d):
@@ -1053,24 +1056,21 @@ def paged_decode_attention(q, codes, centre, W, cache: PagedCache, page_table, K
     c, device, dims, qp, qt, lp, out, op, ws = _paged_call(q, cache, page_table, n, lengths, out,
                                                            workspace, need, stream)
     B, _, Hkv, _, d = dims
-    size = cp_codes_bytes(B, Hkv, cap, L) if logu_table is not None \
-        else codes_bytes(B, Hkv, cap, K, L)
-    if codes is not None:
-        _cuda(codes, "codes")
+    blocks, cp = B * Hkv * ((cap + 1023) // 1024), logu_table is not None
+    size = blocks * L * 1024 if cp else blocks * K * L * 128             # mp_cp_codes_bytes, mp_codes_bytes
     if size and (codes is None or _nbytes(codes) < size):
         raise ValueError(f"codes must hold {size} bytes, for {cap} tokens per head")
     for t, name, most in ((codes, "codes", 0), (radius, "radius", B * Hkv),
                           (logu_table, "logu_table", MP_LOGU_TABLE_ENTRIES),
-                          (W, "W", d * (d if logu_table is not None else K) * L)):
-        if t is not None:
+                          (W, "W", d * (d if cp else K) * L)):
+        if t is not None and (t.get_device() != device or not t.is_contiguous()
+                              or t.numel() < most):
             _on_device(_cuda(t, name), device, name)
-            if t.numel() < most:
-                raise ValueError(f"{name} has {t.numel()} elements, needs {most}")
+            raise ValueError(f"{name} has {t.numel()} elements, needs {most}")
     status = lib().mp_paged_decode_attention(
         qp, qt, None if codes is None else codes.data_ptr(),
-        _needed(centre, device, "centre", torch.float32, (B, Hkv, d)), W.data_ptr(), _dtype(W, "W"),
-        ctypes.byref(c), *dims, lp, ctypes.byref(p), op, ws.data_ptr(), _nbytes(ws),
-        _raw_stream(stream, device))
+        _needed(centre, device, "centre", torch.float32, (B, Hkv, d)), W.data_ptr(), _dtype(W, "W"), c,
+        *dims, lp, ctypes.byref(p), op, ws.data_ptr(), _nbytes(ws), _raw_stream(stream, device))
     if status:
         _check(status, "mp_paged_decode_attention")
     return out

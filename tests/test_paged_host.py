@@ -22,14 +22,14 @@ def L():
 
 
 def _cache(keys=0x10000, table=0x10000, dtype=1, n_pages=10, page=16, slots=7, stride=None):
-    from lsh_sampled_sparse_gb300.binding import _Paged
-    return ctypes.byref(_Paged(keys, 0x10000, table, dtype, n_pages, page, slots,
-                               slots if stride is None else stride))
+    from lsh_sampled_sparse_gb300.binding import _PAGED
+    return _PAGED(keys or 0, 0x10000, table or 0, dtype, n_pages, page, slots,
+                  slots if stride is None else stride)
 
 
 def _rows(data=0x10000, sb=1 << 20, sh=1 << 10, sm=128):
-    from lsh_sampled_sparse_gb300.binding import _Rows
-    return ctypes.byref(_Rows(data, sb, sh, sm))
+    from lsh_sampled_sparse_gb300.binding import _ROWS
+    return _ROWS(data or 0, sb, sh, sm)
 
 
 BAD_CACHES = [(dict(keys=None), INVALID), (dict(keys=0x10008), INVALID), (dict(table=None), INVALID),
