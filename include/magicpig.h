@@ -498,8 +498,9 @@ typedef struct {
  * off by less than 2^-61 |p| (1 + |inv_freq[j]|) + 2^-22 radians at any position. inv_freq NULL
  * (rotary_dims then ignored) turns nothing. An inv_freq that is infinite or NaN has unspecified
  * results.
- * Errors: MP_ERR_INVALID_ARG (shapes, m < 0, Hq + 2 Hkv > 2^19, B m (Hq + 2 Hkv) > 2^31 - 1, n_begin < 0 or n_begin + m >
- * n_slots page_size without positions, null, misalignment: rows, outputs 16 bytes, others 4),
+ * Errors: MP_ERR_INVALID_ARG (shapes, m < 0, Hq + 2 Hkv > 2^18, B m (Hq + 2 Hkv) > 2^31 - 1, n_begin
+ * < 0 or n_begin + m > n_slots page_size without positions, null, misalignment: rows, outputs 16
+ * bytes, others 4),
  * MP_ERR_UNSUPPORTED (d != 128, page_size not a multiple of 8, rotary_dims not a multiple of 16 in
  * [16, 128]). m == 0 does nothing. */
 MP_API mp_status mp_paged_append(const mp_rows* keys, const mp_rows* values, const mp_rows* q,
@@ -631,10 +632,11 @@ MP_API mp_status mp_device_status(int* status);
 
 /* The MP_CHECKS build (the library compiled with -DMP_CHECKS=1, libmagicpig_checks.so): every
  * kernel of the decode path, the bucketed lookup, the tensor-core encoder, the CUDA-core encoders
- * of mp_encode_keys and mp_encode_rows, the 4-bit cache and the paged cache check the indices of their global
- * accesses (code blocks, selection words, K/V rows, partial states, bucket ranges and members, code
- * words written) and skip an access that is out of range instead of making it, raising
- * MP_ERR_BOUNDS in the status word. A stand-in for a memory checker: the paper has no counterpart.
+ * of mp_encode_keys, mp_encode_rows and mp_encode_rows_at, the 4-bit cache and the paged cache check
+ * the indices of their global accesses (code blocks, selection words, K/V rows, partial states, bucket
+ * ranges and members, code words written) and skip an access that is out of range instead of making
+ * it, raising MP_ERR_BOUNDS in the status word. A stand-in for a memory checker: the paper has no
+ * counterpart.
  * Synchronises the device and returns through *enabled 1 in that build, 0 in the product build, and
  * through *site the site of the first failed check since the status word was last reset (0 if
  * none): 1 query encoding stores, 2 scanned code block, 3 selection words written, 4 K/V row

@@ -787,7 +787,7 @@ mp_status mp_paged_append(const mp_rows* keys, const mp_rows* values, const mp_r
         return MP_ERR_INVALID_ARG;
     if (q && (!valid_rows(q, rows_dtype, B, Hq, m) || !q_out)) return MP_ERR_INVALID_ARG;
     const long long heads = (q ? Hq : 0) + 2ll * Hkv;
-    if (heads > 1 << 19 || static_cast<long long>(B) * m > 0x7fffffffll / heads)   // a grid's rows
+    if (heads > 1 << 18 || static_cast<long long>(B) * m > 0x7fffffffll / heads)   // a grid's rows
         return MP_ERR_INVALID_ARG;
     if (!ensure_prepared()) return MP_ERR_CUDA;
     return to_status(launch_paged_append(*keys, *values, q, rows_dtype == MP_BF16, inv_freq,

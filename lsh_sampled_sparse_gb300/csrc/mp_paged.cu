@@ -1,20 +1,18 @@
 // A paged K/V cache at full precision: tokens appended with their rotary positions applied on the
-// way, and exact attention of single query tokens over the pages. The pages of the reference keep
-// K and V in one piece and have no counterpart; the layout is the one magicpig.h describes.
+// way, and exact attention of single query tokens over the pages (of float32; those of bf16:
+// mp_paged_tc.cu). The paper keeps K and V of one sequence in one piece: pages have no counterpart
+// there. The layout is the one magicpig.h describes.
 //
 // The kernels are launched as dependents of what precedes them in the stream: their lives begin
 // before it has written what they read. So no load here is a non-coherent one, which would promise
 // that nobody writes its memory meanwhile; ordinary loads stay behind the wait.
 #include <algorithm>
-#include <type_traits>
 
 #include "mp_paged.cuh"
 
 namespace mp {
 namespace {
 
-constexpr int kSms = 152;                        // of a GB300; a workspace's size is the same on the
-                                                 // host alone
 using Bf16 = __nv_bfloat16;
 
 // ------------------------------------------------------------------------------------------------
@@ -40,7 +38,7 @@ struct AppendArgs {
 constexpr int kAppThreads = 256;
 constexpr int kRowLanes = 8;                     // lanes a row, 2 x 8 dims each
 constexpr int kAppRows = kAppThreads / kRowLanes;
-constexpr int kAppCtas = 6;                      // an SM
+constexpr int kAppCtas = 6;                      // an SM: 40 registers a thread (4, 5 and 8 take as long)
 constexpr int kMaxToks = 4;                      // tokens a block has
 static_assert(kMaxToks * (kD / 2) == kAppThreads, "a thread an angle");
 
@@ -145,8 +143,8 @@ __device__ __forceinline__ uint64_t turn_of(float f) {
 
 // A CTA takes 32 rows of up to 2^tok_shift tokens of one sequence (blockIdx.y: of which heads; the query
 // heads come first, then the key heads, then the value heads), a row to eight lanes, all on their way
-// before anything is known of the tokens. No CTA takes more than that: of what a loop over rows had in
-// flight ahead, less than the rows of the CTAs that fit an SM (8192 tokens of 32 + 8 + 8 heads: 45 us).
+// before anything is known of the tokens. No CTA takes more than that: a loop over rows had less in flight
+// than the rows of the CTAs that fit an SM (8192 tokens of 32 + 8 + 8 heads: 45 us, so 41).
 template <typename T, typename C>
 __global__ void __launch_bounds__(kAppThreads, kAppCtas) paged_append_kernel(const AppendArgs a) {
     __shared__ __align__(16) float2 turn[kMaxToks][kD / 2];
@@ -569,7 +567,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const PArgs
         a.out[row * kD + e] = over_sum(Os, Ls);
 }
 
-constexpr int kSimtCtas = 2 * kSms;
+constexpr int kSimtCtas = 2 * kPagedTcCtas;      // two an SM
+// Tokens a CTA of a cluster may have more than its even share of all: they take as long as the second
+// kernel, which the even shares' states need. One sequence x 8 heads, bf16, in a cluster or evenly: 2K
+// tokens (a cluster's CTA has 128 more) 11.0 and 12.6 us, 8K (512) 18.5 and 19.4, 16K (1152) 27.0 and 24.3,
+// 32K (2432) 43.7 and 34.0; float32, 16K 56.7 and 34.5.
 constexpr int kJoinTokens = 512;
 int simt_heads(int G) { return G <= 2 ? G : (G <= 4 ? 4 : 8); }
 
@@ -583,10 +585,20 @@ PFn pick_simt(int nh, int* smem) {
     return nh == 1 ? simt<1>(smem) : (nh == 2 ? simt<2>(smem) : (nh == 4 ? simt<4>(smem) : simt<8>(smem)));
 }
 
-// The CTAs of the cluster that shares a unit of `tiles` tiles, 0 where all CTAs share all tiles.
-int cluster_size(long long units, int tiles, int ctas, int tile_shift) {
-    if (units > ctas) return 0;
-    const int most = std::min({kPagedMaxCluster, tiles, static_cast<int>(ctas / units)});
+// How many clusters of so many CTAs the GPU holds at once, by whether the kernel is the tensor cores'
+// (asked when the library is prepared on a device). A cluster's CTAs lie in one partition of the GPU, so
+// that of clusters of eight CTAs of an SM each 15 fit, not 19.
+constexpr int kMaxDevices = 64;
+int g_clusters[kMaxDevices][2][kPagedMaxCluster + 1];
+
+// The CTAs of the cluster that shares a unit of `tiles` tiles, 0 where all CTAs share all tiles: as many as
+// leave all clusters running at once (two sequences x 8 heads x 8K tokens, bf16: 23.3 us, in clusters of
+// eight, one of which would wait for the others to end, 33.5), unless a CTA then has kJoinTokens more
+// than its even share.
+int cluster_size(long long units, int tiles, int ctas, int tile_shift, const int* held) {
+    int most = std::min(kPagedMaxCluster, tiles);
+    while (most > 0 && held[most] < units) --most;
+    if (most == 0) return 0;
     const int each = (tiles + most - 1) / most;
     const long long even = (units * tiles + ctas - 1) / ctas;
     return each - even <= kJoinTokens >> tile_shift ? (tiles + each - 1) / each : 0;
@@ -672,7 +684,9 @@ cudaError_t launch_paged_attention(const void* q, bool q_bf16, const mp_paged& c
         if (cache.page_size == 1 << i) a.page_shift = i;
     const int tiles = ((n - 1) >> a.tile_shift) + 1;
     const long long units = static_cast<long long>(B) * Hkv * a.chunks;
-    a.cluster = cluster_size(units, tiles, a.ctas, a.tile_shift);
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    a.cluster = cluster_size(units, tiles, a.ctas, a.tile_shift, g_clusters[dev][tc ? 1 : 0]);
     a.scale = scale * 1.4426950408889634f;
     a.status = device_status_ptr();
     a.part = static_cast<float*>(workspace);
@@ -707,6 +721,15 @@ cudaError_t prepare_paged() {
         if (e != cudaSuccess) return e;
     }
     if ((e = prepare_paged_tc()) != cudaSuccess) return e;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    for (int c = 1; c <= kPagedMaxCluster; ++c) {
+        int smem;
+        const PFn fn = pick_simt(4, &smem);      // all of them fit an SM twice, the tensor cores' once
+        if ((e = max_clusters(fn, kSimtThreads, smem, c, &g_clusters[dev][0][c])) != cudaSuccess ||
+            (e = paged_tc_clusters(c, &g_clusters[dev][1][c])) != cudaSuccess)
+            return e;
+    }
     return cudaFuncGetAttributes(&fa, paged_join_kernel);
 }
 

@@ -253,9 +253,26 @@ __device__ inline void join_cluster(const PArgs& a, const float* share, int b, i
 // Over a bf16 cache, on the tensor cores (mp_paged_tc.cu): query heads a unit takes for a group of G,
 // its CTAs, the tokens of its tiles, and the launch.
 int paged_tc_heads(int G);
-constexpr int kPagedTcCtas = 152, kPagedTcShift = 7;
+constexpr int kPagedTcCtas = 152;                // one an SM of a GB300: a constant, as a workspace's size
+                                                 // is asked for on hosts without one
+constexpr int kPagedTcShift = 7;
 cudaError_t launch_paged_attention_tc(const PArgs& a, const mp_paged& cache, unsigned grid,
                                       cudaStream_t st);
 cudaError_t prepare_paged_tc();
+cudaError_t paged_tc_clusters(int size, int* n);     // clusters of that size that the GPU holds at once
+template <typename Fn>
+cudaError_t max_clusters(Fn fn, int threads, size_t smem, int size, int* n) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = size;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(n, fn, &cfg);
+}
 
 }  // namespace mp

@@ -586,6 +586,12 @@ cudaError_t launch_paged_attention_tc(const PArgs& a, const mp_paged& cache, uns
     return cudaLaunchKernelEx(&cfg, fn, kmap, vmap, a);
 }
 
+cudaError_t paged_tc_clusters(int size, int* n) {
+    uint32_t smem;
+    const TcFn fn = pick_tc(4, true, &smem);
+    return max_clusters(fn, kThreads, smem, size, n);
+}
+
 cudaError_t prepare_paged_tc() {
     for (int i = 0; i < 6; ++i) {
         uint32_t smem;

@@ -426,6 +426,66 @@ def test_calls_back_to_back_equal_calls_waited_for(mp, dtype):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_table_that_repeats_pages_over_a_long_context(mp, dtype):
+    """Four million tokens in 37 pages, and a table that is a view of a wider one."""
+    g = _gen(41)
+    page, pages, slots = 8, 37, 1 << 19
+    n = slots * page - 3
+    cache = mp.paged_cache(pages, 1, page, dtype)
+    for t in cache:
+        t.copy_(_randn(g, *t.shape))
+    wide = torch.full((2, slots + 5), -1, dtype=torch.int32, device="cuda")
+    table = wide[:, :slots]
+    table.copy_(torch.randint(0, pages, (2, slots), generator=g, device="cuda"))
+    q = _randn(g, 2, 2, 128).to(dtype)
+    lens = [n, n // 3]
+    out = mp.paged_attention(q, cache, table, n=n, lengths=_ints(lens))
+    k, v = (t.double().view(-1, 128) for t in cache)
+    for b in range(2):
+        tok = torch.arange(lens[b], device="cuda")
+        times = torch.bincount(table[b, tok // page].long() * page + tok % page, minlength=pages * page)
+        logits = q[b].double() @ k.T * 128 ** -0.5
+        want = torch.softmax(logits + times.double().log(), -1) @ v
+        A = (q[b].double().abs() @ k.abs().T * 128 ** -0.5).max()
+        # paged_reference.attention's
+        tol = R.E * (2 * (32 * A + 4) + 4 * lens[b] ** 0.5 + 16) * v.abs().max()
+        assert ((out[b].double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_calls_on_two_streams_at_once(mp, dtype):
+    """Each with its workspace, on one pool: one stream's sequences grow while the other's are read."""
+    B, Hkv, n, page = 4, 4, 3000, 16
+    g = _gen(51)
+    cache, table = _random_cache(mp, g, 2 * B, Hkv, n, page, dtype, [n] * 2 * B)
+    q = _randn(g, 2 * B, 16, 128).to(dtype)
+    rows = [_randn(g, 2, B, Hkv, 1, 128).to(dtype) for _ in range(8)]
+    halves = (slice(0, B), slice(B, 2 * B))
+    want = [[], []]
+    start = [t.clone() for t in cache]
+    for i in range(8):
+        for j, part in enumerate(halves):
+            mp.paged_append(cache, table[part], rows[i][j], rows[i][j], n_begin=7 * i)
+            want[j].append(mp.paged_attention(q[part], cache, table[part], n=n - 100 * i))
+            torch.cuda.synchronize()
+    for t, was in zip(cache, start):
+        t.copy_(was)
+    streams = [torch.cuda.Stream() for _ in halves]
+    ws = [torch.empty(mp.paged_attention_workspace_bytes(B, 16, Hkv, n), dtype=torch.uint8, device="cuda")
+          for _ in halves]
+    outs = [[torch.empty(B, 16, 128, device="cuda") for _ in range(8)] for _ in halves]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for j, part in enumerate(halves):
+            mp.paged_append(cache, table[part], rows[i][j], rows[i][j], n_begin=7 * i, stream=streams[j])
+            mp.paged_attention(q[part], cache, table[part], n=n - 100 * i, out=outs[j][i], workspace=ws[j],
+                               stream=streams[j])
+    torch.cuda.synchronize()
+    for j in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(outs[j], want[j]))
+
+
 def test_what_was_handed_in_is_filled_and_no_more(mp):
     g = _gen(31)
     for dtype in (BF, F32):
@@ -640,6 +700,70 @@ def test_a_prompt_and_decode_steps_as_they_are_used(mp):
     held, _ = R.held(cache.keys, table.cpu(), 0, prompts[0] + steps)
     want, tol = R.turned(raw_k[0][None], _ints([0]), freq, False)
     assert ((held - want[0]).abs() <= R.rounded(tol, want, BF)[0]).all()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_step_with_its_codes_back_to_back(mp, captured):
+    """Append, codes and both attentions of several steps, queued or captured as one graph, against the
+    same calls each waited for: bit for bit."""
+    B, Hq, Hkv, K, L, page, slots, steps = 3, 8, 2, 8, 60, 16, 40, 5
+    g = _gen(78)
+    lens0 = [500, 1, 257]
+    table, n_pages = _table(g, B, slots)
+    cap = slots * page
+    W, freq = _randn(g, 128, K * L).to(BF), _inv_freq(128)
+    start = mp.paged_cache(n_pages, Hkv, page)
+    first = _randn(g, 2, B, Hkv, max(lens0), 128).to(BF)
+    for t in start:
+        t.zero_()
+    mp.paged_append(start, table, first[0], first[1], counts=_ints(lens0))
+    centre = _randn(g, B, Hkv, 128) * 0.1
+    codes0 = mp.encode_rows(first[0], centre, W, K, L, 0, cap)
+    x = [_randn(g, 2, B, Hkv, 1, 128).to(BF) for _ in range(steps)]
+    q = [_randn(g, B, Hq, 1, 128).to(BF) for _ in range(steps)]
+    ws = torch.empty(max(mp.paged_attention_workspace_bytes(B, Hq, Hkv, cap),
+                         mp.decode_workspace_bytes(B, Hq, Hkv, cap, 128, K, L, 4, 64)), dtype=torch.uint8,
+                     device="cuda")
+    rows, turned = torch.empty(B, Hkv, 1, 128, dtype=BF, device="cuda"), torch.empty_like(q[0])
+
+    def run(wait):
+        cache, codes, pos = mp.PagedCache(*(t.clone() for t in start)), codes0.clone(), _ints(lens0)
+        outs = [torch.empty(B, Hq, 128, device="cuda") for _ in range(2 * steps)]
+
+        def go():
+            for i in range(steps):
+                for call in (
+                        lambda: mp.paged_append(cache, table, x[i][0], x[i][1], positions=pos, inv_freq=freq,
+                                                q=q[i], q_out=turned, keys_out=rows),
+                        lambda: mp.encode_rows_at(rows, centre, W, K, L, pos, cap, codes),
+                        lambda: pos.add_(1),
+                        lambda: mp.paged_attention(turned[:, :, 0], cache, table, lengths=pos,
+                                                   out=outs[2 * i], workspace=ws),
+                        lambda: mp.paged_decode_attention(turned[:, :, 0], codes, centre, W, cache, table, K,
+                                                          L, 4, 64, lengths=pos, out=outs[2 * i + 1],
+                                                          workspace=ws)):
+                    call()
+                    if wait:
+                        torch.cuda.synchronize()
+
+        if captured and not wait:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                go()
+            for _ in range(3):                   # on what it started from
+                for t, was in zip((*cache, codes), (*start, codes0)):
+                    t.copy_(was)
+                pos.copy_(_ints(lens0))
+                graph.replay()
+        else:
+            go()
+        torch.cuda.synchronize()
+        return (*cache, codes, *outs)
+
+    want = run(True)
+    for _ in range(1 if captured else 4):
+        assert all(torch.equal(a, b) for a, b in zip(run(False), want))
+    assert mp.device_status() == 0
 
 
 # ---------------------------------------------------------------- refusals

@@ -64,6 +64,7 @@ def test_append_rejects_bad_arguments_before_launch(L):
     for r in (0, 8, 24, 144):
         assert app(rotary=r) == UNSUPPORTED
     assert app(B=2 ** 20, m=2 ** 10, pos=OK, Hkv=2) == INVALID             # rows past 2^31
+    assert app(q=_rows(), Hq=2 ** 18, B=1, m=1) == INVALID                 # more heads than a grid has
     assert app(m=0, k=_rows(data=None)) == 0                               # nothing to do
 
 
