@@ -593,7 +593,9 @@ __device__ __forceinline__ unsigned atomic_add_acq_rel_gpu(unsigned* p, unsigned
 // neither the centre nor q.mu.
 // kShared: the rows of a partial are shared by a cluster of 2^share CTAs.
 // kPaged: rows lie in pages, each sequence has a length of its own (the scan then leaves valid and T to
-// this kernel's mask), and log u is evaluated for each key, as for the 4-bit cache.
+// this kernel's mask), and log u is evaluated for each key, as for the 4-bit cache. What the pages add to the
+// chain of latencies is a load of the table's entry before a row's: the entries of a CTA's blocks are loaded
+// before the wait (32 query heads x 96K tokens at (10, 150), a call 43.8 to 46.7 us, contiguous 42.6 to 45.6).
 template <KvForm KV, bool kShared, bool kPaged>
 __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
