@@ -576,6 +576,10 @@ constexpr int kSimtCtas = 2 * kPagedTcCtas;      // two an SM
 // tokens (a cluster's CTA has 128 more) 11.0 and 12.6 us, 8K (512) 18.5 and 19.4, 16K (1152) 27.0 and 24.3,
 // 32K (2432) 43.7 and 34.0; float32, 16K 56.7 and 34.5.
 constexpr int kJoinTokens = 512;
+// Tokens of a cluster's CTA at most where sequences have lengths of their own: a long one among short ones
+// leaves its CTAs alone with them. 19 sequences x 8 heads, bf16, one of 32K tokens and the others of 100:
+// 272 us in clusters, 39 evenly; eight sequences, one of 4K: 25.3 and 15.8, all of 4K: 31.3 and 35.1.
+constexpr int kRaggedTokens = 1024;
 int simt_heads(int G) { return G <= 2 ? G : (G <= 4 ? 4 : 8); }
 
 typedef void (*PFn)(const PArgs);
@@ -598,12 +602,13 @@ int g_clusters[kMaxDevices][2][kPagedMaxCluster + 1];
 // leave all clusters running at once (two sequences x 8 heads x 8K tokens, bf16: 23.3 us, in clusters of
 // eight, one of which would wait for the others to end, 33.5), unless a CTA then has kJoinTokens more
 // than its even share.
-int cluster_size(long long units, int tiles, int ctas, int tile_shift, const int* held) {
+int cluster_size(long long units, int tiles, int ctas, int tile_shift, bool ragged, const int* held) {
     int most = std::min(kPagedMaxCluster, tiles);
     while (most > 0 && held[most] < units) --most;
     if (most == 0) return 0;
     const int each = (tiles + most - 1) / most;
     const long long even = (units * tiles + ctas - 1) / ctas;
+    if (ragged && each > kRaggedTokens >> tile_shift) return 0;
     return each - even <= kJoinTokens >> tile_shift ? (tiles + each - 1) / each : 0;
 }
 
@@ -689,7 +694,7 @@ cudaError_t launch_paged_attention(const void* q, bool q_bf16, const mp_paged& c
     const long long units = static_cast<long long>(B) * Hkv * a.chunks;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    a.cluster = cluster_size(units, tiles, a.ctas, a.tile_shift, g_clusters[dev][tc ? 1 : 0]);
+    a.cluster = cluster_size(units, tiles, a.ctas, a.tile_shift, lengths != nullptr, g_clusters[dev][tc ? 1 : 0]);
     a.scale = scale * 1.4426950408889634f;
     a.status = device_status_ptr();
     a.part = static_cast<float*>(workspace);
