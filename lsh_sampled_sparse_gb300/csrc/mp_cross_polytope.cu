@@ -192,6 +192,7 @@ struct CpCArgs {
     const uint8_t* codes;
     const uint8_t* qcodes;
     uint32_t* selmask;
+    const int32_t* lengths;                      // paged cache: of each sequence, or NULL
     int n, nblk, cblk, blk0, Hq, Hkv, L, qbytes, n_sink, n_local;
 };
 
@@ -214,6 +215,10 @@ __global__ void __launch_bounds__(kCpThreads) collide_cp_kernel(const CpCArgs a)
     const int b = bg / a.Hkv, g = bg % a.Hkv;
     const int row0 = b * a.Hq + g * G;
     allow_dependents();
+    if (a.lengths && a.lengths[b] <= blk * kKeysPerBlock) {      // behind the sequence's last key: as in the
+        if (blk == 0) wait_for_predecessor();    // scan of sign codes
+        return;
+    }
     const uint8_t* base = a.codes + (static_cast<size_t>(bg) * a.cblk + blk) * a.L * kKeysPerBlock +
                           lane * 32;
     const int t0 = (a.L * warp) / kCpWarps, t1 = (a.L * (warp + 1)) / kCpWarps;
@@ -445,6 +450,7 @@ cudaError_t launch_collide_cp(const void* q, bool q_bf16, const uint8_t* codes,
     a.L = s.L;
     a.qbytes = s.qwords * 4;
     // over a paged cache T goes by each sequence's own length: the attend kernel's mask
+    a.lengths = kv.pages ? kv.pages->lengths : nullptr;
     a.n_sink = kv.pages ? 0 : s.n_sink;
     a.n_local = kv.pages ? 0 : s.n_local;
     if (blk0 < s.nblk) {

@@ -479,10 +479,10 @@ __global__ void __launch_bounds__(kThreads, 3) collide_kernel(const CArgs a) {
         !mp_check(a.status, blk, a.nblk, kSiteScanCodes))
         return;                                  // the whole CTA: the condition is uniform
     const int b = bg / a.Hkv, g = bg % a.Hkv;
-    if (a.lengths && a.lengths[b] <= blk * kKeysPerBlock) {      // behind the sequence's last key
-        allow_dependents();
-        wait_for_predecessor();
-        return;                                  // its selection words are masked when they are read
+    if (a.lengths && a.lengths[b] <= blk * kKeysPerBlock) {      // behind the sequence's last key: no one
+        allow_dependents();                      // reads its selection words
+        if (blk == 0) wait_for_predecessor();    // (the kernel ends behind its predecessor all the same)
+        return;
     }
     const int row0 = b * a.Hq + g * G;          // first query row of this KV head's group
     uint32_t* qneg = reinterpret_cast<uint32_t*>(smem);                    // [cpad][G]
@@ -605,9 +605,14 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
     const int b = row / a.Hq, h = row % a.Hq;
     const int bg = b * a.Hkv + h / a.G;
     const bool exact = sb == a.nsb;              // this CTA takes T
-    const int nsp = a.nsb + 1;                   // partials per query row
     // inputs of the call, like q and the centre
     const int n = kPaged && a.pages.lengths ? max(0, min(a.n, a.pages.lengths[b])) : a.n;
+    // a sequence's own blocks have partials, and T; CTAs behind them end here (four sequences of 2000 tokens
+    // and n = 128K: 42 -> 27 us)
+    const int nsb = kPaged ? (n + kAttendBlocks * kKeysPerBlock - 1) / (kAttendBlocks * kKeysPerBlock) : a.nsb;
+    if (kPaged && !exact && sb >= nsb) return;
+    const int nsp = nsb + 1;                     // partials of the query row
+    const size_t rb = static_cast<size_t>(row) * (a.nsb + 1);              // the first of them
     const int32_t* slots = kPaged ? a.pages.table + static_cast<long long>(b) * a.pages.stride : nullptr;
 
     constexpr int kRowBytes = attend_row_bytes(KV);
@@ -1047,7 +1052,7 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
         }
     }
     __syncthreads();
-    const size_t prow = static_cast<size_t>(row) * nsp + sb;
+    const size_t prow = rb + (kPaged && exact ? nsb : sb);
     {
         float M = -INFINITY;
 #pragma unroll
@@ -1088,7 +1093,7 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
             if (rank != 0) return;
         }
         if (mp_check(a.status, static_cast<long long>(prow),
-                     static_cast<long long>(gridDim.y) * nsp, kSiteAttendPartial)) {
+                     static_cast<long long>(gridDim.y) * (a.nsb + 1), kSiteAttendPartial)) {
             a.po[prow * kD + tid] = Os;
             if (tid == 0) {
                 a.pm[prow] = M;
@@ -1109,7 +1114,6 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
     //      lane l dims 4l..4l+3; a pass loads kMergeRegs partials per warp into registers at once
     //      (one round trip covers 4 * kMergeRegs partials) and rescales a running maximum. The
     //      four warps' (m, l, o) are then joined through shared memory in warp order.
-    const size_t rb = static_cast<size_t>(row) * nsp;
     float mw = -INFINITY, lw = 0.0f;
     float4 ow = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int j0 = warp; j0 < nsp; j0 += kAWarps * kMergeRegs) {
