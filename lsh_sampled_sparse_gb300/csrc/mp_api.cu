@@ -842,8 +842,8 @@ mp_status mp_paged_decode_attention(const void* q, mp_dtype q_dtype, const uint3
     KvRef kv = kv_ref(cache->keys, cache->values, cache->dtype);
     kv.pages = &pages;
     const DecodeScratch ws = carve_decode_scratch(workspace, s, false);
-    const cudaError_t e = query_encode(q, q_dtype == MP_BF16, centre, W, w_dtype == MP_BF16, s, ws,
-                                       stream);
+    const auto encode = s.cp ? launch_qencode_cp : launch_qencode_rows;
+    const cudaError_t e = encode(q, q_dtype == MP_BF16, centre, W, w_dtype == MP_BF16, s, ws, stream);
     if (e != cudaSuccess) return MP_ERR_CUDA;
     return to_status(scan_and_attend(q, q_dtype == MP_BF16, codes, centre, kv, s, out, ws, stream));
 }

@@ -49,6 +49,7 @@ struct QArgs {
     float* logu_tab;                             // filled by the extra row of CTAs
     int* status;                                 // index checks of the MP_CHECKS build
     int q_bf16, w_bf16, BHq, Hq, G, C, cpad, qwords, n_counters, K, L, qrow_ctas;
+    int w_wide;                                  // rows of W aligned for four elements
 };
 
 __global__ void __launch_bounds__(kThreads) qencode_kernel(const QArgs a) {
@@ -144,6 +145,185 @@ __global__ void __launch_bounds__(kThreads) qencode_kernel(const QArgs a) {
         }
         if (blockIdx.y == 0)
             for (int i = tid; i < a.n_counters; i += kThreads) a.counters[i] = 0u;
+    }
+}
+
+// The same for the decode over pages, whose batches are larger and which needs no table of log u: a CTA takes
+// 128 hyperplanes by 4 R query rows, a lane four planes by R rows, whose sums are the ones above, bit for
+// bit. One plane by one row reads 8 bytes of shared memory a product, which bounds the kernel above from
+// about a hundred rows on; four by four 1.5 (W in bf16; 512 rows x 1500 planes, cold: 24.3 us above, 15.5
+// here with two rows a lane, 12.9 with four).
+constexpr int kQTThreads = 128, kQTPlanes = 128;
+__device__ __forceinline__ void four_planes(const __nv_bfloat16* p, float (&w)[4]) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = __uint_as_float(v.x << 16);
+    w[1] = __uint_as_float(v.x & 0xffff0000u);
+    w[2] = __uint_as_float(v.y << 16);
+    w[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+__device__ __forceinline__ void four_planes(const float* p, float (&w)[4]) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+}
+template <typename TW, int R>
+__global__ void __launch_bounds__(kQTThreads) qencode_rows_kernel(const QArgs a) {
+    constexpr int kRows = 4 * R;
+    __shared__ __align__(16) float Qs[kRows][kD];
+    extern __shared__ __align__(16) uint8_t q_smem[];
+    TW* Ws = reinterpret_cast<TW*>(q_smem);      // [kD][kQTPlanes]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int j0 = blockIdx.x * kQTPlanes, r0 = blockIdx.y * kRows;
+    const int nq = min(kRows, a.BHq - r0), Hkv = a.Hq / a.G;
+    const int mine = r0 + R * warp;              // this warp's rows
+    wait_for_predecessor();
+    allow_dependents();
+    float mu[R][kD / 32];                        // the CTAs of the first planes have the norms, too
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+        const int row = min(mine + u, a.BHq - 1), b = row / a.Hq, g = (row - b * a.Hq) / a.G;
+#pragma unroll
+        for (int k = 0; k < kD / 32; ++k)
+            mu[u][k] = blockIdx.x == 0 ? a.centre[(static_cast<size_t>(b) * Hkv + g) * kD + lane + 32 * k] : 0.0f;
+    }
+    {
+        // all loads first, then the stores
+        float qv[kRows];                         // row k, dim tid
+#pragma unroll
+        for (int k = 0; k < kRows; ++k)
+            qv[k] = k < nq ? load_elem(a.q, a.q_bf16, static_cast<size_t>(r0 + k) * kD + tid) : 0.0f;
+        const TW* W = static_cast<const TW*>(a.W);
+        using Four = typename std::conditional<sizeof(TW) == 2, uint2, uint4>::type;
+        if (a.w_wide) {                          // rows of W aligned for four planes
+            constexpr int kAhead = 32;           // of all 32, four planes a load
+            const int j = j0 + 4 * lane;
+            Four w[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                w[i] = j < a.C ? *reinterpret_cast<const Four*>(W + static_cast<size_t>(warp + 4 * i) * a.C + j)
+                               : Four{};
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                *reinterpret_cast<Four*>(Ws + (warp + 4 * i) * kQTPlanes + 4 * lane) = w[i];
+        } else {
+            constexpr int kAhead = 32;
+            const int j = j0 + tid;
+#pragma unroll 1
+            for (int e0 = 0; e0 < kD; e0 += kAhead) {
+                TW w[kAhead];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+                    w[i] = j < a.C ? W[static_cast<size_t>(e0 + i) * a.C + j] : TW(0.0f);
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) Ws[(e0 + i) * kQTPlanes + tid] = w[i];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) Qs[k][tid] = qv[k];
+    }
+    __syncthreads();
+    if (a.C > 0 && R * warp < nq) {
+        float acc[R][4][4] = {};                 // row, plane, dim mod 4
+#pragma unroll 2
+        for (int e = 0; e < kD; e += 4) {
+            float x[R][4];
+#pragma unroll
+            for (int u = 0; u < R; ++u) {
+                const float4 v = *reinterpret_cast<const float4*>(&Qs[R * warp + u][e]);
+                x[u][0] = v.x;
+                x[u][1] = v.y;
+                x[u][2] = v.z;
+                x[u][3] = v.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float w[4];
+                four_planes(Ws + (e + i) * kQTPlanes + 4 * lane, w);
+#pragma unroll
+                for (int u = 0; u < R; ++u)
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) acc[u][p][i] = fmaf(w[p], x[u][i], acc[u][p][i]);
+            }
+        }
+        uint32_t bits[R];                        // of the lane's planes, one each
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            bits[u] = 0u;
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                bits[u] |= (acc[u][p][0] + acc[u][p][1]) + (acc[u][p][2] + acc[u][p][3]) > 0.0f ? 1u << p : 0u;
+            uint32_t word = bits[u] << 4 * (lane & 7);
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, o);
+            const int wd = j0 / 32 + (lane >> 3);
+            const long long qbi = static_cast<long long>(mine + u) * a.qwords + wd;
+            if ((lane & 7) == 0 && mine + u < a.BHq && wd < a.qwords &&
+                mp_check(a.status, qbi, static_cast<long long>(a.BHq) * a.qwords, kSiteQencodeStore))
+                a.qbits[qbi] = word;
+        }
+        const int j = j0 + 4 * lane;             // below cpad: so are the four
+        if (j < a.cpad) {
+            if (a.G % R == 0) {                  // rows of one group, side by side
+                const int b = mine / a.Hq, h = mine - b * a.Hq, g = h / a.G;
+                const long long qmi = ((static_cast<long long>(b) * Hkv + g) * a.cpad + j) * a.G + (h - g * a.G);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    if (!mp_check(a.status, qmi + p * a.G + R - 1, static_cast<long long>(a.BHq) * a.cpad,
+                                  kSiteQencodeStore))
+                        break;
+                    uint32_t m[R];
+#pragma unroll
+                    for (int u = 0; u < R; ++u) m[u] = bits[u] >> p & 1u ? 0u : 0xffffffffu;
+                    if constexpr (R == 4)
+                        *reinterpret_cast<uint4*>(a.qmask + qmi + p * a.G) = make_uint4(m[0], m[1], m[2], m[3]);
+                    else
+                        *reinterpret_cast<uint2*>(a.qmask + qmi + p * a.G) = make_uint2(m[0], m[1]);
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < R; ++u) {
+                    const int row = mine + u, b = row / a.Hq, h = row - b * a.Hq, g = h / a.G;
+                    const long long qmi = ((static_cast<long long>(b) * Hkv + g) * a.cpad + j) * a.G +
+                                          (h - g * a.G);
+                    if (row < a.BHq &&
+                        mp_check(a.status, qmi + 3 * a.G, static_cast<long long>(a.BHq) * a.cpad,
+                                 kSiteQencodeStore))
+                        for (int p = 0; p < 4; ++p)
+                            a.qmask[qmi + p * a.G] = bits[u] >> p & 1u ? 0u : 0xffffffffu;
+                }
+            }
+        }
+    }
+    if (blockIdx.x != 0) return;
+    // |q| and q.mu, and the counters
+    float nn[R], qm[R];
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+        nn[u] = qm[u] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kD / 32; ++k) {
+            const float x = Qs[R * warp + u][lane + 32 * k];
+            nn[u] = fmaf(x, x, nn[u]);
+            qm[u] = fmaf(x, mu[u][k], qm[u]);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            nn[u] += __shfl_xor_sync(0xffffffffu, nn[u], o);
+            qm[u] += __shfl_xor_sync(0xffffffffu, qm[u], o);
+        }
+    }
+    if (lane == 0) {
+#pragma unroll
+        for (int u = 0; u < R; ++u)
+            if (mine + u < a.BHq && mp_check(a.status, mine + u, a.BHq, kSiteQencodeStore)) {
+                a.qstat[mine + u] = make_float4(sqrtf(nn[u]), qm[u], 0.0f, 0.0f);
+                a.counters[mine + u] = 0u;
+            }
     }
 }
 
@@ -1199,6 +1379,13 @@ KernelFn pick_collide(int G) {
     }
 }
 
+typedef void (*QRowsFn)(const QArgs);
+QRowsFn pick_qencode_rows(bool w_bf16, int rows) {
+    using Bf16 = __nv_bfloat16;
+    if (rows == 2) return w_bf16 ? qencode_rows_kernel<Bf16, 2> : qencode_rows_kernel<float, 2>;
+    return w_bf16 ? qencode_rows_kernel<Bf16, 4> : qencode_rows_kernel<float, 4>;
+}
+
 typedef void (*AttendFn)(const AArgs);
 
 AttendFn pick_attend(KvForm form, bool shared = false, bool paged = false) {
@@ -1270,6 +1457,17 @@ cudaError_t prepare_decode() {
                                              cudaSharedmemCarveoutMaxShared);
         if (e != cudaSuccess) return e;
     }
+    for (int rows : {2, 4}) {
+        for (int w_bf16 : {0, 1}) {
+            const QRowsFn fn = pick_qencode_rows(w_bf16, rows);
+            cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 kD * kQTPlanes * (w_bf16 ? 2 : 4));
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                         cudaSharedmemCarveoutMaxShared);
+            if (e != cudaSuccess) return e;
+        }
+    }
     cudaFuncAttributes fa;
     cudaError_t e = cudaFuncGetAttributes(&fa, log_inclusion_kernel);
     if (e != cudaSuccess) return e;
@@ -1283,9 +1481,9 @@ cudaError_t launch_log_inclusion(const float* cosines, int count, int K, int L, 
     return cudaGetLastError();
 }
 
-cudaError_t launch_qencode(const void* q, bool q_bf16, const float* centre, const void* W,
-                           bool w_bf16, const DecodeShape& s, const DecodeScratch& ws,
-                           cudaStream_t st) {
+namespace {
+QArgs query_args(const void* q, bool q_bf16, const float* centre, const void* W, bool w_bf16,
+                 const DecodeShape& s, const DecodeScratch& ws) {
     QArgs qa;
     qa.q = q;
     qa.W = W;
@@ -1308,6 +1506,15 @@ cudaError_t launch_qencode(const void* q, bool q_bf16, const float* centre, cons
     qa.K = s.K;
     qa.L = s.L;
     qa.qrow_ctas = (qa.BHq + kQRows - 1) / kQRows;
+    qa.w_wide = s.C % 4 == 0 && reinterpret_cast<uintptr_t>(W) % (w_bf16 ? 8 : 16) == 0;
+    return qa;
+}
+}  // namespace
+
+cudaError_t launch_qencode(const void* q, bool q_bf16, const float* centre, const void* W,
+                           bool w_bf16, const DecodeShape& s, const DecodeScratch& ws,
+                           cudaStream_t st) {
+    const QArgs qa = query_args(q, q_bf16, centre, W, w_bf16, s, ws);
     const dim3 qgrid(s.qwords > 0 ? s.qwords : 1, qa.qrow_ctas + 1);
     // As a dependent of what precedes it a call that is queued on a stream starts 2 us sooner (44.7
     // -> 42.4 us at 96K tokens). In a graph, whose launches follow each other closely as it is, the
@@ -1319,6 +1526,19 @@ cudaError_t launch_qencode(const void* q, bool q_bf16, const float* centre, cons
         return launch_dependent(qencode_kernel, qgrid, dim3(kThreads), 0, st, qa);
     qencode_kernel<<<qgrid, kThreads, 0, st>>>(qa);
     return cudaGetLastError();
+}
+
+cudaError_t launch_qencode_rows(const void* q, bool q_bf16, const float* centre, const void* W,
+                                bool w_bf16, const DecodeShape& s, const DecodeScratch& ws,
+                                cudaStream_t st) {
+    const QArgs qa = query_args(q, q_bf16, centre, W, w_bf16, s, ws);
+    // Calls of 128, 512 and 32 query rows with the kernel above 40.3, 45.1 and 47.7 us, with two rows a lane
+    // 39.4, 36.9 and 50.4 (few CTAs, each as long as one alone), with four 40.4, 36.1 and 52.2.
+    if (qa.BHq <= 64) return launch_qencode(q, q_bf16, centre, W, w_bf16, s, ws, st);
+    const int R = qa.BHq <= 256 ? 2 : 4;
+    return launch_dependent(pick_qencode_rows(w_bf16, R),
+                            dim3(std::max(1, (s.C + kQTPlanes - 1) / kQTPlanes), (qa.BHq + 4 * R - 1) / (4 * R)),
+                            dim3(kQTThreads), kD * kQTPlanes * (w_bf16 ? 2 : 4), st, qa);
 }
 
 namespace {

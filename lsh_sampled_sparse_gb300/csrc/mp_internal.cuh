@@ -174,6 +174,10 @@ cudaError_t launch_encode_rows_at(const void* keys, bool keys_bf16, const float*
 cudaError_t launch_qencode(const void* q, bool q_bf16, const float* centre, const void* W,
                            bool w_bf16, const DecodeShape& s, const DecodeScratch& ws,
                            cudaStream_t st);
+// the same bits, norms and counters for the decode over pages, without the table of log u
+cudaError_t launch_qencode_rows(const void* q, bool q_bf16, const float* centre, const void* W,
+                                bool w_bf16, const DecodeShape& s, const DecodeScratch& ws,
+                                cudaStream_t st);
 // The code scan over blocks [blk0, nblk) (selection words of those blocks; every block when
 // blk0 == 0), then the attend kernel over every block. cudaErrorNotSupported if it cannot fit a
 // CTA

@@ -23,7 +23,7 @@ def main() -> None:
     freq = (1e4 ** (-torch.arange(0, 128, 2, device="cuda").double() / 128)).float()
     for dt in (torch.bfloat16, torch.float32):
         for B, Hkv, G, n, page in ((2, 3, 4, 700, 16), (1, 8, 8, 9001, 64), (3, 1, 1, 1, 8),
-                                   (5, 2, 12, 2003, 48), (9, 2, 2, 300, 24)):
+                                   (5, 2, 12, 2003, 48), (9, 2, 2, 300, 24), (70, 1, 4, 90, 8)):
             slots = -(-n // page)
             n_pages = B * slots + 1
             table = torch.randperm(n_pages, generator=gen, device="cuda")[:B * slots].view(B, -1).int()

@@ -618,6 +618,30 @@ def test_sampled_decode_over_pages(mp, dt, Hq, Hkv, n, page, K, L, n_sink, n_loc
     check(None, [n] * len(lens), n)
 
 
+@pytest.mark.parametrize("dt,B,Hq,Hkv,K,L", [(BF, 12, 8, 2, 10, 150), (F32, 9, 8, 4, 6, 40), (BF, 41, 8, 1, 8, 75),
+                                             (F32, 70, 4, 4, 5, 23), (BF, 33, 16, 4, 3, 49)])
+def test_sampled_decode_of_many_sequences(mp, dt, B, Hq, Hkv, K, L):
+    """Batches whose queries are encoded several rows at a time (and hyperplanes that are no multiple of
+    four): the keys that the contiguous cache's encoding samples."""
+    n, page, n_sink, n_local = 300, 16, 2, 9
+    lens = [(37 * b) % (n + 1) for b in range(B)]
+    wl = small_workload(name="pagedb", index=782, B=B, Hq=Hq, Hkv=Hkv, n=n, K=K, L=L, kv_dtype=dt,
+                        q_dtype=dt, w_dtype=dt)
+    g = _gen(B)
+    x = {k: v.cuda() for k, v in make_layer(wl).items()}
+    W = make_hyperplanes(wl).cuda()
+    centre = mp.key_mean(x["keys"])
+    cache, table = _pages_of(mp, g, x, n, page)
+    codes = mp.encode_rows(x["keys"], centre, W, K, L, 0, n)
+    args = (K, L, n_sink, n_local)
+    chosen = _chosen(mp, x, codes, centre, W, lens, n, args, Hkv)
+    out = mp.paged_decode_attention(x["q"], codes, centre, W, cache, table, *args, n=n,
+                                    lengths=_ints(lens), n_capacity=n)
+    want, tol = R.sampled(x["q"], centre, cache.keys, cache.values, table.cpu(), lens, chosen, *args,
+                          128 ** -0.5)
+    assert ((out.double() - want).abs() <= tol).all()
+
+
 @pytest.mark.parametrize("variant,K,L", [("mips", 8, 75), ("cp", 1, 32)])
 def test_variants_run_over_pages(mp, variant, K, L):
     """The same weights as over the contiguous cache: outputs agree to a few roundings of log u."""
