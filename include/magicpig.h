@@ -520,10 +520,11 @@ MP_API size_t mp_paged_attention_workspace_bytes(int B, int Hq, int Hkv, int n, 
  * the lengths themselves, on the device: n may be the table's whole capacity. A sequence of length
  * 0, or whose tokens have no page, gets zero rows. Any Hq that Hkv divides. scale 0 means 1/sqrt(d).
  * Scores, softmax and sums are float32: over a bf16 cache the products are tensor-core products of
- * bf16, a float32 query element or a weight being three bf16 terms (24 bits). What the pages hold
- * beyond a sequence's length is not looked at, NaN included. A NaN or an infinity in a query (float32
- * queries over a bf16 cache: an element past the largest bf16, too), or in a key or value attended
- * to, may give NaN in the rows that it meets.
+ * bf16, a float32 query element or a weight being three bf16 terms (24 bits); over a float32 cache with
+ * more than four query heads a KV head, of tf32, every number being two terms (22 bits and more). What
+ * the pages hold beyond a sequence's length is not looked at, NaN included. A NaN or an infinity in a
+ * query, or in a key or value attended to, may give NaN in the rows that it meets, and so may an element
+ * past the largest bf16 or tf32 where it is split.
  * Errors: MP_ERR_INVALID_ARG (shapes, n > n_slots page_size or 2^30, B Hq > 2^22, B Hq n > 2^35, Hq %
  * Hkv, a scale that is negative, infinite or NaN, null, misalignment: out 16 bytes, lengths 4, workspace 256),
  * MP_ERR_UNSUPPORTED (d != 128, page_size not a multiple of 8), MP_ERR_WORKSPACE. */

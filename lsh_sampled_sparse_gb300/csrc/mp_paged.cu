@@ -212,9 +212,9 @@ __global__ void __launch_bounds__(kAppThreads, kAppCtas) paged_append_kernel(con
 // shared memory (cp.async: 12 KB in flight a warp), across the units of the run; a lane copies what it
 // reads itself. The NH scores of four tokens are summed over the lanes by a reduce-scatter, which leaves
 // a score to 8 / NH lanes, the softmax steps are lane-parallel, weights come back through
-// shared memory. Bound by memory up to four query heads a KV head (8 sequences x 8 heads x 8K tokens: 85, 86
-// and 87 us for 1, 2 and 4, 6.2 TB/s), at eight by what the heads cost a warp that holds 32 sums and 32
-// queries' dims a lane in 128 registers (113 us; one CTA an SM with twice the registers 136).
+// shared memory. Bound by memory: 8 sequences x 8 heads x 8K tokens with 1, 2 and 4 query heads a KV head 85, 86
+// and 87 us, 6.2 TB/s. Eight heads would hold 32 sums and 32 queries' dims a lane in 128 registers (113 us):
+// more than four are mp_paged_mma.cu's.
 constexpr int kSimtWarps = 8;
 constexpr int kSimtThreads = 32 * kSimtWarps;
 constexpr int kSimtShift = 5;                    // log2 of a tile's tokens: four a warp
@@ -570,6 +570,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const PArgs
         a.out[row * kD + e] = over_sum(Os, Ls);
 }
 
+constexpr int kSimtHeads = 4;                    // of a KV head, at most; more: mp_paged_mma.cu
 constexpr int kSimtCtas = 2 * kPagedTcCtas;      // two an SM
 // Tokens a CTA of a cluster may have more than its even share of all: they take as long as the second
 // kernel, which the even shares' states need. One sequence x 8 heads, bf16, in a cluster or evenly: 2K
@@ -580,7 +581,7 @@ constexpr int kJoinTokens = 512;
 // leaves its CTAs alone with them. 19 sequences x 8 heads, bf16, one of 32K tokens and the others of 100:
 // 272 us in clusters, 39 evenly; eight sequences, one of 4K: 25.3 and 15.8, all of 4K: 31.3 and 35.1.
 constexpr int kRaggedTokens = 1024;
-int simt_heads(int G) { return G <= 2 ? G : (G <= 4 ? 4 : 8); }
+int simt_heads(int G) { return G <= 2 ? G : 4; }
 
 typedef void (*PFn)(const PArgs);
 template <int NH>
@@ -589,7 +590,7 @@ PFn simt(int* smem) {
     return paged_attention_simt_kernel<NH>;
 }
 PFn pick_simt(int nh, int* smem) {
-    return nh == 1 ? simt<1>(smem) : (nh == 2 ? simt<2>(smem) : (nh == 4 ? simt<4>(smem) : simt<8>(smem)));
+    return nh == 1 ? simt<1>(smem) : (nh == 2 ? simt<2>(smem) : simt<4>(smem));
 }
 
 // How many clusters of so many CTAs the GPU holds at once, by whether the kernel is the tensor cores'
@@ -661,8 +662,8 @@ cudaError_t launch_paged_append(const mp_rows& keys, const mp_rows& values, cons
 
 size_t paged_attention_scratch_bytes(int Hq, int Hkv) {
     // of either kind of cache: who asks does not say which
-    const size_t parts = std::max(kSimtCtas * simt_heads(Hq / Hkv),
-                                  kPagedTcCtas * paged_tc_heads(Hq / Hkv));
+    const int G = Hq / Hkv;
+    const size_t parts = std::max(G <= kSimtHeads ? kSimtCtas * simt_heads(G) : 0, kPagedTcCtas * paged_tc_heads(G));
     return parts * 2 * kPart * sizeof(float) + (std::max(kSimtCtas, kPagedTcCtas) + 1) * sizeof(int4);
 }
 
@@ -680,12 +681,12 @@ cudaError_t launch_paged_attention(const void* q, bool q_bf16, const mp_paged& c
     a.Hq = Hq;
     a.Hkv = Hkv;
     a.G = Hq / Hkv;
-    const bool tc = cache.dtype == MP_BF16;
-    a.nh = tc ? paged_tc_heads(a.G) : simt_heads(a.G);
+    const bool tc = cache.dtype == MP_BF16, simt = !tc && a.G <= kSimtHeads;
+    a.nh = simt ? simt_heads(a.G) : paged_tc_heads(a.G);
     a.chunks = (a.G + a.nh - 1) / a.nh;
     a.n = n;
-    a.ctas = tc ? kPagedTcCtas : kSimtCtas;
-    a.tile_shift = tc ? kPagedTcShift : kSimtShift;
+    a.ctas = simt ? kSimtCtas : kPagedTcCtas;
+    a.tile_shift = simt ? kSimtShift : kPagedTcShift;
     a.q_wide = (reinterpret_cast<uintptr_t>(q) & 15u) == 0u;
     a.page_shift = -1;
     for (int i = 3; i < 31; ++i)
@@ -694,7 +695,7 @@ cudaError_t launch_paged_attention(const void* q, bool q_bf16, const mp_paged& c
     const long long units = static_cast<long long>(B) * Hkv * a.chunks;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    a.cluster = cluster_size(units, tiles, a.ctas, a.tile_shift, lengths != nullptr, g_clusters[dev][tc ? 1 : 0]);
+    a.cluster = cluster_size(units, tiles, a.ctas, a.tile_shift, lengths != nullptr, g_clusters[dev][simt ? 0 : 1]);
     a.scale = scale * 1.4426950408889634f;
     a.status = device_status_ptr();
     a.part = static_cast<float*>(workspace);
@@ -702,8 +703,9 @@ cudaError_t launch_paged_attention(const void* q, bool q_bf16, const mp_paged& c
     const unsigned grid = a.cluster ? static_cast<unsigned>(units) * a.cluster : a.ctas;
     int smem;
     const cudaError_t e = tc ? launch_paged_attention_tc(a, cache, grid, st)
-                             : launch_dependent(pick_simt(a.nh, &smem), dim3(grid), dim3(kSimtThreads),
-                                                smem, st, a, std::max(1, a.cluster));
+                          : !simt ? launch_paged_attention_mma(a, grid, st)
+                                  : launch_dependent(pick_simt(a.nh, &smem), dim3(grid), dim3(kSimtThreads),
+                                                     smem, st, a, std::max(1, a.cluster));
     if (e != cudaSuccess || a.cluster) return e;
     // where every sequence has the same tiles, the shares may fall on whole units
     const long long total = units * tiles, shares = std::min<long long>(a.ctas, total);
@@ -719,7 +721,7 @@ cudaError_t prepare_paged() {
     for (int i = 0; i < 4; ++i) {
         if ((e = cudaFuncGetAttributes(&fa, pick_append(i & 1, i & 2))) != cudaSuccess) return e;
     }
-    for (int nh : {1, 2, 4, 8}) {
+    for (int nh : {1, 2, 4}) {
         int smem;
         const PFn fn = pick_simt(nh, &smem);
         e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -728,7 +730,7 @@ cudaError_t prepare_paged() {
                                      cudaSharedmemCarveoutMaxShared);
         if (e != cudaSuccess) return e;
     }
-    if ((e = prepare_paged_tc()) != cudaSuccess) return e;
+    if ((e = prepare_paged_tc()) != cudaSuccess || (e = prepare_paged_mma()) != cudaSuccess) return e;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     for (int c = 1; c <= kPagedMaxCluster; ++c) {

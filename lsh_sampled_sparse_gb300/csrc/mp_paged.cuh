@@ -259,6 +259,9 @@ constexpr int kPagedTcShift = 7;
 cudaError_t launch_paged_attention_tc(const PArgs& a, const mp_paged& cache, unsigned grid,
                                       cudaStream_t st);
 cudaError_t prepare_paged_tc();
+// Over a float32 cache, for more than four heads a KV head (mp_paged_mma.cu), with the same CTAs and tiles.
+cudaError_t launch_paged_attention_mma(const PArgs& a, unsigned grid, cudaStream_t st);
+cudaError_t prepare_paged_mma();
 cudaError_t paged_tc_clusters(int size, int* n);     // clusters of that size that the GPU holds at once
 template <typename Fn>
 cudaError_t max_clusters(Fn fn, int threads, size_t smem, int size, int* n) {

@@ -300,7 +300,8 @@ def test_attention_where_a_new_maximum_comes_late(mp, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-def test_attention_passes_nan_and_infinity_on(mp, dtype):
+@pytest.mark.parametrize("G", [2, 7, 11])
+def test_attention_passes_nan_and_infinity_on(mp, dtype, G):
     n = 400
     g = _gen(12)
     cache, table = _random_cache(mp, g, 3, 1, n, 16, dtype, [n] * 3)
@@ -310,13 +311,13 @@ def test_attention_passes_nan_and_infinity_on(mp, dtype):
 
     cache.values[at(0, 111)][100] = float("nan")
     cache.keys[at(1, 222)][5] = float("nan")
-    q = _randn(g, 3, 2, 128)
+    q = _randn(g, 3, G, 128)
     q[2, 1, 7] = float("inf")
     out = mp.paged_attention(q, cache, table, n=n)
     nan = torch.isnan(out)
     assert nan[0, :, 100].all() and not nan[0, :, :100].any() and not nan[0, :, 101:].any()
     assert nan[1].all()
-    assert not nan[2, 0].any() and nan[2, 1].all()
+    assert not nan[2, 0].any() and nan[2, 1].all() and not nan[2, 2:].any()
     short = _ints([111, 222, 400])               # ends before the bad token
     q[2, 1, 7] = 0.0
     _attend_and_check(mp, q, cache, table, n, [111, 222, 400], short)
@@ -488,15 +489,15 @@ def test_calls_on_two_streams_at_once(mp, dtype):
 
 def test_what_was_handed_in_is_filled_and_no_more(mp):
     g = _gen(31)
-    for dtype in (BF, F32):
-        cache, table = _random_cache(mp, g, 1, 2, 3000, 16, dtype, [3000])
-        q = _randn(g, 1, 8, 128).to(BF)
-        room = torch.full((3, 8, 128), 7.0, device="cuda")
-        size = mp.paged_attention_workspace_bytes(1, 8, 2, 3000)
+    for dtype, Hq in ((BF, 8), (F32, 8), (BF, 24), (F32, 16), (F32, 24)):
+        cache, table = _random_cache(mp, g, 1, 2, 30000, 16, dtype, [30000])
+        q = _randn(g, 1, Hq, 128).to(BF)
+        room = torch.full((3, Hq, 128), 7.0, device="cuda")
+        size = mp.paged_attention_workspace_bytes(1, Hq, 2, 30000)
         ws = torch.full((size + 4096,), 0xEE, dtype=torch.uint8, device="cuda")
-        out = mp.paged_attention(q, cache, table, out=room[1:2], workspace=ws, n=3000)
+        out = mp.paged_attention(q, cache, table, out=room[1:2], workspace=ws, n=30000)
         assert out.data_ptr() == room[1].data_ptr()
-        assert torch.equal(out, mp.paged_attention(q, cache, table, n=3000))
+        assert torch.equal(out, mp.paged_attention(q, cache, table, n=30000))
         assert (room[0] == 7).all() and (room[2] == 7).all()
         assert (ws[size:] == 0xEE).all()
 

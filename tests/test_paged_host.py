@@ -125,15 +125,16 @@ def test_encode_rows_at_rejects_bad_arguments_before_launch(L):
     assert enc(m=0, keys=None) == 0 and enc(K=0, keys=None) == 0
 
 
-def test_dependent_kernels_of_the_paged_cache_make_no_non_coherent_load():
+@pytest.mark.parametrize("name,count", [("mp_paged.cu", 3), ("mp_paged_tc.cu", 1), ("mp_paged_mma.cu", 1)])
+def test_dependent_kernels_of_the_paged_cache_make_no_non_coherent_load(name, count):
     """A kernel launched as a dependent begins before its predecessor has written positions, lengths,
     tables, queries or rows; a non-coherent load promises that nobody writes them during its life."""
-    with open(os.path.join(CSRC, "mp_paged.cu")) as f:
+    with open(os.path.join(CSRC, name)) as f:
         code = re.sub(r"//[^\n]*", "", f.read())
     assert "__ldg(" not in code and ".global.nc" not in code and "__restrict__" not in code
     assert "<<<" not in code
     kernels = re.findall(r"__global__.*?\n}\n", code, re.S)
-    assert len(kernels) >= 3 and all("wait_for_predecessor();" in k for k in kernels)
+    assert len(kernels) >= count and all("wait_for_predecessor();" in k for k in kernels)
 
 
 @pytest.mark.parametrize("total", [1, 2, 7, 151, 152, 153, 1000, 10007, 2 ** 45 + 3])
