@@ -546,7 +546,7 @@ struct AArgs {
     FineLogU fine;                               // 4-bit cache: log u of a key, SimHash codes
     int q_bf16, n, nblk, nsb, Hq, Hkv, G, K, L, n_sink, n_local;
     int ncap;                                    // K/V rows per head in memory
-    int share;                                   // 4-bit cache: 2^share CTAs, a cluster, per partial
+    int share;                                   // 4-bit and paged cache: 2^share CTAs, a cluster, per partial
     int* status;                                 // index checks of the MP_CHECKS build
     const float* radius;                         // MIPS variant: longest centred key per head
     float scale;
@@ -841,6 +841,22 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
     //      through the selection words and their prefix counts (no list is materialised)
     const int t_a = min(a.n_sink, n), t_b = max(n - a.n_local, t_a);
     int nsel;
+    // paged: the rows of the pool of the kRowKeys keys selected from entry `base` on, -1 where a slot holds no
+    // page; each thread those of its word
+    auto list_rows = [&](int base) {
+        const int key0 = blk0 * kKeysPerBlock + tid * 32;
+        uint32_t U = wsel[tid];
+        for (int i = wpre[tid]; U; U &= U - 1u, ++i) {
+            const int at = (i >> share) - base;
+            if (at >= kRowKeys) break;
+            if (at < 0 || (i & ((1 << share) - 1)) != rank) continue;
+            const int key = key0 + __ffs(U) - 1, slot = key / a.pages.page_size;
+            const int pg = pslot[slot - slot0];
+            rowkey[at] = pg >= 0 && pg < a.pages.n_pages
+                             ? (pg * a.Hkv + h / a.G) * a.pages.page_size + key - slot * a.pages.page_size
+                             : -1;
+        }
+    };
     if (exact) {
         nsel = t_a + (n - t_b);
     } else {
@@ -879,17 +895,7 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
         } else {
             wpre[tid] = before + incl - c;
         }
-        if constexpr (kPaged) {
-            // the first kRowKeys keys' rows of the pool, -1 where a slot holds no page
-            const int key0 = blk0 * kKeysPerBlock + tid * 32;
-            for (int i = before + incl - c; U && i < kRowKeys; U &= U - 1u, ++i) {
-                const int key = key0 + __ffs(U) - 1, slot = key / a.pages.page_size;
-                const int pg = pslot[slot - slot0];
-                rowkey[i] = pg >= 0 && pg < a.pages.n_pages
-                                ? (pg * a.Hkv + h / a.G) * a.pages.page_size + key - slot * a.pages.page_size
-                                : -1;
-            }
-        }
+        if constexpr (kPaged) list_rows(0);
         if (tid == kAThreads - 1) wpre[kWords] = before + incl;
         __syncthreads();
         nsel = wpre[kWords];
@@ -1108,20 +1114,25 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
     };
     static_assert(kAttendRows == 8 * kHalves, "the stage gives each half-warp 8 row slots");
     // the keys of the first kRowKeys entries, listed once; later ones are found on demand (a 4-bit
-    // cache's are all listed by now, a paged one's as rows of the pool, but for T's)
+    // cache's are all listed by now, a paged one's a window of kRowKeys rows of the pool at a time: one query
+    // head over 3000 tokens at (6, 180), most of them sampled, 478 us with keys found on demand, 42 so, and
+    // with the rows shared by a cluster)
+    int base = 0;                                // of the window
+    auto list_window = [&]() {
+        for (int i = tid; i < min(nsel - base, kRowKeys); i += kAThreads)
+            rowkey[i] = kPaged ? static_cast<int>(paged_row(a.pages, slots, key_of(base + i), a.Hkv, h / a.G))
+                               : key_of(i);
+    };
     if constexpr (KV != kKv4) {
         if (!kPaged || exact) {
-            for (int i = tid; i < min(nsel, kRowKeys); i += kAThreads)
-                rowkey[i] = kPaged ? static_cast<int>(paged_row(a.pages, slots, key_of(i), a.Hkv, h / a.G))
-                                   : key_of(i);
+            list_window();
             __syncthreads();
         }
     }
     // Group k of a warp: entries hw + 8 (4 k + j), j < 4, of its two half-warps, in the slots
     // hw + 8 (4 (k & 1) + j); group k + 2 reuses group k's slots once group k is folded.
     const int lo_hw = 2 * warp;                  // the warp's first half-warp has its most rows
-    const int ngroups = nsel > lo_hw ? ((nsel - lo_hw + kHalves - 1) / kHalves + 3) / 4 : 0;
-    const int my_rows = nsel > hw ? (nsel - hw + kHalves - 1) / kHalves : 0;
+    int count, ngroups, my_rows;                 // entries at hand: all, or the window's
     // paged: which rows of groups k and k + 1 have pages, bit 8 (k & 1) + 2 j + half
     unsigned there = 0u;
     auto issue = [&](int k) {                    // one row (K then V) per instruction, 4-bit: three
@@ -1134,15 +1145,13 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
                 const int pc0 = kAtOnce > 1 ? lane % kPieces : lane;
                 if (kAtOnce > 1 && (jj >= min(8, j0 + kAtOnce))) continue;
                 const int e = lo_hw + (jj & 1) + kHalves * (4 * k + (jj >> 1));
-                if (e >= nsel) continue;
+                if (e >= count) continue;
                 const int r = lo_hw + (jj & 1) + kHalves * (4 * (k & 1) + (jj >> 1));
                 size_t key;
                 if constexpr (KV == kKv4)
                     key = exact ? key_of(e) : blk0 * kKeysPerBlock + rowlist[e];
                 else if constexpr (kPaged) {
-                    const int at = e < kRowKeys
-                        ? rowkey[e]
-                        : static_cast<int>(paged_row(a.pages, slots, key_of(e), a.Hkv, h / a.G));
+                    const int at = rowkey[e];
                     if (at < 0) {                // no page: zeros, which its weight of 0 keeps
                         for (int pc = pc0; pc < kPieces; pc += 32)
                             *reinterpret_cast<uint4*>(stage + r * kRowBytes + 16 * pc) =
@@ -1175,17 +1184,28 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
         const unsigned t = there >> (8 * (k & 1) + half);
         return (t & 1u) | (t >> 1 & 2u) | (t >> 2 & 4u) | (t >> 3 & 8u);
     };
-    issue(0);
-    issue(1);
-    for (int k = 0; k < ngroups; ++k) {
-        cp_async_wait_pending<1>();              // group k has landed (group k + 1 may not have)
-        __syncwarp();
-        fold(hw + kHalves * 4 * (k & 1), min(4, max(0, my_rows - 4 * k)),
-             std::integral_constant<int, 4>(), rows_there(k));
-        __syncwarp();                            // every lane is done with group k's slots
-        issue(k + 2);
+    for (;;) {
+        count = kPaged ? min(nsel - base, kRowKeys) : nsel;
+        ngroups = count > lo_hw ? ((count - lo_hw + kHalves - 1) / kHalves + 3) / 4 : 0;
+        my_rows = count > hw ? (count - hw + kHalves - 1) / kHalves : 0;
+        issue(0);
+        issue(1);
+        for (int k = 0; k < ngroups; ++k) {
+            cp_async_wait_pending<1>();              // group k has landed (group k + 1 may not have)
+            __syncwarp();
+            fold(hw + kHalves * 4 * (k & 1), min(4, max(0, my_rows - 4 * k)),
+                 std::integral_constant<int, 4>(), rows_there(k));
+            __syncwarp();                            // every lane is done with group k's slots
+            issue(k + 2);
+        }
+        cp_async_wait_pending<0>();
+        if (!kPaged || base + kRowKeys >= nsel) break;
+        base += kRowKeys;
+        __syncthreads();                         // the window is read
+        if (exact) list_window();
+        else list_rows(base);
+        __syncthreads();
     }
-    cp_async_wait_pending<0>();
     if (early) {
         wait_for_predecessor();                  // the query's norm, what the last call left in its place
         qn = a.qstat[row].x;
@@ -1390,8 +1410,10 @@ typedef void (*AttendFn)(const AArgs);
 
 AttendFn pick_attend(KvForm form, bool shared = false, bool paged = false) {
     if (paged)
-        return form == kKvBf16 ? attend_kernel<kKvBf16, false, true>
-                               : attend_kernel<kKvF32, false, true>;
+        return form == kKvBf16 ? (shared ? attend_kernel<kKvBf16, true, true>
+                                         : attend_kernel<kKvBf16, false, true>)
+                               : (shared ? attend_kernel<kKvF32, true, true>
+                                         : attend_kernel<kKvF32, false, true>);
     return form == kKv4 ? (shared ? attend_kernel<kKv4, true, false>
                                   : attend_kernel<kKv4, false, false>)
                         : (form == kKvBf16 ? attend_kernel<kKvBf16, false, false>
@@ -1429,7 +1451,8 @@ cudaError_t prepare_decode() {
         if (e != cudaSuccess) return e;
     }
     for (const AttendFn fn : {pick_attend(kKvF32), pick_attend(kKvBf16), pick_attend(kKv4),
-                              pick_attend(kKvF32, false, true), pick_attend(kKvBf16, false, true)}) {
+                              pick_attend(kKvF32, false, true), pick_attend(kKvBf16, false, true),
+                              pick_attend(kKvF32, true, true), pick_attend(kKvBf16, true, true)}) {
         cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(kMaxSmem));
         if (e != cudaSuccess) return e;
@@ -1451,7 +1474,9 @@ cudaError_t prepare_decode() {
                          reinterpret_cast<const void*>(pick_attend(kKv4)),
                          reinterpret_cast<const void*>(pick_attend(kKv4, true)),
                          reinterpret_cast<const void*>(pick_attend(kKvF32, false, true)),
-                         reinterpret_cast<const void*>(pick_attend(kKvBf16, false, true))};
+                         reinterpret_cast<const void*>(pick_attend(kKvBf16, false, true)),
+                         reinterpret_cast<const void*>(pick_attend(kKvF32, true, true)),
+                         reinterpret_cast<const void*>(pick_attend(kKvBf16, true, true))};
     for (const void* f : fns) {
         cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
                                              cudaSharedmemCarveoutMaxShared);
@@ -1632,15 +1657,15 @@ cudaError_t launch_attend(const void* q, bool q_bf16, const float* centre, const
     // slots shares them with up to seven others: of keys without a bias toward the query a share of
     // 1 - (1 + x) e^-x collides twice, x = L times the chance in one table. 16 query heads, 3194
     // keys, (7, 195): 144 us with neither this nor the whole list, 35 us with both; with few rows a
-    // cluster's start and join cost 1 us more than they save. Only over the 4-bit cache: the other
-    // forms' sums keep their order.
+    // cluster's start and join cost 1 us more than they save. Only over the 4-bit cache and over pages: the
+    // other forms' sums keep their order.
     const long long ctas = static_cast<long long>(s.B) * s.Hq * (aa.nsb + 1);
     const double x = s.L * (s.cp ? 0.5 / kD : ldexp(1.0, -s.K));
     const int keys = std::min(s.n, kAttendBlocks * kKeysPerBlock);
     const long long rows = std::max(static_cast<long long>(keys * (1.0 - (1.0 + x) * exp(-x))),
                                     std::min<long long>(s.n, 0ll + s.n_sink + s.n_local));
     aa.share = 0;
-    while (kv.form == kKv4 && rows > 2 * kAttendRows && aa.share < 3 &&
+    while ((kv.form == kKv4 || kv.pages) && rows > 2 * kAttendRows && aa.share < 3 &&
            ctas << (aa.share + 1) <= 6 * device_sm_count())
         ++aa.share;
     const AttendFn attend = pick_attend(kv.form, aa.share > 0, kv.pages != nullptr);

@@ -59,6 +59,10 @@ def main() -> None:
                     out = mp.paged_decode_attention(q, codes, centre, W, cache, table, K, L, 4, 64, n=n,
                                                     lengths=ln)
                     assert torch.isfinite(out).all()
+                    # most keys sampled
+                    out = mp.paged_decode_attention(q, codes, centre, W, cache, table, 1, 40, 40, 640, n=n,
+                                                    lengths=ln)
+                    assert torch.isfinite(out).all()
     torch.cuda.synchronize()
     assert mp.check_report() == (True, 0) and mp.device_status() == 0
     print("checks ok", flush=True)

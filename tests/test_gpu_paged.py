@@ -580,7 +580,10 @@ def _chosen(mp, x, codes, centre, W, lens, cap, args, Hkv, **extra):
 @pytest.mark.parametrize("dt,Hq,Hkv,n,page,K,L,n_sink,n_local", [
     (BF, 8, 2, 5000, 16, 10, 150, 4, 64), (F32, 4, 4, 1500, 24, 6, 40, 0, 3),
     (BF, 8, 1, 4097, 128, 9, 120, 4, 64), (F32, 2, 1, 900, 8, 0, 2, 4, 64),
-    (BF, 4, 2, 2000, 48, 3, 49, 0, 0), (BF, 2, 2, 3000, 64, 20, 1000, 4, 64)])
+    (BF, 4, 2, 2000, 48, 3, 49, 0, 0), (BF, 2, 2, 3000, 64, 20, 1000, 4, 64),
+    # many keys sampled, many in T: CTAs that share a partial's rows, and list them a window at a time
+    (BF, 1, 1, 9000, 16, 6, 180, 4, 64), (F32, 4, 2, 5000, 24, 6, 100, 100, 1500),
+    (BF, 8, 4, 2500, 8, 4, 60, 700, 300)])
 def test_sampled_decode_over_pages(mp, dt, Hq, Hkv, n, page, K, L, n_sink, n_local):
     lens = [n, n // 2 + 1, 0, 1, 70]
     wl = small_workload(name="paged", index=780, B=len(lens), Hq=Hq, Hkv=Hkv, n=n, K=K, L=L,
