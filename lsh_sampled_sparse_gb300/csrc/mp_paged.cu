@@ -71,20 +71,21 @@ __device__ __forceinline__ void turn_pair(float& x, float& y, float2 t) {
     x = fmaf(x0, t.x, -(y * t.y));
     y = fmaf(y, t.x, x0 * t.y);
 }
-// A lane's two pieces of a row, turned (cs: cos and sin of its eight pairs, NULL: as they are) and
-// rounded to D, to dst and, unless it is NULL, to dst2 too.
+// A lane's two pieces of a row, turned (cs: cos and sin of its eight pairs, two of them kRowLanes apart
+// from the next two; NULL: as they are) and rounded to D, to dst and, unless it is NULL, to dst2 too.
 template <typename T, typename D>
-__device__ __forceinline__ void turn_and_store(const Eight<T>& a, const Eight<T>& b, const float2* cs,
+__device__ __forceinline__ void turn_and_store(const Eight<T>& a, const Eight<T>& b, const float4* cs,
                                                bool interleaved, D* dst, D* dst2, int da, int db) {
     auto turned = [&](int e, float2& x, float2& y) {
         x = a.two(e);
         y = b.two(e);
         if (!cs) return;
         if (interleaved) {
-            turn_pair(x.x, x.y, cs[e]);
-            turn_pair(y.x, y.y, cs[e + 4]);
+            const float4 t = cs[kRowLanes * (e >> 1)], u = cs[kRowLanes * (2 + (e >> 1))];
+            turn_pair(x.x, x.y, e & 1 ? make_float2(t.z, t.w) : make_float2(t.x, t.y));
+            turn_pair(y.x, y.y, e & 1 ? make_float2(u.z, u.w) : make_float2(u.x, u.y));
         } else {
-            const float4 t = reinterpret_cast<const float4*>(cs)[e];
+            const float4 t = cs[kRowLanes * e];
             turn_pair(x.x, y.x, make_float2(t.x, t.y));
             turn_pair(x.y, y.y, make_float2(t.z, t.w));
         }
@@ -147,7 +148,9 @@ __device__ __forceinline__ uint64_t turn_of(float f) {
 // than the rows of the CTAs that fit an SM (8192 tokens of 32 + 8 + 8 heads: 45 us, so 41).
 template <typename T, typename C>
 __global__ void __launch_bounds__(kAppThreads, kAppCtas) paged_append_kernel(const AppendArgs a) {
-    __shared__ __align__(16) float2 turn[kMaxToks][kD / 2];
+    // cos and sin of a token's pairs: pair 8 l + 2 j + i is half i of turn[token][j][l], so that the lanes of a
+    // row read side by side
+    __shared__ float4 turn[kMaxToks][4][kRowLanes];
     __shared__ long long place[kMaxToks];        // a token's row of the pool for KV head 0, or -1
     const int tid = threadIdx.x, lane = tid & (kRowLanes - 1), row = tid / kRowLanes;
     const int b = blockIdx.x / a.tok_blocks;
@@ -161,6 +164,8 @@ __global__ void __launch_bounds__(kAppThreads, kAppCtas) paged_append_kernel(con
     const int da = halves ? 8 * lane : 16 * lane, db = halves ? a.pairs + 8 * lane : 16 * lane + 8;
     wait_for_predecessor();
     allow_dependents();
+    // (behind the sequence's last token; of a step's few tokens the rows do not wait for the count)
+    if (a.counts && a.tok_blocks > 1 && i0 >= a.counts[b]) return;
     Eight<T> xa, xb;
     const bool mine = tok < a.m && hv < a.Hkv;
     if (mine) {
@@ -184,11 +189,11 @@ __global__ void __launch_bounds__(kAppThreads, kAppCtas) paged_append_kernel(con
                                                       static_cast<uint64_t>(p0 + (tid >> 6)));
         float s, c;
         sincospif(static_cast<float>(part) * 0x1p-63f, &s, &c);
-        turn[tid >> 6][tid & 63] = make_float2(c, s);
+        reinterpret_cast<float2*>(&turn[tid >> 6][tid >> 1 & 3][tid >> 3 & 7])[tid & 1] = make_float2(c, s);
     }
     __syncthreads();
     if (!mine || tok >= live) return;
-    const float2* cs = hv < 0 && lane < turned ? &turn[i][8 * lane] : nullptr;
+    const float4* cs = hv < 0 && lane < turned ? &turn[i][0][lane] : nullptr;
     if (hk < 0) {
         const long long r = (static_cast<long long>(b) * a.Hq + h) * a.m + tok;
         if (mp_check(a.status, r, static_cast<long long>(a.B) * a.Hq * a.m, kSitePagedOut))
