@@ -337,6 +337,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int off = 16 / NH; off >= 1; off >>= 1)
                         r[0] += __shfl_xor_sync(0xffffffffu, r[0], off);
+                    // (one copy of the sums: a warp may still read those of the unit before. Where a tile
+                    // follows, the maxima's barrier stands between; behind the last one stands this)
+                    if (!more) softmax_sync();
                     if ((lane & (32 / NH - 1)) == 0) sums[warp * NH + lane * NH / 32] = r[0];
                     softmax_sync();
                     const int heads = aborted ? 0 : min(NH, a.G - last.h0);

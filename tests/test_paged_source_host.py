@@ -1,0 +1,82 @@
+"""The barriers of the softmax warps of the bf16 attention over pages, read from the source of its kernel and
+walked through on the host."""
+import itertools
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "lsh_sampled_sparse_gb300", "csrc")
+
+
+def _softmax_loop():
+    """The softmax warps' loop over tiles, without comments."""
+    with open(os.path.join(CSRC, "mp_paged_tc.cu")) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    loop = code[code.index("for (int it = 0; total > 0; ++it)"):code.index("} else if (warp == 4)")]
+    return loop
+
+
+def _events():
+    """[(kind, condition)] of a pass in the order of the source: the barriers among the softmax warps, and
+    what is written to and read from the array of the warps' sums. The condition is that of the innermost
+    `if` that tells passes apart."""
+    found = []
+    block = [None]                               # a condition a brace; None: always
+    token = re.compile(r"if \((more|it > 0|!fresh|fresh|!more)\) (softmax_sync\(\);|\{)|\} else \{|\{|\}|"
+                       r"softmax_sync\(\);|sums\[[^\]]*\] = |sums\[h\]")
+    closed = None
+    for m in token.finditer(_softmax_loop()):
+        t = m.group(0)
+        if m.group(1) and m.group(2) == "{":
+            block.append(m.group(1))
+        elif m.group(1):
+            found.append(("barrier", [*filter(None, block), m.group(1)]))
+        elif t == "} else {":
+            closed = block.pop()
+            block.append("fresh" if closed == "!fresh" else None)
+        elif t == "{":
+            block.append(None)
+        elif t == "}":
+            if len(block) > 1:
+                block.pop()
+        else:
+            kind = "barrier" if t.startswith("softmax") else ("write" if t.endswith("= ") else "read")
+            found.append((kind, list(filter(None, block))))
+    return found
+
+
+def _walk(units):
+    """The barriers and accesses of a warp over a run of units of so many tiles each, in order."""
+    tests = {"more": lambda more, fresh, it: more, "!more": lambda more, fresh, it: not more,
+             "fresh": lambda more, fresh, it: fresh, "!fresh": lambda more, fresh, it: not fresh,
+             "it > 0": lambda more, fresh, it: it > 0}
+    events, total, it, ends = _events(), sum(units), 0, set(itertools.accumulate(units)) | {0}
+    for it in range(total + 1):
+        more, fresh = it < total, it in ends
+        for kind, conditions in events:
+            if all(tests[c](more, fresh, it) for c in conditions):
+                yield kind
+
+
+def test_the_events_of_a_pass_are_found():
+    assert [k for k, _ in _events()].count("write") == 1
+    assert [k for k, _ in _events()].count("read") == 1
+    assert [k for k, _ in _events()].count("barrier") >= 2
+
+
+@pytest.mark.parametrize("units", [[1], [5], [1, 1], [3, 1], [1, 3], [1, 1, 1, 1], [4, 1, 2, 1], [2, 2], [7, 1]])
+def test_no_warp_writes_the_sums_while_another_may_read_the_last_ones(units):
+    """Between an access of the sums and the next one of the other kind stands a barrier of the four warps:
+    else a warp that lags would read the sums of another unit."""
+    since, last, writes = 0, None, 0
+    for kind in _walk(units):
+        if kind == "barrier":
+            since += 1
+            continue
+        writes += kind == "write"
+        if last is not None and last != kind:
+            assert since > 0, (units, last, kind)
+        last, since = kind, 0
+    assert writes == len(units)
