@@ -539,7 +539,8 @@ MP_API mp_status mp_paged_attention(const void* q, mp_dtype q_dtype, const mp_pa
  * means n), and hold the keys' own tokens at their positions (mp_encode_rows, mp_encode_rows_at of
  * the keys that mp_paged_append returns). A token without a page is left out, of T too. log u of the
  * SimHash codes is evaluated for each sampled key. Workspace: mp_decode_workspace_bytes.
- * Errors as mp_decode_attention and mp_paged_attention. */
+ * Errors: those of mp_decode_attention, and MP_ERR_INVALID_ARG (the cache, lengths, n > n_slots
+ * page_size or 2^30), MP_ERR_UNSUPPORTED (page_size not a multiple of 8). */
 MP_API mp_status mp_paged_decode_attention(const void* q, mp_dtype q_dtype, const uint32_t* codes,
                                            const float* centre, const void* W, mp_dtype w_dtype,
                                            const mp_paged* cache, int B, int Hq, int Hkv, int n, int d,

@@ -827,7 +827,8 @@ mp_status mp_paged_decode_attention(const void* q, mp_dtype q_dtype, const uint3
                                     const mp_paged* cache, int B, int Hq, int Hkv, int n, int d,
                                     const int32_t* lengths, const mp_params* prm, float* out,
                                     void* workspace, size_t ws_bytes, cudaStream_t stream) {
-    if (B < 1 || Hkv < 1 || !aligned(lengths, 4)) return MP_ERR_INVALID_ARG;
+    // (tokens, a CTA's share past them included, are numbered in 32 bits)
+    if (B < 1 || Hkv < 1 || n > (1 << 30) || !aligned(lengths, 4)) return MP_ERR_INVALID_ARG;
     const mp_status sp = check_paged(cache, Hkv);
     if (sp != MP_OK) return sp;
     DecodeShape s;
