@@ -228,7 +228,7 @@ MP_API size_t mp_decode_workspace_bytes(int B, int Hq, int Hkv, int n, int d,
  * and T are both empty the output row is zero. Zero-length q or k - mu gives cosine 0 (p = 1/2).
  * A query row with a NaN or infinite element gets a NaN output row; the other rows are unaffected
  * and the status word is not raised.
- * Errors: MP_ERR_INVALID_ARG (shapes, null, Hq % Hkv, n_sink/n_local < 0, flags other than
+ * Errors: MP_ERR_INVALID_ARG (shapes, null, Hq % Hkv, B Hq > 65535, n_sink/n_local < 0, flags other than
  *         MP_FLAG_MIPS or MP_FLAG_CROSS_POLYTOPE, or a flag without its radius / log u table),
  *         MP_ERR_UNSUPPORTED (d != 128, Hq/Hkv not in {1, 2, 4, 8}, or K*L*(Hq/Hkv) so
  *         large that a CTA's query masks no longer fit in shared memory),
@@ -249,7 +249,7 @@ MP_API mp_status mp_decode_attention(const void* q, mp_dtype q_dtype, const uint
  * merged softmax with the exact set T (Algorithm 1's remaining steps). It may load codes, q and
  * centre before the work queued ahead of it has ended: they are to be written before
  * mp_encode_query is called, not between the two (keys and values may be).
- * Errors as mp_decode_attention. */
+ * Errors as mp_decode_attention (mp_encode_query takes any B Hq). */
 MP_API mp_status mp_encode_query(const void* q, mp_dtype q_dtype, const float* centre,
                                  const void* W, mp_dtype w_dtype, int B, int Hq, int Hkv, int n,
                                  int d, const mp_params* prm, void* workspace, size_t ws_bytes,

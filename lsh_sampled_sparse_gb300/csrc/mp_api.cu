@@ -197,6 +197,7 @@ mp_status validate_decode(const void* q, mp_dtype q_dtype, const uint32_t* codes
                           const void* values, mp_dtype kv_dtype, int B, int Hq, int Hkv, int n,
                           int d, const mp_params* prm, const float* out, DecodeShape* s) {
     if (!fill_shape(B, Hq, Hkv, n, d, prm, s)) return MP_ERR_INVALID_ARG;
+    if (static_cast<long long>(B) * Hq > 65535) return MP_ERR_INVALID_ARG;   // query rows of a grid
     if (!valid_dtype(q_dtype) || !valid_dtype(w_dtype) || !valid_dtype(kv_dtype))
         return MP_ERR_INVALID_ARG;
     if (!q || !centre || !keys || !values || !out) return MP_ERR_INVALID_ARG;

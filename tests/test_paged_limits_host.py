@@ -29,3 +29,22 @@ def test_attention_refuses_more_than_it_numbers(L, kw):  # noqa: F811
     a.update(kw)
     assert L.mp_paged_attention(OK, 1, _cache(**HUGE), a["B"], a["Hq"], a["Hkv"], a["n"], 128, None, 0.0, OK,
                                 OK, 2 ** 62, None) == INVALID
+
+
+@pytest.mark.parametrize("B,Hq,Hkv", [(2048, 32, 8), (65536, 1, 1), (8192, 8, 8), (2 ** 28, 32, 8)])
+def test_sampled_decodes_refuse_more_query_rows_than_a_grid_has(L, B, Hq, Hkv):  # noqa: F811
+    """Before anything is launched: not by the last kernel's launch, behind the first ones."""
+    import lsh_sampled_sparse_gb300 as mp
+    from lsh_sampled_sparse_gb300.binding import _KV4
+    assert _decode(L, B=B, Hq=Hq, Hkv=Hkv) == INVALID
+    prm = ctypes.byref(mp.Params(0, 150, 4, 64, 0.0, 0, 100))
+    dims, end = (B, Hq, Hkv, 100, 128, prm, OK, OK, 2 ** 62, None), INVALID
+    kv4 = ctypes.byref(_KV4(0x10000, 0x10000, 0x10000, 100))
+    assert L.mp_decode_attention(OK, 1, OK, OK, OK, 1, OK, OK, 1, *dims) == end
+    assert L.mp_sampled_attention(OK, 1, OK, OK, OK, OK, 1, *dims) == end
+    assert L.mp_sampled_attention_buckets(OK, 1, OK, OK, OK, OK, OK, 1, *dims) == end
+    assert L.mp_kv4_decode_attention(OK, 1, OK, OK, OK, 1, kv4, *dims) == end
+    assert L.mp_kv4_sampled_attention(OK, 1, OK, OK, kv4, *dims) == end
+    # as many as there are places is not what is wrong
+    small = (1, 4, 1, 100, 128, prm, OK, OK, 16, None)
+    assert L.mp_decode_attention(OK, 1, OK, OK, OK, 1, OK, OK, 1, *small) == 5          # the workspace
