@@ -86,9 +86,9 @@ bool fill_shape(int B, int Hq, int Hkv, int n, int d, const mp_params* prm, Deco
     s->C = prm->K * prm->L;
     s->qwords = cp ? (prm->L + 3) / 4 : (s->C + 31) / 32;   // bits, or code bytes
     s->cpad = (s->C + 3) & ~3;
-    s->nblk = (n + kKeysPerBlock - 1) / kKeysPerBlock;
+    s->nblk = key_blocks(n);
     s->ncap = prm->n_capacity > 0 ? prm->n_capacity : n;
-    s->cblk = (s->ncap + kKeysPerBlock - 1) / kKeysPerBlock;
+    s->cblk = key_blocks(s->ncap);
     s->n_indexed = prm->n_indexed > 0 ? prm->n_indexed : n;
     s->radius = prm->radius;
     s->cp = cp;
@@ -305,7 +305,7 @@ mp_status mp_encode_keys(const void* keys, mp_dtype key_dtype, const float* cent
                                               n_begin, n_capacity, n_begin, n_end, K, L, codes,
                                               stream));
     const int blk0 = n_begin / kKeysPerBlock;
-    const int blk1 = (n_end + kKeysPerBlock - 1) / kKeysPerBlock;
+    const int blk1 = key_blocks(n_end);
     if (kbf && wbf) {
         const cudaError_t e = launch_encode_tc(keys, centre, W, B, Hkv, n_capacity, blk0, blk1,
                                                K, L, codes, device_status_ptr(), stream);
@@ -332,7 +332,7 @@ mp_status mp_encode_rows(const void* keys, mp_dtype key_dtype, const float* cent
         return MP_ERR_INVALID_ARG;
     if (!ensure_prepared()) return MP_ERR_CUDA;
     const bool kbf = key_dtype == MP_BF16, wbf = w_dtype == MP_BF16;
-    const int cblk = (n_capacity + kKeysPerBlock - 1) / kKeysPerBlock;
+    const int cblk = key_blocks(n_capacity);
     for (int row = 0; row < m;) {
         const int pos = n_begin + row, at = pos % kKeysPerBlock;
         // whole blocks, or part of one, whose other keys' bits are kept
@@ -419,7 +419,7 @@ mp_status mp_encode_keys_mips(const void* keys, mp_dtype key_dtype, const float*
         n_end - n_begin > kAppendMaxKeys) {
         // whole blocks on the tensor cores: the norms of every key of those blocks first
         const int blk0 = n_begin / kKeysPerBlock;
-        const int blk1 = (n_end + kKeysPerBlock - 1) / kKeysPerBlock;
+        const int blk1 = key_blocks(n_end);
         cudaError_t e = launch_key_radius(keys, true, centre, B * Hkv, n_capacity, n_end, nullptr,
                                           stream, norms_scratch, blk0 * kKeysPerBlock,
                                           std::min(blk1 * kKeysPerBlock, n_capacity));
@@ -460,7 +460,7 @@ mp_status mp_encode_keys_cp(const void* keys, mp_dtype key_dtype, const float* c
     if (key_dtype == MP_BF16 && g_dtype == MP_BF16 && n_end - n_begin > kAppendMaxKeys) {
         // whole 1024-key blocks on the tensor cores (a table is d hyperplanes of the encoder)
         const int blk0 = n_begin / kKeysPerBlock;
-        const int blk1 = (n_end + kKeysPerBlock - 1) / kKeysPerBlock;
+        const int blk1 = key_blocks(n_end);
         const cudaError_t e = launch_encode_tc(keys, centre, G, B, Hkv, n_capacity, blk0, blk1, kD,
                                                L, reinterpret_cast<uint32_t*>(codes),
                                                device_status_ptr(), stream, nullptr, nullptr, true);
@@ -555,7 +555,7 @@ mp_status mp_build_buckets_cap(const uint32_t* codes, int B, int Hkv, int n_capa
     if (!buckets || (K > 0 && !codes)) return MP_ERR_INVALID_ARG;
     if ((codes && !aligned(codes, 16)) || !aligned(buckets, 4)) return MP_ERR_INVALID_ARG;
     if (!ensure_prepared()) return MP_ERR_CUDA;
-    const int cblk = (n_capacity + kKeysPerBlock - 1) / kKeysPerBlock;
+    const int cblk = key_blocks(n_capacity);
     return to_status(launch_bucket_build(codes, B, Hkv, cblk, n, K, L, buckets, stream));
 }
 

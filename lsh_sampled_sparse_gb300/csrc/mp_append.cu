@@ -275,7 +275,7 @@ cudaError_t launch_encode_append(const void* keys, bool keys_bf16, const float* 
     const int C = K * L;
     if (C == 0 || n1 <= n0) return cudaSuccess;
     if (n1 - n0 > kAppendMaxKeys) return cudaErrorInvalidValue;
-    const int cblk = (ncap + kKeysPerBlock - 1) / kKeysPerBlock;
+    const int cblk = key_blocks(ncap);
     const size_t smem = (static_cast<size_t>(kD) * kAppendPlanes +
                          static_cast<size_t>(n1 - n0) * kD) * sizeof(float);
     const dim3 grid((C + kAppendPlanes - 1) / kAppendPlanes, B * Hkv);
@@ -301,7 +301,7 @@ cudaError_t launch_encode_rows_at(const void* keys, bool keys_bf16, const float*
     a.m = m;
     a.ncap = ncap;
     a.C = C;
-    a.cblk = (ncap + kKeysPerBlock - 1) / kKeysPerBlock;
+    a.cblk = key_blocks(ncap);
     a.heads = std::max(1, kAtRows / m);
     a.wide = C % 4 == 0 && reinterpret_cast<uintptr_t>(W) % (w_bf16 ? 8 : 16) == 0;
     return launch_dependent(pick_at(keys_bf16, w_bf16),

@@ -452,7 +452,7 @@ int cluster_ranges(int nblk) {
 
 cudaError_t launch_bucket_build(const uint32_t* codes, int B, int Hkv, int cblk, int n, int K,
                                 int L, uint32_t* buckets, cudaStream_t st) {
-    const int nblk = (n + kKeysPerBlock - 1) / kKeysPerBlock;
+    const int nblk = key_blocks(n);
     const int R = cluster_ranges(nblk);
     const int rb = (nblk + R - 1) / R;
     const size_t csmem = cluster_build_smem(rb, K);

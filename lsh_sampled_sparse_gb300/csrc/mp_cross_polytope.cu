@@ -399,7 +399,7 @@ cudaError_t launch_encode_cp(const void* keys, bool keys_bf16, const float* cent
                              bool g_bf16, int B, int Hkv, int ncap, int n0, int n1, int L,
                              uint8_t* codes, cudaStream_t st) {
     if (n1 <= n0) return cudaSuccess;
-    const int cblk = (ncap + kKeysPerBlock - 1) / kKeysPerBlock;
+    const int cblk = key_blocks(ncap);
     const int tiles = (n1 - 1) / kCpKeys - n0 / kCpKeys + 1;
     const size_t smem = (static_cast<size_t>(kD) * kD + static_cast<size_t>(kCpKeys) * (kD + 1)) *
                         sizeof(float);

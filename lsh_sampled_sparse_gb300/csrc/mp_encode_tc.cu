@@ -727,7 +727,7 @@ cudaError_t launch_encode_tc(const void* keys, const float* centre, const void* 
     a.n = ncap;
     a.lo = lo;
     a.blk0 = blk0;
-    a.cblk = cblk ? cblk : (ncap + kKeysPerBlock - 1) / kKeysPerBlock;
+    a.cblk = cblk ? cblk : key_blocks(ncap);
     a.code_blk = code_blk;
     a.norms = norms;
     a.radius = radius;

@@ -11,6 +11,8 @@
 namespace mp {
 
 constexpr int kKeysPerBlock = MP_KEYS_PER_BLOCK;   // keys per bit-sliced code block
+// Blocks that hold n keys, n >= 1 (not (n + 1023) / 1024: a capacity may be 2^31 - 1)
+__host__ __device__ constexpr int key_blocks(int n) { return (n - 1) / kKeysPerBlock + 1; }
 constexpr int kWordsPerBlock = kKeysPerBlock / 32;  // uint32 words per plane row
 constexpr int kD = 128;                             // the only head dimension supported
 constexpr int kAttendBlockGroup = 4;                // 1024-key blocks per attend CTA

@@ -169,7 +169,7 @@ cudaError_t launch_encode_mips(const void* keys, bool keys_bf16, const float* ce
                                cudaStream_t st) {
     const int C = K * L;
     if (C == 0 || n1 <= n0) return cudaSuccess;
-    const int cblk = (ncap + kKeysPerBlock - 1) / kKeysPerBlock;
+    const int cblk = key_blocks(ncap);
     const int tiles = (n1 - 1) / kMipsKeys - n0 / kMipsKeys + 1;
     const dim3 grid(tiles, B * Hkv);
     encode_mips_kernel<<<grid, kMipsKeys, 0, st>>>(keys, keys_bf16, centre, W, w_bf16, radius,

@@ -301,7 +301,7 @@ cudaError_t launch_encode_simt(const void* keys, bool keys_bf16, const float* ce
     const int C = K * L;
     if (C == 0 || blk1 <= blk0) return cudaSuccess;
     if (head_rows == 0) head_rows = ncap;
-    if (cblk == 0) cblk = (ncap + kKeysPerBlock - 1) / kKeysPerBlock;
+    if (cblk == 0) cblk = key_blocks(ncap);
     encode_simt_kernel<<<simt_grid(blk1 - blk0, B * Hkv, C), kSimtKeys, 0, st>>>(
         keys, keys_bf16, centre, W, w_bf16, 0, ncap, head_rows, 0, false, C, cblk, blk0, code_blk,
         codes, device_status_ptr());
@@ -315,7 +315,7 @@ cudaError_t launch_encode_part(const void* keys, bool keys_bf16, const float* ce
     const int C = K * L, blk0 = n0 / kKeysPerBlock;
     if (C == 0 || n1 <= n0) return cudaSuccess;
     if ((n1 - 1) / kKeysPerBlock != blk0) return cudaErrorInvalidValue;
-    const int cblk = (ncap + kKeysPerBlock - 1) / kKeysPerBlock;
+    const int cblk = key_blocks(ncap);
     encode_simt_kernel<<<simt_grid(1, B * Hkv, C), kSimtKeys, 0, st>>>(
         keys, keys_bf16, centre, W, w_bf16, n0, n1, head_rows, n0 - row0, true, C, cblk, blk0, 0,
         codes, device_status_ptr());
@@ -340,7 +340,7 @@ cudaError_t launch_collision_counts(const uint32_t* codes, const uint32_t* qbits
 
 cudaError_t launch_codes_unpack(const uint32_t* codes, int BH, int n, int K, int L,
                                 uint32_t* out, cudaStream_t st) {
-    const int nblk = (n + kKeysPerBlock - 1) / kKeysPerBlock;
+    const int nblk = key_blocks(n);
     const dim3 grid((n + 255) / 256, BH);
     codes_unpack_kernel<<<grid, 256, 0, st>>>(codes, n, nblk, K, L, out);
     return cudaGetLastError();

@@ -29,3 +29,66 @@ def test_many_units_of_one_tile(mp, dtype, G):
     for _ in range(20):
         assert torch.equal(mp.paged_attention(q, cache, table, n=n, lengths=_ints(lens)), first)
     assert mp.device_status() == 0
+
+
+def test_codes_laid_out_for_the_largest_capacity(mp):
+    """2^31 - 1 tokens a head: the codes' stride is that of 2^21 blocks, and places near the end are there."""
+    Hkv, m, cap, K, L = 3, 64, 2 ** 31 - 1, 1, 1
+    g = _gen(31)
+    keys = _randn(g, 1, Hkv, m, 128)
+    W, centre = _randn(g, 128, K * L), _randn(g, 1, Hkv, 128) * 0.1
+    codes = torch.zeros(Hkv, 2 ** 21, 32, dtype=torch.int32, device="cuda")
+    assert codes.numel() * 4 == mp.codes_bytes(1, Hkv, cap, K, L)
+    for pos, left in ((1024 * 3 + 5, m), (cap - 40, 40), (1024 * 2 ** 20 - 17, m)):
+        codes.zero_()
+        mp.encode_rows_at(keys, centre, W, K, L, _ints([pos]), cap, codes)
+        at = pos % 1024
+        want = mp.encode_rows_at(keys[:, :, :left].contiguous(), centre, W, K, L, _ints([at]), 2048,
+                                 torch.zeros(Hkv, 2, 32, dtype=torch.int32, device="cuda"))
+        first = pos // 1024
+        for h in range(Hkv):
+            nonzero = codes[h].any(-1).nonzero().flatten().tolist()
+            assert nonzero and all(first <= b <= first + 1 for b in nonzero)
+            assert torch.equal(codes[h, first:first + 2], want[h, :min(2, 2 ** 21 - first)])
+
+
+def test_sampled_decode_with_codes_of_the_largest_capacity(mp):
+    B, Hq, Hkv, n, page, K, L = 1, 4, 2, 3000, 16, 2, 3
+    g = _gen(32)
+    cache, table = _random_cache(mp, g, B, Hkv, n, page, BF, [n])
+    keys = _randn(g, B, Hkv, n, 128).to(BF)
+    W, centre = _randn(g, 128, K * L).to(BF), _randn(g, B, Hkv, 128) * 0.1
+    q = _randn(g, B, Hq, 128).to(BF)
+    near = mp.encode_rows(keys, centre, W, K, L, 0, n)
+    want = mp.paged_decode_attention(q, near, centre, W, cache, table, K, L, 4, 64, n=n, n_capacity=n)
+    far = torch.zeros(Hkv, 2 ** 21, K * L * 32, dtype=torch.int32, device="cuda")
+    far[:, :3] = near.view(torch.int32).view(Hkv, 3, -1)
+    assert torch.equal(mp.paged_decode_attention(q, far, centre, W, cache, table, K, L, 4, 64, n=n,
+                                                 n_capacity=2 ** 31 - 1), want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_sampled_decode_of_the_most_rows(mp, dtype):
+    """65520 query rows of 65535: every row is that of a batch of its own."""
+    B, Hq, Hkv, n, page, K, L = 4095, 16, 2, 72, 8, 2, 20
+    g = _gen(33)
+    lens = [b % (n + 1) for b in range(B)]
+    slots = n // page
+    cache = mp.paged_cache(64, Hkv, page, dtype)
+    for t in cache:
+        t.copy_(_randn(g, *t.shape))
+    table = torch.randint(0, 64, (B, slots), generator=g, device="cuda").int()
+    W, centre = _randn(g, 128, K * L).to(dtype), _randn(g, B, Hkv, 128) * 0.1
+    q = _randn(g, B, Hq, 128).to(dtype)
+    rows = cache.keys[table.long()].transpose(1, 2).reshape(B, Hkv, n, 128)
+    codes = mp.encode_rows(rows.contiguous(), centre, W, K, L, 0, n)
+    out = mp.paged_decode_attention(q, codes, centre, W, cache, table, K, L, 2, 9, n=n, lengths=_ints(lens),
+                                    n_capacity=n)
+    per = codes.view(torch.int32).view(B, -1)
+    for b in (0, 1, 5, 72, 2047, 2048, 4000, 4094):
+        own = mp.paged_decode_attention(q[b:b + 1], per[b], centre[b:b + 1], W, cache, table[b:b + 1], K, L, 2,
+                                        9, n=n, lengths=_ints(lens[b:b + 1]), n_capacity=n)
+        # (a single sequence's rows are shared by clusters: sums of the same keys in another order)
+        assert (out[b] - own[0]).abs().max() <= 2e-5
+        assert lens[b] > 0 or (out[b] == 0).all()
+    assert torch.isfinite(out).all()

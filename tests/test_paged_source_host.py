@@ -80,3 +80,31 @@ def test_no_warp_writes_the_sums_while_another_may_read_the_last_ones(units):
             assert since > 0, (units, last, kind)
         last, since = kind, 0
     assert writes == len(units)
+
+
+def test_no_capacity_is_rounded_up_in_32_bits():
+    """A capacity may be 2^31 - 1: n + 1023 wraps there, and the blocks a head has would be negative."""
+    found = []
+    for name in sorted(os.listdir(CSRC)):
+        with open(os.path.join(CSRC, name)) as f:
+            code = re.sub(r"//[^\n]*", "", f.read())
+        found += [(name, m.group(0)) for m in
+                  re.finditer(r"[^\n;(]*\S+ \+ kKeysPerBlock - 1\) / kKeysPerBlock", code)
+                  if "static_cast<size_t>" not in m.group(0) and not m.group(0).startswith("n) +")]
+    assert not found
+
+
+def test_blocks_of_the_largest_capacities(tmp_path):
+    """The product's own count, compiled for the host."""
+    import subprocess
+    from lsh_sampled_sparse_gb300.build import NVCC_FLAGS, nvcc
+    src = tmp_path / "blocks.cu"
+    src.write_text('#include <cstdio>\n#include "mp_internal.cuh"\nint main() {\n'
+                   "    for (int n : {1, 2, 1023, 1024, 1025, 1 << 30, 2147483647 - 1024, 2147483647 - 1023,\n"
+                   "                  2147483647 - 1022, 2147483647})\n"
+                   '        printf("%d %d\\n", n, mp::key_blocks(n));\n}\n')
+    exe = tmp_path / "blocks"
+    subprocess.run([nvcc(), *NVCC_FLAGS, str(src), "-o", str(exe)], check=True)
+    rows = [tuple(map(int, line.split())) for line in
+            subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.splitlines()]
+    assert len(rows) == 10 and all(b == -(-n // 1024) for n, b in rows)
