@@ -20,6 +20,7 @@ std::mutex g_mutex;
 int* g_status_ptr[kMaxDevices] = {};
 int g_sm_count[kMaxDevices] = {};
 bool g_prepared[kMaxDevices] = {};
+bool g_paged[kMaxDevices] = {};
 
 int current_device() {
     int dev = -1;
@@ -43,14 +44,27 @@ bool ensure_prepared() {
     if (prepare_misc() != cudaSuccess || prepare_decode() != cudaSuccess ||
         prepare_buckets() != cudaSuccess || prepare_append() != cudaSuccess ||
         prepare_mips() != cudaSuccess || prepare_cross_polytope() != cudaSuccess ||
-        prepare_kv4() != cudaSuccess || prepare_paged() != cudaSuccess)
+        prepare_kv4() != cudaSuccess)
         return false;
     prepare_encode_tc();   // failure only disables the tensor-core encoder
+    g_paged[dev] = prepare_paged() == cudaSuccess;   // and here the append and the exact attention over pages
     cudaGetLastError();
     g_status_ptr[dev] = static_cast<int*>(p);
     g_sm_count[dev] = sms;
     g_prepared[dev] = true;
     return true;
+}
+
+// ... and what those two calls need, tried again by each where it failed
+bool ensure_paged() {
+    if (!ensure_prepared()) return false;
+    const int dev = current_device();
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (!g_paged[dev]) {
+        g_paged[dev] = prepare_paged() == cudaSuccess;
+        cudaGetLastError();
+    }
+    return g_paged[dev];
 }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -790,7 +804,7 @@ mp_status mp_paged_append(const mp_rows* keys, const mp_rows* values, const mp_r
     const long long heads = (q ? Hq : 0) + 2ll * Hkv;
     if (heads > 1 << 18 || static_cast<long long>(B) * m > 0x7fffffffll / heads)   // a grid's rows
         return MP_ERR_INVALID_ARG;
-    if (!ensure_prepared()) return MP_ERR_CUDA;
+    if (!ensure_paged()) return MP_ERR_CUDA;
     return to_status(launch_paged_append(*keys, *values, q, rows_dtype == MP_BF16, inv_freq,
                                          rotary_dims, interleaved != 0, B, Hq, Hkv, m, n_begin,
                                          positions, counts, *cache, q_out, keys_out, stream));
@@ -817,7 +831,7 @@ mp_status mp_paged_attention(const void* q, mp_dtype q_dtype, const mp_paged* ca
         !aligned(lengths, 4) || !workspace || !aligned(workspace, 256))
         return MP_ERR_INVALID_ARG;
     if (ws_bytes < mp_paged_attention_workspace_bytes(B, Hq, Hkv, n, d)) return MP_ERR_WORKSPACE;
-    if (!ensure_prepared()) return MP_ERR_CUDA;
+    if (!ensure_paged()) return MP_ERR_CUDA;
     return to_status(launch_paged_attention(
         q, q_dtype == MP_BF16, *cache, B, Hq, Hkv, n, lengths,
         scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(d)), out, workspace, stream));
