@@ -27,6 +27,7 @@ static_assert(kAThreads == kD && 4 * 32 == kD,
               "the attend merge: a thread per output dim; a merging lane holds 4 dims");
 constexpr int kRingDepth = 5;                       // tables in flight per warp in the async scan
 constexpr int kRingMinK = 8, kRingMaxK = 11;        // K range the async scan handles
+constexpr float kLowest = -3.402823466e38f;         // of all numbers: no logit is below it
 constexpr int kLuIntervals = kLogUTableIntervals;   // log u tables: cosine grid intervals
 
 // ------------------------------------------------------------------------------------------------
@@ -1061,7 +1062,7 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
 #pragma unroll
         for (int sh = 8; sh; sh >>= 1) bm = fmaxf(bm, __shfl_xor_sync(hmask, bm, sh));
         float mn = fmaxf(m, bm);
-        if (kPaged && mn == -INFINITY) mn = -3.0e38f;          // none of the rows has a page yet
+        if (kPaged && mn == -INFINITY) mn = kLowest;           // none of the rows has a page yet
         const float corr = __expf(m - mn);
         const float wgt = jl < cnt ? __expf(logit - mn) : 0.0f;
         float ws = (hl % LPR) ? 0.0f : wgt;                    // each row counted once

@@ -92,3 +92,23 @@ def test_sampled_decode_of_the_most_rows(mp, dtype):
         assert (out[b] - own[0]).abs().max() <= 2e-5
         assert lens[b] > 0 or (out[b] == 0).all()
     assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("sink", [0, 96])
+def test_sampled_decode_of_the_lowest_logits_behind_a_missing_page(mp, dtype, sink):
+    """Logits of -3.2e38 behind a page that is not there: what stands for its tokens is no higher. The keys are
+    one and the same row, so that all weights are 1, and the output is the mean of the values."""
+    n, page = 96, 32
+    g = _gen(34)
+    q = torch.full((1, 1, 128), -1.0, device="cuda").to(dtype)
+    cache = mp.paged_cache(3, 1, page, dtype)
+    cache.keys.fill_(2.5)                        # q.k = -320, exactly
+    cache.values.copy_(_randn(g, *cache.values.shape))
+    table = _ints([[-1, 0, 2]])
+    W, centre = _randn(g, 128, 2), torch.zeros(1, 1, 128, device="cuda")
+    codes = torch.zeros(4, dtype=torch.int32, device="cuda")             # K = 0: every key is sampled, log u = 0
+    out = mp.paged_decode_attention(q, codes, centre, W, cache, table, 0, 2, sink, 0, scale=1e36)
+    v = torch.cat([cache.values[0, 0], cache.values[2, 0]]).double()
+    # sums of 64 values, each step rounded: 64 half steps of the largest sum at most, and the division
+    assert (out[0, 0].double() - v.mean(0)).abs().max() <= 2.0 ** -24 * 66 * v.abs().max()
