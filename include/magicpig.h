@@ -526,8 +526,9 @@ MP_API size_t mp_paged_attention_workspace_bytes(int B, int Hq, int Hkv, int n, 
  * query, or in a key or value attended to, may give NaN in the rows that it meets, and so may an element
  * past the largest bf16 or tf32 where it is split.
  * Errors: MP_ERR_INVALID_ARG (shapes, n > n_slots page_size or 2^30, B Hq > 2^22, B Hq n > 2^35, Hq %
- * Hkv, a scale that is negative, infinite or NaN, null, misalignment: out 16 bytes, lengths 4, workspace 256),
- * MP_ERR_UNSUPPORTED (d != 128, page_size not a multiple of 8), MP_ERR_WORKSPACE. */
+ * Hkv, a scale that is negative, NaN, or infinite in float32 once multiplied by log2 e, null, misalignment:
+ * out 16 bytes, lengths 4, workspace 256), MP_ERR_UNSUPPORTED (d != 128, page_size not a multiple of 8),
+ * MP_ERR_WORKSPACE. */
 MP_API mp_status mp_paged_attention(const void* q, mp_dtype q_dtype, const mp_paged* cache, int B,
                                     int Hq, int Hkv, int n, int d, const int32_t* lengths,
                                     float scale, float* out, void* workspace, size_t ws_bytes,
@@ -540,7 +541,7 @@ MP_API mp_status mp_paged_attention(const void* q, mp_dtype q_dtype, const mp_pa
  * the keys that mp_paged_append returns). A token without a page is left out, of T too. log u of the
  * SimHash codes is evaluated for each sampled key. Workspace: mp_decode_workspace_bytes.
  * Errors: those of mp_decode_attention, and MP_ERR_INVALID_ARG (the cache, lengths, n > n_slots
- * page_size or 2^30), MP_ERR_UNSUPPORTED (page_size not a multiple of 8). */
+ * page_size or 2^30, an infinite scale), MP_ERR_UNSUPPORTED (page_size not a multiple of 8). */
 MP_API mp_status mp_paged_decode_attention(const void* q, mp_dtype q_dtype, const uint32_t* codes,
                                            const float* centre, const void* W, mp_dtype w_dtype,
                                            const mp_paged* cache, int B, int Hq, int Hkv, int n, int d,

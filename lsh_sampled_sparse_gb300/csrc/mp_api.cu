@@ -822,8 +822,9 @@ mp_status mp_paged_attention(const void* q, mp_dtype q_dtype, const mp_paged* ca
     if (d != kD) return MP_ERR_UNSUPPORTED;
     const mp_status st = check_paged(cache, Hkv);
     if (st != MP_OK) return st;
+    // (the kernels take scale log2 e)
     if (n > static_cast<long long>(cache->n_slots) * cache->page_size || !(scale >= 0.0f) ||
-        isinf(scale))
+        isinf(scale * kLog2E))
         return MP_ERR_INVALID_ARG;
     // the tiles of all units are numbered in 32 bits
     if (static_cast<long long>(B) * Hq * n > 1ll << 35) return MP_ERR_INVALID_ARG;
@@ -851,7 +852,8 @@ mp_status mp_paged_decode_attention(const void* q, mp_dtype q_dtype, const uint3
                                       cache->values, cache->dtype, B, Hq, Hkv, n, d, prm, out,
                                       workspace, ws_bytes, false, &s);
     if (st != MP_OK) return st;
-    if (n > static_cast<long long>(cache->n_slots) * cache->page_size) return MP_ERR_INVALID_ARG;
+    if (n > static_cast<long long>(cache->n_slots) * cache->page_size || isinf(prm->scale))
+        return MP_ERR_INVALID_ARG;
     if (!ensure_prepared()) return MP_ERR_CUDA;
     const PageRef pages{cache->page_table, lengths, cache->n_pages, cache->page_size, cache->n_slots,
                         cache->table_stride};

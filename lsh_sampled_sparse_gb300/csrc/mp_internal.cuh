@@ -250,6 +250,7 @@ cudaError_t launch_paged_append(const mp_rows& keys, const mp_rows& values, cons
                                 bool interleaved, int B, int Hq, int Hkv, int m, int n_begin,
                                 const int32_t* positions, const int32_t* counts,
                                 const mp_paged& cache, void* q_out, void* keys_out, cudaStream_t st);
+constexpr float kLog2E = 1.4426950408889634f;    // the kernels' weights are powers of two
 size_t paged_attention_scratch_bytes(int Hq, int Hkv);
 cudaError_t launch_paged_attention(const void* q, bool q_bf16, const mp_paged& cache, int B, int Hq,
                                    int Hkv, int n, const int32_t* lengths, float scale, float* out,

@@ -701,7 +701,7 @@ cudaError_t launch_paged_attention(const void* q, bool q_bf16, const mp_paged& c
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     a.cluster = cluster_size(units, tiles, a.ctas, a.tile_shift, lengths != nullptr, g_clusters[dev][simt ? 0 : 1]);
-    a.scale = scale * 1.4426950408889634f;
+    a.scale = scale * kLog2E;
     a.status = device_status_ptr();
     a.part = static_cast<float*>(workspace);
     a.begin = reinterpret_cast<int4*>(a.part + static_cast<size_t>(a.ctas) * 2 * a.nh * kPart);

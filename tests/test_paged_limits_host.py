@@ -48,3 +48,16 @@ def test_sampled_decodes_refuse_more_query_rows_than_a_grid_has(L, B, Hq, Hkv): 
     # as many as there are places is not what is wrong
     small = (1, 4, 1, 100, 128, prm, OK, OK, 16, None)
     assert L.mp_decode_attention(OK, 1, OK, OK, OK, 1, OK, OK, 1, *small) == 5          # the workspace
+
+
+def test_scales_that_make_no_number_are_refused(L):  # noqa: F811
+    """The exact attention's kernels take the scale times log2 e, which has to be finite too: every score would
+    be an infinity or NaN."""
+    def att(scale, size=2 ** 62):
+        return L.mp_paged_attention(OK, 1, _cache(), 1, 4, 1, 100, 128, None, scale, OK, OK, size, None)
+
+    for scale in (3.0e38, 2.36e38, float("inf"), float("nan"), -1e-30):
+        assert att(scale) == INVALID
+    assert att(2.35e38, 16) == 5                 # refused for its workspace
+    for scale in (float("inf"), float("nan"), -1.0):
+        assert _decode(L, scale=scale) == INVALID
