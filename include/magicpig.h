@@ -495,9 +495,9 @@ typedef struct {
  * (x cos a - y sin a, y cos a + x sin a), a = p inv_freq[j] (float32 on the device, rotary_dims / 2
  * of them), in float32, rounded once to the type it is stored in. Pairs are dims (j, j + rotary_dims /
  * 2), or with interleaved != 0 dims (2 j, 2 j + 1). The angle is reduced in 64-bit fixed point: it is
- * off by less than 2^-61 |p| (1 + |inv_freq[j]|) + 2^-22 radians at any position. inv_freq NULL
- * (rotary_dims then ignored) turns nothing. An inv_freq that is infinite or NaN has unspecified
- * results.
+ * off by less than 2^-61 |p| (1 + |inv_freq[j]|) + 2^-25 radians at any position (2^-23 where rows and
+ * cache are both bf16). inv_freq NULL (rotary_dims then ignored) turns nothing. An inv_freq that is
+ * infinite or NaN has unspecified results.
  * Errors: MP_ERR_INVALID_ARG (shapes, m < 0, Hq + 2 Hkv > 2^18, B m (Hq + 2 Hkv) > 2^31 - 1, n_begin
  * < 0 or n_begin + m > n_slots page_size without positions, null, misalignment: rows, outputs 16
  * bytes, others 4),

@@ -112,3 +112,28 @@ def test_sampled_decode_of_the_lowest_logits_behind_a_missing_page(mp, dtype, si
     v = torch.cat([cache.values[0, 0], cache.values[2, 0]]).double()
     # sums of 64 values, each step rounded: 64 half steps of the largest sum at most, and the division
     assert (out[0, 0].double() - v.mean(0)).abs().max() <= 2.0 ** -24 * 66 * v.abs().max()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_cosines_and_sines_of_all_quarters_of_a_turn(mp, interleaved):
+    """A pair (1, 0) becomes (cos, sin) exactly, so that these show by themselves: off by what the header gives
+    for the angle, and by a unit in the last place of each (at most 2^-23 of it)."""
+    starts = [0, 1, 2, 3, 5, 97, 1000, 4095, 65537, 2 ** 20 - 3, -1, -4, -70001]
+    B, m, r = len(starts), 64, 128
+    x = torch.zeros(B, 1, m, 128, device="cuda")
+    first, second = (slice(0, r, 2), slice(1, r, 2)) if interleaved else (slice(0, 64), slice(64, 128))
+    x[..., first] = 1.0
+    # every eighth of a turn among the angles at position 1, the quarters and their neighbours too
+    freq = (torch.arange(64, device="cuda").double() / 32 * torch.pi).float()
+    table, cache = torch.full((B, 1), -1, dtype=torch.int32, device="cuda"), mp.paged_cache(1, 1, 8, F32)
+    out = torch.empty_like(x)
+    mp.paged_append(cache, table, x, x, positions=_ints(starts), inv_freq=freq, interleaved=interleaved,
+                    keys_out=out)
+    p = torch.tensor(starts, device="cuda").double()[:, None] + torch.arange(m, device="cuda")
+    a = (p[..., None] * freq.double())[:, None]
+    # 2^-52 of the angle twice: the reference's product and its own reduction
+    angle = 2.0 ** -25 + (2.0 ** -61 * (1 + freq.double()) * p[..., None].abs())[:, None] + 2.0 ** -51 * a.abs()
+    for got, want in ((out[..., first], a.cos()), (out[..., second], a.sin())):
+        off = (got.double() - want).abs() - angle - 2.0 ** -23 * want.abs()
+        assert (off <= 0).all(), off.max().item()
+    assert (out[0, 0, 0, first] == 1).all() and (out[0, 0, 0, second] == 0).all()        # position 0
