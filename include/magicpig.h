@@ -647,8 +647,9 @@ MP_API mp_status mp_device_status(int* status);
  * table's keys, 8 bucket member beyond n_indexed, 9 code words written by the encoders, 10 a row of
  * the 4-bit cache, 11 rows read back from it, partial states and output rows of its attention, 12 a
  * key row that a CUDA-core encoder reads, 13 the list of an attend CTA's selected keys, 14 a row of the
- * paged cache, 15 rows returned by an append to it and output rows of its attention. Neither word is
- * reset. Errors: MP_ERR_INVALID_ARG (null), MP_ERR_CUDA. */
+ * paged cache or a slot of its page table (the boxes that the bf16 attention copies by TMA are checked
+ * by that unit, against the pool), 15 rows returned by an append to it, and of its attention output
+ * rows, partial states and what says where they begin, against the workspace's size. Neither word is reset. Errors: MP_ERR_INVALID_ARG (null), MP_ERR_CUDA. */
 MP_API mp_status mp_debug_check_report(int* enabled, int* site);
 
 #ifdef __cplusplus

@@ -835,7 +835,7 @@ mp_status mp_paged_attention(const void* q, mp_dtype q_dtype, const mp_paged* ca
     if (!ensure_paged()) return MP_ERR_CUDA;
     return to_status(launch_paged_attention(
         q, q_dtype == MP_BF16, *cache, B, Hq, Hkv, n, lengths,
-        scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(d)), out, workspace, stream));
+        scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(d)), out, workspace, ws_bytes, stream));
 }
 
 mp_status mp_paged_decode_attention(const void* q, mp_dtype q_dtype, const uint32_t* codes,

@@ -194,6 +194,9 @@ __global__ void __launch_bounds__(kAtThreads) encode_rows_at_kernel(const AtArgs
 #pragma unroll
         for (int r = 0; r < kAtRows; ++r) {
             const int at = r0 + min(r, rows - 1);
+            if (!mp_check(a.status, static_cast<long long>(bh0) * a.m + at, static_cast<long long>(a.BH) * a.m,
+                          kSiteEncodeRow))
+                continue;
             k[r] = static_cast<const T*>(a.keys)[(static_cast<size_t>(bh0) * a.m + at) * kD + tid];
             mu[r] = a.centre[static_cast<size_t>(bh0 + at / a.m) * kD + tid];
         }
@@ -202,8 +205,7 @@ __global__ void __launch_bounds__(kAtThreads) encode_rows_at_kernel(const AtArgs
             const int r = r0 + min(tid, rows - 1), bh = bh0 + r / a.m;
             const long long p = static_cast<long long>(a.positions[bh / a.Hkv]) + r % a.m;
             const int blk = static_cast<int>(p >> 10);
-            const bool there = tid < rows && p >= 0 && p < a.ncap &&
-                               mp_check(a.status, blk, a.cblk, kSiteEncodeCodes);
+            const bool there = tid < rows && p >= 0 && p < a.ncap;
             word_of[tid] = there ? (static_cast<long long>(bh) * a.cblk + blk) * a.C * kWordsPerBlock +
                                        (static_cast<int>(p) & (kKeysPerBlock - 1)) / 32
                                  : -1;
@@ -252,6 +254,9 @@ __global__ void __launch_bounds__(kAtThreads) encode_rows_at_kernel(const AtArgs
             if (side[u][tid]) set |= bit;
             else clear |= bit;
             if (w != word_of[u + 1]) {
+                if (!mp_check(a.status, w + static_cast<long long>(j) * kWordsPerBlock,
+                              static_cast<long long>(a.BH) * a.cblk * a.C * kWordsPerBlock, kSiteEncodeCodes))
+                    set = clear = 0u;
                 if (set) atomicOr(mine + w, set);
                 if (clear) atomicAnd(mine + w, ~clear);
                 set = clear = 0u;

@@ -825,7 +825,8 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
     const int slot0 = kPaged ? blk0 * kKeysPerBlock / a.pages.page_size : 0;
     if (kPaged && !exact) {
         const int last = min(n, (blk0 + kAttendBlocks) * kKeysPerBlock) - 1;
-        for (int i = tid; slot0 + i <= last / a.pages.page_size; i += kAThreads) pslot[i] = slots[slot0 + i];
+        for (int i = tid; slot0 + i <= last / a.pages.page_size; i += kAThreads)
+            pslot[i] = mp_check(a.status, slot0 + i, a.pages.n_slots, kSitePagedRow) ? slots[slot0 + i] : -1;
     }
     // (paged: T's rows are inputs of the call, too, and folded before the wait)
     const bool early = kPaged && exact;
@@ -1120,9 +1121,14 @@ __global__ void __launch_bounds__(kAThreads, 6) attend_kernel(const AArgs a) {
     // with the rows shared by a cluster)
     int base = 0;                                // of the window
     auto list_window = [&]() {
-        for (int i = tid; i < min(nsel - base, kRowKeys); i += kAThreads)
-            rowkey[i] = kPaged ? static_cast<int>(paged_row(a.pages, slots, key_of(base + i), a.Hkv, h / a.G))
-                               : key_of(i);
+        for (int i = tid; i < min(nsel - base, kRowKeys); i += kAThreads) {
+            const int key = key_of(kPaged ? base + i : i);
+            if constexpr (kPaged)
+                rowkey[i] = mp_check(a.status, key, n, kSitePagedRow)
+                                ? static_cast<int>(paged_row(a.pages, slots, key, a.Hkv, h / a.G)) : -1;
+            else
+                rowkey[i] = key;
+        }
     };
     if constexpr (KV != kKv4) {
         if (!kPaged || exact) {

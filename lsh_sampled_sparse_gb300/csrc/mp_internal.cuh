@@ -48,7 +48,7 @@ enum CheckSite : int {
     kSiteKv4Out = 11,            // rows read back, partial states or output rows of its attention
     kSiteEncodeRow = 12,         // a key row that a CUDA-core encoder reads
     kSiteAttendList = 13,        // the list of selected keys of an attend CTA (shared memory)
-    kSitePagedRow = 14,          // a row of the paged cache written, read or copied
+    kSitePagedRow = 14,          // a row of the paged cache, a slot of the table (TMA checks its boxes itself)
     kSitePagedOut = 15,          // rows returned by an append, partial states, output rows
 };
 
@@ -254,7 +254,7 @@ constexpr float kLog2E = 1.4426950408889634f;    // the kernels' weights are pow
 size_t paged_attention_scratch_bytes(int Hq, int Hkv);
 cudaError_t launch_paged_attention(const void* q, bool q_bf16, const mp_paged& cache, int B, int Hq,
                                    int Hkv, int n, const int32_t* lengths, float scale, float* out,
-                                   void* workspace, cudaStream_t st);
+                                   void* workspace, size_t ws_bytes, cudaStream_t st);
 
 // ---- cross-polytope variant (mp_cross_polytope.cu) ----------------------------------------------
 size_t cp_codes_bytes(int B, int Hkv, int n, int L);

@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attention_simt_kernel(c
     auto entry = [&]() {
         const int tok = (ahead.t + ahead_k) * kSimtTile + 4 * warp;
         return ahead.left > 0 && tok < ahead.len
-                   ? a.pages.table[static_cast<long long>(ahead.b) * a.pages.stride + slot_of(a, tok)]
+                   ? page_in(a, a.pages.table + static_cast<long long>(ahead.b) * a.pages.stride, slot_of(a, tok))
                    : -1;
     };
     int page = entry();
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_attention_simt_kernel(c
                 if (mp_check(a.status, static_cast<long long>(row0 + h),
                              static_cast<long long>(a.B) * a.Hq, kSitePagedOut))
                     a.out[(row0 + h) * kD + e] = over_sum(O, L);
-            } else {
+            } else if (part_there(a, blockIdx.x, w.t == 0, h)) {
                 float* p = part_of(a, w.t == 0, h);
                 p[e] = O;
                 if (e == 0) {
@@ -526,6 +526,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const PArgs
     __shared__ __align__(16) float join[kJoinWarps][kPart];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x + 1;
     wait_for_predecessor();
+    if (!begin_there(a, c) || !begin_there(a, a.ctas)) return;
     const int total = __ldcg(&a.begin[a.ctas].x);
     const int4 at = __ldcg(a.begin + c);         // b, unit, t, tiles
     const Shares share(a, total);
@@ -545,7 +546,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const PArgs
             ms[i] = -INFINITY;
             ls[i] = 0.0f;
             os[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (s <= c1) {
+            if (s <= c1 && part_there(a, s, s == c0, hc)) {
                 // the first share has the unit's beginning; it may have had another's end before
                 const float* p = a.part + ((static_cast<size_t>(s) * 2 + (s == c0 ? 1 : 0)) * a.nh +
                                            hc) * kPart;
@@ -692,7 +693,7 @@ size_t paged_attention_scratch_bytes(int Hq, int Hkv) {
 
 cudaError_t launch_paged_attention(const void* q, bool q_bf16, const mp_paged& cache, int B, int Hq,
                                    int Hkv, int n, const int32_t* lengths, float scale, float* out,
-                                   void* workspace, cudaStream_t st) {
+                                   void* workspace, size_t ws_bytes, cudaStream_t st) {
     PArgs a;
     a.q = q;
     a.keys = cache.keys;
@@ -721,6 +722,7 @@ cudaError_t launch_paged_attention(const void* q, bool q_bf16, const mp_paged& c
     a.cluster = cluster_size(units, tiles, a.ctas, a.tile_shift, lengths != nullptr, g_clusters[dev][simt ? 0 : 1]);
     a.scale = scale * kLog2E;
     a.status = device_status_ptr();
+    a.ws_floats = static_cast<long long>(ws_bytes / sizeof(float));
     a.part = static_cast<float*>(workspace);
     a.begin = reinterpret_cast<int4*>(a.part + static_cast<size_t>(a.ctas) * 2 * a.nh * kPart);
     const unsigned grid = a.cluster ? static_cast<unsigned>(units) * a.cluster : a.ctas;

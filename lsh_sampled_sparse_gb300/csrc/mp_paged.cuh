@@ -43,9 +43,21 @@ struct PArgs {
     int cluster;                                 // CTAs a unit is shared out to, a cluster; 0: all
     int page_shift;                              // log2 of page_size, -1: no power of two
     float scale;                                 // of q.k, times log2 e
-    int* status;                                 // index checks of the MP_CHECKS build
+    int* status;                                 // index checks of the MP_CHECKS build,
+    long long ws_floats;                         // and what the workspace has for them
 };
 constexpr int kPart = kD + 4;
+
+// Index checks of the MP_CHECKS build: a state of the workspace, an entry of begin, a slot of the table
+__device__ __forceinline__ bool part_there(const PArgs& a, int cta, int half, int h) {
+    return mp_check(a.status, ((2ll * cta + half) * a.nh + h + 1) * kPart - 1, a.ws_floats, kSitePagedOut);
+}
+__device__ __forceinline__ bool begin_there(const PArgs& a, int c) {
+    return mp_check(a.status, 2ll * a.ctas * a.nh * kPart + 4 * (c + 1ll) - 1, a.ws_floats, kSitePagedOut);
+}
+__device__ __forceinline__ int page_in(const PArgs& a, const int32_t* slots, int slot) {
+    return mp_check(a.status, slot, a.pages.n_slots, kSitePagedRow) ? slots[slot] : -1;
+}
 
 __device__ __forceinline__ int length_of(const PArgs& a, int b) {
     return a.pages.lengths ? max(0, min(a.n, a.pages.lengths[b])) : a.n;
@@ -123,9 +135,9 @@ __device__ inline Walk plan_run(const PArgs& a, PlanSmem& s) {
         w.t = lo - unit * w.tiles;
         w.b = unit / per_tile;
         w.unit = unit - w.b * per_tile;
-        if (tid == 0) {
+        if (tid == 0 && begin_there(a, c)) {
             a.begin[c] = make_int4(w.b, w.unit, w.t, w.tiles);
-            if (c == 0) a.begin[a.ctas].x = per_tile * a.B * w.tiles;
+            if (c == 0 && begin_there(a, a.ctas)) a.begin[a.ctas].x = per_tile * a.B * w.tiles;
         }
         return w;
     }
@@ -167,9 +179,9 @@ __device__ inline Walk plan_run(const PArgs& a, PlanSmem& s) {
         w.tiles = tiles;
         w.len = len;
         s.walk = w;
-        a.begin[c] = make_int4(w.b, w.unit, w.t, w.tiles);
+        if (begin_there(a, c)) a.begin[c] = make_int4(w.b, w.unit, w.t, w.tiles);
     }
-    if (c == 0 && tid == 0) a.begin[a.ctas].x = total;
+    if (c == 0 && tid == 0 && begin_there(a, a.ctas)) a.begin[a.ctas].x = total;
     __syncthreads();
     return s.walk;
 }

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_mma_kernel(const 
         const int32_t* slots = a.pages.table + static_cast<long long>(ahead.b) * a.pages.stride;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            page[i] = ahead.left > 0 && tok + 8 * i < ahead.len ? slots[slot_of(a, tok + 8 * i)] : -1;
+            page[i] = ahead.left > 0 && tok + 8 * i < ahead.len ? page_in(a, slots, slot_of(a, tok + 8 * i)) : -1;
     };
     entries();
     auto issue = [&](int place) {
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_mma_kernel(const 
                 if (mp_check(a.status, static_cast<long long>(row0 + h),
                              static_cast<long long>(a.B) * a.Hq, kSitePagedOut))
                     a.out[(row0 + h) * kD + e] = over_sum(O, L);
-            } else {
+            } else if (part_there(a, blockIdx.x, w.t == 0, h)) {
                 float* p = part_of(a, w.t == 0, h);
                 p[e] = O;
                 if (e == 0) {

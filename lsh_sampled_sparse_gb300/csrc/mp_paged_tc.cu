@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     now = Unit{w.b, g, (w.unit - g * a.chunks) * NH, w.t, w.len, here == w.tiles};
                     slots = a.pages.table + static_cast<long long>(w.b) * a.pages.stride;
                     const int tok = now.t * kTile + tid;
-                    page = tok < now.len ? slots[slot_of(a, tok)] : -1;
+                    page = tok < now.len ? page_in(a, slots, slot_of(a, tok)) : -1;
                     w.next(a, here);
                 }
             }
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(s_empty + 8 * (it & 1));
                 const bool live = page >= 0 && page < a.pages.n_pages;   // and before the end
                 const int tok = tok0 + kTile + tid;
-                page = k + 1 < here && tok < now.len ? slots[slot_of(a, tok)] : -1;
+                page = k + 1 < here && tok < now.len ? page_in(a, slots, slot_of(a, tok)) : -1;
                 // ---- the tile's maxima, over the warp and over the four
                 float* most = reinterpret_cast<float*>(smem + L::kOffMax) + (it & 1) * kSoftWarps * NH;
                 float mine[NH];
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (mp_check(a.status, static_cast<long long>(row0 + h),
                                          static_cast<long long>(a.B) * a.Hq, kSitePagedOut))
                                 a.out[(row0 + h) * kD + tid] = over_sum(o[h], sum);
-                        } else {
+                        } else if (part_there(a, blockIdx.x, last.t == 0, h)) {
                             float* p = part_of(a, last.t == 0, h);
                             p[tid] = o[h];
                             if (tid == 0) {
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             x.head = kv_head(a, w.unit);
             if (tok < w.len && lane < x.tiles << box_shift) {
                 const int slot = slot_of(a, tok);
-                x.page = a.pages.table[static_cast<long long>(w.b) * a.pages.stride + slot];
+                x.page = page_in(a, a.pages.table + static_cast<long long>(w.b) * a.pages.stride, slot);
                 x.group = (tok - slot * a.pages.page_size) >> 3;
             }
             k += x.tiles;

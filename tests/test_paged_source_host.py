@@ -108,3 +108,30 @@ def test_blocks_of_the_largest_capacities(tmp_path):
     rows = [tuple(map(int, line.split())) for line in
             subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.splitlines()]
     assert len(rows) == 10 and all(b == -(-n // 1024) for n, b in rows)
+
+
+def _code(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def test_the_workspace_and_the_table_are_reached_behind_index_checks_only():
+    """What the header says the checks build checks: partial states and beginnings of runs against the
+    workspace, slots against the table, code words against the codes."""
+    shared = _code("mp_paged.cuh")
+    assert shared.count("a.begin[") == shared.count("begin_there(a, ") == 4
+    for name in ("mp_paged.cu", "mp_paged_tc.cu", "mp_paged_mma.cu"):
+        code = _code(name)
+        stores = re.findall(r"(\S[^\n]*)\n\s*float\* p = part_of\(", code)
+        assert len(stores) == 1 and all("part_there(a, blockIdx.x, " in s for s in stores), name
+        # every entry by page_in, or (an append's) by paged_row, whose tokens were held against the table
+        assert not re.search(r"table\[|slots\[", code), name
+        assert "page_in(" in code
+    join = re.search(r"__global__[^\n]* paged_join_kernel.*?\n}\n", _code("mp_paged.cu"), re.S).group(0)
+    assert join.index("begin_there") < join.index("__ldcg")
+    assert join.count("a.part +") == 1 and "part_there(a, s, s == c0, hc)" in join
+    assert shared.count("slots[") == 1 and "kSitePagedRow) ? slots[slot] : -1" in shared
+    decode = _code("mp_decode.cu")
+    assert decode.count("slots[") == 1 and "a.pages.n_slots, kSitePagedRow) ? slots[slot0 + i] : -1" in decode
+    at = re.search(r"encode_rows_at_kernel\(const AtArgs.*?\n}\n", _code("mp_append.cu"), re.S).group(0)
+    assert at.count("mp_check(") == 2 and at.index("a.cblk * a.C * kWordsPerBlock") < at.index("atomicOr")
