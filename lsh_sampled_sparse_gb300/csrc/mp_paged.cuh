@@ -59,23 +59,23 @@ __device__ __forceinline__ int page_in(const PArgs& a, const int32_t* slots, int
     return mp_check(a.status, slot, a.pages.n_slots, kSitePagedRow) ? slots[slot] : -1;
 }
 
-__device__ __forceinline__ int length_of(const PArgs& a, int b) {
+__host__ __device__ __forceinline__ int length_of(const PArgs& a, int b) {
     return a.pages.lengths ? max(0, min(a.n, a.pages.lengths[b])) : a.n;
 }
-__device__ __forceinline__ int tiles_of(const PArgs& a, int len) {
+__host__ __device__ __forceinline__ int tiles_of(const PArgs& a, int len) {
     return (len + (1 << a.tile_shift) - 1) >> a.tile_shift;
 }
 // `total` tiles (less than 2^31: a call's sizes see to that) shared out to CTAs: the first `more` of
 // them take each + 1, the others `each`
 struct Shares {
     int each, more, n;                           // n: CTAs that have any
-    __device__ __forceinline__ Shares(const PArgs& a, int total) {
+    __host__ __device__ __forceinline__ Shares(const PArgs& a, int total) {
         n = min(a.ctas, total);
         each = n > 0 ? total / n : 0;
         more = total - each * n;
     }
-    __device__ __forceinline__ int first(int c) const { return each * c + min(c, more); }  // tile of CTA c
-    __device__ __forceinline__ int of(int t) const {                     // the CTA that has tile t
+    __host__ __device__ __forceinline__ int first(int c) const { return each * c + min(c, more); }  // tile of CTA c
+    __host__ __device__ __forceinline__ int of(int t) const {                     // the CTA that has tile t
         const int in_more = more * (each + 1);
         return t < in_more ? t / (each + 1) : more + (t - in_more) / each;
     }
@@ -92,9 +92,9 @@ __device__ __forceinline__ int kv_head(const PArgs& a, int unit) {
 struct Walk {
     int left;                                    // tiles of the run from here on
     int b, unit, t, tiles, len;                  // unit of the sequence, its next tile, all its tiles
-    __device__ __forceinline__ int here() const { return min(left, tiles - t); }
+    __host__ __device__ __forceinline__ int here() const { return min(left, tiles - t); }
     // past `here` tiles: the next unit, if the run goes on
-    __device__ __forceinline__ void next(const PArgs& a, int here) {
+    __host__ __device__ __forceinline__ void next(const PArgs& a, int here) {
         left -= here;
         t = 0;
         if (left <= 0 || ++unit < a.Hkv * a.chunks) return;
