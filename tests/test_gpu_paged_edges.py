@@ -2,7 +2,10 @@
 import pytest
 import torch
 
-from tests.test_gpu_paged import BF, F32, _attend_and_check, _gen, _ints, _randn, _random_cache
+from tests import paged_reference as R
+from tests.test_gpu_paged import (BF, F32, _attend_and_check, _chosen, _gen, _ints, _pages_of, _randn,
+                                  _random_cache)
+from workloads import make_hyperplanes, make_layer, small_workload
 
 pytestmark = pytest.mark.gpu
 
@@ -137,3 +140,118 @@ def test_cosines_and_sines_of_all_quarters_of_a_turn(mp, interleaved):
         off = (got.double() - want).abs() - angle - 2.0 ** -23 * want.abs()
         assert (off <= 0).all(), off.max().item()
     assert (out[0, 0, 0, first] == 1).all() and (out[0, 0, 0, second] == 0).all()        # position 0
+
+
+def _layer(B, Hq, Hkv, n, K, L, seed):
+    wl = small_workload(name="pagede", index=seed, B=B, Hq=Hq, Hkv=Hkv, n=n, K=K, L=L, kv_dtype=F32, q_dtype=F32,
+                        w_dtype=F32)
+    return {k: v.cuda() for k, v in make_layer(wl).items()}, make_hyperplanes(wl).cuda()
+
+
+@pytest.mark.parametrize("qt,kt,wt", [(F32, BF, BF), (BF, F32, F32), (BF, BF, F32), (F32, F32, BF),
+                                      (F32, BF, F32), (BF, F32, BF)])
+@pytest.mark.parametrize("B,Hq,Hkv", [(3, 8, 2), (23, 8, 4), (37, 16, 2)])
+def test_sampled_decode_of_mixed_types(mp, qt, kt, wt, B, Hq, Hkv):
+    """Queries, cache and hyperplanes of different types, at batches of each form of the query encoding (24, 184
+    and 592 rows)."""
+    n, page, K, L, args = 600, 24, 6, 50, (6, 50, 3, 20)
+    lens = [(n, 0, 1, 333, 70, 24, 23)[b % 7] for b in range(B)]
+    x, W = _layer(B, Hq, Hkv, n, K, L, 790)
+    x = dict(q=x["q"].to(qt), keys=x["keys"].to(kt), values=x["values"].to(kt))
+    W = W.to(wt)
+    centre = mp.key_mean(x["keys"])
+    g = _gen(B)
+    cache, table = _pages_of(mp, g, x, n, page)
+    codes = mp.encode_rows(x["keys"], centre, W, K, L, 0, n)
+    chosen = _chosen(mp, x, codes, centre, W, lens, n, args, Hkv)
+    out = mp.paged_decode_attention(x["q"], codes, centre, W, cache, table, *args, n=n, lengths=_ints(lens),
+                                    n_capacity=n)
+    want, tol = R.sampled(x["q"], centre, cache.keys, cache.values, table.cpu(), lens, chosen, *args, 128 ** -0.5)
+    assert ((out.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("wt", [BF, F32])
+@pytest.mark.parametrize("B,Hq,Hkv", [(2, 4, 2), (33, 2, 2), (43, 3, 3), (33, 4, 2), (70, 8, 4), (129, 4, 4), (100, 3, 3)])
+def test_hyperplanes_aligned_to_their_element_only(mp, wt, B, Hq, Hkv):
+    """And heads without a group, in each form of the query encoding: the outputs and codes of aligned ones."""
+    n, page, K, L = 200, 8, 4, 40
+    x, W = _layer(B, Hq, Hkv, n, K, L, 791)
+    W = W.to(wt)
+    off = torch.empty(W.numel() + 1, dtype=wt, device="cuda")[1:].view(W.shape)
+    off.copy_(W)
+    assert off.data_ptr() % (2 * off.element_size()) == off.element_size() and W.data_ptr() % 16 == 0
+    lens = [(37 * b) % (n + 1) for b in range(B)]
+    centre = mp.key_mean(x["keys"])
+    g = _gen(B)
+    cache, table = _pages_of(mp, g, x, n, page)
+    codes = mp.encode_rows(x["keys"], centre, W, K, L, 0, n)
+    rows = x["keys"][:, :, :7].contiguous()
+    for kt in (BF, F32):
+        at = _ints([(11 * b) % n for b in range(B)])
+        two = [mp.encode_rows_at(rows.to(kt), centre, w, K, L, at, n, codes.clone()) for w in (W, off)]
+        assert torch.equal(*two)
+    args, kw = (K, L, 2, 9), dict(n=n, lengths=_ints(lens), n_capacity=n)
+    out = mp.paged_decode_attention(x["q"], codes, centre, off, cache, table, *args, **kw)
+    assert torch.equal(mp.paged_decode_attention(x["q"], codes, centre, W, cache, table, *args, **kw), out)
+    chosen = _chosen(mp, x, codes, centre, W, lens, n, args, Hkv)
+    want, tol = R.sampled(x["q"], centre, cache.keys, cache.values, table.cpu(), lens, chosen, *args, 128 ** -0.5)
+    assert ((out.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("B,Hkv,m,cap,K,L", [(5, 3, 17, 3001, 8, 75), (64, 8, 1, 1500, 10, 150), (2, 1, 64, 1100, 3, 7)])
+def test_codes_of_float32_keys_by_bf16_hyperplanes(mp, B, Hkv, m, cap, K, L):
+    g = _gen(cap)
+    keys, centre = _randn(g, B, Hkv, m, 128), _randn(g, B, Hkv, 128) * 0.1
+    W = _randn(g, 128, K * L).to(BF)
+    starts = [(997 * b) % (cap - m + 1) for b in range(B)]
+    old = torch.randint(-2 ** 31, 2 ** 31 - 1, (mp.codes_bytes(B, Hkv, cap, K, L) // 4,), generator=g,
+                        device="cuda").int()
+    codes = mp.encode_rows_at(keys, centre, W, K, L, _ints(starts), cap, old.clone())
+    per = old.numel() // B
+    for b in range(B):
+        want = old[b * per:(b + 1) * per].clone()
+        mp.encode_rows(keys[b:b + 1], centre[b:b + 1], W, K, L, starts[b], cap, codes=want)
+        assert torch.equal(codes[b * per:(b + 1) * per], want)
+
+
+@pytest.mark.parametrize("variant,K,L", [("mips", 8, 75), ("cp", 1, 32)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_variants_over_pages_of_empty_sequences_and_missing_pages(mp, variant, K, L, dtype):
+    n, page, lens = 2100, 16, [0, 2100, 1, 1500, 0]
+    B, Hq, Hkv = len(lens), 4, 2
+    x, W = _layer(B, Hq, Hkv, n, 1 if variant == "cp" else K, L, 792)
+    x = {k: v.to(dtype) for k, v in x.items()}
+    g = _gen(2)
+    centre, extra = mp.key_mean(x["keys"]), {}
+    if variant == "mips":
+        W = torch.cat([W, _randn(g, 1, K * L)]).to(dtype).contiguous()
+        extra["radius"] = mp.key_radius(x["keys"], centre)
+        codes = mp.encode_keys_mips(x["keys"], centre, W, extra["radius"], K, L, 0, n)
+    else:
+        W = _randn(g, L, 128, 128).to(dtype)
+        extra["logu_table"] = mp.cp_logu_table(1, L)
+        codes = mp.encode_keys_cp(x["keys"], centre, W, L, 0, n)
+    cache, table = _pages_of(mp, g, x, n, page)
+
+    def run(**kw):
+        return mp.paged_decode_attention(x["q"], codes, centre, W, cache, table, K, L, 4, 64, n=n, n_capacity=n,
+                                         lengths=_ints(lens), **extra, **kw)
+
+    out = run()
+    per = codes.numel() // B
+    for b, used in enumerate(lens):
+        if used == 0:
+            assert (out[b] == 0).all()
+            continue
+        one = {k: v[b:b + 1].contiguous() if k == "radius" else v for k, v in extra.items()}
+        want = mp.decode_attention(x["q"][b:b + 1], codes.view(-1)[b * per:(b + 1) * per], centre[b:b + 1], W,
+                                   x["keys"][b:b + 1], x["values"][b:b + 1], K, L, 4, 64, n=used, **one)
+        # log u: 2e-5 of the contiguous form's table, twice (weights), of values of up to 5
+        assert (out[b] - want[0]).abs().max() <= 2 * 4e-5 * 5
+    table[1] = -1                                # nothing left of the longest
+    again = run()
+    assert (again[1] == 0).all()
+    assert torch.equal(again[[0, 2, 3, 4]], out[[0, 2, 3, 4]])
+    mp.paged_decode_attention(x["q"], codes, centre, W, cache, table, K, L, 4, 64, n=n, n_capacity=n,
+                              lengths=_ints([0] * B), out=out, **extra)
+    assert (out == 0).all()
