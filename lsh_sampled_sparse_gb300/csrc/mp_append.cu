@@ -103,8 +103,10 @@ __global__ void __launch_bounds__(kAppendThreads)
 // 128 hyperplanes and sixteen rows at a time of whole heads. A lane sums four hyperplanes by four rows, from
 // shared memory (a lane is given 1.5 bytes a sum that way; with one hyperplane a lane and eight rows, 4.5
 // bytes, the sums took three times as long); the signs meet in shared memory, and the thread a hyperplane
-// belongs to sends the bits to their words. What is left is the layout's: a key's K L bits lie in as many
-// words 128 bytes apart (32 sequences x 8 heads at (10, 150): 31 MB read for 384000 words, 14.2 us).
+// belongs to sends the bits to their words. What is left of a row or a few is the layout's: a key's K L bits lie
+// in as many words 128 bytes apart (32 sequences x 8 heads at (10, 150), a key each: 384000 words, for which DRAM
+// is read 979000 sectors of 32 bytes, 31 MB; 13.6 to 14.3 us). Tens of rows are bound by the sums, in float32 on
+// CUDA cores: 64 rows of each of those heads 207 us, 30 TFLOP/s.
 struct AtArgs {
     const void* keys;
     const void* W;
@@ -244,7 +246,7 @@ __global__ void __launch_bounds__(kAtThreads) encode_rows_at_kernel(const AtArgs
         if (!live) continue;
         // rows of one word follow each other: their bits go out after the last, those to set and those
         // to clear, by operations that L2 carries out and nobody waits for (words loaded, changed and
-        // stored: 49 MB read, 23 to 31 us instead of 14)
+        // stored: 49 MB read instead of 31, 23 to 31 us instead of 14)
         uint32_t set = 0u, clear = 0u;
 #pragma unroll
         for (int u = 0; u < kAtRows; ++u) {

@@ -1565,7 +1565,9 @@ cudaError_t launch_qencode_rows(const void* q, bool q_bf16, const float* centre,
                                 cudaStream_t st) {
     const QArgs qa = query_args(q, q_bf16, centre, W, w_bf16, s, ws);
     // Calls of 128, 512 and 32 query rows with the kernel above 40.3, 45.1 and 47.7 us, with two rows a lane
-    // 39.4, 36.9 and 50.4 (few CTAs, each as long as one alone), with four 40.4, 36.1 and 52.2.
+    // 39.4, 36.9 and 50.4 (few CTAs, each as long as one alone), with four 40.4, 36.1 and 52.2. The table of log u
+    // that the kernel above fills beside its codes, which no one reads here, takes no time of a call's (32 rows,
+    // 96K tokens: 47.8 us with it, 47.7 without).
     if (qa.BHq <= 64) return launch_qencode(q, q_bf16, centre, W, w_bf16, s, ws, st);
     const int R = qa.BHq <= 256 ? 2 : 4;
     return launch_dependent(pick_qencode_rows(w_bf16, R),

@@ -176,7 +176,8 @@ cudaError_t launch_encode_rows_at(const void* keys, bool keys_bf16, const float*
 cudaError_t launch_qencode(const void* q, bool q_bf16, const float* centre, const void* W,
                            bool w_bf16, const DecodeShape& s, const DecodeScratch& ws,
                            cudaStream_t st);
-// the same bits, norms and counters for the decode over pages, without the table of log u
+// the same bits, norms and counters for the decode over pages, which reads no table of log u of SimHash codes (up
+// to 64 query rows are launch_qencode's all the same, table included)
 cudaError_t launch_qencode_rows(const void* q, bool q_bf16, const float* centre, const void* W,
                                 bool w_bf16, const DecodeShape& s, const DecodeScratch& ws,
                                 cudaStream_t st);

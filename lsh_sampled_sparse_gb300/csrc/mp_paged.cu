@@ -39,7 +39,9 @@ constexpr int kAppThreads = 256;
 constexpr int kRowLanes = 8;                     // lanes a row, 2 x 8 dims each
 constexpr int kAppRows = kAppThreads / kRowLanes;
 constexpr int kAppCtas = 6;                      // an SM: 40 registers a thread (4, 5 and 8 take as long)
-constexpr int kMaxToks = 4;                      // tokens a block has
+// tokens a block has: of up to eight heads, whatever their number (5 sequences x 333 tokens of 12 + 3 + 3 heads: a
+// quarter of the rows of 1260 CTAs stay empty, and 912 fit at once)
+constexpr int kMaxToks = 4;
 static_assert(kMaxToks * (kD / 2) == kAppThreads, "a thread an angle");
 
 // 8 elements as they are in memory, two of them as floats

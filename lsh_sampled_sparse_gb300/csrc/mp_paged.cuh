@@ -5,13 +5,17 @@
 
 namespace mp {
 
+// Weights, and factors of states: 2^x within 2^-22 of itself, the bound of exp2f too, but 0 below 2^-126, which
+// is nothing beside the largest weight of a row, 1 (7 x 12/12 float32 heads x up to 3001 tokens: outputs off 64 bits
+// by 3.3e-7, by 3.0e-7 where elementary operations in float32 make them)
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
-// A sum of values over the sum of their weights, which is 1 at least, or 0 where there are none (or NaN)
+// A sum of values over the sum of their weights, which is 1 at least, or 0 where there are none (or NaN): by the
+// reciprocal, within 2^-23 of itself, once an output
 __device__ __forceinline__ float over_sum(float o, float sum) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sum));
