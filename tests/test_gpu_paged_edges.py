@@ -255,3 +255,24 @@ def test_variants_over_pages_of_empty_sequences_and_missing_pages(mp, variant, K
     mp.paged_decode_attention(x["q"], codes, centre, W, cache, table, K, L, 4, 64, n=n, n_capacity=n,
                               lengths=_ints([0] * B), out=out, **extra)
     assert (out == 0).all()
+
+
+def test_radii_and_tables_of_other_types_are_refused(mp):
+    """They are read as float32: half as many bytes would be read past their end."""
+    cache = mp.paged_cache(6, 2, 16)
+    table = torch.arange(6, device="cuda").view(2, 3).int()
+    q, W, centre = _randn(_gen(1), 2, 4, 128), torch.zeros(128, 80, device="cuda"), torch.zeros(2, 2, 128, device="cuda")
+    codes = torch.zeros(mp.codes_bytes(2, 2, 48, 8, 10) // 4, dtype=torch.int32, device="cuda")
+    kv4 = mp.kv4_cache(2, 2, 48)
+    entries = torch.zeros(mp.MP_LOGU_TABLE_ENTRIES, device="cuda")
+    for t in (BF, torch.float16, torch.float64, torch.int32):
+        for kw in (dict(radius=torch.ones(2, 2, device="cuda").to(t)), dict(logu_table=entries.to(t))):
+            K, L = (1, 10) if "logu_table" in kw else (8, 10)
+            with pytest.raises(TypeError):
+                mp.paged_decode_attention(q, codes, centre, W, cache, table, K, L, 4, 64, **kw)
+            with pytest.raises(TypeError):
+                mp.kv4_decode_attention(q, codes, centre, W, kv4, K, L, 4, 64, **kw)
+    with pytest.raises(ValueError):
+        mp.paged_decode_attention(q, codes, centre, W, cache, table, 8, 10, 4, 64, radius=torch.ones(3, device="cuda"))
+    torch.cuda.synchronize()
+    assert mp.device_status() == 0
