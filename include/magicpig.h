@@ -525,6 +525,8 @@ MP_API size_t mp_paged_attention_workspace_bytes(int B, int Hq, int Hkv, int n, 
  * the pages hold beyond a sequence's length is not looked at, NaN included. A NaN or an infinity in a
  * query, or in a key or value attended to, may give NaN in the rows that it meets, and so may an element
  * past the largest bf16 or tf32 where it is split.
+ * Sums over tokens take weights of up to 1 each, before the division: they may overflow where the largest
+ * value attended to times the tokens passes 2^127, and so may a score's sum of 128 products.
  * Errors: MP_ERR_INVALID_ARG (shapes, n > n_slots page_size or 2^30, B Hq > 2^22, B Hq n > 2^35, Hq %
  * Hkv, a scale that is negative, NaN, or infinite in float32 once multiplied by log2 e, null, misalignment:
  * out 16 bytes, lengths 4, workspace 256), MP_ERR_UNSUPPORTED (d != 128, page_size not a multiple of 8),
